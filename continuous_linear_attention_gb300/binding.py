@@ -44,6 +44,12 @@ EXPORTED = [
     "gdn_prefill_scratch_bytes", "gdn_pool_last_prefill_path",
     "gdn_in_proj",
     "gdn_out_proj",
+    "gdn_state_pool_copy_blocks",
+    "gdn_state_pool_clear_blocks",
+    "gdn_state_pool_compact",
+    "gdn_lin_pool_layout_for",
+    "gdn_lin_pool_create",
+    "gdn_lin_varlen_forward",
     "gdn_status_string",
 ]
 
@@ -105,6 +111,14 @@ def load() -> ctypes.CDLL:
     lib.gdn_prefill_scratch_bytes.argtypes = [I] * 6 + [PS]
     lib.gdn_in_proj.argtypes = [P, I, I, P, P, P, P, I, I, I, P, P, P, P, P, P]
     lib.gdn_out_proj.argtypes = [P, P, P, ctypes.c_float, P, I, I, I, I, P, P, P, P]
+    L = ctypes.c_int64
+    lib.gdn_state_pool_copy_blocks.argtypes = [P, I, P, P, I, P]
+    lib.gdn_state_pool_clear_blocks.argtypes = [P, I, P, I, P]
+    lib.gdn_state_pool_compact.argtypes = [P, P, P, I, P]
+    lib.gdn_lin_pool_layout_for.argtypes = [I] * 5 + [S, PS, PS]
+    lib.gdn_lin_pool_create.argtypes = [ctypes.POINTER(P)] + [I] * 5 + [S, P, S]
+    lib.gdn_lin_varlen_forward.argtypes = [P, I, P, P, P, L, L, L, I, P, P, P, P,
+                                           ctypes.c_float, P, L, I, I, I, P]
     lib.gdn_diag_umma_gemm.argtypes = [P, P, P, P, I, I, I, P]
     lib.gdn_diag_umma_gemm.restype = I
     lib.gdn_diag_umma_gemm_ex.argtypes = [P, P, P, P, I, I, I, I, I, P]
@@ -133,6 +147,13 @@ def _ptr(t) -> Optional[int]:
         return None
     if isinstance(t, int):
         return t
+    return t.data_ptr()
+
+
+def _index(t) -> Optional[int]:
+    """The address of a list of block indices."""
+    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError("block indices are a contiguous int32 CUDA tensor of one dimension")
     return t.data_ptr()
 
 
@@ -227,6 +248,32 @@ class Pool:
         _check(load().gdn_state_pool_copy_block(self.handle, layer, src, dst, _stream(stream)),
                "gdn_state_pool_copy_block")
 
+    def copy_blocks(self, src, dst, layer=-1, stream=None):
+        """gdn_state_pool_copy_blocks: block dst[i] <- block src[i] for all i
+        at once (int32 device tensors), in one layer or (-1) in all."""
+        if len(src) != len(dst):
+            raise ValueError(f"{len(src)} sources and {len(dst)} destinations")
+        _check(load().gdn_state_pool_copy_blocks(self.handle, layer, _index(src), _index(dst),
+                                                 len(src), _stream(stream)),
+               "gdn_state_pool_copy_blocks")
+
+    def clear_blocks(self, idx, layer=-1, stream=None):
+        """gdn_state_pool_clear_blocks: blocks idx (int32 device tensor) <- zeros."""
+        _check(load().gdn_state_pool_clear_blocks(self.handle, layer, _index(idx), len(idx),
+                                                  _stream(stream)),
+               "gdn_state_pool_clear_blocks")
+
+    def compact(self, idx, new_idx=None, stream=None):
+        """gdn_state_pool_compact: the live blocks idx (int32 device tensor)
+        move to the lowest indices; new_idx (or idx itself) receives where
+        each one is afterwards.  Returns new_idx."""
+        new_idx = idx if new_idx is None else new_idx
+        if len(idx) != len(new_idx):
+            raise ValueError(f"{len(idx)} indices and room for {len(new_idx)}")
+        _check(load().gdn_state_pool_compact(self.handle, _index(idx), _index(new_idx), len(idx),
+                                             _stream(stream)), "gdn_state_pool_compact")
+        return new_idx
+
     def error_flags(self, layer=-1, reset=True, stream=None) -> int:
         v = ctypes.c_uint32()
         _check(load().gdn_get_error(self.handle, layer, ctypes.byref(v), 1 if reset else 0,
@@ -265,6 +312,67 @@ def ssd_varlen_forward(pool: SsdPool, layer: int, xbc, dt, cu_seqlens, state_blo
                                          _ptr(cu_seqlens), _ptr(state_block_idx), _ptr(has_past),
                                          ctypes.byref(w), _ptr(y), T, N, max_seqlen_hint,
                                          _stream(stream)), "gdn_ssd_varlen_forward")
+
+
+def lin_layout_for(num_blocks, num_layers, H, d, act, block_align=0):
+    """(block_stride, total_bytes) of a decayed linear attention pool."""
+    out = [ctypes.c_size_t() for _ in range(2)]
+    _check(load().gdn_lin_pool_layout_for(num_blocks, num_layers, H, d, act_code(act), block_align,
+                                          *[ctypes.byref(o) for o in out]),
+           "gdn_lin_pool_layout_for")
+    return tuple(o.value for o in out)
+
+
+class LinPool(Pool):
+    """A decayed linear attention state pool (gdn_lin_pool_create): blocks of
+    [H][d][d] fp32.  With ``memory`` the pool lives in that CUDA uint8 tensor."""
+
+    def __init__(self, num_blocks, num_layers, H, d, act, block_align=0,
+                 memory: Optional[torch.Tensor] = None):
+        self.dims = (num_blocks, num_layers, H, d)
+        self.act = act_code(act)
+        self.num_blocks, self.num_layers = num_blocks, num_layers
+        self.memory = memory
+        h = ctypes.c_void_p()
+        nbytes = memory.numel() * memory.element_size() if memory is not None else 0
+        _check(load().gdn_lin_pool_create(ctypes.byref(h), num_blocks, num_layers, H, d, self.act,
+                                          block_align, _ptr(memory), nbytes),
+               "gdn_lin_pool_create")
+        self.handle = h
+        s, c, r, b = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_void_p()
+        _check(load().gdn_state_pool_layout(h, ctypes.byref(s), ctypes.byref(c), ctypes.byref(r),
+                                            ctypes.byref(b)), "gdn_state_pool_layout")
+        self.stride, self.conv_off, self.rec_off, self.base = s.value, c.value, r.value, b.value
+
+
+def _heads(t, name, d, act):
+    """(address, row pitch) of rows of heads [T][heads][d]: any row pitch, the
+    rows themselves dense."""
+    want = torch.float32 if act == GDN_F32 else torch.bfloat16
+    if t.dim() != 3 or t.shape[2] != d or t.dtype != want:
+        raise ValueError(f"{name} is [T][heads][{d}] of {want}: got {tuple(t.shape)} of {t.dtype}")
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d)):
+        raise ValueError(f"the rows of {name} have to be dense")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * d
+
+
+def lin_varlen_forward(pool: LinPool, layer: int, q, k, v, cu_seqlens, state_block_idx, has_past,
+                       log_decay, out, T: int, N: int, scale: float = 1.0,
+                       max_seqlen_hint: int = 0, stream=None) -> None:
+    """gdn_lin_varlen_forward on device tensors: q and out [T][H][d], k and v
+    [T][Hkv][d], each with any row pitch (views of a fused projection's rows)."""
+    H, d = pool.dims[2], pool.dims[3]
+    (pq, ldq), (pk, ldk), (pv, ldv), (po, ldo) = (
+        _heads(t, name, d, pool.act) for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out")))
+    if q.shape[1] != H or out.shape[1] != H or k.shape[1] != v.shape[1]:
+        raise ValueError(f"q and out have {H} heads, k and v the same number")
+    if any(t.shape[0] < T for t in (q, k, v, out)):
+        raise ValueError(f"q, k, v and out have at least {T} rows")
+    _check(load().gdn_lin_varlen_forward(pool.handle, layer, pq, pk, pv, ldq, ldk, ldv, k.shape[1],
+                                         _ptr(cu_seqlens), _ptr(state_block_idx), _ptr(has_past),
+                                         _ptr(log_decay), float(scale), po, ldo, T, N,
+                                         max_seqlen_hint, _stream(stream)),
+           "gdn_lin_varlen_forward")
 
 
 def varlen_forward(pool: Pool, layer: int, x_qkv, a, b, cu_seqlens, state_block_idx, has_past,

@@ -12,27 +12,7 @@
 
 #include "gdn.h"
 #include "gdn_internal.cuh"
-
-struct gdn_pool {
-  int num_blocks, num_layers, Hk, Hv, dk, dv, K, act;
-  size_t stride, conv_off, rec_off, total;
-  unsigned char* base;
-  bool owns;
-  int device;
-  int32_t* work;  // num_layers * WorkArea::words(num_blocks) words
-  cudaEvent_t ev_before, ev_after;  // optional timing events (caller-owned)
-  // prefill scratch: chunk-major tiles of the split prefill path (gated delta
-  // net pools, capacity in 64-token chunks) or the fp16 conv output of the
-  // chunked scan (Mamba2 pools, capacity in tokens); allocated stream-ordered
-  unsigned char* scr;
-  size_t scr_bytes;
-  bool scr_grow;  // false: never allocated; the fused chunked kernel is used
-  int last_path;  // GDN_PREFILL_* of the last forward
-  // 0: gated delta net pool (conv + recurrent state); 1: Mamba2 pool (conv +
-  // SSM state [H][P][N] at rec_off), with its dimensions
-  int kind;
-  int ssd_H, ssd_P, ssd_N, ssd_G;
-};
+#include "gdn_pool.cuh"
 
 namespace {
 
@@ -151,6 +131,34 @@ bool is_pow2(size_t v) { return v && !(v & (v - 1)); }
 }  // namespace
 
 namespace gdn {
+int pool_allocate(gdn_pool* p, void* device_mem) {
+  if (cudaGetDevice(&p->device) != cudaSuccess) return GDN_ERR_CUDA;
+  p->owns = device_mem == nullptr;
+  p->base = (unsigned char*)device_mem;
+  if (p->owns && cudaMalloc((void**)&p->base, p->total) != cudaSuccess) {
+    cudaGetLastError();
+    return GDN_ERR_NOMEM;
+  }
+  // the layers' work areas, then the block operations' one
+  const size_t layer_words = WorkArea::words(p->num_blocks) * p->num_layers;
+  const size_t work_bytes = (layer_words + BlockWork::words(p->num_blocks)) * sizeof(int32_t);
+  if (cudaMalloc((void**)&p->work, work_bytes) != cudaSuccess) {
+    cudaGetLastError();
+    if (p->owns) cudaFree(p->base);
+    return GDN_ERR_NOMEM;
+  }
+  p->blk_work = p->work + layer_words;
+  if (cudaMemset(p->base, 0, p->total) != cudaSuccess ||
+      cudaMemset(p->work, 0, work_bytes) != cudaSuccess ||
+      cudaDeviceSynchronize() != cudaSuccess) {
+    cudaGetLastError();
+    if (p->owns) cudaFree(p->base);
+    cudaFree(p->work);
+    return GDN_ERR_CUDA;
+  }
+  return GDN_OK;
+}
+
 size_t prefill_scratch_unit_bytes(int Hk, int Hv, int dk, int dv) {
   size_t b = 0;
   for (int i = 0; i < kScrScalarParts; ++i) b += part_bytes_of(Hk, Hv, dk, dv, i);
@@ -362,36 +370,10 @@ int gdn_state_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int 
   p->conv_off = l.conv_off;
   p->rec_off = l.rec_off;
   p->total = l.total;
-  if (cudaGetDevice(&p->device) != cudaSuccess) {
+  st = gdn::pool_allocate(p, device_mem);
+  if (st != GDN_OK) {
     delete p;
-    return GDN_ERR_CUDA;
-  }
-  if (device_mem) {
-    p->base = (unsigned char*)device_mem;
-    p->owns = false;
-  } else {
-    if (cudaMalloc((void**)&p->base, l.total) != cudaSuccess) {
-      cudaGetLastError();
-      delete p;
-      return GDN_ERR_NOMEM;
-    }
-    p->owns = true;
-  }
-  const size_t work_bytes = gdn::WorkArea::words(num_blocks) * num_layers * sizeof(int32_t);
-  if (cudaMalloc((void**)&p->work, work_bytes) != cudaSuccess) {
-    cudaGetLastError();
-    if (p->owns) cudaFree(p->base);
-    delete p;
-    return GDN_ERR_NOMEM;
-  }
-  if (cudaMemset(p->base, 0, l.total) != cudaSuccess ||
-      cudaMemset(p->work, 0, work_bytes) != cudaSuccess ||
-      cudaDeviceSynchronize() != cudaSuccess) {
-    cudaGetLastError();
-    if (p->owns) cudaFree(p->base);
-    cudaFree(p->work);
-    delete p;
-    return GDN_ERR_CUDA;
+    return st;
   }
   *out = p;
   return GDN_OK;
@@ -405,6 +387,7 @@ int gdn_state_pool_destroy(gdn_pool_t* p) {
   cudaDeviceSynchronize();
   if (p->owns) cudaFree(p->base);
   cudaFree(p->work);
+  cudaFree(p->lin_states);
   scratch_release(p);
   if (prev >= 0) cudaSetDevice(prev);
   delete p;
@@ -501,6 +484,7 @@ int gdn_state_pool_reserve(gdn_pool_t* p, int max_tokens) {
   int prev = -1;
   cudaGetDevice(&prev);
   if (prev != p->device) return GDN_ERR_DEVICE;
+  if (p->kind == 2) return GDN_OK;  // its work memory is there from its creation on
   if (max_tokens > 0) {
     p->scr_grow = true;
     return scratch_grow(p, scratch_units_for(p, max_tokens, max_tokens), 0, true);
@@ -664,36 +648,10 @@ int gdn_ssd_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int H,
   p->conv_off = l.conv_off;
   p->rec_off = l.rec_off;
   p->total = l.total;
-  if (cudaGetDevice(&p->device) != cudaSuccess) {
+  st = gdn::pool_allocate(p, device_mem);
+  if (st != GDN_OK) {
     delete p;
-    return GDN_ERR_CUDA;
-  }
-  if (device_mem) {
-    p->base = (unsigned char*)device_mem;
-    p->owns = false;
-  } else {
-    if (cudaMalloc((void**)&p->base, l.total) != cudaSuccess) {
-      cudaGetLastError();
-      delete p;
-      return GDN_ERR_NOMEM;
-    }
-    p->owns = true;
-  }
-  const size_t work_bytes = gdn::WorkArea::words(num_blocks) * num_layers * sizeof(int32_t);
-  if (cudaMalloc((void**)&p->work, work_bytes) != cudaSuccess) {
-    cudaGetLastError();
-    if (p->owns) cudaFree(p->base);
-    delete p;
-    return GDN_ERR_NOMEM;
-  }
-  if (cudaMemset(p->base, 0, l.total) != cudaSuccess ||
-      cudaMemset(p->work, 0, work_bytes) != cudaSuccess ||
-      cudaDeviceSynchronize() != cudaSuccess) {
-    cudaGetLastError();
-    if (p->owns) cudaFree(p->base);
-    cudaFree(p->work);
-    delete p;
-    return GDN_ERR_CUDA;
+    return st;
   }
   *out = p;
   return GDN_OK;

@@ -1,0 +1,539 @@
+// Block operations of a state pool: copy lists (forks, beam reorders), free
+// and compaction, each from device-side indices over one layer or all of them,
+// without a host round trip ("Continuous batching for linear attention
+// layers", PR description: a state block is copied on fork and never shared).
+//
+// A copy list means "every source is read before any block is overwritten",
+// so a beam reorder may name a block as a source of one entry and the
+// destination of another, in chains and cycles.  No scratch blocks and no
+// second pass over the data are needed for it: the blocks are cut into byte
+// columns, one warp owns a column of every block, and it moves the column's
+// pieces one source at a time in an order in which a block is read before it
+// is written.  With W[x] the source of the entry that writes x, source x must
+// come before source W[x], whose move overwrites x: a graph with one successor
+// per node, i.e. trees whose roots are last moves or cycles.  The planning
+// kernel orders the trees by their distance to the root (pointer jumping) and
+// walks each cycle; a cycle's last source is first read into a spare buffer.
+//
+// Traffic: every distinct source is read once, however many destinations it
+// has, and every destination written once, the least the call can do.  The
+// pieces go global -> shared -> global by bulk copies issued by one lane, so
+// registers hold none of the data.
+#include "gdn_internal.cuh"
+#include "gdn_pool.cuh"
+#include "gdn_ptx.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+// pools of up to this many blocks keep the planning arrays in shared memory
+constexpr int kSmemBlocks = 8192;
+constexpr int kPlanArrays = 6;
+// kinds of a move, in bits 30-31 of its source
+enum Kind : uint32_t { kCopy = 0, kHold = 1, kStoreHeld = 2 };
+constexpr uint32_t kBlockMask = (1u << 30) - 1;
+
+// Exclusive sum of v over the CTA's threads before this one, and the total.
+__device__ int cta_scan(int v, int* total, int* warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int w = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    warp_sums[lane] = w;
+  }
+  __syncthreads();
+  const int before = warp > 0 ? warp_sums[warp - 1] : 0;
+  *total = warp_sums[31];
+  __syncthreads();
+  return before + x - v;
+}
+
+// Orders the moves of a copy list (see above) into bw.
+__global__ void __launch_bounds__(kPlanThreads)
+plan_copies_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n, int nb,
+                   BlockWork bw, uint32_t* err) {
+  extern __shared__ int32_t plan_smem[];
+  __shared__ unsigned s_flags;
+  __shared__ int s_ops, s_dsts, s_cyc;
+  __shared__ int warp_sums[32];
+  pdl_wait_then_release();
+  const int tid = threadIdx.x;
+  int32_t* a = nb <= kSmemBlocks ? plan_smem : bw.tmp();
+  int32_t* W = a;             // source of the entry that writes a block, or -1
+  int32_t* cnt = a + nb;      // destinations of a source
+  int32_t* P = a + 2 * (size_t)nb;
+  int32_t* Q = a + 3 * (size_t)nb;
+  int32_t* DP = a + 4 * (size_t)nb;
+  int32_t* DQ = a + 5 * (size_t)nb;
+  if (tid == 0) {
+    s_flags = 0u;
+    s_ops = s_dsts = s_cyc = 0;
+  }
+  for (int x = tid; x < nb; x += kPlanThreads) {
+    W[x] = -1;
+    cnt[x] = 0;
+    P[x] = 0;
+  }
+  __syncthreads();
+  // how many entries name each destination
+  for (int e = tid; e < n; e += kPlanThreads) {
+    const int s = src[e], d = dst[e];
+    if (s < 0 || d < 0) continue;  // padding
+    if (s >= nb || d >= nb)
+      atomicOr(&s_flags, GDN_FLAG_BLOCK_RANGE);
+    else if (d == 0)
+      atomicOr(&s_flags, GDN_FLAG_TRASH_WRITE);
+    else
+      atomicAdd(&P[d], 1);
+  }
+  __syncthreads();
+  for (int e = tid; e < n; e += kPlanThreads) {
+    const int s = src[e], d = dst[e];
+    if (s < 0 || d <= 0 || s >= nb || d >= nb) continue;
+    if (P[d] > 1) {
+      atomicOr(&s_flags, GDN_FLAG_DUPLICATE);
+    } else if (s != d) {
+      W[d] = s;
+      atomicAdd(&cnt[s], 1);
+    }
+  }
+  __syncthreads();
+  int hazard = 0;
+  for (int x = tid; x < nb; x += kPlanThreads) hazard |= cnt[x] > 0 && W[x] >= 0;
+  int32_t *osrc = bw.src(), *obeg = bw.beg(), *ocnt = bw.cnt();
+  // appends a move at place k; DQ[x] becomes where x's destinations go
+  auto emit = [&](int k, int x, uint32_t kind) {
+    const int c = kind == kHold ? 0 : cnt[x];
+    const int at = atomicAdd(&s_dsts, c);
+    osrc[k] = (int32_t)((uint32_t)x | (kind << 30));
+    obeg[k] = at;
+    ocnt[k] = c;
+    if (kind != kHold) DQ[x] = at;
+  };
+  if (!__syncthreads_or(hazard)) {
+    // no source is written (a fork): any order
+    for (int x = tid; x < nb; x += kPlanThreads)
+      if (cnt[x] > 0) emit(atomicAdd(&s_ops, 1), x, kCopy);
+  } else {
+    int rounds = 1;
+    while ((1 << rounds) < nb) ++rounds;
+    // cycles: 2^rounds >= nb steps from a source that reaches one end on it,
+    // and every source of a cycle is such an end
+    for (int x = tid; x < nb; x += kPlanThreads) P[x] = cnt[x] > 0 ? W[x] : -1;
+    __syncthreads();
+    for (int r = 0; r < rounds; ++r) {
+      for (int x = tid; x < nb; x += kPlanThreads) Q[x] = P[x] < 0 ? -1 : P[P[x]];
+      __syncthreads();
+      int32_t* t = P;
+      P = Q;
+      Q = t;
+    }
+    for (int x = tid; x < nb; x += kPlanThreads) Q[x] = 0;
+    __syncthreads();
+    for (int x = tid; x < nb; x += kPlanThreads)
+      if (P[x] >= 0) Q[P[x]] = 1;
+    __syncthreads();
+    // distance of every other source to its root or cycle
+    int32_t* cyc = Q;
+    int32_t* nxt = P;
+    for (int x = tid; x < nb; x += kPlanThreads) {
+      const bool tree = cnt[x] > 0 && W[x] >= 0 && !cyc[x];
+      nxt[x] = tree ? W[x] : x;
+      DP[x] = tree ? 1 : 0;
+    }
+    __syncthreads();
+    // (pointers jump in place, in two phases, as both their arrays are needed)
+    for (int r = 0; r < rounds; ++r) {
+      for (int x0 = 0; x0 < nb; x0 += kPlanThreads) {
+        const int x = x0 + tid;
+        if (x < nb) DQ[x] = DP[x] + DP[nxt[x]];
+      }
+      __syncthreads();
+      int32_t* t = DP;
+      DP = DQ;
+      DQ = t;
+      // DQ is free until the next round: the jumped pointers pass through it
+      for (int x = tid; x < nb; x += kPlanThreads) DQ[x] = nxt[nxt[x]];
+      __syncthreads();
+      t = nxt;
+      nxt = DQ;
+      DQ = t;
+    }
+    // places by falling distance: counting sort (the histogram over nxt)
+    int32_t* hist = nxt;
+    for (int x = tid; x < nb; x += kPlanThreads) hist[x] = 0;
+    __syncthreads();
+    for (int x = tid; x < nb; x += kPlanThreads)
+      if (cnt[x] > 0 && !cyc[x]) atomicAdd(&hist[DP[x]], 1);
+    __syncthreads();
+    int carry = 0;
+    for (int x0 = 0; x0 < nb; x0 += kPlanThreads) {
+      const int x = nb - 1 - (x0 + tid);
+      int total;
+      const int before = cta_scan(x >= 0 ? hist[x] : 0, &total, warp_sums);
+      if (x >= 0) hist[x] = carry + before;
+      carry += total;
+    }
+    if (tid == 0) s_ops = carry;
+    __syncthreads();
+    for (int x = tid; x < nb; x += kPlanThreads)
+      if (cnt[x] > 0 && !cyc[x]) emit(atomicAdd(&hist[DP[x]], 1), x, kCopy);
+    // each cycle by its lowest block: its last source into the spare buffer,
+    // the others in order, then the held one
+    for (int x = tid; x < nb; x += kPlanThreads) {
+      if (!cyc[x]) continue;
+      int len = 1, y = W[x], last = x;
+      while (y > x) {
+        last = y;
+        y = W[y];
+        ++len;
+      }
+      if (y != x) continue;  // a lower block leads this cycle
+      int k = carry + atomicAdd(&s_cyc, len + 1);
+      emit(k++, last, kHold);
+      for (int z = x; z != last; z = W[z]) emit(k++, z, kCopy);
+      emit(k, last, kStoreHeld);
+    }
+  }
+  __syncthreads();
+  int32_t* odst = bw.dst();
+  for (int e = tid; e < n; e += kPlanThreads) {
+    const int s = src[e], d = dst[e];
+    if (s < 0 || d <= 0 || s >= nb || d >= nb || s == d || W[d] != s) continue;
+    odst[atomicAdd(&DQ[s], 1)] = d;
+  }
+  if (tid == 0) {
+    bw.header()[0] = s_ops + s_cyc;
+    if (s_flags) atomicOr(err, s_flags);
+  }
+}
+
+// Plans a compaction: with m live blocks, the i-th live block above m moves to
+// the i-th free block of 1..m, both ascending.  The two lists are disjoint.
+__global__ void __launch_bounds__(kPlanThreads)
+plan_compact_kernel(const int32_t* idx, int32_t* new_idx, int n, int nb, BlockWork bw,
+                    uint32_t* err) {
+  extern __shared__ int32_t plan_smem[];
+  __shared__ unsigned s_flags;
+  __shared__ int warp_sums[32];
+  pdl_wait_then_release();
+  const int tid = threadIdx.x;
+  int32_t* live = nb <= kSmemBlocks ? plan_smem : bw.tmp();
+  int32_t* to = live + nb;
+  if (tid == 0) s_flags = 0u;
+  for (int x = tid; x < nb; x += kPlanThreads) live[x] = 0;
+  __syncthreads();
+  for (int e = tid; e < n; e += kPlanThreads) {
+    const int b = idx[e];
+    if (b >= nb)
+      atomicOr(&s_flags, GDN_FLAG_BLOCK_RANGE);
+    else if (b > 0)
+      live[b] = 1;
+  }
+  __syncthreads();
+  int m = 0;
+  for (int x0 = 0; x0 < nb; x0 += kPlanThreads)
+    m += __syncthreads_count(x0 + tid < nb && live[x0 + tid]);
+  int32_t *osrc = bw.src(), *obeg = bw.beg(), *ocnt = bw.cnt(), *odst = bw.dst();
+  int holes = 0, highs = 0;
+  for (int x0 = 0; x0 < nb; x0 += kPlanThreads) {
+    const int x = x0 + tid;
+    const int hole = x >= 1 && x <= m && !live[x < nb ? x : 0] ? 1 : 0;
+    const int high = x > m && x < nb && live[x < nb ? x : 0] ? 1 : 0;
+    int th, tg;
+    const int rh = holes + cta_scan(hole, &th, warp_sums);
+    const int rg = highs + cta_scan(high, &tg, warp_sums);
+    holes += th;
+    highs += tg;
+    if (hole) odst[rh] = x;
+    if (high) {
+      osrc[rg] = x;
+      obeg[rg] = rg;
+      ocnt[rg] = 1;
+    }
+  }
+  __syncthreads();
+  for (int r = tid; r < highs; r += kPlanThreads) to[osrc[r]] = odst[r];
+  __syncthreads();
+  for (int e = tid; e < n; e += kPlanThreads) {
+    const int b = idx[e];
+    new_idx[e] = b > m && b < nb ? to[b] : b;
+  }
+  if (tid == 0) {
+    bw.header()[0] = highs;
+    if (s_flags) atomicOr(err, s_flags);
+  }
+}
+
+// --- the moves -------------------------------------------------------------
+constexpr int kWarps = 4;
+constexpr int kPiece = 8192;   // bytes of a column, at most
+constexpr int kSlots = 5;      // pieces in flight per warp
+constexpr int kCached = 1024;  // moves (and destinations) kept in shared memory
+struct MoveSmem {
+  unsigned char buf[kWarps][kSlots + 1][kPiece];  // the last one holds a cycle's source
+  uint64_t full[kWarps][kSlots + 1];
+  int32_t src[kCached], beg[kCached], cnt[kCached], dst[kCached];
+};
+static_assert(sizeof(MoveSmem) <= 227 * 1024, "shared memory of one CTA");
+
+struct MoveParams {
+  unsigned char* base;  // block 0 of the first layer moved
+  size_t stride;
+  int nb, layers, piece, cols;  // cols: columns of `piece` bytes per block
+  BlockWork bw;
+  uint32_t* err;
+};
+
+__global__ void __launch_bounds__(kWarps * 32, 1) move_blocks_kernel(MoveParams p) {
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  MoveSmem& sm = *reinterpret_cast<MoveSmem*>(smem_raw);
+  pdl_wait_then_release();
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int ops = p.bw.header()[0];
+  if (ops == 0) return;
+  for (int i = tid; i < kCached; i += kWarps * 32) {
+    if (i < ops) {
+      sm.src[i] = p.bw.src()[i];
+      sm.beg[i] = p.bw.beg()[i];
+      sm.cnt[i] = p.bw.cnt()[i];
+    }
+    if (i < p.nb) sm.dst[i] = p.bw.dst()[i];
+  }
+  if ((tid & 31) == 0) {
+    for (int i = 0; i <= kSlots; ++i) mbar_init(&sm.full[warp][i], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if ((tid & 31) != 0) return;
+  const int32_t *gsrc = p.bw.src(), *gbeg = p.bw.beg(), *gcnt = p.bw.cnt(), *gdst = p.bw.dst();
+  auto src_of = [&](int k) { return (uint32_t)(k < kCached ? sm.src[k] : gsrc[k]); };
+  auto dst_of = [&](int i) { return i < kCached ? sm.dst[i] : gdst[i]; };
+  unsigned char(*buf)[kPiece] = sm.buf[warp];
+  uint64_t* full = sm.full[warp];
+
+  const long long ncol = (long long)p.layers * p.cols;
+  const long long step = (long long)gridDim.x * kWarps;
+  // the load cursor runs ahead of the store cursor over (column, move)
+  long long lcol = (long long)blockIdx.x * kWarps + warp, scol = lcol;
+  int lk = 0, sk = 0;
+  long long loads = 0, stores = 0;  // pieces loaded into, and stored from, the ring
+  long long holds = 0;
+  bool held = false;
+  auto piece_at = [&](long long col, uint32_t* bytes) {
+    const int layer = (int)(col / p.cols), c = (int)(col % p.cols);
+    const size_t off = (size_t)c * p.piece;
+    *bytes = (uint32_t)min((size_t)p.piece, p.stride - off);
+    return p.base + (size_t)layer * p.nb * p.stride + off;
+  };
+  while (scol < ncol) {
+    // loads: as far ahead as the ring (free: all pieces but those being
+    // loaded or stored) and the spare buffer allow
+    while (lcol < ncol) {
+      const uint32_t s = src_of(lk), kind = s >> 30;
+      if (kind == kCopy && loads - stores >= kSlots) break;
+      if (kind == kHold && held) break;
+      if (kind != kStoreHeld) {
+        uint32_t bytes;
+        const unsigned char* at = piece_at(lcol, &bytes) + (size_t)(s & kBlockMask) * p.stride;
+        const int slot = kind == kHold ? kSlots : (int)(loads % kSlots);
+        mbar_arrive_expect_tx(&full[slot], bytes);
+        bulk_g2s(buf[slot], at, bytes, &full[slot]);
+        if (kind == kHold) held = true;
+        else ++loads;
+      }
+      if (++lk == ops) {
+        lk = 0;
+        lcol += step;
+      }
+    }
+    // one move
+    const uint32_t s = src_of(sk), kind = s >> 30;
+    const bool ring = kind == kCopy;
+    const int slot = ring ? (int)(stores % kSlots) : kSlots;
+    if (kind != kStoreHeld) {
+      const uint32_t parity = ring ? (uint32_t)((stores / kSlots) & 1) : (uint32_t)(holds & 1);
+      if (!mbar_wait_bounded(&full[slot], parity)) {
+        atomicOr(p.err, GDN_FLAG_TIMEOUT);
+        // the copies already issued land before the CTA ends
+        for (long long i = stores + (ring ? 1 : 0); i < loads; ++i)
+          mbar_wait_bounded(&full[i % kSlots], (uint32_t)((i / kSlots) & 1));
+        if (held && ring) mbar_wait_bounded(&full[kSlots], (uint32_t)(holds & 1));
+        bulk_wait_all();
+        return;
+      }
+      if (kind == kHold) ++holds;
+    }
+    if (kind != kHold) {
+      uint32_t bytes;
+      unsigned char* at = piece_at(scol, &bytes);
+      const int beg = sk < kCached ? sm.beg[sk] : gbeg[sk];
+      const int cnt = sk < kCached ? sm.cnt[sk] : gcnt[sk];
+      for (int i = 0; i < cnt; ++i)
+        bulk_s2g(at + (size_t)dst_of(beg + i) * p.stride, buf[slot], bytes);
+      bulk_commit();
+      bulk_wait_read_all();  // the piece may be loaded over
+      if (ring) ++stores;
+      else held = false;
+    }
+    if (++sk == ops) {
+      sk = 0;
+      scol += step;
+    }
+  }
+  bulk_wait_all();
+}
+
+// Zeroes the named blocks, a piece at a time from a zeroed shared buffer.
+constexpr int kZero = 16384;
+__global__ void __launch_bounds__(128)
+clear_blocks_kernel(unsigned char* base, size_t stride, int nb, int layers, int cols,
+                    const int32_t* __restrict__ idx, int n, uint32_t* err) {
+  __shared__ __align__(128) unsigned char zero[kZero];
+  pdl_wait_then_release();
+  for (int i = threadIdx.x * 16; i < kZero; i += 128 * 16)
+    *reinterpret_cast<uint4*>(zero + i) = make_uint4(0, 0, 0, 0);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  const long long per = (long long)layers * cols;
+  for (long long u = blockIdx.x; u < per * n; u += gridDim.x) {
+    const int e = (int)(u / per);
+    const long long r = u % per;
+    const int b = idx[e];
+    if (b < 0) continue;  // padding
+    if (b == 0 || b >= nb) {
+      if (r == 0) atomicOr(err, b == 0 ? GDN_FLAG_TRASH_WRITE : GDN_FLAG_BLOCK_RANGE);
+      continue;
+    }
+    const int layer = (int)(r / cols);
+    const size_t off = (size_t)(r % cols) * kZero;
+    bulk_s2g(base + ((size_t)layer * nb + b) * stride + off, zero,
+             (uint32_t)min((size_t)kZero, stride - off));
+    bulk_commit();
+  }
+  bulk_wait_all();
+}
+
+int num_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return 1;
+  return n;
+}
+
+// What every block operation checks on the host.
+int check_call(const gdn_pool* p, int layer, int n, bool pointers) {
+  if (!p) return GDN_ERR_NULL;
+  if (layer < -1 || layer >= p->num_layers || n < 0) return GDN_ERR_RANGE;
+  if (n > 0 && !pointers) return GDN_ERR_NULL;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GDN_ERR_CUDA;
+  return dev == p->device ? GDN_OK : GDN_ERR_DEVICE;
+}
+
+uint32_t* error_word(const gdn_pool* p, int layer) {
+  return reinterpret_cast<uint32_t*>(p->work + (size_t)(layer < 0 ? 0 : layer) *
+                                                   WorkArea::words(p->num_blocks) + kErr);
+}
+unsigned char* first_layer(const gdn_pool* p, int layer) {
+  return p->base + (size_t)(layer < 0 ? 0 : layer) * p->num_blocks * p->stride;
+}
+
+size_t plan_smem_bytes(int nb) {
+  return nb <= kSmemBlocks ? (size_t)kPlanArrays * nb * sizeof(int32_t) : 0;
+}
+
+cudaError_t launch_moves(const gdn_pool* p, int layer, const BlockWork& bw, cudaStream_t s) {
+  MoveParams mp;
+  mp.base = first_layer(p, layer);
+  mp.stride = p->stride;
+  mp.nb = p->num_blocks;
+  mp.layers = layer < 0 ? p->num_layers : 1;
+  mp.bw = bw;
+  mp.err = error_word(p, layer);
+  const int sms = num_sms();
+  // columns: as wide as leaves every warp eight of them, down to 1 KiB
+  mp.piece = kPiece;
+  while (mp.piece > 1024 &&
+         (long long)mp.layers * (long long)((p->stride + mp.piece - 1) / mp.piece) < 8ll * sms * kWarps)
+    mp.piece /= 2;
+  mp.cols = (int)((p->stride + mp.piece - 1) / mp.piece);
+  const long long ctas = ((long long)mp.layers * mp.cols + kWarps - 1) / kWarps;
+  cudaError_t e = cudaFuncSetAttribute(move_blocks_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)sizeof(MoveSmem));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(move_blocks_kernel, dim3((unsigned)(ctas < sms ? ctas : sms)),
+                    dim3(kWarps * 32), sizeof(MoveSmem), s, mp);
+}
+
+template <typename K, typename... Args>
+cudaError_t launch_plan(K kernel, int nb, cudaStream_t s, Args... args) {
+  const size_t smem = plan_smem_bytes(nb);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)plan_smem_bytes(kSmemBlocks));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(1), dim3(kPlanThreads), smem, s, args...);
+}
+
+}  // namespace
+}  // namespace gdn
+
+extern "C" {
+
+int gdn_state_pool_copy_blocks(gdn_pool_t* p, int layer, const int32_t* src, const int32_t* dst,
+                               int n, void* stream) {
+  const int st = gdn::check_call(p, layer, n, src && dst);
+  if (st != GDN_OK || n == 0) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  const gdn::BlockWork bw{p->blk_work, p->num_blocks};
+  if (gdn::launch_plan(gdn::plan_copies_kernel, p->num_blocks, s, src, dst, n, p->num_blocks, bw,
+                       gdn::error_word(p, layer)) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  return gdn::launch_moves(p, layer, bw, s) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+int gdn_state_pool_compact(gdn_pool_t* p, const int32_t* idx, int32_t* new_idx, int n,
+                           void* stream) {
+  const int st = gdn::check_call(p, -1, n, idx && new_idx);
+  if (st != GDN_OK || n == 0) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  const gdn::BlockWork bw{p->blk_work, p->num_blocks};
+  if (gdn::launch_plan(gdn::plan_compact_kernel, p->num_blocks, s, idx, new_idx, n, p->num_blocks,
+                       bw, gdn::error_word(p, -1)) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  return gdn::launch_moves(p, -1, bw, s) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+int gdn_state_pool_clear_blocks(gdn_pool_t* p, int layer, const int32_t* idx, int n,
+                                void* stream) {
+  const int st = gdn::check_call(p, layer, n, idx != nullptr);
+  if (st != GDN_OK || n == 0) return st;
+  const int layers = layer < 0 ? p->num_layers : 1;
+  const int cols = (int)((p->stride + gdn::kZero - 1) / gdn::kZero);
+  const long long units = (long long)layers * cols * n;
+  const long long most = 8ll * gdn::num_sms();
+  if (gdn::launch_pdl(gdn::clear_blocks_kernel, dim3((unsigned)(units < most ? units : most)),
+                      dim3(128), 0, (cudaStream_t)stream, gdn::first_layer(p, layer), p->stride,
+                      p->num_blocks, layers, cols, idx, n,
+                      gdn::error_word(p, layer)) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  return GDN_OK;
+}
+
+}  // extern "C"

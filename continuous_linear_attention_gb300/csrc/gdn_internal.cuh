@@ -54,6 +54,27 @@ struct WorkArea {
   static constexpr size_t words(int num_blocks) { return kHeaderWords + 8 * (size_t)num_blocks + 1; }
 };
 
+// Work area of the pool's block operations (gdn_blocks.cu), int32 words:
+//   [0]           number of moves
+//   [1 .. 15]     unused
+//   then          src[2 * num_blocks]      per move, in order: its source block | kind << 30
+//                 beg[2 * num_blocks]      its first destination in dst[]
+//                 cnt[2 * num_blocks]      how many destinations it has
+//                 dst[num_blocks]          the destinations, grouped by move
+//                 tmp[6 * num_blocks]      the planning kernel's own arrays, where they
+//                                          do not fit into shared memory
+struct BlockWork {
+  int32_t* base;
+  int num_blocks;
+  __host__ __device__ int32_t* header() const { return base; }
+  __host__ __device__ int32_t* src() const { return base + 16; }
+  __host__ __device__ int32_t* beg() const { return base + 16 + 2 * (size_t)num_blocks; }
+  __host__ __device__ int32_t* cnt() const { return base + 16 + 4 * (size_t)num_blocks; }
+  __host__ __device__ int32_t* dst() const { return base + 16 + 6 * (size_t)num_blocks; }
+  __host__ __device__ int32_t* tmp() const { return base + 16 + 7 * (size_t)num_blocks; }
+  static constexpr size_t words(int num_blocks) { return 16 + 13 * (size_t)num_blocks; }
+};
+
 // Everything a forward kernel needs, passed by value.
 struct FwdParams {
   const void* x;        // [T][C] act

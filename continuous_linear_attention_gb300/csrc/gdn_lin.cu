@@ -1,0 +1,467 @@
+// Linear attention with one decay per head over a packed batch, continued
+// from each request's state in a paged pool (the lightning / simple gated
+// linear attention layers among the families the model support tracker
+// lists):
+//   S_t = e^{g_h} S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t
+// with S [d_k][d_v] fp32 per request and head.
+//
+// This file: the recurrent form, the batch scheduler and the C entry points.
+// The recurrent kernel is bound by HBM: a head's state (64 KiB at d = 128) is
+// read once and written once whatever the number of tokens.  A CTA owns 32
+// columns v of one head's state (the columns are independent of each other),
+// every thread 4 columns of d/16 rows in registers; all of a CTA's state
+// loads are issued before anything else, and six CTAs per SM keep about
+// 100 KB of reads in flight.
+#include <cuda_runtime.h>
+
+#include <new>
+
+#include "gdn_lin.cuh"
+#include "gdn_pool.cuh"
+#include "gdn_ptx.cuh"
+
+namespace gdn {
+namespace {
+
+// --- recurrent form ----------------------------------------------------------
+constexpr int kRecThreads = 128;
+constexpr int kSlice = 32;                          // state columns per CTA
+constexpr int kColT = kSlice / 4;                   // threads across the columns
+constexpr int kRowT = kRecThreads / kColT;          // threads across the rows
+constexpr int kTile = 16;                           // tokens staged at a time
+// calls of up to this many sequences check the batch in every CTA, while its
+// state loads are in flight, which saves the scheduler's launch
+constexpr int kSelfCheck = 512;
+
+// kN consecutive elements as fp32 (kN * sizeof(T) aligned).
+template <typename T, int kN> struct Vec;
+template <int kN> struct Vec<float, kN> {
+  static __device__ __forceinline__ void load(const float* p, float* o) {
+    if constexpr (kN % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < kN; i += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p + i);
+        o[i] = v.x; o[i + 1] = v.y; o[i + 2] = v.z; o[i + 3] = v.w;
+      }
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(p);
+      o[0] = v.x; o[1] = v.y;
+    }
+  }
+};
+template <int kN> struct Vec<__nv_bfloat16, kN> {
+  static __device__ __forceinline__ void unpack(uint32_t w, float* o) {
+    o[0] = __uint_as_float(w << 16);
+    o[1] = __uint_as_float(w & 0xffff0000u);
+  }
+  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* o) {
+    if constexpr (kN == 8) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      unpack(v.x, o); unpack(v.y, o + 2); unpack(v.z, o + 4); unpack(v.w, o + 6);
+    } else if constexpr (kN == 4) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      unpack(v.x, o); unpack(v.y, o + 2);
+    } else {
+      unpack(*reinterpret_cast<const uint32_t*>(p), o);
+    }
+  }
+};
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+template <typename T, int D>
+struct RecSmem {
+  T q[2][kTile][D], k[2][kTile][D], v[2][kTile][kSlice];
+  float part[kTile][kRecThreads / 32][kSlice];
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kRecThreads)
+lin_recurrent_kernel(LinParams p) {
+  constexpr int kRows = D / kRowT;      // state rows per thread
+  constexpr int kSlices = D / kSlice;
+  __shared__ __align__(16) RecSmem<T, D> sm;
+  if (p.late)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  else
+    pdl_wait_then_release();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int32_t* hdr = p.work.header();
+  const int slice = blockIdx.x % kSlices;
+  const int h = (blockIdx.x / kSlices) % p.H;
+  int s = blockIdx.x / (kSlices * p.H);
+  if (p.listed) {
+    if (s >= hdr[kNDec]) {
+      if (p.late) asm volatile("griddepcontrol.wait;" ::: "memory");
+      return;
+    }
+    s = p.work.dec()[s];
+  }
+  const int row0 = p.cu[s], len = p.cu[s + 1] - row0;
+  const int blk = p.blk[s];
+  // loads may be issued for what looks right here; nothing is written before
+  // the whole batch has been checked
+  bool active = len > 0 && blk > 0 && blk < p.num_blocks;
+  if (!p.listed)
+    active = active && row0 >= 0 && len <= p.T && row0 <= p.T - len && (p.hint == 0 || len <= p.hint);
+  const int c0 = slice * kSlice + (tid % kColT) * 4;  // this thread's columns
+  const int r0 = (tid / kColT) * kRows;               // and rows
+  float* S_g = reinterpret_cast<float*>(p.layer_base + (size_t)(active ? blk : 0) * p.stride) +
+               ((size_t)h * D + r0) * D + c0;
+  float4 S[kRows];
+  const bool past = active && p.has_past[s];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+    S[i] = past ? *reinterpret_cast<const float4*>(S_g + (size_t)i * D) : make_float4(0.f, 0.f, 0.f, 0.f);
+  const DecayPair a = decay_pair(finite_decay(p.log_decay[h]));
+  const int hk = h / p.group;
+  const T* q = static_cast<const T*>(p.q) + (size_t)(active ? row0 : 0) * p.ldq + (size_t)h * D;
+  const T* k = static_cast<const T*>(p.k) + (size_t)(active ? row0 : 0) * p.ldk + (size_t)hk * D;
+  const T* v = static_cast<const T*>(p.v) + (size_t)(active ? row0 : 0) * p.ldv + (size_t)hk * D +
+               slice * kSlice;
+  T* out = static_cast<T*>(p.out) + (size_t)(active ? row0 : 0) * p.ldo + (size_t)h * D +
+           slice * kSlice;
+
+  // one token: S <- e^g S + k v^T, and this thread's part of S^T q
+  auto token = [&](const float* qr, const float* kr, const float* vc) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      float4 t = S[i];
+      t.x = fmaf(a.hi, t.x, fmaf(a.lo, t.x, kr[i] * vc[0]));
+      t.y = fmaf(a.hi, t.y, fmaf(a.lo, t.y, kr[i] * vc[1]));
+      t.z = fmaf(a.hi, t.z, fmaf(a.lo, t.z, kr[i] * vc[2]));
+      t.w = fmaf(a.hi, t.w, fmaf(a.lo, t.w, kr[i] * vc[3]));
+      S[i] = t;
+      o.x = fmaf(qr[i], t.x, o.x);
+      o.y = fmaf(qr[i], t.y, o.y);
+      o.z = fmaf(qr[i], t.z, o.z);
+      o.w = fmaf(qr[i], t.w, o.w);
+    }
+#pragma unroll
+    for (int w = kColT; w < 32; w <<= 1) {
+      o.x += __shfl_xor_sync(0xffffffffu, o.x, w);
+      o.y += __shfl_xor_sync(0xffffffffu, o.y, w);
+      o.z += __shfl_xor_sync(0xffffffffu, o.z, w);
+      o.w += __shfl_xor_sync(0xffffffffu, o.w, w);
+    }
+    return o;
+  };
+  float q0[kRows], k0[kRows], v0[4];
+  if (active && len == 1) {
+    Vec<T, kRows>::load(q + r0, q0);
+    Vec<T, kRows>::load(k + r0, k0);
+    Vec<T, 4>::load(v + (tid % kColT) * 4, v0);
+  }
+  if (!p.listed) {
+    // the batch: cu_seqlens from 0 to T and never falling, no block named
+    // twice by sequences with tokens
+    int bad = 0, twice = 0;
+    for (int i = tid; i < p.N; i += kRecThreads) {
+      const int lo = p.cu[i], hi = p.cu[i + 1];
+      bad |= hi < lo;
+      twice |= i != s && hi > lo && p.blk[i] == blk;
+    }
+    if (tid == 0) bad |= p.cu[0] != 0 || p.cu[p.N] != p.T;
+    bad = __syncthreads_or(bad);
+    twice = __syncthreads_or(twice);
+    unsigned flags = 0;
+    if (bad) {
+      flags = GDN_FLAG_SEQLENS;
+    } else if (len > 0 && blk >= 0) {
+      if (blk >= p.num_blocks) flags = GDN_FLAG_BLOCK_RANGE;
+      else if (blk == 0) flags = GDN_FLAG_TRASH_WRITE;
+      else if (twice) flags = GDN_FLAG_DUPLICATE;
+      else if (p.hint > 0 && len > p.hint) flags = GDN_FLAG_HINT;
+    }
+    if (flags && tid == 0 && h == 0 && slice == 0) atomicOr((unsigned*)&hdr[kErr], flags);
+    if (flags) active = false;
+  }
+  if (active && len == 1) {
+    const float4 o = token(q0, k0, v0);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) *reinterpret_cast<float4*>(S_g + (size_t)i * D) = S[i];
+    if (lane < kColT) *reinterpret_cast<float4*>(&sm.part[0][warp][lane * 4]) = o;
+    __syncthreads();
+    if (tid < kSlice) {
+      float acc = 0.f;
+#pragma unroll
+      for (int w = 0; w < kRecThreads / 32; ++w) acc += sm.part[0][w][tid];
+      out[tid] = from_f32<T>(acc * p.scale);
+    }
+  } else if (active) {
+    // tokens in tiles, staged one tile ahead
+    auto stage = [&](int t0, int b) {
+      const int n = min(kTile, len - t0);
+      constexpr int kRow16 = D * (int)sizeof(T) / 16, kSl16 = kSlice * (int)sizeof(T) / 16;
+      constexpr int kPer = 16 / (int)sizeof(T);
+      for (int i = tid; i < n * kRow16; i += kRecThreads) {
+        const int t = i / kRow16, c = (i % kRow16) * kPer;
+        cp_async16(&sm.q[b][t][c], q + (size_t)(t0 + t) * p.ldq + c);
+        cp_async16(&sm.k[b][t][c], k + (size_t)(t0 + t) * p.ldk + c);
+      }
+      for (int i = tid; i < n * kSl16; i += kRecThreads) {
+        const int t = i / kSl16, c = (i % kSl16) * kPer;
+        cp_async16(&sm.v[b][t][c], v + (size_t)(t0 + t) * p.ldv + c);
+      }
+      cp_async_commit();
+    };
+    stage(0, 0);
+    for (int t0 = 0, b = 0; t0 < len; t0 += kTile, b ^= 1) {
+      if (t0 + kTile < len) {
+        stage(t0 + kTile, b ^ 1);
+        cp_async_wait<1>();
+      } else {
+        cp_async_wait<0>();
+      }
+      __syncthreads();  // the tile has landed, and the last one's sums are read
+      const int n = min(kTile, len - t0);
+      for (int t = 0; t < n; ++t) {
+        float qr[kRows], kr[kRows], vc[4];
+        Vec<T, kRows>::load(&sm.q[b][t][r0], qr);
+        Vec<T, kRows>::load(&sm.k[b][t][r0], kr);
+        Vec<T, 4>::load(&sm.v[b][t][(tid % kColT) * 4], vc);
+        const float4 o = token(qr, kr, vc);
+        if (lane < kColT) *reinterpret_cast<float4*>(&sm.part[t][warp][lane * 4]) = o;
+      }
+      __syncthreads();  // the tile's sums are there, and its buffer may be staged over
+      for (int i = tid; i < n * kSlice; i += kRecThreads) {
+        const int t = i / kSlice, c = i % kSlice;
+        float acc = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRecThreads / 32; ++w) acc += sm.part[t][w][c];
+        out[(size_t)(t0 + t) * p.ldo + c] = from_f32<T>(acc * p.scale);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) *reinterpret_cast<float4*>(S_g + (size_t)i * D) = S[i];
+  }
+  if (p.late) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// --- scheduler ---------------------------------------------------------------
+constexpr int kSchedThreads = 1024;
+
+// One CTA.  Checks the batch as the pool's contract demands and lists its
+// sequences (in no particular order: every one is computed by itself).
+__global__ void __launch_bounds__(kSchedThreads)
+lin_schedule_kernel(LinParams p, int short_max) {
+  __shared__ unsigned s_flags;
+  __shared__ int s_dec, s_pre;
+  pdl_wait_then_release();
+  const int tid = threadIdx.x, N = p.N, nb = p.num_blocks;
+  int32_t* hdr = p.work.header();
+  int32_t* uses = p.work.blk_count();
+  if (tid == 0) {
+    s_flags = 0u;
+    s_dec = s_pre = 0;
+  }
+  for (int i = tid; i < nb; i += kSchedThreads) uses[i] = 0;
+  int bad = tid == 0 && (p.cu[0] != 0 || p.cu[N] != p.T);
+  for (int s = tid; s < N; s += kSchedThreads) bad |= p.cu[s + 1] < p.cu[s];
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) {
+      atomicOr((unsigned*)&hdr[kErr], GDN_FLAG_SEQLENS);
+      hdr[kNDec] = hdr[kNPre] = 0;
+    }
+    return;
+  }
+  for (int s = tid; s < N; s += kSchedThreads) {
+    const int b = p.blk[s];
+    if (b < 0 || p.cu[s + 1] == p.cu[s]) continue;  // padding or empty
+    if (b >= nb) atomicOr(&s_flags, GDN_FLAG_BLOCK_RANGE);
+    else if (b == 0) atomicOr(&s_flags, GDN_FLAG_TRASH_WRITE);
+    else atomicAdd(&uses[b], 1);
+  }
+  __syncthreads();
+  for (int s = tid; s < N; s += kSchedThreads) {
+    const int b = p.blk[s], len = p.cu[s + 1] - p.cu[s];
+    if (b <= 0 || b >= nb || len == 0) continue;
+    if (atomicAdd(&uses[b], 0) > 1) {
+      atomicOr(&s_flags, GDN_FLAG_DUPLICATE);
+    } else if (p.hint > 0 && len > p.hint) {
+      atomicOr(&s_flags, GDN_FLAG_HINT);
+    } else if (len <= short_max) {
+      p.work.dec()[atomicAdd(&s_dec, 1)] = s;
+    } else {
+      p.work.pre()[atomicAdd(&s_pre, 1)] = s;
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    if (s_flags) atomicOr((unsigned*)&hdr[kErr], s_flags);
+    hdr[kNDec] = s_dec;
+    hdr[kNPre] = s_pre;
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_rec(const LinParams& p, int max_items, cudaStream_t s) {
+  const long long ctas = (long long)max_items * p.H * (D / kSlice);
+  return launch_pdl(lin_recurrent_kernel<T, D>, dim3((unsigned)ctas), dim3(kRecThreads), 0, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_lin_recurrent(const LinParams& p, int d, int act, int max_items,
+                                 cudaStream_t s) {
+  if (max_items <= 0) return cudaSuccess;
+  if (act == GDN_F32) {
+    if (d == 32) return launch_rec<float, 32>(p, max_items, s);
+    if (d == 64) return launch_rec<float, 64>(p, max_items, s);
+    return launch_rec<float, 128>(p, max_items, s);
+  }
+  if (d == 32) return launch_rec<__nv_bfloat16, 32>(p, max_items, s);
+  if (d == 64) return launch_rec<__nv_bfloat16, 64>(p, max_items, s);
+  return launch_rec<__nv_bfloat16, 128>(p, max_items, s);
+}
+
+cudaError_t launch_lin_schedule(const LinParams& p, int short_max, cudaStream_t s) {
+  return launch_pdl(lin_schedule_kernel, dim3(1), dim3(kSchedThreads), 0, s, p, short_max);
+}
+
+namespace {
+
+size_t roundup(size_t v, size_t m) { return (v + m - 1) / m * m; }
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+int check_lin_dims(int num_blocks, int num_layers, int H, int d, int act, size_t align) {
+  if (num_blocks < 2 || num_layers < 1) return GDN_ERR_RANGE;
+  if (H < 1 || H > 4096 || (d != 32 && d != 64 && d != 128)) return GDN_ERR_DIMS;
+  if (act != GDN_F32 && act != GDN_BF16) return GDN_ERR_DIMS;
+  if (align != 0 && (align < 128 || (align & (align - 1)) != 0)) return GDN_ERR_DIMS;
+  if ((long long)num_blocks * num_layers > (1ll << 30)) return GDN_ERR_RANGE;
+  return GDN_OK;
+}
+
+size_t lin_stride(int H, int d, size_t align) {
+  return roundup((size_t)H * d * d * sizeof(float), align > 128 ? align : 128);
+}
+
+}  // namespace
+}  // namespace gdn
+
+extern "C" {
+
+int gdn_lin_pool_layout_for(int num_blocks, int num_layers, int num_heads, int d, int act,
+                            size_t block_align, size_t* block_stride, size_t* total_bytes) {
+  const int st = gdn::check_lin_dims(num_blocks, num_layers, num_heads, d, act, block_align);
+  if (st != GDN_OK) return st;
+  const size_t stride = gdn::lin_stride(num_heads, d, block_align);
+  if (block_stride) *block_stride = stride;
+  if (total_bytes) *total_bytes = stride * (size_t)num_blocks * (size_t)num_layers;
+  return GDN_OK;
+}
+
+int gdn_lin_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int num_heads, int d,
+                        int act, size_t block_align, void* device_mem, size_t device_bytes) {
+  if (!out) return GDN_ERR_NULL;
+  *out = nullptr;
+  int st = gdn::check_lin_dims(num_blocks, num_layers, num_heads, d, act, block_align);
+  if (st != GDN_OK) return st;
+  const size_t stride = gdn::lin_stride(num_heads, d, block_align);
+  const size_t total = stride * (size_t)num_blocks * (size_t)num_layers;
+  if (device_mem) {
+    if (device_bytes < total) return GDN_ERR_NOMEM;
+    if (((uintptr_t)device_mem & 255u) != 0) return GDN_ERR_ALIGN;
+  }
+  gdn_pool* p = new (std::nothrow) gdn_pool();
+  if (!p) return GDN_ERR_NOMEM;
+  p->kind = 2;
+  p->num_blocks = num_blocks;
+  p->num_layers = num_layers;
+  p->Hv = num_heads;
+  p->dk = p->dv = d;
+  p->act = act;
+  p->last_path = GDN_PREFILL_NONE;
+  p->stride = stride;
+  p->total = total;
+  st = gdn::pool_allocate(p, device_mem);
+  if (st != GDN_OK) {
+    delete p;
+    return st;
+  }
+  *out = p;
+  return GDN_OK;
+}
+
+int gdn_lin_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* k, const void* v,
+                           int64_t ldq, int64_t ldk, int64_t ldv, int num_kv_heads,
+                           const int32_t* cu_seqlens, const int32_t* state_block_idx,
+                           const uint8_t* has_past, const float* log_decay, float scale, void* out,
+                           int64_t ldo, int T, int N, int max_seqlen_hint, void* stream) {
+  if (!p) return GDN_ERR_NULL;
+  if (p->kind != 2) return GDN_ERR_DIMS;
+  if (layer < 0 || layer >= p->num_layers || T < 0 || N < 0 || max_seqlen_hint < 0)
+    return GDN_ERR_RANGE;
+  if (num_kv_heads < 1 || p->Hv % num_kv_heads != 0) return GDN_ERR_DIMS;
+  if (N == 0) return T == 0 ? GDN_OK : GDN_ERR_RANGE;
+  if (!cu_seqlens || !state_block_idx || !has_past || !log_decay) return GDN_ERR_NULL;
+  if (T > 0 && (!q || !k || !v || !out)) return GDN_ERR_NULL;
+  const int d = p->dk, H = p->Hv;
+  const int per16 = p->act == GDN_F32 ? 4 : 8;
+  if (T > 0) {
+    if (!gdn::aligned16(q) || !gdn::aligned16(k) || !gdn::aligned16(v) || !gdn::aligned16(out) ||
+        ldq % per16 != 0 || ldk % per16 != 0 || ldv % per16 != 0 || ldo % per16 != 0)
+      return GDN_ERR_ALIGN;
+    const int64_t qcols = (int64_t)H * d, kcols = (int64_t)num_kv_heads * d;
+    const int64_t most = (int64_t)1 << 38;
+    if (ldq < qcols || ldo < qcols || ldk < kcols || ldv < kcols || ldq > most || ldk > most ||
+        ldv > most || ldo > most)
+      return GDN_ERR_RANGE;
+  }
+  int max_items = N < p->num_blocks - 1 ? N : p->num_blocks - 1;
+  if (max_items > T) max_items = T;
+  if ((long long)(N <= gdn::kSelfCheck ? N : max_items) * H * (d / gdn::kSlice) > 0x7fffffffll)
+    return GDN_ERR_RANGE;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GDN_ERR_CUDA;
+  if (dev != p->device) return GDN_ERR_DEVICE;
+
+  gdn::LinParams lp = {};
+  lp.q = q;
+  lp.k = k;
+  lp.v = v;
+  lp.out = out;
+  lp.ldq = ldq;
+  lp.ldk = ldk;
+  lp.ldv = ldv;
+  lp.ldo = ldo;
+  lp.cu = cu_seqlens;
+  lp.blk = state_block_idx;
+  lp.has_past = has_past;
+  lp.log_decay = log_decay;
+  lp.scale = scale;
+  lp.layer_base = p->base + (size_t)layer * p->num_blocks * p->stride;
+  lp.stride = p->stride;
+  lp.T = T;
+  lp.N = N;
+  lp.H = H;
+  lp.group = H / num_kv_heads;
+  lp.num_blocks = p->num_blocks;
+  lp.hint = max_seqlen_hint;
+  lp.work.base = p->work + (size_t)layer * gdn::WorkArea::words(p->num_blocks);
+  lp.work.num_blocks = p->num_blocks;
+
+  cudaStream_t s = (cudaStream_t)stream;
+  p->last_path = T > 1 && max_seqlen_hint != 1 ? GDN_PREFILL_SERIAL : GDN_PREFILL_NONE;
+  lp.listed = N > gdn::kSelfCheck;
+  if (lp.listed && gdn::launch_lin_schedule(lp, INT32_MAX, s) != cudaSuccess) return GDN_ERR_CUDA;
+  if (p->ev_before && cudaEventRecord(p->ev_before, s) != cudaSuccess) return GDN_ERR_CUDA;
+  if (gdn::launch_lin_recurrent(lp, d, p->act, lp.listed ? max_items : N, s) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  if (p->ev_after && cudaEventRecord(p->ev_after, s) != cudaSuccess) return GDN_ERR_CUDA;
+  return GDN_OK;
+}
+
+}  // extern "C"

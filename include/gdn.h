@@ -135,6 +135,46 @@ int gdn_state_pool_layout(const gdn_pool_t* pool, size_t* block_stride, size_t* 
  * and never shared).  dst must not be 0 (the trash block).  Stream-ordered. */
 int gdn_state_pool_copy_block(gdn_pool_t* pool, int layer, int src, int dst, void* stream);
 
+/* Block operations from device-side indices, over one layer or (layer = -1)
+ * all of them, on a pool of any kind.  Each is one planning and one moving
+ * kernel (clear: one kernel), stream-ordered, graph-capturable, and allocates
+ * nothing.  Calls on one pool must be ordered on one stream with each other
+ * and with its forwards (they share a work area).  Negative indices are
+ * padding entries and skipped.  Bad indices raise a flag in the layer's error
+ * word (layer = -1: layer 0's) and their entries are skipped:
+ * GDN_FLAG_BLOCK_RANGE (>= num_blocks), GDN_FLAG_TRASH_WRITE (block 0 as a
+ * destination), GDN_FLAG_DUPLICATE (a destination named by two entries: both
+ * skipped).  n >= 0; n = 0 does nothing.
+ *
+ * gdn_state_pool_copy_blocks: block dst[i] <- block src[i] for all i at once:
+ * every source is read before any block is overwritten, so that a block may
+ * be a source of some entries and the destination of another (a beam search's
+ * reorder in place, swaps and cycles among it), and a source may be named by
+ * any number of entries (a fork).  Block 0 as a source gives zeros.
+ *   src, dst : [n] int32 device */
+int gdn_state_pool_copy_blocks(gdn_pool_t* pool, int layer, const int32_t* src, const int32_t* dst,
+                               int n, void* stream);
+
+/* Blocks idx[i] <- zeros (a freed block gives nothing of its request away; a
+ * forward needs no cleared block, as has_past = 0 reads the trash block).
+ * The same index may be named twice.
+ *   idx : [n] int32 device */
+int gdn_state_pool_clear_blocks(gdn_pool_t* pool, int layer, const int32_t* idx, int n,
+                                void* stream);
+
+/* Move the live blocks of all layers to the lowest indices: with m different
+ * blocks named in idx, the i-th of those above m moves to the i-th index of
+ * 1..m that is not named, both in ascending order; the others stay.  Blocks
+ * that are not named are free: what they hold afterwards is unspecified
+ * (those moved into hold the moved ones).  Entries <= 0 or out of range
+ * (flagged) are passed through; entries that name the same block get the same
+ * new index.
+ *   idx     : [n] int32 device, the block of each request
+ *   new_idx : [n] int32 device, receives the block where it is afterwards;
+ *             may be idx itself */
+int gdn_state_pool_compact(gdn_pool_t* pool, const int32_t* idx, int32_t* new_idx, int n,
+                           void* stream);
+
 /* Prefill scratch of the pool.  Sequences longer than one token run as two
  * kernels when the pool has scratch for the call: a chunk-parallel kernel
  * (conv, norms, gates and the state-independent products of every 64-token
@@ -279,6 +319,48 @@ int gdn_ssd_varlen_forward(gdn_pool_t* pool, int layer, const void* xbc, const v
                            const int32_t* cu_seqlens, const int32_t* state_block_idx,
                            const uint8_t* has_past, const gdn_ssd_weights_t* weights, void* y,
                            int T, int N, int max_seqlen_hint, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Linear attention with one fixed decay per head (the lightning / simple
+ * gated linear attention layers among the linear-attention families of the
+ * model support tracker): per token and head h, with kv head h / (H / Hkv),
+ *   S_t = e^{g_h} S_{t-1} + k_t v_t^T            (S [d][d] fp32: row k, column v)
+ *   o_t = scale * S_t^T q_t
+ * There is no convolution and no gate from the data; feature maps, norms and
+ * rotary positions are the caller's, before this call.  The pool is the same
+ * kind of paged pool (block 0 = trash, one block per request, overwritten in
+ * place; destroy, layout, get_error, timing events and the block operations
+ * apply to it), with a block holding the state [H][d][d] fp32 at offset 0,
+ * element S_h[k][v] at ((h*d)+k)*d + v, and
+ *   block_stride = roundup(H*d*d*4, max(128, block_align)).
+ * Supported: d in {32, 64, 128}, 1 <= H <= 4096, GDN_F32 or GDN_BF16 (q, k,
+ * v, out).  gdn_state_pool_reserve has nothing to do for it. */
+int gdn_lin_pool_layout_for(int num_blocks, int num_layers, int num_heads, int d, int act_dtype,
+                            size_t block_align, size_t* block_stride, size_t* total_bytes);
+
+/* As gdn_state_pool_create, for a decayed linear attention pool. */
+int gdn_lin_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int num_heads, int d,
+                        int act_dtype, size_t block_align, void* device_mem, size_t device_bytes);
+
+/* Forward of one decayed linear attention layer over a packed batch.
+ *   q            : T rows of H heads x d, activation dtype, row pitch ldq elements
+ *   k, v         : T rows of Hkv heads x d, row pitches ldk, ldv (H % Hkv == 0)
+ *   log_decay    : [H] fp32 device, g_h <= 0; -inf is no memory (e^{g} = 0)
+ *   out          : T rows of H heads x d, activation dtype, row pitch ldo;
+ *                  rows of skipped or padding sequences are not written
+ * q, k, v and out are 16-byte aligned and their pitches multiples of 16 bytes
+ * (GDN_ERR_ALIGN); they may be views of one wider row (a fused projection);
+ * out must not overlap them.  cu_seqlens, state_block_idx, has_past, T, N,
+ * max_seqlen_hint, the skip rules, error flags and stream contract: as
+ * gdn_varlen_forward.  The pool must come from gdn_lin_pool_create
+ * (GDN_ERR_DIMS otherwise).  An output row depends on its own and earlier
+ * tokens of its sequence only, whatever the later ones hold (NaN and
+ * infinities among them).  Never synchronises; graph-capturable. */
+int gdn_lin_varlen_forward(gdn_pool_t* pool, int layer, const void* q, const void* k,
+                           const void* v, int64_t ldq, int64_t ldk, int64_t ldv, int num_kv_heads,
+                           const int32_t* cu_seqlens, const int32_t* state_block_idx,
+                           const uint8_t* has_past, const float* log_decay, float scale, void* out,
+                           int64_t ldo, int T, int N, int max_seqlen_hint, void* stream);
 
 /* Bytes of prefill scratch the split prefill needs for calls of at most
  * max_tokens tokens (any number of sequences) on a pool of these dimensions
