@@ -20,6 +20,7 @@
 // pieces go global -> shared -> global by bulk copies issued by one lane, so
 // registers hold none of the data.
 #include "gdn_internal.cuh"
+#include "gdn_cta.cuh"
 #include "gdn_pool.cuh"
 #include "gdn_ptx.cuh"
 
@@ -33,33 +34,6 @@ constexpr int kPlanArrays = 6;
 // kinds of a move, in bits 30-31 of its source
 enum Kind : uint32_t { kCopy = 0, kHold = 1, kStoreHeld = 2 };
 constexpr uint32_t kBlockMask = (1u << 30) - 1;
-
-// Exclusive sum of v over the CTA's threads before this one, and the total.
-__device__ int cta_scan(int v, int* total, int* warp_sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    int w = warp_sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    warp_sums[lane] = w;
-  }
-  __syncthreads();
-  const int before = warp > 0 ? warp_sums[warp - 1] : 0;
-  *total = warp_sums[31];
-  __syncthreads();
-  return before + x - v;
-}
 
 // Orders the moves of a copy list (see above) into bw.
 __global__ void __launch_bounds__(kPlanThreads)
@@ -426,14 +400,6 @@ clear_blocks_kernel(unsigned char* base, size_t stride, int nb, int layers, int 
     bulk_commit();
   }
   bulk_wait_all();
-}
-
-int num_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    return 1;
-  return n;
 }
 
 // What every block operation checks on the host.

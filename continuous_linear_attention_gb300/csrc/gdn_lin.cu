@@ -16,6 +16,7 @@
 
 #include <new>
 
+#include "gdn_cta.cuh"
 #include "gdn_lin.cuh"
 #include "gdn_pool.cuh"
 #include "gdn_ptx.cuh"
@@ -85,34 +86,20 @@ struct RecSmem {
   float part[kTile][kRecThreads / 32][kSlice];
 };
 
+// Sequence s, head h, columns 32 slice ..: read, advanced by all its tokens
+// and written back.  check: nothing has looked at the batch yet.
 template <typename T, int D>
-__global__ void __launch_bounds__(kRecThreads)
-lin_recurrent_kernel(LinParams p) {
+__device__ __forceinline__ void recurrent_unit(const LinParams& p, RecSmem<T, D>& sm, int s, int h,
+                                               int slice, bool check) {
   constexpr int kRows = D / kRowT;      // state rows per thread
-  constexpr int kSlices = D / kSlice;
-  __shared__ __align__(16) RecSmem<T, D> sm;
-  if (p.late)
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  else
-    pdl_wait_then_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int32_t* hdr = p.work.header();
-  const int slice = blockIdx.x % kSlices;
-  const int h = (blockIdx.x / kSlices) % p.H;
-  int s = blockIdx.x / (kSlices * p.H);
-  if (p.listed) {
-    if (s >= hdr[kNDec]) {
-      if (p.late) asm volatile("griddepcontrol.wait;" ::: "memory");
-      return;
-    }
-    s = p.work.dec()[s];
-  }
   const int row0 = p.cu[s], len = p.cu[s + 1] - row0;
   const int blk = p.blk[s];
   // loads may be issued for what looks right here; nothing is written before
   // the whole batch has been checked
   bool active = len > 0 && blk > 0 && blk < p.num_blocks;
-  if (!p.listed)
+  if (check)
     active = active && row0 >= 0 && len <= p.T && row0 <= p.T - len && (p.hint == 0 || len <= p.hint);
   const int c0 = slice * kSlice + (tid % kColT) * 4;  // this thread's columns
   const int r0 = (tid / kColT) * kRows;               // and rows
@@ -163,7 +150,7 @@ lin_recurrent_kernel(LinParams p) {
     Vec<T, kRows>::load(k + r0, k0);
     Vec<T, 4>::load(v + (tid % kColT) * 4, v0);
   }
-  if (!p.listed) {
+  if (check) {
     // the batch: cu_seqlens from 0 to T and never falling, no block named
     // twice by sequences with tokens
     int bad = 0, twice = 0;
@@ -246,25 +233,73 @@ lin_recurrent_kernel(LinParams p) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) *reinterpret_cast<float4*>(S_g + (size_t)i * D) = S[i];
   }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kRecThreads)
+lin_recurrent_kernel(LinParams p) {
+  constexpr int kSlices = D / kSlice;
+  __shared__ __align__(16) RecSmem<T, D> sm;
+  // late: launched behind the chunk kernel, whose idle SMs it takes without
+  // waiting for it (other sequences, other blocks); it waits before it ends
+  if (p.late)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  else
+    pdl_wait_then_release();
+  const int slice = blockIdx.x % kSlices;
+  const int h = (blockIdx.x / kSlices) % p.H;
+  int s = blockIdx.x / (kSlices * p.H);
+  const bool here = !p.listed || s < p.work.header()[kNDec];
+  if (here) {
+    if (p.listed) s = p.work.dec()[s];
+    recurrent_unit<T, D>(p, sm, s, h, slice, !p.listed);
+  }
   if (p.late) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// The chains that the chunked form has marked, whose blocks still hold the
+// old state.
+__global__ void __launch_bounds__(kRecThreads) lin_redo_kernel(LinParams p) {
+  constexpr int kSlices = 128 / kSlice;
+  __shared__ __align__(16) RecSmem<__nv_bfloat16, 128> sm;
+  pdl_wait_then_release();
+  const int32_t* hdr = p.work.header();
+  if (!hdr[kLinBad]) return;
+  const long long n = (long long)hdr[kNPre] * p.H * kSlices;
+  for (long long u = blockIdx.x; u < n; u += gridDim.x) {
+    const long long chain = u / kSlices;
+    if (!p.bad[chain]) continue;
+    __syncthreads();
+    recurrent_unit<__nv_bfloat16, 128>(p, sm, p.work.pre()[chain / p.H], (int)(chain % p.H),
+                                       (int)(u % kSlices), false);
+  }
 }
 
 // --- scheduler ---------------------------------------------------------------
 constexpr int kSchedThreads = 1024;
 
-// One CTA.  Checks the batch as the pool's contract demands and lists its
-// sequences (in no particular order: every one is computed by itself).
+constexpr int kSortMax = 8192;  // long sequences that are put in order
+constexpr int kMinSegment = 8;  // chunks
+
+// One CTA.  Checks the batch as the pool's contract demands, lists its
+// sequences and cuts the long ones into segments.
 __global__ void __launch_bounds__(kSchedThreads)
-lin_schedule_kernel(LinParams p, int short_max) {
+lin_schedule_kernel(LinParams p, int short_max, int num_sms) {
   __shared__ unsigned s_flags;
-  __shared__ int s_dec, s_pre;
+  __shared__ int s_dec, s_pre, s_segs;
+  __shared__ unsigned long long s_total;
+  __shared__ int32_t chunks[kSortMax];
+  __shared__ int warp_sums[32];
   pdl_wait_then_release();
   const int tid = threadIdx.x, N = p.N, nb = p.num_blocks;
   int32_t* hdr = p.work.header();
   int32_t* uses = p.work.blk_count();
   if (tid == 0) {
     s_flags = 0u;
-    s_dec = s_pre = 0;
+    s_dec = s_pre = s_segs = 0;
+    s_total = 0;
+    hdr[kLinStateItems] = hdr[kLinHead] = hdr[kLinItems] = hdr[kLinStateHead] = 0;
+    hdr[kLinSplit] = hdr[kLinSegChunks] = hdr[kLinBad] = 0;
   }
   for (int i = tid; i < nb; i += kSchedThreads) uses[i] = 0;
   int bad = tid == 0 && (p.cu[0] != 0 || p.cu[N] != p.T);
@@ -284,6 +319,7 @@ lin_schedule_kernel(LinParams p, int short_max) {
     else atomicAdd(&uses[b], 1);
   }
   __syncthreads();
+  int32_t *pre = p.work.pre(), *pre_tmp = p.work.pre_tmp(), *first = p.work.pre_cp();
   for (int s = tid; s < N; s += kSchedThreads) {
     const int b = p.blk[s], len = p.cu[s + 1] - p.cu[s];
     if (b <= 0 || b >= nb || len == 0) continue;
@@ -294,14 +330,78 @@ lin_schedule_kernel(LinParams p, int short_max) {
     } else if (len <= short_max) {
       p.work.dec()[atomicAdd(&s_dec, 1)] = s;
     } else {
-      p.work.pre()[atomicAdd(&s_pre, 1)] = s;
+      const int k = atomicAdd(&s_pre, 1), c = (len - 1) / kLinChunk + 1;
+      pre_tmp[k] = s;
+      if (k < kSortMax) chunks[k] = c;
+      atomicAdd(&s_total, (unsigned long long)c);
     }
   }
   __syncthreads();
+  const int n_pre = s_pre;
   if (tid == 0) {
     if (s_flags) atomicOr((unsigned*)&hdr[kErr], s_flags);
     hdr[kNDec] = s_dec;
-    hdr[kNPre] = s_pre;
+    hdr[kNPre] = n_pre;
+  }
+  if (n_pre == 0) return;
+  const bool sorted = n_pre <= kSortMax;
+  // longest first, ties by sequence (so that a call's order is always the same)
+  for (int i = tid; i < n_pre; i += kSchedThreads) {
+    int rank = i;
+    if (sorted) {
+      const int ci = chunks[i], si = pre_tmp[i];
+      rank = 0;
+      for (int j = 0; j < n_pre; ++j)
+        rank += chunks[j] > ci || (chunks[j] == ci && pre_tmp[j] < si);
+    }
+    pre[rank] = pre_tmp[i];
+  }
+  __syncthreads();
+  auto chunks_of = [&](int k) {
+    return (p.cu[pre[k] + 1] - p.cu[pre[k]] - 1) / kLinChunk + 1;
+  };
+  // One SM works a chain off in order, so the call takes at least the longest
+  // chain; its share of all chunks is what it takes at best.  Where the
+  // longest is more than a quarter above that, long sequences are cut into
+  // segments of half a share, which costs a second read of k and v.
+  const unsigned long long share = (s_total * p.H + num_sms - 1) / num_sms;
+  int per = 0x7fffffff;
+  if (p.seg_states && sorted && 4ull * chunks_of(0) > 5 * share && chunks_of(0) >= 2 * kMinSegment) {
+    per = (int)((share + 1) / 2);
+    if (per < kMinSegment) per = kMinSegment;
+    for (;;) {  // until the segments of split sequences fit into the slots
+      if (tid == 0) s_segs = 0;
+      __syncthreads();
+      int mine = 0;
+      for (int k = tid; k < n_pre; k += kSchedThreads)
+        if (chunks_of(k) > per) mine += (chunks_of(k) + per - 1) / per;
+      if (mine) atomicAdd(&s_segs, mine);
+      __syncthreads();
+      const long long need = (long long)s_segs * p.H;
+      __syncthreads();
+      if (need <= p.seg_slots) break;
+      per = per > 0x3fffffff ? 0x7fffffff : per * 2;
+    }
+  }
+  int carry = 0, n_split = 0;
+  for (int k0 = 0; k0 < n_pre; k0 += kSchedThreads) {
+    const int k = k0 + tid;
+    const int segs = k < n_pre ? (chunks_of(k) - 1) / per + 1 : 0;
+    n_split += __syncthreads_count(segs > 1);
+    int total;
+    const int before = carry + cta_scan(segs, &total, warp_sums);
+    if (k < n_pre) {
+      first[k] = before;
+      if (k == n_pre - 1) first[n_pre] = before + segs;
+      if (segs > 1) atomicAdd(&hdr[kLinStateItems], segs);
+    }
+    carry += total;
+  }
+  for (long long i = tid; i < (long long)n_pre * p.H; i += kSchedThreads) p.bad[i] = 0;
+  if (tid == 0) {
+    hdr[kLinItems] = carry;
+    hdr[kLinSplit] = n_split;
+    hdr[kLinSegChunks] = per;
   }
 }
 
@@ -326,8 +426,12 @@ cudaError_t launch_lin_recurrent(const LinParams& p, int d, int act, int max_ite
   return launch_rec<__nv_bfloat16, 128>(p, max_items, s);
 }
 
-cudaError_t launch_lin_schedule(const LinParams& p, int short_max, cudaStream_t s) {
-  return launch_pdl(lin_schedule_kernel, dim3(1), dim3(kSchedThreads), 0, s, p, short_max);
+cudaError_t launch_lin_schedule(const LinParams& p, int short_max, int num_sms, cudaStream_t s) {
+  return launch_pdl(lin_schedule_kernel, dim3(1), dim3(kSchedThreads), 0, s, p, short_max, num_sms);
+}
+
+cudaError_t launch_lin_redo(const LinParams& p, int num_sms, cudaStream_t s) {
+  return launch_pdl(lin_redo_kernel, dim3(4 * num_sms), dim3(kRecThreads), 0, s, p);
 }
 
 namespace {
@@ -343,6 +447,9 @@ int check_lin_dims(int num_blocks, int num_layers, int H, int d, int act, size_t
   if ((long long)num_blocks * num_layers > (1ll << 30)) return GDN_ERR_RANGE;
   return GDN_OK;
 }
+
+// room for the states of two segments per SM and then some
+constexpr int kSegSlots = 512;
 
 size_t lin_stride(int H, int d, size_t align) {
   return roundup((size_t)H * d * d * sizeof(float), align > 128 ? align : 128);
@@ -390,6 +497,17 @@ int gdn_lin_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int nu
   if (st != GDN_OK) {
     delete p;
     return st;
+  }
+  if (gdn::lin_chunk_supported(d, act)) {
+    // the chunked form's segment states, then its marks
+    p->lin_slots = gdn::kSegSlots;
+    const size_t states = (size_t)p->lin_slots * d * d * sizeof(float);
+    if (cudaMalloc((void**)&p->lin_states, states + (size_t)num_blocks * num_heads) != cudaSuccess) {
+      cudaGetLastError();
+      p->lin_states = nullptr;
+      gdn_state_pool_destroy(p);
+      return GDN_ERR_NOMEM;
+    }
   }
   *out = p;
   return GDN_OK;
@@ -454,12 +572,32 @@ int gdn_lin_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
   lp.work.num_blocks = p->num_blocks;
 
   cudaStream_t s = (cudaStream_t)stream;
-  p->last_path = T > 1 && max_seqlen_hint != 1 ? GDN_PREFILL_SERIAL : GDN_PREFILL_NONE;
-  lp.listed = N > gdn::kSelfCheck;
-  if (lp.listed && gdn::launch_lin_schedule(lp, INT32_MAX, s) != cudaSuccess) return GDN_ERR_CUDA;
+  const int sms = gdn::num_sms();
+  // prompts in the chunked form, where it has a kernel and the call room for one
+  int max_long = T / (gdn::kLinShort + 1);
+  if (max_long > max_items) max_long = max_items;
+  if (max_seqlen_hint > 0 && max_seqlen_hint <= gdn::kLinShort) max_long = 0;
+  const bool chunked = max_long > 0 && gdn::lin_chunk_supported(d, p->act);
+  p->last_path = chunked                             ? GDN_PREFILL_FUSED
+                 : T > 1 && max_seqlen_hint != 1 ? GDN_PREFILL_SERIAL
+                                                     : GDN_PREFILL_NONE;
+  // heads enough for every SM, or too few tokens to cut: never split
+  const bool may_split = H < 2 * sms && T >= 2 * 8 * gdn::kLinChunk;
+  if (chunked) {
+    lp.seg_states = may_split ? p->lin_states : nullptr;
+    lp.seg_slots = p->lin_slots;
+    lp.bad = reinterpret_cast<unsigned char*>(p->lin_states + (size_t)p->lin_slots * d * d);
+  }
+  lp.listed = chunked || N > gdn::kSelfCheck;
+  lp.late = chunked;
+  if (lp.listed && gdn::launch_lin_schedule(lp, chunked ? gdn::kLinShort : INT32_MAX, sms, s) !=
+                       cudaSuccess)
+    return GDN_ERR_CUDA;
   if (p->ev_before && cudaEventRecord(p->ev_before, s) != cudaSuccess) return GDN_ERR_CUDA;
+  if (chunked && gdn::launch_lin_chunk(lp, may_split, sms, s) != cudaSuccess) return GDN_ERR_CUDA;
   if (gdn::launch_lin_recurrent(lp, d, p->act, lp.listed ? max_items : N, s) != cudaSuccess)
     return GDN_ERR_CUDA;
+  if (chunked && gdn::launch_lin_redo(lp, sms, s) != cudaSuccess) return GDN_ERR_CUDA;
   if (p->ev_after && cudaEventRecord(p->ev_after, s) != cudaSuccess) return GDN_ERR_CUDA;
   return GDN_OK;
 }

@@ -5,6 +5,22 @@
 
 namespace gdn {
 
+constexpr int kLinChunk = 128;  // tokens per chunk of the chunked form
+// Sequences of up to this many tokens take the recurrent form.
+constexpr int kLinShort = 16;
+
+// Header words of a layer's work area in these forwards (besides kErr, kNDec
+// and kNPre): the segments of the long sequences, longest first.
+enum LinCnt : int {
+  kLinStateItems = 4,  // segments of the split sequences (the first ones)
+  kLinHead = 5,        // work counter of the output pass
+  kLinItems = 6,       // all segments
+  kLinStateHead = 7,   // work counter of the state pass
+  kLinSplit = 8,       // sequences of more than one segment
+  kLinSegChunks = 9,   // chunks per segment of those
+  kLinBad = 10,        // a chain has been left to the token-serial kernel
+};
+
 // What the kernels of one gdn_lin_varlen_forward get, by value.
 struct LinParams {
   const void *q, *k, *v;  // rows of H, Hkv and Hkv heads of d elements
@@ -22,6 +38,12 @@ struct LinParams {
   int listed;   // the scheduler has run: take the sequences from its list
   int late;     // (recurrent kernel) launched behind the chunk kernel
   WorkArea work;
+  // the chunked form's: states of the split sequences' segments [slots][d][d]
+  // (nullptr: never split) and its marks for chains left to the token-serial
+  // kernel [index in the list of long sequences][H]
+  float* seg_states;
+  int seg_slots;
+  unsigned char* bad;
 };
 
 // e^x as a pair whose sum is it to about 2^-24 |x| relative, so that a state
@@ -48,10 +70,17 @@ __device__ __forceinline__ DecayPair decay_pair(float x) {
 __device__ __forceinline__ float finite_decay(float g) { return g == -INFINITY ? -1e30f : g; }
 
 // Validates the batch and lists the sequences: dec[] those of at most
-// short_max tokens, pre[] the longer ones.
-cudaError_t launch_lin_schedule(const LinParams& p, int short_max, cudaStream_t s);
+// short_max tokens, pre[] the longer ones, longest first, with their segments
+// (pre_cp[]: segments before entry k).
+cudaError_t launch_lin_schedule(const LinParams& p, int short_max, int num_sms, cudaStream_t s);
 // The token-serial kernel over the scheduler's dec[] list (p.listed) or over
 // all N sequences, which it then validates itself.
 cudaError_t launch_lin_recurrent(const LinParams& p, int d, int act, int max_items, cudaStream_t s);
+// The same over the chains that the chunked form has marked (d = 128, bf16).
+cudaError_t launch_lin_redo(const LinParams& p, int num_sms, cudaStream_t s);
+// The chunked form over pre[] (d = 128, bf16); may_split: with the state pass
+// that split sequences need.
+bool lin_chunk_supported(int d, int act);
+cudaError_t launch_lin_chunk(const LinParams& p, bool may_split, int num_sms, cudaStream_t s);
 
 }  // namespace gdn
