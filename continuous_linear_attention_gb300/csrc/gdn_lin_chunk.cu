@@ -16,11 +16,12 @@
 // a loop over the CTA's chunks that meets the others at mbarriers only:
 //   producer  one thread: TMA loads of a chunk's q, k, v tiles, two stages
 //   MMA 1     one thread: P = Q K^T, O = Q S0, O += P V
-//   MMA 2     one thread: U = sum of the decayed v k^T, in halves of 64 tokens
+//   MMA 2     one thread: U = sum of the decayed v k^T, 32 tokens at a time
 //   store     one thread: the staged output tile to global memory by TMA
-//   O warps   P with its decay -> bf16 A operand; O <- e^{g(i+1)} O; output
+//   O warps   P with its decay -> bf16 A operand; O <- e^{g(i+1)} O; output;
+//             the check of k for values that are not finite
 //   V warps   e^{g(n-1-j)} v_j -> A operand of U, rows past the chunk's end
-//             zeroed, and the check for values that are not finite
+//             zeroed, and the same check of v
 //   S warps   the state, fp32 in registers (thread v holds S[.][v]): to bf16
 //             as operand of O, S <- e^{g n} S + U
 //
@@ -59,8 +60,9 @@ constexpr uint32_t TILE = 32768, BOX = 16384;  // a [128][128] bf16 tile: two 64
 constexpr uint32_t ST_Q = 0, ST_K = TILE, ST_V = 2 * TILE, ST_BYTES = 3 * TILE;
 constexpr uint32_t OFF_S = kStages * ST_BYTES;  // S0 as B operand: [v][k], two 64-k blocks
 // tensor memory columns: P fp32 (bf16 over its first half), O, U, then the
-// three terms of 64 decayed v rows (32 columns each)
+// three terms of 32 decayed v rows (16 columns each), twice
 constexpr uint32_t TM_P = 0, TM_O = 128, TM_U = 256, TM_V = 384, TM_COLS = 512;
+constexpr int QT = 32;  // tokens per step of U
 
 enum Flag : int {
   kFirst = 1,   // first chunk of its chain (or segment)
@@ -78,10 +80,10 @@ struct Desc {
 
 struct Ctl {
   Desc desc[kStages];
-  uint64_t full[kStages], empty[kStages], zeroed[kStages], staged[kStages];
+  uint64_t full[kStages], empty[kStages], zeroed[kStages], staged[kStages], checked[kStages];
   uint64_t p_full, pb_full, qs_full, o_scaled, o_full, o_free, s_ready;
-  uint64_t v_full, v_free, u_full, u_free;
-  uint32_t bad[kStages][4];
+  uint64_t v_full[2], v_free[2], u_full, u_free;
+  uint32_t bad_k[kStages][4], bad_v[kStages][4];
   uint32_t tmem;
 };
 constexpr uint32_t OFF_CTL = OFF_S + TILE;
@@ -114,11 +116,64 @@ template <int kRegs>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
+// Pairs of fp32 in one 64-bit register: packed arithmetic (one instruction per
+// pair).
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unf2(F2 v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf2(F2 v) {
+  float x, y;
+  unf2(v, x, y);
+  return tc::pack2(x, y, (__nv_bfloat16*)nullptr);
+}
+// The two bf16 of a word as fp32.
+__device__ __forceinline__ F2 widen(uint32_t w) {
+  return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+// Four transposed 8 x 8 matrices of 16-bit elements: lane l gives the address
+// of row l % 8 of matrix l / 8 and gets of each matrix column l / 4, rows
+// 2 (l % 4) and the next.
+__device__ __forceinline__ void ldmatrix4_t(const void* at, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(at))
+               : "memory");
+}
+// The same fragments as words of 16 tensor memory lanes x 8 columns: words 0
+// and 1 are lanes l / 4 and l / 4 + 8 of column l % 4, words 2 and 3 of column
+// 4 + l % 4.
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
 __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
   return tc::pack2(lo, hi, (__nv_bfloat16*)nullptr);
 }
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// acc stays 0 while every bf16 of w is finite, else becomes NaN.
+__device__ __forceinline__ void track_finite(__nv_bfloat162& acc, uint32_t w) {
+  acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w), __floats2bfloat162_rn(0.f, 0.f), acc);
+}
+__device__ __forceinline__ bool any_not_finite(__nv_bfloat162 acc) {
+  const float2 f = __bfloat1622float2(acc);
+  return __any_sync(0xffffffffu, !(f.x == 0.f && f.y == 0.f));
+}
 
 template <bool kState>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -140,10 +195,13 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
   if (tid == 0) {
     for (int b = 0; b < kStages; ++b) {
       mbar_init(&ctl.full[b], 1);
-      // V warps, S warps, MMA 2 (and MMA 1, store)
-      mbar_init(&ctl.empty[b], kState ? 9 : 11);
+      // V warps, S warps, MMA 2 and the O warps, or for them MMA 1 and store
+      mbar_init(&ctl.empty[b], kState ? 13 : 11);
       mbar_init(&ctl.zeroed[b], 4);
       mbar_init(&ctl.staged[b], 4);
+      mbar_init(&ctl.checked[b], 4);
+      mbar_init(&ctl.v_full[b], 4);
+      mbar_init(&ctl.v_free[b], 1);
     }
     mbar_init(&ctl.p_full, 1);
     mbar_init(&ctl.pb_full, 4);
@@ -152,8 +210,6 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
     mbar_init(&ctl.o_full, 1);
     mbar_init(&ctl.o_free, 4);
     mbar_init(&ctl.s_ready, 4);
-    mbar_init(&ctl.v_full, 4);
-    mbar_init(&ctl.v_free, 1);
     mbar_init(&ctl.u_full, 1);
     mbar_init(&ctl.u_free, 4);
     fence_mbar_init();
@@ -168,122 +224,163 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
   if (warp < 4) {
     // ============================== O warps ===============================
     regs_dec<112>();
-    if (!kState) {
-      const int i = tid;                               // row of the chunk, TMEM lane
-      const uint32_t tl = (uint32_t)(warp * 32) << 16;
-      int h = -1;
-      float tab = 0.f, after = 0.f;   // e^{g lane}; scale e^{g (i+1)}
-      float base[4];                  // scale e^{g (i - 32 jb - 31)} per block left of the diagonal
-      float col[32];                  // e^{g (31 - jj)}
-      for (int c = 0;; ++c) {
-        const int b = c & 1;
-        const uint32_t ph = (uint32_t)(c & 1);
-        if (!warp_wait(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
-        const Desc d = ctl.desc[b];
-        if (d.flags & kEnd) break;
-        if (d.h != h) {
-          h = d.h;
-          const float g = finite_decay(p.log_decay[h]);
-          tab = expf(g * (float)lane);
-          after = p.scale * expf(g * (float)(i + 1));
-#pragma unroll
-          for (int jb = 0; jb < 4; ++jb)
-            base[jb] = jb < warp ? p.scale * expf(g * (float)(i - 32 * jb - 31)) : 0.f;
-#pragma unroll
-          for (int jj = 0; jj < 32; ++jj) col[jj] = __shfl_sync(0xffffffffu, tab, 31 - jj);
-        }
-        // ---- P: decay and mask, to bf16 over its own columns (block jb's 16
-        // land on fp32 columns read before)
-        if (!warp_wait(&ctl.p_full, ph)) { dead = true; break; }
-        tc::fence_after_sync();
-#pragma unroll
-        for (int jb = 0; jb < 4; ++jb) {
-          uint32_t w[16];
-          if (jb <= warp) {
-            float x[32];
-            tc::tmem_ld32(tmem + tl + TM_P + jb * 32, x);
-            tc::tmem_wait_ld();
-            if (jb < warp) {
-#pragma unroll
-              for (int jj = 0; jj < 32; ++jj) x[jj] *= base[jb] * col[jj];
-            } else {
-#pragma unroll
-              for (int jj = 0; jj < 32; ++jj) {
-                const float f = __shfl_sync(0xffffffffu, tab, lane - jj) * p.scale;
-                x[jj] = jj <= lane ? x[jj] * f : 0.f;
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = bf2(x[2 * e], x[2 * e + 1]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = 0u;
-          }
-          tc::tmem_st16u(tmem + tl + TM_P + jb * 16, w);
-        }
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        warp_arrive(&ctl.pb_full);
-        // ---- O = Q S0 times its row's decay
-        if (!warp_wait(&ctl.qs_full, ph)) { dead = true; break; }
-        tc::fence_after_sync();
-#pragma unroll
-        for (int jb = 0; jb < 4; ++jb) {
-          float x[32];
-          tc::tmem_ld32(tmem + tl + TM_O + jb * 32, x);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int jj = 0; jj < 32; ++jj) x[jj] *= after;
-          tc::tmem_st32(tmem + tl + TM_O + jb * 32, x);
-        }
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        warp_arrive(&ctl.o_scaled);
-        // ---- the chunk's outputs: staged over the q tile (its products are
-        // done), or, past a sequence's end, the valid rows straight out
-        if (!warp_wait(&ctl.o_full, ph)) { dead = true; break; }
-        tc::fence_after_sync();
-        unsigned char* stage = sm + b * ST_BYTES + ST_Q;
-        __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) +
-                              (size_t)(d.row + i) * p.ldo + (size_t)d.h * D;
-#pragma unroll
-        for (int jb = 0; jb < 4; ++jb) {
-          float x[32];
-          tc::tmem_ld32(tmem + tl + TM_O + jb * 32, x);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint4 w;
-            w.x = bf2(x[8 * e], x[8 * e + 1]);
-            w.y = bf2(x[8 * e + 2], x[8 * e + 3]);
-            w.z = bf2(x[8 * e + 4], x[8 * e + 5]);
-            w.w = bf2(x[8 * e + 6], x[8 * e + 7]);
-            if (d.n == CH)
-              *reinterpret_cast<uint4*>(stage + (jb >> 1) * BOX +
-                                        tc::sw128_offset(i, (jb & 1) * 32 + 8 * e)) = w;
-            else if (i < d.n)
-              *reinterpret_cast<uint4*>(orow + jb * 32 + 8 * e) = w;
+    const int i = tid;  // row of the chunk, TMEM lane
+    const uint32_t tl = (uint32_t)(warp * 32) << 16;
+    int h = -1;
+    float tab = 0.f, after = 0.f;             // e^{g lane}; scale e^{g (i+1)}
+    float left0 = 0.f, left1 = 0.f, left2 = 0.f;  // scale e^{g (i - 32 jb - 31)}, jb < warp
+    F2 col[16];                               // e^{g (31 - jj)}
+    for (int c = 0;; ++c) {
+      const int b = c & 1;
+      const uint32_t ph = (uint32_t)(c & 1);
+      if (!warp_wait(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
+      const Desc d = ctl.desc[b];
+      if (d.flags & kEnd) break;
+      {
+        // ---- k of the chunk: all finite?  (the rows past its end may be
+        // zeroed meanwhile, and are not looked at)
+        const unsigned char* kt = sm + b * ST_BYTES + ST_K;
+        __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll 4
+        for (int e = i; e < 2 * 128 * 8; e += 128) {
+          const int row = (e >> 3) & 127;
+          if (row < d.n) {
+            const uint4 x = *reinterpret_cast<const uint4*>(kt + (uint32_t)(e >> 10) * BOX +
+                                                            row * 128 + (e & 7) * 16);
+            track_finite(acc, x.x);
+            track_finite(acc, x.y);
+            track_finite(acc, x.z);
+            track_finite(acc, x.w);
           }
         }
-        tc::fence_proxy_async_smem();
-        tc::fence_before_sync();
-        warp_arrive(&ctl.o_free);
-        if (lane == 0) arrive(&ctl.staged[b]);
+        const bool bad = any_not_finite(acc);
+        if (lane == 0) {
+          ctl.bad_k[b][warp] = bad;
+          if (bad) {
+            p.bad[(size_t)d.entry * p.H + d.h] = 1;
+            hdr[kLinBad] = 1;
+          }
+        }
+        warp_arrive(&ctl.checked[b]);
       }
+      if (kState) {
+        warp_arrive(&ctl.empty[b]);
+        continue;
+      }
+      if (d.h != h) {
+        h = d.h;
+        const float g = finite_decay(p.log_decay[h]);
+        tab = expf(g * (float)lane);
+        after = p.scale * expf(g * (float)(i + 1));
+        if (warp > 0) left0 = p.scale * expf(g * (float)(i - 31));
+        if (warp > 1) left1 = p.scale * expf(g * (float)(i - 63));
+        if (warp > 2) left2 = p.scale * expf(g * (float)(i - 95));
+#pragma unroll
+        for (int jj = 0; jj < 16; ++jj)
+          col[jj] = f2(__shfl_sync(0xffffffffu, tab, 31 - 2 * jj),
+                       __shfl_sync(0xffffffffu, tab, 30 - 2 * jj));
+      }
+      // ---- P: decay and mask, to bf16 over its own columns (block jb's 16
+      // land on fp32 columns read before)
+      if (!warp_wait(&ctl.p_full, ph)) { dead = true; break; }
+      tc::fence_after_sync();
+#pragma unroll 1
+      for (int jb = 0; jb < 4; ++jb) {
+        uint32_t w[16];
+        if (jb < warp) {
+          float x[32];
+          tc::tmem_ld32(tmem + tl + TM_P + jb * 32, x);
+          const float lf = jb == 0 ? left0 : jb == 1 ? left1 : left2;
+          const F2 left = f2(lf, lf);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] = bf2(mul2(mul2(f2(x[2 * e], x[2 * e + 1]), col[e]), left));
+        } else if (jb == warp) {
+          float x[32];
+          tc::tmem_ld32(tmem + tl + TM_P + jb * 32, x);
+          tc::tmem_wait_ld();
+          const float ts = tab * p.scale;
+#pragma unroll
+          for (int jj = 0; jj < 32; ++jj) {
+            const float f = __shfl_sync(0xffffffffu, ts, lane - jj);
+            x[jj] = jj <= lane ? x[jj] * f : 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = bf2(x[2 * e], x[2 * e + 1]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = 0u;
+        }
+        tc::tmem_st16u(tmem + tl + TM_P + jb * 16, w);
+      }
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      warp_arrive(&ctl.pb_full);
+      // ---- O = Q S0 times its row's decay
+      if (!warp_wait(&ctl.qs_full, ph)) { dead = true; break; }
+      tc::fence_after_sync();
+      const F2 aft = f2(after, after);
+#pragma unroll 1
+      for (int jb = 0; jb < 4; ++jb) {
+        float x[32];
+        tc::tmem_ld32(tmem + tl + TM_O + jb * 32, x);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) unf2(mul2(f2(x[2 * e], x[2 * e + 1]), aft), x[2 * e], x[2 * e + 1]);
+        tc::tmem_st32(tmem + tl + TM_O + jb * 32, x);
+      }
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      warp_arrive(&ctl.o_scaled);
+      // ---- the chunk's outputs: staged over the q tile (its products are
+      // done), or, past a sequence's end, the valid rows straight out
+      if (!warp_wait(&ctl.o_full, ph)) { dead = true; break; }
+      tc::fence_after_sync();
+      unsigned char* stage = sm + b * ST_BYTES + ST_Q;
+      __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + (size_t)(d.row + i) * p.ldo +
+                            (size_t)d.h * D;
+#pragma unroll 1
+      for (int jb = 0; jb < 4; ++jb) {
+        float x[32];
+        tc::tmem_ld32(tmem + tl + TM_O + jb * 32, x);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint4 w;
+          w.x = bf2(x[8 * e], x[8 * e + 1]);
+          w.y = bf2(x[8 * e + 2], x[8 * e + 3]);
+          w.z = bf2(x[8 * e + 4], x[8 * e + 5]);
+          w.w = bf2(x[8 * e + 6], x[8 * e + 7]);
+          if (d.n == CH)
+            *reinterpret_cast<uint4*>(stage + (jb >> 1) * BOX +
+                                      tc::sw128_offset(i, (jb & 1) * 32 + 8 * e)) = w;
+          else if (i < d.n)
+            *reinterpret_cast<uint4*>(orow + jb * 32 + 8 * e) = w;
+        }
+      }
+      tc::fence_proxy_async_smem();
+      tc::fence_before_sync();
+      warp_arrive(&ctl.o_free);
+      if (lane == 0) arrive(&ctl.staged[b]);
     }
   } else if (warp < 8) {
     // ============================== V warps ===============================
+    // Warp w makes the operand rows (TMEM lanes) 32 w .. 32 w + 31 = elements
+    // v, from 16 tokens at a time as transposed 8 x 8 fragments: this lane
+    // gets tokens 2 (lane % 4) and the next of each 8, elements lane / 4 of
+    // each 8.
     regs_dec<112>();
-    const int v = tid - 128;
-    const uint32_t tl = (uint32_t)((warp - 4) * 32) << 16;
-    // byte of element v in row t of a V tile: (t >> 3) KiB, then off[t & 7]
-    uint32_t off[8];
-#pragma unroll
-    for (int r = 0; r < 8; ++r)
-      off[r] = (uint32_t)(v >> 6) * BOX + r * 128 + ((((v & 63) >> 3) ^ r) << 4) + (v & 7) * 2;
-    int h = -1, halves = 0;
-    float g = 0.f, w4[4];
-    int w_n = 0;
+    const int vw = warp - 4;
+    const uint32_t tl = (uint32_t)(vw * 32) << 16;
+    const int mr = lane & 7, mt = lane >> 4, mv = (lane >> 3) & 1;  // matrix row, token and element half
+    const uint32_t off = (uint32_t)(vw >> 1) * BOX + (mt * 8 + mr) * 128 +
+                         ((((vw & 1) * 4 + mv) ^ mr) << 4);
+    const int tl0 = 2 * (lane & 3);  // this lane's first token of each 8
+    const F2 minus = f2(-1.f, -1.f);
+    int h = -1, steps = 0;
+    float g = 0.f, blk8 = 0.f;  // e^{8 g lane}
+    F2 in8 = 0;                 // e^{g (7 - token)} of this lane's tokens in each 8
     for (int c = 0;; ++c) {
       const int b = c & 1;
       if (!warp_wait(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
@@ -291,38 +388,11 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       if (d.flags & kEnd) break;
       unsigned char* kt = sm + b * ST_BYTES + ST_K;
       unsigned char* vt = sm + b * ST_BYTES + ST_V;
-      // ---- k and v of the chunk: all finite?  Thread: 16-byte pieces of
-      // both; x * 0 is NaN for what is not
-      {
-        __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
-        const __nv_bfloat162 zero = acc;
-#pragma unroll 4
-        for (int e = v; e < 2 * 128 * 8; e += 128) {
-          const int row = (e >> 3) & 127;
-          if (row < d.n) {
-            const uint32_t at = (uint32_t)(e >> 10) * BOX + row * 128 + (e & 7) * 16;
-            const uint4 x = *reinterpret_cast<const uint4*>(kt + at);
-            const uint4 y = *reinterpret_cast<const uint4*>(vt + at);
-            const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u[q]), zero, acc);
-          }
-        }
-        const float2 f = __bfloat1622float2(acc);
-        const bool bad = __any_sync(0xffffffffu, !(f.x == 0.f && f.y == 0.f));
-        if (lane == 0) {
-          ctl.bad[b][warp - 4] = bad;
-          if (bad) {
-            p.bad[(size_t)d.entry * p.H + d.h] = 1;
-            hdr[kLinBad] = 1;
-          }
-        }
-      }
+      const bool full = d.n == CH;
       // ---- rows past the sequence are another's: zeros, so that they add
       // nothing (their weights are zero, but 0 * inf is not)
-      if (d.n < CH) {
-        for (int e = v; e < 2 * 128 * 8; e += 128) {
+      if (!full) {
+        for (int e = tid - 128; e < 2 * 128 * 8; e += 128) {
           const int row = (e >> 3) & 127;
           if (row >= d.n) {
             const uint32_t at = (uint32_t)(e >> 10) * BOX + row * 128 + (e & 7) * 16;
@@ -333,56 +403,85 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         tc::fence_proxy_async_smem();
       }
       warp_arrive(&ctl.zeroed[b]);
-      if (!(d.flags & kNoU)) {
-        if (d.h != h || d.n != w_n) {
-          if (d.h != h) g = finite_decay(p.log_decay[d.h]);
-          h = d.h;
-          w_n = d.n;
-          // lane l: e^{g (n-1-j)} of tokens j = 4 l .. 4 l + 3, 0 past the end
+      if (d.h != h) {
+        h = d.h;
+        g = finite_decay(p.log_decay[h]);
+        blk8 = expf(g * 8.f * (float)lane);
+        in8 = f2(expf(g * (float)(7 - tl0)), expf(g * (float)(6 - tl0)));
+      }
+      __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
+      const int nq = (d.n + QT - 1) / QT;
+      for (int q = 0; q < nq; ++q) {
+        const int buf = steps & 1;
+        if (!(d.flags & kNoU)) {
+          if (steps >= 2 && !warp_wait(&ctl.v_free[buf], ((steps >> 1) - 1) & 1)) { dead = true; break; }
+          tc::fence_after_sync();
+        }
+#pragma unroll 1
+        for (int t0 = q * QT; t0 < q * QT + QT; t0 += 16) {
+          uint32_t x[8];
+          ldmatrix4_t(vt + t0 * 128 + off, x);
+          ldmatrix4_t(vt + t0 * 128 + (off ^ 32u), x + 4);
+          F2 w[2];  // the weights of this lane's tokens in each 8
+          bool ok[2][2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int back = w_n - 1 - (4 * lane + e);
-            w4[e] = back >= 0 ? expf(g * (float)back) : 0.f;
+          for (int m = 0; m < 2; ++m) {
+            const int t = t0 + 8 * m + tl0;
+            ok[m][0] = t < d.n;
+            ok[m][1] = t + 1 < d.n;
+            if (full) {
+              const float a = __shfl_sync(0xffffffffu, blk8, 15 - (t0 >> 3) - m);
+              w[m] = mul2(in8, f2(a, a));
+            } else {
+              w[m] = f2(ok[m][0] ? expf(g * (float)(d.n - 1 - t)) : 0.f,
+                        ok[m][1] ? expf(g * (float)(d.n - 2 - t)) : 0.f);
+            }
+          }
+          uint32_t hi[8], mid[8], lo[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int m = (e >> 1) & 1;
+            // rows past n read as zeros or, before another warp's stores, as
+            // the neighbour's bits
+            if (!full) x[e] &= (ok[m][0] ? 0xffffu : 0u) | (ok[m][1] ? 0xffff0000u : 0u);
+            track_finite(acc, x[e]);
+            F2 f = mul2(widen(x[e]), w[m]);
+            hi[e] = bf2(f);
+            f = fma2(widen(hi[e]), minus, f);
+            mid[e] = bf2(f);
+            f = fma2(widen(mid[e]), minus, f);
+            lo[e] = bf2(f);
+          }
+          if (!(d.flags & kNoU)) {
+            const uint32_t at = tmem + tl + TM_V + buf * 48 + ((t0 & 16) >> 1);
+            constexpr uint32_t kUpper = 16u << 16;  // lanes 16 ..
+            tmem_st_frag(at, hi);
+            tmem_st_frag(at + kUpper, hi + 4);
+            tmem_st_frag(at + 16, mid);
+            tmem_st_frag(at + 16 + kUpper, mid + 4);
+            tmem_st_frag(at + 32, lo);
+            tmem_st_frag(at + 32 + kUpper, lo + 4);
           }
         }
-        const int nh = d.n > 64 ? 2 : 1;
-        for (int hf = 0; hf < nh; ++hf, ++halves) {
-          if (halves > 0 && !warp_wait(&ctl.v_free, (halves - 1) & 1)) { dead = true; break; }
-          tc::fence_after_sync();
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {  // 32 tokens: 16 columns of each term
-            uint32_t hi[16], mid[16], lo[16];
-            const int t0 = hf * 64 + q * 32;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int t = 2 * e;
-              const unsigned char* at = vt + (t0 + t) / 8 * 1024;
-              // rows past n read as zero from other warps' stores or as the
-              // neighbour's bits from before them: the weight decides
-              float f0 = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(at + off[t & 7]) << 16);
-              float f1 = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(at + off[(t + 1) & 7]) << 16);
-              const float wa = __shfl_sync(0xffffffffu, w4[t & 3], (t0 + t) >> 2);
-              const float wb = __shfl_sync(0xffffffffu, w4[(t + 1) & 3], (t0 + t) >> 2);
-              f0 = t0 + t < d.n ? f0 * wa : 0.f;
-              f1 = t0 + t + 1 < d.n ? f1 * wb : 0.f;
-              hi[e] = bf2(f0, f1);
-              f0 -= bf_lo(hi[e]);
-              f1 -= bf_hi(hi[e]);
-              mid[e] = bf2(f0, f1);
-              f0 -= bf_lo(mid[e]);
-              f1 -= bf_hi(mid[e]);
-              lo[e] = bf2(f0, f1);
+        if (q == nq - 1) {
+          // before the last arrival, so that it orders the mark for the S warps
+          const bool bad = any_not_finite(acc);
+          if (lane == 0) {
+            ctl.bad_v[b][vw] = bad;
+            if (bad) {
+              p.bad[(size_t)d.entry * p.H + d.h] = 1;
+              hdr[kLinBad] = 1;
             }
-            tc::tmem_st16u(tmem + tl + TM_V + q * 16, hi);
-            tc::tmem_st16u(tmem + tl + TM_V + 32 + q * 16, mid);
-            tc::tmem_st16u(tmem + tl + TM_V + 64 + q * 16, lo);
           }
+        }
+        if (!(d.flags & kNoU)) {
           tc::tmem_wait_st();
           tc::fence_before_sync();
-          warp_arrive(&ctl.v_full);
+          warp_arrive(&ctl.v_full[buf]);
+          ++steps;
         }
-        if (dead) break;
       }
+      if (dead) break;
       warp_arrive(&ctl.empty[b]);
     }
   } else if (warp < 12) {
@@ -390,7 +489,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
     regs_inc<200>();
     const int v = tid - 256;
     const uint32_t tl = (uint32_t)((warp - 8) * 32) << 16;
-    float S[D];
+    F2 S[D / 2];  // S[k][v], k = 2 i, 2 i + 1
     bool bad = false;
     int ups = 0;  // updates so far
     for (int c = 0;; ++c) {
@@ -408,20 +507,32 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
             src = reinterpret_cast<const float*>(p.layer_base + (size_t)d.rblk * p.stride) +
                   (size_t)d.h * D * D;
         }
+        if (src) {
 #pragma unroll
-        for (int k = 0; k < D; ++k) S[k] = src ? src[(size_t)k * D + v] : 0.f;
+          for (int k = 0; k < D; k += 2) S[k / 2] = f2(src[(size_t)k * D + v], src[(size_t)(k + 1) * D + v]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < D / 2; ++k) S[k] = 0;
+        }
       }
       if (!kState) {
         // ---- S0 as the B operand [v][k] of O = Q S0
         if (c > 0 && !warp_wait(&ctl.qs_full, (c - 1) & 1)) { dead = true; break; }
 #pragma unroll
-        for (int k = 0; k < D; k += 8)
-          tc::sw128_store8<__nv_bfloat16>(sm + OFF_S + (k >> 6) * BOX, v, k & 63, S + k);
+        for (int k = 0; k < D; k += 8) {
+          uint4 w;
+          w.x = bf2(S[k / 2]);
+          w.y = bf2(S[k / 2 + 1]);
+          w.z = bf2(S[k / 2 + 2]);
+          w.w = bf2(S[k / 2 + 3]);
+          *reinterpret_cast<uint4*>(sm + OFF_S + (k >> 6) * BOX + tc::sw128_offset(v, k & 63)) = w;
+        }
         tc::fence_proxy_async_smem();
         warp_arrive(&ctl.s_ready);
       }
       if (!(d.flags & kNoU)) {
         const DecayPair a = decay_pair(finite_decay(p.log_decay[d.h]) * (float)d.n);
+        const F2 ahi = f2(a.hi, a.hi), alo = f2(a.lo, a.lo);
         if (!warp_wait(&ctl.u_full, ups & 1)) { dead = true; break; }
         ++ups;
         tc::fence_after_sync();
@@ -431,13 +542,18 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
           tc::tmem_ld32(tmem + tl + TM_U + kb * 32, x);
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            S[kb * 32 + e] = fmaf(a.hi, S[kb * 32 + e], fmaf(a.lo, S[kb * 32 + e], x[e]));
+          for (int e = 0; e < 16; ++e) {
+            F2& s = S[kb * 16 + e];
+            s = fma2(ahi, s, fma2(alo, s, f2(x[2 * e], x[2 * e + 1])));
+          }
         }
         tc::fence_before_sync();
         warp_arrive(&ctl.u_free);
+        // (v's marks came with u_full)
+        if (!warp_wait(&ctl.checked[b], (c >> 1) & 1)) { dead = true; break; }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) bad |= (ctl.bad_k[b][w] | ctl.bad_v[b][w]) != 0;
       }
-      bad |= (ctl.bad[b][0] | ctl.bad[b][1] | ctl.bad[b][2] | ctl.bad[b][3]) != 0;
       if (d.flags & kLast) {
         float* dst = nullptr;
         if (kState) {
@@ -450,7 +566,12 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         }
         if (dst) {
 #pragma unroll
-          for (int k = 0; k < D; ++k) dst[(size_t)k * D + v] = S[k];
+          for (int k = 0; k < D; k += 2) {
+            float x, y;
+            unf2(S[k / 2], x, y);
+            dst[(size_t)k * D + v] = x;
+            dst[(size_t)(k + 1) * D + v] = y;
+          }
         }
       }
       warp_arrive(&ctl.empty[b]);
@@ -563,7 +684,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
     } else if (warp == 14 && lane == 0) {
       // ============================== MMA 2 =================================
       constexpr uint32_t kIdMN = tc::idesc_bf16_f32(128, 128, false, true);
-      int halves = 0, ups = 0;
+      int steps = 0, ups = 0;
       for (int c = 0; !dead; ++c) {
         const int b = c & 1;
         const uint32_t kt = sbase + b * ST_BYTES + ST_K;
@@ -575,17 +696,18 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
           continue;
         }
         if (ups > 0 && !mbar_wait_bounded(&ctl.u_free, (ups - 1) & 1)) { dead = true; break; }
-        const int nh = n > 64 ? 2 : 1;
-        for (int hf = 0; hf < nh; ++hf, ++halves) {
-          if (!mbar_wait_bounded(&ctl.v_full, halves & 1)) { dead = true; break; }
+        const int nq = (n + QT - 1) / QT;
+        for (int q = 0; q < nq; ++q, ++steps) {
+          const int buf = steps & 1;
+          if (!mbar_wait_bounded(&ctl.v_full[buf], (steps >> 1) & 1)) { dead = true; break; }
           tc::fence_after_sync();
-          // U (+)= (lo + mid + hi) K over 64 tokens, the smallest term first
+          // U (+)= (lo + mid + hi) K over 32 tokens, the smallest term first
 #pragma unroll
           for (int term = 2; term >= 0; --term)
-            tc::mma_op_ts(tmem + TM_U, tmem + TM_V + term * 32,
-                          tc::Opnd{kt + (uint32_t)hf * 8192u, BOX, true}, 4, kIdMN,
-                          hf > 0 || term < 2);
-          tc::commit(&ctl.v_free);
+            tc::mma_op_ts(tmem + TM_U, tmem + TM_V + buf * 48 + term * 16,
+                          tc::Opnd{kt + (uint32_t)q * (QT * 128), BOX, true}, QT / 16, kIdMN,
+                          q > 0 || term < 2);
+          tc::commit(&ctl.v_free[buf]);
         }
         if (dead) break;
         ++ups;
