@@ -15,13 +15,13 @@
 // One CTA per SM, chains claimed from a counter, longest first.  Roles, each
 // a loop over the CTA's chunks that meets the others at mbarriers only:
 //   producer  one thread: TMA loads of a chunk's q, k, v tiles, two stages
-//   MMA 1     one thread: P = Q K^T, O = Q S0, O += P V
+//   MMA 1     one thread: P = Q K^T, O = Q S0, then O += P V in two halves of
+//             64 columns, so that the O warps' work on one half runs beside it
 //   MMA 2     one thread: U = sum of the decayed v k^T, 32 tokens at a time
 //   store     one thread: the staged output tile to global memory by TMA
-//   O warps   P with its decay -> bf16 A operand; O <- e^{g(i+1)} O; output;
-//             the check of k for values that are not finite
+//   O warps   P with its decay -> bf16 A operand; O <- e^{g(i+1)} O; output
 //   V warps   e^{g(n-1-j)} v_j -> A operand of U, rows past the chunk's end
-//             zeroed, and the same check of v
+//             zeroed, and the check for values that are not finite
 //   S warps   the state, fp32 in registers (thread v holds S[.][v]): to bf16
 //             as operand of O, S <- e^{g n} S + U
 //
@@ -34,9 +34,10 @@
 // (see decay_pair).  Accumulating into S itself in tensor memory would add a
 // rounding of S at each of 24 MMA steps per chunk.
 //
-// A non-finite k or v in a chunk would reach rows of earlier tokens through
-// 0 * inf in the masked products; such a chain is left to the token-serial
-// kernel (its block keeps the old state, see the redo below).
+// A non-finite v in a chunk would reach rows of earlier tokens through 0 * inf
+// in the masked products; such a chain is left to the token-serial kernel (its
+// block keeps the old state).  A non-finite q or k reaches only its own row
+// and the later ones, as it should: P's mask selects, it does not multiply.
 //
 // Few long chains: when the longest chain is far above an SM's share, the
 // scheduler cuts long sequences into segments.  A first launch of this kernel
@@ -80,10 +81,10 @@ struct Desc {
 
 struct Ctl {
   Desc desc[kStages];
-  uint64_t full[kStages], empty[kStages], zeroed[kStages], staged[kStages], checked[kStages];
-  uint64_t p_full, pb_full, qs_full, o_scaled, o_full, o_free, s_ready;
+  uint64_t full[kStages], empty[kStages], zeroed[kStages], staged[kStages];
+  uint64_t p_full, pb_full, qs_full, o_scaled[2], o_full[2], o_free, s_ready;
   uint64_t v_full[2], v_free[2], u_full, u_free;
-  uint32_t bad_k[kStages][4], bad_v[kStages][4];
+  uint32_t bad[kStages][4];
   uint32_t tmem;
 };
 constexpr uint32_t OFF_CTL = OFF_S + TILE;
@@ -195,19 +196,20 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
   if (tid == 0) {
     for (int b = 0; b < kStages; ++b) {
       mbar_init(&ctl.full[b], 1);
-      // V warps, S warps, MMA 2 and the O warps, or for them MMA 1 and store
-      mbar_init(&ctl.empty[b], kState ? 13 : 11);
+      // V warps, S warps, MMA 2 (and MMA 1, store)
+      mbar_init(&ctl.empty[b], kState ? 9 : 11);
       mbar_init(&ctl.zeroed[b], 4);
       mbar_init(&ctl.staged[b], 4);
-      mbar_init(&ctl.checked[b], 4);
       mbar_init(&ctl.v_full[b], 4);
       mbar_init(&ctl.v_free[b], 1);
     }
     mbar_init(&ctl.p_full, 1);
     mbar_init(&ctl.pb_full, 4);
     mbar_init(&ctl.qs_full, 1);
-    mbar_init(&ctl.o_scaled, 4);
-    mbar_init(&ctl.o_full, 1);
+    for (int hf = 0; hf < 2; ++hf) {
+      mbar_init(&ctl.o_scaled[hf], 4);
+      mbar_init(&ctl.o_full[hf], 1);
+    }
     mbar_init(&ctl.o_free, 4);
     mbar_init(&ctl.s_ready, 4);
     mbar_init(&ctl.u_full, 1);
@@ -223,50 +225,19 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
 
   if (warp < 4) {
     // ============================== O warps ===============================
-    regs_dec<112>();
+    // (as launched: 128 registers a thread)
     const int i = tid;  // row of the chunk, TMEM lane
     const uint32_t tl = (uint32_t)(warp * 32) << 16;
     int h = -1;
     float tab = 0.f, after = 0.f;             // e^{g lane}; scale e^{g (i+1)}
     float left0 = 0.f, left1 = 0.f, left2 = 0.f;  // scale e^{g (i - 32 jb - 31)}, jb < warp
     F2 col[16];                               // e^{g (31 - jj)}
-    for (int c = 0;; ++c) {
+    for (int c = 0; !kState; ++c) {
       const int b = c & 1;
       const uint32_t ph = (uint32_t)(c & 1);
       if (!warp_wait(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
       const Desc d = ctl.desc[b];
       if (d.flags & kEnd) break;
-      {
-        // ---- k of the chunk: all finite?  (the rows past its end may be
-        // zeroed meanwhile, and are not looked at)
-        const unsigned char* kt = sm + b * ST_BYTES + ST_K;
-        __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
-#pragma unroll 4
-        for (int e = i; e < 2 * 128 * 8; e += 128) {
-          const int row = (e >> 3) & 127;
-          if (row < d.n) {
-            const uint4 x = *reinterpret_cast<const uint4*>(kt + (uint32_t)(e >> 10) * BOX +
-                                                            row * 128 + (e & 7) * 16);
-            track_finite(acc, x.x);
-            track_finite(acc, x.y);
-            track_finite(acc, x.z);
-            track_finite(acc, x.w);
-          }
-        }
-        const bool bad = any_not_finite(acc);
-        if (lane == 0) {
-          ctl.bad_k[b][warp] = bad;
-          if (bad) {
-            p.bad[(size_t)d.entry * p.H + d.h] = 1;
-            hdr[kLinBad] = 1;
-          }
-        }
-        warp_arrive(&ctl.checked[b]);
-      }
-      if (kState) {
-        warp_arrive(&ctl.empty[b]);
-        continue;
-      }
       if (d.h != h) {
         h = d.h;
         const float g = finite_decay(p.log_decay[h]);
@@ -322,43 +293,49 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       tc::fence_after_sync();
       const F2 aft = f2(after, after);
 #pragma unroll 1
-      for (int jb = 0; jb < 4; ++jb) {
-        float x[32];
-        tc::tmem_ld32(tmem + tl + TM_O + jb * 32, x);
+      for (int hf = 0; hf < 2; ++hf) {
+        float x[32], y[32];
+        const uint32_t at = tmem + tl + TM_O + hf * 64;
+        tc::tmem_ld32(at, x);
+        tc::tmem_ld32(at + 32, y);
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) unf2(mul2(f2(x[2 * e], x[2 * e + 1]), aft), x[2 * e], x[2 * e + 1]);
-        tc::tmem_st32(tmem + tl + TM_O + jb * 32, x);
+        for (int e = 0; e < 32; e += 2) unf2(mul2(f2(x[e], x[e + 1]), aft), x[e], x[e + 1]);
+        tc::tmem_st32(at, x);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) unf2(mul2(f2(y[e], y[e + 1]), aft), y[e], y[e + 1]);
+        tc::tmem_st32(at + 32, y);
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        warp_arrive(&ctl.o_scaled[hf]);
       }
-      tc::tmem_wait_st();
-      tc::fence_before_sync();
-      warp_arrive(&ctl.o_scaled);
       // ---- the chunk's outputs: staged over the q tile (its products are
       // done), or, past a sequence's end, the valid rows straight out
-      if (!warp_wait(&ctl.o_full, ph)) { dead = true; break; }
-      tc::fence_after_sync();
       unsigned char* stage = sm + b * ST_BYTES + ST_Q;
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + (size_t)(d.row + i) * p.ldo +
                             (size_t)d.h * D;
 #pragma unroll 1
-      for (int jb = 0; jb < 4; ++jb) {
-        float x[32];
-        tc::tmem_ld32(tmem + tl + TM_O + jb * 32, x);
+      for (int hf = 0; hf < 2; ++hf) {
+        if (!warp_wait(&ctl.o_full[hf], ph)) { dead = true; break; }
+        tc::fence_after_sync();
+        float x[64];
+        tc::tmem_ld32(tmem + tl + TM_O + hf * 64, x);
+        tc::tmem_ld32(tmem + tl + TM_O + hf * 64 + 32, x + 32);
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 8; ++e) {
           uint4 w;
           w.x = bf2(x[8 * e], x[8 * e + 1]);
           w.y = bf2(x[8 * e + 2], x[8 * e + 3]);
           w.z = bf2(x[8 * e + 4], x[8 * e + 5]);
           w.w = bf2(x[8 * e + 6], x[8 * e + 7]);
           if (d.n == CH)
-            *reinterpret_cast<uint4*>(stage + (jb >> 1) * BOX +
-                                      tc::sw128_offset(i, (jb & 1) * 32 + 8 * e)) = w;
+            *reinterpret_cast<uint4*>(stage + hf * BOX + tc::sw128_offset(i, 8 * e)) = w;
           else if (i < d.n)
-            *reinterpret_cast<uint4*>(orow + jb * 32 + 8 * e) = w;
+            *reinterpret_cast<uint4*>(orow + hf * 64 + 8 * e) = w;
         }
       }
+      if (dead) break;
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
       warp_arrive(&ctl.o_free);
@@ -467,7 +444,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
           // before the last arrival, so that it orders the mark for the S warps
           const bool bad = any_not_finite(acc);
           if (lane == 0) {
-            ctl.bad_v[b][vw] = bad;
+            ctl.bad[b][vw] = bad;
             if (bad) {
               p.bad[(size_t)d.entry * p.H + d.h] = 1;
               hdr[kLinBad] = 1;
@@ -549,10 +526,8 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         }
         tc::fence_before_sync();
         warp_arrive(&ctl.u_free);
-        // (v's marks came with u_full)
-        if (!warp_wait(&ctl.checked[b], (c >> 1) & 1)) { dead = true; break; }
-#pragma unroll
-        for (int w = 0; w < 4; ++w) bad |= (ctl.bad_k[b][w] | ctl.bad_v[b][w]) != 0;
+        // (the V warps' marks came with u_full)
+        bad |= (ctl.bad[b][0] | ctl.bad[b][1] | ctl.bad[b][2] | ctl.bad[b][3]) != 0;
       }
       if (d.flags & kLast) {
         float* dst = nullptr;
@@ -577,7 +552,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       warp_arrive(&ctl.empty[b]);
     }
   } else {
-    regs_dec<80>();
+    regs_dec<72>();
     if (warp == 12 && lane == 0) {
       // ============================== producer ==============================
       int c = 0;
@@ -648,14 +623,14 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
     } else if (warp == 13 && lane == 0 && !kState) {
       // ============================== MMA 1 =================================
       constexpr uint32_t kId = tc::idesc_bf16_f32(128, 128);
-      constexpr uint32_t kIdMN = tc::idesc_bf16_f32(128, 128, false, true);
+      constexpr uint32_t kIdMN = tc::idesc_bf16_f32(128, 64, false, true);
       for (int c = 0;; ++c) {
         const int b = c & 1;
         const uint32_t ph = (uint32_t)(c & 1), st = sbase + b * ST_BYTES;
         if (!mbar_wait_bounded(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
         if (ctl.desc[b].flags & kEnd) break;
         // P = Q K^T, once the last chunk's P V has read P
-        if (c > 0 && !mbar_wait_bounded(&ctl.o_full, ph ^ 1)) { dead = true; break; }
+        if (c > 0 && !mbar_wait_bounded(&ctl.o_full[1], ph ^ 1)) { dead = true; break; }
         tc::fence_after_sync();
         tc::mma_op(tmem + TM_P, tc::Opnd{st + ST_Q, BOX, false}, tc::Opnd{st + ST_K, BOX, false}, 8,
                    kId, false);
@@ -671,14 +646,18 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
                    8, kId, false);
         tc::commit(&ctl.qs_full);
         // O += P V
-        if (!mbar_wait_bounded(&ctl.zeroed[b], (c >> 1) & 1) || !mbar_wait_bounded(&ctl.pb_full, ph) ||
-            !mbar_wait_bounded(&ctl.o_scaled, ph)) {
+        if (!mbar_wait_bounded(&ctl.zeroed[b], (c >> 1) & 1) || !mbar_wait_bounded(&ctl.pb_full, ph)) {
           dead = true;
           break;
         }
-        tc::fence_after_sync();
-        tc::mma_op_ts(tmem + TM_O, tmem + TM_P, tc::Opnd{st + ST_V, BOX, true}, 8, kIdMN, true);
-        tc::commit(&ctl.o_full);
+        for (int hf = 0; hf < 2; ++hf) {
+          if (!mbar_wait_bounded(&ctl.o_scaled[hf], ph)) { dead = true; break; }
+          tc::fence_after_sync();
+          tc::mma_op_ts(tmem + TM_O + hf * 64, tmem + TM_P, tc::Opnd{st + ST_V + hf * BOX, BOX, true},
+                        8, kIdMN, true);
+          tc::commit(&ctl.o_full[hf]);
+        }
+        if (dead) break;
         tc::commit(&ctl.empty[b]);
       }
     } else if (warp == 14 && lane == 0) {
