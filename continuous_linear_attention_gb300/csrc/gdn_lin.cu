@@ -257,21 +257,21 @@ lin_recurrent_kernel(LinParams p) {
   if (p.late) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// The chains that the chunked form has marked, whose blocks still hold the
-// old state.
+// What the chunked form has marked: columns whose blocks still hold the old
+// state.
 __global__ void __launch_bounds__(kRecThreads) lin_redo_kernel(LinParams p) {
-  constexpr int kSlices = 128 / kSlice;
+  static_assert(kLinSlices * kSlice == 128, "a mark covers one unit");
   __shared__ __align__(16) RecSmem<__nv_bfloat16, 128> sm;
   pdl_wait_then_release();
   const int32_t* hdr = p.work.header();
   if (!hdr[kLinBad]) return;
-  const long long n = (long long)hdr[kNPre] * p.H * kSlices;
+  const long long n = (long long)hdr[kNPre] * p.H * kLinSlices;
   for (long long u = blockIdx.x; u < n; u += gridDim.x) {
-    const long long chain = u / kSlices;
-    if (!p.bad[chain]) continue;
+    if (!p.bad[u]) continue;
+    const long long chain = u / kLinSlices;
     __syncthreads();
     recurrent_unit<__nv_bfloat16, 128>(p, sm, p.work.pre()[chain / p.H], (int)(chain % p.H),
-                                       (int)(u % kSlices), false);
+                                       (int)(u % kLinSlices), false);
   }
 }
 
@@ -397,7 +397,8 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms) {
     }
     carry += total;
   }
-  for (long long i = tid; i < (long long)n_pre * p.H; i += kSchedThreads) p.bad[i] = 0;
+  for (long long i = tid; i < (long long)n_pre * p.H * kLinSlices; i += kSchedThreads)
+    p.bad[i] = 0;
   if (tid == 0) {
     hdr[kLinItems] = carry;
     hdr[kLinSplit] = n_split;
@@ -502,7 +503,7 @@ int gdn_lin_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int nu
     // the chunked form's segment states, then its marks
     p->lin_slots = gdn::kSegSlots;
     const size_t states = (size_t)p->lin_slots * d * d * sizeof(float);
-    if (cudaMalloc((void**)&p->lin_states, states + (size_t)num_blocks * num_heads) != cudaSuccess) {
+    if (cudaMalloc((void**)&p->lin_states, states + (size_t)num_blocks * num_heads * gdn::kLinSlices) != cudaSuccess) {
       cudaGetLastError();
       p->lin_states = nullptr;
       gdn_state_pool_destroy(p);

@@ -6,6 +6,7 @@
 namespace gdn {
 
 constexpr int kLinChunk = 128;  // tokens per chunk of the chunked form
+constexpr int kLinSlices = 4;   // parts of 32 columns of a head's state (d = 128)
 // Sequences of up to this many tokens take the recurrent form.
 constexpr int kLinShort = 16;
 
@@ -18,7 +19,7 @@ enum LinCnt : int {
   kLinStateHead = 7,   // work counter of the state pass
   kLinSplit = 8,       // sequences of more than one segment
   kLinSegChunks = 9,   // chunks per segment of those
-  kLinBad = 10,        // a chain has been left to the token-serial kernel
+  kLinBad = 10,        // something has been left to the token-serial kernel
 };
 
 // What the kernels of one gdn_lin_varlen_forward get, by value.
@@ -39,8 +40,8 @@ struct LinParams {
   int late;     // (recurrent kernel) launched behind the chunk kernel
   WorkArea work;
   // the chunked form's: states of the split sequences' segments [slots][d][d]
-  // (nullptr: never split) and its marks for chains left to the token-serial
-  // kernel [index in the list of long sequences][H]
+  // (nullptr: never split) and its marks for what is left to the token-serial
+  // kernel [index in the list of long sequences][H][kLinSlices]
   float* seg_states;
   int seg_slots;
   unsigned char* bad;
@@ -76,7 +77,7 @@ cudaError_t launch_lin_schedule(const LinParams& p, int short_max, int num_sms, 
 // The token-serial kernel over the scheduler's dec[] list (p.listed) or over
 // all N sequences, which it then validates itself.
 cudaError_t launch_lin_recurrent(const LinParams& p, int d, int act, int max_items, cudaStream_t s);
-// The same over the chains that the chunked form has marked (d = 128, bf16).
+// The same over what the chunked form has marked (d = 128, bf16).
 cudaError_t launch_lin_redo(const LinParams& p, int num_sms, cudaStream_t s);
 // The chunked form over pre[] (d = 128, bf16); may_split: with the state pass
 // that split sequences need.

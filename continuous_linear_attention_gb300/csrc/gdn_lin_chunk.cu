@@ -6,11 +6,14 @@
 //   o_i     = scale e^{g (i+1)} S0^T q_i + sum_j P[i][j] v_j
 //   S_n     = e^{g n} S0 + sum_j e^{g (n-1-j)} k_j v_j^T
 // so a (sequence, head) chain is four 128^3 products per chunk, and all but
-// the first term of each line does not depend on the chunks before.
+// the first term of each line does not depend on the chunks before.  Where
+// e^{128 |g|} is far inside bf16's range (kGentle) the row's decay leaves P,
+//   o_i = scale e^{g (i+1)} (S0^T q_i + sum_j e^{-g (j+1)} (q_i . k_j) v_j),
+// so that both products accumulate without a pass over O between them.
 //
 // Bytes bound it: q, k, v and o are 128 KB per chunk and head (2.9 us of one
-// SM's share of HBM); the products, the state's in three terms, are six 128^3
-// (1.9 us of one SM's tensor rate at the measured peak).
+// SM's share of HBM); the products, the state's in four terms, are seven 128^3
+// (2.3 us of one SM's tensor rate at the measured peak).
 //
 // One CTA per SM, chains claimed from a counter, longest first.  Roles, each
 // a loop over the CTA's chunks that meets the others at mbarriers only:
@@ -19,25 +22,32 @@
 //             64 columns, so that the O warps' work on one half runs beside it
 //   MMA 2     one thread: U = sum of the decayed v k^T, 32 tokens at a time
 //   store     one thread: the staged output tile to global memory by TMA
-//   O warps   P with its decay -> bf16 A operand; O <- e^{g(i+1)} O; output
+//   O warps   P with its decay -> bf16 A operand; O <- e^{g(i+1)} O where the
+//             decay is steep; output
 //   V warps   e^{g(n-1-j)} v_j -> A operand of U, rows past the chunk's end
-//             zeroed, and the check for values that are not finite
+//             zeroed
 //   S warps   the state, fp32 in registers (thread v holds S[.][v]): to bf16
 //             as operand of O, S <- e^{g n} S + U
 //
 // Precision.  P and S0 enter as bf16 operands (their partners are bf16, and
-// one MMA takes one type): each is off by 2^-9 rms like the output's own
-// rounding, which they follow.  The state is an output in fp32 and carried
-// over the whole prompt, so its update is not rounded: a decayed v has 8 + 24
-// significant bits and goes in as three bf16 terms (hi, mid, lo: 24 bits), the
-// smallest first, and U is added to S in fp32 registers with a decay pair
-// (see decay_pair).  Accumulating into S itself in tensor memory would add a
-// rounding of S at each of 24 MMA steps per chunk.
+// one MMA takes one type): each is off by as much as the output's own
+// rounding.  The state is an output in fp32 and carried
+// over the whole prompt, so its update is not rounded to bf16: a decayed v has
+// 8 + 24 significant bits and goes in as four bf16 terms.  With the weight as
+// wh + wm + wl (8 bits each), v wh is its bf16 rounding plus a remainder that
+// an fma gives exactly and that is a bf16 again, v wm likewise, and v wl joins
+// the last remainder (2^-18 of the whole, off by 2^-27): five packed bf16
+// instructions for two elements, where splitting the fp32 product took twelve.
+// The terms enter the smallest first, and U is added to S in fp32 registers
+// with a decay pair (see decay_pair).  Accumulating into S itself in tensor
+// memory would add a rounding of S at each of 32 MMA steps per chunk.
 //
-// A non-finite v in a chunk would reach rows of earlier tokens through 0 * inf
-// in the masked products; such a chain is left to the token-serial kernel (its
-// block keeps the old state).  A non-finite q or k reaches only its own row
-// and the later ones, as it should: P's mask selects, it does not multiply.
+// A non-finite v reaches its column of earlier tokens' rows through 0 * inf in
+// the masked products.  It also makes that column of the state non-finite for
+// good, which is seen at the chain's end: those columns are left to the
+// token-serial kernel, and their block keeps the old state until then.  A
+// non-finite q or k reaches only its own row and the later ones, as it should:
+// P's mask selects, it does not multiply.
 //
 // Few long chains: when the longest chain is far above an SM's share, the
 // scheduler cuts long sequences into segments.  A first launch of this kernel
@@ -55,15 +65,18 @@ namespace {
 
 constexpr int D = 128;
 constexpr int CH = kLinChunk;  // 128
-constexpr int kThreads = 512;  // O, V and S warps (4 each), then four single-thread warps
+constexpr int kThreads = 640;  // O, V and S warps (4, 8, 4), then four single-thread warps
+constexpr int kVWarps = 8, kSWarp = 12, kCtlWarp = 16;
 constexpr int kStages = 2;
 constexpr uint32_t TILE = 32768, BOX = 16384;  // a [128][128] bf16 tile: two 64-column boxes
 constexpr uint32_t ST_Q = 0, ST_K = TILE, ST_V = 2 * TILE, ST_BYTES = 3 * TILE;
 constexpr uint32_t OFF_S = kStages * ST_BYTES;  // S0 as B operand: [v][k], two 64-k blocks
 // tensor memory columns: P fp32 (bf16 over its first half), O, U, then the
-// three terms of 32 decayed v rows (16 columns each), twice
+// four terms of 32 decayed v rows (16 columns each), twice
 constexpr uint32_t TM_P = 0, TM_O = 128, TM_U = 256, TM_V = 384, TM_COLS = 512;
 constexpr int QT = 32;  // tokens per step of U
+constexpr int kTerms = 4;
+constexpr float kGentle = 32.f;  // largest 128 |g| whose e^{128 |g|} may stand in P
 
 enum Flag : int {
   kFirst = 1,   // first chunk of its chain (or segment)
@@ -82,18 +95,26 @@ struct Desc {
 struct Ctl {
   Desc desc[kStages];
   uint64_t full[kStages], empty[kStages], zeroed[kStages], staged[kStages];
-  uint64_t p_full, pb_full, qs_full, o_scaled[2], o_full[2], o_free, s_ready;
+  uint64_t p_full, pb_full, qs_full, o_scaled, o_full[2], o_free, s_ready;
   uint64_t v_full[2], v_free[2], u_full, u_free;
-  uint32_t bad[kStages][4];
   uint32_t tmem;
 };
 constexpr uint32_t OFF_CTL = OFF_S + TILE;
 constexpr uint32_t SMEM_BYTES = OFF_CTL + sizeof(Ctl);
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
 
-// A warp's bounded wait: false for all lanes if any gave up.
+// A bounded wait in few instructions, as the waiting warps share the issue
+// slots with the working ones: a test that has not succeeded suspends the
+// thread for some 0.2 us, so the limit is a few seconds (at least 0.1 s).
+constexpr int kWaitTests = 1 << 24;
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+  for (int i = 0; i < kWaitTests; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
+// The same for a warp: false for all lanes if any gave up.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+  return __all_sync(0xffffffffu, wait_for(bar, parity));
 }
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -167,15 +188,25 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t* r) 
 __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
   return tc::pack2(lo, hi, (__nv_bfloat16*)nullptr);
 }
-// acc stays 0 while every bf16 of w is finite, else becomes NaN.
-__device__ __forceinline__ void track_finite(__nv_bfloat162& acc, uint32_t w) {
-  acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w), __floats2bfloat162_rn(0.f, 0.f), acc);
+// Packed bf16 products, each rounded once.
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
-__device__ __forceinline__ bool any_not_finite(__nv_bfloat162 acc) {
-  const float2 f = __bfloat1622float2(acc);
-  return __any_sync(0xffffffffu, !(f.x == 0.f && f.y == 0.f));
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
 }
-
+// a b - c
+__device__ __forceinline__ uint32_t hfms2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 m;\n\tneg.bf16x2 m, %3;\n\tfma.rn.bf16x2 %0, %1, %2, m;\n\t}"
+      : "=r"(r)
+      : "r"(a), "r"(b), "r"(c));
+  return r;
+}
 template <bool kState>
 __global__ void __launch_bounds__(kThreads, 1)
 lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
@@ -197,19 +228,18 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
     for (int b = 0; b < kStages; ++b) {
       mbar_init(&ctl.full[b], 1);
       // V warps, S warps, MMA 2 (and MMA 1, store)
-      mbar_init(&ctl.empty[b], kState ? 9 : 11);
-      mbar_init(&ctl.zeroed[b], 4);
+      mbar_init(&ctl.empty[b], kVWarps + 4 + (kState ? 1 : 3));
+      mbar_init(&ctl.zeroed[b], kVWarps);
       mbar_init(&ctl.staged[b], 4);
-      mbar_init(&ctl.v_full[b], 4);
+      mbar_init(&ctl.v_full[b], kVWarps);
       mbar_init(&ctl.v_free[b], 1);
     }
     mbar_init(&ctl.p_full, 1);
     mbar_init(&ctl.pb_full, 4);
     mbar_init(&ctl.qs_full, 1);
-    for (int hf = 0; hf < 2; ++hf) {
-      mbar_init(&ctl.o_scaled[hf], 4);
-      mbar_init(&ctl.o_full[hf], 1);
-    }
+    mbar_init(&ctl.o_scaled, 4);
+    mbar_init(&ctl.o_full[0], 1);
+    mbar_init(&ctl.o_full[1], 1);
     mbar_init(&ctl.o_free, 4);
     mbar_init(&ctl.s_ready, 4);
     mbar_init(&ctl.u_full, 1);
@@ -223,14 +253,14 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
   const uint32_t tmem = ctl.tmem;
   bool dead = false;
 
+  // registers a thread, of 96 at launch: O 96, V 72, S 184, the others 56
   if (warp < 4) {
     // ============================== O warps ===============================
-    // (as launched: 128 registers a thread)
     const int i = tid;  // row of the chunk, TMEM lane
     const uint32_t tl = (uint32_t)(warp * 32) << 16;
     int h = -1;
-    float tab = 0.f, after = 0.f;             // e^{g lane}; scale e^{g (i+1)}
-    float left0 = 0.f, left1 = 0.f, left2 = 0.f;  // scale e^{g (i - 32 jb - 31)}, jb < warp
+    float g = 0.f, after = 0.f;  // scale e^{g (i+1)}
+    bool gentle = true;
     F2 col[16];                               // e^{g (31 - jj)}
     for (int c = 0; !kState; ++c) {
       const int b = c & 1;
@@ -240,12 +270,10 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       if (d.flags & kEnd) break;
       if (d.h != h) {
         h = d.h;
-        const float g = finite_decay(p.log_decay[h]);
-        tab = expf(g * (float)lane);
+        g = finite_decay(p.log_decay[h]);
+        gentle = fabsf(g) * (float)CH <= kGentle;
         after = p.scale * expf(g * (float)(i + 1));
-        if (warp > 0) left0 = p.scale * expf(g * (float)(i - 31));
-        if (warp > 1) left1 = p.scale * expf(g * (float)(i - 63));
-        if (warp > 2) left2 = p.scale * expf(g * (float)(i - 95));
+        const float tab = expf(g * (float)lane);
 #pragma unroll
         for (int jj = 0; jj < 16; ++jj)
           col[jj] = f2(__shfl_sync(0xffffffffu, tab, 31 - 2 * jj),
@@ -258,30 +286,33 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
 #pragma unroll 1
       for (int jb = 0; jb < 4; ++jb) {
         uint32_t w[16];
-        if (jb < warp) {
-          float x[32];
-          tc::tmem_ld32(tmem + tl + TM_P + jb * 32, x);
-          const float lf = jb == 0 ? left0 : jb == 1 ? left1 : left2;
-          const F2 left = f2(lf, lf);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            w[e] = bf2(mul2(mul2(f2(x[2 * e], x[2 * e + 1]), col[e]), left));
-        } else if (jb == warp) {
-          float x[32];
-          tc::tmem_ld32(tmem + tl + TM_P + jb * 32, x);
-          tc::tmem_wait_ld();
-          const float ts = tab * p.scale;
-#pragma unroll
-          for (int jj = 0; jj < 32; ++jj) {
-            const float f = __shfl_sync(0xffffffffu, ts, lane - jj);
-            x[jj] = jj <= lane ? x[jj] * f : 0.f;
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = bf2(x[2 * e], x[2 * e + 1]);
-        } else {
+        if (jb > warp) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) w[e] = 0u;
+        } else {
+          float x[32];
+          tc::tmem_ld32(tmem + tl + TM_P + jb * 32, x);
+          // times col: e^{-g (j+1)}, or scale e^{g (i-j)} left of the diagonal
+          const float lf = gentle ? expf(-g * (float)(32 * jb + 32))
+                                  : p.scale * expf(g * (float)(i - 32 * jb - 31));
+          const F2 left = f2(lf, lf);
+          tc::tmem_wait_ld();
+          if (gentle || jb < warp) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              w[e] = bf2(mul2(mul2(f2(x[2 * e], x[2 * e + 1]), col[e]), left));
+          } else {
+            const float ts = p.scale * expf(g * (float)lane);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              w[e] = bf2(x[2 * e] * __shfl_sync(0xffffffffu, ts, lane - 2 * e),
+                         x[2 * e + 1] * __shfl_sync(0xffffffffu, ts, lane - 2 * e - 1));
+          }
+          if (jb == warp) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              w[e] = lane > 2 * e ? w[e] : lane == 2 * e ? w[e] & 0xffffu : 0u;
+          }
         }
         tc::tmem_st16u(tmem + tl + TM_P + jb * 16, w);
       }
@@ -289,50 +320,51 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       tc::fence_before_sync();
       warp_arrive(&ctl.pb_full);
       // ---- O = Q S0 times its row's decay
-      if (!warp_wait(&ctl.qs_full, ph)) { dead = true; break; }
-      tc::fence_after_sync();
-      const F2 aft = f2(after, after);
+      if (!gentle) {
+        if (!warp_wait(&ctl.qs_full, ph)) { dead = true; break; }
+        tc::fence_after_sync();
+        const F2 aft = f2(after, after);
 #pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf) {
-        float x[32], y[32];
-        const uint32_t at = tmem + tl + TM_O + hf * 64;
-        tc::tmem_ld32(at, x);
-        tc::tmem_ld32(at + 32, y);
-        tc::tmem_wait_ld();
+        for (int jb = 0; jb < 4; ++jb) {
+          float x[32];
+          tc::tmem_ld32(tmem + tl + TM_O + jb * 32, x);
+          tc::tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) unf2(mul2(f2(x[e], x[e + 1]), aft), x[e], x[e + 1]);
-        tc::tmem_st32(at, x);
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) unf2(mul2(f2(y[e], y[e + 1]), aft), y[e], y[e + 1]);
-        tc::tmem_st32(at + 32, y);
+          for (int e = 0; e < 32; e += 2) unf2(mul2(f2(x[e], x[e + 1]), aft), x[e], x[e + 1]);
+          tc::tmem_st32(tmem + tl + TM_O + jb * 32, x);
+        }
         tc::tmem_wait_st();
         tc::fence_before_sync();
-        warp_arrive(&ctl.o_scaled[hf]);
       }
+      warp_arrive(&ctl.o_scaled);
       // ---- the chunk's outputs: staged over the q tile (its products are
       // done), or, past a sequence's end, the valid rows straight out
       unsigned char* stage = sm + b * ST_BYTES + ST_Q;
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + (size_t)(d.row + i) * p.ldo +
                             (size_t)d.h * D;
+      const float of = gentle ? after : 1.f;
+      const F2 of2 = f2(of, of);
 #pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf) {
-        if (!warp_wait(&ctl.o_full[hf], ph)) { dead = true; break; }
-        tc::fence_after_sync();
-        float x[64];
-        tc::tmem_ld32(tmem + tl + TM_O + hf * 64, x);
-        tc::tmem_ld32(tmem + tl + TM_O + hf * 64 + 32, x + 32);
+      for (int jb = 0; jb < 4; ++jb) {
+        if ((jb & 1) == 0) {
+          if (!warp_wait(&ctl.o_full[jb >> 1], ph)) { dead = true; break; }
+          tc::fence_after_sync();
+        }
+        float x[32];
+        tc::tmem_ld32(tmem + tl + TM_O + jb * 32, x);
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 4; ++e) {
           uint4 w;
-          w.x = bf2(x[8 * e], x[8 * e + 1]);
-          w.y = bf2(x[8 * e + 2], x[8 * e + 3]);
-          w.z = bf2(x[8 * e + 4], x[8 * e + 5]);
-          w.w = bf2(x[8 * e + 6], x[8 * e + 7]);
+          w.x = bf2(mul2(f2(x[8 * e], x[8 * e + 1]), of2));
+          w.y = bf2(mul2(f2(x[8 * e + 2], x[8 * e + 3]), of2));
+          w.z = bf2(mul2(f2(x[8 * e + 4], x[8 * e + 5]), of2));
+          w.w = bf2(mul2(f2(x[8 * e + 6], x[8 * e + 7]), of2));
           if (d.n == CH)
-            *reinterpret_cast<uint4*>(stage + hf * BOX + tc::sw128_offset(i, 8 * e)) = w;
+            *reinterpret_cast<uint4*>(stage + (jb >> 1) * BOX +
+                                      tc::sw128_offset(i, (jb & 1) * 32 + 8 * e)) = w;
           else if (i < d.n)
-            *reinterpret_cast<uint4*>(orow + hf * 64 + 8 * e) = w;
+            *reinterpret_cast<uint4*>(orow + jb * 32 + 8 * e) = w;
         }
       }
       if (dead) break;
@@ -341,14 +373,15 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       warp_arrive(&ctl.o_free);
       if (lane == 0) arrive(&ctl.staged[b]);
     }
-  } else if (warp < 8) {
+  } else if (warp < kSWarp) {
     // ============================== V warps ===============================
-    // Warp w makes the operand rows (TMEM lanes) 32 w .. 32 w + 31 = elements
-    // v, from 16 tokens at a time as transposed 8 x 8 fragments: this lane
-    // gets tokens 2 (lane % 4) and the next of each 8, elements lane / 4 of
-    // each 8.
-    regs_dec<112>();
-    const int vw = warp - 4;
+    // Warps w and w + 4 make the operand rows (TMEM lanes) 32 w .. 32 w + 31 =
+    // elements v, each of 16 of a step's 32 tokens, as transposed 8 x 8
+    // fragments: this lane gets tokens 2 (lane % 4) and the next of each 8,
+    // elements lane / 4 of each 8.  (With one warp per sub-partition these
+    // dependent chains took 4,800 of a chunk's 8,400 cycles.)
+    regs_dec<72>();
+    const int vw = warp & 3, half = (warp >> 2) - 1;
     const uint32_t tl = (uint32_t)(vw * 32) << 16;
     const int mr = lane & 7, mt = lane >> 4, mv = (lane >> 3) & 1;  // matrix row, token and element half
     const uint32_t off = (uint32_t)(vw >> 1) * BOX + (mt * 8 + mr) * 128 +
@@ -369,7 +402,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       // ---- rows past the sequence are another's: zeros, so that they add
       // nothing (their weights are zero, but 0 * inf is not)
       if (!full) {
-        for (int e = tid - 128; e < 2 * 128 * 8; e += 128) {
+        for (int e = tid - 128; e < 2 * 128 * 8; e += 32 * kVWarps) {
           const int row = (e >> 3) & 127;
           if (row >= d.n) {
             const uint32_t at = (uint32_t)(e >> 10) * BOX + row * 128 + (e & 7) * 16;
@@ -386,7 +419,6 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         blk8 = expf(g * 8.f * (float)lane);
         in8 = f2(expf(g * (float)(7 - tl0)), expf(g * (float)(6 - tl0)));
       }
-      __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
       const int nq = (d.n + QT - 1) / QT;
       for (int q = 0; q < nq; ++q) {
         const int buf = steps & 1;
@@ -394,61 +426,54 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
           if (steps >= 2 && !warp_wait(&ctl.v_free[buf], ((steps >> 1) - 1) & 1)) { dead = true; break; }
           tc::fence_after_sync();
         }
-#pragma unroll 1
-        for (int t0 = q * QT; t0 < q * QT + QT; t0 += 16) {
-          uint32_t x[8];
-          ldmatrix4_t(vt + t0 * 128 + off, x);
-          ldmatrix4_t(vt + t0 * 128 + (off ^ 32u), x + 4);
-          F2 w[2];  // the weights of this lane's tokens in each 8
-          bool ok[2][2];
+        const int t0 = q * QT + 16 * half;
+        uint32_t x[8];
+        ldmatrix4_t(vt + t0 * 128 + off, x);
+        ldmatrix4_t(vt + t0 * 128 + (off ^ 32u), x + 4);
+        F2 w[2];  // the weights of this lane's tokens in each 8
+        bool ok[2][2];
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const int t = t0 + 8 * m + tl0;
-            ok[m][0] = t < d.n;
-            ok[m][1] = t + 1 < d.n;
-            if (full) {
-              const float a = __shfl_sync(0xffffffffu, blk8, 15 - (t0 >> 3) - m);
-              w[m] = mul2(in8, f2(a, a));
-            } else {
-              w[m] = f2(ok[m][0] ? expf(g * (float)(d.n - 1 - t)) : 0.f,
-                        ok[m][1] ? expf(g * (float)(d.n - 2 - t)) : 0.f);
-            }
-          }
-          uint32_t hi[8], mid[8], lo[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int m = (e >> 1) & 1;
-            // rows past n read as zeros or, before another warp's stores, as
-            // the neighbour's bits
-            if (!full) x[e] &= (ok[m][0] ? 0xffffu : 0u) | (ok[m][1] ? 0xffff0000u : 0u);
-            track_finite(acc, x[e]);
-            F2 f = mul2(widen(x[e]), w[m]);
-            hi[e] = bf2(f);
-            f = fma2(widen(hi[e]), minus, f);
-            mid[e] = bf2(f);
-            f = fma2(widen(mid[e]), minus, f);
-            lo[e] = bf2(f);
-          }
-          if (!(d.flags & kNoU)) {
-            const uint32_t at = tmem + tl + TM_V + buf * 48 + ((t0 & 16) >> 1);
-            constexpr uint32_t kUpper = 16u << 16;  // lanes 16 ..
-            tmem_st_frag(at, hi);
-            tmem_st_frag(at + kUpper, hi + 4);
-            tmem_st_frag(at + 16, mid);
-            tmem_st_frag(at + 16 + kUpper, mid + 4);
-            tmem_st_frag(at + 32, lo);
-            tmem_st_frag(at + 32 + kUpper, lo + 4);
+        for (int m = 0; m < 2; ++m) {
+          const int tok = t0 + 8 * m + tl0;
+          ok[m][0] = tok < d.n;
+          ok[m][1] = tok + 1 < d.n;
+          if (full) {
+            const float a = __shfl_sync(0xffffffffu, blk8, 15 - (t0 >> 3) - m);
+            w[m] = mul2(in8, f2(a, a));
+          } else {
+            w[m] = f2(ok[m][0] ? expf(g * (float)(d.n - 1 - tok)) : 0.f,
+                      ok[m][1] ? expf(g * (float)(d.n - 2 - tok)) : 0.f);
           }
         }
-        if (q == nq - 1) {
-          // before the last arrival, so that it orders the mark for the S warps
-          const bool bad = any_not_finite(acc);
-          if (lane == 0) {
-            ctl.bad[b][vw] = bad;
-            if (bad) {
-              p.bad[(size_t)d.entry * p.H + d.h] = 1;
-              hdr[kLinBad] = 1;
-            }
+        // the weights' three bf16 terms, and their products' four
+        uint32_t wh[2], wm[2], wl[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          wh[m] = bf2(w[m]);
+          w[m] = fma2(widen(wh[m]), minus, w[m]);
+          wm[m] = bf2(w[m]);
+          w[m] = fma2(widen(wm[m]), minus, w[m]);
+          wl[m] = bf2(w[m]);
+        }
+        uint32_t t[kTerms][8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int m = (e >> 1) & 1;
+          // rows past n read as zeros or, before another warp's stores, as
+          // the neighbour's bits
+          if (!full) x[e] &= (ok[m][0] ? 0xffffu : 0u) | (ok[m][1] ? 0xffff0000u : 0u);
+          t[0][e] = hmul2(x[e], wh[m]);
+          t[1][e] = hfms2(x[e], wh[m], t[0][e]);
+          t[2][e] = hmul2(x[e], wm[m]);
+          t[3][e] = hfma2(x[e], wl[m], hfms2(x[e], wm[m], t[2][e]));
+        }
+        if (!(d.flags & kNoU)) {
+          const uint32_t at = tmem + tl + TM_V + buf * (16 * kTerms) + 8 * half;
+          constexpr uint32_t kUpper = 16u << 16;  // lanes 16 ..
+#pragma unroll
+          for (int k = 0; k < kTerms; ++k) {
+            tmem_st_frag(at + 16 * k, t[k]);
+            tmem_st_frag(at + 16 * k + kUpper, t[k] + 4);
           }
         }
         if (!(d.flags & kNoU)) {
@@ -461,13 +486,12 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       if (dead) break;
       warp_arrive(&ctl.empty[b]);
     }
-  } else if (warp < 12) {
+  } else if (warp < kCtlWarp) {
     // ============================== S warps ===============================
-    regs_inc<200>();
-    const int v = tid - 256;
-    const uint32_t tl = (uint32_t)((warp - 8) * 32) << 16;
+    regs_inc<184>();
+    const int v = tid - 32 * kSWarp;
+    const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
     F2 S[D / 2];  // S[k][v], k = 2 i, 2 i + 1
-    bool bad = false;
     int ups = 0;  // updates so far
     for (int c = 0;; ++c) {
       const int b = c & 1;
@@ -475,7 +499,6 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       const Desc d = ctl.desc[b];
       if (d.flags & kEnd) break;
       if (d.flags & kFirst) {
-        bad = false;
         const float* src = nullptr;
         if (!kState) {
           if (d.slot >= 0)
@@ -526,18 +549,29 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         }
         tc::fence_before_sync();
         warp_arrive(&ctl.u_free);
-        // (the V warps' marks came with u_full)
-        bad |= (ctl.bad[b][0] | ctl.bad[b][1] | ctl.bad[b][2] | ctl.bad[b][3]) != 0;
       }
       if (d.flags & kLast) {
         float* dst = nullptr;
         if (kState) {
           dst = p.seg_states + (size_t)d.slot * D * D;
-        } else if ((d.flags & kFinal) && !bad &&
-                   (d.slot < 0 || !p.bad[(size_t)d.entry * p.H + d.h])) {
-          // (an earlier segment's mark is the state pass's, which has ended)
-          dst = reinterpret_cast<float*>(p.layer_base + (size_t)d.wblk * p.stride) +
-                (size_t)d.h * D * D;
+        } else if (d.flags & kFinal) {
+          // a v that is not finite has made its column of S so, in this or an
+          // earlier segment: this warp's 32 columns of the chain are left to
+          // the token-serial kernel
+          F2 acc = 0;
+#pragma unroll
+          for (int k = 0; k < D / 2; ++k) acc = fma2(S[k], 0, acc);
+          float x, y;
+          unf2(acc, x, y);
+          if (__any_sync(0xffffffffu, !(x + y == 0.f))) {
+            if (lane == 0) {
+              p.bad[((size_t)d.entry * p.H + d.h) * kLinSlices + (warp & 3)] = 1;
+              hdr[kLinBad] = 1;
+            }
+          } else {
+            dst = reinterpret_cast<float*>(p.layer_base + (size_t)d.wblk * p.stride) +
+                  (size_t)d.h * D * D;
+          }
         }
         if (dst) {
 #pragma unroll
@@ -552,8 +586,8 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       warp_arrive(&ctl.empty[b]);
     }
   } else {
-    regs_dec<72>();
-    if (warp == 12 && lane == 0) {
+    regs_dec<56>();
+    if (warp == kCtlWarp && lane == 0) {
       // ============================== producer ==============================
       int c = 0;
       for (bool end = false; !end && !dead;) {
@@ -584,7 +618,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         const int hk = h / p.group;
         for (int k = c0; k < c1; ++k, ++c) {
           const int b = c & 1;
-          if (c >= kStages && !mbar_wait_bounded(&ctl.empty[b], ((c >> 1) - 1) & 1)) {
+          if (c >= kStages && !wait_for(&ctl.empty[b], ((c >> 1) - 1) & 1)) {
             dead = true;
             break;
           }
@@ -618,26 +652,26 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       if (dead) {
         // the loads already issued land before the CTA ends
         for (int k = c > kStages ? c - kStages : 0; k < c; ++k)
-          mbar_wait_bounded(&ctl.full[k & 1], (k >> 1) & 1);
+          wait_for(&ctl.full[k & 1], (k >> 1) & 1);
       }
-    } else if (warp == 13 && lane == 0 && !kState) {
+    } else if (warp == kCtlWarp + 1 && lane == 0 && !kState) {
       // ============================== MMA 1 =================================
       constexpr uint32_t kId = tc::idesc_bf16_f32(128, 128);
       constexpr uint32_t kIdMN = tc::idesc_bf16_f32(128, 64, false, true);
       for (int c = 0;; ++c) {
         const int b = c & 1;
         const uint32_t ph = (uint32_t)(c & 1), st = sbase + b * ST_BYTES;
-        if (!mbar_wait_bounded(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
+        if (!wait_for(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
         if (ctl.desc[b].flags & kEnd) break;
         // P = Q K^T, once the last chunk's P V has read P
-        if (c > 0 && !mbar_wait_bounded(&ctl.o_full[1], ph ^ 1)) { dead = true; break; }
+        if (c > 0 && !wait_for(&ctl.o_full[1], ph ^ 1)) { dead = true; break; }
         tc::fence_after_sync();
         tc::mma_op(tmem + TM_P, tc::Opnd{st + ST_Q, BOX, false}, tc::Opnd{st + ST_K, BOX, false}, 8,
                    kId, false);
         tc::commit(&ctl.p_full);
         // O = Q S0
-        if (!mbar_wait_bounded(&ctl.s_ready, ph) ||
-            (c > 0 && !mbar_wait_bounded(&ctl.o_free, ph ^ 1))) {
+        if (!wait_for(&ctl.s_ready, ph) ||
+            (c > 0 && !wait_for(&ctl.o_free, ph ^ 1))) {
           dead = true;
           break;
         }
@@ -646,46 +680,46 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
                    8, kId, false);
         tc::commit(&ctl.qs_full);
         // O += P V
-        if (!mbar_wait_bounded(&ctl.zeroed[b], (c >> 1) & 1) || !mbar_wait_bounded(&ctl.pb_full, ph)) {
+        if (!wait_for(&ctl.zeroed[b], (c >> 1) & 1) || !wait_for(&ctl.pb_full, ph) ||
+            !wait_for(&ctl.o_scaled, ph)) {
           dead = true;
           break;
         }
+        tc::fence_after_sync();
+#pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
-          if (!mbar_wait_bounded(&ctl.o_scaled[hf], ph)) { dead = true; break; }
-          tc::fence_after_sync();
           tc::mma_op_ts(tmem + TM_O + hf * 64, tmem + TM_P, tc::Opnd{st + ST_V + hf * BOX, BOX, true},
                         8, kIdMN, true);
           tc::commit(&ctl.o_full[hf]);
         }
-        if (dead) break;
         tc::commit(&ctl.empty[b]);
       }
-    } else if (warp == 14 && lane == 0) {
+    } else if (warp == kCtlWarp + 2 && lane == 0) {
       // ============================== MMA 2 =================================
       constexpr uint32_t kIdMN = tc::idesc_bf16_f32(128, 128, false, true);
       int steps = 0, ups = 0;
       for (int c = 0; !dead; ++c) {
         const int b = c & 1;
         const uint32_t kt = sbase + b * ST_BYTES + ST_K;
-        if (!mbar_wait_bounded(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
+        if (!wait_for(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
         const int flags = ctl.desc[b].flags, n = ctl.desc[b].n;
         if (flags & kEnd) break;
         if (flags & kNoU) {
           arrive(&ctl.empty[b]);
           continue;
         }
-        if (ups > 0 && !mbar_wait_bounded(&ctl.u_free, (ups - 1) & 1)) { dead = true; break; }
+        if (ups > 0 && !wait_for(&ctl.u_free, (ups - 1) & 1)) { dead = true; break; }
         const int nq = (n + QT - 1) / QT;
         for (int q = 0; q < nq; ++q, ++steps) {
           const int buf = steps & 1;
-          if (!mbar_wait_bounded(&ctl.v_full[buf], (steps >> 1) & 1)) { dead = true; break; }
+          if (!wait_for(&ctl.v_full[buf], (steps >> 1) & 1)) { dead = true; break; }
           tc::fence_after_sync();
-          // U (+)= (lo + mid + hi) K over 32 tokens, the smallest term first
-#pragma unroll
-          for (int term = 2; term >= 0; --term)
-            tc::mma_op_ts(tmem + TM_U, tmem + TM_V + buf * 48 + term * 16,
+          // U (+)= the decayed v's terms times K over 32 tokens, the smallest first
+#pragma unroll 1
+          for (int term = kTerms - 1; term >= 0; --term)
+            tc::mma_op_ts(tmem + TM_U, tmem + TM_V + (buf * kTerms + term) * 16,
                           tc::Opnd{kt + (uint32_t)q * (QT * 128), BOX, true}, QT / 16, kIdMN,
-                          q > 0 || term < 2);
+                          q > 0 || term < kTerms - 1);
           tc::commit(&ctl.v_free[buf]);
         }
         if (dead) break;
@@ -693,14 +727,14 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         tc::commit(&ctl.u_full);
         tc::commit(&ctl.empty[b]);
       }
-    } else if (warp == 15 && lane == 0 && !kState) {
+    } else if (warp == kCtlWarp + 3 && lane == 0 && !kState) {
       // ============================== store =================================
       for (int c = 0;; ++c) {
         const int b = c & 1;
-        if (!mbar_wait_bounded(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
+        if (!wait_for(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
         const Desc d = ctl.desc[b];
         if (d.flags & kEnd) break;
-        if (!mbar_wait_bounded(&ctl.staged[b], (c >> 1) & 1)) { dead = true; break; }
+        if (!wait_for(&ctl.staged[b], (c >> 1) & 1)) { dead = true; break; }
         if (d.n == CH) {
           const unsigned char* st = sm + b * ST_BYTES + ST_Q;
           tma_store_2d(&to, d.h * D, d.row, st);
