@@ -65,13 +65,13 @@ namespace {
 
 constexpr int D = 128;
 constexpr int CH = kLinChunk;  // 128
-constexpr int kThreads = 640;  // O, V and S warps (4, 8, 4), then four single-thread warps
-constexpr int kVWarps = 8, kSWarp = 12, kCtlWarp = 16;
+constexpr int kThreads = 768;  // O, V and S warps (8, 8, 4), then four single-thread warps
+constexpr int kOWarps = 8, kVWarps = 8, kSWarp = 16, kCtlWarp = 20;
 constexpr int kStages = 2;
 constexpr uint32_t TILE = 32768, BOX = 16384;  // a [128][128] bf16 tile: two 64-column boxes
 constexpr uint32_t ST_Q = 0, ST_K = TILE, ST_V = 2 * TILE, ST_BYTES = 3 * TILE;
 constexpr uint32_t OFF_S = kStages * ST_BYTES;  // S0 as B operand: [v][k], two 64-k blocks
-// tensor memory columns: P fp32 (bf16 over its first half), O, U, then the
+// tensor memory columns: P fp32 (bf16 over the first 32 of each 64), O, U, then the
 // four terms of 32 decayed v rows (16 columns each), twice
 constexpr uint32_t TM_P = 0, TM_O = 128, TM_U = 256, TM_V = 384, TM_COLS = 512;
 constexpr int QT = 32;  // tokens per step of U
@@ -104,10 +104,23 @@ constexpr uint32_t SMEM_BYTES = OFF_CTL + sizeof(Ctl);
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
 
 // A bounded wait in few instructions, as the waiting warps share the issue
-// slots with the working ones: a test that has not succeeded suspends the
-// thread for some 0.2 us, so the limit is a few seconds (at least 0.1 s).
+// slots with the working ones.  The first test has no suspend time, which
+// would add 30 cycles to a wait whose phase is complete (55); the later ones
+// have one, and the limit is a few seconds (at least 0.4 s).
 constexpr int kWaitTests = 1 << 24;
+__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+  if (try_wait(bar, parity)) return true;
   for (int i = 0; i < kWaitTests; ++i)
     if (mbar_try_wait(bar, parity)) return true;
   return false;
@@ -207,6 +220,29 @@ __device__ __forceinline__ uint32_t hfms2(uint32_t a, uint32_t b, uint32_t c) {
       : "r"(a), "r"(b), "r"(c));
   return r;
 }
+// MMA issue.  A whole warp runs the issuing loop, so that descriptors and
+// addresses stay in uniform registers, and one elected lane issues: with a
+// lone thread every operand had to be moved there, 110 cycles per MMA, which
+// bound the kernel.  Descriptors differ in their low word only: K-major
+// operands advance by 32 bytes per 16 elements (two blocks of 64, BOX apart),
+// MN-major ones by 16 rows of 128 bytes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ uint32_t desc_k(uint32_t addr) {
+  return ((addr & 0x3FFFFu) >> 4) | (1u << 16);
+}
+__device__ __forceinline__ uint32_t desc_mn(uint32_t addr) {
+  return ((addr & 0x3FFFFu) >> 4) | ((BOX >> 4) << 16);
+}
+// the high word of both: groups of 8 rows 1024 bytes apart, 128-byte swizzle
+constexpr uint64_t kDescHi = ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+__host__ __device__ constexpr uint32_t step_k(int s) { return (uint32_t)(s >> 2) * (BOX >> 4) + (uint32_t)(s & 3) * 2u; }
+constexpr uint32_t kStepMN = 2048u >> 4;
+
 template <bool kState>
 __global__ void __launch_bounds__(kThreads, 1)
 lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
@@ -215,7 +251,8 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
   extern __shared__ __align__(1024) unsigned char sm[];
   Ctl& ctl = *reinterpret_cast<Ctl*>(sm + OFF_CTL);
   pdl_wait_then_release();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   int32_t* hdr = p.work.header();
   const int n_units = (kState ? hdr[kLinStateItems] : hdr[kLinItems]) * p.H;
   if ((int)blockIdx.x >= n_units) return;
@@ -230,17 +267,17 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       // V warps, S warps, MMA 2 (and MMA 1, store)
       mbar_init(&ctl.empty[b], kVWarps + 4 + (kState ? 1 : 3));
       mbar_init(&ctl.zeroed[b], kVWarps);
-      mbar_init(&ctl.staged[b], 4);
+      mbar_init(&ctl.staged[b], kOWarps);
       mbar_init(&ctl.v_full[b], kVWarps);
       mbar_init(&ctl.v_free[b], 1);
     }
     mbar_init(&ctl.p_full, 1);
-    mbar_init(&ctl.pb_full, 4);
+    mbar_init(&ctl.pb_full, kOWarps);
     mbar_init(&ctl.qs_full, 1);
-    mbar_init(&ctl.o_scaled, 4);
+    mbar_init(&ctl.o_scaled, kOWarps);
     mbar_init(&ctl.o_full[0], 1);
     mbar_init(&ctl.o_full[1], 1);
-    mbar_init(&ctl.o_free, 4);
+    mbar_init(&ctl.o_free, kOWarps);
     mbar_init(&ctl.s_ready, 4);
     mbar_init(&ctl.u_full, 1);
     mbar_init(&ctl.u_free, 4);
@@ -253,15 +290,19 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
   const uint32_t tmem = ctl.tmem;
   bool dead = false;
 
-  // registers a thread, of 96 at launch: O 96, V 72, S 184, the others 56
-  if (warp < 4) {
+  // registers a thread, of 80 at launch: O 72, V 56, S 184, the others 40
+  if (warp < kOWarps) {
     // ============================== O warps ===============================
-    const int i = tid;  // row of the chunk, TMEM lane
-    const uint32_t tl = (uint32_t)(warp * 32) << 16;
+    // Warps w and w + 4 have rows 32 w .. 32 w + 31 of the chunk (TMEM lanes)
+    // and columns 0 .. 63 or 64 .. 127 of P and O.
+    regs_dec<72>();
+    const int rw = warp & 3, hf = warp >> 2;
+    const int i = rw * 32 + lane;
+    const uint32_t tl = (uint32_t)(rw * 32) << 16;
     int h = -1;
     float g = 0.f, after = 0.f;  // scale e^{g (i+1)}
+    float col = 0.f;             // e^{g (31 - lane)}
     bool gentle = true;
-    F2 col[16];                               // e^{g (31 - jj)}
     for (int c = 0; !kState; ++c) {
       const int b = c & 1;
       const uint32_t ph = (uint32_t)(c & 1);
@@ -273,48 +314,43 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         g = finite_decay(p.log_decay[h]);
         gentle = fabsf(g) * (float)CH <= kGentle;
         after = p.scale * expf(g * (float)(i + 1));
-        const float tab = expf(g * (float)lane);
-#pragma unroll
-        for (int jj = 0; jj < 16; ++jj)
-          col[jj] = f2(__shfl_sync(0xffffffffu, tab, 31 - 2 * jj),
-                       __shfl_sync(0xffffffffu, tab, 30 - 2 * jj));
+        col = expf(g * (float)(31 - lane));
       }
-      // ---- P: decay and mask, to bf16 over its own columns (block jb's 16
-      // land on fp32 columns read before)
+      // ---- P: decay and mask, to bf16 over the first 32 of this warp's own 64
+      // columns (block u's 16 land on fp32 columns read before)
       if (!warp_wait(&ctl.p_full, ph)) { dead = true; break; }
       tc::fence_after_sync();
 #pragma unroll 1
-      for (int jb = 0; jb < 4; ++jb) {
+      for (int u = 0; u < 2; ++u) {
+        const int jb = 2 * hf + u;
         uint32_t w[16];
-        if (jb > warp) {
+        if (jb > rw) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) w[e] = 0u;
         } else {
           float x[32];
           tc::tmem_ld32(tmem + tl + TM_P + jb * 32, x);
           // times col: e^{-g (j+1)}, or scale e^{g (i-j)} left of the diagonal
-          const float lf = gentle ? expf(-g * (float)(32 * jb + 32))
-                                  : p.scale * expf(g * (float)(i - 32 * jb - 31));
-          const F2 left = f2(lf, lf);
+          const bool direct = !gentle && jb == rw;
+          const float left = gentle   ? expf(-g * (float)(32 * jb + 32))
+                             : direct ? p.scale
+                                      : p.scale * expf(g * (float)(i - 32 * jb - 31));
+          // on the diagonal of a steep head: e^{g (lane - jj)} itself
+          const float tab = direct ? expf(g * (float)lane) : col;
           tc::tmem_wait_ld();
-          if (gentle || jb < warp) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              w[e] = bf2(mul2(mul2(f2(x[2 * e], x[2 * e + 1]), col[e]), left));
-          } else {
-            const float ts = p.scale * expf(g * (float)lane);
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              w[e] = bf2(x[2 * e] * __shfl_sync(0xffffffffu, ts, lane - 2 * e),
-                         x[2 * e + 1] * __shfl_sync(0xffffffffu, ts, lane - 2 * e - 1));
+          for (int e = 0; e < 16; ++e) {
+            const float f0 = __shfl_sync(0xffffffffu, tab, direct ? lane - 2 * e : 2 * e);
+            const float f1 = __shfl_sync(0xffffffffu, tab, direct ? lane - 2 * e - 1 : 2 * e + 1);
+            w[e] = bf2(x[2 * e] * (f0 * left), x[2 * e + 1] * (f1 * left));
           }
-          if (jb == warp) {
+          if (jb == rw) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               w[e] = lane > 2 * e ? w[e] : lane == 2 * e ? w[e] & 0xffffu : 0u;
           }
         }
-        tc::tmem_st16u(tmem + tl + TM_P + jb * 16, w);
+        tc::tmem_st16u(tmem + tl + TM_P + hf * 64 + u * 16, w);
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
@@ -323,15 +359,15 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       if (!gentle) {
         if (!warp_wait(&ctl.qs_full, ph)) { dead = true; break; }
         tc::fence_after_sync();
-        const F2 aft = f2(after, after);
 #pragma unroll 1
-        for (int jb = 0; jb < 4; ++jb) {
+        for (int u = 0; u < 2; ++u) {
           float x[32];
-          tc::tmem_ld32(tmem + tl + TM_O + jb * 32, x);
+          const uint32_t at = tmem + tl + TM_O + hf * 64 + u * 32;
+          tc::tmem_ld32(at, x);
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) unf2(mul2(f2(x[e], x[e + 1]), aft), x[e], x[e + 1]);
-          tc::tmem_st32(tmem + tl + TM_O + jb * 32, x);
+          for (int e = 0; e < 32; ++e) x[e] *= after;
+          tc::tmem_st32(at, x);
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
@@ -339,35 +375,30 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       warp_arrive(&ctl.o_scaled);
       // ---- the chunk's outputs: staged over the q tile (its products are
       // done), or, past a sequence's end, the valid rows straight out
-      unsigned char* stage = sm + b * ST_BYTES + ST_Q;
+      unsigned char* stage = sm + b * ST_BYTES + ST_Q + hf * BOX;
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + (size_t)(d.row + i) * p.ldo +
-                            (size_t)d.h * D;
+                            (size_t)d.h * D + hf * 64;
       const float of = gentle ? after : 1.f;
-      const F2 of2 = f2(of, of);
+      if (!warp_wait(&ctl.o_full[hf], ph)) { dead = true; break; }
+      tc::fence_after_sync();
 #pragma unroll 1
-      for (int jb = 0; jb < 4; ++jb) {
-        if ((jb & 1) == 0) {
-          if (!warp_wait(&ctl.o_full[jb >> 1], ph)) { dead = true; break; }
-          tc::fence_after_sync();
-        }
+      for (int u = 0; u < 2; ++u) {
         float x[32];
-        tc::tmem_ld32(tmem + tl + TM_O + jb * 32, x);
+        tc::tmem_ld32(tmem + tl + TM_O + hf * 64 + u * 32, x);
         tc::tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint4 w;
-          w.x = bf2(mul2(f2(x[8 * e], x[8 * e + 1]), of2));
-          w.y = bf2(mul2(f2(x[8 * e + 2], x[8 * e + 3]), of2));
-          w.z = bf2(mul2(f2(x[8 * e + 4], x[8 * e + 5]), of2));
-          w.w = bf2(mul2(f2(x[8 * e + 6], x[8 * e + 7]), of2));
+          w.x = bf2(x[8 * e] * of, x[8 * e + 1] * of);
+          w.y = bf2(x[8 * e + 2] * of, x[8 * e + 3] * of);
+          w.z = bf2(x[8 * e + 4] * of, x[8 * e + 5] * of);
+          w.w = bf2(x[8 * e + 6] * of, x[8 * e + 7] * of);
           if (d.n == CH)
-            *reinterpret_cast<uint4*>(stage + (jb >> 1) * BOX +
-                                      tc::sw128_offset(i, (jb & 1) * 32 + 8 * e)) = w;
+            *reinterpret_cast<uint4*>(stage + tc::sw128_offset(i, u * 32 + 8 * e)) = w;
           else if (i < d.n)
-            *reinterpret_cast<uint4*>(orow + jb * 32 + 8 * e) = w;
+            *reinterpret_cast<uint4*>(orow + u * 32 + 8 * e) = w;
         }
       }
-      if (dead) break;
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
       warp_arrive(&ctl.o_free);
@@ -380,8 +411,8 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
     // fragments: this lane gets tokens 2 (lane % 4) and the next of each 8,
     // elements lane / 4 of each 8.  (With one warp per sub-partition these
     // dependent chains took 4,800 of a chunk's 8,400 cycles.)
-    regs_dec<72>();
-    const int vw = warp & 3, half = (warp >> 2) - 1;
+    regs_dec<56>();
+    const int vw = warp & 3, half = (warp >> 2) & 1;
     const uint32_t tl = (uint32_t)(vw * 32) << 16;
     const int mr = lane & 7, mt = lane >> 4, mv = (lane >> 3) & 1;  // matrix row, token and element half
     const uint32_t off = (uint32_t)(vw >> 1) * BOX + (mt * 8 + mr) * 128 +
@@ -402,7 +433,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       // ---- rows past the sequence are another's: zeros, so that they add
       // nothing (their weights are zero, but 0 * inf is not)
       if (!full) {
-        for (int e = tid - 128; e < 2 * 128 * 8; e += 32 * kVWarps) {
+        for (int e = tid - 32 * kOWarps; e < 2 * 128 * 8; e += 32 * kVWarps) {
           const int row = (e >> 3) & 127;
           if (row >= d.n) {
             const uint32_t at = (uint32_t)(e >> 10) * BOX + row * 128 + (e & 7) * 16;
@@ -586,7 +617,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       warp_arrive(&ctl.empty[b]);
     }
   } else {
-    regs_dec<56>();
+    regs_dec<40>();
     if (warp == kCtlWarp && lane == 0) {
       // ============================== producer ==============================
       int c = 0;
@@ -654,78 +685,99 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         for (int k = c > kStages ? c - kStages : 0; k < c; ++k)
           wait_for(&ctl.full[k & 1], (k >> 1) & 1);
       }
-    } else if (warp == kCtlWarp + 1 && lane == 0 && !kState) {
+    } else if (warp == kCtlWarp + 1 && !kState) {
       // ============================== MMA 1 =================================
       constexpr uint32_t kId = tc::idesc_bf16_f32(128, 128);
       constexpr uint32_t kIdMN = tc::idesc_bf16_f32(128, 64, false, true);
+      const uint32_t s_lo = desc_k(sbase + OFF_S);
+      const bool one = elect_one();
       for (int c = 0;; ++c) {
         const int b = c & 1;
         const uint32_t ph = (uint32_t)(c & 1), st = sbase + b * ST_BYTES;
-        if (!wait_for(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
+        if (!warp_wait(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
         if (ctl.desc[b].flags & kEnd) break;
+        const uint32_t q_lo = desc_k(st + ST_Q), k_lo = desc_k(st + ST_K), v_lo = desc_mn(st + ST_V);
         // P = Q K^T, once the last chunk's P V has read P
-        if (c > 0 && !wait_for(&ctl.o_full[1], ph ^ 1)) { dead = true; break; }
+        if (c > 0 && !warp_wait(&ctl.o_full[1], ph ^ 1)) { dead = true; break; }
         tc::fence_after_sync();
-        tc::mma_op(tmem + TM_P, tc::Opnd{st + ST_Q, BOX, false}, tc::Opnd{st + ST_K, BOX, false}, 8,
-                   kId, false);
-        tc::commit(&ctl.p_full);
+        if (one) {
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+            tc::mma_bf16(tmem + TM_P, kDescHi | (q_lo + step_k(t)), kDescHi | (k_lo + step_k(t)), kId, t > 0);
+          tc::commit(&ctl.p_full);
+        }
+        __syncwarp();
         // O = Q S0
-        if (!wait_for(&ctl.s_ready, ph) ||
-            (c > 0 && !wait_for(&ctl.o_free, ph ^ 1))) {
+        if (!warp_wait(&ctl.s_ready, ph) || (c > 0 && !warp_wait(&ctl.o_free, ph ^ 1))) {
           dead = true;
           break;
         }
         tc::fence_after_sync();
-        tc::mma_op(tmem + TM_O, tc::Opnd{st + ST_Q, BOX, false}, tc::Opnd{sbase + OFF_S, BOX, false},
-                   8, kId, false);
-        tc::commit(&ctl.qs_full);
-        // O += P V
-        if (!wait_for(&ctl.zeroed[b], (c >> 1) & 1) || !wait_for(&ctl.pb_full, ph) ||
-            !wait_for(&ctl.o_scaled, ph)) {
+        if (one) {
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+            tc::mma_bf16(tmem + TM_O, kDescHi | (q_lo + step_k(t)), kDescHi | (s_lo + step_k(t)), kId, t > 0);
+          tc::commit(&ctl.qs_full);
+        }
+        __syncwarp();
+        // O += P V (P's tokens 64 .. 127 are 64 columns on)
+        if (!warp_wait(&ctl.zeroed[b], (c >> 1) & 1) || !warp_wait(&ctl.pb_full, ph) ||
+            !warp_wait(&ctl.o_scaled, ph)) {
           dead = true;
           break;
         }
         tc::fence_after_sync();
-#pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          tc::mma_op_ts(tmem + TM_O + hf * 64, tmem + TM_P, tc::Opnd{st + ST_V + hf * BOX, BOX, true},
-                        8, kIdMN, true);
-          tc::commit(&ctl.o_full[hf]);
+        if (one) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+              tc::mma_ts(tmem + TM_O + hf * 64, tmem + TM_P + (t >> 2) * 64 + (t & 3) * 8,
+                         kDescHi | (v_lo + hf * (BOX >> 4) + t * kStepMN), kIdMN, 1u);
+            tc::commit(&ctl.o_full[hf]);
+          }
+          tc::commit(&ctl.empty[b]);
         }
-        tc::commit(&ctl.empty[b]);
+        __syncwarp();
       }
-    } else if (warp == kCtlWarp + 2 && lane == 0) {
+    } else if (warp == kCtlWarp + 2) {
       // ============================== MMA 2 =================================
       constexpr uint32_t kIdMN = tc::idesc_bf16_f32(128, 128, false, true);
+      const bool one = elect_one();
       int steps = 0, ups = 0;
       for (int c = 0; !dead; ++c) {
         const int b = c & 1;
-        const uint32_t kt = sbase + b * ST_BYTES + ST_K;
-        if (!wait_for(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
+        const uint32_t k_lo = desc_mn(sbase + b * ST_BYTES + ST_K);
+        if (!warp_wait(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
         const int flags = ctl.desc[b].flags, n = ctl.desc[b].n;
         if (flags & kEnd) break;
         if (flags & kNoU) {
-          arrive(&ctl.empty[b]);
+          warp_arrive(&ctl.empty[b]);
           continue;
         }
-        if (ups > 0 && !wait_for(&ctl.u_free, (ups - 1) & 1)) { dead = true; break; }
+        if (ups > 0 && !warp_wait(&ctl.u_free, (ups - 1) & 1)) { dead = true; break; }
         const int nq = (n + QT - 1) / QT;
         for (int q = 0; q < nq; ++q, ++steps) {
           const int buf = steps & 1;
-          if (!wait_for(&ctl.v_full[buf], (steps >> 1) & 1)) { dead = true; break; }
+          if (!warp_wait(&ctl.v_full[buf], (steps >> 1) & 1)) { dead = true; break; }
           tc::fence_after_sync();
           // U (+)= the decayed v's terms times K over 32 tokens, the smallest first
-#pragma unroll 1
-          for (int term = kTerms - 1; term >= 0; --term)
-            tc::mma_op_ts(tmem + TM_U, tmem + TM_V + (buf * kTerms + term) * 16,
-                          tc::Opnd{kt + (uint32_t)q * (QT * 128), BOX, true}, QT / 16, kIdMN,
-                          q > 0 || term < kTerms - 1);
-          tc::commit(&ctl.v_free[buf]);
+          if (one) {
+#pragma unroll
+            for (int k = 0; k < 2 * kTerms; ++k)
+              tc::mma_ts(tmem + TM_U, tmem + TM_V + (buf * kTerms + kTerms - 1 - k / 2) * 16 + (k & 1) * 8,
+                         kDescHi | (k_lo + (2 * q + (k & 1)) * kStepMN), kIdMN, q > 0 || k > 0);
+            tc::commit(&ctl.v_free[buf]);
+          }
+          __syncwarp();
         }
         if (dead) break;
         ++ups;
-        tc::commit(&ctl.u_full);
-        tc::commit(&ctl.empty[b]);
+        if (one) {
+          tc::commit(&ctl.u_full);
+          tc::commit(&ctl.empty[b]);
+        }
+        __syncwarp();
       }
     } else if (warp == kCtlWarp + 3 && lane == 0 && !kState) {
       // ============================== store =================================
