@@ -72,7 +72,7 @@ constexpr uint32_t TILE = 32768, BOX = 16384;  // a [128][128] bf16 tile: two 64
 constexpr uint32_t ST_Q = 0, ST_K = TILE, ST_V = 2 * TILE, ST_BYTES = 3 * TILE;
 constexpr uint32_t OFF_S = kStages * ST_BYTES;  // S0 as B operand: [v][k], two 64-k blocks
 // tensor memory columns: P fp32 (bf16 over the first 32 of each 64), O, U, then the
-// four terms of 32 decayed v rows (16 columns each), twice
+// four terms of 32 decayed v rows, twice: per 16 rows 8 columns of each term
 constexpr uint32_t TM_P = 0, TM_O = 128, TM_U = 256, TM_V = 384, TM_COLS = 512;
 constexpr int QT = 32;  // tokens per step of U
 constexpr int kTerms = 4;
@@ -162,11 +162,6 @@ __device__ __forceinline__ F2 f2(float x, float y) {
 __device__ __forceinline__ void unf2(F2 v, float& x, float& y) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
 }
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   F2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -190,13 +185,16 @@ __device__ __forceinline__ void ldmatrix4_t(const void* at, uint32_t* r) {
                : "r"(smem_u32(at))
                : "memory");
 }
-// The same fragments as words of 16 tensor memory lanes x 8 columns: words 0
-// and 1 are lanes l / 4 and l / 4 + 8 of column l % 4, words 2 and 3 of column
-// 4 + l % 4.
-__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-               : "memory");
+// Four pairs of such fragments as words of 16 tensor memory lanes x 32 columns:
+// words 4 i and 4 i + 1 are lanes l / 4 and l / 4 + 8 of column 8 i + l % 4,
+// words 4 i + 2 and 4 i + 3 of column 8 i + 4 + l % 4.
+__device__ __forceinline__ void tmem_st_frag4(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
   return tc::pack2(lo, hi, (__nv_bfloat16*)nullptr);
@@ -330,20 +328,24 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         } else {
           float x[32];
           tc::tmem_ld32(tmem + tl + TM_P + jb * 32, x);
-          // times col: e^{-g (j+1)}, or scale e^{g (i-j)} left of the diagonal
+          // column jj's weight comes from a lane's: e^{-g (j+1)} (gentle), on
+          // the diagonal of a steep head scale e^{g (lane - jj)}, left of it
+          // e^{g (31 - jj)} times the row's scale e^{g (i - 32 jb - 31)}
           const bool direct = !gentle && jb == rw;
-          const float left = gentle   ? expf(-g * (float)(32 * jb + 32))
-                             : direct ? p.scale
-                                      : p.scale * expf(g * (float)(i - 32 * jb - 31));
-          // on the diagonal of a steep head: e^{g (lane - jj)} itself
-          const float tab = direct ? expf(g * (float)lane) : col;
+          const float tab = gentle   ? col * expf(-g * (float)(32 * jb + 32))
+                            : direct ? p.scale * expf(g * (float)lane)
+                                     : col;
+          const int dir = direct ? -1 : 1, from = direct ? lane : 0;
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float f0 = __shfl_sync(0xffffffffu, tab, direct ? lane - 2 * e : 2 * e);
-            const float f1 = __shfl_sync(0xffffffffu, tab, direct ? lane - 2 * e - 1 : 2 * e + 1);
-            w[e] = bf2(x[2 * e] * (f0 * left), x[2 * e + 1] * (f1 * left));
+          for (int e = 0; e < 32; ++e) x[e] *= __shfl_sync(0xffffffffu, tab, from + dir * e);
+          if (!gentle && !direct) {
+            const float row = p.scale * expf(g * (float)(i - 32 * jb - 31));
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] *= row;
           }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = bf2(x[2 * e], x[2 * e + 1]);
           if (jb == rw) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
@@ -418,10 +420,10 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
     const uint32_t off = (uint32_t)(vw >> 1) * BOX + (mt * 8 + mr) * 128 +
                          ((((vw & 1) * 4 + mv) ^ mr) << 4);
     const int tl0 = 2 * (lane & 3);  // this lane's first token of each 8
-    const F2 minus = f2(-1.f, -1.f);
-    int h = -1, steps = 0;
-    float g = 0.f, blk8 = 0.f;  // e^{8 g lane}
-    F2 in8 = 0;                 // e^{g (7 - token)} of this lane's tokens in each 8
+    int h = -1, w_n = -1, steps = 0;
+    // the weights' three bf16 terms of tokens 2 lane and 2 lane + 1 (wa), and
+    // 64 more (wb)
+    uint32_t wa[3] = {0, 0, 0}, wb[3] = {0, 0, 0};
     for (int c = 0;; ++c) {
       const int b = c & 1;
       if (!warp_wait(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
@@ -444,11 +446,23 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         tc::fence_proxy_async_smem();
       }
       warp_arrive(&ctl.zeroed[b]);
-      if (d.h != h) {
+      if (d.h != h || d.n != w_n) {
         h = d.h;
-        g = finite_decay(p.log_decay[h]);
-        blk8 = expf(g * 8.f * (float)lane);
-        in8 = f2(expf(g * (float)(7 - tl0)), expf(g * (float)(6 - tl0)));
+        w_n = d.n;
+        const float g = finite_decay(p.log_decay[h]);
+        const F2 minus = f2(-1.f, -1.f);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int back = w_n - 1 - 64 * u - 2 * lane;  // tokens behind the first of the pair
+          F2 w = f2(back >= 0 ? expf(g * (float)back) : 0.f,
+                    back >= 1 ? expf(g * (float)(back - 1)) : 0.f);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            const uint32_t r = bf2(w);
+            w = fma2(widen(r), minus, w);
+            (u ? wb : wa)[k] = r;
+          }
+        }
       }
       const int nq = (d.n + QT - 1) / QT;
       for (int q = 0; q < nq; ++q) {
@@ -461,51 +475,43 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         uint32_t x[8];
         ldmatrix4_t(vt + t0 * 128 + off, x);
         ldmatrix4_t(vt + t0 * 128 + (off ^ 32u), x + 4);
-        F2 w[2];  // the weights of this lane's tokens in each 8
-        bool ok[2][2];
+        // the weights of this lane's tokens in each 8
+        uint32_t w[2][3];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          const int tok = t0 + 8 * m + tl0;
-          ok[m][0] = tok < d.n;
-          ok[m][1] = tok + 1 < d.n;
-          if (full) {
-            const float a = __shfl_sync(0xffffffffu, blk8, 15 - (t0 >> 3) - m);
-            w[m] = mul2(in8, f2(a, a));
-          } else {
-            w[m] = f2(ok[m][0] ? expf(g * (float)(d.n - 1 - tok)) : 0.f,
-                      ok[m][1] ? expf(g * (float)(d.n - 2 - tok)) : 0.f);
+          const int from = ((t0 & 63) >> 1) + 4 * m + (lane & 3);
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            w[m][k] = __shfl_sync(0xffffffffu, t0 < 64 ? wa[k] : wb[k], from);
+        }
+        if (!full) {
+          // rows past n read as zeros or, before another warp's stores, as the
+          // neighbour's bits
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const int left = d.n - (t0 + 8 * m + tl0);
+            const uint32_t keep = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
+            x[2 * m] &= keep;
+            x[2 * m + 1] &= keep;
+            x[2 * m + 4] &= keep;
+            x[2 * m + 5] &= keep;
           }
         }
-        // the weights' three bf16 terms, and their products' four
-        uint32_t wh[2], wm[2], wl[2];
+        // the products' four terms, 16 elements v at a time
+        const uint32_t at = tmem + tl + TM_V + (buf * 2 + half) * (8 * kTerms);
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          wh[m] = bf2(w[m]);
-          w[m] = fma2(widen(wh[m]), minus, w[m]);
-          wm[m] = bf2(w[m]);
-          w[m] = fma2(widen(wm[m]), minus, w[m]);
-          wl[m] = bf2(w[m]);
-        }
-        uint32_t t[kTerms][8];
+        for (int v2 = 0; v2 < 2; ++v2) {
+          uint32_t t[kTerms][4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int m = (e >> 1) & 1;
-          // rows past n read as zeros or, before another warp's stores, as
-          // the neighbour's bits
-          if (!full) x[e] &= (ok[m][0] ? 0xffffu : 0u) | (ok[m][1] ? 0xffff0000u : 0u);
-          t[0][e] = hmul2(x[e], wh[m]);
-          t[1][e] = hfms2(x[e], wh[m], t[0][e]);
-          t[2][e] = hmul2(x[e], wm[m]);
-          t[3][e] = hfma2(x[e], wl[m], hfms2(x[e], wm[m], t[2][e]));
-        }
-        if (!(d.flags & kNoU)) {
-          const uint32_t at = tmem + tl + TM_V + buf * (16 * kTerms) + 8 * half;
-          constexpr uint32_t kUpper = 16u << 16;  // lanes 16 ..
-#pragma unroll
-          for (int k = 0; k < kTerms; ++k) {
-            tmem_st_frag(at + 16 * k, t[k]);
-            tmem_st_frag(at + 16 * k + kUpper, t[k] + 4);
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t y = x[4 * v2 + e];
+            const uint32_t* wt = w[e >> 1];
+            t[0][e] = hmul2(y, wt[0]);
+            t[1][e] = hfms2(y, wt[0], t[0][e]);
+            t[2][e] = hmul2(y, wt[1]);
+            t[3][e] = hfma2(y, wt[2], hfms2(y, wt[1], t[2][e]));
           }
+          if (!(d.flags & kNoU)) tmem_st_frag4(at + v2 * (16u << 16), t[0]);
         }
         if (!(d.flags & kNoU)) {
           tc::tmem_wait_st();
@@ -765,7 +771,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
           if (one) {
 #pragma unroll
             for (int k = 0; k < 2 * kTerms; ++k)
-              tc::mma_ts(tmem + TM_U, tmem + TM_V + (buf * kTerms + kTerms - 1 - k / 2) * 16 + (k & 1) * 8,
+              tc::mma_ts(tmem + TM_U, tmem + TM_V + ((buf * 2 + (k & 1)) * kTerms + kTerms - 1 - k / 2) * 8,
                          kDescHi | (k_lo + (2 * q + (k & 1)) * kStepMN), kIdMN, q > 0 || k > 0);
             tc::commit(&ctl.v_free[buf]);
           }
