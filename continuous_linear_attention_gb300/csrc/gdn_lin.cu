@@ -241,7 +241,9 @@ lin_recurrent_kernel(LinParams p) {
   constexpr int kSlices = D / kSlice;
   __shared__ __align__(16) RecSmem<T, D> sm;
   // late: launched behind the chunk kernel, whose idle SMs it takes without
-  // waiting for it (other sequences, other blocks); it waits before it ends
+  // waiting for it (other sequences, other blocks); before it ends it waits,
+  // and computes what the chunk kernel has marked: columns whose blocks still
+  // hold the old state
   if (p.late)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   else
@@ -254,31 +256,25 @@ lin_recurrent_kernel(LinParams p) {
     if (p.listed) s = p.work.dec()[s];
     recurrent_unit<T, D>(p, sm, s, h, slice, !p.listed);
   }
-  if (p.late) asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-// What the chunked form has marked: columns whose blocks still hold the old
-// state.
-__global__ void __launch_bounds__(kRecThreads) lin_redo_kernel(LinParams p) {
-  static_assert(kLinSlices * kSlice == 128, "a mark covers one unit");
-  __shared__ __align__(16) RecSmem<__nv_bfloat16, 128> sm;
-  pdl_wait_then_release();
+  if (!p.late) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int32_t* hdr = p.work.header();
   if (!hdr[kLinBad]) return;
-  const long long n = (long long)hdr[kNPre] * p.H * kLinSlices;
+  const long long n = (long long)hdr[kNPre] * p.H * kSlices;
   for (long long u = blockIdx.x; u < n; u += gridDim.x) {
     if (!p.bad[u]) continue;
-    const long long chain = u / kLinSlices;
+    const long long chain = u / kSlices;
     __syncthreads();
-    recurrent_unit<__nv_bfloat16, 128>(p, sm, p.work.pre()[chain / p.H], (int)(chain % p.H),
-                                       (int)(u % kLinSlices), false);
+    recurrent_unit<T, D>(p, sm, p.work.pre()[chain / p.H], (int)(chain % p.H), (int)(u % kSlices),
+                         false);
   }
 }
 
 // --- scheduler ---------------------------------------------------------------
 constexpr int kSchedThreads = 1024;
 
-constexpr int kSortMax = 8192;  // long sequences that are put in order
+constexpr int kSortMax = 4096;    // long sequences that are put in order
+constexpr int kSmemCounts = 4096;  // pools whose block-use counts fit into shared memory
 constexpr int kMinSegment = 8;  // chunks
 
 // One CTA.  Checks the batch as the pool's contract demands, lists its
@@ -288,12 +284,12 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms) {
   __shared__ unsigned s_flags;
   __shared__ int s_dec, s_pre, s_segs;
   __shared__ unsigned long long s_total;
-  __shared__ int32_t chunks[kSortMax];
+  __shared__ int32_t chunks[kSortMax], counts[kSmemCounts];
   __shared__ int warp_sums[32];
   pdl_wait_then_release();
   const int tid = threadIdx.x, N = p.N, nb = p.num_blocks;
   int32_t* hdr = p.work.header();
-  int32_t* uses = p.work.blk_count();
+  int32_t* uses = nb <= kSmemCounts ? counts : p.work.blk_count();
   if (tid == 0) {
     s_flags = 0u;
     s_dec = s_pre = s_segs = 0;
@@ -429,10 +425,6 @@ cudaError_t launch_lin_recurrent(const LinParams& p, int d, int act, int max_ite
 
 cudaError_t launch_lin_schedule(const LinParams& p, int short_max, int num_sms, cudaStream_t s) {
   return launch_pdl(lin_schedule_kernel, dim3(1), dim3(kSchedThreads), 0, s, p, short_max, num_sms);
-}
-
-cudaError_t launch_lin_redo(const LinParams& p, int num_sms, cudaStream_t s) {
-  return launch_pdl(lin_redo_kernel, dim3(4 * num_sms), dim3(kRecThreads), 0, s, p);
 }
 
 namespace {
@@ -582,8 +574,12 @@ int gdn_lin_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
   p->last_path = chunked                             ? GDN_PREFILL_FUSED
                  : T > 1 && max_seqlen_hint != 1 ? GDN_PREFILL_SERIAL
                                                      : GDN_PREFILL_NONE;
-  // heads enough for every SM, or too few tokens to cut: never split
-  const bool may_split = H < 2 * sms && T >= 2 * 8 * gdn::kLinChunk;
+  // the scheduler's rule for splitting (see there) on what the host knows: no
+  // sequence is longer than T or the hint, and all tokens are some chunk's
+  const long long longest =
+      ((max_seqlen_hint > 0 && max_seqlen_hint < T ? max_seqlen_hint : T) - 1) / gdn::kLinChunk + 1;
+  const bool may_split = longest >= 2 * gdn::kMinSegment &&
+                         4 * longest * sms > 5ll * (T / gdn::kLinChunk) * H;
   if (chunked) {
     lp.seg_states = may_split ? p->lin_states : nullptr;
     lp.seg_slots = p->lin_slots;
@@ -598,7 +594,6 @@ int gdn_lin_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
   if (chunked && gdn::launch_lin_chunk(lp, may_split, sms, s) != cudaSuccess) return GDN_ERR_CUDA;
   if (gdn::launch_lin_recurrent(lp, d, p->act, lp.listed ? max_items : N, s) != cudaSuccess)
     return GDN_ERR_CUDA;
-  if (chunked && gdn::launch_lin_redo(lp, sms, s) != cudaSuccess) return GDN_ERR_CUDA;
   if (p->ev_after && cudaEventRecord(p->ev_after, s) != cudaSuccess) return GDN_ERR_CUDA;
   return GDN_OK;
 }

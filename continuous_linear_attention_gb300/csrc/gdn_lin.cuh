@@ -75,10 +75,9 @@ __device__ __forceinline__ float finite_decay(float g) { return g == -INFINITY ?
 // (pre_cp[]: segments before entry k).
 cudaError_t launch_lin_schedule(const LinParams& p, int short_max, int num_sms, cudaStream_t s);
 // The token-serial kernel over the scheduler's dec[] list (p.listed) or over
-// all N sequences, which it then validates itself.
+// all N sequences, which it then validates itself; behind the chunked form
+// (p.late) also over what that has marked.
 cudaError_t launch_lin_recurrent(const LinParams& p, int d, int act, int max_items, cudaStream_t s);
-// The same over what the chunked form has marked (d = 128, bf16).
-cudaError_t launch_lin_redo(const LinParams& p, int num_sms, cudaStream_t s);
 // The chunked form over pre[] (d = 128, bf16); may_split: with the state pass
 // that split sequences need.
 bool lin_chunk_supported(int d, int act);

@@ -814,12 +814,13 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
 
 // The states at the segments' starts, from the segments' own: in place,
 // Z[0] <- S0, Z[i] <- e^{g n} Z[i-1] + (the old Z[i-1]) with n tokens per
-// segment.  One float4 of one head's state per thread.
+// segment.  One float4 of one head's state per thread, the reads of eight
+// segments at a time in flight.
 __global__ void __launch_bounds__(256) lin_segments_kernel(LinParams p) {
   pdl_wait_then_release();
   const int32_t* hdr = p.work.header();
   const int n_split = hdr[kLinSplit];
-  constexpr int kParts = D * D / 4 / 256;
+  constexpr int kParts = D * D / 4 / 256, kAhead = 8;
   const int n_units = n_split * p.H * kParts;
   for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
     const int part = u % kParts, h = (u / kParts) % p.H, e = u / (kParts * p.H);
@@ -833,13 +834,20 @@ __global__ void __launch_bounds__(256) lin_segments_kernel(LinParams p) {
       S = reinterpret_cast<const float4*>(p.layer_base + (size_t)blk * p.stride)[(size_t)h * D * D / 4 + at];
     float4* z = reinterpret_cast<float4*>(p.seg_states) + ((size_t)first * p.H + h) * (D * D / 4) + at;
     const size_t step = (size_t)p.H * (D * D / 4);
-    for (int i = 0; i < nseg; ++i, z += step) {
-      const float4 own = i < nseg - 1 ? *z : S;
-      *z = S;
-      S.x = fmaf(a.hi, S.x, fmaf(a.lo, S.x, own.x));
-      S.y = fmaf(a.hi, S.y, fmaf(a.lo, S.y, own.y));
-      S.z = fmaf(a.hi, S.z, fmaf(a.lo, S.z, own.z));
-      S.w = fmaf(a.hi, S.w, fmaf(a.lo, S.w, own.w));
+    for (int i0 = 0; i0 < nseg; i0 += kAhead) {
+      float4 own[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)  // (the last segment's own state is not there)
+        if (i0 + i < nseg - 1) own[i] = z[(i0 + i) * step];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (i0 + i >= nseg) break;
+        z[(i0 + i) * step] = S;
+        S.x = fmaf(a.hi, S.x, fmaf(a.lo, S.x, own[i].x));
+        S.y = fmaf(a.hi, S.y, fmaf(a.lo, S.y, own[i].y));
+        S.z = fmaf(a.hi, S.z, fmaf(a.lo, S.z, own[i].z));
+        S.w = fmaf(a.hi, S.w, fmaf(a.lo, S.w, own[i].w));
+      }
     }
   }
 }
