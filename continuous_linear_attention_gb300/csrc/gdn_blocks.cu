@@ -14,6 +14,8 @@
 // per node, i.e. trees whose roots are last moves or cycles.  The planning
 // kernel orders the trees by their distance to the root (pointer jumping) and
 // walks each cycle; a cycle's last source is first read into a spare buffer.
+// Components of that graph are independent of each other, so the work is cut
+// into (part of the components, column).
 //
 // Traffic: every distinct source is read once, however many destinations it
 // has, and every destination written once, the least the call can do.  The
@@ -31,6 +33,7 @@ constexpr int kPlanThreads = 1024;
 // pools of up to this many blocks keep the planning arrays in shared memory
 constexpr int kSmemBlocks = 8192;
 constexpr int kPlanArrays = 6;
+constexpr int kMaxLevels = 64;  // deeper trees are not divided into components
 // kinds of a move, in bits 30-31 of its source
 enum Kind : uint32_t { kCopy = 0, kHold = 1, kStoreHeld = 2 };
 constexpr uint32_t kBlockMask = (1u << 30) - 1;
@@ -41,7 +44,7 @@ plan_copies_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ 
                    BlockWork bw, uint32_t* err) {
   extern __shared__ int32_t plan_smem[];
   __shared__ unsigned s_flags;
-  __shared__ int s_ops, s_dsts, s_cyc;
+  __shared__ int s_ops, s_dsts, s_comps, s_depth;
   __shared__ int warp_sums[32];
   pdl_wait_then_release();
   const int tid = threadIdx.x;
@@ -54,7 +57,7 @@ plan_copies_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ 
   int32_t* DQ = a + 5 * (size_t)nb;
   if (tid == 0) {
     s_flags = 0u;
-    s_ops = s_dsts = s_cyc = 0;
+    s_ops = s_dsts = s_comps = s_depth = 0;
   }
   for (int x = tid; x < nb; x += kPlanThreads) {
     W[x] = -1;
@@ -88,19 +91,36 @@ plan_copies_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ 
   int hazard = 0;
   for (int x = tid; x < nb; x += kPlanThreads) hazard |= cnt[x] > 0 && W[x] >= 0;
   int32_t *osrc = bw.src(), *obeg = bw.beg(), *ocnt = bw.cnt();
-  // appends a move at place k; DQ[x] becomes where x's destinations go
+  // move k is x's; cnt[x] becomes where x's destinations go
   auto emit = [&](int k, int x, uint32_t kind) {
     const int c = kind == kHold ? 0 : cnt[x];
     const int at = atomicAdd(&s_dsts, c);
     osrc[k] = (int32_t)((uint32_t)x | (kind << 30));
     obeg[k] = at;
     ocnt[k] = c;
-    if (kind != kHold) DQ[x] = at;
+    if (kind != kHold) cnt[x] = at;
   };
+  // a cycle from x, its lowest block: its last source into the spare buffer,
+  // the others in order, then the held one
+  auto emit_cycle = [&](int k, int x) {
+    int last = x;
+    while (W[last] != x) last = W[last];
+    emit(k++, last, kHold);
+    for (int z = x; z != last; z = W[z]) emit(k++, z, kCopy);
+    emit(k, last, kStoreHeld);
+  };
+  // moves of the cycle that x leads, or 0 if a lower block does
+  auto cycle_moves = [&](int x) {
+    int len = 2, y = W[x];
+    for (; y > x; y = W[y]) ++len;
+    return y == x ? len : 0;
+  };
+  int single = 0;
   if (!__syncthreads_or(hazard)) {
-    // no source is written (a fork): any order
+    // no source is written (a fork): any order, every move by itself
     for (int x = tid; x < nb; x += kPlanThreads)
       if (cnt[x] > 0) emit(atomicAdd(&s_ops, 1), x, kCopy);
+    single = 1;
   } else {
     int rounds = 1;
     while ((1 << rounds) < nb) ++rounds;
@@ -108,19 +128,27 @@ plan_copies_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ 
     // and every source of a cycle is such an end
     for (int x = tid; x < nb; x += kPlanThreads) P[x] = cnt[x] > 0 ? W[x] : -1;
     __syncthreads();
-    for (int r = 0; r < rounds; ++r) {
-      for (int x = tid; x < nb; x += kPlanThreads) Q[x] = P[x] < 0 ? -1 : P[P[x]];
-      __syncthreads();
+    bool cycles = true;
+    for (int r = 0; r < rounds && cycles; ++r) {
+      int more = 0;
+      for (int x = tid; x < nb; x += kPlanThreads) {
+        const int y = P[x] < 0 ? -1 : P[P[x]];
+        Q[x] = y;
+        more |= y >= 0;
+      }
+      cycles = __syncthreads_or(more) != 0;
       int32_t* t = P;
       P = Q;
       Q = t;
     }
     for (int x = tid; x < nb; x += kPlanThreads) Q[x] = 0;
     __syncthreads();
-    for (int x = tid; x < nb; x += kPlanThreads)
-      if (P[x] >= 0) Q[P[x]] = 1;
+    if (cycles)
+      for (int x = tid; x < nb; x += kPlanThreads)
+        if (P[x] >= 0) Q[P[x]] = 1;
     __syncthreads();
-    // distance of every other source to its root or cycle
+    // every other source's root (a last source, or one on a cycle) and its
+    // distance to it
     int32_t* cyc = Q;
     int32_t* nxt = P;
     for (int x = tid; x < nb; x += kPlanThreads) {
@@ -129,57 +157,106 @@ plan_copies_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ 
       DP[x] = tree ? 1 : 0;
     }
     __syncthreads();
-    // (pointers jump in place, in two phases, as both their arrays are needed)
     for (int r = 0; r < rounds; ++r) {
-      for (int x0 = 0; x0 < nb; x0 += kPlanThreads) {
-        const int x = x0 + tid;
-        if (x < nb) DQ[x] = DP[x] + DP[nxt[x]];
-      }
+      for (int x = tid; x < nb; x += kPlanThreads) DQ[x] = DP[x] + DP[nxt[x]];
       __syncthreads();
       int32_t* t = DP;
       DP = DQ;
       DQ = t;
-      // DQ is free until the next round: the jumped pointers pass through it
-      for (int x = tid; x < nb; x += kPlanThreads) DQ[x] = nxt[nxt[x]];
-      __syncthreads();
+      // the old distances' array takes the jumped pointers
+      int more = 0;
+      for (int x = tid; x < nb; x += kPlanThreads) {
+        const int y = nxt[nxt[x]];
+        more |= y != nxt[x];
+        DQ[x] = y;
+      }
       t = nxt;
       nxt = DQ;
       DQ = t;
+      if (!__syncthreads_or(more)) break;
     }
-    // places by falling distance: counting sort (the histogram over nxt)
-    int32_t* hist = nxt;
-    for (int x = tid; x < nb; x += kPlanThreads) hist[x] = 0;
-    __syncthreads();
     for (int x = tid; x < nb; x += kPlanThreads)
-      if (cnt[x] > 0 && !cyc[x]) atomicAdd(&hist[DP[x]], 1);
+      if (cnt[x] > 0) atomicMax(&s_depth, DP[x]);
+    // the lowest block of a cycle leads it: the root of its component
+    if (cycles)
+      for (int x = tid; x < nb; x += kPlanThreads)
+        if (cyc[x] && cycle_moves(x)) {
+          int z = x;
+          do {
+            nxt[z] = x;
+            z = W[z];
+          } while (z != x);
+        }
     __syncthreads();
-    int carry = 0;
-    for (int x0 = 0; x0 < nb; x0 += kPlanThreads) {
-      const int x = nb - 1 - (x0 + tid);
-      int total;
-      const int before = cta_scan(x >= 0 ? hist[x] : 0, &total, warp_sums);
-      if (x >= 0) hist[x] = carry + before;
-      carry += total;
-    }
-    if (tid == 0) s_ops = carry;
+    const int depth = s_depth;
+    int32_t* place = DQ;
+    for (int x = tid; x < nb; x += kPlanThreads) place[x] = 0;
     __syncthreads();
-    for (int x = tid; x < nb; x += kPlanThreads)
-      if (cnt[x] > 0 && !cyc[x]) emit(atomicAdd(&hist[DP[x]], 1), x, kCopy);
-    // each cycle by its lowest block: its last source into the spare buffer,
-    // the others in order, then the held one
-    for (int x = tid; x < nb; x += kPlanThreads) {
-      if (!cyc[x]) continue;
-      int len = 1, y = W[x], last = x;
-      while (y > x) {
-        last = y;
-        y = W[y];
-        ++len;
+    if (depth <= kMaxLevels) {
+      // components one after the other, in each the trees from the leaves
+      // down, then the cycle
+      auto root = [&](int x) { return nxt[nxt[x]]; };
+      for (int x = tid; x < nb; x += kPlanThreads) {
+        if (cnt[x] == 0) continue;
+        if (!cyc[x]) atomicAdd(&place[root(x)], 1);
+        else if (nxt[x] == x) atomicAdd(&place[x], cycle_moves(x));
       }
-      if (y != x) continue;  // a lower block leads this cycle
-      int k = carry + atomicAdd(&s_cyc, len + 1);
-      emit(k++, last, kHold);
-      for (int z = x; z != last; z = W[z]) emit(k++, z, kCopy);
-      emit(k, last, kStoreHeld);
+      __syncthreads();
+      int moves = 0, comps = 0;
+      for (int x0 = 0; x0 < nb; x0 += kPlanThreads) {
+        const int x = x0 + tid, n_x = x < nb ? place[x] : 0;
+        int tm, tc;
+        const int at = moves + cta_scan(n_x, &tm, warp_sums);
+        const int ct = comps + cta_scan(n_x > 0, &tc, warp_sums);
+        if (n_x > 0) {
+          place[x] = at;
+          bw.start()[ct] = at;
+        }
+        moves += tm;
+        comps += tc;
+      }
+      if (tid == 0) {
+        s_ops = moves;
+        s_comps = comps;
+        bw.start()[comps] = moves;
+      }
+      for (int level = depth; level >= 0; --level) {
+        __syncthreads();
+        for (int x = tid; x < nb; x += kPlanThreads)
+          if (DP[x] == level && !cyc[x] && cnt[x] > 0)
+            emit(atomicAdd(&place[root(x)], 1), x, kCopy);
+      }
+      __syncthreads();
+      if (cycles)
+        for (int x = tid; x < nb; x += kPlanThreads)
+          if (cyc[x] && nxt[x] == x) emit_cycle(place[x], x);
+    } else {
+      // long chains: all trees by falling distance (a counting sort), then the
+      // cycles, as one run of moves
+      for (int x = tid; x < nb; x += kPlanThreads)
+        if (cnt[x] > 0 && !cyc[x]) atomicAdd(&place[DP[x]], 1);
+      __syncthreads();
+      int moves = 0;
+      for (int x0 = 0; x0 < nb; x0 += kPlanThreads) {
+        const int x = nb - 1 - (x0 + tid);
+        int total;
+        const int before = cta_scan(x >= 0 ? place[x] : 0, &total, warp_sums);
+        if (x >= 0) place[x] = moves + before;
+        moves += total;
+      }
+      if (tid == 0) s_ops = moves;
+      __syncthreads();
+      for (int x = tid; x < nb; x += kPlanThreads)
+        if (cnt[x] > 0 && !cyc[x]) emit(atomicAdd(&place[DP[x]], 1), x, kCopy);
+      __syncthreads();
+      for (int x = tid; x < nb; x += kPlanThreads)
+        if (cyc[x] && nxt[x] == x) emit_cycle(atomicAdd(&s_ops, cycle_moves(x)), x);
+      __syncthreads();
+      if (tid == 0) {
+        s_comps = 1;
+        bw.start()[0] = 0;
+        bw.start()[1] = s_ops;
+      }
     }
   }
   __syncthreads();
@@ -187,10 +264,13 @@ plan_copies_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ 
   for (int e = tid; e < n; e += kPlanThreads) {
     const int s = src[e], d = dst[e];
     if (s < 0 || d <= 0 || s >= nb || d >= nb || s == d || W[d] != s) continue;
-    odst[atomicAdd(&DQ[s], 1)] = d;
+    odst[atomicAdd(&cnt[s], 1)] = d;
   }
   if (tid == 0) {
-    bw.header()[0] = s_ops + s_cyc;
+    bw.header()[0] = s_ops;
+    bw.header()[1] = single ? s_ops : s_comps;
+    bw.header()[2] = 0;
+    bw.header()[3] = single;
     if (s_flags) atomicOr(err, s_flags);
   }
 }
@@ -247,19 +327,30 @@ plan_compact_kernel(const int32_t* idx, int32_t* new_idx, int n, int nb, BlockWo
     new_idx[e] = b > m && b < nb ? to[b] : b;
   }
   if (tid == 0) {
-    bw.header()[0] = highs;
+    bw.header()[0] = bw.header()[1] = highs;
+    bw.header()[2] = 0;
+    bw.header()[3] = 1;
     if (s_flags) atomicOr(err, s_flags);
   }
 }
 
 // --- the moves -------------------------------------------------------------
 constexpr int kWarps = 4;
-constexpr int kPiece = 8192;   // bytes of a column, at most
-constexpr int kSlots = 5;      // pieces in flight per warp
-constexpr int kCached = 1024;  // moves (and destinations) kept in shared memory
+constexpr int kPiece = 8192;     // bytes of a column, at most
+constexpr int kMinPiece = 1024;  // and at least
+constexpr int kSlots = 5;        // pieces in flight per warp, loads and stores
+constexpr int kPending = 2;      // stores that may still read their pieces
+constexpr int kCached = 1024;    // moves (and destinations) kept in shared memory
+constexpr int kUnits = 8;        // units a warp has begun and not finished
+struct Unit {
+  unsigned char* at;  // the column in block 0
+  uint32_t bytes;
+  int k0, k1;         // moves
+};
 struct MoveSmem {
   unsigned char buf[kWarps][kSlots + 1][kPiece];  // the last one holds a cycle's source
   uint64_t full[kWarps][kSlots + 1];
+  Unit unit[kWarps][kUnits];
   int32_t src[kCached], beg[kCached], cnt[kCached], dst[kCached];
 };
 static_assert(sizeof(MoveSmem) <= 227 * 1024, "shared memory of one CTA");
@@ -267,7 +358,7 @@ static_assert(sizeof(MoveSmem) <= 227 * 1024, "shared memory of one CTA");
 struct MoveParams {
   unsigned char* base;  // block 0 of the first layer moved
   size_t stride;
-  int nb, layers, piece, cols;  // cols: columns of `piece` bytes per block
+  int nb, layers;
   BlockWork bw;
   uint32_t* err;
 };
@@ -277,7 +368,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) move_blocks_kernel(MoveParams 
   MoveSmem& sm = *reinterpret_cast<MoveSmem*>(smem_raw);
   pdl_wait_then_release();
   const int tid = threadIdx.x, warp = tid >> 5;
-  const int ops = p.bw.header()[0];
+  int32_t* hdr = p.bw.header();
+  const int ops = hdr[0], comps = hdr[1];
+  const bool single = hdr[3] != 0;
   if (ops == 0) return;
   for (int i = tid; i < kCached; i += kWarps * 32) {
     if (i < ops) {
@@ -299,42 +392,74 @@ __global__ void __launch_bounds__(kWarps * 32, 1) move_blocks_kernel(MoveParams 
   unsigned char(*buf)[kPiece] = sm.buf[warp];
   uint64_t* full = sm.full[warp];
 
-  const long long ncol = (long long)p.layers * p.cols;
-  const long long step = (long long)gridDim.x * kWarps;
-  // the load cursor runs ahead of the store cursor over (column, move)
-  long long lcol = (long long)blockIdx.x * kWarps + warp, scol = lcol;
-  int lk = 0, sk = 0;
-  long long loads = 0, stores = 0;  // pieces loaded into, and stored from, the ring
-  long long holds = 0;
-  bool held = false;
-  auto piece_at = [&](long long col, uint32_t* bytes) {
-    const int layer = (int)(col / p.cols), c = (int)(col % p.cols);
-    const size_t off = (size_t)c * p.piece;
-    *bytes = (uint32_t)min((size_t)p.piece, p.stride - off);
-    return p.base + (size_t)layer * p.nb * p.stride + off;
+  // The units: columns as wide as leaves four per warp, by as many parts of
+  // the components as make eight.
+  const long long warps = (long long)gridDim.x * kWarps;
+  int piece = kPiece;
+  auto cols_of = [&](int b) { return (long long)((p.stride + b - 1) / b); };
+  while (piece > kMinPiece && p.layers * cols_of(piece) * comps < 4 * warps) piece /= 2;
+  const long long cols = cols_of(piece), ncol = p.layers * cols;
+  const long long want = (8 * warps + ncol - 1) / ncol;
+  const int parts = (int)(want < comps ? want : comps);
+  // first move of part i: that of the first component at or behind its share
+  auto part_begin = [&](int i) {
+    const int at = (int)((long long)i * ops / parts);
+    if (single || at == ops) return at;
+    const int32_t* start = p.bw.start();
+    int lo = 0, hi = comps;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (start[mid] < at) lo = mid + 1; else hi = mid;
+    }
+    return start[lo];
   };
-  while (scol < ncol) {
-    // loads: as far ahead as the ring (free: all pieces but those being
-    // loaded or stored) and the spare buffer allow
-    while (lcol < ncol) {
+  const unsigned long long n_units = (unsigned long long)ncol * parts;
+  // the next unit that has moves, claimed one ahead
+  auto claim = [&]() {
+    Unit u = {nullptr, 0, 0, 0};
+    for (;;) {
+      const unsigned long long i = atomicAdd((unsigned*)&hdr[2], 1u);
+      if (i >= n_units) return u;
+      const int part = (int)(i % parts);
+      const long long col = (long long)(i / parts);
+      u.k0 = part_begin(part);
+      u.k1 = part_begin(part + 1);
+      if (u.k0 == u.k1) continue;
+      const size_t off = (size_t)(col % cols) * piece;
+      u.bytes = (uint32_t)min((size_t)piece, p.stride - off);
+      u.at = p.base + (size_t)(col / cols) * p.nb * p.stride + off;
+      return u;
+    }
+  };
+  // the load cursor runs ahead of the store cursor over the units' moves;
+  // pieces of the ring: loaded, issued to store, and read by their store
+  Unit lu = claim(), next = lu.at ? claim() : lu;
+  int lk = lu.k0, lq = 0, sq = 0, sk = lu.k0;
+  sm.unit[warp][0] = lu;
+  long long loads = 0, stores = 0, holds = 0;
+  bool held = false;
+  while (sm.unit[warp][sq % kUnits].at) {
+    // loads, as far ahead as the ring and the spare buffer allow
+    while (lu.at) {
       const uint32_t s = src_of(lk), kind = s >> 30;
-      if (kind == kCopy && loads - stores >= kSlots) break;
+      if (kind == kCopy && loads - max(stores - kPending, 0ll) >= kSlots) break;
       if (kind == kHold && held) break;
       if (kind != kStoreHeld) {
-        uint32_t bytes;
-        const unsigned char* at = piece_at(lcol, &bytes) + (size_t)(s & kBlockMask) * p.stride;
         const int slot = kind == kHold ? kSlots : (int)(loads % kSlots);
-        mbar_arrive_expect_tx(&full[slot], bytes);
-        bulk_g2s(buf[slot], at, bytes, &full[slot]);
+        mbar_arrive_expect_tx(&full[slot], lu.bytes);
+        bulk_g2s(buf[slot], lu.at + (size_t)(s & kBlockMask) * p.stride, lu.bytes, &full[slot]);
         if (kind == kHold) held = true;
         else ++loads;
       }
-      if (++lk == ops) {
-        lk = 0;
-        lcol += step;
+      if (++lk == lu.k1) {
+        lu = next;
+        lk = lu.k0;
+        sm.unit[warp][++lq % kUnits] = lu;
+        if (lu.at) next = claim();
       }
     }
     // one move
+    const Unit su = sm.unit[warp][sq % kUnits];
     const uint32_t s = src_of(sk), kind = s >> 30;
     const bool ring = kind == kCopy;
     const int slot = ring ? (int)(stores % kSlots) : kSlots;
@@ -352,20 +477,23 @@ __global__ void __launch_bounds__(kWarps * 32, 1) move_blocks_kernel(MoveParams 
       if (kind == kHold) ++holds;
     }
     if (kind != kHold) {
-      uint32_t bytes;
-      unsigned char* at = piece_at(scol, &bytes);
       const int beg = sk < kCached ? sm.beg[sk] : gbeg[sk];
       const int cnt = sk < kCached ? sm.cnt[sk] : gcnt[sk];
       for (int i = 0; i < cnt; ++i)
-        bulk_s2g(at + (size_t)dst_of(beg + i) * p.stride, buf[slot], bytes);
+        bulk_s2g(su.at + (size_t)dst_of(beg + i) * p.stride, buf[slot], su.bytes);
       bulk_commit();
-      bulk_wait_read_all();  // the piece may be loaded over
-      if (ring) ++stores;
-      else held = false;
+      if (ring) {
+        // all pieces but those of the last kPending stores may be loaded over
+        asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
+        ++stores;
+      } else {
+        bulk_wait_read_all();
+        held = false;
+      }
     }
-    if (++sk == ops) {
-      sk = 0;
-      scol += step;
+    if (++sk == su.k1) {
+      ++sq;
+      sk = sm.unit[warp][sq % kUnits].k0;
     }
   }
   bulk_wait_all();
@@ -432,20 +560,11 @@ cudaError_t launch_moves(const gdn_pool* p, int layer, const BlockWork& bw, cuda
   mp.layers = layer < 0 ? p->num_layers : 1;
   mp.bw = bw;
   mp.err = error_word(p, layer);
-  const int sms = num_sms();
-  // columns: as wide as leaves every warp eight of them, down to 1 KiB
-  mp.piece = kPiece;
-  while (mp.piece > 1024 &&
-         (long long)mp.layers * (long long)((p->stride + mp.piece - 1) / mp.piece) < 8ll * sms * kWarps)
-    mp.piece /= 2;
-  mp.cols = (int)((p->stride + mp.piece - 1) / mp.piece);
-  const long long ctas = ((long long)mp.layers * mp.cols + kWarps - 1) / kWarps;
   cudaError_t e = cudaFuncSetAttribute(move_blocks_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)sizeof(MoveSmem));
   if (e != cudaSuccess) return e;
-  return launch_pdl(move_blocks_kernel, dim3((unsigned)(ctas < sms ? ctas : sms)),
-                    dim3(kWarps * 32), sizeof(MoveSmem), s, mp);
+  return launch_pdl(move_blocks_kernel, dim3(num_sms()), dim3(kWarps * 32), sizeof(MoveSmem), s, mp);
 }
 
 template <typename K, typename... Args>

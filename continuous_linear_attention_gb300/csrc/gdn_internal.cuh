@@ -55,12 +55,15 @@ struct WorkArea {
 };
 
 // Work area of the pool's block operations (gdn_blocks.cu), int32 words:
-//   [0]           number of moves
-//   [1 .. 15]     unused
+//   [0]           moves
+//   [1]           components: runs of moves that depend on each other only
+//   [2]           work counter of the moving kernel
+//   [3]           every move is a component (start[] is not written)
 //   then          src[2 * num_blocks]      per move, in order: its source block | kind << 30
 //                 beg[2 * num_blocks]      its first destination in dst[]
 //                 cnt[2 * num_blocks]      how many destinations it has
 //                 dst[num_blocks]          the destinations, grouped by move
+//                 start[num_blocks + 1]    first move of each component, and behind the last
 //                 tmp[6 * num_blocks]      the planning kernel's own arrays, where they
 //                                          do not fit into shared memory
 struct BlockWork {
@@ -71,8 +74,9 @@ struct BlockWork {
   __host__ __device__ int32_t* beg() const { return base + 16 + 2 * (size_t)num_blocks; }
   __host__ __device__ int32_t* cnt() const { return base + 16 + 4 * (size_t)num_blocks; }
   __host__ __device__ int32_t* dst() const { return base + 16 + 6 * (size_t)num_blocks; }
-  __host__ __device__ int32_t* tmp() const { return base + 16 + 7 * (size_t)num_blocks; }
-  static constexpr size_t words(int num_blocks) { return 16 + 13 * (size_t)num_blocks; }
+  __host__ __device__ int32_t* start() const { return base + 16 + 7 * (size_t)num_blocks; }
+  __host__ __device__ int32_t* tmp() const { return base + 17 + 8 * (size_t)num_blocks; }
+  static constexpr size_t words(int num_blocks) { return 17 + 14 * (size_t)num_blocks; }
 };
 
 // Everything a forward kernel needs, passed by value.
