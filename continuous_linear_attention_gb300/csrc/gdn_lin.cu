@@ -273,7 +273,7 @@ lin_recurrent_kernel(LinParams p) {
 // --- scheduler ---------------------------------------------------------------
 constexpr int kSchedThreads = 1024;
 
-constexpr int kSortMax = 4096;    // long sequences that are put in order
+constexpr int kSortMax = 2048;     // long sequences that are put in order
 constexpr int kSmemCounts = 4096;  // pools whose block-use counts fit into shared memory
 constexpr int kMinSegment = 8;  // chunks
 
@@ -284,7 +284,8 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms) {
   __shared__ unsigned s_flags;
   __shared__ int s_dec, s_pre, s_segs;
   __shared__ unsigned long long s_total;
-  __shared__ int32_t chunks[kSortMax], counts[kSmemCounts];
+  // the long sequences and their chunks, as found and in order
+  __shared__ int32_t found[kSortMax], chunks[kSortMax], in_order[kSortMax], counts[kSmemCounts];
   __shared__ int warp_sums[32];
   pdl_wait_then_release();
   const int tid = threadIdx.x, N = p.N, nb = p.num_blocks;
@@ -328,7 +329,10 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms) {
     } else {
       const int k = atomicAdd(&s_pre, 1), c = (len - 1) / kLinChunk + 1;
       pre_tmp[k] = s;
-      if (k < kSortMax) chunks[k] = c;
+      if (k < kSortMax) {
+        found[k] = s;
+        chunks[k] = c;
+      }
       atomicAdd(&s_total, (unsigned long long)c);
     }
   }
@@ -343,18 +347,19 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms) {
   const bool sorted = n_pre <= kSortMax;
   // longest first, ties by sequence (so that a call's order is always the same)
   for (int i = tid; i < n_pre; i += kSchedThreads) {
-    int rank = i;
     if (sorted) {
-      const int ci = chunks[i], si = pre_tmp[i];
-      rank = 0;
-      for (int j = 0; j < n_pre; ++j)
-        rank += chunks[j] > ci || (chunks[j] == ci && pre_tmp[j] < si);
+      const int ci = chunks[i], si = found[i];
+      int rank = 0;
+      for (int j = 0; j < n_pre; ++j) rank += chunks[j] > ci || (chunks[j] == ci && found[j] < si);
+      pre[rank] = si;
+      in_order[rank] = ci;
+    } else {
+      pre[i] = pre_tmp[i];
     }
-    pre[rank] = pre_tmp[i];
   }
   __syncthreads();
   auto chunks_of = [&](int k) {
-    return (p.cu[pre[k] + 1] - p.cu[pre[k]] - 1) / kLinChunk + 1;
+    return sorted ? in_order[k] : (p.cu[pre[k] + 1] - p.cu[pre[k]] - 1) / kLinChunk + 1;
   };
   // One SM works a chain off in order, so the call takes at least the longest
   // chain; its share of all chunks is what it takes at best.  Where the

@@ -67,15 +67,30 @@ constexpr int D = 128;
 constexpr int CH = kLinChunk;  // 128
 constexpr int kThreads = 768;  // O, V and S warps (8, 8, 4), then four single-thread warps
 constexpr int kOWarps = 8, kVWarps = 8, kSWarp = 16, kCtlWarp = 20;
-constexpr int kStages = 2;
 constexpr uint32_t TILE = 32768, BOX = 16384;  // a [128][128] bf16 tile: two 64-column boxes
-constexpr uint32_t ST_Q = 0, ST_K = TILE, ST_V = 2 * TILE, ST_BYTES = 3 * TILE;
-constexpr uint32_t OFF_S = kStages * ST_BYTES;  // S0 as B operand: [v][k], two 64-k blocks
+// stages of a chunk's q, k and v (three of k and v for the state pass), then
+// S0 as B operand: [v][k], two 64-k blocks
+constexpr int kMaxStages = 3;
+constexpr uint32_t OFF_S = 6 * TILE;
+// Stage of a role's current chunk and the parity of its pass over the stages.
+template <int kStages>
+struct Pos {
+  int b = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++b == kStages) {
+      b = 0;
+      ph ^= 1;
+    }
+  }
+};
 // tensor memory columns: P fp32 (bf16 over the first 32 of each 64), O, U, then the
 // four terms of 32 decayed v rows, twice: per 16 rows 8 columns of each term
 constexpr uint32_t TM_P = 0, TM_O = 128, TM_U = 256, TM_V = 384, TM_COLS = 512;
 constexpr int QT = 32;  // tokens per step of U
 constexpr int kTerms = 4;
+// the state pass has no P and O: two buffers for U and four for the decayed v
+constexpr uint32_t TM_U1 = 0, TM_V1 = 128;
 constexpr float kGentle = 32.f;  // largest 128 |g| whose e^{128 |g|} may stand in P
 
 enum Flag : int {
@@ -93,10 +108,10 @@ struct Desc {
 };
 
 struct Ctl {
-  Desc desc[kStages];
-  uint64_t full[kStages], empty[kStages], zeroed[kStages], staged[kStages];
+  Desc desc[kMaxStages];
+  uint64_t full[kMaxStages], empty[kMaxStages], zeroed[kMaxStages], staged[kMaxStages];
   uint64_t p_full, pb_full, qs_full, o_scaled, o_full[2], o_free, s_ready;
-  uint64_t v_full[2], v_free[2], u_full, u_free;
+  uint64_t v_full[4], v_free[4], u_full[2], u_free[2];
   uint32_t tmem;
 };
 constexpr uint32_t OFF_CTL = OFF_S + TILE;
@@ -246,6 +261,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
                  const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                  const __grid_constant__ CUtensorMap to) {
+  constexpr int kStages = kState ? 3 : 2;
+  constexpr uint32_t ST_Q = 0, ST_K = kState ? 0 : TILE, ST_V = ST_K + TILE, ST_BYTES = ST_V + TILE;
+  static_assert(kStages * ST_BYTES == OFF_S && kStages <= kMaxStages, "stages fill their room");
   extern __shared__ __align__(1024) unsigned char sm[];
   Ctl& ctl = *reinterpret_cast<Ctl*>(sm + OFF_CTL);
   pdl_wait_then_release();
@@ -266,8 +284,6 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       mbar_init(&ctl.empty[b], kVWarps + 4 + (kState ? 1 : 3));
       mbar_init(&ctl.zeroed[b], kVWarps);
       mbar_init(&ctl.staged[b], kOWarps);
-      mbar_init(&ctl.v_full[b], kVWarps);
-      mbar_init(&ctl.v_free[b], 1);
     }
     mbar_init(&ctl.p_full, 1);
     mbar_init(&ctl.pb_full, kOWarps);
@@ -277,8 +293,14 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
     mbar_init(&ctl.o_full[1], 1);
     mbar_init(&ctl.o_free, kOWarps);
     mbar_init(&ctl.s_ready, 4);
-    mbar_init(&ctl.u_full, 1);
-    mbar_init(&ctl.u_free, 4);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ctl.u_full[b], 1);
+      mbar_init(&ctl.u_free[b], 4);
+    }
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(&ctl.v_full[b], kVWarps);
+      mbar_init(&ctl.v_free[b], 1);
+    }
     fence_mbar_init();
   }
   if (warp == 0) tc::tmem_alloc(&ctl.tmem, TM_COLS);
@@ -287,6 +309,11 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
   tc::fence_after_sync();
   const uint32_t tmem = ctl.tmem;
   bool dead = false;
+  // buffers of U and of the decayed v: their number (a power of two, by its
+  // logarithm) and tensor memory columns
+  constexpr int kULog = kState ? 1 : 0, kVLog = kState ? 2 : 1;
+  auto u_col = [](int b) { return b == 0 ? TM_U : TM_U1; };
+  auto v_col = [](int b) { return (b < 2 ? TM_V : TM_V1) + (uint32_t)(b & 1) * (16 * kTerms); };
 
   // registers a thread, of 80 at launch: O 72, V 56, S 184, the others 40
   if (warp < kOWarps) {
@@ -301,10 +328,11 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
     float g = 0.f, after = 0.f;  // scale e^{g (i+1)}
     float col = 0.f;             // e^{g (31 - lane)}
     bool gentle = true;
-    for (int c = 0; !kState; ++c) {
-      const int b = c & 1;
+    Pos<kStages> pos;
+    for (int c = 0; !kState; ++c, pos.next()) {
+      const int b = pos.b;
       const uint32_t ph = (uint32_t)(c & 1);
-      if (!warp_wait(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
+      if (!warp_wait(&ctl.full[b], pos.ph)) { dead = true; break; }
       const Desc d = ctl.desc[b];
       if (d.flags & kEnd) break;
       if (d.h != h) {
@@ -424,9 +452,10 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
     // the weights' three bf16 terms of tokens 2 lane and 2 lane + 1 (wa), and
     // 64 more (wb)
     uint32_t wa[3] = {0, 0, 0}, wb[3] = {0, 0, 0};
-    for (int c = 0;; ++c) {
-      const int b = c & 1;
-      if (!warp_wait(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
+    Pos<kStages> pos;
+    for (int c = 0;; ++c, pos.next()) {
+      const int b = pos.b;
+      if (!warp_wait(&ctl.full[b], pos.ph)) { dead = true; break; }
       const Desc d = ctl.desc[b];
       if (d.flags & kEnd) break;
       unsigned char* kt = sm + b * ST_BYTES + ST_K;
@@ -466,9 +495,12 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       }
       const int nq = (d.n + QT - 1) / QT;
       for (int q = 0; q < nq; ++q) {
-        const int buf = steps & 1;
+        const int buf = steps & ((1 << kVLog) - 1);
         if (!(d.flags & kNoU)) {
-          if (steps >= 2 && !warp_wait(&ctl.v_free[buf], ((steps >> 1) - 1) & 1)) { dead = true; break; }
+          if ((steps >> kVLog) > 0 && !warp_wait(&ctl.v_free[buf], ((steps >> kVLog) - 1) & 1)) {
+            dead = true;
+            break;
+          }
           tc::fence_after_sync();
         }
         const int t0 = q * QT + 16 * half;
@@ -498,7 +530,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
           }
         }
         // the products' four terms, 16 elements v at a time
-        const uint32_t at = tmem + tl + TM_V + (buf * 2 + half) * (8 * kTerms);
+        const uint32_t at = tmem + tl + v_col(buf) + half * (8 * kTerms);
 #pragma unroll
         for (int v2 = 0; v2 < 2; ++v2) {
           uint32_t t[kTerms][4];
@@ -530,9 +562,10 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
     const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
     F2 S[D / 2];  // S[k][v], k = 2 i, 2 i + 1
     int ups = 0;  // updates so far
-    for (int c = 0;; ++c) {
-      const int b = c & 1;
-      if (!warp_wait(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
+    Pos<kStages> pos;
+    for (int c = 0;; ++c, pos.next()) {
+      const int b = pos.b;
+      if (!warp_wait(&ctl.full[b], pos.ph)) { dead = true; break; }
       const Desc d = ctl.desc[b];
       if (d.flags & kEnd) break;
       if (d.flags & kFirst) {
@@ -570,13 +603,14 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       if (!(d.flags & kNoU)) {
         const DecayPair a = decay_pair(finite_decay(p.log_decay[d.h]) * (float)d.n);
         const F2 ahi = f2(a.hi, a.hi), alo = f2(a.lo, a.lo);
-        if (!warp_wait(&ctl.u_full, ups & 1)) { dead = true; break; }
+        const int ub = ups & ((1 << kULog) - 1);
+        if (!warp_wait(&ctl.u_full[ub], (ups >> kULog) & 1)) { dead = true; break; }
         ++ups;
         tc::fence_after_sync();
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb) {
           float x[32];
-          tc::tmem_ld32(tmem + tl + TM_U + kb * 32, x);
+          tc::tmem_ld32(tmem + tl + u_col(ub) + kb * 32, x);
           tc::tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -585,7 +619,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
           }
         }
         tc::fence_before_sync();
-        warp_arrive(&ctl.u_free);
+        warp_arrive(&ctl.u_free[ub]);
       }
       if (d.flags & kLast) {
         float* dst = nullptr;
@@ -627,6 +661,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
     if (warp == kCtlWarp && lane == 0) {
       // ============================== producer ==============================
       int c = 0;
+      Pos<kStages> pos;
       for (bool end = false; !end && !dead;) {
         const int u = atomicAdd(&hdr[kState ? kLinStateHead : kLinHead], 1);
         end = u >= n_units;
@@ -653,9 +688,9 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
           if (kState && seg == nseg - 1) continue;
         }
         const int hk = h / p.group;
-        for (int k = c0; k < c1; ++k, ++c) {
-          const int b = c & 1;
-          if (c >= kStages && !wait_for(&ctl.empty[b], ((c >> 1) - 1) & 1)) {
+        for (int k = c0; k < c1; ++k, ++c, pos.next()) {
+          const int b = pos.b;
+          if (c >= kStages && !wait_for(&ctl.empty[b], pos.ph ^ 1)) {
             dead = true;
             break;
           }
@@ -689,7 +724,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       if (dead) {
         // the loads already issued land before the CTA ends
         for (int k = c > kStages ? c - kStages : 0; k < c; ++k)
-          wait_for(&ctl.full[k & 1], (k >> 1) & 1);
+          wait_for(&ctl.full[k % kStages], (uint32_t)(k / kStages) & 1);
       }
     } else if (warp == kCtlWarp + 1 && !kState) {
       // ============================== MMA 1 =================================
@@ -697,10 +732,11 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       constexpr uint32_t kIdMN = tc::idesc_bf16_f32(128, 64, false, true);
       const uint32_t s_lo = desc_k(sbase + OFF_S);
       const bool one = elect_one();
-      for (int c = 0;; ++c) {
-        const int b = c & 1;
+      Pos<kStages> pos;
+      for (int c = 0;; ++c, pos.next()) {
+        const int b = pos.b;
         const uint32_t ph = (uint32_t)(c & 1), st = sbase + b * ST_BYTES;
-        if (!warp_wait(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
+        if (!warp_wait(&ctl.full[b], pos.ph)) { dead = true; break; }
         if (ctl.desc[b].flags & kEnd) break;
         const uint32_t q_lo = desc_k(st + ST_Q), k_lo = desc_k(st + ST_K), v_lo = desc_mn(st + ST_V);
         // P = Q K^T, once the last chunk's P V has read P
@@ -727,7 +763,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         }
         __syncwarp();
         // O += P V (P's tokens 64 .. 127 are 64 columns on)
-        if (!warp_wait(&ctl.zeroed[b], (c >> 1) & 1) || !warp_wait(&ctl.pb_full, ph) ||
+        if (!warp_wait(&ctl.zeroed[b], pos.ph) || !warp_wait(&ctl.pb_full, ph) ||
             !warp_wait(&ctl.o_scaled, ph)) {
           dead = true;
           break;
@@ -751,27 +787,32 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       constexpr uint32_t kIdMN = tc::idesc_bf16_f32(128, 128, false, true);
       const bool one = elect_one();
       int steps = 0, ups = 0;
-      for (int c = 0; !dead; ++c) {
-        const int b = c & 1;
+      Pos<kStages> pos;
+      for (int c = 0; !dead; ++c, pos.next()) {
+        const int b = pos.b;
         const uint32_t k_lo = desc_mn(sbase + b * ST_BYTES + ST_K);
-        if (!warp_wait(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
+        if (!warp_wait(&ctl.full[b], pos.ph)) { dead = true; break; }
         const int flags = ctl.desc[b].flags, n = ctl.desc[b].n;
         if (flags & kEnd) break;
         if (flags & kNoU) {
           warp_arrive(&ctl.empty[b]);
           continue;
         }
-        if (ups > 0 && !warp_wait(&ctl.u_free, (ups - 1) & 1)) { dead = true; break; }
+        const int ub = ups & ((1 << kULog) - 1);
+        if ((ups >> kULog) > 0 && !warp_wait(&ctl.u_free[ub], ((ups >> kULog) - 1) & 1)) {
+          dead = true;
+          break;
+        }
         const int nq = (n + QT - 1) / QT;
         for (int q = 0; q < nq; ++q, ++steps) {
-          const int buf = steps & 1;
-          if (!warp_wait(&ctl.v_full[buf], (steps >> 1) & 1)) { dead = true; break; }
+          const int buf = steps & ((1 << kVLog) - 1);
+          if (!warp_wait(&ctl.v_full[buf], (steps >> kVLog) & 1)) { dead = true; break; }
           tc::fence_after_sync();
           // U (+)= the decayed v's terms times K over 32 tokens, the smallest first
           if (one) {
 #pragma unroll
             for (int k = 0; k < 2 * kTerms; ++k)
-              tc::mma_ts(tmem + TM_U, tmem + TM_V + ((buf * 2 + (k & 1)) * kTerms + kTerms - 1 - k / 2) * 8,
+              tc::mma_ts(tmem + u_col(ub), tmem + v_col(buf) + ((k & 1) * kTerms + kTerms - 1 - k / 2) * 8,
                          kDescHi | (k_lo + (2 * q + (k & 1)) * kStepMN), kIdMN, q > 0 || k > 0);
             tc::commit(&ctl.v_free[buf]);
           }
@@ -780,19 +821,20 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         if (dead) break;
         ++ups;
         if (one) {
-          tc::commit(&ctl.u_full);
+          tc::commit(&ctl.u_full[ub]);
           tc::commit(&ctl.empty[b]);
         }
         __syncwarp();
       }
     } else if (warp == kCtlWarp + 3 && lane == 0 && !kState) {
       // ============================== store =================================
-      for (int c = 0;; ++c) {
-        const int b = c & 1;
-        if (!wait_for(&ctl.full[b], (c >> 1) & 1)) { dead = true; break; }
+      Pos<kStages> pos;
+      for (int c = 0;; ++c, pos.next()) {
+        const int b = pos.b;
+        if (!wait_for(&ctl.full[b], pos.ph)) { dead = true; break; }
         const Desc d = ctl.desc[b];
         if (d.flags & kEnd) break;
-        if (!wait_for(&ctl.staged[b], (c >> 1) & 1)) { dead = true; break; }
+        if (!wait_for(&ctl.staged[b], pos.ph)) { dead = true; break; }
         if (d.n == CH) {
           const unsigned char* st = sm + b * ST_BYTES + ST_Q;
           tma_store_2d(&to, d.h * D, d.row, st);
