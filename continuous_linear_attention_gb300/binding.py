@@ -157,8 +157,14 @@ def _index(t) -> Optional[int]:
     return t.data_ptr()
 
 
+# torch.cuda.current_stream() builds a Stream object, half of a small call's host time
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -331,6 +337,7 @@ class LinPool(Pool):
                  memory: Optional[torch.Tensor] = None):
         self.dims = (num_blocks, num_layers, H, d)
         self.act = act_code(act)
+        self.dtype = torch.float32 if self.act == GDN_F32 else torch.bfloat16
         self.num_blocks, self.num_layers = num_blocks, num_layers
         self.memory = memory
         h = ctypes.c_void_p()
@@ -345,15 +352,16 @@ class LinPool(Pool):
         self.stride, self.conv_off, self.rec_off, self.base = s.value, c.value, r.value, b.value
 
 
-def _heads(t, name, d, act):
-    """(address, row pitch) of rows of heads [T][heads][d]: any row pitch, the
-    rows themselves dense."""
-    want = torch.float32 if act == GDN_F32 else torch.bfloat16
-    if t.dim() != 3 or t.shape[2] != d or t.dtype != want:
-        raise ValueError(f"{name} is [T][heads][{d}] of {want}: got {tuple(t.shape)} of {t.dtype}")
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d)):
+def _heads(t, name, heads, d, dtype, T):
+    """(address, row pitch) of at least T rows of heads [T][heads][d]: any row
+    pitch, the rows themselves dense."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or t.dtype != dtype or shape[0] < T:
+        raise ValueError(f"{name} is [>= {T}][{heads}][{d}] of {dtype}: got {tuple(shape)} of "
+                         f"{t.dtype}")
+    if shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != d)):
         raise ValueError(f"the rows of {name} have to be dense")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * d
+    return t.data_ptr(), stride[0] if shape[0] > 1 else heads * d
 
 
 def lin_varlen_forward(pool: LinPool, layer: int, q, k, v, cu_seqlens, state_block_idx, has_past,
@@ -361,17 +369,16 @@ def lin_varlen_forward(pool: LinPool, layer: int, q, k, v, cu_seqlens, state_blo
                        max_seqlen_hint: int = 0, stream=None) -> None:
     """gdn_lin_varlen_forward on device tensors: q and out [T][H][d], k and v
     [T][Hkv][d], each with any row pitch (views of a fused projection's rows)."""
-    H, d = pool.dims[2], pool.dims[3]
-    (pq, ldq), (pk, ldk), (pv, ldv), (po, ldo) = (
-        _heads(t, name, d, pool.act) for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out")))
-    if q.shape[1] != H or out.shape[1] != H or k.shape[1] != v.shape[1]:
-        raise ValueError(f"q and out have {H} heads, k and v the same number")
-    if any(t.shape[0] < T for t in (q, k, v, out)):
-        raise ValueError(f"q, k, v and out have at least {T} rows")
-    _check(load().gdn_lin_varlen_forward(pool.handle, layer, pq, pk, pv, ldq, ldk, ldv, k.shape[1],
+    H, d, dtype = pool.dims[2], pool.dims[3], pool.dtype
+    Hkv = k.shape[1]
+    pq, ldq = _heads(q, "q", H, d, dtype, T)
+    pk, ldk = _heads(k, "k", Hkv, d, dtype, T)
+    pv, ldv = _heads(v, "v", Hkv, d, dtype, T)
+    po, ldo = _heads(out, "out", H, d, dtype, T)
+    _check(load().gdn_lin_varlen_forward(pool.handle, layer, pq, pk, pv, ldq, ldk, ldv, Hkv,
                                          _ptr(cu_seqlens), _ptr(state_block_idx), _ptr(has_past),
-                                         _ptr(log_decay), float(scale), po, ldo, T, N,
-                                         max_seqlen_hint, _stream(stream)),
+                                         _ptr(log_decay), scale, po, ldo, T, N, max_seqlen_hint,
+                                         _stream(stream)),
            "gdn_lin_varlen_forward")
 
 

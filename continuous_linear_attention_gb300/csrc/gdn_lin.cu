@@ -15,6 +15,7 @@
 #include <cuda_runtime.h>
 
 #include <new>
+#include <type_traits>
 
 #include "gdn_cta.cuh"
 #include "gdn_lin.cuh"
@@ -80,17 +81,22 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kOne>
 struct RecSmem {
   T q[2][kTile][D], k[2][kTile][D], v[2][kTile][kSlice];
   float part[kTile][kRecThreads / 32][kSlice];
 };
+template <typename T, int D>
+struct RecSmem<T, D, true> {
+  float part[1][kRecThreads / 32][kSlice];
+};
 
 // Sequence s, head h, columns 32 slice ..: read, advanced by all its tokens
-// and written back.  check: nothing has looked at the batch yet.
-template <typename T, int D>
-__device__ __forceinline__ void recurrent_unit(const LinParams& p, RecSmem<T, D>& sm, int s, int h,
-                                               int slice, bool check) {
+// and written back.  check: nothing has looked at the batch yet.  kOne: no
+// sequence has more than one token (p.hint is 1).
+template <typename T, int D, bool kOne>
+__device__ __forceinline__ void recurrent_unit(const LinParams& p, RecSmem<T, D, kOne>& sm, int s,
+                                               int h, int slice, bool check) {
   constexpr int kRows = D / kRowT;      // state rows per thread
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int32_t* hdr = p.work.header();
@@ -135,6 +141,10 @@ __device__ __forceinline__ void recurrent_unit(const LinParams& p, RecSmem<T, D>
       o.z = fmaf(qr[i], t.z, o.z);
       o.w = fmaf(qr[i], t.w, o.w);
     }
+    return o;
+  };
+  // the sum over the warp's row groups
+  auto across = [](float4 o) {
 #pragma unroll
     for (int w = kColT; w < 32; w <<= 1) {
       o.x += __shfl_xor_sync(0xffffffffu, o.x, w);
@@ -144,11 +154,37 @@ __device__ __forceinline__ void recurrent_unit(const LinParams& p, RecSmem<T, D>
     }
     return o;
   };
+  // a single token's q, k and v; with kOne before the checks, else (where they
+  // would take registers from the longer sequences) behind them
   float q0[kRows], k0[kRows], v0[4];
-  if (active && len == 1) {
-    Vec<T, kRows>::load(q + r0, q0);
-    Vec<T, kRows>::load(k + r0, k0);
-    Vec<T, 4>::load(v + (tid % kColT) * 4, v0);
+  auto load_one = [&]() {
+    if (active && len == 1) {
+      Vec<T, kRows>::load(q + r0, q0);
+      Vec<T, kRows>::load(k + r0, k0);
+      Vec<T, 4>::load(v + (tid % kColT) * 4, v0);
+    }
+  };
+  if constexpr (kOne) load_one();
+  // stages tile t0 .. of the tokens in buffer b
+  [[maybe_unused]] auto stage = [&](int t0, int b) {
+    if constexpr (!kOne) {
+      const int n = min(kTile, len - t0);
+      constexpr int kRow16 = D * (int)sizeof(T) / 16, kSl16 = kSlice * (int)sizeof(T) / 16;
+      constexpr int kPer = 16 / (int)sizeof(T);
+      for (int i = tid; i < n * kRow16; i += kRecThreads) {
+        const int t = i / kRow16, c = (i % kRow16) * kPer;
+        cp_async16(&sm.q[b][t][c], q + (size_t)(t0 + t) * p.ldq + c);
+        cp_async16(&sm.k[b][t][c], k + (size_t)(t0 + t) * p.ldk + c);
+      }
+      for (int i = tid; i < n * kSl16; i += kRecThreads) {
+        const int t = i / kSl16, c = (i % kSl16) * kPer;
+        cp_async16(&sm.v[b][t][c], v + (size_t)(t0 + t) * p.ldv + c);
+      }
+      cp_async_commit();
+    }
+  };
+  if constexpr (!kOne) {
+    if (active && len > 1) stage(0, 0);
   }
   if (check) {
     // the batch: cu_seqlens from 0 to T and never falling, no block named
@@ -174,8 +210,9 @@ __device__ __forceinline__ void recurrent_unit(const LinParams& p, RecSmem<T, D>
     if (flags && tid == 0 && h == 0 && slice == 0) atomicOr((unsigned*)&hdr[kErr], flags);
     if (flags) active = false;
   }
+  if constexpr (!kOne) load_one();
   if (active && len == 1) {
-    const float4 o = token(q0, k0, v0);
+    const float4 o = across(token(q0, k0, v0));
 #pragma unroll
     for (int i = 0; i < kRows; ++i) *reinterpret_cast<float4*>(S_g + (size_t)i * D) = S[i];
     if (lane < kColT) *reinterpret_cast<float4*>(&sm.part[0][warp][lane * 4]) = o;
@@ -186,24 +223,9 @@ __device__ __forceinline__ void recurrent_unit(const LinParams& p, RecSmem<T, D>
       for (int w = 0; w < kRecThreads / 32; ++w) acc += sm.part[0][w][tid];
       out[tid] = from_f32<T>(acc * p.scale);
     }
-  } else if (active) {
+  } else if constexpr (!kOne) if (active) {
     // tokens in tiles, staged one tile ahead
-    auto stage = [&](int t0, int b) {
-      const int n = min(kTile, len - t0);
-      constexpr int kRow16 = D * (int)sizeof(T) / 16, kSl16 = kSlice * (int)sizeof(T) / 16;
-      constexpr int kPer = 16 / (int)sizeof(T);
-      for (int i = tid; i < n * kRow16; i += kRecThreads) {
-        const int t = i / kRow16, c = (i % kRow16) * kPer;
-        cp_async16(&sm.q[b][t][c], q + (size_t)(t0 + t) * p.ldq + c);
-        cp_async16(&sm.k[b][t][c], k + (size_t)(t0 + t) * p.ldk + c);
-      }
-      for (int i = tid; i < n * kSl16; i += kRecThreads) {
-        const int t = i / kSl16, c = (i % kSl16) * kPer;
-        cp_async16(&sm.v[b][t][c], v + (size_t)(t0 + t) * p.ldv + c);
-      }
-      cp_async_commit();
-    };
-    stage(0, 0);
+    constexpr int kBatch = D == 128 ? 2 : 4;
     for (int t0 = 0, b = 0; t0 < len; t0 += kTile, b ^= 1) {
       if (t0 + kTile < len) {
         stage(t0 + kTile, b ^ 1);
@@ -213,14 +235,30 @@ __device__ __forceinline__ void recurrent_unit(const LinParams& p, RecSmem<T, D>
       }
       __syncthreads();  // the tile has landed, and the last one's sums are read
       const int n = min(kTile, len - t0);
-      for (int t = 0; t < n; ++t) {
-        float qr[kRows], kr[kRows], vc[4];
-        Vec<T, kRows>::load(&sm.q[b][t][r0], qr);
-        Vec<T, kRows>::load(&sm.k[b][t][r0], kr);
-        Vec<T, 4>::load(&sm.v[b][t][(tid % kColT) * 4], vc);
-        const float4 o = token(qr, kr, vc);
-        if (lane < kColT) *reinterpret_cast<float4*>(&sm.part[t][warp][lane * 4]) = o;
-      }
+      // kN tokens: their reads come first and their sums run side by side
+      auto batch = [&](int t, auto count) {
+        constexpr int kN = decltype(count)::value;
+        float qr[kN][kRows], kr[kN][kRows], vc[kN][4];
+#pragma unroll
+        for (int u = 0; u < kN; ++u) {
+          Vec<T, kRows>::load(&sm.q[b][t + u][r0], qr[u]);
+          Vec<T, kRows>::load(&sm.k[b][t + u][r0], kr[u]);
+          Vec<T, 4>::load(&sm.v[b][t + u][(tid % kColT) * 4], vc[u]);
+        }
+        float4 o[kN];
+#pragma unroll
+        for (int u = 0; u < kN; ++u) o[u] = token(qr[u], kr[u], vc[u]);
+#pragma unroll
+        for (int u = 0; u < kN; ++u) o[u] = across(o[u]);
+        if (lane < kColT) {
+#pragma unroll
+          for (int u = 0; u < kN; ++u)
+            *reinterpret_cast<float4*>(&sm.part[t + u][warp][lane * 4]) = o[u];
+        }
+      };
+      int t = 0;
+      for (; t + kBatch <= n; t += kBatch) batch(t, std::integral_constant<int, kBatch>());
+      for (; t < n; ++t) batch(t, std::integral_constant<int, 1>());
       __syncthreads();  // the tile's sums are there, and its buffer may be staged over
       for (int i = tid; i < n * kSlice; i += kRecThreads) {
         const int t = i / kSlice, c = i % kSlice;
@@ -235,11 +273,16 @@ __device__ __forceinline__ void recurrent_unit(const LinParams& p, RecSmem<T, D>
   }
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kRecThreads)
+// CTAs per SM that the registers leave room for: as many state reads in flight.
+constexpr int rec_ctas(int D, bool one) {
+  return one ? (D == 128 ? 7 : 8) : D == 32 ? 6 : 5;
+}
+
+template <typename T, int D, bool kOne>
+__global__ void __launch_bounds__(kRecThreads, rec_ctas(D, kOne))
 lin_recurrent_kernel(LinParams p) {
   constexpr int kSlices = D / kSlice;
-  __shared__ __align__(16) RecSmem<T, D> sm;
+  __shared__ __align__(16) RecSmem<T, D, kOne> sm;
   // late: launched behind the chunk kernel, whose idle SMs it takes without
   // waiting for it (other sequences, other blocks); before it ends it waits,
   // and computes what the chunk kernel has marked: columns whose blocks still
@@ -254,7 +297,7 @@ lin_recurrent_kernel(LinParams p) {
   const bool here = !p.listed || s < p.work.header()[kNDec];
   if (here) {
     if (p.listed) s = p.work.dec()[s];
-    recurrent_unit<T, D>(p, sm, s, h, slice, !p.listed);
+    recurrent_unit<T, D, kOne>(p, sm, s, h, slice, !p.listed);
   }
   if (!p.late) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -265,7 +308,7 @@ lin_recurrent_kernel(LinParams p) {
     if (!p.bad[u]) continue;
     const long long chain = u / kSlices;
     __syncthreads();
-    recurrent_unit<T, D>(p, sm, p.work.pre()[chain / p.H], (int)(chain % p.H), (int)(u % kSlices),
+    recurrent_unit<T, D, kOne>(p, sm, p.work.pre()[chain / p.H], (int)(chain % p.H), (int)(u % kSlices),
                          false);
   }
 }
@@ -410,7 +453,8 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms) {
 template <typename T, int D>
 cudaError_t launch_rec(const LinParams& p, int max_items, cudaStream_t s) {
   const long long ctas = (long long)max_items * p.H * (D / kSlice);
-  return launch_pdl(lin_recurrent_kernel<T, D>, dim3((unsigned)ctas), dim3(kRecThreads), 0, s, p);
+  auto kern = p.hint == 1 ? lin_recurrent_kernel<T, D, true> : lin_recurrent_kernel<T, D, false>;
+  return launch_pdl(kern, dim3((unsigned)ctas), dim3(kRecThreads), 0, s, p);
 }
 
 }  // namespace
