@@ -616,9 +616,11 @@ int gdn_lin_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
   cudaStream_t s = (cudaStream_t)stream;
   const int sms = gdn::num_sms();
   // prompts in the chunked form, where it has a kernel and the call room for one
-  int max_long = T / (gdn::kLinShort + 1);
+  const int short_max = (long long)N * H * gdn::kLinSlices <= 5ll * sms ? gdn::kLinShortFew
+                                                                       : gdn::kLinShort;
+  int max_long = T / (short_max + 1);
   if (max_long > max_items) max_long = max_items;
-  if (max_seqlen_hint > 0 && max_seqlen_hint <= gdn::kLinShort) max_long = 0;
+  if (max_seqlen_hint > 0 && max_seqlen_hint <= short_max) max_long = 0;
   const bool chunked = max_long > 0 && gdn::lin_chunk_supported(d, p->act);
   p->last_path = chunked                             ? GDN_PREFILL_FUSED
                  : T > 1 && max_seqlen_hint != 1 ? GDN_PREFILL_SERIAL
@@ -636,8 +638,7 @@ int gdn_lin_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
   }
   lp.listed = chunked || N > gdn::kSelfCheck;
   lp.late = chunked;
-  if (lp.listed && gdn::launch_lin_schedule(lp, chunked ? gdn::kLinShort : INT32_MAX, sms, s) !=
-                       cudaSuccess)
+  if (lp.listed && gdn::launch_lin_schedule(lp, chunked ? short_max : INT32_MAX, sms, s) != cudaSuccess)
     return GDN_ERR_CUDA;
   if (p->ev_before && cudaEventRecord(p->ev_before, s) != cudaSuccess) return GDN_ERR_CUDA;
   if (chunked && gdn::launch_lin_chunk(lp, may_split, sms, s) != cudaSuccess) return GDN_ERR_CUDA;

@@ -7,8 +7,12 @@ namespace gdn {
 
 constexpr int kLinChunk = 128;  // tokens per chunk of the chunked form
 constexpr int kLinSlices = 4;   // parts of 32 columns of a head's state (d = 128)
-// Sequences of up to this many tokens take the recurrent form.
-constexpr int kLinShort = 16;
+// Sequences of up to this many tokens take the recurrent form.  64 sequences of
+// 32 heads: 76 us of 8 tokens (chunked form 101), 119 us of 16 (103).  Where
+// all its CTAs run at once the recurrent form is ahead for longer: one sequence
+// of 16 heads 10 us of 24 tokens (chunked 16), 14 us of 64 (16), and eight of
+// them 17 us of 24 (17), 39 us of 64 (17).
+constexpr int kLinShort = 12, kLinShortFew = 32;
 
 // Header words of a layer's work area in these forwards (besides kErr, kNDec
 // and kNPre): the segments of the long sequences, longest first.
