@@ -35,37 +35,28 @@ constexpr int kTile = 16;                           // tokens staged at a time
 // state loads are in flight, which saves the scheduler's launch
 constexpr int kSelfCheck = 512;
 
-// kN consecutive elements as fp32 (kN * sizeof(T) aligned).
-template <typename T, int kN> struct Vec;
-template <int kN> struct Vec<float, kN> {
-  static __device__ __forceinline__ void load(const float* p, float* o) {
-    if constexpr (kN % 4 == 0) {
+// kN consecutive elements (kN * sizeof(T) aligned): as they lie, and as fp32.
+template <typename T, int kN>
+struct Vec {
+  static constexpr int kWords = kN * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kWords % 4 == 0) {
 #pragma unroll
-      for (int i = 0; i < kN; i += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p + i);
-        o[i] = v.x; o[i + 1] = v.y; o[i + 2] = v.z; o[i + 3] = v.w;
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+        w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
       }
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(p);
-      o[0] = v.x; o[1] = v.y;
-    }
-  }
-};
-template <int kN> struct Vec<__nv_bfloat16, kN> {
-  static __device__ __forceinline__ void unpack(uint32_t w, float* o) {
-    o[0] = __uint_as_float(w << 16);
-    o[1] = __uint_as_float(w & 0xffff0000u);
-  }
-  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* o) {
-    if constexpr (kN == 8) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      unpack(v.x, o); unpack(v.y, o + 2); unpack(v.z, o + 4); unpack(v.w, o + 6);
-    } else if constexpr (kN == 4) {
+    } else if constexpr (kWords == 2) {
       const uint2 v = *reinterpret_cast<const uint2*>(p);
-      unpack(v.x, o); unpack(v.y, o + 2);
+      w[0] = v.x; w[1] = v.y;
     } else {
-      unpack(*reinterpret_cast<const uint32_t*>(p), o);
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
     }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
   }
 };
 
@@ -91,55 +82,49 @@ struct RecSmem<T, D, true> {
   float part[1][kRecThreads / 32][kSlice];
 };
 
-// Sequence s, head h, columns 32 slice ..: read, advanced by all its tokens
-// and written back.  check: nothing has looked at the batch yet.  kOne: no
-// sequence has more than one token (p.hint is 1).
-template <typename T, int D, bool kOne>
-__device__ __forceinline__ void recurrent_unit(const LinParams& p, RecSmem<T, D, kOne>& sm, int s,
-                                               int h, int slice, bool check) {
+// Columns 32 slice .. of head h over len tokens from row row0: the state is
+// read from src (unless zero: it starts at zeros), advanced and written to dst
+// (nullptr: not), both the head's [D][D].  ok() is asked once all reads are on their way, and
+// nothing is written where it says no.  kOne: len is at most 1.  kState: the
+// state only, no outputs.
+template <typename T, int D, bool kOne, bool kState, typename Ok>
+__device__ __forceinline__ void recurrent_body(const LinParams& p, RecSmem<T, D, kOne>& sm,
+                                               int row0, int len, int h, int slice,
+                                               bool zero, const float* src, float* dst, Ok ok) {
   constexpr int kRows = D / kRowT;      // state rows per thread
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int32_t* hdr = p.work.header();
-  const int row0 = p.cu[s], len = p.cu[s + 1] - row0;
-  const int blk = p.blk[s];
-  // loads may be issued for what looks right here; nothing is written before
-  // the whole batch has been checked
-  bool active = len > 0 && blk > 0 && blk < p.num_blocks;
-  if (check)
-    active = active && row0 >= 0 && len <= p.T && row0 <= p.T - len && (p.hint == 0 || len <= p.hint);
   const int c0 = slice * kSlice + (tid % kColT) * 4;  // this thread's columns
   const int r0 = (tid / kColT) * kRows;               // and rows
-  float* S_g = reinterpret_cast<float*>(p.layer_base + (size_t)(active ? blk : 0) * p.stride) +
-               ((size_t)h * D + r0) * D + c0;
+  const size_t at = (size_t)r0 * D + c0;
   float4 S[kRows];
-  const bool past = active && p.has_past[s];
 #pragma unroll
   for (int i = 0; i < kRows; ++i)
-    S[i] = past ? *reinterpret_cast<const float4*>(S_g + (size_t)i * D) : make_float4(0.f, 0.f, 0.f, 0.f);
+    S[i] = zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                : *reinterpret_cast<const float4*>(src + at + (size_t)i * D);
   const DecayPair a = decay_pair(finite_decay(p.log_decay[h]));
   const int hk = h / p.group;
-  const T* q = static_cast<const T*>(p.q) + (size_t)(active ? row0 : 0) * p.ldq + (size_t)h * D;
-  const T* k = static_cast<const T*>(p.k) + (size_t)(active ? row0 : 0) * p.ldk + (size_t)hk * D;
-  const T* v = static_cast<const T*>(p.v) + (size_t)(active ? row0 : 0) * p.ldv + (size_t)hk * D +
+  const T* q = static_cast<const T*>(p.q) + (size_t)row0 * p.ldq + (size_t)h * D;
+  const T* k = static_cast<const T*>(p.k) + (size_t)row0 * p.ldk + (size_t)hk * D;
+  const T* v = static_cast<const T*>(p.v) + (size_t)row0 * p.ldv + (size_t)hk * D +
                slice * kSlice;
-  T* out = static_cast<T*>(p.out) + (size_t)(active ? row0 : 0) * p.ldo + (size_t)h * D +
-           slice * kSlice;
-
   // one token: S <- e^g S + k v^T, and this thread's part of S^T q
-  auto token = [&](const float* qr, const float* kr, const float* vc) {
+  auto token = [&](const Vec<T, kRows>& qr, const Vec<T, kRows>& kr, const Vec<T, 4>& vc) {
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
+      const float ki = kr.at(i);
       float4 t = S[i];
-      t.x = fmaf(a.hi, t.x, fmaf(a.lo, t.x, kr[i] * vc[0]));
-      t.y = fmaf(a.hi, t.y, fmaf(a.lo, t.y, kr[i] * vc[1]));
-      t.z = fmaf(a.hi, t.z, fmaf(a.lo, t.z, kr[i] * vc[2]));
-      t.w = fmaf(a.hi, t.w, fmaf(a.lo, t.w, kr[i] * vc[3]));
+      t.x = fmaf(a.hi, t.x, fmaf(a.lo, t.x, ki * vc.at(0)));
+      t.y = fmaf(a.hi, t.y, fmaf(a.lo, t.y, ki * vc.at(1)));
+      t.z = fmaf(a.hi, t.z, fmaf(a.lo, t.z, ki * vc.at(2)));
+      t.w = fmaf(a.hi, t.w, fmaf(a.lo, t.w, ki * vc.at(3)));
       S[i] = t;
-      o.x = fmaf(qr[i], t.x, o.x);
-      o.y = fmaf(qr[i], t.y, o.y);
-      o.z = fmaf(qr[i], t.z, o.z);
-      o.w = fmaf(qr[i], t.w, o.w);
+      if constexpr (!kState) {
+        o.x = fmaf(qr.at(i), t.x, o.x);
+        o.y = fmaf(qr.at(i), t.y, o.y);
+        o.z = fmaf(qr.at(i), t.z, o.z);
+        o.w = fmaf(qr.at(i), t.w, o.w);
+      }
     }
     return o;
   };
@@ -156,12 +141,13 @@ __device__ __forceinline__ void recurrent_unit(const LinParams& p, RecSmem<T, D,
   };
   // a single token's q, k and v; with kOne before the checks, else (where they
   // would take registers from the longer sequences) behind them
-  float q0[kRows], k0[kRows], v0[4];
+  Vec<T, kRows> q0, k0;
+  Vec<T, 4> v0;
   auto load_one = [&]() {
-    if (active && len == 1) {
-      Vec<T, kRows>::load(q + r0, q0);
-      Vec<T, kRows>::load(k + r0, k0);
-      Vec<T, 4>::load(v + (tid % kColT) * 4, v0);
+    if (len == 1) {
+      if constexpr (!kState) q0.load(q + r0);
+      k0.load(k + r0);
+      v0.load(v + (tid % kColT) * 4);
     }
   };
   if constexpr (kOne) load_one();
@@ -173,7 +159,7 @@ __device__ __forceinline__ void recurrent_unit(const LinParams& p, RecSmem<T, D,
       constexpr int kPer = 16 / (int)sizeof(T);
       for (int i = tid; i < n * kRow16; i += kRecThreads) {
         const int t = i / kRow16, c = (i % kRow16) * kPer;
-        cp_async16(&sm.q[b][t][c], q + (size_t)(t0 + t) * p.ldq + c);
+        if constexpr (!kState) cp_async16(&sm.q[b][t][c], q + (size_t)(t0 + t) * p.ldq + c);
         cp_async16(&sm.k[b][t][c], k + (size_t)(t0 + t) * p.ldk + c);
       }
       for (int i = tid; i < n * kSl16; i += kRecThreads) {
@@ -184,12 +170,106 @@ __device__ __forceinline__ void recurrent_unit(const LinParams& p, RecSmem<T, D,
     }
   };
   if constexpr (!kOne) {
-    if (active && len > 1) stage(0, 0);
+    if (len > 1) stage(0, 0);
   }
-  if (check) {
+  const bool active = ok();
+  [[maybe_unused]] T* out =
+      static_cast<T*>(p.out) + (size_t)row0 * p.ldo + (size_t)h * D + slice * kSlice;
+  if constexpr (!kOne) load_one();
+  auto store = [&]() {
+    if (!dst) return;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) *reinterpret_cast<float4*>(dst + at + (size_t)i * D) = S[i];
+  };
+  if (active && len == 1) {
+    const float4 mine = token(q0, k0, v0);
+    store();
+    if constexpr (!kState) {
+      const float4 o = across(mine);
+      if (lane < kColT) *reinterpret_cast<float4*>(&sm.part[0][warp][lane * 4]) = o;
+      __syncthreads();
+      if (tid < kSlice) {
+        float acc = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRecThreads / 32; ++w) acc += sm.part[0][w][tid];
+        out[tid] = from_f32<T>(acc * p.scale);
+      }
+    }
+  } else if constexpr (!kOne) if (active && len > 1) {
+    // tokens in tiles, staged one tile ahead
+    constexpr int kBatch = D == 128 ? 2 : 4;
+    for (int t0 = 0, b = 0; t0 < len; t0 += kTile, b ^= 1) {
+      if (t0 + kTile < len) {
+        stage(t0 + kTile, b ^ 1);
+        cp_async_wait<1>();
+      } else {
+        cp_async_wait<0>();
+      }
+      __syncthreads();  // the tile has landed, and the last one's sums are read
+      const int n = min(kTile, len - t0);
+      // kN tokens: their reads come first and their sums run side by side
+      auto batch = [&](int t, auto count) {
+        constexpr int kN = decltype(count)::value;
+        Vec<T, kRows> qr[kN], kr[kN];
+        Vec<T, 4> vc[kN];
+#pragma unroll
+        for (int u = 0; u < kN; ++u) {
+          if constexpr (!kState) qr[u].load(&sm.q[b][t + u][r0]);
+          kr[u].load(&sm.k[b][t + u][r0]);
+          vc[u].load(&sm.v[b][t + u][(tid % kColT) * 4]);
+        }
+        float4 o[kN];
+#pragma unroll
+        for (int u = 0; u < kN; ++u) o[u] = token(qr[u], kr[u], vc[u]);
+        if constexpr (!kState) {
+#pragma unroll
+          for (int u = 0; u < kN; ++u) o[u] = across(o[u]);
+          if (lane < kColT) {
+#pragma unroll
+            for (int u = 0; u < kN; ++u)
+              *reinterpret_cast<float4*>(&sm.part[t + u][warp][lane * 4]) = o[u];
+          }
+        }
+      };
+      int t = 0;
+      for (; t + kBatch <= n; t += kBatch) batch(t, std::integral_constant<int, kBatch>());
+      for (; t < n; ++t) batch(t, std::integral_constant<int, 1>());
+      __syncthreads();  // the tile's sums are there, and its buffer may be staged over
+      if constexpr (!kState) {
+        for (int i = tid; i < n * kSlice; i += kRecThreads) {
+          const int t = i / kSlice, c = i % kSlice;
+          float acc = 0.f;
+#pragma unroll
+          for (int w = 0; w < kRecThreads / 32; ++w) acc += sm.part[t][w][c];
+          out[(size_t)(t0 + t) * p.ldo + c] = from_f32<T>(acc * p.scale);
+        }
+      }
+    }
+    store();
+  }
+}
+
+// Sequence s, head h, columns 32 slice ..: its block's state advanced by all
+// its tokens.  check: nothing has looked at the batch yet.
+template <typename T, int D, bool kOne>
+__device__ __forceinline__ void recurrent_unit(const LinParams& p, RecSmem<T, D, kOne>& sm, int s,
+                                               int h, int slice, bool check) {
+  const int tid = threadIdx.x;
+  const int row0 = p.cu[s], len = p.cu[s + 1] - row0;
+  const int blk = p.blk[s];
+  // reads may be issued for what looks right here
+  bool active = len > 0 && blk > 0 && blk < p.num_blocks;
+  if (check)
+    active = active && row0 >= 0 && len <= p.T && row0 <= p.T - len && (p.hint == 0 || len <= p.hint);
+  float* state = active ? reinterpret_cast<float*>(p.layer_base + (size_t)blk * p.stride) +
+                              (size_t)h * D * D
+                        : nullptr;
+  auto ok = [&]() {
+    if (!check) return active;
     // the batch: cu_seqlens from 0 to T and never falling, no block named
     // twice by sequences with tokens
     int bad = 0, twice = 0;
+#pragma unroll 1
     for (int i = tid; i < p.N; i += kRecThreads) {
       const int lo = p.cu[i], hi = p.cu[i + 1];
       bad |= hi < lo;
@@ -207,75 +287,16 @@ __device__ __forceinline__ void recurrent_unit(const LinParams& p, RecSmem<T, D,
       else if (twice) flags = GDN_FLAG_DUPLICATE;
       else if (p.hint > 0 && len > p.hint) flags = GDN_FLAG_HINT;
     }
-    if (flags && tid == 0 && h == 0 && slice == 0) atomicOr((unsigned*)&hdr[kErr], flags);
-    if (flags) active = false;
-  }
-  if constexpr (!kOne) load_one();
-  if (active && len == 1) {
-    const float4 o = across(token(q0, k0, v0));
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) *reinterpret_cast<float4*>(S_g + (size_t)i * D) = S[i];
-    if (lane < kColT) *reinterpret_cast<float4*>(&sm.part[0][warp][lane * 4]) = o;
-    __syncthreads();
-    if (tid < kSlice) {
-      float acc = 0.f;
-#pragma unroll
-      for (int w = 0; w < kRecThreads / 32; ++w) acc += sm.part[0][w][tid];
-      out[tid] = from_f32<T>(acc * p.scale);
-    }
-  } else if constexpr (!kOne) if (active) {
-    // tokens in tiles, staged one tile ahead
-    constexpr int kBatch = D == 128 ? 2 : 4;
-    for (int t0 = 0, b = 0; t0 < len; t0 += kTile, b ^= 1) {
-      if (t0 + kTile < len) {
-        stage(t0 + kTile, b ^ 1);
-        cp_async_wait<1>();
-      } else {
-        cp_async_wait<0>();
-      }
-      __syncthreads();  // the tile has landed, and the last one's sums are read
-      const int n = min(kTile, len - t0);
-      // kN tokens: their reads come first and their sums run side by side
-      auto batch = [&](int t, auto count) {
-        constexpr int kN = decltype(count)::value;
-        float qr[kN][kRows], kr[kN][kRows], vc[kN][4];
-#pragma unroll
-        for (int u = 0; u < kN; ++u) {
-          Vec<T, kRows>::load(&sm.q[b][t + u][r0], qr[u]);
-          Vec<T, kRows>::load(&sm.k[b][t + u][r0], kr[u]);
-          Vec<T, 4>::load(&sm.v[b][t + u][(tid % kColT) * 4], vc[u]);
-        }
-        float4 o[kN];
-#pragma unroll
-        for (int u = 0; u < kN; ++u) o[u] = token(qr[u], kr[u], vc[u]);
-#pragma unroll
-        for (int u = 0; u < kN; ++u) o[u] = across(o[u]);
-        if (lane < kColT) {
-#pragma unroll
-          for (int u = 0; u < kN; ++u)
-            *reinterpret_cast<float4*>(&sm.part[t + u][warp][lane * 4]) = o[u];
-        }
-      };
-      int t = 0;
-      for (; t + kBatch <= n; t += kBatch) batch(t, std::integral_constant<int, kBatch>());
-      for (; t < n; ++t) batch(t, std::integral_constant<int, 1>());
-      __syncthreads();  // the tile's sums are there, and its buffer may be staged over
-      for (int i = tid; i < n * kSlice; i += kRecThreads) {
-        const int t = i / kSlice, c = i % kSlice;
-        float acc = 0.f;
-#pragma unroll
-        for (int w = 0; w < kRecThreads / 32; ++w) acc += sm.part[t][w][c];
-        out[(size_t)(t0 + t) * p.ldo + c] = from_f32<T>(acc * p.scale);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) *reinterpret_cast<float4*>(S_g + (size_t)i * D) = S[i];
-  }
+    if (flags && tid == 0 && h == 0 && slice == 0) atomicOr((unsigned*)&p.work.header()[kErr], flags);
+    return active && !flags;
+  };
+  recurrent_body<T, D, kOne, false>(p, sm, active ? row0 : 0, active ? len : 0, h, slice,
+                                    !active || !p.has_past[s], state, state, ok);
 }
 
 // CTAs per SM that the registers leave room for: as many state reads in flight.
 constexpr int rec_ctas(int D, bool one) {
-  return one ? (D == 128 ? 7 : 8) : D == 32 ? 6 : 5;
+  return one ? (D == 128 ? 6 : 8) : D == 32 ? 6 : 5;
 }
 
 template <typename T, int D, bool kOne>
@@ -299,17 +320,101 @@ lin_recurrent_kernel(LinParams p) {
     if (p.listed) s = p.work.dec()[s];
     recurrent_unit<T, D, kOne>(p, sm, s, h, slice, !p.listed);
   }
-  if (!p.late) return;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int32_t* hdr = p.work.header();
-  if (!hdr[kLinBad]) return;
-  const long long n = (long long)hdr[kNPre] * p.H * kSlices;
-  for (long long u = blockIdx.x; u < n; u += gridDim.x) {
-    if (!p.bad[u]) continue;
-    const long long chain = u / kSlices;
+  if constexpr (!kOne) {
+    if (!p.late) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int32_t* hdr = p.work.header();
+    if (!hdr[kLinBad]) return;
+    const long long n = (long long)hdr[kNPre] * p.H * kSlices;
+    for (long long u = blockIdx.x; u < n; u += gridDim.x) {
+      if (!p.bad[u]) continue;
+      const long long chain = u / kSlices;
+      __syncthreads();
+      recurrent_unit<T, D, kOne>(p, sm, p.work.pre()[chain / p.H], (int)(chain % p.H),
+                                 (int)(u % kSlices), false);
+    }
+  }
+}
+
+// The segments of long sequences, from a counter: kState, each one's own state
+// (from zeros; the last one's is not needed by any other) to its slot, else
+// their outputs from the states at their starts, which lin_segments_kernel has
+// left there, and the last one's final state to the block.
+template <typename T, int D, bool kState>
+__global__ void __launch_bounds__(kRecThreads, rec_ctas(D, false))
+lin_rec_segments_kernel(LinParams p) {
+  constexpr int kSlices = D / kSlice;
+  __shared__ __align__(16) RecSmem<T, D, false> sm;
+  __shared__ int claimed;
+  pdl_wait_then_release();
+  int32_t* hdr = p.work.header();
+  const int32_t* first = p.work.pre_cp();  // first[k]: segments before entry k
+  const int n_units = (kState ? hdr[kLinStateItems] : hdr[kLinItems]) * p.H * kSlices;
+  const int per = hdr[kLinSegChunks], n_pre = hdr[kNPre];
+  for (;;) {
     __syncthreads();
-    recurrent_unit<T, D, kOne>(p, sm, p.work.pre()[chain / p.H], (int)(chain % p.H), (int)(u % kSlices),
-                         false);
+    if (threadIdx.x == 0) claimed = atomicAdd(&hdr[kState ? kLinStateHead : kLinHead], 1);
+    __syncthreads();
+    const int u = claimed;
+    if (u >= n_units) return;
+    const int slice = u % kSlices, h = (u / kSlices) % p.H, item = u / (kSlices * p.H);
+    int lo = 0, hi = n_pre - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first[mid] <= item) lo = mid; else hi = mid - 1;
+    }
+    const int seg = item - first[lo], nseg = first[lo + 1] - first[lo], s = p.work.pre()[lo];
+    if (kState && seg == nseg - 1) continue;
+    const int row0 = p.cu[s], len = p.cu[s + 1] - row0;
+    const int t0 = nseg > 1 ? seg * per * p.chunk : 0;
+    const int n = nseg > 1 ? min(per * p.chunk, len - t0) : len;
+    float* block = reinterpret_cast<float*>(p.layer_base + (size_t)p.blk[s] * p.stride) + (size_t)h * D * D;
+    float* slot = p.seg_states + ((size_t)item * p.H + h) * D * D;
+    const bool zero = kState || (nseg == 1 && !p.has_past[s]);
+    float* dst = kState ? slot : seg == nseg - 1 ? block : nullptr;
+    recurrent_body<T, D, false, kState>(p, sm, row0 + t0, n, h, slice, zero, nseg > 1 ? slot : block,
+                                        dst, [] { return true; });
+  }
+}
+
+// The states at the segments' starts, from the segments' own: in place,
+// Z[0] <- S0, Z[i] <- e^{g n} Z[i-1] + (the old Z[i-1]) with n tokens per
+// segment.  One float4 of one head's state per thread, the reads of eight
+// segments at a time in flight.
+__global__ void __launch_bounds__(256) lin_segments_kernel(LinParams p) {
+  pdl_wait_then_release();
+  const int32_t* hdr = p.work.header();
+  const int n_split = hdr[kLinSplit];
+  constexpr int kAhead = 8;
+  const int words = p.d * p.d / 4, parts = words / 256;
+  const int n_units = n_split * p.H * parts;
+  for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
+    const int part = u % parts, h = (u / parts) % p.H, e = u / (parts * p.H);
+    const int s = p.work.pre()[e], blk = p.blk[s];
+    const int first = p.work.pre_cp()[e], nseg = p.work.pre_cp()[e + 1] - first;
+    const size_t at = (size_t)part * 256 + threadIdx.x;
+    const DecayPair a =
+        decay_pair(finite_decay(p.log_decay[h]) * (float)(hdr[kLinSegChunks] * p.chunk));
+    float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.has_past[s])
+      S = reinterpret_cast<const float4*>(p.layer_base + (size_t)blk * p.stride)[(size_t)h * words + at];
+    float4* z = reinterpret_cast<float4*>(p.seg_states) + ((size_t)first * p.H + h) * words + at;
+    const size_t step = (size_t)p.H * words;
+    for (int i0 = 0; i0 < nseg; i0 += kAhead) {
+      float4 own[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)  // (the last segment's own state is not there)
+        if (i0 + i < nseg - 1) own[i] = z[(i0 + i) * step];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (i0 + i >= nseg) break;
+        z[(i0 + i) * step] = S;
+        S.x = fmaf(a.hi, S.x, fmaf(a.lo, S.x, own[i].x));
+        S.y = fmaf(a.hi, S.y, fmaf(a.lo, S.y, own[i].y));
+        S.z = fmaf(a.hi, S.z, fmaf(a.lo, S.z, own[i].z));
+        S.w = fmaf(a.hi, S.w, fmaf(a.lo, S.w, own[i].w));
+      }
+    }
   }
 }
 
@@ -318,12 +423,16 @@ constexpr int kSchedThreads = 1024;
 
 constexpr int kSortMax = 2048;     // long sequences that are put in order
 constexpr int kSmemCounts = 4096;  // pools whose block-use counts fit into shared memory
-constexpr int kMinSegment = 8;  // chunks
+constexpr int kMinSegment = 8;     // chunks, of the chunked form
+// The token-serial form's segments, in tiles of kTile tokens: at least
+// kMinSerial, and the launches they need cost about kSerialCost of them.
+constexpr int kMinSerial = 4, kSerialCost = 6;
+constexpr int kSerialPerSm = 4;    // CTAs that work on an SM side by side
 
 // One CTA.  Checks the batch as the pool's contract demands, lists its
 // sequences and cuts the long ones into segments.
 __global__ void __launch_bounds__(kSchedThreads)
-lin_schedule_kernel(LinParams p, int short_max, int num_sms) {
+lin_schedule_kernel(LinParams p, int short_max, int num_sms, int serial_ctas) {
   __shared__ unsigned s_flags;
   __shared__ int s_dec, s_pre, s_segs;
   __shared__ unsigned long long s_total;
@@ -370,7 +479,7 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms) {
     } else if (len <= short_max) {
       p.work.dec()[atomicAdd(&s_dec, 1)] = s;
     } else {
-      const int k = atomicAdd(&s_pre, 1), c = (len - 1) / kLinChunk + 1;
+      const int k = atomicAdd(&s_pre, 1), c = (len - 1) / p.chunk + 1;
       pre_tmp[k] = s;
       if (k < kSortMax) {
         found[k] = s;
@@ -402,17 +511,30 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms) {
   }
   __syncthreads();
   auto chunks_of = [&](int k) {
-    return sorted ? in_order[k] : (p.cu[pre[k] + 1] - p.cu[pre[k]] - 1) / kLinChunk + 1;
+    return sorted ? in_order[k] : (p.cu[pre[k] + 1] - p.cu[pre[k]] - 1) / p.chunk + 1;
   };
-  // One SM works a chain off in order, so the call takes at least the longest
-  // chain; its share of all chunks is what it takes at best.  Where the
-  // longest is more than a quarter above that, long sequences are cut into
-  // segments of half a share, which costs a second read of k and v.
-  const unsigned long long share = (s_total * p.H + num_sms - 1) / num_sms;
   int per = 0x7fffffff;
-  if (p.seg_states && sorted && 4ull * chunks_of(0) > 5 * share && chunks_of(0) >= 2 * kMinSegment) {
-    per = (int)((share + 1) / 2);
-    if (per < kMinSegment) per = kMinSegment;
+  bool split;
+  if (serial_ctas == 0) {
+    // Chunked form: one SM works a chain off in order, so the call takes at
+    // least the longest chain; its share of all chunks is what it takes at
+    // best.  Where the longest is more than a quarter above that, long
+    // sequences are cut into segments of half a share, which costs a second
+    // read of k and v.
+    const unsigned long long share = (s_total * p.H + num_sms - 1) / num_sms;
+    split = 4ull * chunks_of(0) > 5 * share && chunks_of(0) >= 2 * kMinSegment;
+    per = max((int)min((share + 1) / 2, 0x3fffffffull), kMinSegment);
+  } else {
+    // Token-serial form: the same with a head's columns over serial_ctas CTAs
+    // and segments of a share, which go over the tokens twice.
+    const int workers = kSerialPerSm * num_sms;
+    const unsigned long long share = (s_total * p.H * serial_ctas + workers - 1) / workers;
+    per = max((int)min(share, 0x3fffffffull), kMinSerial);
+    split = chunks_of(0) > 2ll * per + kSerialCost;
+  }
+  if (!split || !p.seg_states || !sorted) {
+    per = 0x7fffffff;
+  } else {
     for (;;) {  // until the segments of split sequences fit into the slots
       if (tid == 0) s_segs = 0;
       __syncthreads();
@@ -441,8 +563,8 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms) {
     }
     carry += total;
   }
-  for (long long i = tid; i < (long long)n_pre * p.H * kLinSlices; i += kSchedThreads)
-    p.bad[i] = 0;
+  if (p.bad)
+    for (long long i = tid; i < (long long)n_pre * p.H * kLinSlices; i += kSchedThreads) p.bad[i] = 0;
   if (tid == 0) {
     hdr[kLinItems] = carry;
     hdr[kLinSplit] = n_split;
@@ -473,7 +595,33 @@ cudaError_t launch_lin_recurrent(const LinParams& p, int d, int act, int max_ite
 }
 
 cudaError_t launch_lin_schedule(const LinParams& p, int short_max, int num_sms, cudaStream_t s) {
-  return launch_pdl(lin_schedule_kernel, dim3(1), dim3(kSchedThreads), 0, s, p, short_max, num_sms);
+  return launch_pdl(lin_schedule_kernel, dim3(1), dim3(kSchedThreads), 0, s, p, short_max, num_sms, 0);
+}
+
+cudaError_t launch_lin_segments(const LinParams& p, int num_sms, cudaStream_t s) {
+  return launch_pdl(lin_segments_kernel, dim3(4 * num_sms), dim3(256), 0, s, p);
+}
+
+cudaError_t launch_lin_serial_split(const LinParams& p, int act, int num_sms, cudaStream_t s) {
+  const bool f32 = act == GDN_F32;
+  auto run = [&](auto state, auto out) {
+    cudaError_t e = launch_pdl(lin_schedule_kernel, dim3(1), dim3(kSchedThreads), 0, s, p, 0, num_sms,
+                               p.d / kSlice);
+    const dim3 grid(5 * num_sms), block(kRecThreads);
+    if (e == cudaSuccess) e = launch_pdl(state, grid, block, 0, s, p);
+    if (e == cudaSuccess) e = launch_lin_segments(p, num_sms, s);
+    if (e == cudaSuccess) e = launch_pdl(out, grid, block, 0, s, p);
+    return e;
+  };
+  if (p.d == 32)
+    return f32 ? run(lin_rec_segments_kernel<float, 32, true>, lin_rec_segments_kernel<float, 32, false>)
+               : run(lin_rec_segments_kernel<__nv_bfloat16, 32, true>,
+                     lin_rec_segments_kernel<__nv_bfloat16, 32, false>);
+  if (p.d == 64)
+    return f32 ? run(lin_rec_segments_kernel<float, 64, true>, lin_rec_segments_kernel<float, 64, false>)
+               : run(lin_rec_segments_kernel<__nv_bfloat16, 64, true>,
+                     lin_rec_segments_kernel<__nv_bfloat16, 64, false>);
+  return run(lin_rec_segments_kernel<float, 128, true>, lin_rec_segments_kernel<float, 128, false>);
 }
 
 namespace {
@@ -490,8 +638,8 @@ int check_lin_dims(int num_blocks, int num_layers, int H, int d, int act, size_t
   return GDN_OK;
 }
 
-// room for the states of two segments per SM and then some
-constexpr int kSegSlots = 512;
+// room for segments' states: 512 of d = 128 (three per SM), more smaller ones
+constexpr size_t kSegBytes = 512 * 128 * 128 * sizeof(float);
 
 size_t lin_stride(int H, int d, size_t align) {
   return roundup((size_t)H * d * d * sizeof(float), align > 128 ? align : 128);
@@ -540,16 +688,15 @@ int gdn_lin_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int nu
     delete p;
     return st;
   }
-  if (gdn::lin_chunk_supported(d, act)) {
-    // the chunked form's segment states, then its marks
-    p->lin_slots = gdn::kSegSlots;
-    const size_t states = (size_t)p->lin_slots * d * d * sizeof(float);
-    if (cudaMalloc((void**)&p->lin_states, states + (size_t)num_blocks * num_heads * gdn::kLinSlices) != cudaSuccess) {
-      cudaGetLastError();
-      p->lin_states = nullptr;
-      gdn_state_pool_destroy(p);
-      return GDN_ERR_NOMEM;
-    }
+  // segment states, then the chunked form's marks
+  p->lin_slots = (int)(gdn::kSegBytes / ((size_t)d * d * sizeof(float)));
+  const size_t marks =
+      gdn::lin_chunk_supported(d, act) ? (size_t)num_blocks * num_heads * gdn::kLinSlices : 0;
+  if (cudaMalloc((void**)&p->lin_states, gdn::kSegBytes + marks) != cudaSuccess) {
+    cudaGetLastError();
+    p->lin_states = nullptr;
+    gdn_state_pool_destroy(p);
+    return GDN_ERR_NOMEM;
   }
   *out = p;
   return GDN_OK;
@@ -625,16 +772,28 @@ int gdn_lin_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
   p->last_path = chunked                             ? GDN_PREFILL_FUSED
                  : T > 1 && max_seqlen_hint != 1 ? GDN_PREFILL_SERIAL
                                                      : GDN_PREFILL_NONE;
-  // the scheduler's rule for splitting (see there) on what the host knows: no
-  // sequence is longer than T or the hint, and all tokens are some chunk's
-  const long long longest =
-      ((max_seqlen_hint > 0 && max_seqlen_hint < T ? max_seqlen_hint : T) - 1) / gdn::kLinChunk + 1;
-  const bool may_split = longest >= 2 * gdn::kMinSegment &&
-                         4 * longest * sms > 5ll * (T / gdn::kLinChunk) * H;
+  // the scheduler's rules for splitting (see there) on what the host knows: no
+  // sequence is longer than T or the hint, and all tokens are some sequence's
+  const long long longest = max_seqlen_hint > 0 && max_seqlen_hint < T ? max_seqlen_hint : T;
+  lp.seg_slots = p->lin_slots;
+  lp.d = d;
+  lp.chunk = chunked ? gdn::kLinChunk : gdn::kTile;
+  bool may_split;
   if (chunked) {
-    lp.seg_states = may_split ? p->lin_states : nullptr;
-    lp.seg_slots = p->lin_slots;
-    lp.bad = reinterpret_cast<unsigned char*>(p->lin_states + (size_t)p->lin_slots * d * d);
+    const long long chunks = (longest - 1) / gdn::kLinChunk + 1;
+    may_split = chunks >= 2 * gdn::kMinSegment && 4 * chunks * sms > 5ll * (T / gdn::kLinChunk) * H;
+    lp.bad = reinterpret_cast<unsigned char*>(p->lin_states) + gdn::kSegBytes;
+  } else {
+    const long long tiles = (longest - 1) / gdn::kTile + 1;
+    const long long share = (long long)(T / gdn::kTile) * H * (d / gdn::kSlice) / (gdn::kSerialPerSm * sms);
+    may_split = T > 1 && tiles > 2 * (share > gdn::kMinSerial ? share : gdn::kMinSerial) + gdn::kSerialCost;
+  }
+  if (may_split) lp.seg_states = p->lin_states;
+  if (!chunked && may_split) {
+    if (p->ev_before && cudaEventRecord(p->ev_before, s) != cudaSuccess) return GDN_ERR_CUDA;
+    if (gdn::launch_lin_serial_split(lp, p->act, sms, s) != cudaSuccess) return GDN_ERR_CUDA;
+    if (p->ev_after && cudaEventRecord(p->ev_after, s) != cudaSuccess) return GDN_ERR_CUDA;
+    return GDN_OK;
   }
   lp.listed = chunked || N > gdn::kSelfCheck;
   lp.late = chunked;

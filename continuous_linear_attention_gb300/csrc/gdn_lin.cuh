@@ -39,12 +39,13 @@ struct LinParams {
   unsigned char* layer_base;
   size_t stride;
   int T, N, H, group;  // group = H / Hkv
+  int d, chunk;        // head size; tokens per chunk that the scheduler counts in
   int num_blocks, hint;
   int listed;   // the scheduler has run: take the sequences from its list
   int late;     // (recurrent kernel) launched behind the chunk kernel
   WorkArea work;
-  // the chunked form's: states of the split sequences' segments [slots][d][d]
-  // (nullptr: never split) and its marks for what is left to the token-serial
+  // states of the split sequences' segments [slots][d][d] (nullptr: never
+  // split), and the chunked form's marks for what is left to the token-serial
   // kernel [index in the list of long sequences][H][kLinSlices]
   float* seg_states;
   int seg_slots;
@@ -82,6 +83,11 @@ cudaError_t launch_lin_schedule(const LinParams& p, int short_max, int num_sms, 
 // all N sequences, which it then validates itself; behind the chunked form
 // (p.late) also over what that has marked.
 cudaError_t launch_lin_recurrent(const LinParams& p, int d, int act, int max_items, cudaStream_t s);
+// The states at the segments' starts from the segments' own.
+cudaError_t launch_lin_segments(const LinParams& p, int num_sms, cudaStream_t s);
+// The whole forward in the token-serial form with long sequences cut into
+// segments: scheduler, state pass, segment states, output pass.
+cudaError_t launch_lin_serial_split(const LinParams& p, int act, int num_sms, cudaStream_t s);
 // The chunked form over pre[] (d = 128, bf16); may_split: with the state pass
 // that split sequences need.
 bool lin_chunk_supported(int d, int act);

@@ -854,46 +854,6 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
   if (warp == 0) tc::tmem_dealloc(tmem, TM_COLS);
 }
 
-// The states at the segments' starts, from the segments' own: in place,
-// Z[0] <- S0, Z[i] <- e^{g n} Z[i-1] + (the old Z[i-1]) with n tokens per
-// segment.  One float4 of one head's state per thread, the reads of eight
-// segments at a time in flight.
-__global__ void __launch_bounds__(256) lin_segments_kernel(LinParams p) {
-  pdl_wait_then_release();
-  const int32_t* hdr = p.work.header();
-  const int n_split = hdr[kLinSplit];
-  constexpr int kParts = D * D / 4 / 256, kAhead = 8;
-  const int n_units = n_split * p.H * kParts;
-  for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
-    const int part = u % kParts, h = (u / kParts) % p.H, e = u / (kParts * p.H);
-    const int s = p.work.pre()[e], blk = p.blk[s];
-    const int first = p.work.pre_cp()[e], nseg = p.work.pre_cp()[e + 1] - first;
-    const size_t at = (size_t)part * 256 + threadIdx.x;
-    const DecayPair a =
-        decay_pair(finite_decay(p.log_decay[h]) * (float)(hdr[kLinSegChunks] * CH));
-    float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.has_past[s])
-      S = reinterpret_cast<const float4*>(p.layer_base + (size_t)blk * p.stride)[(size_t)h * D * D / 4 + at];
-    float4* z = reinterpret_cast<float4*>(p.seg_states) + ((size_t)first * p.H + h) * (D * D / 4) + at;
-    const size_t step = (size_t)p.H * (D * D / 4);
-    for (int i0 = 0; i0 < nseg; i0 += kAhead) {
-      float4 own[kAhead];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i)  // (the last segment's own state is not there)
-        if (i0 + i < nseg - 1) own[i] = z[(i0 + i) * step];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (i0 + i >= nseg) break;
-        z[(i0 + i) * step] = S;
-        S.x = fmaf(a.hi, S.x, fmaf(a.lo, S.x, own[i].x));
-        S.y = fmaf(a.hi, S.y, fmaf(a.lo, S.y, own[i].y));
-        S.z = fmaf(a.hi, S.z, fmaf(a.lo, S.z, own[i].z));
-        S.w = fmaf(a.hi, S.w, fmaf(a.lo, S.w, own[i].w));
-      }
-    }
-  }
-}
-
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
@@ -939,7 +899,7 @@ cudaError_t launch_lin_chunk(const LinParams& p, bool may_split, int num_sms, cu
     if (e == cudaSuccess)
       e = launch_pdl(kern, dim3(num_sms), dim3(kThreads), SMEM_BYTES, s, p, tq, tk, tv, to);
     if (e == cudaSuccess && state)
-      e = launch_pdl(lin_segments_kernel, dim3(4 * num_sms), dim3(256), 0, s, p);
+      e = launch_lin_segments(p, num_sms, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -304,3 +304,21 @@ def test_refusals():
         with pytest.raises(ValueError):
             binding.lin_varlen_forward(run.pool, 0, kw["q"], kw["k"], kw["v"], run.cu_d, run.blk_d,
                                        run.past_d, run.decay_d, kw["out"], 4, 2)
+
+
+@pytest.mark.parametrize("act,d", FORMS[:-1])
+@pytest.mark.parametrize("lens,H,Hkv", [([700], 2, 1), ([3, 900, 1, 0, 64, 385], 3, 3), ([257, 260], 1, 1)])
+def test_long_sequences_of_few_heads_are_split(act, d, lens, H, Hkv):
+    """The token-serial form over segments side by side: their own states
+    first, then the outputs from the states at their starts."""
+    _, errs = run_and_check(lens, [1, 0] * (len(lens) // 2) + [1] * (len(lens) % 2), H, Hkv, d, act,
+                            log_decay=[-1e-3, -0.05, 0.0][:H], seed=d)
+    if act == "f32":
+        assert errs["out"] <= fp32_walk(max(lens)) and errs["state"] <= fp32_walk(max(lens)), errs
+
+
+def test_a_split_call_skips_what_it_should():
+    run_and_check([400, 300, 2, 350], [1, 1, 0, 1], 2, 1, 64, "f32", blocks=[3, 9, -1, 3], num_blocks=8,
+                  rows_after=2)
+    run_and_check([400, 30, 2, 350], [1, 1, 0, 1], 2, 1, 32, "bf16", blocks=[3, 2, -1, 5], num_blocks=8,
+                  hint=380)
