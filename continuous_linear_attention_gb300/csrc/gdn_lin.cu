@@ -423,7 +423,11 @@ constexpr int kSchedThreads = 1024;
 
 constexpr int kSortMax = 2048;     // long sequences that are put in order
 constexpr int kSmemCounts = 4096;  // pools whose block-use counts fit into shared memory
-constexpr int kMinSegment = 8;     // chunks, of the chunked form
+// The chunked form's segments, in chunks: from kMinSegment up, at most
+// kMaxSegments of them, and of sequences from kMinSplit on.  (Two heads: 1,024
+// tokens 30 us in segments of two chunks and 32 us whole, 768 tokens 30 and 27;
+// 13,311 tokens 51 us in segments of two and 45 us in segments of four.)
+constexpr int kMinSegment = 2, kMaxSegments = 32, kMinSplit = 8;
 // The token-serial form's segments, in tiles of kTile tokens: at least
 // kMinSerial, and the launches they need cost about kSerialCost of them.
 constexpr int kMinSerial = 4, kSerialCost = 6;
@@ -522,8 +526,9 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms, int serial_ctas) {
     // sequences are cut into segments of half a share, which costs a second
     // read of k and v.
     const unsigned long long share = (s_total * p.H + num_sms - 1) / num_sms;
-    split = 4ull * chunks_of(0) > 5 * share && chunks_of(0) >= 2 * kMinSegment;
-    per = max((int)min((share + 1) / 2, 0x3fffffffull), kMinSegment);
+    split = 4ull * chunks_of(0) > 5 * share && chunks_of(0) >= kMinSplit;
+    per = max((int)min((share + 1) / 2, 0x3fffffffull),
+              max(kMinSegment, (chunks_of(0) - 1) / kMaxSegments + 1));
   } else {
     // Token-serial form: the same with a head's columns over serial_ctas CTAs
     // and segments of a share, which go over the tokens twice.
@@ -781,7 +786,7 @@ int gdn_lin_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
   bool may_split;
   if (chunked) {
     const long long chunks = (longest - 1) / gdn::kLinChunk + 1;
-    may_split = chunks >= 2 * gdn::kMinSegment && 4 * chunks * sms > 5ll * (T / gdn::kLinChunk) * H;
+    may_split = chunks >= gdn::kMinSplit && 4 * chunks * sms > 5ll * (T / gdn::kLinChunk) * H;
     lp.bad = reinterpret_cast<unsigned char*>(p->lin_states) + gdn::kSegBytes;
   } else {
     const long long tiles = (longest - 1) / gdn::kTile + 1;
