@@ -6,10 +6,10 @@
 //   o_i     = scale e^{g (i+1)} S0^T q_i + sum_j P[i][j] v_j
 //   S_n     = e^{g n} S0 + sum_j e^{g (n-1-j)} k_j v_j^T
 // so a (sequence, head) chain is four 128^3 products per chunk, and all but
-// the first term of each line does not depend on the chunks before.  Where
-// e^{128 |g|} is far inside bf16's range (kGentle) the row's decay leaves P,
-//   o_i = scale e^{g (i+1)} (S0^T q_i + sum_j e^{-g (j+1)} (q_i . k_j) v_j),
-// so that both products accumulate without a pass over O between them.
+// the first term of each line does not depend on the chunks before.  No weight
+// is a growing power that another one takes back, so any decay will do.  (With
+// the row's decay taken out of P where e^{128 |g|} allows it, the pass over
+// Q S0 goes, for 1% of the prompt batch's time.)
 //
 // Bytes bound it: q, k, v and o are 128 KB per chunk and head (2.9 us of one
 // SM's share of HBM); the products, the state's in four terms, are seven 128^3
@@ -18,12 +18,11 @@
 // One CTA per SM, chains claimed from a counter, longest first.  Roles, each
 // a loop over the CTA's chunks that meets the others at mbarriers only:
 //   producer  one thread: TMA loads of a chunk's q, k, v tiles, two stages
-//   MMA 1     one thread: P = Q K^T, O = Q S0, then O += P V in two halves of
-//             64 columns, so that the O warps' work on one half runs beside it
-//   MMA 2     one thread: U = sum of the decayed v k^T, 32 tokens at a time
+//   MMA 1     one warp: P = Q K^T, O = Q S0, then O += P V in two halves of 64
+//             columns, so that the O warps' work on one half runs beside it
+//   MMA 2     one warp: U = sum of the decayed v k^T, 32 tokens at a time
 //   store     one thread: the staged output tile to global memory by TMA
-//   O warps   P with its decay -> bf16 A operand; O <- e^{g(i+1)} O where the
-//             decay is steep; output
+//   O warps   P with its decay -> bf16 A operand; O <- scale e^{g(i+1)} O; output
 //   V warps   e^{g(n-1-j)} v_j -> A operand of U, rows past the chunk's end
 //             zeroed
 //   S warps   the state, fp32 in registers (thread v holds S[.][v]): to bf16
@@ -31,9 +30,9 @@
 //
 // Precision.  P and S0 enter as bf16 operands (their partners are bf16, and
 // one MMA takes one type): each is off by as much as the output's own
-// rounding.  The state is an output in fp32 and carried
-// over the whole prompt, so its update is not rounded to bf16: a decayed v has
-// 8 + 24 significant bits and goes in as four bf16 terms.  With the weight as
+// rounding.  The state is an output in fp32 and carried over the whole prompt,
+// so its update is not rounded to bf16: a decayed v has 8 + 24 significant bits
+// and goes in as four bf16 terms.  With the weight as
 // wh + wm + wl (8 bits each), v wh is its bf16 rounding plus a remainder that
 // an fma gives exactly and that is a bf16 again, v wm likewise, and v wl joins
 // the last remainder (2^-18 of the whole, off by 2^-27): five packed bf16
@@ -91,7 +90,6 @@ constexpr int QT = 32;  // tokens per step of U
 constexpr int kTerms = 4;
 // the state pass has no P and O: two buffers for U and four for the decayed v
 constexpr uint32_t TM_U1 = 0, TM_V1 = 128;
-constexpr float kGentle = 32.f;  // largest 128 |g| whose e^{128 |g|} may stand in P
 
 enum Flag : int {
   kFirst = 1,   // first chunk of its chain (or segment)
@@ -118,12 +116,9 @@ constexpr uint32_t OFF_CTL = OFF_S + TILE;
 constexpr uint32_t SMEM_BYTES = OFF_CTL + sizeof(Ctl);
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
 
-// A bounded wait in few instructions, as the waiting warps share the issue
-// slots with the working ones.  The first test has no suspend time, which
-// would add 30 cycles to a wait whose phase is complete (55); the later ones
-// have one, and the limit is a few seconds (at least 0.4 s).
-constexpr int kWaitTests = 1 << 24;
-__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
+// A bounded wait.  The first test has no suspend time, which would add 30
+// cycles to a wait whose phase is complete (55).
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -132,13 +127,7 @@ __device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
-  if (try_wait(bar, parity)) return true;
-  for (int i = 0; i < kWaitTests; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return false;
+  return ok != 0 || mbar_wait_bounded(bar, parity);
 }
 // The same for a warp: false for all lanes if any gave up.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
@@ -315,32 +304,30 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
   auto u_col = [](int b) { return b == 0 ? TM_U : TM_U1; };
   auto v_col = [](int b) { return (b < 2 ? TM_V : TM_V1) + (uint32_t)(b & 1) * (16 * kTerms); };
 
-  // registers a thread, of 80 at launch: O 72, V 56, S 184, the others 40
+  // registers a thread, of 80 at launch: O as launched, V 48, S 184, the others 40
   if (warp < kOWarps) {
     // ============================== O warps ===============================
     // Warps w and w + 4 have rows 32 w .. 32 w + 31 of the chunk (TMEM lanes)
     // and columns 0 .. 63 or 64 .. 127 of P and O.
-    regs_dec<72>();
     const int rw = warp & 3, hf = warp >> 2;
     const int i = rw * 32 + lane;
     const uint32_t tl = (uint32_t)(rw * 32) << 16;
     int h = -1;
     float g = 0.f, after = 0.f;  // scale e^{g (i+1)}
-    float col = 0.f;             // e^{g (31 - lane)}
-    bool gentle = true;
+    float col = 0.f, dia = 0.f;  // e^{g (31 - lane)}, scale e^{g lane}
     Pos<kStages> pos;
     for (int c = 0; !kState; ++c, pos.next()) {
       const int b = pos.b;
       const uint32_t ph = (uint32_t)(c & 1);
       if (!warp_wait(&ctl.full[b], pos.ph)) { dead = true; break; }
-      const Desc d = ctl.desc[b];
-      if (d.flags & kEnd) break;
-      if (d.h != h) {
-        h = d.h;
+      if (ctl.desc[b].flags & kEnd) break;
+      const int row = ctl.desc[b].row, n = ctl.desc[b].n;
+      if (ctl.desc[b].h != h) {
+        h = ctl.desc[b].h;
         g = finite_decay(p.log_decay[h]);
-        gentle = fabsf(g) * (float)CH <= kGentle;
         after = p.scale * expf(g * (float)(i + 1));
         col = expf(g * (float)(31 - lane));
+        dia = p.scale * expf(g * (float)lane);
       }
       // ---- P: decay and mask, to bf16 over the first 32 of this warp's own 64
       // columns (block u's 16 land on fp32 columns read before)
@@ -356,25 +343,23 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         } else {
           float x[32];
           tc::tmem_ld32(tmem + tl + TM_P + jb * 32, x);
-          // column jj's weight comes from a lane's: e^{-g (j+1)} (gentle), on
-          // the diagonal of a steep head scale e^{g (lane - jj)}, left of it
-          // e^{g (31 - jj)} times the row's scale e^{g (i - 32 jb - 31)}
-          const bool direct = !gentle && jb == rw;
-          const float tab = gentle   ? col * expf(-g * (float)(32 * jb + 32))
-                            : direct ? p.scale * expf(g * (float)lane)
-                                     : col;
-          const int dir = direct ? -1 : 1, from = direct ? lane : 0;
+          // column jj's weight comes from a lane: on the diagonal block
+          // scale e^{g (lane - jj)}, left of it e^{g (31 - jj)} times the row's
+          // scale e^{g (i - 32 jb - 31)}
+          const bool diagonal = jb == rw;
+          const float tab = diagonal ? dia : col;
+          const int dir = diagonal ? -1 : 1, from = diagonal ? lane : 0;
           tc::tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; ++e) x[e] *= __shfl_sync(0xffffffffu, tab, from + dir * e);
-          if (!gentle && !direct) {
-            const float row = p.scale * expf(g * (float)(i - 32 * jb - 31));
+          if (!diagonal) {
+            const float rowf = p.scale * expf(g * (float)(i - 32 * jb - 31));
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] *= row;
+            for (int e = 0; e < 32; ++e) x[e] *= rowf;
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e) w[e] = bf2(x[2 * e], x[2 * e + 1]);
-          if (jb == rw) {
+          if (diagonal) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               w[e] = lane > 2 * e ? w[e] : lane == 2 * e ? w[e] & 0xffffu : 0u;
@@ -386,31 +371,28 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       tc::fence_before_sync();
       warp_arrive(&ctl.pb_full);
       // ---- O = Q S0 times its row's decay
-      if (!gentle) {
-        if (!warp_wait(&ctl.qs_full, ph)) { dead = true; break; }
-        tc::fence_after_sync();
+      if (!warp_wait(&ctl.qs_full, ph)) { dead = true; break; }
+      tc::fence_after_sync();
 #pragma unroll 1
-        for (int u = 0; u < 2; ++u) {
-          float x[32];
-          const uint32_t at = tmem + tl + TM_O + hf * 64 + u * 32;
-          tc::tmem_ld32(at, x);
-          tc::tmem_wait_ld();
+      for (int u = 0; u < 2; ++u) {
+        float x[32];
+        const uint32_t at = tmem + tl + TM_O + hf * 64 + u * 32;
+        tc::tmem_ld32(at, x);
+        tc::tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] *= after;
-          tc::tmem_st32(at, x);
-        }
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
+        for (int e = 0; e < 32; ++e) x[e] *= after;
+        tc::tmem_st32(at, x);
       }
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
       warp_arrive(&ctl.o_scaled);
       // ---- the chunk's outputs: staged over the q tile (its products are
       // done), or, past a sequence's end, the valid rows straight out
-      unsigned char* stage = sm + b * ST_BYTES + ST_Q + hf * BOX;
-      __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + (size_t)(d.row + i) * p.ldo +
-                            (size_t)d.h * D + hf * 64;
-      const float of = gentle ? after : 1.f;
       if (!warp_wait(&ctl.o_full[hf], ph)) { dead = true; break; }
       tc::fence_after_sync();
+      unsigned char* stage = sm + b * ST_BYTES + ST_Q + hf * BOX;
+      __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + (size_t)(row + i) * p.ldo +
+                            (size_t)h * D + hf * 64;
 #pragma unroll 1
       for (int u = 0; u < 2; ++u) {
         float x[32];
@@ -419,13 +401,13 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint4 w;
-          w.x = bf2(x[8 * e] * of, x[8 * e + 1] * of);
-          w.y = bf2(x[8 * e + 2] * of, x[8 * e + 3] * of);
-          w.z = bf2(x[8 * e + 4] * of, x[8 * e + 5] * of);
-          w.w = bf2(x[8 * e + 6] * of, x[8 * e + 7] * of);
-          if (d.n == CH)
+          w.x = bf2(x[8 * e], x[8 * e + 1]);
+          w.y = bf2(x[8 * e + 2], x[8 * e + 3]);
+          w.z = bf2(x[8 * e + 4], x[8 * e + 5]);
+          w.w = bf2(x[8 * e + 6], x[8 * e + 7]);
+          if (n == CH)
             *reinterpret_cast<uint4*>(stage + tc::sw128_offset(i, u * 32 + 8 * e)) = w;
-          else if (i < d.n)
+          else if (i < n)
             *reinterpret_cast<uint4*>(orow + u * 32 + 8 * e) = w;
         }
       }
@@ -441,7 +423,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
     // fragments: this lane gets tokens 2 (lane % 4) and the next of each 8,
     // elements lane / 4 of each 8.  (With one warp per sub-partition these
     // dependent chains took 4,800 of a chunk's 8,400 cycles.)
-    regs_dec<56>();
+    regs_dec<48>();
     const int vw = warp & 3, half = (warp >> 2) & 1;
     const uint32_t tl = (uint32_t)(vw * 32) << 16;
     const int mr = lane & 7, mt = lane >> 4, mv = (lane >> 3) & 1;  // matrix row, token and element half
