@@ -844,15 +844,14 @@ typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void
 // Tensor map of `rows` rows of `cols` bf16 at a pitch of ld elements, in
 // boxes of 64 columns x 128 rows, 128-byte swizzled, zero fill past the end.
 cudaError_t rows_map(CUtensorMap* m, const void* base, int rows, long long cols, long long ld) {
-  static EncodeFn encode = nullptr;
-  if (!encode) {
+  static const EncodeFn encode = [] {  // (set once, whichever threads come first)
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
     const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
                                                            cudaEnableDefault, &q);
-    if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
-    encode = reinterpret_cast<EncodeFn>(fn);
-  }
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeFn>(fn) : nullptr;
+  }();
+  if (!encode) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
   const cuuint32_t box[2] = {64, (cuuint32_t)CH}, estr[2] = {1, 1};

@@ -87,7 +87,7 @@ def check(run, tensor_cores=False, before=None):
     to its type (relative to the value).  The tensor-core form adds one bf16
     rounding (2^-8) of the weights (q k^T with the decay) and of the state as
     operands, each relative to its own part of A, and keeps the state itself
-    as fp32: three bf16 terms per decayed operand (2^-24) and fp32
+    as fp32: four bf16 terms per decayed operand (2^-27) and fp32
     accumulation, at most 32 steps per chunk (2^-23 each, should the unit
     truncate).  Below fp32's range a rounding is off by up to 2^-126 whatever
     the value, in a state term once more times q in the output."""

@@ -253,3 +253,45 @@ def test_a_beam_search_and_its_end():
         assert np.linalg.norm(got - states[0]) <= 1e-5 * np.linalg.norm(states[0])
         o = last[j].double().cpu().numpy()
         assert np.linalg.norm(o - out[-1]) <= 2.0 ** -7 * np.linalg.norm(out[-1])
+
+
+def test_block_operations_follow_their_stream():
+    """On a stream of their own behind slow work that writes the blocks and the
+    lists, while another pool is busy on another stream."""
+    a, b = Blocks("gdn", 12, seed=1), Blocks("lin", 40, seed=2)
+    first, zero = idx([1, 2, 3]), idx([0, 0, 0])
+    src, dst, dead = zero.clone(), zero.clone(), zero.clone()
+    lists = idx([2, 1, 1]), idx([1, 2, 5]), idx([7, 7, -1])
+    fresh = torch.randint_like(a.mem, 2 ** 31 - 1)
+    fresh[:, 0] = 0
+    torch.cuda.synchronize()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(2_000_000)
+        a.mem.copy_(fresh)
+        for x, y in zip((src, dst, dead), lists):
+            x.copy_(y)
+        a.pool.copy_blocks(src, dst)
+        a.pool.clear_blocks(dead)
+        for x in (src, dst, dead):
+            x.copy_(first)
+    with torch.cuda.stream(t):
+        b.pool.copy_blocks(idx([4, 5]), idx([5, 4]))
+    torch.cuda.synchronize()
+    a.before = fresh
+    a.check({1: 2, 2: 1, 5: 1, 7: None}, 0)
+    b.check({5: 4, 4: 5}, 0)
+
+
+def test_operations_one_after_the_other_without_a_host_wait():
+    """Each operation's plan may not overtake the moves before it."""
+    b = Blocks("lin", 64, seed=5)
+    rng = np.random.default_rng(6)
+    where = np.arange(64)
+    for _ in range(40):
+        dst = rng.permutation(np.arange(1, 64))[:rng.integers(1, 63)]
+        src = rng.integers(1, 64, len(dst))
+        b.pool.copy_blocks(idx(src), idx(dst))
+        where[dst] = where[src]
+    torch.cuda.synchronize()
+    b.check({x: int(where[x]) for x in range(64)}, 0)

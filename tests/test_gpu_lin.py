@@ -322,3 +322,114 @@ def test_a_split_call_skips_what_it_should():
                   rows_after=2)
     run_and_check([400, 30, 2, 350], [1, 1, 0, 1], 2, 1, 32, "bf16", blocks=[3, 2, -1, 5], num_blocks=8,
                   hint=380)
+
+
+@pytest.mark.parametrize("act,d", [("f32", 64), ("bf16", 128)])
+@pytest.mark.parametrize("n", [6, 600])
+def test_a_hint_of_one_flags_what_is_longer(act, d, n):
+    """Few sequences check themselves, many are listed; either way one of two
+    tokens, a padding entry and a block named twice are left out."""
+    lens = [1] * n
+    lens[2], lens[4] = 2, 0
+    blocks = list(range(n + 1, 1, -1))
+    blocks[1], blocks[5] = -1, blocks[0]
+    run_and_check(lens, [1, 0] * (n // 2), 2, 1, d, act, blocks=blocks, num_blocks=n + 2, hint=1, rows_after=1)
+
+
+@pytest.mark.parametrize("lens,H,Hkv", [([1030], 1, 1), ([1500, 1, 0, 40, 1153], 3, 1), ([4000, 1024], 2, 2)])
+@pytest.mark.parametrize("past", [0, 1])
+def test_long_prompts_of_few_heads_are_split(lens, H, Hkv, past):
+    """The chunked form over segments side by side, with decays from none to
+    more than a segment remembers."""
+    run_and_check(lens, [past] * len(lens), H, Hkv, 128, "bf16", log_decay=[-0.004, 0.0, -3.0][:H],
+                  tensor_cores=True, seed=H)
+
+
+@pytest.mark.parametrize("blocks,hint", [([3, 9, 5, 1], 0), ([3, -1, 5, 3], 0), ([3, 0, 5, 1], 1200)])
+def test_a_split_prompt_batch_skips_what_it_should(blocks, hint):
+    run_and_check([1100, 1300, 3, 1150], [1, 1, 0, 1], 2, 1, 128, "bf16", blocks=blocks, num_blocks=8,
+                  hint=hint, rows_after=2, tensor_cores=True)
+
+
+@pytest.mark.parametrize("act,d,at", [("bf16", 128, 700), ("bf16", 128, 1410), ("f32", 32, 700)])
+def test_values_that_are_not_finite_in_a_split_sequence(act, d, at):
+    """Earlier rows of every segment and the other columns come out as if the
+    value were a number."""
+    col = 5  # of v
+
+    def put(x, run):
+        x[at, (run.H + run.Hkv) * d + col] = float("inf")
+
+    run = LinRun([1420, 3], [1, 1], 2, 1, d, act, values=put, log_decay=[-0.01, -0.2], dense=True)
+    run.run()
+    torch.cuda.synchronize()
+    assert run.pool.error_flags() == 0
+    run.x[at, (run.H + run.Hkv) * d + col] = 0.0
+    out, states = run.expected()
+    got = run.out.double().cpu().numpy()
+    view = run.view[0].cpu().double().numpy()[run.blk[0]]
+    tol, st_tol = (1e-5, 1e-5) if act == "f32" else (2.0 ** -7, 1e-5)
+    fine = np.ones(d, bool)
+    fine[col] = False
+    n = np.linalg.norm
+    assert n(got[:at] - out[:at]) <= tol * n(out[:at])
+    assert n(got[at:, :, fine] - out[at:, :, fine]) <= tol * n(out[at:, :, fine])
+    assert n(view[..., fine] - states[0][..., fine]) <= st_tol * n(states[0][..., fine])
+    assert not np.isfinite(got[at:1420, :, col]).any() and not np.isfinite(view[..., col]).any()
+
+
+@pytest.mark.parametrize("act,d,lens", [("bf16", 128, [1500, 1, 40, 3]), ("f32", 32, [900, 1, 40, 3])])
+def test_a_captured_split_call_replays_over_a_batch_that_is_not_split(act, d, lens):
+    a = LinRun(lens, [1, 0, 1, 1], 2, 1, d, act, seed=2)
+    short = [len_ for len_ in (a.T // 4,) * 3] + [a.T - 3 * (a.T // 4)]
+    b = LinRun(short, [0, 1, 0, 1], 2, 1, d, act, seed=3, blocks=a.blk)
+    before = b.mem.clone()
+    a.run()
+    torch.cuda.synchronize()
+    check(a, tensor_cores=act == "bf16")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.run(torch.cuda.current_stream())
+    for x, y in ((a.q._base, b.q._base), (a.cu_d, b.cu_d), (a.past_d, b.past_d), (a.mem, before)):
+        x.copy_(y)
+    graph.replay()
+    b.run()
+    torch.cuda.synchronize()
+    assert torch.equal(a.out, b.out) and torch.equal(a.mem, b.mem)
+    check(b, tensor_cores=act == "bf16")
+
+
+def test_two_pools_on_two_streams_at_once():
+    runs = [LinRun([1300, 1, 200], [1, 1, 0], 2, 2, 128, "bf16", seed=11),
+            LinRun([700, 2, 90], [0, 1, 1], 3, 1, 64, "f32", seed=12)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    for r, s in zip(runs, streams):
+        r.run(s)
+    torch.cuda.synchronize()
+    for r in runs:
+        check(r, tensor_cores=r.act == "bf16")
+
+
+@pytest.mark.parametrize("lens", [[1, 39], [20] * 2])
+def test_row_offsets_past_32_bits(lens):
+    """q, k, v and out as columns of rows of 2^28 elements: the last row starts
+    beyond 2^33 elements."""
+    run = LinRun(lens, [1] * len(lens), 2, 1, 128, "bf16", seed=7)
+    wide = torch.empty(run.T, 2 ** 28, dtype=torch.bfloat16, device="cuda")
+    for name, x, at in (("q", run.q, 0), ("k", run.k, 2 ** 27), ("v", run.v, 2 ** 28 - 512),
+                        ("out", run.out, 2 ** 28 - 256)):
+        cols = wide[:, at:at + x.shape[1] * 128]
+        cols.copy_(x.flatten(1))
+        setattr(run, name, cols.unflatten(1, (-1, 128)))
+    run.run()
+    torch.cuda.synchronize()
+    check(run, tensor_cores=True)
+
+
+def test_has_past_is_any_value_but_zero():
+    run = LinRun([1, 40, 3], [1, 1, 0], 2, 1, 128, "bf16")
+    run.past_d.copy_(torch.tensor([255, 2, 0], dtype=torch.uint8))
+    run.run()
+    torch.cuda.synchronize()
+    check(run, tensor_cores=True)
