@@ -34,6 +34,9 @@ constexpr int kTile = 16;                           // tokens staged at a time
 // calls of up to this many sequences check the batch in every CTA, while its
 // state loads are in flight, which saves the scheduler's launch
 constexpr int kSelfCheck = 512;
+// groups of kRecThreads that work on segments side by side on an SM (their
+// shared memory: 184 KB of fp32 at d = 128)
+constexpr int kSerialPerSm = 4;
 
 // kN consecutive elements (kN * sizeof(T) aligned): as they lie, and as fp32.
 template <typename T, int kN>
@@ -82,17 +85,27 @@ struct RecSmem<T, D, true> {
   float part[1][kRecThreads / 32][kSlice];
 };
 
+// Barrier of the kRecThreads threads that work on one unit: the CTA, or one of
+// its groups.
+template <bool kGroups>
+__device__ __forceinline__ void unit_sync() {
+  if constexpr (kGroups)
+    asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.x / kRecThreads), "n"(kRecThreads) : "memory");
+  else
+    __syncthreads();
+}
+
 // Columns 32 slice .. of head h over len tokens from row row0: the state is
 // read from src (unless zero: it starts at zeros), advanced and written to dst
 // (nullptr: not), both the head's [D][D].  ok() is asked once all reads are on their way, and
 // nothing is written where it says no.  kOne: len is at most 1.  kState: the
 // state only, no outputs.
-template <typename T, int D, bool kOne, bool kState, typename Ok>
+template <typename T, int D, bool kOne, bool kState, bool kGroups, typename Ok>
 __device__ __forceinline__ void recurrent_body(const LinParams& p, RecSmem<T, D, kOne>& sm,
                                                int row0, int len, int h, int slice,
                                                bool zero, const float* src, float* dst, Ok ok) {
   constexpr int kRows = D / kRowT;      // state rows per thread
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = kGroups ? threadIdx.x % kRecThreads : threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int c0 = slice * kSlice + (tid % kColT) * 4;  // this thread's columns
   const int r0 = (tid / kColT) * kRows;               // and rows
   const size_t at = (size_t)r0 * D + c0;
@@ -187,7 +200,7 @@ __device__ __forceinline__ void recurrent_body(const LinParams& p, RecSmem<T, D,
     if constexpr (!kState) {
       const float4 o = across(mine);
       if (lane < kColT) *reinterpret_cast<float4*>(&sm.part[0][warp][lane * 4]) = o;
-      __syncthreads();
+      unit_sync<kGroups>();
       if (tid < kSlice) {
         float acc = 0.f;
 #pragma unroll
@@ -205,7 +218,7 @@ __device__ __forceinline__ void recurrent_body(const LinParams& p, RecSmem<T, D,
       } else {
         cp_async_wait<0>();
       }
-      __syncthreads();  // the tile has landed, and the last one's sums are read
+      unit_sync<kGroups>();  // the tile has landed, and the last one's sums are read
       const int n = min(kTile, len - t0);
       // kN tokens: their reads come first and their sums run side by side
       auto batch = [&](int t, auto count) {
@@ -234,7 +247,7 @@ __device__ __forceinline__ void recurrent_body(const LinParams& p, RecSmem<T, D,
       int t = 0;
       for (; t + kBatch <= n; t += kBatch) batch(t, std::integral_constant<int, kBatch>());
       for (; t < n; ++t) batch(t, std::integral_constant<int, 1>());
-      __syncthreads();  // the tile's sums are there, and its buffer may be staged over
+      unit_sync<kGroups>();  // the tile's sums are there, and its buffer may be staged over
       if constexpr (!kState) {
         for (int i = tid; i < n * kSlice; i += kRecThreads) {
           const int t = i / kSlice, c = i % kSlice;
@@ -290,7 +303,7 @@ __device__ __forceinline__ void recurrent_unit(const LinParams& p, RecSmem<T, D,
     if (flags && tid == 0 && h == 0 && slice == 0) atomicOr((unsigned*)&p.work.header()[kErr], flags);
     return active && !flags;
   };
-  recurrent_body<T, D, kOne, false>(p, sm, active ? row0 : 0, active ? len : 0, h, slice,
+  recurrent_body<T, D, kOne, false, false>(p, sm, active ? row0 : 0, active ? len : 0, h, slice,
                                     !active || !p.has_past[s], state, state, ok);
 }
 
@@ -336,27 +349,32 @@ lin_recurrent_kernel(LinParams p) {
   }
 }
 
-// The segments of long sequences, from a counter: kState, each one's own state
+// The segments of long sequences: kState, each one's own state
 // (from zeros; the last one's is not needed by any other) to its slot, else
 // their outputs from the states at their starts, which lin_segments_kernel has
-// left there, and the last one's final state to the block.
+// left there, and the last one's final state to the block.  One CTA per SM, of
+// kSerialPerSm groups that work by themselves.  The first units go to the CTAs'
+// first groups and so on, which spreads them over the SMs (as CTAs of their
+// own, several of the first ones shared an SM: twice the time of a call of few
+// chains), the others are taken from a counter.
 template <typename T, int D, bool kState>
-__global__ void __launch_bounds__(kRecThreads, rec_ctas(D, false))
-lin_rec_segments_kernel(LinParams p) {
+__global__ void __launch_bounds__(kRecThreads* kSerialPerSm, 1) lin_rec_segments_kernel(LinParams p) {
   constexpr int kSlices = D / kSlice;
-  __shared__ __align__(16) RecSmem<T, D, false> sm;
-  __shared__ int claimed;
+  extern __shared__ __align__(128) unsigned char rec_smem[];
+  __shared__ int claimed[kSerialPerSm];
+  const int group = threadIdx.x / kRecThreads;
+  RecSmem<T, D, false>& sm = reinterpret_cast<RecSmem<T, D, false>*>(rec_smem)[group];
   pdl_wait_then_release();
   int32_t* hdr = p.work.header();
   const int32_t* first = p.work.pre_cp();  // first[k]: segments before entry k
   const int n_units = (kState ? hdr[kLinStateItems] : hdr[kLinItems]) * p.H * kSlices;
-  const int per = hdr[kLinSegChunks], n_pre = hdr[kNPre];
-  for (;;) {
-    __syncthreads();
-    if (threadIdx.x == 0) claimed = atomicAdd(&hdr[kState ? kLinStateHead : kLinHead], 1);
-    __syncthreads();
-    const int u = claimed;
-    if (u >= n_units) return;
+  const int per = hdr[kLinSegChunks], n_pre = hdr[kNPre], groups = gridDim.x * kSerialPerSm;
+  for (int u = group * gridDim.x + blockIdx.x, next; u < n_units; u = next) {
+    if (threadIdx.x % kRecThreads == 0)
+      claimed[group] =
+          n_units > groups ? groups + atomicAdd(&hdr[kState ? kLinStateHead : kLinHead], 1) : n_units;
+    unit_sync<true>();
+    next = claimed[group];
     const int slice = u % kSlices, h = (u / kSlices) % p.H, item = u / (kSlices * p.H);
     int lo = 0, hi = n_pre - 1;
     while (lo < hi) {
@@ -364,7 +382,6 @@ lin_rec_segments_kernel(LinParams p) {
       if (first[mid] <= item) lo = mid; else hi = mid - 1;
     }
     const int seg = item - first[lo], nseg = first[lo + 1] - first[lo], s = p.work.pre()[lo];
-    if (kState && seg == nseg - 1) continue;
     const int row0 = p.cu[s], len = p.cu[s + 1] - row0;
     const int t0 = nseg > 1 ? seg * per * p.chunk : 0;
     const int n = nseg > 1 ? min(per * p.chunk, len - t0) : len;
@@ -372,21 +389,24 @@ lin_rec_segments_kernel(LinParams p) {
     float* slot = p.seg_states + ((size_t)item * p.H + h) * D * D;
     const bool zero = kState || (nseg == 1 && !p.has_past[s]);
     float* dst = kState ? slot : seg == nseg - 1 ? block : nullptr;
-    recurrent_body<T, D, false, kState>(p, sm, row0 + t0, n, h, slice, zero, nseg > 1 ? slot : block,
-                                        dst, [] { return true; });
+    if (!(kState && seg == nseg - 1))
+      recurrent_body<T, D, false, kState, true>(p, sm, row0 + t0, n, h, slice, zero,
+                                                nseg > 1 ? slot : block, dst, [] { return true; });
+    unit_sync<true>();
   }
 }
 
 // The states at the segments' starts, from the segments' own: in place,
 // Z[0] <- S0, Z[i] <- e^{g n} Z[i-1] + (the old Z[i-1]) with n tokens per
-// segment.  One float4 of one head's state per thread, the reads of eight
-// segments at a time in flight.
+// segment.  One element of one head's state per thread: a chain of as many
+// steps as there are segments, whose reads are independent, so that many of
+// them are in flight at a time.
 __global__ void __launch_bounds__(256) lin_segments_kernel(LinParams p) {
   pdl_wait_then_release();
   const int32_t* hdr = p.work.header();
   const int n_split = hdr[kLinSplit];
-  constexpr int kAhead = 8;
-  const int words = p.d * p.d / 4, parts = words / 256;
+  constexpr int kAhead = 32;
+  const int words = p.d * p.d, parts = words / 256;
   const int n_units = n_split * p.H * parts;
   for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
     const int part = u % parts, h = (u / parts) % p.H, e = u / (parts * p.H);
@@ -395,13 +415,13 @@ __global__ void __launch_bounds__(256) lin_segments_kernel(LinParams p) {
     const size_t at = (size_t)part * 256 + threadIdx.x;
     const DecayPair a =
         decay_pair(finite_decay(p.log_decay[h]) * (float)(hdr[kLinSegChunks] * p.chunk));
-    float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+    float S = 0.f;
     if (p.has_past[s])
-      S = reinterpret_cast<const float4*>(p.layer_base + (size_t)blk * p.stride)[(size_t)h * words + at];
-    float4* z = reinterpret_cast<float4*>(p.seg_states) + ((size_t)first * p.H + h) * words + at;
+      S = reinterpret_cast<const float*>(p.layer_base + (size_t)blk * p.stride)[(size_t)h * words + at];
+    float* z = p.seg_states + ((size_t)first * p.H + h) * words + at;
     const size_t step = (size_t)p.H * words;
     for (int i0 = 0; i0 < nseg; i0 += kAhead) {
-      float4 own[kAhead];
+      float own[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)  // (the last segment's own state is not there)
         if (i0 + i < nseg - 1) own[i] = z[(i0 + i) * step];
@@ -409,10 +429,7 @@ __global__ void __launch_bounds__(256) lin_segments_kernel(LinParams p) {
       for (int i = 0; i < kAhead; ++i) {
         if (i0 + i >= nseg) break;
         z[(i0 + i) * step] = S;
-        S.x = fmaf(a.hi, S.x, fmaf(a.lo, S.x, own[i].x));
-        S.y = fmaf(a.hi, S.y, fmaf(a.lo, S.y, own[i].y));
-        S.z = fmaf(a.hi, S.z, fmaf(a.lo, S.z, own[i].z));
-        S.w = fmaf(a.hi, S.w, fmaf(a.lo, S.w, own[i].w));
+        S = fmaf(a.hi, S, fmaf(a.lo, S, own[i]));
       }
     }
   }
@@ -423,23 +440,31 @@ constexpr int kSchedThreads = 1024;
 
 constexpr int kSortMax = 2048;     // long sequences that are put in order
 constexpr int kSmemCounts = 4096;  // pools whose block-use counts fit into shared memory
-// The chunked form's segments, in chunks: from kMinSegment up, at most
-// kMaxSegments of them, and of sequences from kMinSplit on.  (Two heads: 1,024
-// tokens 30 us in segments of two chunks and 32 us whole, 768 tokens 30 and 27;
-// 13,311 tokens 51 us in segments of two and 45 us in segments of four.)
-constexpr int kMinSegment = 2, kMaxSegments = 32, kMinSplit = 8;
-// The token-serial form's segments, in tiles of kTile tokens: at least
-// kMinSerial, and the launches they need cost about kSerialCost of them.
-constexpr int kMinSerial = 4, kSerialCost = 6;
-constexpr int kSerialPerSm = 4;    // CTAs that work on an SM side by side
+// What the split of a call into segments is weighed by.  A round of segments of
+// n chunks, one per SM, takes n + 1.5 in each of its two passes (both wait for
+// first loads, and there are two launches more), all in chunks of a chain alone.
+constexpr int kMinSegment = 2;
+__host__ __device__ constexpr long long chunk_cost(long long n, long long rounds, int passes) {
+  return rounds * (passes * n + (passes == 2 ? 3 : 0));
+}
+// The token-serial form's tiles of kTile tokens take the longer the more units
+// share an SM: 1.6 us with one, 2.7, 3.0 and 3.6 with four (bf16, d = 64; fp32
+// with d = 128 2.3 to 5.9), here 4 + 3 units; the second pass and its launches
+// cost about 15 us.
+constexpr int kMinSerial = 4, kSerialLaunch = 64;
+__host__ __device__ constexpr long long serial_cost(long long n, long long per_sm, int passes) {
+  return passes * n * (4 * ((per_sm + kSerialPerSm - 1) / kSerialPerSm) + 3 * per_sm) +
+         (passes == 2 ? kSerialLaunch : 0);
+}
 
 // One CTA.  Checks the batch as the pool's contract demands, lists its
-// sequences and cuts the long ones into segments.
+// sequences and cuts the long ones into segments (slices: the parts of a head's
+// state that the token-serial form works on by themselves; 0: the chunked form).
 __global__ void __launch_bounds__(kSchedThreads)
-lin_schedule_kernel(LinParams p, int short_max, int num_sms, int serial_ctas) {
+lin_schedule_kernel(LinParams p, int short_max, int num_sms, int slices) {
   __shared__ unsigned s_flags;
-  __shared__ int s_dec, s_pre, s_segs;
-  __shared__ unsigned long long s_total;
+  __shared__ int s_dec, s_pre;
+  __shared__ unsigned long long s_best;
   // the long sequences and their chunks, as found and in order
   __shared__ int32_t found[kSortMax], chunks[kSortMax], in_order[kSortMax], counts[kSmemCounts];
   __shared__ int warp_sums[32];
@@ -449,8 +474,8 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms, int serial_ctas) {
   int32_t* uses = nb <= kSmemCounts ? counts : p.work.blk_count();
   if (tid == 0) {
     s_flags = 0u;
-    s_dec = s_pre = s_segs = 0;
-    s_total = 0;
+    s_dec = s_pre = 0;
+    s_best = ~0ull << 31;  // (no segments)
     hdr[kLinStateItems] = hdr[kLinHead] = hdr[kLinItems] = hdr[kLinStateHead] = 0;
     hdr[kLinSplit] = hdr[kLinSegChunks] = hdr[kLinBad] = 0;
   }
@@ -489,7 +514,6 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms, int serial_ctas) {
         found[k] = s;
         chunks[k] = c;
       }
-      atomicAdd(&s_total, (unsigned long long)c);
     }
   }
   __syncthreads();
@@ -517,42 +541,39 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms, int serial_ctas) {
   auto chunks_of = [&](int k) {
     return sorted ? in_order[k] : (p.cu[pre[k] + 1] - p.cu[pre[k]] - 1) / p.chunk + 1;
   };
+  // A chain is worked off in order by one SM (token-serial form: each of its
+  // 32 columns by a group of an SM's threads), so that the call takes at least
+  // the longest one.  Cut into segments, which are computed side by side, it
+  // takes rounds of them over the SMs, each twice: first the segments' own
+  // states, then the outputs from the states at their starts.  Each thread
+  // weighs one length; the best counts if it beats the whole sequences, and of
+  // equals the longest one (fewer states to write and read).  Sequences longer
+  // than half a segment count as whole ones, and shorter ones fill the gaps.
   int per = 0x7fffffff;
-  bool split;
-  if (serial_ctas == 0) {
-    // Chunked form: one SM works a chain off in order, so the call takes at
-    // least the longest chain; its share of all chunks is what it takes at
-    // best.  Where the longest is more than a quarter above that, long
-    // sequences are cut into segments of half a share, which costs a second
-    // read of k and v.
-    const unsigned long long share = (s_total * p.H + num_sms - 1) / num_sms;
-    split = 4ull * chunks_of(0) > 5 * share && chunks_of(0) >= kMinSplit;
-    per = max((int)min((share + 1) / 2, 0x3fffffffull),
-              max(kMinSegment, (chunks_of(0) - 1) / kMaxSegments + 1));
-  } else {
-    // Token-serial form: the same with a head's columns over serial_ctas CTAs
-    // and segments of a share, which go over the tokens twice.
-    const int workers = kSerialPerSm * num_sms;
-    const unsigned long long share = (s_total * p.H * serial_ctas + workers - 1) / workers;
-    per = max((int)min(share, 0x3fffffffull), kMinSerial);
-    split = chunks_of(0) > 2ll * per + kSerialCost;
-  }
-  if (!split || !p.seg_states || !sorted) {
-    per = 0x7fffffff;
-  } else {
-    for (;;) {  // until the segments of split sequences fit into the slots
-      if (tid == 0) s_segs = 0;
-      __syncthreads();
-      int mine = 0;
-      for (int k = tid; k < n_pre; k += kSchedThreads)
-        if (chunks_of(k) > per) mine += (chunks_of(k) + per - 1) / per;
-      if (mine) atomicAdd(&s_segs, mine);
-      __syncthreads();
-      const long long need = (long long)s_segs * p.H;
-      __syncthreads();
-      if (need <= p.seg_slots) break;
-      per = per > 0x3fffffff ? 0x7fffffff : per * 2;
+  if (p.seg_states && sorted) {
+    const int longest = chunks_of(0);
+    auto cost_of = [&](int n, int passes, unsigned* slots) {
+      unsigned items = 0;
+      *slots = 0;
+      for (int k = 0; k < n_pre && in_order[k] > n / 2; ++k) {
+        const unsigned c = in_order[k];
+        items += (c + n / 2) / n;
+        if (c > n) *slots += (c - 1) / n + 1;
+      }
+      const long long per_sm = ((long long)items * p.H * (slices ? slices : 1) + num_sms - 1) / num_sms;
+      return slices ? serial_cost(n, per_sm, passes) : chunk_cost(n, per_sm, passes);
+    };
+    unsigned slots;
+    const int least = slices ? kMinSerial : kMinSegment;
+    const int mine = least + tid * (longest / kSchedThreads + 1);
+    const long long whole = cost_of(longest, 1, &slots);
+    if (mine < longest) {
+      const long long cost = cost_of(mine, 2, &slots);
+      if ((long long)slots * p.H <= p.seg_slots && cost < min(whole, 0xffffffffll))
+        atomicMin(&s_best, (unsigned long long)cost << 32 | (unsigned)(0x7fffffff - mine));
     }
+    __syncthreads();
+    per = 0x7fffffff - (int)(s_best & 0x7fffffffu);
   }
   int carry = 0, n_split = 0;
   for (int k0 = 0; k0 < n_pre; k0 += kSchedThreads) {
@@ -609,13 +630,22 @@ cudaError_t launch_lin_segments(const LinParams& p, int num_sms, cudaStream_t s)
 
 cudaError_t launch_lin_serial_split(const LinParams& p, int act, int num_sms, cudaStream_t s) {
   const bool f32 = act == GDN_F32;
+  const size_t smem = kSerialPerSm * (p.d == 32   ? f32 ? sizeof(RecSmem<float, 32, false>)
+                                                        : sizeof(RecSmem<__nv_bfloat16, 32, false>)
+                                      : p.d == 64 ? f32 ? sizeof(RecSmem<float, 64, false>)
+                                                        : sizeof(RecSmem<__nv_bfloat16, 64, false>)
+                                                  : sizeof(RecSmem<float, 128, false>));
   auto run = [&](auto state, auto out) {
     cudaError_t e = launch_pdl(lin_schedule_kernel, dim3(1), dim3(kSchedThreads), 0, s, p, 0, num_sms,
                                p.d / kSlice);
-    const dim3 grid(5 * num_sms), block(kRecThreads);
-    if (e == cudaSuccess) e = launch_pdl(state, grid, block, 0, s, p);
+    const dim3 grid(num_sms), block(kRecThreads * kSerialPerSm);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(state, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(out, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) e = launch_pdl(state, grid, block, smem, s, p);
     if (e == cudaSuccess) e = launch_lin_segments(p, num_sms, s);
-    if (e == cudaSuccess) e = launch_pdl(out, grid, block, 0, s, p);
+    if (e == cudaSuccess) e = launch_pdl(out, grid, block, smem, s, p);
     return e;
   };
   if (p.d == 32)
@@ -777,22 +807,22 @@ int gdn_lin_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
   p->last_path = chunked                             ? GDN_PREFILL_FUSED
                  : T > 1 && max_seqlen_hint != 1 ? GDN_PREFILL_SERIAL
                                                      : GDN_PREFILL_NONE;
-  // the scheduler's rules for splitting (see there) on what the host knows: no
+  // the scheduler's rule for splitting (see there) on what the host knows: no
   // sequence is longer than T or the hint, and all tokens are some sequence's
   const long long longest = max_seqlen_hint > 0 && max_seqlen_hint < T ? max_seqlen_hint : T;
   lp.seg_slots = p->lin_slots;
   lp.d = d;
   lp.chunk = chunked ? gdn::kLinChunk : gdn::kTile;
-  bool may_split;
-  if (chunked) {
-    const long long chunks = (longest - 1) / gdn::kLinChunk + 1;
-    may_split = chunks >= gdn::kMinSplit && 4 * chunks * sms > 5ll * (T / gdn::kLinChunk) * H;
-    lp.bad = reinterpret_cast<unsigned char*>(p->lin_states) + gdn::kSegBytes;
-  } else {
-    const long long tiles = (longest - 1) / gdn::kTile + 1;
-    const long long share = (long long)(T / gdn::kTile) * H * (d / gdn::kSlice) / (gdn::kSerialPerSm * sms);
-    may_split = T > 1 && tiles > 2 * (share > gdn::kMinSerial ? share : gdn::kMinSerial) + gdn::kSerialCost;
-  }
+  const long long steps = (longest - 1) / lp.chunk + 1;
+  const long long work = (long long)(T / lp.chunk) * H * (chunked ? 1 : d / gdn::kSlice) / sms;
+  // (the least that two passes can cost: all SMs busy all the time)
+  const bool may_split =
+      T > 0 && (chunked ? gdn::chunk_cost(steps, 1, 1) >
+                              gdn::chunk_cost(work > gdn::kMinSegment ? work : gdn::kMinSegment, 1, 2)
+                        : gdn::serial_cost(steps, 1, 1) >
+                              gdn::serial_cost(work > 4 * gdn::kMinSerial ? work / 4 : gdn::kMinSerial,
+                                               work > 4 * gdn::kMinSerial ? 4 : 1, 2));
+  if (chunked) lp.bad = reinterpret_cast<unsigned char*>(p->lin_states) + gdn::kSegBytes;
   if (may_split) lp.seg_states = p->lin_states;
   if (!chunked && may_split) {
     if (p->ev_before && cudaEventRecord(p->ev_before, s) != cudaSuccess) return GDN_ERR_CUDA;
