@@ -61,6 +61,7 @@ struct Vec {
     if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
     else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
   }
+  __device__ __forceinline__ F2 pair(int i) const { return f2(at(i), at(i + 1)); }
 };
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
@@ -109,11 +110,14 @@ __device__ __forceinline__ void recurrent_body(const LinParams& p, RecSmem<T, D,
   const int c0 = slice * kSlice + (tid % kColT) * 4;  // this thread's columns
   const int r0 = (tid / kColT) * kRows;               // and rows
   const size_t at = (size_t)r0 * D + c0;
-  float4 S[kRows];
+  float4 read[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i)
-    S[i] = zero ? make_float4(0.f, 0.f, 0.f, 0.f)
-                : *reinterpret_cast<const float4*>(src + at + (size_t)i * D);
+    read[i] = zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                   : *reinterpret_cast<const float4*>(src + at + (size_t)i * D);
+  // rows in pairs, for packed arithmetic: S[i][c] is rows 2 i and 2 i + 1 of
+  // column c (made of the reads when all others are on their way)
+  F2 S[kRows / 2][4];
   const DecayPair a = decay_pair(finite_decay(p.log_decay[h]));
   const int hk = h / p.group;
   const T* q = static_cast<const T*>(p.q) + (size_t)row0 * p.ldq + (size_t)h * D;
@@ -121,25 +125,45 @@ __device__ __forceinline__ void recurrent_body(const LinParams& p, RecSmem<T, D,
   const T* v = static_cast<const T*>(p.v) + (size_t)row0 * p.ldv + (size_t)hk * D +
                slice * kSlice;
   // one token: S <- e^g S + k v^T, and this thread's part of S^T q
+  const F2 ahi = f2(a.hi, a.hi), alo = f2(a.lo, a.lo);
   auto token = [&](const Vec<T, kRows>& qr, const Vec<T, kRows>& kr, const Vec<T, 4>& vc) {
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    F2 o[4], v2[4];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const float ki = kr.at(i);
-      float4 t = S[i];
-      t.x = fmaf(a.hi, t.x, fmaf(a.lo, t.x, ki * vc.at(0)));
-      t.y = fmaf(a.hi, t.y, fmaf(a.lo, t.y, ki * vc.at(1)));
-      t.z = fmaf(a.hi, t.z, fmaf(a.lo, t.z, ki * vc.at(2)));
-      t.w = fmaf(a.hi, t.w, fmaf(a.lo, t.w, ki * vc.at(3)));
-      S[i] = t;
-      if constexpr (!kState) {
-        o.x = fmaf(qr.at(i), t.x, o.x);
-        o.y = fmaf(qr.at(i), t.y, o.y);
-        o.z = fmaf(qr.at(i), t.z, o.z);
-        o.w = fmaf(qr.at(i), t.w, o.w);
+    for (int c = 0; c < 4; ++c) v2[c] = f2(vc.at(c), vc.at(c));
+#pragma unroll
+    for (int i = 0; i < kRows / 2; ++i) {
+      const F2 k2 = kr.pair(2 * i), q2 = kState ? 0 : qr.pair(2 * i);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        F2 t = mul2(k2, v2[c]);
+        if constexpr (kOne) t = fma2(alo, S[i][c], t);
+        S[i][c] = t = fma2(ahi, S[i][c], t);
+        if constexpr (!kState) o[c] = i == 0 ? mul2(q2, t) : fma2(q2, t, o[c]);
       }
     }
-    return o;
+    float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+    if constexpr (!kState) {
+      float x, y;
+      unf2(o[0], x, y); r.x = x + y;
+      unf2(o[1], x, y); r.y = x + y;
+      unf2(o[2], x, y); r.z = x + y;
+      unf2(o[3], x, y); r.w = x + y;
+    }
+    return r;
+  };
+  // The rest of the decay, a.lo, for n tokens at once, which saves a quarter of
+  // the arithmetic: the newest of them get at most kTile 2^-25 too much of it,
+  // once, while without it the error would grow with every token.
+  auto settle = [&](int n) {
+    if constexpr (!kOne) {
+      if (a.lo == 0.f) return;
+      const float r = a.lo / a.hi * (float)n;
+      const F2 r2 = f2(r, r);
+#pragma unroll
+      for (int i = 0; i < kRows / 2; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) S[i][c] = fma2(r2, S[i][c], S[i][c]);
+    }
   };
   // the sum over the warp's row groups
   auto across = [](float4 o) {
@@ -189,13 +213,29 @@ __device__ __forceinline__ void recurrent_body(const LinParams& p, RecSmem<T, D,
   [[maybe_unused]] T* out =
       static_cast<T*>(p.out) + (size_t)row0 * p.ldo + (size_t)h * D + slice * kSlice;
   if constexpr (!kOne) load_one();
+#pragma unroll
+  for (int i = 0; i < kRows; i += 2) {
+    S[i / 2][0] = f2(read[i].x, read[i + 1].x);
+    S[i / 2][1] = f2(read[i].y, read[i + 1].y);
+    S[i / 2][2] = f2(read[i].z, read[i + 1].z);
+    S[i / 2][3] = f2(read[i].w, read[i + 1].w);
+  }
   auto store = [&]() {
     if (!dst) return;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) *reinterpret_cast<float4*>(dst + at + (size_t)i * D) = S[i];
+    for (int i = 0; i < kRows; i += 2) {
+      float4 x, y;
+      unf2(S[i / 2][0], x.x, y.x);
+      unf2(S[i / 2][1], x.y, y.y);
+      unf2(S[i / 2][2], x.z, y.z);
+      unf2(S[i / 2][3], x.w, y.w);
+      *reinterpret_cast<float4*>(dst + at + (size_t)i * D) = x;
+      *reinterpret_cast<float4*>(dst + at + (size_t)(i + 1) * D) = y;
+    }
   };
   if (active && len == 1) {
     const float4 mine = token(q0, k0, v0);
+    settle(1);
     store();
     if constexpr (!kState) {
       const float4 o = across(mine);
@@ -247,6 +287,7 @@ __device__ __forceinline__ void recurrent_body(const LinParams& p, RecSmem<T, D,
       int t = 0;
       for (; t + kBatch <= n; t += kBatch) batch(t, std::integral_constant<int, kBatch>());
       for (; t < n; ++t) batch(t, std::integral_constant<int, 1>());
+      settle(n);
       unit_sync<kGroups>();  // the tile's sums are there, and its buffer may be staged over
       if constexpr (!kState) {
         for (int i = tid; i < n * kSlice; i += kRecThreads) {
@@ -451,7 +492,7 @@ __host__ __device__ constexpr long long chunk_cost(long long n, long long rounds
 // share an SM: 1.6 us with one, 2.7, 3.0 and 3.6 with four (bf16, d = 64; fp32
 // with d = 128 2.3 to 5.9), here 4 + 3 units; the second pass and its launches
 // cost about 15 us.
-constexpr int kMinSerial = 4, kSerialLaunch = 64;
+constexpr int kMinSerial = 4, kSerialLaunch = 32;
 __host__ __device__ constexpr long long serial_cost(long long n, long long per_sm, int passes) {
   return passes * n * (4 * ((per_sm + kSerialPerSm - 1) / kSerialPerSm) + 3 * per_sm) +
          (passes == 2 ? kSerialLaunch : 0);
@@ -798,8 +839,10 @@ int gdn_lin_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
   cudaStream_t s = (cudaStream_t)stream;
   const int sms = gdn::num_sms();
   // prompts in the chunked form, where it has a kernel and the call room for one
-  const int short_max = (long long)N * H * gdn::kLinSlices <= 5ll * sms ? gdn::kLinShortFew
-                                                                       : gdn::kLinShort;
+  const long long units = (long long)N * H * gdn::kLinSlices;
+  const int short_max = units <= sms       ? gdn::kLinShortLone
+                        : units <= 5ll * sms ? gdn::kLinShortFew
+                                             : gdn::kLinShort;
   int max_long = T / (short_max + 1);
   if (max_long > max_items) max_long = max_items;
   if (max_seqlen_hint > 0 && max_seqlen_hint <= short_max) max_long = 0;

@@ -8,11 +8,11 @@ namespace gdn {
 constexpr int kLinChunk = 128;  // tokens per chunk of the chunked form
 constexpr int kLinSlices = 4;   // parts of 32 columns of a head's state (d = 128)
 // Sequences of up to this many tokens take the recurrent form.  64 sequences of
-// 32 heads: 76 us of 8 tokens (chunked form 101), 119 us of 16 (103).  Where
-// all its CTAs run at once the recurrent form is ahead for longer: one sequence
-// of 16 heads 10 us of 24 tokens (chunked 16), 14 us of 64 (16), and eight of
-// them 17 us of 24 (17), 39 us of 64 (17).
-constexpr int kLinShort = 12, kLinShortFew = 32;
+// 32 heads: 87 us of 12 tokens (chunked form 106), 103 of 16 (104), 124 of 20
+// (107).  Where all its CTAs run at once the recurrent form is ahead for longer:
+// four sequences of 40 heads 25 us of 32 tokens (28), 31 of 40 (28); and longer
+// still with an SM for each: one sequence of 16 heads 17 us of 64 tokens (21).
+constexpr int kLinShort = 16, kLinShortFew = 32, kLinShortLone = 64;
 
 // Header words of a layer's work area in these forwards (besides kErr, kNDec
 // and kNPre): the segments of the long sequences, longest first.
@@ -71,6 +71,28 @@ __device__ __forceinline__ DecayPair decay_pair(float x) {
   }
   return d;
 }
+// Pairs of fp32 in one 64-bit register: packed arithmetic (one instruction per
+// pair).
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unf2(F2 v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // A head's log decay, with -inf (no memory at all) as a finite number, so
 // that zero steps of it are no decay.
 __device__ __forceinline__ float finite_decay(float g) { return g == -INFINITY ? -1e30f : g; }
