@@ -6,12 +6,15 @@
 // with S [d_k][d_v] fp32 per request and head.
 //
 // This file: the recurrent form, the batch scheduler and the C entry points.
-// The recurrent kernel is bound by HBM: a head's state (64 KiB at d = 128) is
-// read once and written once whatever the number of tokens.  A CTA owns 32
-// columns v of one head's state (the columns are independent of each other),
-// every thread 4 columns of d/16 rows in registers; all of a CTA's state
-// loads are issued before anything else, and six CTAs per SM keep about
-// 100 KB of reads in flight.
+// The recurrent kernel is bound by HBM for single tokens: a head's state
+// (64 KiB at d = 128) is read once and written once whatever the number of
+// tokens.  A CTA owns 32 columns v of one head's state (the columns are
+// independent of each other), every thread 4 columns of d/16 rows in registers;
+// all of a CTA's state loads are issued before anything else, and six CTAs per
+// SM keep about 100 KB of reads in flight: 256 requests x 32 heads 160 us,
+// 6.78 TB/s.  With more tokens the arithmetic (4 d^2 multiply-adds per token and
+// head with the decay, in packed fp32) shares the time: 64 requests of 4 tokens
+// x 32 heads 53 us, 0.75 of the copy bandwidth.
 #include <cuda_runtime.h>
 
 #include <new>
@@ -481,20 +484,22 @@ constexpr int kSchedThreads = 1024;
 
 constexpr int kSortMax = 2048;     // long sequences that are put in order
 constexpr int kSmemCounts = 4096;  // pools whose block-use counts fit into shared memory
+constexpr int kLanes = 8;          // threads that weigh a length of segments together
 // What the split of a call into segments is weighed by.  A round of segments of
 // n chunks, one per SM, takes n + 1.5 in each of its two passes (both wait for
 // first loads, and there are two launches more), all in chunks of a chain alone.
 constexpr int kMinSegment = 2;
-__host__ __device__ constexpr long long chunk_cost(long long n, long long rounds, int passes) {
+template <typename U>
+__host__ __device__ constexpr U chunk_cost(U n, U rounds, int passes) {
   return rounds * (passes * n + (passes == 2 ? 3 : 0));
 }
 // The token-serial form's tiles of kTile tokens take the longer the more units
-// share an SM: 1.6 us with one, 2.7, 3.0 and 3.6 with four (bf16, d = 64; fp32
-// with d = 128 2.3 to 5.9), here 4 + 3 units; the second pass and its launches
-// cost about 15 us.
+// share an SM: 1.5 us with one, 2.6 with four (bf16, d = 64), here 3 and one more
+// for each; the second pass and its launches cost about 12 us.
 constexpr int kMinSerial = 4, kSerialLaunch = 32;
-__host__ __device__ constexpr long long serial_cost(long long n, long long per_sm, int passes) {
-  return passes * n * (4 * ((per_sm + kSerialPerSm - 1) / kSerialPerSm) + 3 * per_sm) +
+template <typename U>
+__host__ __device__ constexpr U serial_cost(U n, U per_sm, int passes) {
+  return passes * n * (3 * ((per_sm + kSerialPerSm - 1) / kSerialPerSm) + per_sm) +
          (passes == 2 ? kSerialLaunch : 0);
 }
 
@@ -505,7 +510,7 @@ __global__ void __launch_bounds__(kSchedThreads)
 lin_schedule_kernel(LinParams p, int short_max, int num_sms, int slices) {
   __shared__ unsigned s_flags;
   __shared__ int s_dec, s_pre;
-  __shared__ unsigned long long s_best;
+  __shared__ unsigned long long s_total, s_best;
   // the long sequences and their chunks, as found and in order
   __shared__ int32_t found[kSortMax], chunks[kSortMax], in_order[kSortMax], counts[kSmemCounts];
   __shared__ int warp_sums[32];
@@ -516,6 +521,7 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms, int slices) {
   if (tid == 0) {
     s_flags = 0u;
     s_dec = s_pre = 0;
+    s_total = 0;
     s_best = ~0ull << 31;  // (no segments)
     hdr[kLinStateItems] = hdr[kLinHead] = hdr[kLinItems] = hdr[kLinStateHead] = 0;
     hdr[kLinSplit] = hdr[kLinSegChunks] = hdr[kLinBad] = 0;
@@ -539,6 +545,7 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms, int slices) {
   }
   __syncthreads();
   int32_t *pre = p.work.pre(), *pre_tmp = p.work.pre_tmp(), *first = p.work.pre_cp();
+  unsigned long long total = 0;  // chunks of the long sequences
   for (int s = tid; s < N; s += kSchedThreads) {
     const int b = p.blk[s], len = p.cu[s + 1] - p.cu[s];
     if (b <= 0 || b >= nb || len == 0) continue;
@@ -555,8 +562,12 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms, int slices) {
         found[k] = s;
         chunks[k] = c;
       }
+      total += c;
     }
   }
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) total += __shfl_xor_sync(0xffffffffu, total, w);
+  if ((tid & 31) == 0 && total) atomicAdd(&s_total, total);
   __syncthreads();
   const int n_pre = s_pre;
   if (tid == 0) {
@@ -586,32 +597,42 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms, int slices) {
   // 32 columns by a group of an SM's threads), so that the call takes at least
   // the longest one.  Cut into segments, which are computed side by side, it
   // takes rounds of them over the SMs, each twice: first the segments' own
-  // states, then the outputs from the states at their starts.  Each thread
-  // weighs one length; the best counts if it beats the whole sequences, and of
-  // equals the longest one (fewer states to write and read).  Sequences longer
-  // than half a segment count as whole ones, and shorter ones fill the gaps.
+  // states, then the outputs from the states at their starts.  Lengths
+  // around an SM's share of all chunks are weighed; the best counts if it
+  // beats the whole sequences, and of equals the longest one (fewer states to
+  // write and read).  Sequences longer than half a segment count as whole ones,
+  // and shorter ones fill the gaps.
   int per = 0x7fffffff;
   if (p.seg_states && sorted) {
-    const int longest = chunks_of(0);
-    auto cost_of = [&](int n, int passes, unsigned* slots) {
-      unsigned items = 0;
-      *slots = 0;
-      for (int k = 0; k < n_pre && in_order[k] > n / 2; ++k) {
-        const unsigned c = in_order[k];
-        items += (c + n / 2) / n;
-        if (c > n) *slots += (c - 1) / n + 1;
-      }
-      const long long per_sm = ((long long)items * p.H * (slices ? slices : 1) + num_sms - 1) / num_sms;
+    // (32 bits hold all of this: q, k and v of that much work would not fit)
+    const unsigned chains = p.H * (slices ? slices : 1);
+    const unsigned share = (unsigned)((s_total * chains + num_sms - 1) / num_sms);
+    const unsigned longest = chunks_of(0), least = slices ? kMinSerial : kMinSegment;
+    auto cost = [&](unsigned items, unsigned n, int passes) {
+      const unsigned per_sm = max((items * chains + num_sms - 1) / num_sms, (share - 1) / n + 1);
       return slices ? serial_cost(n, per_sm, passes) : chunk_cost(n, per_sm, passes);
     };
-    unsigned slots;
-    const int least = slices ? kMinSerial : kMinSegment;
-    const int mine = least + tid * (longest / kSchedThreads + 1);
-    const long long whole = cost_of(longest, 1, &slots);
-    if (mine < longest) {
-      const long long cost = cost_of(mine, 2, &slots);
-      if ((long long)slots * p.H <= p.seg_slots && cost < min(whole, 0xffffffffll))
-        atomicMin(&s_best, (unsigned long long)cost << 32 | (unsigned)(0x7fffffff - mine));
+    int count = 0;
+    for (int k = 0; k < n_pre; k += kSchedThreads)
+      count += __syncthreads_count(k + tid < n_pre && in_order[k + tid] > longest / 2);
+    const unsigned whole = cost(count, longest, 1);
+    const unsigned lo = max(least, share / (slices ? 4 * kSerialPerSm : 4));
+    const unsigned hi = min(longest, 2 * share + least);
+    const unsigned n = lo + tid / kLanes * ((hi - min(hi, lo)) / (kSchedThreads / kLanes) + 1);
+    unsigned items = 0, slots = 0;
+    for (int k = tid % kLanes; n < hi && k < n_pre && in_order[k] > n / 2; k += kLanes) {
+      const unsigned c = in_order[k];
+      items += (c + n / 2) / n;
+      if (c > n) slots += (c - 1) / n + 1;
+    }
+#pragma unroll
+    for (int w = 1; w < kLanes; w <<= 1) {
+      items += __shfl_xor_sync(0xffffffffu, items, w);
+      slots += __shfl_xor_sync(0xffffffffu, slots, w);
+    }
+    if (tid % kLanes == 0 && n < hi && slots * p.H <= p.seg_slots) {
+      const unsigned mine = cost(items, n, 2);
+      if (mine < whole) atomicMin(&s_best, (unsigned long long)mine << 32 | (0x7fffffffu - n));
     }
     __syncthreads();
     per = 0x7fffffff - (int)(s_best & 0x7fffffffu);
@@ -857,14 +878,18 @@ int gdn_lin_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
   lp.d = d;
   lp.chunk = chunked ? gdn::kLinChunk : gdn::kTile;
   const long long steps = (longest - 1) / lp.chunk + 1;
-  const long long work = (long long)(T / lp.chunk) * H * (chunked ? 1 : d / gdn::kSlice) / sms;
   // (the least that two passes can cost: all SMs busy all the time)
-  const bool may_split =
-      T > 0 && (chunked ? gdn::chunk_cost(steps, 1, 1) >
-                              gdn::chunk_cost(work > gdn::kMinSegment ? work : gdn::kMinSegment, 1, 2)
-                        : gdn::serial_cost(steps, 1, 1) >
-                              gdn::serial_cost(work > 4 * gdn::kMinSerial ? work / 4 : gdn::kMinSerial,
-                                               work > 4 * gdn::kMinSerial ? 4 : 1, 2));
+  const long long work = (long long)(T / lp.chunk) * H * (chunked ? 1 : d / gdn::kSlice) / sms;
+  long long whole, split;
+  if (chunked) {
+    whole = steps;
+    split = gdn::chunk_cost(work > gdn::kMinSegment ? work : gdn::kMinSegment, 1ll, 2);
+  } else {
+    const long long per_sm = work > gdn::kSerialPerSm * gdn::kMinSerial ? gdn::kSerialPerSm : 1;
+    whole = gdn::serial_cost(steps, 1ll, 1);
+    split = gdn::serial_cost(per_sm > 1 ? work / per_sm : gdn::kMinSerial, per_sm, 2);
+  }
+  const bool may_split = T > 0 && whole > split;
   if (chunked) lp.bad = reinterpret_cast<unsigned char*>(p->lin_states) + gdn::kSegBytes;
   if (may_split) lp.seg_states = p->lin_states;
   if (!chunked && may_split) {

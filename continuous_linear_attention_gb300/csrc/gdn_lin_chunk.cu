@@ -13,7 +13,9 @@
 //
 // Bytes bound it: q, k, v and o are 128 KB per chunk and head (2.9 us of one
 // SM's share of HBM); the products, the state's in four terms, are seven 128^3
-// (2.3 us of one SM's tensor rate at the measured peak).
+// (2.3 us of one SM's tensor rate at the measured peak).  Measured: 4.0 us per
+// chunk with all SMs busy (15,843 tokens x 64 heads in 212 us, 5.1 TB/s; the
+// loads and stores of this pipeline alone take 177), 2.8 us for a chain alone.
 //
 // One CTA per SM, chains claimed from a counter, longest first.  Roles, each
 // a loop over the CTA's chunks that meets the others at mbarriers only:
@@ -48,11 +50,12 @@
 // non-finite q or k reaches only its own row and the later ones, as it should:
 // P's mask selects, it does not multiply.
 //
-// Few long chains: when the longest chain is far above an SM's share, the
-// scheduler cuts long sequences into segments.  A first launch of this kernel
+// Few long chains: where it is cheaper (see the scheduler), long sequences are
+// cut into segments.  A first launch of this kernel
 // (kState) computes every segment's own state from k and v alone, a small
 // kernel turns those into the states at the segments' starts, and the output
-// pass then runs all segments at once; k and v are read twice.
+// pass then runs all segments at once; k and v are read twice (32,768 tokens x 16
+// heads 177 us, of one head 48 us; unsplit 730 us).
 #include <cuda.h>
 
 #include "gdn_lin.cuh"
