@@ -514,7 +514,6 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms, int slices) {
   // the long sequences and their chunks, as found and in order
   __shared__ int32_t found[kSortMax], chunks[kSortMax], in_order[kSortMax], counts[kSmemCounts];
   __shared__ int warp_sums[32];
-  pdl_wait_then_release();
   const int tid = threadIdx.x, N = p.N, nb = p.num_blocks;
   int32_t* hdr = p.work.header();
   int32_t* uses = nb <= kSmemCounts ? counts : p.work.blk_count();
@@ -523,12 +522,28 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms, int slices) {
     s_dec = s_pre = 0;
     s_total = 0;
     s_best = ~0ull << 31;  // (no segments)
+  }
+  if (uses == counts)
+    for (int i = tid; i < nb; i += kSchedThreads) uses[i] = 0;
+  pdl_wait_then_release();
+  // a thread's first sequence is read once
+  int cu0 = 0, cu1 = 0, blk0 = -1;
+  if (tid < N) {
+    cu0 = p.cu[tid];
+    cu1 = p.cu[tid + 1];
+    blk0 = p.blk[tid];
+  }
+  auto length = [&](int q) { return q == tid ? cu1 - cu0 : p.cu[q + 1] - p.cu[q]; };
+  auto block = [&](int q) { return q == tid ? blk0 : p.blk[q]; };
+  if (tid == 0) {
     hdr[kLinStateItems] = hdr[kLinHead] = hdr[kLinItems] = hdr[kLinStateHead] = 0;
     hdr[kLinSplit] = hdr[kLinSegChunks] = hdr[kLinBad] = 0;
   }
-  for (int i = tid; i < nb; i += kSchedThreads) uses[i] = 0;
-  int bad = tid == 0 && (p.cu[0] != 0 || p.cu[N] != p.T);
-  for (int s = tid; s < N; s += kSchedThreads) bad |= p.cu[s + 1] < p.cu[s];
+  if (uses != counts)
+    for (int i = tid; i < nb; i += kSchedThreads) uses[i] = 0;
+  int bad = (tid == 0 && cu0 != 0) || (tid == (N - 1) % kSchedThreads && p.cu[N] != p.T);
+  for (int q = tid; q < N; q += kSchedThreads)  // (a difference could wrap)
+    bad |= q == tid ? cu1 < cu0 : p.cu[q + 1] < p.cu[q];
   if (__syncthreads_or(bad)) {
     if (tid == 0) {
       atomicOr((unsigned*)&hdr[kErr], GDN_FLAG_SEQLENS);
@@ -537,8 +552,8 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms, int slices) {
     return;
   }
   for (int s = tid; s < N; s += kSchedThreads) {
-    const int b = p.blk[s];
-    if (b < 0 || p.cu[s + 1] == p.cu[s]) continue;  // padding or empty
+    const int b = block(s);
+    if (b < 0 || length(s) == 0) continue;  // padding or empty
     if (b >= nb) atomicOr(&s_flags, GDN_FLAG_BLOCK_RANGE);
     else if (b == 0) atomicOr(&s_flags, GDN_FLAG_TRASH_WRITE);
     else atomicAdd(&uses[b], 1);
@@ -547,7 +562,7 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms, int slices) {
   int32_t *pre = p.work.pre(), *pre_tmp = p.work.pre_tmp(), *first = p.work.pre_cp();
   unsigned long long total = 0;  // chunks of the long sequences
   for (int s = tid; s < N; s += kSchedThreads) {
-    const int b = p.blk[s], len = p.cu[s + 1] - p.cu[s];
+    const int b = block(s), len = length(s);
     if (b <= 0 || b >= nb || len == 0) continue;
     if (atomicAdd(&uses[b], 0) > 1) {
       atomicOr(&s_flags, GDN_FLAG_DUPLICATE);

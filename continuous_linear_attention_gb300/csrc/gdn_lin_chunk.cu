@@ -242,17 +242,10 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
   static_assert(kStages * ST_BYTES == OFF_S && kStages <= kMaxStages, "stages fill their room");
   extern __shared__ __align__(1024) unsigned char sm[];
   Ctl& ctl = *reinterpret_cast<Ctl*>(sm + OFF_CTL);
-  pdl_wait_then_release();
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   int32_t* hdr = p.work.header();
-  const int n_units = (kState ? hdr[kLinStateItems] : hdr[kLinItems]) * p.H;
-  if ((int)blockIdx.x >= n_units) return;
   const uint32_t sbase = smem_u32(sm);
-  if ((sbase & 1023u) != 0) {  // the operand tiles' swizzle counts on it
-    if (tid == 0) atomicOr((unsigned*)&hdr[kErr], GDN_FLAG_TIMEOUT);
-    return;
-  }
   if (tid == 0) {
     for (int b = 0; b < kStages; ++b) {
       mbar_init(&ctl.full[b], 1);
@@ -284,6 +277,15 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = ctl.tmem;
+  // (up to here beside the kernel before this one)
+  pdl_wait_then_release();
+  const int n_units = (kState ? hdr[kLinStateItems] : hdr[kLinItems]) * p.H;
+  const bool aligned = (sbase & 1023u) == 0;  // the operand tiles' swizzle counts on it
+  if (!aligned && tid == 0) atomicOr((unsigned*)&hdr[kErr], GDN_FLAG_TIMEOUT);
+  if ((int)blockIdx.x >= n_units || !aligned) {
+    if (warp == 0) tc::tmem_dealloc(tmem, TM_COLS);
+    return;
+  }
   bool dead = false;
   // buffers of U and of the decayed v: their number (a power of two, by its
   // logarithm) and tensor memory columns

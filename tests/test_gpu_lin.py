@@ -433,3 +433,18 @@ def test_has_past_is_any_value_but_zero():
     run.run()
     torch.cuda.synchronize()
     check(run, tensor_cores=True)
+
+
+@pytest.mark.parametrize("act,d", [("f32", 64), ("bf16", 128)])
+@pytest.mark.parametrize("n", [3, 700])
+def test_bad_cu_seqlens_whose_differences_wrap(act, d, n):
+    """No difference of these is negative in 32 bits."""
+    lens = [300, 300, 300] + [0] * (n - 3)
+    run = LinRun(lens, [1] * n, 1, 1, d, act, num_blocks=n + 1)
+    before = run.mem.clone()
+    run.cu = [0, 2_000_000_000, -2_000_000_000] + [run.T] * (n - 2)
+    run.cu_d.copy_(torch.tensor(run.cu, dtype=torch.int32))
+    run.run()
+    torch.cuda.synchronize()
+    check(run)
+    assert torch.equal(run.mem, before)
