@@ -18,7 +18,7 @@
 // into (part of the components, column).
 //
 // Measured: a reorder of 256 blocks of 2.1 MB in 3 layers 335 us, 0.94 of the
-// copy bandwidth; 400 blocks of 19 KiB in 8 layers 35 us, of which the plan takes
+// copy bandwidth; 400 blocks of 19 KiB in 8 layers 32 us, of which the plan takes
 // 11; clearing 37 blocks in 6 layers 86 us, 5.5 TB/s of writes.
 //
 // Traffic: every distinct source is read once, however many destinations it
@@ -396,14 +396,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1) move_blocks_kernel(MoveParams 
   unsigned char(*buf)[kPiece] = sm.buf[warp];
   uint64_t* full = sm.full[warp];
 
-  // The units: columns as wide as leaves four per warp, by as many parts of
-  // the components as make eight.
+  // The units: columns, narrowed while half of the warps would have nothing to
+  // do (six requests' beams of 143 KB blocks, 4 layers: 23 us, 39 with four
+  // units per warp wherever possible), by parts of the components: eight units
+  // per warp, but eight pieces in each where that leaves two (100 requests'
+  // beams of 19 KiB, 8 layers: 37 us, 41 with eight units each; at 64 requests'
+  // of 2.1 MB two per warp take 355 us and eight 339).
   const long long warps = (long long)gridDim.x * kWarps;
   int piece = kPiece;
   auto cols_of = [&](int b) { return (long long)((p.stride + b - 1) / b); };
-  while (piece > kMinPiece && p.layers * cols_of(piece) * comps < 4 * warps) piece /= 2;
+  while (piece > kMinPiece && p.layers * cols_of(piece) * comps < warps / 2) piece /= 2;
   const long long cols = cols_of(piece), ncol = p.layers * cols;
-  const long long want = (8 * warps + ncol - 1) / ncol;
+  const long long units = min(max(ncol * ops / 8, 2 * warps), 8 * warps);
+  const long long want = (units + ncol - 1) / ncol;
   const int parts = (int)(want < comps ? want : comps);
   // first move of part i: that of the first component at or behind its share
   auto part_begin = [&](int i) {
