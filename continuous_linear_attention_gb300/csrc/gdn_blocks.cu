@@ -12,8 +12,8 @@
 // is written.  With W[x] the source of the entry that writes x, source x must
 // come before source W[x], whose move overwrites x: a graph with one successor
 // per node, i.e. trees whose roots are last moves or cycles.  The planning
-// kernel orders the trees by their distance to the root (pointer jumping) and
-// walks each cycle; a cycle's last source is first read into a spare buffer.
+// kernel orders the trees by their distance to the root (walked where it is
+// short, else by pointer jumping: 2 us more) and walks each cycle; a cycle's last source is first read into a spare buffer.
 // Components of that graph are independent of each other, so the work is cut
 // into (part of the components, column).
 //
@@ -38,12 +38,13 @@ constexpr int kPlanThreads = 1024;
 constexpr int kSmemBlocks = 8192;
 constexpr int kPlanArrays = 6;
 constexpr int kMaxLevels = 64;  // deeper trees are not divided into components
+constexpr int kWalk = 16;       // steps to a root that are walked
 // kinds of a move, in bits 30-31 of its source
 enum Kind : uint32_t { kCopy = 0, kHold = 1, kStoreHeld = 2 };
 constexpr uint32_t kBlockMask = (1u << 30) - 1;
 
 // Orders the moves of a copy list (see above) into bw.
-__global__ void __launch_bounds__(kPlanThreads)
+__global__ void __launch_bounds__(kPlanThreads, 1)
 plan_copies_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n, int nb,
                    BlockWork bw, uint32_t* err) {
   extern __shared__ int32_t plan_smem[];
@@ -126,58 +127,101 @@ plan_copies_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ 
       if (cnt[x] > 0) emit(atomicAdd(&s_ops, 1), x, kCopy);
     single = 1;
   } else {
-    int rounds = 1;
-    while ((1 << rounds) < nb) ++rounds;
-    // cycles: 2^rounds >= nb steps from a source that reaches one end on it,
-    // and every source of a cycle is such an end
-    for (int x = tid; x < nb; x += kPlanThreads) P[x] = cnt[x] > 0 ? W[x] : -1;
-    __syncthreads();
-    bool cycles = true;
-    for (int r = 0; r < rounds && cycles; ++r) {
-      int more = 0;
-      for (int x = tid; x < nb; x += kPlanThreads) {
-        const int y = P[x] < 0 ? -1 : P[P[x]];
-        Q[x] = y;
-        more |= y >= 0;
-      }
-      cycles = __syncthreads_or(more) != 0;
-      int32_t* t = P;
-      P = Q;
-      Q = t;
-    }
-    for (int x = tid; x < nb; x += kPlanThreads) Q[x] = 0;
-    __syncthreads();
-    if (cycles)
-      for (int x = tid; x < nb; x += kPlanThreads)
-        if (P[x] >= 0) Q[P[x]] = 1;
-    __syncthreads();
-    // every other source's root (a last source, or one on a cycle) and its
-    // distance to it
+    // Every source's root (a last source, or one on a cycle) and its distance to
+    // it: by walking up to kWalk steps, first to an end or back to the start,
+    // then to a cycle ...
     int32_t* cyc = Q;
     int32_t* nxt = P;
+    int far = 0, on_cycle = 0;
     for (int x = tid; x < nb; x += kPlanThreads) {
-      const bool tree = cnt[x] > 0 && W[x] >= 0 && !cyc[x];
-      nxt[x] = tree ? W[x] : x;
-      DP[x] = tree ? 1 : 0;
-    }
-    __syncthreads();
-    for (int r = 0; r < rounds; ++r) {
-      for (int x = tid; x < nb; x += kPlanThreads) DQ[x] = DP[x] + DP[nxt[x]];
-      __syncthreads();
-      int32_t* t = DP;
-      DP = DQ;
-      DQ = t;
-      // the old distances' array takes the jumped pointers
-      int more = 0;
-      for (int x = tid; x < nb; x += kPlanThreads) {
-        const int y = nxt[nxt[x]];
-        more |= y != nxt[x];
-        DQ[x] = y;
+      int y = x, next = cnt[x] > 0 ? W[x] : -1, steps = 0;
+      while (next >= 0 && next != x && steps < kWalk) {
+        y = next;
+        next = W[y];
+        ++steps;
       }
-      t = nxt;
-      nxt = DQ;
-      DQ = t;
-      if (!__syncthreads_or(more)) break;
+      cyc[x] = next == x;
+      DP[x] = next < 0 ? steps : 0;
+      nxt[x] = next < 0 ? y : next == x ? x : -1;
+      on_cycle |= next == x;
+      far |= nxt[x] < 0;
+    }
+    bool cycles = __syncthreads_or(on_cycle) != 0;
+    if (__syncthreads_or(far)) {
+      far = 0;
+      for (int x = tid; x < nb; x += kPlanThreads) {
+        if (nxt[x] >= 0) continue;
+        int y = x, steps = 0;
+        while (!cyc[y] && steps < kWalk && W[y] >= 0) {
+          y = W[y];
+          ++steps;
+        }
+        if (cyc[y]) {
+          DP[x] = steps;
+          nxt[x] = y;
+        } else {
+          far = 1;
+        }
+      }
+      far = __syncthreads_or(far);
+    } else {
+      far = 0;
+    }
+    if (far) {
+      // ... and, where that does not get everywhere, by pointer jumping.
+      int rounds = 1;
+      while ((1 << rounds) < nb) ++rounds;
+      // cycles: 2^rounds >= nb steps from a source that reaches one end on it,
+      // and every source of a cycle is such an end
+      for (int x = tid; x < nb; x += kPlanThreads) P[x] = cnt[x] > 0 ? W[x] : -1;
+      __syncthreads();
+      cycles = true;
+      for (int r = 0; r < rounds && cycles; ++r) {
+        int more = 0;
+        for (int x = tid; x < nb; x += kPlanThreads) {
+          const int y = P[x] < 0 ? -1 : P[P[x]];
+          Q[x] = y;
+          more |= y >= 0;
+        }
+        cycles = __syncthreads_or(more) != 0;
+        int32_t* t = P;
+        P = Q;
+        Q = t;
+      }
+      for (int x = tid; x < nb; x += kPlanThreads) Q[x] = 0;
+      __syncthreads();
+      if (cycles)
+        for (int x = tid; x < nb; x += kPlanThreads)
+          if (P[x] >= 0) Q[P[x]] = 1;
+      __syncthreads();
+      // every other source's root (a last source, or one on a cycle) and its
+      // distance to it
+      cyc = Q;
+      nxt = P;
+      for (int x = tid; x < nb; x += kPlanThreads) {
+        const bool tree = cnt[x] > 0 && W[x] >= 0 && !cyc[x];
+        nxt[x] = tree ? W[x] : x;
+        DP[x] = tree ? 1 : 0;
+      }
+      __syncthreads();
+      for (int r = 0; r < rounds; ++r) {
+        for (int x = tid; x < nb; x += kPlanThreads) DQ[x] = DP[x] + DP[nxt[x]];
+        __syncthreads();
+        int32_t* t = DP;
+        DP = DQ;
+        DQ = t;
+        // the old distances' array takes the jumped pointers
+        int more = 0;
+        for (int x = tid; x < nb; x += kPlanThreads) {
+          const int y = nxt[nxt[x]];
+          more |= y != nxt[x];
+          DQ[x] = y;
+        }
+        t = nxt;
+        nxt = DQ;
+        DQ = t;
+        if (!__syncthreads_or(more)) break;
+      }
     }
     for (int x = tid; x < nb; x += kPlanThreads)
       if (cnt[x] > 0) atomicMax(&s_depth, DP[x]);
@@ -281,7 +325,7 @@ plan_copies_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ 
 
 // Plans a compaction: with m live blocks, the i-th live block above m moves to
 // the i-th free block of 1..m, both ascending.  The two lists are disjoint.
-__global__ void __launch_bounds__(kPlanThreads)
+__global__ void __launch_bounds__(kPlanThreads, 1)
 plan_compact_kernel(const int32_t* idx, int32_t* new_idx, int n, int nb, BlockWork bw,
                     uint32_t* err) {
   extern __shared__ int32_t plan_smem[];

@@ -295,3 +295,30 @@ def test_operations_one_after_the_other_without_a_host_wait():
         where[dst] = where[src]
     torch.cuda.synchronize()
     b.check({x: int(where[x]) for x in range(64)}, 0)
+
+
+@pytest.mark.parametrize("n", [15, 16, 17, 18, 33])
+@pytest.mark.parametrize("shape", ["chain", "cycle", "tail_into_cycle", "tail_into_long_cycle", "tails"])
+def test_walks_around_the_length_that_is_walked(n, shape):
+    """Chains, cycles and tails of blocks about as long as the plan follows
+    them step by step, among short ones."""
+    order = np.random.default_rng(n).permutation(np.arange(1, 120)).tolist()
+    pairs = [(order[0], order[1]), (order[2], order[3]), (order[3], order[2])]
+    line = order[4:4 + n]
+    # (source, destination): the last of the line is the one that is read first
+    pairs += list(zip(line[1:], line))
+    ring = {"cycle": line, "tail_into_cycle": order[60:62], "tail_into_long_cycle": order[60:60 + n]}.get(shape)
+    if shape == "cycle":
+        pairs.append((line[0], line[-1]))
+    elif ring:
+        pairs += list(zip(ring[1:], ring)) + [(ring[0], ring[-1]), (ring[0], line[-1])]
+    elif shape == "tails":
+        other = order[60:60 + n]
+        pairs += list(zip(other[1:], other)) + [(line[0], other[-1])]
+    src, dst = zip(*pairs)
+    b = Blocks("lin", 130, seed=n)
+    b.pool.copy_blocks(idx(src), idx(dst))
+    want, flags = expect(130, src, dst)
+    torch.cuda.synchronize()
+    b.check(want, flags)
+    assert flags == 0
