@@ -13,13 +13,14 @@
 // come before source W[x], whose move overwrites x: a graph with one successor
 // per node, i.e. trees whose roots are last moves or cycles.  The planning
 // kernel orders the trees by their distance to the root (walked where it is
-// short, else by pointer jumping: 2 us more) and walks each cycle; a cycle's last source is first read into a spare buffer.
-// Components of that graph are independent of each other, so the work is cut
-// into (part of the components, column).
+// short, else by pointer jumping: 2 us more) and walks each cycle; a cycle's
+// last source is first read into a spare buffer.  Components of that graph are
+// independent of each other, so the work is cut into (part of the components,
+// column).
 //
-// Measured: a reorder of 256 blocks of 2.1 MB in 3 layers 335 us, 0.94 of the
-// copy bandwidth; 400 blocks of 19 KiB in 8 layers 32 us, of which the plan takes
-// 11; clearing 37 blocks in 6 layers 86 us, 5.5 TB/s of writes.
+// Measured: a reorder of 256 blocks of 2.1 MB in 3 layers 333 us, 0.94 of the
+// copy bandwidth; 400 blocks of 19 KiB in 8 layers 30 us, of which the plan takes
+// 9; clearing 37 blocks in 6 layers 86 us, 5.5 TB/s of writes.
 //
 // Traffic: every distinct source is read once, however many destinations it
 // has, and every destination written once, the least the call can do.  The

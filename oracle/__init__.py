@@ -26,6 +26,7 @@ Contents:
     -- independent restatements of the recurrences used only to pin the token
     loops (numpy); ``ssd_quadratic_form`` / ``ssd_chunked_forward`` the same
     for the scan.
+``oracle.lin`` has decayed linear attention and the pool's block operations.
 
 Every function cites the passage it follows; the readings taken where the
 sources are silent are listed in the module docstring of gdn_oracle.c.
