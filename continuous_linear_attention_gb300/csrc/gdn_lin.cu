@@ -127,9 +127,16 @@ __device__ __forceinline__ void recurrent_body(const LinParams& p, RecSmem<T, D,
   const T* k = static_cast<const T*>(p.k) + (size_t)row0 * p.ldk + (size_t)hk * D;
   const T* v = static_cast<const T*>(p.v) + (size_t)row0 * p.ldv + (size_t)hk * D +
                slice * kSlice;
-  // one token: S <- e^g S + k v^T, and this thread's part of S^T q
-  const F2 ahi = f2(a.hi, a.hi), alo = f2(a.lo, a.lo);
-  auto token = [&](const Vec<T, kRows>& qr, const Vec<T, kRows>& kr, const Vec<T, 4>& vc) {
+  // One token: S <- e^g S + k v^T, and this thread's part of S^T q.  The rest of
+  // the decay, a.lo, is added for a whole tile at its first token (rest: that
+  // many times a.lo), which saves a quarter of the arithmetic: the tile's own
+  // tokens go without it until the next one (at most 15 times 2^-25, once), and
+  // it is part of a sum that is rounded once, where a product with 1 + a.lo would
+  // round it away.
+  const F2 ahi = f2(a.hi, a.hi);
+  auto rest_of = [&](int n) { return f2(a.lo * (float)n, a.lo * (float)n); };
+  auto token = [&](const Vec<T, kRows>& qr, const Vec<T, kRows>& kr, const Vec<T, 4>& vc,
+                   auto with_rest, F2 rest) {
     F2 o[4], v2[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) v2[c] = f2(vc.at(c), vc.at(c));
@@ -139,7 +146,7 @@ __device__ __forceinline__ void recurrent_body(const LinParams& p, RecSmem<T, D,
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         F2 t = mul2(k2, v2[c]);
-        if constexpr (kOne) t = fma2(alo, S[i][c], t);
+        if constexpr (decltype(with_rest)::value) t = fma2(rest, S[i][c], t);
         S[i][c] = t = fma2(ahi, S[i][c], t);
         if constexpr (!kState) o[c] = i == 0 ? mul2(q2, t) : fma2(q2, t, o[c]);
       }
@@ -153,20 +160,6 @@ __device__ __forceinline__ void recurrent_body(const LinParams& p, RecSmem<T, D,
       unf2(o[3], x, y); r.w = x + y;
     }
     return r;
-  };
-  // The rest of the decay, a.lo, for n tokens at once, which saves a quarter of
-  // the arithmetic: the newest of them get at most kTile 2^-25 too much of it,
-  // once, while without it the error would grow with every token.
-  auto settle = [&](int n) {
-    if constexpr (!kOne) {
-      if (a.lo == 0.f) return;
-      const float r = a.lo / a.hi * (float)n;
-      const F2 r2 = f2(r, r);
-#pragma unroll
-      for (int i = 0; i < kRows / 2; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) S[i][c] = fma2(r2, S[i][c], S[i][c]);
-    }
   };
   // the sum over the warp's row groups
   auto across = [](float4 o) {
@@ -237,8 +230,7 @@ __device__ __forceinline__ void recurrent_body(const LinParams& p, RecSmem<T, D,
     }
   };
   if (active && len == 1) {
-    const float4 mine = token(q0, k0, v0);
-    settle(1);
+    const float4 mine = token(q0, k0, v0, std::true_type(), rest_of(1));
     store();
     if constexpr (!kState) {
       const float4 o = across(mine);
@@ -264,7 +256,8 @@ __device__ __forceinline__ void recurrent_body(const LinParams& p, RecSmem<T, D,
       unit_sync<kGroups>();  // the tile has landed, and the last one's sums are read
       const int n = min(kTile, len - t0);
       // kN tokens: their reads come first and their sums run side by side
-      auto batch = [&](int t, auto count) {
+      const F2 rest = rest_of(n);
+      auto batch = [&](int t, auto count, auto first) {
         constexpr int kN = decltype(count)::value;
         Vec<T, kRows> qr[kN], kr[kN];
         Vec<T, 4> vc[kN];
@@ -276,7 +269,10 @@ __device__ __forceinline__ void recurrent_body(const LinParams& p, RecSmem<T, D,
         }
         float4 o[kN];
 #pragma unroll
-        for (int u = 0; u < kN; ++u) o[u] = token(qr[u], kr[u], vc[u]);
+        for (int u = 0; u < kN; ++u) {
+          if (u == 0) o[u] = token(qr[u], kr[u], vc[u], first, rest);
+          else o[u] = token(qr[u], kr[u], vc[u], std::false_type(), rest);
+        }
         if constexpr (!kState) {
 #pragma unroll
           for (int u = 0; u < kN; ++u) o[u] = across(o[u]);
@@ -287,10 +283,16 @@ __device__ __forceinline__ void recurrent_body(const LinParams& p, RecSmem<T, D,
           }
         }
       };
-      int t = 0;
-      for (; t + kBatch <= n; t += kBatch) batch(t, std::integral_constant<int, kBatch>());
-      for (; t < n; ++t) batch(t, std::integral_constant<int, 1>());
-      settle(n);
+      int t = 1;
+      if (n >= kBatch) {
+        batch(0, std::integral_constant<int, kBatch>(), std::true_type());
+        t = kBatch;
+      } else {
+        batch(0, std::integral_constant<int, 1>(), std::true_type());
+      }
+      for (; t + kBatch <= n; t += kBatch)
+        batch(t, std::integral_constant<int, kBatch>(), std::false_type());
+      for (; t < n; ++t) batch(t, std::integral_constant<int, 1>(), std::false_type());
       unit_sync<kGroups>();  // the tile's sums are there, and its buffer may be staged over
       if constexpr (!kState) {
         for (int i = tid; i < n * kSlice; i += kRecThreads) {

@@ -448,3 +448,17 @@ def test_bad_cu_seqlens_whose_differences_wrap(act, d, n):
     torch.cuda.synchronize()
     check(run)
     assert torch.equal(run.mem, before)
+
+
+@pytest.mark.parametrize("hint", [0, 1])
+def test_slow_decay_keeps_the_state_over_many_single_tokens(hint):
+    """One token per call, in the kernel for single tokens and in the one for
+    any length."""
+    run = LinRun([1200], [1], 2, 1, 64, "f32", log_decay=[-1e-4, -1e-6])
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    for t in range(run.T):
+        binding.lin_varlen_forward(run.pool, 0, run.q[t:], run.k[t:], run.v[t:], cu, run.blk_d, run.past_d,
+                                   run.decay_d, run.out[t:], 1, 1, scale=run.scale, max_seqlen_hint=hint)
+    torch.cuda.synchronize()
+    errs = check(run)
+    assert errs["state"] <= fp32_walk(1200) and errs["out"] <= fp32_walk(1200), errs
