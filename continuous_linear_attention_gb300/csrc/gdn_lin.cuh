@@ -8,11 +8,11 @@ namespace gdn {
 constexpr int kLinChunk = 128;  // tokens per chunk of the chunked form
 constexpr int kLinSlices = 4;   // parts of 32 columns of a head's state (d = 128)
 // Sequences of up to this many tokens take the recurrent form.  64 sequences of
-// 32 heads: 87 us of 12 tokens (chunked form 106), 103 of 16 (104), 124 of 20
-// (107).  Where all its CTAs run at once the recurrent form is ahead for longer:
-// four sequences of 40 heads 25 us of 32 tokens (28), 31 of 40 (28); and longer
-// still with an SM for each: one sequence of 16 heads 17 us of 64 tokens (21).
-constexpr int kLinShort = 16, kLinShortFew = 32, kLinShortLone = 64;
+// 32 heads: 95 us of 16 tokens (chunked form 105), 103 of 18 (104), 115 of 20
+// (106).  Where all its CTAs run at once the recurrent form is ahead for longer:
+// four sequences of 40 heads 25 us of 32 tokens (28), 29 of 40 (28); and longer
+// still with an SM for each: one sequence of 16 heads 17 us of 64 tokens (20).
+constexpr int kLinShort = 18, kLinShortFew = 32, kLinShortLone = 64;
 
 // Header words of a layer's work area in these forwards (besides kErr, kNDec
 // and kNPre): the segments of the long sequences, longest first.
