@@ -52,28 +52,39 @@ plan_copies_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ 
   __shared__ unsigned s_flags;
   __shared__ int s_ops, s_dsts, s_comps, s_depth;
   __shared__ int warp_sums[32];
-  pdl_wait_then_release();
   const int tid = threadIdx.x;
-  int32_t* a = nb <= kSmemBlocks ? plan_smem : bw.tmp();
+  const bool in_smem = nb <= kSmemBlocks;
+  int32_t* a = in_smem ? plan_smem : bw.tmp();
   int32_t* W = a;             // source of the entry that writes a block, or -1
   int32_t* cnt = a + nb;      // destinations of a source
   int32_t* P = a + 2 * (size_t)nb;
   int32_t* Q = a + 3 * (size_t)nb;
   int32_t* DP = a + 4 * (size_t)nb;
   int32_t* DQ = a + 5 * (size_t)nb;
+  auto init = [&]() {
+    for (int x = tid; x < nb; x += kPlanThreads) {
+      W[x] = -1;
+      cnt[x] = 0;
+      P[x] = 0;
+    }
+  };
   if (tid == 0) {
     s_flags = 0u;
     s_ops = s_dsts = s_comps = s_depth = 0;
   }
-  for (int x = tid; x < nb; x += kPlanThreads) {
-    W[x] = -1;
-    cnt[x] = 0;
-    P[x] = 0;
+  if (in_smem) init();
+  pdl_wait_then_release();
+  if (!in_smem) init();
+  // a thread's first entry is read once
+  int src0 = -1, dst0 = -1;
+  if (tid < n) {
+    src0 = src[tid];
+    dst0 = dst[tid];
   }
   __syncthreads();
   // how many entries name each destination
   for (int e = tid; e < n; e += kPlanThreads) {
-    const int s = src[e], d = dst[e];
+    const int s = e == tid ? src0 : src[e], d = e == tid ? dst0 : dst[e];
     if (s < 0 || d < 0) continue;  // padding
     if (s >= nb || d >= nb)
       atomicOr(&s_flags, GDN_FLAG_BLOCK_RANGE);
@@ -84,7 +95,7 @@ plan_copies_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ 
   }
   __syncthreads();
   for (int e = tid; e < n; e += kPlanThreads) {
-    const int s = src[e], d = dst[e];
+    const int s = e == tid ? src0 : src[e], d = e == tid ? dst0 : dst[e];
     if (s < 0 || d <= 0 || s >= nb || d >= nb) continue;
     if (P[d] > 1) {
       atomicOr(&s_flags, GDN_FLAG_DUPLICATE);
@@ -311,7 +322,7 @@ plan_copies_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ 
   __syncthreads();
   int32_t* odst = bw.dst();
   for (int e = tid; e < n; e += kPlanThreads) {
-    const int s = src[e], d = dst[e];
+    const int s = e == tid ? src0 : src[e], d = e == tid ? dst0 : dst[e];
     if (s < 0 || d <= 0 || s >= nb || d >= nb || s == d || W[d] != s) continue;
     odst[atomicAdd(&cnt[s], 1)] = d;
   }
@@ -332,12 +343,16 @@ plan_compact_kernel(const int32_t* idx, int32_t* new_idx, int n, int nb, BlockWo
   extern __shared__ int32_t plan_smem[];
   __shared__ unsigned s_flags;
   __shared__ int warp_sums[32];
-  pdl_wait_then_release();
   const int tid = threadIdx.x;
-  int32_t* live = nb <= kSmemBlocks ? plan_smem : bw.tmp();
+  const bool in_smem = nb <= kSmemBlocks;
+  int32_t* live = in_smem ? plan_smem : bw.tmp();
   int32_t* to = live + nb;
   if (tid == 0) s_flags = 0u;
-  for (int x = tid; x < nb; x += kPlanThreads) live[x] = 0;
+  if (in_smem)
+    for (int x = tid; x < nb; x += kPlanThreads) live[x] = 0;
+  pdl_wait_then_release();
+  if (!in_smem)
+    for (int x = tid; x < nb; x += kPlanThreads) live[x] = 0;
   __syncthreads();
   for (int e = tid; e < n; e += kPlanThreads) {
     const int b = idx[e];
@@ -415,8 +430,12 @@ struct MoveParams {
 __global__ void __launch_bounds__(kWarps * 32, 1) move_blocks_kernel(MoveParams p) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
   MoveSmem& sm = *reinterpret_cast<MoveSmem*>(smem_raw);
-  pdl_wait_then_release();
   const int tid = threadIdx.x, warp = tid >> 5;
+  if ((tid & 31) == 0) {
+    for (int i = 0; i <= kSlots; ++i) mbar_init(&sm.full[warp][i], 1);
+    fence_mbar_init();
+  }
+  pdl_wait_then_release();
   int32_t* hdr = p.bw.header();
   const int ops = hdr[0], comps = hdr[1];
   const bool single = hdr[3] != 0;
@@ -428,10 +447,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) move_blocks_kernel(MoveParams 
       sm.cnt[i] = p.bw.cnt()[i];
     }
     if (i < p.nb) sm.dst[i] = p.bw.dst()[i];
-  }
-  if ((tid & 31) == 0) {
-    for (int i = 0; i <= kSlots; ++i) mbar_init(&sm.full[warp][i], 1);
-    fence_mbar_init();
   }
   __syncthreads();
   if ((tid & 31) != 0) return;
