@@ -18,8 +18,8 @@
 // independent of each other, so the work is cut into (part of the components,
 // column).
 //
-// Measured: a reorder of 256 blocks of 2.1 MB in 3 layers 333 us, 0.94 of the
-// copy bandwidth; 400 blocks of 19 KiB in 8 layers 30 us, of which the plan takes
+// Measured: a reorder of 256 blocks of 2.1 MB in 3 layers 331 us, 0.95 of the
+// copy bandwidth; 400 blocks of 19 KiB in 8 layers 29 us, of which the plan takes
 // 9; clearing 37 blocks in 6 layers 86 us, 5.5 TB/s of writes.
 //
 // Traffic: every distinct source is read once, however many destinations it

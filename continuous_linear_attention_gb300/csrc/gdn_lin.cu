@@ -515,7 +515,8 @@ __global__ void __launch_bounds__(kSchedThreads)
 lin_schedule_kernel(LinParams p, int short_max, int num_sms, int slices) {
   __shared__ unsigned s_flags;
   __shared__ int s_dec, s_pre;
-  __shared__ unsigned long long s_total, s_best;
+  __shared__ unsigned s_total;
+  __shared__ unsigned long long s_best;
   // the long sequences and their chunks, as found and in order
   __shared__ int32_t found[kSortMax], chunks[kSortMax], in_order[kSortMax], counts[kSmemCounts];
   __shared__ int warp_sums[32];
@@ -565,7 +566,7 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms, int slices) {
   }
   __syncthreads();
   int32_t *pre = p.work.pre(), *pre_tmp = p.work.pre_tmp(), *first = p.work.pre_cp();
-  unsigned long long total = 0;  // chunks of the long sequences
+  unsigned total = 0;  // chunks of the long sequences
   for (int s = tid; s < N; s += kSchedThreads) {
     const int b = block(s), len = length(s);
     if (b <= 0 || b >= nb || len == 0) continue;
@@ -585,8 +586,7 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms, int slices) {
       total += c;
     }
   }
-#pragma unroll
-  for (int w = 16; w > 0; w >>= 1) total += __shfl_xor_sync(0xffffffffu, total, w);
+  total = __reduce_add_sync(0xffffffffu, total);
   if ((tid & 31) == 0 && total) atomicAdd(&s_total, total);
   __syncthreads();
   const int n_pre = s_pre;
@@ -596,12 +596,17 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms, int slices) {
     hdr[kNPre] = n_pre;
   }
   if (n_pre == 0) return;
+  static_assert(kLinSlices == 4, "a head's marks are a word");
+  if (p.bad)
+    for (long long i = tid; i < (long long)n_pre * p.H; i += kSchedThreads)
+      reinterpret_cast<uint32_t*>(p.bad)[i] = 0u;
   const bool sorted = n_pre <= kSortMax;
   // longest first, ties by sequence (so that a call's order is always the same)
   for (int i = tid; i < n_pre; i += kSchedThreads) {
     if (sorted) {
       const int ci = chunks[i], si = found[i];
       int rank = 0;
+#pragma unroll 4
       for (int j = 0; j < n_pre; ++j) rank += chunks[j] > ci || (chunks[j] == ci && found[j] < si);
       pre[rank] = si;
       in_order[rank] = ci;
@@ -626,7 +631,7 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms, int slices) {
   if (p.seg_states && sorted) {
     // (32 bits hold all of this: q, k and v of that much work would not fit)
     const unsigned chains = p.H * (slices ? slices : 1);
-    const unsigned share = (unsigned)((s_total * chains + num_sms - 1) / num_sms);
+    const unsigned share = (s_total * chains + num_sms - 1) / num_sms;
     const unsigned longest = chunks_of(0), least = slices ? kMinSerial : kMinSegment;
     auto cost = [&](unsigned items, unsigned n, int passes) {
       const unsigned per_sm = max((items * chains + num_sms - 1) / num_sms, (share - 1) / n + 1);
@@ -658,21 +663,36 @@ lin_schedule_kernel(LinParams p, int short_max, int num_sms, int slices) {
     per = 0x7fffffff - (int)(s_best & 0x7fffffffu);
   }
   int carry = 0, n_split = 0;
-  for (int k0 = 0; k0 < n_pre; k0 += kSchedThreads) {
-    const int k = k0 + tid;
-    const int segs = k < n_pre ? (chunks_of(k) - 1) / per + 1 : 0;
-    n_split += __syncthreads_count(segs > 1);
-    int total;
-    const int before = carry + cta_scan(segs, &total, warp_sums);
-    if (k < n_pre) {
-      first[k] = before;
-      if (k == n_pre - 1) first[n_pre] = before + segs;
-      if (segs > 1) atomicAdd(&hdr[kLinStateItems], segs);
+  if (n_pre <= 32) {  // one warp needs no barriers
+    if (tid >= 32) return;
+    const int segs = tid < n_pre ? (chunks_of(tid) - 1) / per + 1 : 0;
+    int upto = segs;
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) {
+      const int before = __shfl_up_sync(0xffffffffu, upto, w);
+      if (tid >= w) upto += before;
     }
-    carry += total;
+    if (tid < n_pre) first[tid] = upto - segs;
+    if (tid == n_pre - 1) first[n_pre] = upto;
+    carry = __shfl_sync(0xffffffffu, upto, 31);
+    n_split = __popc(__ballot_sync(0xffffffffu, segs > 1));
+    const int split_segs = __reduce_add_sync(0xffffffffu, segs > 1 ? segs : 0);
+    if (tid == 0) hdr[kLinStateItems] = split_segs;
+  } else {
+    for (int k0 = 0; k0 < n_pre; k0 += kSchedThreads) {
+      const int k = k0 + tid;
+      const int segs = k < n_pre ? (chunks_of(k) - 1) / per + 1 : 0;
+      n_split += __syncthreads_count(segs > 1);
+      int total;
+      const int before = carry + cta_scan(segs, &total, warp_sums);
+      if (k < n_pre) {
+        first[k] = before;
+        if (k == n_pre - 1) first[n_pre] = before + segs;
+        if (segs > 1) atomicAdd(&hdr[kLinStateItems], segs);
+      }
+      carry += total;
+    }
   }
-  if (p.bad)
-    for (long long i = tid; i < (long long)n_pre * p.H * kLinSlices; i += kSchedThreads) p.bad[i] = 0;
   if (tid == 0) {
     hdr[kLinItems] = carry;
     hdr[kLinSplit] = n_split;
