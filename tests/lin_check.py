@@ -52,9 +52,10 @@ class LinRun:
         self.view = self.mem.view(torch.float32).view(num_layers, self.num_blocks, H, d, d)
         self.view.copy_(torch.randn(self.view.shape[1:], generator=g).expand(self.view.shape))
         self.view[:, 0] = 0
-        for s, b in enumerate(self.blk):
-            if 0 < b < self.num_blocks:
-                self.view[layer, b] = self.states[s].cuda()
+        # (a block may be named by empty sequences too: theirs first)
+        for s in sorted(range(self.N), key=lambda s: lens[s] > 0):
+            if 0 < self.blk[s] < self.num_blocks:
+                self.view[layer, self.blk[s]] = self.states[s].cuda()
         self.out = torch.full((T, H, d), SENTINEL, dtype=dtype, device="cuda")
         i32 = dict(dtype=torch.int32, device="cuda")
         self.cu_d = torch.tensor(self.cu, **i32)

@@ -462,3 +462,60 @@ def test_slow_decay_keeps_the_state_over_many_single_tokens(hint):
     torch.cuda.synchronize()
     errs = check(run)
     assert errs["state"] <= fp32_walk(1200) and errs["out"] <= fp32_walk(1200), errs
+
+
+def many_long(short):
+    """2,100 sequences that are all long, one of them long enough to be split,
+    which is done only for lists that are sorted."""
+    lens = [short] * 2100
+    lens[1234] = 1300
+    return lens
+
+
+def test_more_long_sequences_than_are_put_in_order():
+    run_and_check(many_long(20), [1, 0] * 1050, 1, 1, 32, "f32", log_decay=[-0.03])
+
+
+def test_more_long_prompts_than_are_put_in_order_equal_two_calls():
+    """(The half with the long one splits it: other roundings.)"""
+    run = LinRun(many_long(19), [1, 0] * 1050, 1, 1, 128, "bf16", log_decay=[-0.03])
+    before = run.mem.clone()
+    run.run()
+    out, mem = run.out.clone(), run.view.clone()
+    run.mem.copy_(before)
+    for lo, hi in ((0, 1050), (1050, 2100)):
+        rows = slice(run.cu[lo], run.cu[hi])
+        binding.lin_varlen_forward(run.pool, 0, run.q[rows], run.k[rows], run.v[rows],
+                                   run.cu_d[lo:hi + 1] - run.cu[lo], run.blk_d[lo:hi], run.past_d[lo:hi],
+                                   run.decay_d, run.out[rows], run.cu[hi] - run.cu[lo], hi - lo,
+                                   scale=run.scale)
+    torch.cuda.synchronize()
+    assert run.pool.error_flags() == 0
+    long_rows, long_block = slice(run.cu[1234], run.cu[1235]), run.blk[1234]
+    for a, b, at, tol in ((out, run.out, long_rows, 2.0 ** -7), (mem[0], run.view[0], long_block, 1e-5)):
+        assert (a[at].double() - b[at].double()).norm() <= tol * b[at].double().norm()
+        a[at] = b[at]
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("act,d", [("f32", 64), ("bf16", 128)])
+def test_batches_padded_far_beyond_the_pool(act, d):
+    """4,000 sequences on a pool of seven blocks: padding, empty ones that name
+    any block, and six with tokens."""
+    n = 4000
+    rng = np.random.default_rng(3)
+    lens, blocks = [0] * n, rng.integers(-3, 40, n).tolist()
+    at = rng.permutation(n)[:6].tolist()
+    for b, s in enumerate(at):
+        lens[s], blocks[s] = [1, 300, 17, 64, 1, 2][b], b + 1
+    lens[(at[0] + 1) % n or 1] = 5
+    blocks[(at[0] + 1) % n or 1] = -2
+    run_and_check(lens, [1] * n, 2, 1, d, act, blocks=blocks, num_blocks=7, tensor_cores=act == "bf16")
+
+
+@pytest.mark.parametrize("n", [512, 513])
+@pytest.mark.parametrize("hint", [0, 1, 2])
+def test_the_number_of_sequences_that_check_themselves(n, hint):
+    lens = [1] * n
+    lens[7] = 0
+    run_and_check(lens, [1] * n, 1, 1, 32, "f32", hint=hint, num_blocks=n + 1)
