@@ -161,10 +161,12 @@ def _index(t) -> Optional[int]:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, device: Optional[int] = None) -> Optional[int]:
+    """A stream's handle; None: the current one, of the current device or the
+    one given."""
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if device is None else device)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -359,9 +361,18 @@ def _heads(t, name, heads, d, dtype, T):
     if len(shape) != 3 or shape[1] != heads or shape[2] != d or t.dtype != dtype or shape[0] < T:
         raise ValueError(f"{name} is [>= {T}][{heads}][{d}] of {dtype}: got {tuple(shape)} of "
                          f"{t.dtype}")
-    if shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != d)):
-        raise ValueError(f"the rows of {name} have to be dense")
-    return t.data_ptr(), stride[0] if shape[0] > 1 else heads * d
+    rows = shape[0]
+    if rows and (stride[2] != 1 or (heads > 1 and stride[1] != d) or not t.is_cuda):
+        raise ValueError(f"the rows of {name} have to be dense, on a CUDA device")
+    return t.data_ptr(), stride[0] if rows > 1 else heads * d
+
+
+def _list(t, name, dtype, n):
+    """The address of a dense device list of at least n elements."""
+    if t.dtype != dtype or t.numel() < n or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} is a contiguous CUDA tensor of >= {n} {dtype}: got {t.numel()} of "
+                         f"{t.dtype} on {t.device}")
+    return t.data_ptr()
 
 
 def lin_varlen_forward(pool: LinPool, layer: int, q, k, v, cu_seqlens, state_block_idx, has_past,
@@ -375,11 +386,13 @@ def lin_varlen_forward(pool: LinPool, layer: int, q, k, v, cu_seqlens, state_blo
     pk, ldk = _heads(k, "k", Hkv, d, dtype, T)
     pv, ldv = _heads(v, "v", Hkv, d, dtype, T)
     po, ldo = _heads(out, "out", H, d, dtype, T)
-    _check(load().gdn_lin_varlen_forward(pool.handle, layer, pq, pk, pv, ldq, ldk, ldv, Hkv,
-                                         _ptr(cu_seqlens), _ptr(state_block_idx), _ptr(has_past),
-                                         _ptr(log_decay), scale, po, ldo, T, N, max_seqlen_hint,
-                                         _stream(stream)),
-           "gdn_lin_varlen_forward")
+    _check(load().gdn_lin_varlen_forward(
+        pool.handle, layer, pq, pk, pv, ldq, ldk, ldv, Hkv,
+        _list(cu_seqlens, "cu_seqlens", torch.int32, N + 1),
+        _list(state_block_idx, "state_block_idx", torch.int32, N),
+        _list(has_past, "has_past", torch.uint8, N), _list(log_decay, "log_decay", torch.float32, H),
+        scale, po, ldo, T, N, max_seqlen_hint, _stream(stream, cu_seqlens.get_device())),
+        "gdn_lin_varlen_forward")
 
 
 def varlen_forward(pool: Pool, layer: int, x_qkv, a, b, cu_seqlens, state_block_idx, has_past,

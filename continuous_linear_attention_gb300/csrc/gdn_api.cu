@@ -11,6 +11,7 @@
 #include <new>
 
 #include "gdn.h"
+#include "gdn_cta.cuh"
 #include "gdn_internal.cuh"
 #include "gdn_pool.cuh"
 
@@ -133,6 +134,7 @@ bool is_pow2(size_t v) { return v && !(v & (v - 1)); }
 namespace gdn {
 int pool_allocate(gdn_pool* p, void* device_mem) {
   if (cudaGetDevice(&p->device) != cudaSuccess) return GDN_ERR_CUDA;
+  p->sms = num_sms();
   p->owns = device_mem == nullptr;
   p->base = (unsigned char*)device_mem;
   if (p->owns && cudaMalloc((void**)&p->base, p->total) != cudaSuccess) {

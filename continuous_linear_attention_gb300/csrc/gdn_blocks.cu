@@ -633,7 +633,7 @@ cudaError_t launch_moves(const gdn_pool* p, int layer, const BlockWork& bw, cuda
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)sizeof(MoveSmem));
   if (e != cudaSuccess) return e;
-  return launch_pdl(move_blocks_kernel, dim3(num_sms()), dim3(kWarps * 32), sizeof(MoveSmem), s, mp);
+  return launch_pdl(move_blocks_kernel, dim3(p->sms), dim3(kWarps * 32), sizeof(MoveSmem), s, mp);
 }
 
 template <typename K, typename... Args>
@@ -681,7 +681,7 @@ int gdn_state_pool_clear_blocks(gdn_pool_t* p, int layer, const int32_t* idx, in
   const int layers = layer < 0 ? p->num_layers : 1;
   const int cols = (int)((p->stride + gdn::kZero - 1) / gdn::kZero);
   const long long units = (long long)layers * cols * n;
-  const long long most = 8ll * gdn::num_sms();
+  const long long most = 8ll * p->sms;
   if (gdn::launch_pdl(gdn::clear_blocks_kernel, dim3((unsigned)(units < most ? units : most)),
                       dim3(128), 0, (cudaStream_t)stream, gdn::first_layer(p, layer), p->stride,
                       p->num_blocks, layers, cols, idx, n,

@@ -898,7 +898,7 @@ int gdn_lin_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
   lp.work.num_blocks = p->num_blocks;
 
   cudaStream_t s = (cudaStream_t)stream;
-  const int sms = gdn::num_sms();
+  const int sms = p->sms;
   // prompts in the chunked form, where it has a kernel and the call room for one
   const long long units = (long long)N * H * gdn::kLinSlices;
   const int short_max = units <= sms       ? gdn::kLinShortLone

@@ -11,7 +11,7 @@ struct gdn_pool {
   size_t stride, conv_off, rec_off, total;
   unsigned char* base;
   bool owns;
-  int device;
+  int device, sms;  // and its streaming multiprocessors
   int32_t* work;  // num_layers * WorkArea::words(num_blocks) words
   cudaEvent_t ev_before, ev_after;  // optional timing events (caller-owned)
   // prefill scratch: chunk-major tiles of the split prefill path (gated delta

@@ -519,3 +519,18 @@ def test_the_number_of_sequences_that_check_themselves(n, hint):
     lens = [1] * n
     lens[7] = 0
     run_and_check(lens, [1] * n, 1, 1, 32, "f32", hint=hint, num_blocks=n + 1)
+
+
+def test_lists_of_another_type_size_or_place_are_refused():
+    run = LinRun([3, 1], [1, 1], 2, 1, 64, "f32")
+    kw = dict(q=run.q, k=run.k, v=run.v, cu_seqlens=run.cu_d, state_block_idx=run.blk_d,
+              has_past=run.past_d, log_decay=run.decay_d, out=run.out, T=4, N=2)
+    for bad in (dict(cu_seqlens=run.cu_d.long()), dict(cu_seqlens=run.cu_d[:2]),
+                dict(cu_seqlens=run.cu_d.cpu()), dict(state_block_idx=run.blk_d[:1]),
+                dict(state_block_idx=torch.stack([run.blk_d, run.blk_d], 1)[:, 0]),
+                dict(has_past=run.past_d.int()), dict(log_decay=run.decay_d.double()),
+                dict(log_decay=run.decay_d[:1]), dict(q=run.q.cpu()), dict(N=3)):
+        with pytest.raises(ValueError):
+            binding.lin_varlen_forward(run.pool, 0, **(kw | bad))
+    torch.cuda.synchronize()
+    assert (run.out == SENTINEL).all() and run.pool.error_flags() == 0
