@@ -34,9 +34,11 @@ constexpr int kSlice = 32;                          // state columns per CTA
 constexpr int kColT = kSlice / 4;                   // threads across the columns
 constexpr int kRowT = kRecThreads / kColT;          // threads across the rows
 constexpr int kTile = 16;                           // tokens staged at a time
-// calls of up to this many sequences check the batch in every CTA, while its
-// state loads are in flight, which saves the scheduler's launch
-constexpr int kSelfCheck = 512;
+// Calls of up to this many sequences check the batch in every CTA, while its
+// state loads are in flight, which saves the scheduler's launch: 256 single
+// tokens x 32 heads 164 us (167 with the scheduler), 512 x 16 heads 171 and 171,
+// 1,024 363 and 330; 128 times four tokens x 16 heads 54 (57), 256 101 and 100.
+constexpr int kSelfCheck = 256;
 // groups of kRecThreads that work on segments side by side on an SM (their
 // shared memory: 184 KB of fp32 at d = 128)
 constexpr int kSerialPerSm = 4;

@@ -513,7 +513,7 @@ def test_batches_padded_far_beyond_the_pool(act, d):
     run_and_check(lens, [1] * n, 2, 1, d, act, blocks=blocks, num_blocks=7, tensor_cores=act == "bf16")
 
 
-@pytest.mark.parametrize("n", [512, 513])
+@pytest.mark.parametrize("n", [256, 257, 512, 513])
 @pytest.mark.parametrize("hint", [0, 1, 2])
 def test_the_number_of_sequences_that_check_themselves(n, hint):
     lens = [1] * n
