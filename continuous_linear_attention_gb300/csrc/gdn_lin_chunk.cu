@@ -7,19 +7,21 @@
 //   S_n     = e^{g n} S0 + sum_j e^{g (n-1-j)} k_j v_j^T
 // so a (sequence, head) chain is four 128^3 products per chunk, and all but
 // the first term of each line does not depend on the chunks before.  No weight
-// is a growing power that another one takes back, so any decay will do.  (With
-// the row's decay taken out of P where e^{128 |g|} allows it, the pass over
-// Q S0 goes, for 1% of the prompt batch's time.)
+// is a growing power that another one takes back, so any decay will do.
 //
-// Bytes bound it: q, k, v and o are 128 KB per chunk and head (2.9 us of one
-// SM's share of HBM); the products, the state's in four terms, are seven 128^3
-// (2.3 us of one SM's tensor rate at the measured peak).  Measured: 4.0 us per
-// chunk with all SMs busy (15,843 tokens x 64 heads in 212 us, 5.1 TB/s; the
-// loads and stores of this pipeline alone take 177), 2.8 us for a chain alone.
+// Bytes are its floor: q, k, v and o are 128 KB per chunk and head (2.9 us of
+// one SM's share of HBM); the products, P V and Q S0 in two terms and the
+// state's in four, are nine 128^3 (2.9 us of one SM's tensor rate at the
+// measured peak).  Measured: 4.7 us per chunk with all SMs busy (15,843 tokens
+// x 64 heads in 252 us, 4.3 TB/s; the loads and stores of this pipeline alone
+// take 177).  What bounds it is the O warps' chain through a chunk: P's
+// conversion, the scaling of Q S0, P V and the output one after the other.
 //
 // One CTA per SM, chains claimed from a counter, longest first.  Roles, each
 // a loop over the CTA's chunks that meets the others at mbarriers only:
-//   producer  one thread: TMA loads of a chunk's q, k, v tiles, two stages
+//   producer  one thread: TMA loads of a chunk's q, k, v tiles, two stages; k and
+//             v as soon as their products are done, q when its tile has been
+//             stored as output (2% faster than all three at once)
 //   MMA 1     one warp: P = Q K^T, O = Q S0, then O += P V in two halves of 64
 //             columns, so that the O warps' work on one half runs beside it
 //   MMA 2     one warp: U = sum of the decayed v k^T, 32 tokens at a time
@@ -27,14 +29,16 @@
 //   O warps   P with its decay -> bf16 A operand; O <- scale e^{g(i+1)} O; output
 //   V warps   e^{g(n-1-j)} v_j -> A operand of U, rows past the chunk's end
 //             zeroed
-//   S warps   the state, fp32 in registers (thread v holds S[.][v]): to bf16
-//             as operand of O, S <- e^{g n} S + U
+//   S warps   the state, fp32 in registers (thread v holds S[.][v]): its bf16
+//             terms in turn as operand of O, S <- e^{g n} S + U
 //
-// Precision.  P and S0 enter as bf16 operands (their partners are bf16, and
-// one MMA takes one type): each is off by as much as the output's own
-// rounding.  The state is an output in fp32 and carried over the whole prompt,
-// so its update is not rounded to bf16: a decayed v has 8 + 24 significant bits
-// and goes in as four bf16 terms.  With the weight as
+// Precision.  The partners of P and S0 are bf16, and one MMA takes one type:
+// both enter as two bf16 terms, exact to 2^-16, which leaves the output's own
+// rounding the only one that counts, as in the recurrent form (rel. L2 1.7e-3;
+// one term each made it 2.3e-3, in 217 us for the call above).  The state is
+// an output in fp32 and carried over the whole prompt, so its update takes
+// more: a decayed v has 8 + 24 significant bits and goes in as four bf16 terms.
+// With the weight as
 // wh + wm + wl (8 bits each), v wh is its bf16 rounding plus a remainder that
 // an fma gives exactly and that is a bf16 again, v wm likewise, and v wl joins
 // the last remainder (2^-18 of the whole, off by 2^-27): five packed bf16
@@ -49,6 +53,10 @@
 // token-serial kernel, and their block keeps the old state until then.  A
 // non-finite q or k reaches only its own row and the later ones, as it should:
 // P's mask selects, it does not multiply.
+//
+// Weights.  P's weights scale e^{g (i-j)} are a head's table in shared memory,
+// four loaded at a time; made of two factors, one of them by a shuffle per
+// element, they took 3,400 cycles a chunk of the O warps instead of 2,200.
 //
 // Few long chains: where it is cheaper (see the scheduler), long sequences are
 // cut into segments.  A first launch of this kernel
@@ -71,7 +79,7 @@ constexpr int kThreads = 768;  // O, V and S warps (8, 8, 4), then four single-t
 constexpr int kOWarps = 8, kVWarps = 8, kSWarp = 16, kCtlWarp = 20;
 constexpr uint32_t TILE = 32768, BOX = 16384;  // a [128][128] bf16 tile: two 64-column boxes
 // stages of a chunk's q, k and v (three of k and v for the state pass), then
-// S0 as B operand: [v][k], two 64-k blocks
+// S0 as B operand, one bf16 term at a time: [v][k], two 64-k blocks
 constexpr int kMaxStages = 3;
 constexpr uint32_t OFF_S = 6 * TILE;
 // Stage of a role's current chunk and the parity of its pass over the stages.
@@ -86,8 +94,9 @@ struct Pos {
     }
   }
 };
-// tensor memory columns: P fp32 (bf16 over the first 32 of each 64), O, U, then the
-// four terms of 32 decayed v rows, twice: per 16 rows 8 columns of each term
+// tensor memory columns: P fp32 (per 32 columns then the two bf16 terms, 16 columns
+// each), O, U, then the four terms of 32 decayed v rows, twice: per 16 rows 8
+// columns of each term
 constexpr uint32_t TM_P = 0, TM_O = 128, TM_U = 256, TM_V = 384, TM_COLS = 512;
 constexpr int QT = 32;  // tokens per step of U
 constexpr int kTerms = 4;
@@ -105,15 +114,21 @@ struct Desc {
   int row, n, h, flags;
   int entry;            // index in the scheduler's list of long sequences
   int slot;             // segment state slot, or -1
-  long long rblk, wblk;  // blocks read (0: zeros) and written
+  int rblk, wblk;       // blocks read (0: zeros) and written
 };
 
+// A head's weights scale e^{g m}, 0 <= m < 128, by falling m and then zeros:
+// copy r begins with the r-th, so that a thread reads four from any place on
+// as one 16-byte load, and the copies lie a quarter of the banks apart.
+constexpr int kWeights = 160, kWeightCopy = kWeights + 8;
 struct Ctl {
   Desc desc[kMaxStages];
-  uint64_t full[kMaxStages], empty[kMaxStages], zeroed[kMaxStages], staged[kMaxStages];
-  uint64_t p_full, pb_full, qs_full, o_scaled, o_full[2], o_free, s_ready;
+  uint64_t full[kMaxStages], kv_free[kMaxStages], q_free[kMaxStages], zeroed[kMaxStages], staged[kMaxStages];
+  uint64_t p_full, pb_full, qs_full, o_scaled, o_full[2], o_free, s_ready, s_read;
   uint64_t v_full[4], v_free[4], u_full[2], u_free[2];
+  uint64_t w_ready;
   uint32_t tmem;
+  alignas(16) float weight[3 * kWeightCopy + kWeights];
 };
 constexpr uint32_t OFF_CTL = OFF_S + TILE;
 constexpr uint32_t SMEM_BYTES = OFF_CTL + sizeof(Ctl);
@@ -158,15 +173,29 @@ template <int kRegs>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
+__device__ __forceinline__ uint32_t bf2(float lo, float hi) {
+  return tc::pack2(lo, hi, (__nv_bfloat16*)nullptr);
+}
 __device__ __forceinline__ uint32_t bf2(F2 v) {
   float x, y;
   unf2(v, x, y);
-  return tc::pack2(x, y, (__nv_bfloat16*)nullptr);
+  return bf2(x, y);
 }
 // The two bf16 of a word as fp32.
 __device__ __forceinline__ F2 widen(uint32_t w) {
   return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
+// A pair as two bf16 terms.  The first one of an infinity is the largest number,
+// so that the second one and their sum are that infinity and not NaN.  (Volatile:
+// computed again for the second term, where keeping 64 first ones would spill.)
+__device__ __forceinline__ uint32_t term1(F2 v) {
+  float x, y;
+  unf2(v, x, y);
+  uint32_t r;
+  asm volatile("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t term2(F2 v) { return bf2(fma2(widen(term1(v)), f2(-1.f, -1.f), v)); }
 // Four transposed 8 x 8 matrices of 16-bit elements: lane l gives the address
 // of row l % 8 of matrix l / 8 and gets of each matrix column l / 4, rows
 // 2 (l % 4) and the next.
@@ -186,9 +215,6 @@ __device__ __forceinline__ void tmem_st_frag4(uint32_t taddr, const uint32_t* r)
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
-}
-__device__ __forceinline__ uint32_t bf2(float lo, float hi) {
-  return tc::pack2(lo, hi, (__nv_bfloat16*)nullptr);
 }
 // Packed bf16 products, each rounded once.
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -248,12 +274,14 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
   const uint32_t sbase = smem_u32(sm);
   if (tid == 0) {
     for (int b = 0; b < kStages; ++b) {
-      mbar_init(&ctl.full[b], 1);
-      // V warps, S warps, MMA 2 (and MMA 1, store)
-      mbar_init(&ctl.empty[b], kVWarps + 4 + (kState ? 1 : 3));
+      // of the k and v tiles, and of the q tile and the descriptor
+      mbar_init(&ctl.full[b], kState ? 1 : 2);
+      mbar_init(&ctl.kv_free[b], kVWarps + (kState ? 1 : 2));  // V warps, MMA 2 (and 1)
+      mbar_init(&ctl.q_free[b], 4 + (kState ? 0 : 1));         // S warps (and the store)
       mbar_init(&ctl.zeroed[b], kVWarps);
       mbar_init(&ctl.staged[b], kOWarps);
     }
+    mbar_init(&ctl.w_ready, kOWarps);
     mbar_init(&ctl.p_full, 1);
     mbar_init(&ctl.pb_full, kOWarps);
     mbar_init(&ctl.qs_full, 1);
@@ -262,6 +290,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
     mbar_init(&ctl.o_full[1], 1);
     mbar_init(&ctl.o_free, kOWarps);
     mbar_init(&ctl.s_ready, 4);
+    mbar_init(&ctl.s_read, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ctl.u_full[b], 1);
       mbar_init(&ctl.u_free[b], 4);
@@ -302,8 +331,8 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
     const int i = rw * 32 + lane;
     const uint32_t tl = (uint32_t)(rw * 32) << 16;
     int h = -1;
-    float g = 0.f, after = 0.f;  // scale e^{g (i+1)}
-    float col = 0.f, dia = 0.f;  // e^{g (31 - lane)}, scale e^{g lane}
+    uint32_t heads = 0;
+    float after = 0.f;  // scale e^{g (i+1)}
     Pos<kStages> pos;
     for (int c = 0; !kState; ++c, pos.next()) {
       const int b = pos.b;
@@ -313,48 +342,58 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       const int row = ctl.desc[b].row, n = ctl.desc[b].n;
       if (ctl.desc[b].h != h) {
         h = ctl.desc[b].h;
-        g = finite_decay(p.log_decay[h]);
+        const float g = finite_decay(p.log_decay[h]);
         after = p.scale * expf(g * (float)(i + 1));
-        col = expf(g * (float)(31 - lane));
-        dia = p.scale * expf(g * (float)lane);
+        // the last head's weights have been used
+        if (c > 0 && !warp_wait(&ctl.pb_full, ph ^ 1)) { dead = true; break; }
+        for (int e = tid; e < 4 * kWeights; e += 32 * kOWarps) {
+          const int copy = e / kWeights, at = e % kWeights, m = CH - 1 - at - copy;
+          ctl.weight[copy * kWeightCopy + at] = m >= 0 ? p.scale * expf(g * (float)m) : 0.f;
+        }
+        warp_arrive(&ctl.w_ready);
+        if (!warp_wait(&ctl.w_ready, heads)) { dead = true; break; }
+        heads ^= 1;
       }
-      // ---- P: decay and mask, to bf16 over the first 32 of this warp's own 64
-      // columns (block u's 16 land on fp32 columns read before)
+      // ---- P: decay and mask, each block of 32 columns to its two bf16 terms
+      // in place, 16 columns each
       if (!warp_wait(&ctl.p_full, ph)) { dead = true; break; }
       tc::fence_after_sync();
 #pragma unroll 1
       for (int u = 0; u < 2; ++u) {
         const int jb = 2 * hf + u;
-        uint32_t w[16];
+        const uint32_t at = tmem + tl + TM_P + jb * 32;
         if (jb > rw) {
+          uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) w[e] = 0u;
+          tc::tmem_st16u(at, w);
+          tc::tmem_st16u(at + 16, w);
         } else {
           float x[32];
-          tc::tmem_ld32(tmem + tl + TM_P + jb * 32, x);
-          // column jj's weight comes from a lane: on the diagonal block
-          // scale e^{g (lane - jj)}, left of it e^{g (31 - jj)} times the row's
-          // scale e^{g (i - 32 jb - 31)}
+          F2 y[16];
+          tc::tmem_ld32(at, x);
           const bool diagonal = jb == rw;
-          const float tab = diagonal ? dia : col;
-          const int dir = diagonal ? -1 : 1, from = diagonal ? lane : 0;
+          const float* wt = ctl.weight + (~lane & 3) * kWeightCopy + (CH - 4 - (i & ~3) + 32 * jb);
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] *= __shfl_sync(0xffffffffu, tab, from + dir * e);
-          if (!diagonal) {
-            const float rowf = p.scale * expf(g * (float)(i - 32 * jb - 31));
-#pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] *= rowf;
+          for (int e = 0; e < 32; e += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(wt + e);
+            y[e / 2] = mul2(f2(x[e], x[e + 1]), f2(f.x, f.y));
+            y[e / 2 + 1] = mul2(f2(x[e + 2], x[e + 3]), f2(f.z, f.w));
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = bf2(x[2 * e], x[2 * e + 1]);
-          if (diagonal) {
+          for (int t = 0; t < 2; ++t) {
+            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              w[e] = lane > 2 * e ? w[e] : lane == 2 * e ? w[e] & 0xffffu : 0u;
+            for (int e = 0; e < 16; ++e) w[e] = t == 0 ? term1(y[e]) : term2(y[e]);
+            if (diagonal) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                w[e] = lane > 2 * e ? w[e] : lane == 2 * e ? w[e] & 0xffffu : 0u;
+            }
+            tc::tmem_st16u(at + 16 * t, w);
           }
         }
-        tc::tmem_st16u(tmem + tl + TM_P + hf * 64 + u * 16, w);
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
@@ -524,7 +563,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         }
       }
       if (dead) break;
-      warp_arrive(&ctl.empty[b]);
+      warp_arrive(&ctl.kv_free[b]);
     }
   } else if (warp < kCtlWarp) {
     // ============================== S warps ===============================
@@ -557,19 +596,25 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         }
       }
       if (!kState) {
-        // ---- S0 as the B operand [v][k] of O = Q S0
+        // ---- S0 as the B operand [v][k] of O = Q S0: its first bf16 term, then,
+        // once that has been read, the second one in its place
         if (c > 0 && !warp_wait(&ctl.qs_full, (c - 1) & 1)) { dead = true; break; }
+        auto put = [&](auto term) {
 #pragma unroll
-        for (int k = 0; k < D; k += 8) {
-          uint4 w;
-          w.x = bf2(S[k / 2]);
-          w.y = bf2(S[k / 2 + 1]);
-          w.z = bf2(S[k / 2 + 2]);
-          w.w = bf2(S[k / 2 + 3]);
-          *reinterpret_cast<uint4*>(sm + OFF_S + (k >> 6) * BOX + tc::sw128_offset(v, k & 63)) = w;
-        }
-        tc::fence_proxy_async_smem();
-        warp_arrive(&ctl.s_ready);
+          for (int k = 0; k < D; k += 8) {
+            uint4 w;
+            w.x = term(S[k / 2]);
+            w.y = term(S[k / 2 + 1]);
+            w.z = term(S[k / 2 + 2]);
+            w.w = term(S[k / 2 + 3]);
+            *reinterpret_cast<uint4*>(sm + OFF_S + (k >> 6) * BOX + tc::sw128_offset(v, k & 63)) = w;
+          }
+          tc::fence_proxy_async_smem();
+          warp_arrive(&ctl.s_ready);
+        };
+        put([](F2 s) { return term1(s); });
+        if (!warp_wait(&ctl.s_read, c & 1)) { dead = true; break; }
+        put([](F2 s) { return term2(s); });
       }
       if (!(d.flags & kNoU)) {
         const DecayPair a = decay_pair(finite_decay(p.log_decay[d.h]) * (float)d.n);
@@ -625,7 +670,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
           }
         }
       }
-      warp_arrive(&ctl.empty[b]);
+      warp_arrive(&ctl.q_free[b]);
     }
   } else {
     regs_dec<40>();
@@ -633,6 +678,13 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
       // ============================== producer ==============================
       int c = 0;
       Pos<kStages> pos;
+      auto load_kv = [&](unsigned char* st, int hk, int row, uint64_t* bar) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          tma_load_2d(st + ST_K + x * BOX, &tk, hk * D + x * 64, row, bar);
+          tma_load_2d(st + ST_V + x * BOX, &tv, hk * D + x * 64, row, bar);
+        }
+      };
       for (bool end = false; !end && !dead;) {
         const int u = atomicAdd(&hdr[kState ? kLinStateHead : kLinHead], 1);
         end = u >= n_units;
@@ -661,10 +713,6 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         const int hk = h / p.group;
         for (int k = c0; k < c1; ++k, ++c, pos.next()) {
           const int b = pos.b;
-          if (c >= kStages && !wait_for(&ctl.empty[b], pos.ph ^ 1)) {
-            dead = true;
-            break;
-          }
           Desc d;
           d.row = end ? 0 : p.cu[s] + k * CH;
           d.n = end ? 0 : min(CH, L - k * CH);
@@ -677,18 +725,33 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
                         : (k == c0 ? kFirst : 0) | (k == c1 - 1 ? kLast : 0) |
                               (seg == nseg - 1 ? kFinal : 0) |
                               (!kState && k == c1 - 1 && seg < nseg - 1 ? kNoU : 0);
+          unsigned char* st = sm + b * ST_BYTES;
+          // k and v over the last ones' while their outputs are still written, then
+          // (all roles have read the last descriptor) q
+          if (c >= kStages && !wait_for(&ctl.kv_free[b], pos.ph ^ 1)) { dead = true; break; }
+          if (!kState && !end) {
+            mbar_arrive_expect_tx(&ctl.full[b], 2 * TILE);
+            load_kv(st, hk, d.row, &ctl.full[b]);
+          }
+          if (c >= kStages && !wait_for(&ctl.q_free[b], pos.ph ^ 1)) {
+            dead = true;
+            ++c;
+            break;
+          }
           ctl.desc[b] = d;
           if (end) {
             arrive(&ctl.full[b]);
+            if (!kState) arrive(&ctl.full[b]);
             break;
           }
-          unsigned char* st = sm + b * ST_BYTES;
-          mbar_arrive_expect_tx(&ctl.full[b], kState ? 2 * TILE : 3 * TILE);
+          if (kState) {
+            mbar_arrive_expect_tx(&ctl.full[b], 2 * TILE);
+            load_kv(st, hk, d.row, &ctl.full[b]);
+          } else {
+            mbar_arrive_expect_tx(&ctl.full[b], TILE);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            tma_load_2d(st + ST_K + x * BOX, &tk, hk * D + x * 64, d.row, &ctl.full[b]);
-            if (!kState) tma_load_2d(st + ST_Q + x * BOX, &tq, h * D + x * 64, d.row, &ctl.full[b]);
-            tma_load_2d(st + ST_V + x * BOX, &tv, hk * D + x * 64, d.row, &ctl.full[b]);
+            for (int x = 0; x < 2; ++x)
+              tma_load_2d(st + ST_Q + x * BOX, &tq, h * D + x * 64, d.row, &ctl.full[b]);
           }
         }
       }
@@ -720,20 +783,22 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
           tc::commit(&ctl.p_full);
         }
         __syncwarp();
-        // O = Q S0
-        if (!warp_wait(&ctl.s_ready, ph) || (c > 0 && !warp_wait(&ctl.o_free, ph ^ 1))) {
-          dead = true;
-          break;
-        }
-        tc::fence_after_sync();
-        if (one) {
+        // O = Q S0, of S0's two terms in turn
+        if (c > 0 && !warp_wait(&ctl.o_free, ph ^ 1)) { dead = true; break; }
+        for (uint32_t term = 0; term < 2; ++term) {
+          if (!warp_wait(&ctl.s_ready, term)) { dead = true; break; }
+          tc::fence_after_sync();
+          if (one) {
 #pragma unroll
-          for (int t = 0; t < 8; ++t)
-            tc::mma_bf16(tmem + TM_O, kDescHi | (q_lo + step_k(t)), kDescHi | (s_lo + step_k(t)), kId, t > 0);
-          tc::commit(&ctl.qs_full);
+            for (int t = 0; t < 8; ++t)
+              tc::mma_bf16(tmem + TM_O, kDescHi | (q_lo + step_k(t)), kDescHi | (s_lo + step_k(t)), kId,
+                           t > 0 || term > 0);
+            tc::commit(term == 0 ? &ctl.s_read : &ctl.qs_full);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        // O += P V (P's tokens 64 .. 127 are 64 columns on)
+        if (dead) break;
+        // O += P V, of P's two terms: 16 tokens' are 8 columns of each
         if (!warp_wait(&ctl.zeroed[b], pos.ph) || !warp_wait(&ctl.pb_full, ph) ||
             !warp_wait(&ctl.o_scaled, ph)) {
           dead = true;
@@ -744,12 +809,12 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
-              tc::mma_ts(tmem + TM_O + hf * 64, tmem + TM_P + (t >> 2) * 64 + (t & 3) * 8,
-                         kDescHi | (v_lo + hf * (BOX >> 4) + t * kStepMN), kIdMN, 1u);
+            for (int t = 0; t < 16; ++t)
+              tc::mma_ts(tmem + TM_O + hf * 64, tmem + TM_P + (t >> 2) * 32 + (t & 3) * 8,
+                         kDescHi | (v_lo + hf * (BOX >> 4) + ((t >> 2) * 2 + (t & 1)) * kStepMN), kIdMN, 1u);
             tc::commit(&ctl.o_full[hf]);
           }
-          tc::commit(&ctl.empty[b]);
+          tc::commit(&ctl.kv_free[b]);
         }
         __syncwarp();
       }
@@ -766,7 +831,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         const int flags = ctl.desc[b].flags, n = ctl.desc[b].n;
         if (flags & kEnd) break;
         if (flags & kNoU) {
-          warp_arrive(&ctl.empty[b]);
+          warp_arrive(&ctl.kv_free[b]);
           continue;
         }
         const int ub = ups & ((1 << kULog) - 1);
@@ -793,7 +858,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
         ++ups;
         if (one) {
           tc::commit(&ctl.u_full[ub]);
-          tc::commit(&ctl.empty[b]);
+          tc::commit(&ctl.kv_free[b]);
         }
         __syncwarp();
       }
@@ -813,7 +878,7 @@ lin_chunk_kernel(LinParams p, const __grid_constant__ CUtensorMap tq,
           bulk_commit();
           bulk_wait_read_all();
         }
-        arrive(&ctl.empty[b]);
+        arrive(&ctl.q_free[b]);
       }
       bulk_wait_all();
     }

@@ -359,7 +359,10 @@ int gdn_lin_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int nu
  * gdn_varlen_forward.  The pool must come from gdn_lin_pool_create
  * (GDN_ERR_DIMS otherwise).  An output row depends on its own and earlier
  * tokens of its sequence only, whatever the later ones hold (NaN and
- * infinities among them).  Never synchronises; graph-capturable. */
+ * infinities among them).  States and sums are fp32 in every form; where the
+ * chunked form hands the state and q k^T to the tensor cores it does so in 16
+ * significant bits, so that an output is off by its own rounding alone,
+ * however many tokens the call has.  Never synchronises; graph-capturable. */
 int gdn_lin_varlen_forward(gdn_pool_t* pool, int layer, const void* q, const void* k,
                            const void* v, int64_t ldq, int64_t ldk, int64_t ldv, int num_kv_heads,
                            const int32_t* cu_seqlens, const int32_t* state_block_idx,
