@@ -150,7 +150,7 @@ __device__ __forceinline__ void recurrent_body(const LinParams& p, RecSmem<T, D,
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         F2 t = mul2(k2, v2[c]);
-        if constexpr (decltype(with_rest)::value) t = fma2(rest, S[i][c], t);
+        if constexpr (decltype(with_rest)::value) t = fma2(rest, bounded(S[i][c]), t);
         S[i][c] = t = fma2(ahi, S[i][c], t);
         if constexpr (!kState) o[c] = i == 0 ? mul2(q2, t) : fma2(q2, t, o[c]);
       }
@@ -464,8 +464,8 @@ __global__ void __launch_bounds__(256) lin_segments_kernel(LinParams p) {
     const int s = p.work.pre()[e], blk = p.blk[s];
     const int first = p.work.pre_cp()[e], nseg = p.work.pre_cp()[e + 1] - first;
     const size_t at = (size_t)part * 256 + threadIdx.x;
-    const DecayPair a =
-        decay_pair(finite_decay(p.log_decay[h]) * (float)(hdr[kLinSegChunks] * p.chunk));
+    const float g = finite_decay(p.log_decay[h]), one = decay_pair(g).hi;
+    const DecayPair a = decay_pair(g * (float)(hdr[kLinSegChunks] * p.chunk));
     float S = 0.f;
     if (p.has_past[s])
       S = reinterpret_cast<const float*>(p.layer_base + (size_t)blk * p.stride)[(size_t)h * words + at];
@@ -480,7 +480,8 @@ __global__ void __launch_bounds__(256) lin_segments_kernel(LinParams p) {
       for (int i = 0; i < kAhead; ++i) {
         if (i0 + i >= nseg) break;
         z[(i0 + i) * step] = S;
-        S = fmaf(a.hi, S, fmaf(a.lo, S, own[i]));
+        // (an infinite state stays so over any number of decays that are not zero)
+        S = fmaf(fabsf(S) <= 3.402823466e38f ? a.hi : one, S, fmaf(a.lo, bounded(S), own[i]));
       }
     }
   }

@@ -71,6 +71,14 @@ __device__ __forceinline__ DecayPair decay_pair(float x) {
   }
   return d;
 }
+// x, or the largest number of its sign where it is infinite: what the pair's
+// second number multiplies, since a zero or negative one times an infinity
+// would make NaN of a state that the recurrence leaves infinite.
+__device__ __forceinline__ float bounded(float x) {
+  float r;
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(3.402823466e38f));
+  return r;
+}
 // Pairs of fp32 in one 64-bit register: packed arithmetic (one instruction per
 // pair).
 using F2 = unsigned long long;
@@ -81,6 +89,11 @@ __device__ __forceinline__ F2 f2(float x, float y) {
 }
 __device__ __forceinline__ void unf2(F2 v, float& x, float& y) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ F2 bounded(F2 v) {
+  float x, y;
+  unf2(v, x, y);
+  return f2(bounded(x), bounded(y));
 }
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   F2 r;

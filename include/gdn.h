@@ -362,7 +362,10 @@ int gdn_lin_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int nu
  * infinities among them).  States and sums are fp32 in every form; where the
  * chunked form hands the state and q k^T to the tensor cores it does so in 16
  * significant bits, so that an output is off by its own rounding alone,
- * however many tokens the call has.  Never synchronises; graph-capturable. */
+ * however many tokens the call has.  An infinite k, v or past makes its entries
+ * of the state infinite as the recurrence does, in every form, and NaN where it
+ * does (inf - inf, a decay that fp32 holds as 0 times inf); a non-finite q
+ * makes its own row non-finite.  Never synchronises; graph-capturable. */
 int gdn_lin_varlen_forward(gdn_pool_t* pool, int layer, const void* q, const void* k,
                            const void* v, int64_t ldq, int64_t ldk, int64_t ldv, int num_kv_heads,
                            const int32_t* cu_seqlens, const int32_t* state_block_idx,
