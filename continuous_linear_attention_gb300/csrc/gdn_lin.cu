@@ -210,6 +210,10 @@ __device__ __forceinline__ void recurrent_body(const LinParams& p, RecSmem<T, D,
     if (len > 1) stage(0, 0);
   }
   const bool active = ok();
+  if constexpr (!kOne) {
+    // (what is left out has its first tile on the way: it lands before the CTA ends)
+    if (!active) cp_async_wait<0>();
+  }
   [[maybe_unused]] T* out =
       static_cast<T*>(p.out) + (size_t)row0 * p.ldo + (size_t)h * D + slice * kSlice;
   if constexpr (!kOne) load_one();
