@@ -150,10 +150,12 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-def _index(t) -> Optional[int]:
-    """The address of a list of block indices."""
+def _index(t, device: Optional[int] = None) -> Optional[int]:
+    """The address of a list of block indices, on the pool's device."""
     if t.dtype != torch.int32 or not t.is_cuda or t.dim() != 1 or not t.is_contiguous():
         raise ValueError("block indices are a contiguous int32 CUDA tensor of one dimension")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"block indices on {t.device}: the pool is on cuda:{device}")
     return t.data_ptr()
 
 
@@ -215,7 +217,7 @@ class Pool:
         _check(load().gdn_state_pool_create(ctypes.byref(h), num_blocks, num_layers, Hk, Hv, dk,
                                             dv, K, self.act, block_align, _ptr(memory), nbytes),
                "gdn_state_pool_create")
-        self.handle = h
+        self.handle, self.device = h, torch.cuda.current_device()
         s, c, r, b = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_void_p()
         _check(load().gdn_state_pool_layout(h, ctypes.byref(s), ctypes.byref(c), ctypes.byref(r),
                                             ctypes.byref(b)), "gdn_state_pool_layout")
@@ -261,14 +263,15 @@ class Pool:
         at once (int32 device tensors), in one layer or (-1) in all."""
         if len(src) != len(dst):
             raise ValueError(f"{len(src)} sources and {len(dst)} destinations")
-        _check(load().gdn_state_pool_copy_blocks(self.handle, layer, _index(src), _index(dst),
-                                                 len(src), _stream(stream)),
+        dev = self.device
+        _check(load().gdn_state_pool_copy_blocks(self.handle, layer, _index(src, dev),
+                                                 _index(dst, dev), len(src), _stream(stream)),
                "gdn_state_pool_copy_blocks")
 
     def clear_blocks(self, idx, layer=-1, stream=None):
         """gdn_state_pool_clear_blocks: blocks idx (int32 device tensor) <- zeros."""
-        _check(load().gdn_state_pool_clear_blocks(self.handle, layer, _index(idx), len(idx),
-                                                  _stream(stream)),
+        _check(load().gdn_state_pool_clear_blocks(self.handle, layer, _index(idx, self.device),
+                                                  len(idx), _stream(stream)),
                "gdn_state_pool_clear_blocks")
 
     def compact(self, idx, new_idx=None, stream=None):
@@ -278,8 +281,9 @@ class Pool:
         new_idx = idx if new_idx is None else new_idx
         if len(idx) != len(new_idx):
             raise ValueError(f"{len(idx)} indices and room for {len(new_idx)}")
-        _check(load().gdn_state_pool_compact(self.handle, _index(idx), _index(new_idx), len(idx),
-                                             _stream(stream)), "gdn_state_pool_compact")
+        dev = self.device
+        _check(load().gdn_state_pool_compact(self.handle, _index(idx, dev), _index(new_idx, dev),
+                                             len(idx), _stream(stream)), "gdn_state_pool_compact")
         return new_idx
 
     def error_flags(self, layer=-1, reset=True, stream=None) -> int:
@@ -304,7 +308,7 @@ class SsdPool(Pool):
         _check(load().gdn_ssd_pool_create(ctypes.byref(h), num_blocks, num_layers, H, P, N, G, K,
                                           self.act, block_align, _ptr(memory), nbytes),
                "gdn_ssd_pool_create")
-        self.handle = h
+        self.handle, self.device = h, torch.cuda.current_device()
         s, c, r, b = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_void_p()
         _check(load().gdn_state_pool_layout(h, ctypes.byref(s), ctypes.byref(c), ctypes.byref(r),
                                             ctypes.byref(b)), "gdn_state_pool_layout")
@@ -343,18 +347,21 @@ class LinPool(Pool):
         self.num_blocks, self.num_layers = num_blocks, num_layers
         self.memory = memory
         h = ctypes.c_void_p()
+        if memory is not None and not (memory.is_contiguous() and memory.is_cuda and
+                                       memory.get_device() == torch.cuda.current_device()):
+            raise ValueError("the pool's memory is a contiguous tensor on the current CUDA device")
         nbytes = memory.numel() * memory.element_size() if memory is not None else 0
         _check(load().gdn_lin_pool_create(ctypes.byref(h), num_blocks, num_layers, H, d, self.act,
                                           block_align, _ptr(memory), nbytes),
                "gdn_lin_pool_create")
-        self.handle = h
+        self.handle, self.device = h, torch.cuda.current_device()
         s, c, r, b = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_void_p()
         _check(load().gdn_state_pool_layout(h, ctypes.byref(s), ctypes.byref(c), ctypes.byref(r),
                                             ctypes.byref(b)), "gdn_state_pool_layout")
         self.stride, self.conv_off, self.rec_off, self.base = s.value, c.value, r.value, b.value
 
 
-def _heads(t, name, heads, d, dtype, T):
+def _heads(t, name, heads, d, dtype, T, device):
     """(address, row pitch) of at least T rows of heads [T][heads][d]: any row
     pitch, the rows themselves dense."""
     shape, stride = t.shape, t.stride()
@@ -362,16 +369,18 @@ def _heads(t, name, heads, d, dtype, T):
         raise ValueError(f"{name} is [>= {T}][{heads}][{d}] of {dtype}: got {tuple(shape)} of "
                          f"{t.dtype}")
     rows = shape[0]
-    if rows and (stride[2] != 1 or (heads > 1 and stride[1] != d) or not t.is_cuda):
-        raise ValueError(f"the rows of {name} have to be dense, on a CUDA device")
+    if rows and (stride[2] != 1 or (heads > 1 and stride[1] != d) or not t.is_cuda or
+                 t.get_device() != device):
+        raise ValueError(f"the rows of {name} have to be dense, on cuda:{device}")
     return t.data_ptr(), stride[0] if rows > 1 else heads * d
 
 
-def _list(t, name, dtype, n):
+def _list(t, name, dtype, n, device):
     """The address of a dense device list of at least n elements."""
-    if t.dtype != dtype or t.numel() < n or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} is a contiguous CUDA tensor of >= {n} {dtype}: got {t.numel()} of "
-                         f"{t.dtype} on {t.device}")
+    if (t.dtype != dtype or t.numel() < n or not t.is_cuda or t.get_device() != device or
+            not t.is_contiguous()):
+        raise ValueError(f"{name} is a contiguous tensor of >= {n} {dtype} on cuda:{device}: got "
+                         f"{t.numel()} of {t.dtype} on {t.device}")
     return t.data_ptr()
 
 
@@ -380,18 +389,21 @@ def lin_varlen_forward(pool: LinPool, layer: int, q, k, v, cu_seqlens, state_blo
                        max_seqlen_hint: int = 0, stream=None) -> None:
     """gdn_lin_varlen_forward on device tensors: q and out [T][H][d], k and v
     [T][Hkv][d], each with any row pitch (views of a fused projection's rows)."""
-    H, d, dtype = pool.dims[2], pool.dims[3], pool.dtype
+    H, d, dtype, dev = pool.dims[2], pool.dims[3], pool.dtype, pool.device
+    if k.dim() != 3:
+        raise ValueError(f"k is [>= {T}][heads][{d}]: got {tuple(k.shape)}")
     Hkv = k.shape[1]
-    pq, ldq = _heads(q, "q", H, d, dtype, T)
-    pk, ldk = _heads(k, "k", Hkv, d, dtype, T)
-    pv, ldv = _heads(v, "v", Hkv, d, dtype, T)
-    po, ldo = _heads(out, "out", H, d, dtype, T)
+    pq, ldq = _heads(q, "q", H, d, dtype, T, dev)
+    pk, ldk = _heads(k, "k", Hkv, d, dtype, T, dev)
+    pv, ldv = _heads(v, "v", Hkv, d, dtype, T, dev)
+    po, ldo = _heads(out, "out", H, d, dtype, T, dev)
     _check(load().gdn_lin_varlen_forward(
         pool.handle, layer, pq, pk, pv, ldq, ldk, ldv, Hkv,
-        _list(cu_seqlens, "cu_seqlens", torch.int32, N + 1),
-        _list(state_block_idx, "state_block_idx", torch.int32, N),
-        _list(has_past, "has_past", torch.uint8, N), _list(log_decay, "log_decay", torch.float32, H),
-        scale, po, ldo, T, N, max_seqlen_hint, _stream(stream, cu_seqlens.get_device())),
+        _list(cu_seqlens, "cu_seqlens", torch.int32, N + 1, dev),
+        _list(state_block_idx, "state_block_idx", torch.int32, N, dev),
+        _list(has_past, "has_past", torch.uint8, N, dev),
+        _list(log_decay, "log_decay", torch.float32, H, dev),
+        scale, po, ldo, T, N, max_seqlen_hint, _stream(stream, dev)),
         "gdn_lin_varlen_forward")
 
 
