@@ -435,6 +435,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) move_blocks_kernel(MoveParams 
     for (int i = 0; i <= kSlots; ++i) mbar_init(&sm.full[warp][i], 1);
     fence_mbar_init();
   }
+  // (in this order: a scheduler behind this kernel may read the list that the
+  // plan has rewritten before it waits for this kernel)
   pdl_wait_then_release();
   int32_t* hdr = p.bw.header();
   const int ops = hdr[0], comps = hdr[1];

@@ -373,9 +373,12 @@ lin_recurrent_kernel(LinParams p) {
   constexpr int kSlices = D / kSlice;
   __shared__ __align__(16) RecSmem<T, D, kOne> sm;
   // late: launched behind the chunk kernel, whose idle SMs it takes without
-  // waiting for it (other sequences, other blocks); before it ends it waits,
-  // and computes what the chunk kernel has marked: columns whose blocks still
-  // hold the old state
+  // waiting for it (other sequences, other blocks; the scheduler's lists are
+  // there, as the chunk kernel releases after its own wait); before it ends it
+  // waits, and computes what the chunk kernel has marked: columns whose blocks
+  // still hold the old state.  A CTA keeps its place until then, so an SM that
+  // comes free takes one round of units beside the last chains, and the rest
+  // of the single tokens follow when the chunk kernel has ended.
   if (p.late)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   else

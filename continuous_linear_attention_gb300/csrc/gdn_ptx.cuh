@@ -68,8 +68,18 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
 // on the stream has completed and its writes are visible (returns at once for
 // a grid launched without the programmatic attribute), then allow the next
 // grid to be scheduled while this one runs (its own wait keeps it ordered).
-// Every kernel of a forward call runs this before its first global access,
-// so completion stays transitive along the call's kernels.
+// The order of a stream's kernels rests on these rules:
+//  - every kernel waits before it ends, so that its completion is also that of
+//    all before it, and writes to global memory before its wait only what no
+//    kernel before it touches;
+//  - a kernel that is to read global memory before its wait reads what the
+//    kernels before its predecessor have written, which is there if the
+//    predecessor releases after its own wait, as here.
+// Reading early are schedule_kernel (the call's lists; it also releases at
+// once, so none of its dependents may) and the late kernels behind a prompt
+// batch's last one (the scheduler's lists, the inputs and states of other
+// sequences; they release at once too).  plan_compact_kernel writes lists:
+// move_blocks_kernel, always behind it, must not release before its wait.
 __device__ __forceinline__ void pdl_wait_then_release() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -32,7 +32,9 @@ schedule_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ blk,
   __shared__ int32_t s_counts[kSmemCounts];
   // A programmatic dependent of the stream's previous kernel: the reads of
   // this call's inputs and the block counts (which only this kernel uses) run
-  // before griddepcontrol.wait, overlapping that kernel's tail; every write
+  // before griddepcontrol.wait, overlapping that kernel's tail (the library's
+  // own writer of such lists, the compaction's plan, has the moving kernel
+  // behind it, which lets this one start only once the plan is done); every write
   // the previous forward's kernels could still read (the header, the lists,
   // the records) comes after it.  The next kernel may launch at once.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
