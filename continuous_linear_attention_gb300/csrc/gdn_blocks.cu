@@ -13,10 +13,14 @@
 // come before source W[x], whose move overwrites x: a graph with one successor
 // per node, i.e. trees whose roots are last moves or cycles.  The planning
 // kernel orders the trees by their distance to the root (walked where it is
-// short, else by pointer jumping: 2 us more) and walks each cycle; a cycle's
+// short, else by pointer jumping: 2 us more) and lists each cycle from its
+// lowest block (one thread: 0.13 us a block, 0.2 above 8192 blocks); a cycle's
 // last source is first read into a spare buffer.  Components of that graph are
 // independent of each other, so the work is cut into (part of the components,
 // column).
+//
+// What depends on each other is moved one after the other: a chain or cycle of
+// all 8,191 blocks of 4 KB takes 0.77 us of moves a block.
 //
 // Measured: a reorder of 256 blocks of 2.1 MB in 3 layers 331 us, 0.95 of the
 // copy bandwidth; 400 blocks of 19 KiB in 8 layers 29 us, of which the plan takes
@@ -184,21 +188,29 @@ plan_copies_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ 
       int rounds = 1;
       while ((1 << rounds) < nb) ++rounds;
       // cycles: 2^rounds >= nb steps from a source that reaches one end on it,
-      // and every source of a cycle is such an end
-      for (int x = tid; x < nb; x += kPlanThreads) P[x] = cnt[x] > 0 ? W[x] : -1;
+      // and every source of a cycle is such an end; on the way the lowest block
+      // passed, which for a source of a cycle is the cycle's
+      for (int x = tid; x < nb; x += kPlanThreads) {
+        P[x] = cnt[x] > 0 ? W[x] : -1;
+        DP[x] = x;
+      }
       __syncthreads();
       cycles = true;
       for (int r = 0; r < rounds && cycles; ++r) {
         int more = 0;
         for (int x = tid; x < nb; x += kPlanThreads) {
-          const int y = P[x] < 0 ? -1 : P[P[x]];
+          const int z = P[x], y = z < 0 ? -1 : P[z];
           Q[x] = y;
+          DQ[x] = z < 0 ? DP[x] : min(DP[x], DP[z]);
           more |= y >= 0;
         }
         cycles = __syncthreads_or(more) != 0;
         int32_t* t = P;
         P = Q;
         Q = t;
+        t = DP;
+        DP = DQ;
+        DQ = t;
       }
       for (int x = tid; x < nb; x += kPlanThreads) Q[x] = 0;
       __syncthreads();
@@ -206,13 +218,13 @@ plan_copies_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ 
         for (int x = tid; x < nb; x += kPlanThreads)
           if (P[x] >= 0) Q[P[x]] = 1;
       __syncthreads();
-      // every other source's root (a last source, or one on a cycle) and its
-      // distance to it
+      // every other source's root (a last source, or the lowest of a cycle) and
+      // its distance to it (steps along the cycle count nothing)
       cyc = Q;
       nxt = P;
       for (int x = tid; x < nb; x += kPlanThreads) {
         const bool tree = cnt[x] > 0 && W[x] >= 0 && !cyc[x];
-        nxt[x] = tree ? W[x] : x;
+        nxt[x] = tree ? W[x] : cyc[x] ? DP[x] : x;
         DP[x] = tree ? 1 : 0;
       }
       __syncthreads();
@@ -237,8 +249,9 @@ plan_copies_kernel(const int32_t* __restrict__ src, const int32_t* __restrict__ 
     }
     for (int x = tid; x < nb; x += kPlanThreads)
       if (cnt[x] > 0) atomicMax(&s_depth, DP[x]);
-    // the lowest block of a cycle leads it: the root of its component
-    if (cycles)
+    // the lowest block of a cycle leads it: the root of its component (found by
+    // walking the short cycles, with the pointers on the others)
+    if (cycles && !far)
       for (int x = tid; x < nb; x += kPlanThreads)
         if (cyc[x] && cycle_moves(x)) {
           int z = x;
