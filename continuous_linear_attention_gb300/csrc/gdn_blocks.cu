@@ -22,9 +22,10 @@
 // What depends on each other is moved one after the other: a chain or cycle of
 // all 8,191 blocks of 4 KB takes 0.77 us of moves a block.
 //
-// Measured: a reorder of 256 blocks of 2.1 MB in 3 layers 331 us, 0.95 of the
-// copy bandwidth; 400 blocks of 19 KiB in 8 layers 29 us, of which the plan takes
-// 9; clearing 37 blocks in 6 layers 86 us, 5.5 TB/s of writes.
+// Measured (whole calls among others, the blocks out of cache): a reorder of 256
+// blocks of 2.1 MB in 3 layers 331 us, 0.95 of the copy bandwidth; 400 blocks of
+// 19 KiB in 8 layers 29 us, of which the plan takes 10; clearing 37 blocks in 6
+// layers 86 us, 5.5 TB/s of writes.
 //
 // Traffic: every distinct source is read once, however many destinations it
 // has, and every destination written once, the least the call can do.  The
@@ -472,11 +473,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) move_blocks_kernel(MoveParams 
   uint64_t* full = sm.full[warp];
 
   // The units: columns, narrowed while half of the warps would have nothing to
-  // do (six requests' beams of 143 KB blocks, 4 layers: 23 us, 39 with four
+  // do (six requests' beams of 143 KB blocks, 4 layers: 13 us, 26 with four
   // units per warp wherever possible), by parts of the components: eight units
   // per warp, but eight pieces in each where that leaves two (100 requests'
-  // beams of 19 KiB, 8 layers: 37 us, 41 with eight units each; at 64 requests'
-  // of 2.1 MB two per warp take 355 us and eight 339).
+  // beams of 19 KiB, 8 layers: 29 us, 32 with eight units each; at 64 requests'
+  // of 2.1 MB two per warp take 354 us and eight 331).
   const long long warps = (long long)gridDim.x * kWarps;
   int piece = kPiece;
   auto cols_of = [&](int b) { return (long long)((p.stride + b - 1) / b); };

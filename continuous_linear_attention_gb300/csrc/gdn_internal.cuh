@@ -148,7 +148,7 @@ struct SsdParams {
 
 // Launch with programmatic stream serialization: the grid may be scheduled
 // before the previous kernel on the stream completes; the kernel orders
-// itself with pdl_wait_then_release() before touching global memory.
+// itself with griddepcontrol.wait (the rules are at pdl_wait_then_release).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t stream, Args&&... args) {

@@ -12,9 +12,11 @@
 // independent of each other), every thread 4 columns of d/16 rows in registers;
 // all of a CTA's state loads are issued before anything else, and six CTAs per
 // SM keep about 100 KB of reads in flight: 256 requests x 32 heads 160 us,
-// 6.78 TB/s.  With more tokens the arithmetic (4 d^2 multiply-adds per token and
-// head with the decay, in packed fp32) shares the time: 64 requests of 4 tokens
-// x 32 heads 49 us, 0.83 of the copy bandwidth.
+// 6.78 TB/s (fp32 161; d = 64, 64 heads 86, 6.3 TB/s; d = 32, 128 heads 57, 4.9
+// TB/s: 4 KB of state a CTA).  With more tokens the arithmetic (4 d^2 multiply-adds
+// per token and head with the decay, in packed fp32) shares the time: 64
+// requests of 4 tokens x 32 heads 49 us, 0.82 of the copy bandwidth (fp32 64;
+// d = 64, 64 heads 37 and 39; d = 32, 128 heads 26 and 27).
 #include <cuda_runtime.h>
 
 #include <new>
@@ -36,11 +38,11 @@ constexpr int kRowT = kRecThreads / kColT;          // threads across the rows
 constexpr int kTile = 16;                           // tokens staged at a time
 // Calls of up to this many sequences check the batch in every CTA, while its
 // state loads are in flight, which saves the scheduler's launch: 256 single
-// tokens x 32 heads 164 us (167 with the scheduler), 512 x 16 heads 171 and 171,
-// 1,024 363 and 330; 128 times four tokens x 16 heads 54 (57), 256 101 and 100.
+// tokens x 32 heads 160 us (163 with the scheduler), 512 x 16 heads 167 and 166,
+// 1,024 358 and 328; 128 times four tokens x 16 heads 50 (52), 256 100 and 96.
 constexpr int kSelfCheck = 256;
 // groups of kRecThreads that work on segments side by side on an SM (their
-// shared memory: 184 KB of fp32 at d = 128)
+// shared memory: 176 KB of fp32 at d = 128)
 constexpr int kSerialPerSm = 4;
 
 // kN consecutive elements (kN * sizeof(T) aligned): as they lie, and as fp32.
@@ -361,8 +363,10 @@ __device__ __forceinline__ void recurrent_unit(const LinParams& p, RecSmem<T, D,
                                     !active || !p.has_past[s], state, state, ok);
 }
 
-// CTAs per SM, as many as the registers leave room for: state reads in flight
-// (64 requests of 4 tokens x 32 heads: 58 us with five, 54 with six and seven).
+// CTAs per SM, as many as the registers leave room for: state reads in flight.
+// 64 requests of 4 tokens with five, six and seven, which spill the more: bf16,
+// d = 128, 32 heads 54, 49 and 52 us, fp32 65, 64 and 71; d = 64, 64 heads 38,
+// 37 and 35, fp32 40, 39 and 40; fp32, d = 32, 128 heads 29, 27 and 27.
 constexpr int rec_ctas(int D, bool one) {
   return one && D < 128 ? 8 : 6;
 }

@@ -7,11 +7,16 @@ namespace gdn {
 
 constexpr int kLinChunk = 128;  // tokens per chunk of the chunked form
 constexpr int kLinSlices = 4;   // parts of 32 columns of a head's state (d = 128)
-// Sequences of up to this many tokens take the recurrent form.  64 sequences of
-// 32 heads: 95 us of 16 tokens (chunked form 105), 103 of 18 (104), 115 of 20
-// (106).  Where all its CTAs run at once the recurrent form is ahead for longer:
-// four sequences of 40 heads 25 us of 32 tokens (28), 29 of 40 (28); and longer
-// still with an SM for each: one sequence of 16 heads 17 us of 64 tokens (20).
+// Sequences of up to this many tokens take the recurrent form.  (Times, here as
+// in the other files of these operators: whole calls among others, their inputs
+// out of cache.)  64 sequences of 32 heads: 91 us of 16 tokens (chunked form
+// 118), 101 of 18 (118), 111 of 20 (119), 121 of 22 (120).  Where all its CTAs
+// run at once the recurrent form is ahead for longer: four sequences of 40 heads
+// 19.3 us of 28 tokens (19.3), 21.3 of 32 (19.8), one of 64 heads 12.4 of 32
+// (15.1), 17.2 of 48 (15.3); and longer still with an SM for each: one sequence
+// of 16 heads 11.7 us of 64 tokens (15.2), 16.4 of 96 (15.4).  (The lengths were
+// chosen when the chunked form was a little cheaper: they lie somewhat below
+// where the forms meet now.)
 constexpr int kLinShort = 18, kLinShortFew = 32, kLinShortLone = 64;
 
 // Header words of a layer's work area in these forwards (besides kErr, kNDec

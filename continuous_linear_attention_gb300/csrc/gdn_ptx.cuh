@@ -76,10 +76,12 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
 //    kernels before its predecessor have written, which is there if the
 //    predecessor releases after its own wait, as here.
 // Reading early are schedule_kernel (the call's lists; it also releases at
-// once, so none of its dependents may) and the late kernels behind a prompt
+// once, so the kernel behind it may not) and the late kernels behind a prompt
 // batch's last one (the scheduler's lists, the inputs and states of other
-// sequences; they release at once too).  plan_compact_kernel writes lists:
-// move_blocks_kernel, always behind it, must not release before its wait.
+// sequences; they release at once too, so that a scheduler may start beside
+// them and the kernel before them, which write no lists).  The one writer of
+// lists is plan_compact_kernel: move_blocks_kernel, always behind it, must not
+// release before its wait.
 __device__ __forceinline__ void pdl_wait_then_release() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -335,7 +335,8 @@ int gdn_ssd_varlen_forward(gdn_pool_t* pool, int layer, const void* xbc, const v
  *   block_stride = roundup(H*d*d*4, max(128, block_align)).
  * Supported: d in {32, 64, 128}, 1 <= H <= 4096, GDN_F32 or GDN_BF16 (q, k,
  * v, out).  Beside its blocks a pool holds 32 MiB for the states between the
- * segments of long sequences; gdn_state_pool_reserve has nothing to do for it.
+ * segments of long sequences (shared by its layers) and, for bf16 at d = 128,
+ * num_blocks * H * 4 bytes of marks; gdn_state_pool_reserve has nothing to do for it.
  * gdn_pool_last_prefill_path: GDN_PREFILL_FUSED where the chunked form (bf16,
  * d = 128) was launched for what the call may hold, GDN_PREFILL_SERIAL where
  * the recurrent form does all of it, GDN_PREFILL_NONE for single tokens. */
