@@ -50,6 +50,14 @@ EXPORTED = [
     "gdn_lin_pool_layout_for",
     "gdn_lin_pool_create",
     "gdn_lin_varlen_forward",
+    "gdn_sel_pool_layout_for",
+    "gdn_sel_pool_create",
+    "gdn_sel_conv_varlen_forward",
+    "gdn_sel_scan_varlen_forward",
+    "gdn_win_pool_layout_for",
+    "gdn_win_pool_create",
+    "gdn_win_varlen_forward",
+    "gdn_qk_norm_rope",
     "gdn_status_string",
 ]
 
@@ -70,6 +78,10 @@ class Weights(ctypes.Structure):
 class SsdWeights(ctypes.Structure):
     _fields_ = [("conv_w", ctypes.c_void_p), ("A_log", ctypes.c_void_p),
                 ("dt_bias", ctypes.c_void_p), ("D", ctypes.c_void_p)]
+
+
+class SelWeights(ctypes.Structure):
+    _fields_ = [("A_log", ctypes.c_void_p), ("D", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p)]
 
 
 _lib = None
@@ -119,6 +131,16 @@ def load() -> ctypes.CDLL:
     lib.gdn_lin_pool_create.argtypes = [ctypes.POINTER(P)] + [I] * 5 + [S, P, S]
     lib.gdn_lin_varlen_forward.argtypes = [P, I, P, P, P, L, L, L, I, P, P, P, P,
                                            ctypes.c_float, P, L, I, I, I, P]
+    F = ctypes.c_float
+    lib.gdn_sel_pool_layout_for.argtypes = [I] * 6 + [S, PS, PS, PS, PS]
+    lib.gdn_sel_pool_create.argtypes = [ctypes.POINTER(P)] + [I] * 6 + [S, P, S]
+    lib.gdn_sel_conv_varlen_forward.argtypes = [P, I, P, L] + [P] * 6 + [L, I, I, I, P]
+    lib.gdn_sel_scan_varlen_forward.argtypes = [P, I] + [P, L] * 5 + [P, P, P] + [
+        ctypes.POINTER(SelWeights), P, L, I, I, I, P]
+    lib.gdn_win_pool_layout_for.argtypes = [I] * 7 + [S, PS, PS, PS]
+    lib.gdn_win_pool_create.argtypes = [ctypes.POINTER(P)] + [I] * 7 + [S, P, S]
+    lib.gdn_win_varlen_forward.argtypes = [P, I, P, P, P, L, L, L, I, P, P, P, F, P, L, I, I, I, P]
+    lib.gdn_qk_norm_rope.argtypes = [P, P, L, L, P, P, I, I, P, P, F, F] + [I] * 5 + [P, P, L, L, P]
     lib.gdn_diag_umma_gemm.argtypes = [P, P, P, P, I, I, I, P]
     lib.gdn_diag_umma_gemm.restype = I
     lib.gdn_diag_umma_gemm_ex.argtypes = [P, P, P, P, I, I, I, I, I, P]
@@ -405,6 +427,182 @@ def lin_varlen_forward(pool: LinPool, layer: int, q, k, v, cu_seqlens, state_blo
         _list(log_decay, "log_decay", torch.float32, H, dev),
         scale, po, ldo, T, N, max_seqlen_hint, _stream(stream, dev)),
         "gdn_lin_varlen_forward")
+
+
+def sel_layout_for(num_blocks, num_layers, channels, N, K, act, block_align=0):
+    """(block_stride, conv_off, ssm_off, total_bytes) of a selective scan pool."""
+    out = [ctypes.c_size_t() for _ in range(4)]
+    _check(load().gdn_sel_pool_layout_for(num_blocks, num_layers, channels, N, K, act_code(act),
+                                          block_align, *[ctypes.byref(o) for o in out]),
+           "gdn_sel_pool_layout_for")
+    return tuple(o.value for o in out)
+
+
+def win_layout_for(num_blocks, num_layers, Hkv, d, window, sinks, act, block_align=0):
+    """(block_stride, v_off, total_bytes) of a windowed attention pool."""
+    out = [ctypes.c_size_t() for _ in range(3)]
+    _check(load().gdn_win_pool_layout_for(num_blocks, num_layers, Hkv, d, window, sinks,
+                                          act_code(act), block_align,
+                                          *[ctypes.byref(o) for o in out]),
+           "gdn_win_pool_layout_for")
+    return tuple(o.value for o in out)
+
+
+class _TypedPool(Pool):
+    """What the pools of the selective scan and of windowed attention share."""
+
+    def _create(self, create, dims, act, block_align, memory):
+        self.dims = tuple(dims)
+        self.act = act_code(act)
+        self.dtype = torch.float32 if self.act == GDN_F32 else torch.bfloat16
+        self.num_blocks, self.num_layers = dims[0], dims[1]
+        self.memory = memory
+        h = ctypes.c_void_p()
+        if memory is not None and not (memory.is_contiguous() and memory.is_cuda and
+                                       memory.get_device() == torch.cuda.current_device()):
+            raise ValueError("the pool's memory is a contiguous tensor on the current CUDA device")
+        nbytes = memory.numel() * memory.element_size() if memory is not None else 0
+        _check(getattr(load(), create)(ctypes.byref(h), *dims, self.act, block_align, _ptr(memory),
+                                       nbytes), create)
+        self.handle, self.device = h, torch.cuda.current_device()
+        s, c, r, b = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_void_p()
+        _check(load().gdn_state_pool_layout(h, ctypes.byref(s), ctypes.byref(c), ctypes.byref(r),
+                                            ctypes.byref(b)), "gdn_state_pool_layout")
+        self.stride, self.conv_off, self.rec_off, self.base = s.value, c.value, r.value, b.value
+
+
+class SelPool(_TypedPool):
+    """A selective scan pool (gdn_sel_pool_create): blocks of a conv state
+    [K-1][channels] and, at ``rec_off``, a state [channels][N] fp32.  With
+    ``memory`` the pool lives in that CUDA uint8 tensor."""
+
+    handle = None
+
+    def __init__(self, num_blocks, num_layers, channels, N, K, act, block_align=0,
+                 memory: Optional[torch.Tensor] = None):
+        self._create("gdn_sel_pool_create", (num_blocks, num_layers, channels, N, K), act,
+                     block_align, memory)
+
+
+class WinPool(_TypedPool):
+    """A windowed attention pool (gdn_win_pool_create): blocks of the keys
+    and, at ``rec_off``, the values [Hkv][sinks + window][d].  With ``memory``
+    the pool lives in that CUDA uint8 tensor."""
+
+    handle = None
+
+    def __init__(self, num_blocks, num_layers, Hkv, d, window, sinks, act, block_align=0,
+                 memory: Optional[torch.Tensor] = None):
+        self._create("gdn_win_pool_create", (num_blocks, num_layers, Hkv, d, window, sinks), act,
+                     block_align, memory)
+
+
+def _rows(t, name, cols, dtype, T, device):
+    """(address, row pitch) of at least T dense rows [T][cols], any row pitch."""
+    if t.dim() != 2 or t.shape[1] != cols or t.dtype != dtype or t.shape[0] < T:
+        raise ValueError(f"{name} is [>= {T}][{cols}] of {dtype}: got {tuple(t.shape)} of {t.dtype}")
+    if t.shape[0] and (t.stride(1) != 1 or not t.is_cuda or t.get_device() != device):
+        raise ValueError(f"the rows of {name} have to be dense, on cuda:{device}")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else cols
+
+
+def _maybe(t, name, dtype, n, device):
+    return None if t is None else _list(t, name, dtype, n, device)
+
+
+def sel_conv_varlen_forward(pool: SelPool, layer: int, x, cu_seqlens, state_block_idx, has_past,
+                            conv_w, conv_b, out, T: int, N: int, max_seqlen_hint: int = 0,
+                            stream=None) -> None:
+    """gdn_sel_conv_varlen_forward on device tensors: x and out [T][channels],
+    each with any row pitch; conv_w [channels][K], conv_b [channels] or None."""
+    C, K, dtype, dev = pool.dims[2], pool.dims[4], pool.dtype, pool.device
+    px, ldx = _rows(x, "x", C, dtype, T, dev)
+    po, ldo = _rows(out, "out", C, dtype, T, dev)
+    _check(load().gdn_sel_conv_varlen_forward(
+        pool.handle, layer, px, ldx,
+        _list(cu_seqlens, "cu_seqlens", torch.int32, N + 1, dev),
+        _list(state_block_idx, "state_block_idx", torch.int32, N, dev),
+        _list(has_past, "has_past", torch.uint8, N, dev),
+        _list(conv_w, "conv_w", dtype, C * K, dev), _maybe(conv_b, "conv_b", dtype, C, dev),
+        po, ldo, T, N, max_seqlen_hint, _stream(stream, dev)), "gdn_sel_conv_varlen_forward")
+
+
+def sel_scan_varlen_forward(pool: SelPool, layer: int, u, dt, B, C, z, cu_seqlens, state_block_idx,
+                            has_past, A_log, D, dt_bias, y, T: int, N: int,
+                            max_seqlen_hint: int = 0, stream=None) -> None:
+    """gdn_sel_scan_varlen_forward on device tensors: u, dt, z (or None) and y
+    [T][channels], B and C [T][d_state], each with any row pitch; A_log
+    [channels][d_state], D and dt_bias [channels] or None, fp32."""
+    chan, n, dtype, dev = pool.dims[2], pool.dims[3], pool.dtype, pool.device
+    rows = []
+    for t, name, cols in ((u, "u", chan), (dt, "dt", chan), (B, "B", n), (C, "C", n), (z, "z", chan)):
+        rows += (None, 0) if t is None and name == "z" else _rows(t, name, cols, dtype, T, dev)
+    py, ldy = _rows(y, "y", chan, dtype, T, dev)
+    w = SelWeights(_list(A_log, "A_log", torch.float32, chan * n, dev),
+                   _maybe(D, "D", torch.float32, chan, dev),
+                   _maybe(dt_bias, "dt_bias", torch.float32, chan, dev))
+    _check(load().gdn_sel_scan_varlen_forward(
+        pool.handle, layer, *rows,
+        _list(cu_seqlens, "cu_seqlens", torch.int32, N + 1, dev),
+        _list(state_block_idx, "state_block_idx", torch.int32, N, dev),
+        _list(has_past, "has_past", torch.uint8, N, dev), ctypes.byref(w), py, ldy, T, N,
+        max_seqlen_hint, _stream(stream, dev)), "gdn_sel_scan_varlen_forward")
+
+
+def win_varlen_forward(pool: WinPool, layer: int, q, k, v, cu_seqlens, state_block_idx, past_lens,
+                       out, T: int, N: int, scale: float = 1.0, max_seqlen_hint: int = 0,
+                       stream=None) -> None:
+    """gdn_win_varlen_forward on device tensors: q and out [T][H][d], k and v
+    [T][Hkv][d], each with any row pitch (views of a fused projection's rows);
+    past_lens [N] int32, the requests' tokens before this call."""
+    Hkv, d, dtype, dev = pool.dims[2], pool.dims[3], pool.dtype, pool.device
+    if q.dim() != 3:
+        raise ValueError(f"q is [>= {T}][heads][{d}]: got {tuple(q.shape)}")
+    H = q.shape[1]
+    pq, ldq = _heads(q, "q", H, d, dtype, T, dev)
+    pk, ldk = _heads(k, "k", Hkv, d, dtype, T, dev)
+    pv, ldv = _heads(v, "v", Hkv, d, dtype, T, dev)
+    po, ldo = _heads(out, "out", H, d, dtype, T, dev)
+    _check(load().gdn_win_varlen_forward(
+        pool.handle, layer, pq, pk, pv, ldq, ldk, ldv, H,
+        _list(cu_seqlens, "cu_seqlens", torch.int32, N + 1, dev),
+        _list(state_block_idx, "state_block_idx", torch.int32, N, dev),
+        _list(past_lens, "past_lens", torch.int32, N, dev),
+        scale, po, ldo, T, N, max_seqlen_hint, _stream(stream, dev)),
+        "gdn_win_varlen_forward")
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, q_out=None, k_out=None,
+                 eps: float = 1e-6, weight_offset: float = 0.0, interleaved: bool = False,
+                 stream=None):
+    """gdn_qk_norm_rope on device tensors: q [T][H][d] and k [T][Hkv][d] (k may
+    be None), each with any row pitch; positions [T] int32; inv_freq [rot/2]
+    fp32 (None: no rotation).  Without q_out and k_out in place.  Returns
+    (q_out, k_out)."""
+    if q.dim() != 3 or (k is not None and k.dim() != 3):
+        raise ValueError("q and k are [T][heads][d]")
+    T, H, d = q.shape
+    dtype, dev = q.dtype, q.get_device()
+    if not q.is_cuda or dev != torch.cuda.current_device():
+        raise ValueError(f"q is on {q.device}, not on the current CUDA device")
+    q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    if k is not None and k.shape[0] != T:
+        raise ValueError(f"{T} rows of q and {k.shape[0]} of k")
+    Hkv = 0 if k is None else k.shape[1]
+    pq, ldq = _heads(q, "q", H, d, dtype, T, dev)
+    pqo, ldqo = _heads(q_out, "q_out", H, d, dtype, T, dev)
+    pk, ldk = (None, 0) if k is None else _heads(k, "k", Hkv, d, dtype, T, dev)
+    pko, ldko = (None, 0) if k is None else _heads(k_out, "k_out", Hkv, d, dtype, T, dev)
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    _check(load().gdn_qk_norm_rope(
+        pq, pk, ldq, ldk, _list(positions, "positions", torch.int32, T, dev),
+        _maybe(inv_freq, "inv_freq", torch.float32, rot // 2, dev), rot, 1 if interleaved else 0,
+        _maybe(q_weight, "q_weight", torch.float32, d, dev),
+        _maybe(k_weight, "k_weight", torch.float32, d, dev), weight_offset, eps, T, H, Hkv, d,
+        act_code(dtype), pqo, pko, ldqo, ldko, _stream(stream, dev)), "gdn_qk_norm_rope")
+    return q_out, k_out
 
 
 def varlen_forward(pool: Pool, layer: int, x_qkv, a, b, cu_seqlens, state_block_idx, has_past,

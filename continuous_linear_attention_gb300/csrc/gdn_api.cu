@@ -390,6 +390,7 @@ int gdn_state_pool_destroy(gdn_pool_t* p) {
   if (p->owns) cudaFree(p->base);
   cudaFree(p->work);
   cudaFree(p->lin_states);
+  cudaFree(p->win_parts);
   scratch_release(p);
   if (prev >= 0) cudaSetDevice(prev);
   delete p;
@@ -486,7 +487,7 @@ int gdn_state_pool_reserve(gdn_pool_t* p, int max_tokens) {
   int prev = -1;
   cudaGetDevice(&prev);
   if (prev != p->device) return GDN_ERR_DEVICE;
-  if (p->kind == 2) return GDN_OK;  // its work memory is there from its creation on
+  if (p->kind >= 2) return GDN_OK;  // its work memory is there from its creation on
   if (max_tokens > 0) {
     p->scr_grow = true;
     return scratch_grow(p, scratch_units_for(p, max_tokens, max_tokens), 0, true);

@@ -23,14 +23,20 @@ struct gdn_pool {
   int last_path;  // GDN_PREFILL_* of the last forward
   // 0: gated delta net pool (conv + recurrent state); 1: Mamba2 pool (conv +
   // SSM state [H][P][N] at rec_off), with its dimensions; 2: decayed linear
-  // attention pool (state [Hv][dk][dv] at 0, no conv state)
+  // attention pool (state [Hv][dk][dv] at 0, no conv state); 3: selective scan
+  // pool (conv state, state [sel_C][sel_N] at rec_off); 4: windowed attention
+  // pool (keys, then values, [Hk][sinks + window][dk])
   int kind;
+  int sel_C, sel_N;
+  int window, sinks;
   int ssd_H, ssd_P, ssd_N, ssd_G;
   int32_t* blk_work;  // work area of the block operations (gdn::BlockWork)
   // decayed linear attention pools: states between the segments of a split
   // prompt, fp32 [lin_slots][dk][dv] (gdn_lin_chunk.cu), or NULL
   float* lin_states;
   int lin_slots;
+  // windowed attention pools: partial results of split windows (gdn_win.cu)
+  void* win_parts;
 };
 
 namespace gdn {

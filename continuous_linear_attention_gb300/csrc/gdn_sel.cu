@@ -1,0 +1,703 @@
+// The selective state space mixer's two stateful operations over a packed
+// batch, continued from each request's states in a paged pool (the mixers with
+// one decay per channel and state entry among the hybrid families of the model
+// support tracker): the short causal convolution with SiLU, and, behind the
+// projections that make the time step, B and C of its output, the scan
+//   dt = softplus(dt_raw + dt_bias),  A = -exp(A_log)
+//   h_t[n] = e^{dt A[n]} h_{t-1}[n] + dt u_t B_t[n]        (per channel, fp32)
+//   y_t = (sum_n h_t[n] C_t[n] + D u_t) * silu(z_t)
+// A block holds the conv state [K-1][C] (activation dtype) and the state
+// [C][N] fp32.
+//
+// This file: the kernels and the C entry points.
+#include <cuda_runtime.h>
+
+#include <new>
+
+#include "gdn_cta.cuh"
+#include "gdn_pool.cuh"
+#include "gdn_seqs.cuh"
+
+namespace gdn {
+namespace {
+
+template <typename T>
+struct Vec16 {  // 16 bytes of elements
+  static constexpr int kN = 16 / (int)sizeof(T);
+  uint4 w;
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(&w);
+    if constexpr (sizeof(T) == 4) return __uint_as_float(u[i]);
+    else return __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+  }
+};
+template <typename T>
+__device__ __forceinline__ Vec16<T> load16(const T* p) {
+  Vec16<T> v;
+  v.w = *reinterpret_cast<const uint4*>(p);
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ void store16(T* p, const float* f) {
+  uint4 w;
+  uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(f[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 p2 = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&p2);
+    }
+  }
+  *reinterpret_cast<uint4*>(p) = w;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// 2^x for a decay (x <= 0).  Near 0, where a state keeps its value over many
+// steps and a bias of the exponential adds up over as many (the hardware's is
+// about 2^-27 there: 2e-5 of the state after 3,000 steps of 2^-13), from its
+// series, whose next term is 1.3e-9 at -1/16, rounded to nearest.
+__device__ __forceinline__ float decay2(float x) {
+  const float p = fmaf(x, fmaf(x, fmaf(x, fmaf(x, 9.6181291e-3f, 5.5504109e-2f), 2.4022651e-1f), 6.9314718e-1f), 1.f);
+  const float a = ex2(x);
+  return x > -0.0625f ? p : a;
+}
+
+// --- convolution -------------------------------------------------------------
+// Bound by HBM: each input is read once (the K-1 rows before a piece twice, out
+// of L2) and each output written once.  A thread owns 16 bytes of channels and
+// walks the tokens of a piece with the K-1 inputs before in registers.
+constexpr int kConvThreads = 128;
+constexpr int kConvTokens = 32;  // per piece
+
+struct ConvParams {
+  Batch batch;
+  const void* x;
+  const void* w;     // [C][K]
+  const void* bias;  // [C] or NULL
+  void* out;
+  long long ldx, ldo;
+  unsigned char* layer_base;
+  size_t stride;
+  int C;
+  int tx;  // threads across the channels (a power of two); the others take pieces
+};
+
+template <typename T, int K>
+__global__ void __launch_bounds__(kConvThreads) sel_conv_kernel(ConvParams p) {
+  constexpr int kV = Vec16<T>::kN;
+  constexpr int kAhead = 8;  // tokens whose reads are on their way together
+  __shared__ PlanSmem plan;
+  pdl_wait_then_release();
+  const Batch& b = p.batch;
+  const SeqList list = b.listed ? listed_long(b)
+                                : plan_self(b, Pieces{1, 0x7fffffff, kConvTokens}, plan, blockIdx.x == 0);
+  const int vecs = p.C / kV, ch_blocks = (vecs + p.tx - 1) / p.tx, rows = kConvThreads / p.tx;
+  const int tx = threadIdx.x % p.tx, ty = threadIdx.x / p.tx;
+  const long long units = (long long)((list.total + rows - 1) / rows) * ch_blocks;
+  // (the grid is a multiple of ch_blocks, or all units: a CTA's channels stay the same)
+  const int c0 = ((int)(blockIdx.x % ch_blocks) * p.tx + tx) * kV;
+  if (c0 >= p.C) return;
+  float w[K][kV], bias[kV];
+  {
+    const T* wp = static_cast<const T*>(p.w) + (size_t)c0 * K;
+    float flat[K * kV];
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const Vec16<T> v = load16(wp + i * kV);
+#pragma unroll
+      for (int j = 0; j < kV; ++j) flat[i * kV + j] = v.at(j);
+    }
+#pragma unroll
+    for (int j = 0; j < kV; ++j)
+#pragma unroll
+      for (int k = 0; k < K; ++k) w[k][j] = flat[j * K + k];
+    Vec16<T> v;
+    v.w = make_uint4(0, 0, 0, 0);
+    if (p.bias) v = load16(static_cast<const T*>(p.bias) + c0);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) bias[j] = v.at(j);
+  }
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const int piece = (int)(u / ch_blocks) * rows + ty;
+    if (piece >= list.total) continue;
+    const int e = entry_of(list, piece), s = list.items[e];
+    const int at = (piece - list.first[e]) * kConvTokens;
+    const int row0 = b.cu[s], len = b.cu[s + 1] - row0, n = min(kConvTokens, len - at);
+    const T* x = static_cast<const T*>(p.x) + (size_t)row0 * p.ldx + c0;
+    T* out = static_cast<T*>(p.out) + (size_t)row0 * p.ldo + c0;
+    Vec16<T> win[K - 1];
+    if (at == 0) {
+      // the state, and (only this thread reads it) its new rows: the last K-1
+      // inputs, former ones among them where the sequence is short
+      T* st = reinterpret_cast<T*>(p.layer_base + (size_t)b.blk[s] * p.stride) + c0;
+      const bool past = b.has_past[s];
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) {
+        win[j].w = make_uint4(0, 0, 0, 0);
+        if (past) win[j] = load16(st + (size_t)j * p.C);
+      }
+      Vec16<T> next[K - 1];
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) {
+        const int t = len - (K - 1) + j;
+        if (t >= 0) {
+          next[j] = load16(x + (size_t)t * p.ldx);
+        } else {
+          next[j] = win[K - 2];
+#pragma unroll
+          for (int i = 0; i < K - 1; ++i)
+            if (i == t + K - 1) next[j] = win[i];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) *reinterpret_cast<uint4*>(st + (size_t)j * p.C) = next[j].w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) win[j] = load16(x + (size_t)(at - (K - 1) + j) * p.ldx);
+    }
+    for (int t = 0; t < n; t += kAhead) {
+      Vec16<T> in[K - 1 + kAhead];
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) in[j] = win[j];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (t + i < n) in[K - 1 + i] = load16(x + (size_t)(at + t + i) * p.ldx);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (t + i >= n) break;
+        float y[kV];
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+          float acc = bias[j];
+#pragma unroll
+          for (int k = 0; k < K; ++k) acc = fmaf(w[k][j], in[i + k].at(j), acc);
+          y[j] = silu_f32(acc);
+        }
+        store16(out + (size_t)(at + t + i) * p.ldo, y);
+      }
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) win[j] = in[kAhead + j];
+    }
+  }
+}
+
+// --- scan --------------------------------------------------------------------
+struct ScanParams {
+  Batch batch;
+  const void *u, *dt, *B, *C, *z;  // z may be NULL
+  void* y;
+  long long ldu, lddt, ldb, ldc, ldz, ldy;
+  const float *A_log, *D, *dt_bias;  // D and dt_bias may be NULL
+  unsigned char* layer_base;
+  size_t stride, ssm_off;
+  int channels;
+  int report;  // this kernel raises the batch's flags
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Single tokens: each state is read once and written once, bound by HBM.  A
+// thread has four entries of a channel's state; a CTA keeps its channels and
+// walks the sequences, kSeqs of them at a time on their way.
+constexpr int kStepThreads = 256;
+
+template <typename T, int N>
+__global__ void __launch_bounds__(kStepThreads) sel_step_kernel(ScanParams p) {
+  constexpr int kLanes = N / 4;  // threads per channel
+  constexpr int kSeqs = 4;
+  __shared__ PlanSmem plan;
+  pdl_wait_then_release();
+  const Batch& b = p.batch;
+  SeqList list;
+  if (b.listed) {
+    list.items = b.work.dec();
+    list.n = b.work.header()[kNDec];
+  } else {
+    list = plan_self(b, Pieces{1, 1, 1}, plan, p.report && blockIdx.x == 0 && blockIdx.y == 0);
+  }
+  const int c = (blockIdx.x * kStepThreads + threadIdx.x) / kLanes, g = threadIdx.x % kLanes;
+  const bool live = c < p.channels;
+  const size_t at = (size_t)(live ? c : 0) * N + g * 4;
+  const float4 al = *reinterpret_cast<const float4*>(p.A_log + at);
+  const float A[4] = {-expf(al.x) * kLog2e, -expf(al.y) * kLog2e, -expf(al.z) * kLog2e,
+                      -expf(al.w) * kLog2e};
+  const float bias = p.dt_bias && live ? p.dt_bias[c] : 0.f, skip = p.D && live ? p.D[c] : 0.f;
+  for (int i0 = blockIdx.y * kSeqs; i0 < list.n; i0 += gridDim.y * kSeqs) {
+    const int m = min(kSeqs, list.n - i0);
+    float4 h[kSeqs];
+    float* st[kSeqs];
+    float B[kSeqs][4], C[kSeqs][4], u[kSeqs], dt[kSeqs], z[kSeqs];
+    size_t row[kSeqs];
+#pragma unroll
+    for (int i = 0; i < kSeqs; ++i) {
+      if (i >= m || !live) continue;
+      const int s = list.items[i0 + i];
+      row[i] = b.cu[s];
+      st[i] = reinterpret_cast<float*>(p.layer_base + (size_t)b.blk[s] * p.stride + p.ssm_off) + at;
+      h[i] = b.has_past[s] ? *reinterpret_cast<const float4*>(st[i]) : make_float4(0.f, 0.f, 0.f, 0.f);
+      u[i] = to_f32(static_cast<const T*>(p.u)[row[i] * p.ldu + c]);
+      dt[i] = to_f32(static_cast<const T*>(p.dt)[row[i] * p.lddt + c]);
+      z[i] = p.z ? to_f32(static_cast<const T*>(p.z)[row[i] * p.ldz + c]) : 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        B[i][k] = to_f32(static_cast<const T*>(p.B)[row[i] * p.ldb + g * 4 + k]);
+        C[i][k] = to_f32(static_cast<const T*>(p.C)[row[i] * p.ldc + g * 4 + k]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kSeqs; ++i) {
+      if (i >= m) continue;  // (the same for the whole CTA)
+      float y = 0.f;
+      if (live) {
+        const float d = softplus_f32(dt[i] + bias), du = d * u[i];
+        h[i].x = fmaf(h[i].x, decay2(d * A[0]), du * B[i][0]);
+        h[i].y = fmaf(h[i].y, decay2(d * A[1]), du * B[i][1]);
+        h[i].z = fmaf(h[i].z, decay2(d * A[2]), du * B[i][2]);
+        h[i].w = fmaf(h[i].w, decay2(d * A[3]), du * B[i][3]);
+        *reinterpret_cast<float4*>(st[i]) = h[i];
+        y = fmaf(h[i].x, C[i][0], fmaf(h[i].y, C[i][1], fmaf(h[i].z, C[i][2], h[i].w * C[i][3])));
+      }
+#pragma unroll
+      for (int w = 1; w < kLanes; w <<= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
+      if (live && g == 0) {
+        y = fmaf(skip, u[i], y);
+        if (p.z) y *= silu_f32(z[i]);
+        static_cast<T*>(p.y)[row[i] * p.ldy + c] = from_f32<T>(y);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// Longer sequences: a CTA walks the tokens of one sequence for kCB channels,
+// kG threads per channel with N / kG states each in registers, a tile of kTT
+// tokens at a time, the next one on its way.
+constexpr int kScanThreads = 128;
+
+template <typename T, int N, int kG>
+struct ScanSmem {
+  static constexpr int kCB = kScanThreads / kG;
+  static constexpr int kTT = kG == 1 ? 16 : 32;
+  static constexpr int kPad = kG > 1 ? 32 / kG : 0;  // the lanes of a channel write rows of y: apart by banks
+  T u[2][kTT][kCB], dt[2][kTT][kCB], z[2][kTT][kCB];
+  T B[2][kTT][N], C[2][kTT][N];
+  float2 step[kTT][kCB];  // dt and dt u
+  float Bf[kTT][N], Cf[kTT][N];
+  float y[kTT][kCB + kPad];
+  PlanSmem plan;
+};
+
+template <typename T, int N, int kG>
+__global__ void __launch_bounds__(kScanThreads) sel_scan_kernel(ScanParams p) {
+  using Smem = ScanSmem<T, N, kG>;
+  constexpr int kCB = Smem::kCB, kTT = Smem::kTT, kNS = N / kG, kPer = 16 / (int)sizeof(T);
+  extern __shared__ __align__(16) unsigned char scan_smem[];
+  Smem& sm = *reinterpret_cast<Smem*>(scan_smem);
+  pdl_wait_then_release();
+  const Batch& b = p.batch;
+  const SeqList list =
+      b.listed ? listed_long(b)
+               : plan_self(b, Pieces{2, 0x7fffffff, 0x7fffffff}, sm.plan, p.report && blockIdx.x == 0);
+  const int ch_blocks = (p.channels + kCB - 1) / kCB;
+  const int piece = blockIdx.x / ch_blocks;
+  if (piece >= list.total) return;
+  const int s = list.items[entry_of(list, piece)];
+  const int cb = (int)(blockIdx.x % ch_blocks) * kCB;  // first channel
+  const int row0 = b.cu[s], len = b.cu[s + 1] - row0;
+  const int tid = threadIdx.x, c = tid / kG, g = tid % kG;
+  const bool live = cb + c < p.channels;
+  const int wide = min(kCB, p.channels - cb);
+
+  auto stage = [&](int t0, int buf) {
+    const int n = min(kTT, len - t0);
+    constexpr int kRow = kCB / kPer, kStates = N / kPer;
+    for (int i = tid; i < n * kRow; i += kScanThreads) {
+      const int t = i / kRow, x = i % kRow * kPer;
+      if (x >= wide) continue;
+      const size_t row = row0 + t0 + t;
+      cp_async16(&sm.u[buf][t][x], static_cast<const T*>(p.u) + row * p.ldu + cb + x);
+      cp_async16(&sm.dt[buf][t][x], static_cast<const T*>(p.dt) + row * p.lddt + cb + x);
+      if (p.z) cp_async16(&sm.z[buf][t][x], static_cast<const T*>(p.z) + row * p.ldz + cb + x);
+    }
+    for (int i = tid; i < n * kStates; i += kScanThreads) {
+      const int t = i / kStates, x = i % kStates * kPer;
+      const size_t row = row0 + t0 + t;
+      cp_async16(&sm.B[buf][t][x], static_cast<const T*>(p.B) + row * p.ldb + x);
+      cp_async16(&sm.C[buf][t][x], static_cast<const T*>(p.C) + row * p.ldc + x);
+    }
+    cp_async_commit();
+  };
+  stage(0, 0);
+
+  float* st = reinterpret_cast<float*>(p.layer_base + (size_t)b.blk[s] * p.stride + p.ssm_off) +
+              (size_t)(cb + c) * N + g * kNS;
+  float h[kNS], A[kNS];
+  const bool past = b.has_past[s];
+#pragma unroll
+  for (int i = 0; i < kNS; ++i) {
+    h[i] = live && past ? st[i] : 0.f;
+    A[i] = live ? -expf(p.A_log[(size_t)(cb + c) * N + g * kNS + i]) * kLog2e : 0.f;
+  }
+  for (int t0 = 0, buf = 0; t0 < len; t0 += kTT, buf ^= 1) {
+    const int n = min(kTT, len - t0);
+    if (t0 + kTT < len) {
+      stage(t0 + kTT, buf ^ 1);
+      cp_async_wait<1>();
+    } else {
+      cp_async_wait<0>();
+    }
+    __syncthreads();  // the tile has landed, and the last one's y is read
+    // the time steps, and B and C in fp32
+    for (int i = tid; i < n * kCB; i += kScanThreads) {
+      const int t = i / kCB, x = i % kCB;
+      if (x >= wide) continue;
+      const float d = softplus_f32(to_f32(sm.dt[buf][t][x]) + (p.dt_bias ? p.dt_bias[cb + x] : 0.f));
+      sm.step[t][x] = make_float2(d, d * to_f32(sm.u[buf][t][x]));
+    }
+    for (int i = tid; i < n * N; i += kScanThreads) {
+      (&sm.Bf[0][0])[i] = to_f32((&sm.B[buf][0][0])[i]);
+      (&sm.Cf[0][0])[i] = to_f32((&sm.C[buf][0][0])[i]);
+    }
+    __syncthreads();
+    for (int t = 0; t < n; t += kG) {
+      float part[kG];
+#pragma unroll
+      for (int k = 0; k < kG; ++k) {
+        part[k] = 0.f;
+        if (t + k >= n) continue;
+        const float2 d = sm.step[t + k][c];
+#pragma unroll
+        for (int i = 0; i < kNS; ++i) {
+          h[i] = fmaf(h[i], decay2(d.x * A[i]), d.y * sm.Bf[t + k][g * kNS + i]);
+          part[k] = fmaf(h[i], sm.Cf[t + k][g * kNS + i], part[k]);
+        }
+      }
+      // the sums over a channel's lanes: lane k ends up with token k's
+#pragma unroll
+      for (int w = kG / 2; w >= 1; w >>= 1) {
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+          const bool up = g & w;
+          const float send = up ? part[i] : part[i + w], keep = up ? part[i + w] : part[i];
+          part[i] = keep + __shfl_xor_sync(0xffffffffu, send, w);
+        }
+      }
+      if (t + g < n) sm.y[t + g][c] = part[0];
+    }
+    __syncthreads();
+    for (int i = tid; i < n * kCB; i += kScanThreads) {
+      const int t = i / kCB, x = i % kCB;
+      if (x >= wide) continue;
+      float y = sm.y[t][x];
+      if (p.D) y = fmaf(p.D[cb + x], to_f32(sm.u[buf][t][x]), y);
+      if (p.z) y *= silu_f32(to_f32(sm.z[buf][t][x]));
+      static_cast<T*>(p.y)[(size_t)(row0 + t0 + t) * p.ldy + cb + x] = from_f32<T>(y);
+    }
+    __syncthreads();  // the buffer may be staged over
+  }
+  if (live) {
+#pragma unroll
+    for (int i = 0; i < kNS; ++i) st[i] = h[i];
+  }
+}
+
+template <typename T, int N, int kG>
+cudaError_t launch_scan(const ScanParams& p, int max_items, cudaStream_t s) {
+  constexpr int kCB = kScanThreads / kG;
+  auto kern = sel_scan_kernel<T, N, kG>;
+  const size_t smem = sizeof(ScanSmem<T, N, kG>);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const long long ctas = (long long)max_items * ((p.channels + kCB - 1) / kCB);
+  return launch_pdl(kern, dim3((unsigned)ctas), dim3(kScanThreads), smem, s, p);
+}
+
+template <typename T, int N>
+cudaError_t launch_step(const ScanParams& p, int max_items, int sms, cudaStream_t s) {
+  const int per = kStepThreads / (N / 4), x = (p.channels + per - 1) / per;
+  int y = (4 * sms + x - 1) / x;  // about four CTAs per SM
+  const int most = (max_items + 3) / 4;
+  if (y > most) y = most;
+  return launch_pdl(sel_step_kernel<T, N>, dim3(x, y), dim3(kStepThreads), 0, s, p);
+}
+
+template <typename T>
+cudaError_t launch_scan_of(const ScanParams& p, int n, int max_long, int max_one, int sms,
+                           cudaStream_t s) {
+  ScanParams q = p;
+  cudaError_t e = cudaSuccess;
+  q.report = 1;
+  if (max_long > 0) {
+    e = n == 16   ? launch_scan<T, 16, 4>(q, max_long, s)
+        : n == 32 ? launch_scan<T, 32, 4>(q, max_long, s)
+                  : launch_scan<T, 64, 8>(q, max_long, s);
+    q.report = 0;
+  }
+  if (max_one > 0 && e == cudaSuccess)
+    e = n == 16   ? launch_step<T, 16>(q, max_one, sms, s)
+        : n == 32 ? launch_step<T, 32>(q, max_one, sms, s)
+                  : launch_step<T, 64>(q, max_one, sms, s);
+  return e;
+}
+
+template <typename T>
+cudaError_t launch_conv(const ConvParams& p, int K, unsigned ctas, cudaStream_t s) {
+  auto kern = K == 2 ? sel_conv_kernel<T, 2> : K == 3 ? sel_conv_kernel<T, 3> : sel_conv_kernel<T, 4>;
+  return launch_pdl(kern, dim3(ctas), dim3(kConvThreads), 0, s, p);
+}
+
+size_t roundup(size_t v, size_t m) { return (v + m - 1) / m * m; }
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+constexpr int kMaxChannels = 65536;
+
+int check_sel_dims(int num_blocks, int num_layers, int C, int N, int K, int act, size_t align) {
+  if (num_blocks < 2 || num_layers < 1) return GDN_ERR_RANGE;
+  if (C < 8 || C % 8 != 0 || C > kMaxChannels || (N != 16 && N != 32 && N != 64)) return GDN_ERR_DIMS;
+  if (K < 2 || K > kMaxConvK) return GDN_ERR_DIMS;
+  if (act != GDN_F32 && act != GDN_BF16) return GDN_ERR_DIMS;
+  if (align != 0 && (align < 128 || (align & (align - 1)) != 0)) return GDN_ERR_DIMS;
+  if ((long long)num_blocks * num_layers >= (1ll << 30)) return GDN_ERR_RANGE;
+  return GDN_OK;
+}
+
+size_t sel_ssm_off(int C, int K, int act) {
+  return roundup((size_t)(K - 1) * C * (act == GDN_F32 ? 4 : 2), 128);
+}
+size_t sel_stride(int C, int N, int K, int act, size_t align) {
+  return roundup(sel_ssm_off(C, K, act) + (size_t)C * N * sizeof(float), align > 128 ? align : 128);
+}
+
+// What both forwards check, in the order of the other forwards' checks.
+// *empty: nothing to do.
+int check_sel_call(const gdn_pool_t* p, int layer, int T, int N, int hint, bool* empty) {
+  *empty = false;
+  if (!p) return GDN_ERR_NULL;
+  if (p->kind != 3) return GDN_ERR_DIMS;
+  if (layer < 0 || layer >= p->num_layers || T < 0 || N < 0 || hint < 0) return GDN_ERR_RANGE;
+  if (N == 0) {
+    *empty = true;
+    return T == 0 ? GDN_OK : GDN_ERR_RANGE;
+  }
+  return GDN_OK;
+}
+
+// A row-wise tensor: [T] rows of cols elements, pitch ld.
+int check_rows(const void* t, int64_t ld, int64_t cols, int act) {
+  if (!aligned16(t) || ld % (act == GDN_F32 ? 4 : 8) != 0) return GDN_ERR_ALIGN;
+  return ld < cols || ld > (int64_t)1 << 38 ? GDN_ERR_RANGE : GDN_OK;
+}
+
+Batch batch_of(gdn_pool_t* p, int layer, const int32_t* cu, const int32_t* blk,
+               const uint8_t* has_past, int T, int N, int hint) {
+  Batch b = {};
+  b.cu = cu;
+  b.blk = blk;
+  b.has_past = has_past;
+  b.N = N;
+  b.T = T;
+  b.num_blocks = p->num_blocks;
+  b.hint = hint;
+  b.listed = N > kSelfPlan;
+  b.work.base = p->work + (size_t)layer * WorkArea::words(p->num_blocks);
+  b.work.num_blocks = p->num_blocks;
+  return b;
+}
+
+}  // namespace
+}  // namespace gdn
+
+extern "C" {
+
+int gdn_sel_pool_layout_for(int num_blocks, int num_layers, int channels, int d_state, int conv_k,
+                            int act, size_t block_align, size_t* block_stride, size_t* conv_off,
+                            size_t* ssm_off, size_t* total_bytes) {
+  const int st = gdn::check_sel_dims(num_blocks, num_layers, channels, d_state, conv_k, act, block_align);
+  if (st != GDN_OK) return st;
+  const size_t stride = gdn::sel_stride(channels, d_state, conv_k, act, block_align);
+  if (block_stride) *block_stride = stride;
+  if (conv_off) *conv_off = 0;
+  if (ssm_off) *ssm_off = gdn::sel_ssm_off(channels, conv_k, act);
+  if (total_bytes) *total_bytes = stride * (size_t)num_blocks * (size_t)num_layers;
+  return GDN_OK;
+}
+
+int gdn_sel_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int channels, int d_state,
+                        int conv_k, int act, size_t block_align, void* device_mem,
+                        size_t device_bytes) {
+  if (!out) return GDN_ERR_NULL;
+  *out = nullptr;
+  int st = gdn::check_sel_dims(num_blocks, num_layers, channels, d_state, conv_k, act, block_align);
+  if (st != GDN_OK) return st;
+  const size_t stride = gdn::sel_stride(channels, d_state, conv_k, act, block_align);
+  const size_t total = stride * (size_t)num_blocks * (size_t)num_layers;
+  if (device_mem) {
+    if (device_bytes < total) return GDN_ERR_NOMEM;
+    if (((uintptr_t)device_mem & 255u) != 0) return GDN_ERR_ALIGN;
+  }
+  gdn_pool* p = new (std::nothrow) gdn_pool();
+  if (!p) return GDN_ERR_NOMEM;
+  p->kind = 3;
+  p->num_blocks = num_blocks;
+  p->num_layers = num_layers;
+  p->sel_C = channels;
+  p->sel_N = d_state;
+  p->K = conv_k;
+  p->act = act;
+  p->last_path = GDN_PREFILL_NONE;
+  p->stride = stride;
+  p->rec_off = gdn::sel_ssm_off(channels, conv_k, act);
+  p->total = total;
+  st = gdn::pool_allocate(p, device_mem);
+  if (st != GDN_OK) {
+    delete p;
+    return st;
+  }
+  *out = p;
+  return GDN_OK;
+}
+
+int gdn_sel_conv_varlen_forward(gdn_pool_t* p, int layer, const void* x, int64_t ldx,
+                                const int32_t* cu_seqlens, const int32_t* state_block_idx,
+                                const uint8_t* has_past, const void* conv_w, const void* conv_b,
+                                void* out, int64_t ldo, int T, int N, int max_seqlen_hint,
+                                void* stream) {
+  bool empty;
+  int st = gdn::check_sel_call(p, layer, T, N, max_seqlen_hint, &empty);
+  if (st != GDN_OK || empty) return st;
+  if (!cu_seqlens || !state_block_idx || !has_past || !conv_w || (T > 0 && (!x || !out)))
+    return GDN_ERR_NULL;
+  if (!gdn::aligned16(conv_w) || !gdn::aligned16(conv_b)) return GDN_ERR_ALIGN;
+  if (T > 0) {
+    st = gdn::check_rows(x, ldx, p->sel_C, p->act);
+    if (st == GDN_OK) st = gdn::check_rows(out, ldo, p->sel_C, p->act);
+    if (st != GDN_OK) return st;
+  }
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GDN_ERR_CUDA;
+  if (dev != p->device) return GDN_ERR_DEVICE;
+  gdn::ConvParams cp = {};
+  cp.batch = gdn::batch_of(p, layer, cu_seqlens, state_block_idx, has_past, T, N, max_seqlen_hint);
+  cp.x = x;
+  cp.w = conv_w;
+  cp.bias = conv_b;
+  cp.out = out;
+  cp.ldx = ldx;
+  cp.ldo = ldo;
+  cp.layer_base = p->base + (size_t)layer * p->num_blocks * p->stride;
+  cp.stride = p->stride;
+  cp.C = p->sel_C;
+  const int vecs = cp.C / (p->act == GDN_F32 ? 4 : 8);
+  cp.tx = 1;
+  while (cp.tx < vecs && cp.tx < gdn::kConvThreads) cp.tx *= 2;
+  const int ch_blocks = (vecs + cp.tx - 1) / cp.tx, rows = gdn::kConvThreads / cp.tx;
+  // pieces, at most: every sequence's last one, and the full ones
+  long long pieces = (long long)T / gdn::kConvTokens + (N < T ? N : T);
+  if (pieces < 1) pieces = 1;
+  const long long units = (pieces + rows - 1) / rows * ch_blocks;
+  long long ctas = (long long)(12 * p->sms / ch_blocks > 0 ? 12 * p->sms / ch_blocks : 1) * ch_blocks;
+  if (ctas > units) ctas = units;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (cp.batch.listed &&
+      gdn::launch_plan(cp.batch, gdn::Pieces{1, 0x7fffffff, gdn::kConvTokens}, s) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  if (p->ev_before && cudaEventRecord(p->ev_before, s) != cudaSuccess) return GDN_ERR_CUDA;
+  const cudaError_t e = p->act == GDN_F32
+                            ? gdn::launch_conv<float>(cp, p->K, (unsigned)ctas, s)
+                            : gdn::launch_conv<__nv_bfloat16>(cp, p->K, (unsigned)ctas, s);
+  if (e != cudaSuccess) return GDN_ERR_CUDA;
+  if (p->ev_after && cudaEventRecord(p->ev_after, s) != cudaSuccess) return GDN_ERR_CUDA;
+  return GDN_OK;
+}
+
+int gdn_sel_scan_varlen_forward(gdn_pool_t* p, int layer, const void* u, int64_t ldu, const void* dt,
+                                int64_t lddt, const void* B, int64_t ldb, const void* C, int64_t ldc,
+                                const void* z, int64_t ldz, const int32_t* cu_seqlens,
+                                const int32_t* state_block_idx, const uint8_t* has_past,
+                                const gdn_sel_weights_t* w, void* y, int64_t ldy, int T, int N,
+                                int max_seqlen_hint, void* stream) {
+  if (!w) return GDN_ERR_NULL;
+  bool empty;
+  int st = gdn::check_sel_call(p, layer, T, N, max_seqlen_hint, &empty);
+  if (st != GDN_OK || empty) return st;
+  if (!cu_seqlens || !state_block_idx || !has_past || !w->A_log ||
+      (T > 0 && (!u || !dt || !B || !C || !y)))
+    return GDN_ERR_NULL;
+  if (!gdn::aligned16(w->A_log)) return GDN_ERR_ALIGN;
+  if (T > 0) {
+    const int chan = p->sel_C, n = p->sel_N;
+    st = gdn::check_rows(u, ldu, chan, p->act);
+    if (st == GDN_OK) st = gdn::check_rows(dt, lddt, chan, p->act);
+    if (st == GDN_OK) st = gdn::check_rows(B, ldb, n, p->act);
+    if (st == GDN_OK) st = gdn::check_rows(C, ldc, n, p->act);
+    if (st == GDN_OK && z) st = gdn::check_rows(z, ldz, chan, p->act);
+    if (st == GDN_OK) st = gdn::check_rows(y, ldy, chan, p->act);
+    if (st != GDN_OK) return st;
+  }
+  // (the grid: a CTA per sequence and 8 channels, at most)
+  if ((long long)N * (p->sel_C / 8) > 0x7fffffffll) return GDN_ERR_RANGE;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GDN_ERR_CUDA;
+  if (dev != p->device) return GDN_ERR_DEVICE;
+  gdn::ScanParams sp = {};
+  sp.batch = gdn::batch_of(p, layer, cu_seqlens, state_block_idx, has_past, T, N, max_seqlen_hint);
+  sp.u = u;
+  sp.dt = dt;
+  sp.B = B;
+  sp.C = C;
+  sp.z = z;
+  sp.y = y;
+  sp.ldu = ldu;
+  sp.lddt = lddt;
+  sp.ldb = ldb;
+  sp.ldc = ldc;
+  sp.ldz = ldz;
+  sp.ldy = ldy;
+  sp.A_log = w->A_log;
+  sp.D = w->D;
+  sp.dt_bias = w->dt_bias;
+  sp.layer_base = p->base + (size_t)layer * p->num_blocks * p->stride;
+  sp.stride = p->stride;
+  sp.ssm_off = p->rec_off;
+  sp.channels = p->sel_C;
+  // what the call can hold: single tokens, and longer sequences
+  int max_one = N < p->num_blocks - 1 ? N : p->num_blocks - 1;
+  if (max_one > T) max_one = T;
+  int max_long = max_one < T / 2 ? max_one : T / 2;
+  if (max_seqlen_hint == 1) max_long = 0;
+  if (N == 1 && T > 1) max_one = 0;
+  if (max_one == 0 && max_long == 0) max_one = 1;  // (a kernel that looks at the batch)
+  p->last_path = max_long > 0 ? GDN_PREFILL_SERIAL : GDN_PREFILL_NONE;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (sp.batch.listed && gdn::launch_plan(sp.batch, gdn::Pieces{2, 0x7fffffff, 0x7fffffff}, s) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  if (p->ev_before && cudaEventRecord(p->ev_before, s) != cudaSuccess) return GDN_ERR_CUDA;
+  const cudaError_t e =
+      p->act == GDN_F32
+          ? gdn::launch_scan_of<float>(sp, p->sel_N, max_long, max_one, p->sms, s)
+          : gdn::launch_scan_of<__nv_bfloat16>(sp, p->sel_N, max_long, max_one, p->sms, s);
+  if (e != cudaSuccess) return GDN_ERR_CUDA;
+  if (p->ev_after && cudaEventRecord(p->ev_after, s) != cudaSuccess) return GDN_ERR_CUDA;
+  return GDN_OK;
+}
+
+}  // extern "C"

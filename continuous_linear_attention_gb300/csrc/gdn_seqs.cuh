@@ -1,0 +1,194 @@
+// The sequences of a packed batch as the selective scan's and the windowed
+// attention's kernels take them: checked as the pool's contract demands, and
+// listed with a prefix of their pieces of work.  A call of up to
+// kSelfPlan sequences is listed by every CTA for itself, in shared memory (one
+// launch less); a larger one by plan_kernel, into the layer's work area.
+#pragma once
+
+#include "gdn_internal.cuh"
+#include "gdn_ptx.cuh"
+
+namespace gdn {
+
+constexpr int kSelfPlan = 256;
+
+struct Batch {
+  const int32_t* cu;
+  const int32_t* blk;
+  const uint8_t* has_past;  // or
+  const int32_t* past_len;  // tokens before the call (windowed attention)
+  int N, T, num_blocks, hint;
+  int listed;  // plan_kernel has run
+  WorkArea work;
+};
+
+// Which sequences a kernel takes, in pieces of how many tokens.
+struct Pieces {
+  int least, most;  // lengths
+  int tokens;       // of a piece
+  __host__ __device__ int of(int len) const {
+    return len < least || len > most ? 0 : (len - 1) / tokens + 1;
+  }
+};
+
+struct SeqList {
+  const int32_t* items;  // sequences with pieces
+  const int32_t* first;  // first[i]: pieces before items[i]; first[n]: all
+  int n, total;
+};
+
+constexpr int kPlanSlots = 2 * kSelfPlan;  // of the hash table that finds blocks named twice
+constexpr int kPlanSort = 32;              // lists of up to this many are put in order
+
+struct PlanSmem {
+  int32_t lo[kSelfPlan + 1], blk[kSelfPlan], len[kSelfPlan], items[kSelfPlan], first[kSelfPlan + 1];
+  int32_t named[kPlanSlots];  // a block index, kPlanTwice with it where two sequences name it
+  unsigned flags;
+  int n, total;
+};
+constexpr int kPlanTwice = 0x40000000;  // (block indices are below 2^30)
+
+// What is wrong with a sequence of len tokens by itself, as GDN_FLAG_* (0:
+// nothing; a padding entry or an empty sequence has nothing wrong either).
+__device__ __forceinline__ unsigned sequence_flags(const Batch& b, int s, int len, int blk) {
+  if (blk < 0 || len == 0) return 0u;
+  if (blk >= b.num_blocks) return GDN_FLAG_BLOCK_RANGE;
+  if (blk == 0) return GDN_FLAG_TRASH_WRITE;
+  if (b.hint > 0 && len > b.hint) return GDN_FLAG_HINT;
+  if (b.past_len) {
+    const int past = b.past_len[s];
+    if (past < 0 || past > 0x7fffffff - len) return GDN_FLAG_RANGE;
+  }
+  return 0u;
+}
+
+// Every thread of the CTA (whole warps): the list of a call of up to kSelfPlan
+// sequences.  raise: this CTA reports what is wrong.  A block named by two
+// sequences with tokens leaves both out.  Up to kPlanSort sequences are listed
+// longest first (of equals the lower index first), more in order of their
+// indices.  Some 250 instructions a warp, and the latency of two dependent reads.
+__device__ inline SeqList plan_self(const Batch& b, const Pieces& pieces, PlanSmem& sm, bool raise) {
+  const int tid = threadIdx.x, threads = blockDim.x, N = b.N;
+  if (tid == 0) {
+    sm.flags = 0u;
+    sm.n = sm.total = 0;
+  }
+  for (int i = tid; i < kPlanSlots; i += threads) sm.named[i] = -1;
+  for (int i = tid; i <= N; i += threads) sm.lo[i] = b.cu[i];
+  for (int i = tid; i < N; i += threads) sm.blk[i] = b.blk[i];
+  __syncthreads();
+  auto slot_of = [](int blk) { return (int)((unsigned)blk * 2654435761u >> 23); };
+  static_assert(kPlanSlots == 512, "nine bits of the hash");
+  int bad = tid == 0 && (sm.lo[0] != 0 || sm.lo[N] != b.T);
+  for (int i = tid; i < N; i += threads) {
+    const int lo = sm.lo[i], hi = sm.lo[i + 1], blk = sm.blk[i];
+    bad |= hi < lo;
+    if (hi <= lo || blk <= 0 || blk >= b.num_blocks) continue;
+    for (int at = slot_of(blk);; at = (at + 1) % kPlanSlots) {  // (half of the slots stay empty)
+      const int was = atomicCAS(&sm.named[at], -1, blk);
+      if (was == -1) break;
+      if ((was & ~kPlanTwice) == blk) {
+        atomicOr(&sm.named[at], kPlanTwice);
+        break;
+      }
+    }
+  }
+  SeqList list = {sm.items, sm.first, 0, 0};
+  if (__syncthreads_or(bad)) {
+    if (raise && tid == 0) atomicOr((unsigned*)&b.work.header()[kErr], GDN_FLAG_SEQLENS);
+    return list;
+  }
+  for (int i = tid; i < N; i += threads) {
+    int len = sm.lo[i + 1] - sm.lo[i];
+    const int blk = sm.blk[i];
+    unsigned flags = sequence_flags(b, i, len, blk);
+    if (len > 0 && blk > 0 && blk < b.num_blocks) {
+      int at = slot_of(blk);
+      while ((sm.named[at] & ~kPlanTwice) != blk) at = (at + 1) % kPlanSlots;
+      if (sm.named[at] & kPlanTwice) flags = GDN_FLAG_DUPLICATE;
+    }
+    if (flags && raise) atomicOr(&sm.flags, flags);
+    if (flags || blk < 0 || len == 0 || !pieces.of(len)) len = 0;  // nothing to do here
+    sm.len[i] = len;
+  }
+  __syncthreads();
+  if (raise && tid == 0 && sm.flags) atomicOr((unsigned*)&b.work.header()[kErr], sm.flags);
+  if (tid < 32) {
+    // the list's entries and pieces before each run of kRun sequences
+    constexpr int kRun = kSelfPlan / 32;
+    int n = 0, sum = 0;
+    for (int i = tid * kRun; i < min(N, (tid + 1) * kRun); ++i) {
+      const int len = sm.len[i];
+      n += len > 0;
+      sum += len > 0 ? pieces.of(len) : 0;
+    }
+    int n_upto = n, sum_upto = sum;
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, n_upto, w), y = __shfl_up_sync(0xffffffffu, sum_upto, w);
+      if (tid >= w) {
+        n_upto += x;
+        sum_upto += y;
+      }
+    }
+    const int all = __shfl_sync(0xffffffffu, n_upto, 31);
+    int at = n_upto - n, before = sum_upto - sum;
+    for (int i = tid * kRun; i < min(N, (tid + 1) * kRun); ++i) {
+      const int len = sm.len[i];
+      if (len == 0) continue;
+      sm.items[at] = i;
+      sm.first[at++] = before;
+      before += pieces.of(len);
+    }
+    if (tid == 31) {
+      sm.first[all] = sum_upto;
+      sm.n = all;
+      sm.total = sum_upto;
+    }
+    __syncwarp();
+    if (all <= kPlanSort && all > 1) {
+      const int mine = tid < all ? sm.items[tid] : -1, len = tid < all ? sm.len[mine] : 0;
+      const int count = tid < all ? pieces.of(len) : 0;
+      int rank = 0, ahead = 0;
+      for (int j = 0; j < all; ++j) {
+        const int lj = __shfl_sync(0xffffffffu, len, j), cj = __shfl_sync(0xffffffffu, count, j);
+        if (lj > len || (lj == len && j < tid)) {
+          ++rank;
+          ahead += cj;
+        }
+      }
+      if (tid < all) {
+        sm.items[rank] = mine;
+        sm.first[rank] = ahead;
+      }
+    }
+  }
+  __syncthreads();
+  list.n = sm.n;
+  list.total = sm.total;
+  return list;
+}
+
+// plan_kernel's lists: those of the longer sequences in pre() and pre_cp(), of
+// single tokens in dec() (a piece each: their first[] is not needed).
+__device__ inline SeqList listed_long(const Batch& b) {
+  const int32_t* hdr = b.work.header();
+  return {b.work.pre(), b.work.pre_cp(), hdr[kNPre], hdr[kPreChunks]};
+}
+
+// The list entry that piece u belongs to.
+__device__ __forceinline__ int entry_of(const SeqList& list, int u) {
+  int lo = 0, hi = list.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (list.first[mid] <= u) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// A call's sequences of pieces.least to pieces.most tokens into pre() and
+// pre_cp(), those of a single token (if pieces.least > 1) into dec(), in order
+// of their indices.
+cudaError_t launch_plan(const Batch& b, const Pieces& pieces, cudaStream_t s);
+
+}  // namespace gdn

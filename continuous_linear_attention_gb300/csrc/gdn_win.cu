@@ -1,0 +1,397 @@
+// Causal attention with a sliding window and a few first tokens that stay
+// visible, over a packed batch, continued from each request's keys and values
+// in its block of a paged pool (the windowed layers beside the linear ones in
+// hybrid models: their cache has a fixed size per request, as a linear layer's
+// state has).  Position p of a request sees j <= p with j > p - window or
+// j < sinks:
+//   o_p = sum_j w_j v_j / sum_j w_j,   w_j = e^{scale q_p k_j - m_p}
+// A block holds the keys and the values of the first `sinks` positions and of
+// a ring of the last `window` ones, per kv head.
+//
+// This file: the form for any type and shape, the append of the new keys and
+// values, and the C entry points.
+#include <cuda_runtime.h>
+
+#include <new>
+
+#include "gdn_cta.cuh"
+#include "gdn_pool.cuh"
+#include "gdn_win.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// --- any type and shape ------------------------------------------------------
+// A CTA takes kRows rows of one kv head (queries of consecutive tokens, the
+// heads that share the kv head next to each other) and walks the keys in tiles
+// of kKeys, with the running maximum and sum of the softmax: fp32 throughout.
+constexpr int kRowThreads = 128;
+constexpr int kRows = 32, kKeys = 32;
+
+template <int D>
+struct RowSmem {
+  float q[kRows][D + 4], k[kKeys][D + 4], v[kKeys][D + 4];
+  float p[kRows][kKeys + 1];  // the weights; -1: masked
+  float top[kRows], sum[kRows], shrink[kRows];
+  PlanSmem plan;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kRowThreads) win_rows_kernel(WinParams p, Pieces pieces) {
+  extern __shared__ __align__(16) unsigned char row_smem[];
+  RowSmem<D>& sm = *reinterpret_cast<RowSmem<D>*>(row_smem);
+  pdl_wait_then_release();
+  const Batch& b = p.batch;
+  const SeqList list = b.listed ? listed_long(b)
+                                : plan_self(b, pieces, sm.plan, p.report && blockIdx.x == 0);
+  const int subs = (p.group + kRows - 1) / kRows;  // parts of a token's heads
+  const int sub = blockIdx.x % subs, hk = blockIdx.x / subs % p.Hkv;
+  const int piece = blockIdx.x / (subs * p.Hkv);
+  if (piece >= list.total) return;
+  const int e = entry_of(list, piece), s = list.items[e];
+  const int t0 = (piece - list.first[e]) * pieces.tokens;
+  const int row0 = b.cu[s], len = b.cu[s + 1] - row0, past = b.past_len[s], blk = b.blk[s];
+  const int tokens = min(pieces.tokens, len - t0);
+  const int per = min(kRows, p.group - sub * kRows);  // heads of a token here
+  const int rows = subs > 1 ? per : tokens * p.group;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const T* ring_k = ring_of<T>(p, blk, 0, hk);
+  const T* ring_v = ring_of<T>(p, blk, 1, hk);
+  auto head = [&](int r) { return hk * p.group + sub * kRows + r % per; };
+  for (int i = tid; i < kRows * D; i += kRowThreads) {
+    const int r = i / D, c = i % D;
+    float x = 0.f;
+    if (r < rows)
+      x = to_f32(static_cast<const T*>(p.q)[(size_t)(row0 + t0 + r / per) * p.ldq +
+                                            (size_t)head(r) * D + c]);
+    sm.q[r][c] = x;
+  }
+  if (tid < kRows) {
+    sm.top[tid] = -INFINITY;
+    sm.sum[tid] = 0.f;
+  }
+  // the positions that any row sees: sinks before the window's first, then those
+  const int p0 = past + t0, p1 = p0 + tokens;
+  const int lo = max(0, p0 - p.window + 1), before = min(p.sinks, lo), n_keys = before + p1 - lo;
+  auto position = [&](int i) { return i < before ? i : lo + i - before; };
+  constexpr int kCols = D / 16;  // each thread's part of the output: 4 rows, D/16 columns
+  const int or0 = tid / 16 * 4, oc = tid % 16;
+  float acc[4][kCols];
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) acc[r][c] = 0.f;
+  const float to2 = p.scale * kLog2e;
+  for (int k0 = 0; k0 < n_keys; k0 += kKeys) {
+    const int n = min(kKeys, n_keys - k0);
+    __syncthreads();  // the last tile is read
+    for (int i = tid; i < n * D; i += kRowThreads) {
+      const int r = i / D, c = i % D, j = position(k0 + r);
+      const T *pk, *pv;
+      if (j < past) {
+        const size_t at = (size_t)slot_of(p, j) * D + c;
+        pk = ring_k + at;
+        pv = ring_v + at;
+      } else {
+        const size_t row = row0 + (j - past);
+        pk = static_cast<const T*>(p.k) + row * p.ldk + (size_t)hk * D + c;
+        pv = static_cast<const T*>(p.v) + row * p.ldv + (size_t)hk * D + c;
+      }
+      sm.k[r][c] = to_f32(*pk);
+      sm.v[r][c] = to_f32(*pv);
+    }
+    __syncthreads();
+    // scores: a warp has 8 rows, a lane one key
+    const int j = lane < n ? position(k0 + lane) : 0;
+    float sc[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) sc[r] = 0.f;
+    if (lane < n) {
+#pragma unroll 4
+      for (int c = 0; c < D; c += 4) {
+        const float4 kk = *reinterpret_cast<const float4*>(&sm.k[lane][c]);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const float4 qq = *reinterpret_cast<const float4*>(&sm.q[warp * 8 + r][c]);
+          sc[r] = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, fmaf(qq.z, kk.z, fmaf(qq.w, kk.w, sc[r]))));
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int row = warp * 8 + r;
+      const bool seen = row < rows && lane < n && sees(p, p0 + row / per, j);
+      const float x = seen ? sc[r] * to2 : -INFINITY;
+      float m = x;
+#pragma unroll
+      for (int w = 16; w >= 1; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+      const float was = sm.top[row], top = fmaxf(was, m);
+      // (nothing but -inf so far: any number in the maximum's place)
+      const float base = top == -INFINITY ? 0.f : top;
+      const float w = seen ? exp2f(x - base) : 0.f;
+      float sum = w;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      sm.p[row][lane] = seen ? w : -1.f;
+      __syncwarp();
+      if (lane == 0) {
+        const float shrink = exp2f(was - base);
+        sm.top[row] = top;
+        sm.sum[row] = fmaf(sm.sum[row], shrink, sum);
+        sm.shrink[row] = shrink;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float f = sm.shrink[or0 + r];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) acc[r][c] *= f;
+    }
+    for (int i = 0; i < n; ++i) {
+      float w[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) w[r] = sm.p[or0 + r][i];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        const float vv = sm.v[i][oc + 16 * c];
+        // (a masked value is not touched: it may be infinite or NaN)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (!(w[r] < 0.f)) acc[r][c] = fmaf(w[r], vv, acc[r][c]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int row = or0 + r;
+    if (row >= rows) continue;
+    const float inv = 1.f / sm.sum[row];
+    T* o = static_cast<T*>(p.out) + (size_t)(row0 + t0 + row / per) * p.ldo + (size_t)head(row) * D;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) o[oc + 16 * c] = from_f32<T>(acc[r][c] * inv);
+  }
+}
+
+// --- the new keys and values into the blocks ----------------------------------
+// Behind the attention, which reads what they replace.
+constexpr int kAppendThreads = 256;
+constexpr int kAppendTokens = 16;  // per piece
+
+template <typename T>
+__global__ void __launch_bounds__(kAppendThreads) win_append_kernel(WinParams p, Pieces pieces) {
+  __shared__ PlanSmem plan;
+  pdl_wait_then_release();
+  const Batch& b = p.batch;
+  const SeqList list = b.listed ? listed_long(b) : plan_self(b, pieces, plan, p.report && blockIdx.x == 0);
+  const int row16 = p.Hkv * p.d * (int)sizeof(T) / 16, head16 = p.d * (int)sizeof(T) / 16;
+  for (int piece = blockIdx.x; piece < list.total; piece += gridDim.x) {
+    const int e = entry_of(list, piece), s = list.items[e];
+    const int t0 = (piece - list.first[e]) * pieces.tokens;
+    const int row0 = b.cu[s], len = b.cu[s + 1] - row0, past = b.past_len[s], blk = b.blk[s];
+    const int n = min(pieces.tokens, len - t0);
+    if (past + t0 >= p.sinks && t0 + n <= len - p.window) continue;  // out of every later window
+    for (int i = threadIdx.x; i < n * row16; i += kAppendThreads) {
+      const int t = t0 + i / row16, x = i % row16, hk = x / head16, c = x % head16;
+      const int j = past + t;
+      if (j >= p.sinks && t < len - p.window) continue;
+      const size_t at = (size_t)slot_of(p, j) * head16 + c;
+      const size_t row = row0 + t;
+      reinterpret_cast<uint4*>(ring_of<T>(p, blk, 0, hk))[at] =
+          reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + row * p.ldk + (size_t)hk * p.d)[c];
+      reinterpret_cast<uint4*>(ring_of<T>(p, blk, 1, hk))[at] =
+          reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + row * p.ldv + (size_t)hk * p.d)[c];
+    }
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_rows(const WinParams& p, const Pieces& of, unsigned ctas, cudaStream_t s) {
+  auto kern = win_rows_kernel<T, D>;
+  const size_t smem = sizeof(RowSmem<D>);
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(ctas), dim3(kRowThreads), smem, s, p, of);
+}
+
+size_t roundup(size_t v, size_t m) { return (v + m - 1) / m * m; }
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+int check_win_dims(int num_blocks, int num_layers, int Hkv, int d, int window, int sinks, int act,
+                   size_t align) {
+  if (num_blocks < 2 || num_layers < 1) return GDN_ERR_RANGE;
+  if (Hkv < 1 || Hkv > 1024 || (d != 32 && d != 64 && d != 128)) return GDN_ERR_DIMS;
+  if (window < 1 || window > (1 << 20) || sinks < 0 || sinks > 4096) return GDN_ERR_DIMS;
+  if (act != GDN_F32 && act != GDN_BF16) return GDN_ERR_DIMS;
+  if (align != 0 && (align < 128 || (align & (align - 1)) != 0)) return GDN_ERR_DIMS;
+  if ((long long)num_blocks * num_layers >= (1ll << 30)) return GDN_ERR_RANGE;
+  return GDN_OK;
+}
+
+size_t win_stride(int Hkv, int d, int window, int sinks, int act, size_t align) {
+  const size_t row = (size_t)d * (act == GDN_F32 ? 4 : 2);
+  return roundup(2 * (size_t)Hkv * ((size_t)window + sinks) * row, align > 128 ? align : 128);
+}
+
+}  // namespace
+
+cudaError_t launch_win_rows(const WinParams& p, int act, const Pieces& of, int max_pieces,
+                            cudaStream_t s) {
+  const int subs = (p.group + kRows - 1) / kRows;
+  const unsigned ctas = (unsigned)max_pieces * subs * p.Hkv;
+  if (act == GDN_F32)
+    return p.d == 32   ? launch_rows<float, 32>(p, of, ctas, s)
+           : p.d == 64 ? launch_rows<float, 64>(p, of, ctas, s)
+                       : launch_rows<float, 128>(p, of, ctas, s);
+  return p.d == 32   ? launch_rows<__nv_bfloat16, 32>(p, of, ctas, s)
+         : p.d == 64 ? launch_rows<__nv_bfloat16, 64>(p, of, ctas, s)
+                     : launch_rows<__nv_bfloat16, 128>(p, of, ctas, s);
+}
+
+
+cudaError_t launch_win_append(const WinParams& p, int act, const Pieces& of, int max_pieces, int sms,
+                              cudaStream_t s) {
+  const int ctas = max_pieces < 4 * sms ? max_pieces : 4 * sms;
+  auto kern = act == GDN_F32 ? win_append_kernel<float> : win_append_kernel<__nv_bfloat16>;
+  return launch_pdl(kern, dim3(ctas), dim3(kAppendThreads), 0, s, p, of);
+}
+
+}  // namespace gdn
+
+extern "C" {
+
+int gdn_win_pool_layout_for(int num_blocks, int num_layers, int num_kv_heads, int d, int window,
+                            int sinks, int act, size_t block_align, size_t* block_stride,
+                            size_t* v_off, size_t* total_bytes) {
+  const int st = gdn::check_win_dims(num_blocks, num_layers, num_kv_heads, d, window, sinks, act, block_align);
+  if (st != GDN_OK) return st;
+  const size_t stride = gdn::win_stride(num_kv_heads, d, window, sinks, act, block_align);
+  if (block_stride) *block_stride = stride;
+  if (v_off) *v_off = (size_t)num_kv_heads * ((size_t)window + sinks) * d * (act == GDN_F32 ? 4 : 2);
+  if (total_bytes) *total_bytes = stride * (size_t)num_blocks * (size_t)num_layers;
+  return GDN_OK;
+}
+
+int gdn_win_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int num_kv_heads, int d,
+                        int window, int sinks, int act, size_t block_align, void* device_mem,
+                        size_t device_bytes) {
+  if (!out) return GDN_ERR_NULL;
+  *out = nullptr;
+  int st = gdn::check_win_dims(num_blocks, num_layers, num_kv_heads, d, window, sinks, act, block_align);
+  if (st != GDN_OK) return st;
+  const size_t stride = gdn::win_stride(num_kv_heads, d, window, sinks, act, block_align);
+  const size_t total = stride * (size_t)num_blocks * (size_t)num_layers;
+  if (device_mem) {
+    if (device_bytes < total) return GDN_ERR_NOMEM;
+    if (((uintptr_t)device_mem & 255u) != 0) return GDN_ERR_ALIGN;
+  }
+  gdn_pool* p = new (std::nothrow) gdn_pool();
+  if (!p) return GDN_ERR_NOMEM;
+  p->kind = 4;
+  p->num_blocks = num_blocks;
+  p->num_layers = num_layers;
+  p->Hk = num_kv_heads;
+  p->dk = p->dv = d;
+  p->window = window;
+  p->sinks = sinks;
+  p->act = act;
+  p->last_path = GDN_PREFILL_NONE;
+  p->stride = stride;
+  p->rec_off = (size_t)num_kv_heads * ((size_t)window + sinks) * d * (act == GDN_F32 ? 4 : 2);
+  p->total = total;
+  st = gdn::pool_allocate(p, device_mem);
+  if (st != GDN_OK) {
+    delete p;
+    return st;
+  }
+  *out = p;
+  return GDN_OK;
+}
+
+int gdn_win_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* k, const void* v,
+                           int64_t ldq, int64_t ldk, int64_t ldv, int num_heads,
+                           const int32_t* cu_seqlens, const int32_t* state_block_idx,
+                           const int32_t* past_lens, float scale, void* out, int64_t ldo, int T,
+                           int N, int max_seqlen_hint, void* stream) {
+  if (!p) return GDN_ERR_NULL;
+  if (p->kind != 4) return GDN_ERR_DIMS;
+  if (layer < 0 || layer >= p->num_layers || T < 0 || N < 0 || max_seqlen_hint < 0)
+    return GDN_ERR_RANGE;
+  if (num_heads < 1 || num_heads > 4096 || num_heads % p->Hk != 0) return GDN_ERR_DIMS;
+  if (N == 0) return T == 0 ? GDN_OK : GDN_ERR_RANGE;
+  if (!cu_seqlens || !state_block_idx || !past_lens) return GDN_ERR_NULL;
+  if (T > 0 && (!q || !k || !v || !out)) return GDN_ERR_NULL;
+  const int d = p->dk;
+  const int per16 = p->act == GDN_F32 ? 4 : 8;
+  if (T > 0) {
+    if (!gdn::aligned16(q) || !gdn::aligned16(k) || !gdn::aligned16(v) || !gdn::aligned16(out) ||
+        ldq % per16 != 0 || ldk % per16 != 0 || ldv % per16 != 0 || ldo % per16 != 0)
+      return GDN_ERR_ALIGN;
+    const int64_t qcols = (int64_t)num_heads * d, kcols = (int64_t)p->Hk * d;
+    const int64_t most = (int64_t)1 << 38;
+    if (ldq < qcols || ldo < qcols || ldk < kcols || ldv < kcols || ldq > most || ldk > most ||
+        ldv > most || ldo > most)
+      return GDN_ERR_RANGE;
+  }
+  int max_items = N < p->num_blocks - 1 ? N : p->num_blocks - 1;
+  if (max_items > T) max_items = T;
+  // (the grid: a CTA per token and 32 heads at most)
+  if (((long long)T + max_items) * num_heads > 0x7fffffffll) return GDN_ERR_RANGE;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GDN_ERR_CUDA;
+  if (dev != p->device) return GDN_ERR_DEVICE;
+
+  gdn::WinParams wp = {};
+  gdn::Batch& b = wp.batch;
+  b.cu = cu_seqlens;
+  b.blk = state_block_idx;
+  b.past_len = past_lens;
+  b.N = N;
+  b.T = T;
+  b.num_blocks = p->num_blocks;
+  b.hint = max_seqlen_hint;
+  b.listed = N > gdn::kSelfPlan;
+  b.work.base = p->work + (size_t)layer * gdn::WorkArea::words(p->num_blocks);
+  b.work.num_blocks = p->num_blocks;
+  wp.q = q;
+  wp.k = k;
+  wp.v = v;
+  wp.out = out;
+  wp.ldq = ldq;
+  wp.ldk = ldk;
+  wp.ldv = ldv;
+  wp.ldo = ldo;
+  wp.scale = scale;
+  wp.layer_base = p->base + (size_t)layer * p->num_blocks * p->stride;
+  wp.stride = p->stride;
+  wp.H = num_heads;
+  wp.Hkv = p->Hk;
+  wp.group = num_heads / p->Hk;
+  wp.d = d;
+  wp.window = p->window;
+  wp.sinks = p->sinks;
+  wp.report = 1;
+  p->last_path = T > 1 && max_seqlen_hint != 1 ? GDN_PREFILL_SERIAL : GDN_PREFILL_NONE;
+
+  cudaStream_t s = (cudaStream_t)stream;
+  gdn::Pieces of = {1, 0x7fffffff, wp.group < gdn::kRows ? gdn::kRows / wp.group : 1};
+  auto most_pieces = [&](int tokens) {
+    const int n = T / tokens + max_items;
+    return n > 0 ? n : 1;  // (a kernel that looks at the batch)
+  };
+  if (b.listed && gdn::launch_plan(b, of, s) != cudaSuccess) return GDN_ERR_CUDA;
+  if (p->ev_before && cudaEventRecord(p->ev_before, s) != cudaSuccess) return GDN_ERR_CUDA;
+  if (gdn::launch_win_rows(wp, p->act, of, most_pieces(of.tokens), s) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  wp.report = 0;
+  if (!b.listed) of.tokens = gdn::kAppendTokens;
+  if (gdn::launch_win_append(wp, p->act, of, most_pieces(of.tokens), p->sms, s) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  if (p->ev_after && cudaEventRecord(p->ev_after, s) != cudaSuccess) return GDN_ERR_CUDA;
+  return GDN_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,42 @@
+// Windowed attention: parameters and helpers shared by its kernels.
+#pragma once
+
+#include "gdn_seqs.cuh"
+
+namespace gdn {
+
+// What the kernels of one gdn_win_varlen_forward get, by value.
+struct WinParams {
+  Batch batch;
+  const void *q, *k, *v;  // rows of H, Hkv and Hkv heads of d elements
+  void* out;
+  long long ldq, ldk, ldv, ldo;  // row pitches, elements
+  float scale;
+  unsigned char* layer_base;
+  size_t stride;
+  int H, Hkv, group, d;  // group = H / Hkv
+  int window, sinks;
+  int report;  // this kernel raises the batch's flags
+};
+
+// Where a block keeps position j: the first `sinks` ones at their own index,
+// the others in a ring behind them.
+__device__ __forceinline__ int slot_of(const WinParams& p, int j) {
+  return j < p.sinks ? j : p.sinks + (j - p.sinks) % p.window;
+}
+// A block's keys (part 0) or values (part 1) of kv head h: [sinks + window][d].
+template <typename T>
+__device__ __forceinline__ T* ring_of(const WinParams& p, int blk, int part, int h) {
+  return reinterpret_cast<T*>(p.layer_base + (size_t)blk * p.stride) +
+         (size_t)(part * p.Hkv + h) * (p.sinks + p.window) * p.d;
+}
+// Whether position pos sees position j.
+__device__ __forceinline__ bool sees(const WinParams& p, int pos, int j) {
+  return j <= pos && (j > pos - p.window || j < p.sinks);
+}
+
+cudaError_t launch_win_rows(const WinParams& p, int act, const Pieces& of, int max_pieces, cudaStream_t s);
+cudaError_t launch_win_append(const WinParams& p, int act, const Pieces& of, int max_pieces, int sms,
+                              cudaStream_t s);
+
+}  // namespace gdn

@@ -71,7 +71,8 @@ extern "C" {
 #define GDN_FLAG_DUPLICATE 0x8u   /* two active sequences name the same block: both skipped */
 #define GDN_FLAG_TIMEOUT 0x10u    /* a kernel's bounded wait gave up (its results are incomplete) */
 #define GDN_FLAG_HINT 0x20u       /* a sequence is longer than max_seqlen_hint: it was skipped */
-#define GDN_FLAG_RANGE 0x40u      /* Mamba2 pools only: an SSM state entering the chunked scan's
+#define GDN_FLAG_RANGE 0x40u      /* Windowed attention pools: a past length out of range, the sequence
+                                     was skipped.  Mamba2 pools: an SSM state entering the chunked scan's
                                      fp16 operand left the fp16 range (|value| > 65000); that
                                      sequence's results are invalid.  (The gated delta net
                                      forwards never raise it: a (sequence, v-head) whose chunked-
@@ -372,6 +373,152 @@ int gdn_lin_varlen_forward(gdn_pool_t* pool, int layer, const void* q, const voi
                            const int32_t* cu_seqlens, const int32_t* state_block_idx,
                            const uint8_t* has_past, const float* log_decay, float scale, void* out,
                            int64_t ldo, int T, int N, int max_seqlen_hint, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The selective state space mixers with one decay per channel and state entry
+ * (the other state space mixers among the families that the model support
+ * tracker lists with a conv state and an SSM state per request), in two
+ * operations, since their time step, B and C are projections of the
+ * convolution's output:
+ *   u     = SiLU(causal depthwise conv of x + bias)
+ *   dt    = softplus(dt_raw + dt_bias[c]),  A[c][n] = -exp(A_log[c][n])
+ *   h_t[c][n] = e^{dt A[c][n]} h_{t-1}[c][n] + dt u_t[c] B_t[n]     (fp32)
+ *   y_t[c] = (sum_n h_t[c][n] C_t[n] + D[c] u_t[c]) * SiLU(z_t[c])
+ * The pool is the same kind of paged pool (block 0 = trash, one block per
+ * request, overwritten in place; the destroy, layout, get_error and timing
+ * entry points and the block operations apply to it), with a block holding
+ *   conv state [K-1][C] activation dtype at offset 0, oldest row first
+ *   state      [C][N] fp32 at ssm_off = roundup(conv bytes, 128)
+ *   block_stride = roundup(ssm_off + state bytes, max(128, block_align)).
+ * Supported: C (channels) a multiple of 8 up to 65536, N (d_state) in
+ * {16, 32, 64}, 2 <= conv_k <= 4, GDN_F32 or GDN_BF16.  gdn_state_pool_reserve
+ * has nothing to do for it; gdn_pool_last_prefill_path after a scan:
+ * GDN_PREFILL_SERIAL where the call may have held more than single tokens. */
+typedef struct {
+  const float* A_log;    /* [C][N], 16-byte aligned */
+  const float* D;        /* [C] skip weight, or NULL: none */
+  const float* dt_bias;  /* [C], or NULL: none */
+} gdn_sel_weights_t;
+
+int gdn_sel_pool_layout_for(int num_blocks, int num_layers, int channels, int d_state, int conv_k,
+                            int act_dtype, size_t block_align, size_t* block_stride,
+                            size_t* conv_off, size_t* ssm_off, size_t* total_bytes);
+
+/* As gdn_state_pool_create, for a selective scan pool. */
+int gdn_sel_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int channels, int d_state,
+                        int conv_k, int act_dtype, size_t block_align, void* device_mem,
+                        size_t device_bytes);
+
+/* The convolution and SiLU over a packed batch, continued from the blocks'
+ * conv states, which are overwritten with the last K-1 inputs.
+ *   x, out : T rows of C channels, activation dtype, row pitches ldx, ldo
+ *            elements (views of wider rows; out must not overlap x)
+ *   conv_w : [C][K] activation dtype, w[c][K-1] multiplies the current token
+ *   conv_b : [C] activation dtype, or NULL: none
+ * Pointers are 16-byte aligned and pitches multiples of 16 bytes
+ * (GDN_ERR_ALIGN).  cu_seqlens, state_block_idx, has_past, T, N,
+ * max_seqlen_hint, the skip rules, error flags and stream contract: as
+ * gdn_varlen_forward.  Never synchronises; graph-capturable. */
+int gdn_sel_conv_varlen_forward(gdn_pool_t* pool, int layer, const void* x, int64_t ldx,
+                                const int32_t* cu_seqlens, const int32_t* state_block_idx,
+                                const uint8_t* has_past, const void* conv_w, const void* conv_b,
+                                void* out, int64_t ldo, int T, int N, int max_seqlen_hint,
+                                void* stream);
+
+/* The scan over a packed batch, continued from the blocks' states, which are
+ * overwritten.
+ *   u, dt : T rows of C channels, activation dtype (dt: before dt_bias)
+ *   B, C  : T rows of N, activation dtype (views of one projection's rows)
+ *   z     : T rows of C channels, or NULL: no gate
+ *   y     : T rows of C channels; must not overlap the inputs
+ * with their row pitches in elements; alignment and everything else as
+ * gdn_sel_conv_varlen_forward.  The state and all sums are fp32; y is rounded
+ * once.  An output row depends on its own and earlier tokens of its sequence
+ * only. */
+int gdn_sel_scan_varlen_forward(gdn_pool_t* pool, int layer, const void* u, int64_t ldu,
+                                const void* dt, int64_t lddt, const void* B, int64_t ldb,
+                                const void* C, int64_t ldc, const void* z, int64_t ldz,
+                                const int32_t* cu_seqlens, const int32_t* state_block_idx,
+                                const uint8_t* has_past, const gdn_sel_weights_t* weights, void* y,
+                                int64_t ldy, int T, int N, int max_seqlen_hint, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Causal attention with a sliding window and a few first tokens that stay
+ * visible (sinks): the softmax layers that hybrid models put beside their
+ * linear ones.  What such a layer keeps of a request has a fixed size, so it
+ * lives in a block of the same kind of paged pool (block 0 = trash, never
+ * read here; destroy, layout, get_error, timing events and the block
+ * operations apply to it): the keys, then at v_off the values, each
+ * [Hkv][sinks + window][d], of the first `sinks` positions (slot j: position j)
+ * and of a ring of the last `window` ones (position j >= sinks in slot
+ * sinks + (j - sinks) % window); block_stride = roundup(v_off * 2, max(128,
+ * block_align)).  With the number of the request's tokens so far (past_lens),
+ * which the caller keeps, a block is all there is of it.
+ * Supported: d in {32, 64, 128}, 1 <= Hkv <= 1024, 1 <= window <= 2^20,
+ * 0 <= sinks <= 4096, GDN_F32 or GDN_BF16.  gdn_state_pool_reserve has nothing
+ * to do for it. */
+int gdn_win_pool_layout_for(int num_blocks, int num_layers, int num_kv_heads, int d, int window,
+                            int sinks, int act_dtype, size_t block_align, size_t* block_stride,
+                            size_t* v_off, size_t* total_bytes);
+
+/* As gdn_state_pool_create, for a windowed attention pool. */
+int gdn_win_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int num_kv_heads, int d,
+                        int window, int sinks, int act_dtype, size_t block_align, void* device_mem,
+                        size_t device_bytes);
+
+/* Forward of one windowed attention layer over a packed batch: the query at
+ * position pos of its request (past_lens[s] + its index in the sequence) sees
+ * the keys of positions j <= pos with j > pos - window or j < sinks, from its
+ * block and from this call's tokens,
+ *   o = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q.k_j - max)
+ * and the block then holds the request's keys and values with this call's.
+ *   q, out : T rows of num_heads heads x d, row pitches ldq, ldo elements;
+ *            num_heads is a multiple of Hkv (head h reads kv head h / (num_heads / Hkv))
+ *   k, v   : T rows of Hkv heads x d, row pitches ldk, ldv
+ *   past_lens : [N] int32 device, the request's tokens before this call (0: a
+ *            new request, its block is not read)
+ * q, k, v and out are 16-byte aligned and their pitches multiples of 16 bytes
+ * (GDN_ERR_ALIGN); out must not overlap the inputs.  cu_seqlens,
+ * state_block_idx, T, N, max_seqlen_hint, the skip rules, error flags and
+ * stream contract: as gdn_varlen_forward; a past length below 0, or whose sum
+ * with the sequence's length passes 2^31 - 1, raises GDN_FLAG_RANGE and the
+ * sequence is skipped.  Scores, maxima, sums and outputs are fp32 (bf16: the
+ * weights are rounded to bf16 for their product with the values) and rounded
+ * once to the activation dtype.  What a query does not see does not
+ * change its output, NaN and infinities among it; slots that hold no position
+ * yet are not read.  Never synchronises; graph-capturable. */
+int gdn_win_varlen_forward(gdn_pool_t* pool, int layer, const void* q, const void* k,
+                           const void* v, int64_t ldq, int64_t ldk, int64_t ldv, int num_heads,
+                           const int32_t* cu_seqlens, const int32_t* state_block_idx,
+                           const int32_t* past_lens, float scale, void* out, int64_t ldo, int T,
+                           int N, int max_seqlen_hint, void* stream);
+
+/* Norms of queries and keys for each head, with the position rotation in the
+ * same pass, as attention layers apply them before gdn_win_varlen_forward (and
+ * callers of gdn_lin_varlen_forward may): per row and head
+ *   y = x / sqrt(mean_c(x_c^2) + eps) * (weight_c + weight_offset)
+ * (weight NULL: y = x), then for the pairs i < rot/2 of channels (a, b) =
+ * (i, i + rot/2), or (2i, 2i + 1) if interleaved, with the angle
+ * positions[t] * inv_freq[i] (exact for any position: it is reduced modulo a
+ * turn before it is rounded),
+ *   (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin)
+ * and channels from rot on as they are; fp32, rounded once.
+ *   q, k         : T rows of H and Hkv heads x d, row pitches in elements; H or
+ *                  Hkv may be 0
+ *   q_out, k_out : the same; each may be its input itself (same address and
+ *                  pitch) and must not overlap the inputs otherwise
+ *   positions    : [T] int32 device; rows of a negative position are left out
+ *                  (not written)
+ *   inv_freq     : [rot/2] fp32 device (NULL if rot is 0)
+ *   q_weight, k_weight : [d] fp32 device, or NULL
+ * Supported: d in {32, 64, 128, 256}, rot even and at most d, H and Hkv up to
+ * 4096.  Alignment as gdn_win_varlen_forward.  Works on the current device;
+ * never synchronises; graph-capturable; needs no pool. */
+int gdn_qk_norm_rope(const void* q, const void* k, int64_t ldq, int64_t ldk,
+                     const int32_t* positions, const float* inv_freq, int rot, int interleaved,
+                     const float* q_weight, const float* k_weight, float weight_offset, float eps,
+                     int T, int H, int Hkv, int d, int act_dtype, void* q_out, void* k_out,
+                     int64_t ldqo, int64_t ldko, void* stream);
 
 /* Bytes of prefill scratch the split prefill needs for calls of at most
  * max_tokens tokens (any number of sequences) on a pool of these dimensions
