@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Batch b, Pieces piec
     if (blk > 0 && blk < nb && b.cu[i + 1] > b.cu[i]) atomicAdd(&uses[blk], 1);
   }
   __syncthreads();
-  int n_long = 0, n_one = 0, before = 0;  // so far
+  int n_long = 0, n_rest = 0, before = 0;  // so far
   for (int i0 = 0; i0 < N; i0 += kPlanThreads) {
     const int i = i0 + tid;
     int len = 0, mine = 0;
@@ -46,26 +46,26 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Batch b, Pieces piec
       if (flags || blk < 0) len = 0;
       mine = len > 0 ? pieces.of(len) : 0;
     }
-    const bool one = mine == 0 && len == 1;
+    const bool rest = mine == 0 && len > 0;
     int total;
     const int at = n_long + cta_scan(mine > 0, &total, warp_sums);
     n_long += total;
-    const int single = n_one + cta_scan(one, &total, warp_sums);
-    n_one += total;
+    const int other = n_rest + cta_scan(rest, &total, warp_sums);
+    n_rest += total;
     const int first = before + cta_scan(mine, &total, warp_sums);
     before += total;
     if (mine > 0) {
       b.work.pre()[at] = i;
       b.work.pre_cp()[at] = first;
-    } else if (one) {
-      b.work.dec()[single] = i;
+    } else if (rest) {
+      b.work.dec()[other] = i;
     }
   }
   __syncthreads();
   if (tid == 0) {
     b.work.pre_cp()[n_long] = before;
     hdr[kNPre] = n_long;
-    hdr[kNDec] = n_one;
+    hdr[kNDec] = n_rest;
     hdr[kPreChunks] = before;
     if (s_flags) atomicOr((unsigned*)&hdr[kErr], s_flags);
   }

@@ -169,8 +169,8 @@ __device__ inline SeqList plan_self(const Batch& b, const Pieces& pieces, PlanSm
   return list;
 }
 
-// plan_kernel's lists: those of the longer sequences in pre() and pre_cp(), of
-// single tokens in dec() (a piece each: their first[] is not needed).
+// plan_kernel's list of the sequences with pieces (the others are in dec(),
+// hdr[kNDec] of them).
 __device__ inline SeqList listed_long(const Batch& b) {
   const int32_t* hdr = b.work.header();
   return {b.work.pre(), b.work.pre_cp(), hdr[kNPre], hdr[kPreChunks]};
@@ -187,8 +187,7 @@ __device__ __forceinline__ int entry_of(const SeqList& list, int u) {
 }
 
 // A call's sequences of pieces.least to pieces.most tokens into pre() and
-// pre_cp(), those of a single token (if pieces.least > 1) into dec(), in order
-// of their indices.
+// pre_cp(), the others that have tokens into dec(), in order of their indices.
 cudaError_t launch_plan(const Batch& b, const Pieces& pieces, cudaStream_t s);
 
 }  // namespace gdn

@@ -307,6 +307,22 @@ int gdn_win_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int nu
     delete p;
     return st;
   }
+  if (gdn::win_short_supported(d, act)) {
+    const size_t room = gdn::win_short_room(p->sms, d);
+    if (cudaMalloc(&p->win_parts, room) != cudaSuccess) {
+      cudaGetLastError();
+      p->win_parts = nullptr;
+      gdn_state_pool_destroy(p);
+      return GDN_ERR_NOMEM;
+    }
+    // the arrival counters
+    if (cudaMemset(p->win_parts, 0, gdn::kWinCounterBytes) != cudaSuccess ||
+        cudaDeviceSynchronize() != cudaSuccess) {
+      cudaGetLastError();
+      gdn_state_pool_destroy(p);
+      return GDN_ERR_CUDA;
+    }
+  }
   *out = p;
   return GDN_OK;
 }
@@ -374,22 +390,34 @@ int gdn_win_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
   wp.window = p->window;
   wp.sinks = p->sinks;
   wp.report = 1;
-  p->last_path = T > 1 && max_seqlen_hint != 1 ? GDN_PREFILL_SERIAL : GDN_PREFILL_NONE;
 
   cudaStream_t s = (cudaStream_t)stream;
-  gdn::Pieces of = {1, 0x7fffffff, wp.group < gdn::kRows ? gdn::kRows / wp.group : 1};
+  // few tokens in a form of their own, where there is one
+  const int few = gdn::win_short_supported(d, p->act) ? gdn::win_short_tokens(wp.group) : 0;
+  const bool may_long = few == 0 || (T > few && (max_seqlen_hint == 0 || max_seqlen_hint > few));
+  const bool may_short = few > 0 && !(N == 1 && T > few);
+  gdn::Pieces of = {few + 1, 0x7fffffff, wp.group < gdn::kRows ? gdn::kRows / wp.group : 1};
+  const int max_long = max_items < T / (few + 1) ? max_items : T / (few + 1);
   auto most_pieces = [&](int tokens) {
-    const int n = T / tokens + max_items;
+    const int n = T / tokens + max_long;
     return n > 0 ? n : 1;  // (a kernel that looks at the batch)
   };
+  p->last_path = may_long && T > 1 && max_seqlen_hint != 1 ? GDN_PREFILL_SERIAL : GDN_PREFILL_NONE;
   if (b.listed && gdn::launch_plan(b, of, s) != cudaSuccess) return GDN_ERR_CUDA;
   if (p->ev_before && cudaEventRecord(p->ev_before, s) != cudaSuccess) return GDN_ERR_CUDA;
-  if (gdn::launch_win_rows(wp, p->act, of, most_pieces(of.tokens), s) != cudaSuccess)
-    return GDN_ERR_CUDA;
-  wp.report = 0;
-  if (!b.listed) of.tokens = gdn::kAppendTokens;
-  if (gdn::launch_win_append(wp, p->act, of, most_pieces(of.tokens), p->sms, s) != cudaSuccess)
-    return GDN_ERR_CUDA;
+  if (may_long) {
+    if (gdn::launch_win_rows(wp, p->act, of, most_pieces(of.tokens), s) != cudaSuccess)
+      return GDN_ERR_CUDA;
+    wp.report = 0;
+    if (!b.listed) of.tokens = gdn::kAppendTokens;
+    if (gdn::launch_win_append(wp, p->act, of, most_pieces(of.tokens), p->sms, s) != cudaSuccess)
+      return GDN_ERR_CUDA;
+  }
+  if (may_short) {
+    of = {1, few, 0x7fffffff};
+    if (gdn::launch_win_short(wp, of, max_items, p->sms, p->win_parts, s) != cudaSuccess)
+      return GDN_ERR_CUDA;
+  }
   if (p->ev_after && cudaEventRecord(p->ev_after, s) != cudaSuccess) return GDN_ERR_CUDA;
   return GDN_OK;
 }
