@@ -3,12 +3,12 @@
 // heads that share a kv head).
 //
 // Bound by HBM: a kv head's window streams in once for all of those rows.  A
-// block keeps it as one contiguous run of slots, so a producer warp brings it
-// into a ring of stages with bulk copies, kKeys slots of keys and values at a
+// block keeps it as one contiguous run of slots, so bulk copies bring it into a
+// ring of stages, kKeys slots of keys and values at a
 // time, whatever the positions in them: the softmax does not depend on the
 // keys' order, and slots that a row does not see are masked by their position.
-// The new tokens come as a last stage, a copy per row.  Four consumer warps
-// work on 16 keys each (or, with more than 16 rows, on a part of the rows and
+// The new tokens come as a last stage, a copy per row.  Four warps work on
+// 16 keys each (or, with more than 16 rows, on a part of the rows and
 // more keys): S = Q K^T and O += P V as m16n8k16 products of fragments read
 // from shared memory as they lie: the products' inner index may be in any order
 // that is the same for both sides, so a lane takes 16 consecutive channels'
@@ -33,8 +33,8 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kKeys = 64;     // per stage
 constexpr int kStages = 3;    // per CTA, two CTAs per SM
-constexpr int kWarps = 4;     // consumers
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxRows = 16 * kWarps;
 
 template <int D>
@@ -61,10 +61,6 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack(float a, float b) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&p);
-}
-// The consumer warps' barrier.
-__device__ __forceinline__ void consumer_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -138,48 +134,61 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
     if (lane == 0) atomicOr((unsigned*)&b.work.header()[kErr], GDN_FLAG_TIMEOUT);
   };
 
-  if (warp == kWarps) {
-    // the producer
-    uint32_t fill = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
-      const Unit w = unit_of(p, list, u, parts);
-      const __nv_bfloat16* rk = ring_of<__nv_bfloat16>(p, w.blk, 0, w.hk);
-      const __nv_bfloat16* rv = ring_of<__nv_bfloat16>(p, w.blk, 1, w.hk);
-      for (int st = w.first; st < w.end; ++st, ++fill) {
-        const int slot = fill % kStages;
-        wait(&sm.empty[slot], (fill / kStages & 1) ^ 1);
-        if (dead) continue;
-        __syncwarp();
-        if (st < w.ring_stages) {
-          const int n = min(kKeys, w.slots - st * kKeys);
+  // Warp 0 brings the stages in: all of the first ones, and, whenever it has
+  // done with a stage, the one that takes the place of the stage before that (the
+  // other warps have left it long ago).  A dedicated warp would cost more: its
+  // share of the registers makes the others spill (361 us for 256 single tokens
+  // x 8 kv heads x 1,028 slots; TIME_256 like this).
+  uint32_t fill = 0;
+  int fill_u = blockIdx.x, fill_st = 0;
+  Unit fw;
+  if (warp == 0 && fill_u < units) {
+    fw = unit_of(p, list, fill_u, parts);
+    fill_st = fw.first;
+  }
+  auto bring = [&](uint32_t upto) {
+    while (fill < upto && fill_u < units) {
+      if (fill_st >= fw.end) {
+        fill_u += gridDim.x;
+        if (fill_u >= units) return;
+        fw = unit_of(p, list, fill_u, parts);
+        fill_st = fw.first;
+        continue;
+      }
+      const int slot = fill % kStages, st = fill_st;
+      wait(&sm.empty[slot], (fill / kStages & 1) ^ 1);
+      if (!dead) {
+        if (st < fw.ring_stages) {
           if (lane == 0) {
-            const uint32_t bytes = (uint32_t)n * D * 2;
+            const uint32_t bytes = (uint32_t)min(kKeys, fw.slots - st * kKeys) * D * 2;
             mbar_arrive_expect_tx(&sm.full[slot], 2 * bytes);
-            bulk_g2s(&sm.kv[slot][0][0][0], rk + (size_t)st * kKeys * D, bytes, &sm.full[slot]);
-            bulk_g2s(&sm.kv[slot][1][0][0], rv + (size_t)st * kKeys * D, bytes, &sm.full[slot]);
+            bulk_g2s(&sm.kv[slot][0][0][0],
+                     ring_of<__nv_bfloat16>(p, fw.blk, 0, fw.hk) + (size_t)st * kKeys * D, bytes,
+                     &sm.full[slot]);
+            bulk_g2s(&sm.kv[slot][1][0][0],
+                     ring_of<__nv_bfloat16>(p, fw.blk, 1, fw.hk) + (size_t)st * kKeys * D, bytes,
+                     &sm.full[slot]);
           }
         } else {
-          if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], (uint32_t)w.len * D * 4);
+          if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], (uint32_t)fw.len * D * 4);
           __syncwarp();
-          for (int i = lane; i < w.len; i += 32) {
-            const size_t row = w.row0 + i;
+          for (int i = lane; i < fw.len; i += 32) {
+            const size_t row = fw.row0 + i;
             bulk_g2s(&sm.kv[slot][0][i][0],
-                     static_cast<const __nv_bfloat16*>(p.k) + row * p.ldk + (size_t)w.hk * D, D * 2,
+                     static_cast<const __nv_bfloat16*>(p.k) + row * p.ldk + (size_t)fw.hk * D, D * 2,
                      &sm.full[slot]);
             bulk_g2s(&sm.kv[slot][1][i][0],
-                     static_cast<const __nv_bfloat16*>(p.v) + row * p.ldv + (size_t)w.hk * D, D * 2,
+                     static_cast<const __nv_bfloat16*>(p.v) + row * p.ldv + (size_t)fw.hk * D, D * 2,
                      &sm.full[slot]);
           }
         }
       }
+      ++fill;
+      ++fill_st;
     }
-    // what is on its way lands before this warp ends
-    for (uint32_t i = fill > kStages ? fill - kStages : 0; i < fill; ++i)
-      mbar_wait_bounded(&sm.full[i % kStages], i / kStages & 1);
-    return;
-  }
+  };
+  if (warp == 0) bring(kStages);
 
-  // a consumer
   const int g = lane >> 2, t = lane & 3;
   const float to2 = p.scale * kLog2e;
   uint32_t take = 0;
@@ -253,14 +262,16 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
             mma16816(sc[h], hi, x.z, x.w);
           }
         }
-        // this lane's values: keys 2t, 2t+1, 2t+8, 2t+9, channels 8g .. of each half
-        uint4 v[4][kHalves];
+        // this lane's keys' values: 2t, 2t+1, 2t+8, 2t+9, channels 8g .. of each half
         auto key_of = [&](int i) { return k0 + 2 * t + (i & 1) + 8 * (i >> 1); };
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int h = 0; h < kHalves; ++h)
-            v[i][h] = *reinterpret_cast<const uint4*>(&sm.kv[slot][1][key_of(i)][64 * h + 8 * g]);
+        auto value = [&](int i, int h) {
+          return *reinterpret_cast<const uint4*>(&sm.kv[slot][1][key_of(i)][64 * h + 8 * g]);
+        };
+        // position of key i (only of one that is there)
+        auto position = [&](int i) {
+          const int key = key_of(i), sl = st * kKeys + key;
+          return fresh ? w.past + key : sl < p.sinks ? sl : sl + (w.past - 1 - sl) / p.window * p.window;
+        };
         const int s0 = st * kKeys + k0;
         const bool partly = fresh || k0 + 16 > n || (s0 < m1 && s0 + 16 > m0) || (s0 < n1 && s0 + 16 > n0);
         unsigned seen = 0xffu;  // bit 2 i + r: row r sees key i
@@ -270,20 +281,16 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
           bool odd = false;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int key = key_of(i), sl = st * kKeys + key;
-            bool there = key < n;
-            int j = 0;  // its position
-            if (fresh) j = w.past + key;
-            else if (sl < p.sinks) j = sl;
-            else if (there) j = sl + (w.past - 1 - sl) / p.window * p.window;
+            if (key_of(i) >= n) continue;
+            const int j = position(i);
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-              if (there && sees(p, pos[r], j)) seen |= 1u << (2 * i + r);
+              if (sees(p, pos[r], j)) seen |= 1u << (2 * i + r);
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
-              if (!there) v[i][h] = make_uint4(0, 0, 0, 0);
+              const uint4 x4 = value(i, h);
+              const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
               // an exponent of all ones
-              const uint32_t x[4] = {v[i][h].x, v[i][h].y, v[i][h].z, v[i][h].w};
 #pragma unroll
               for (int c = 0; c < 4; ++c)
                 odd |= (x[c] & 0x7f80u) == 0x7f80u || (x[c] & 0x7f800000u) == 0x7f800000u;
@@ -338,10 +345,14 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
         if (!split) {
 #pragma unroll
           for (int h = 0; h < kHalves; ++h) {
-            const uint32_t x[4][4] = {{v[0][h].x, v[0][h].y, v[0][h].z, v[0][h].w},
-                                      {v[1][h].x, v[1][h].y, v[1][h].z, v[1][h].w},
-                                      {v[2][h].x, v[2][h].y, v[2][h].z, v[2][h].w},
-                                      {v[3][h].x, v[3][h].y, v[3][h].z, v[3][h].w}};
+            uint32_t x[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint4 v = value(i, h);
+              // (what lies behind the last key may be anything)
+              if (partly && key_of(i) >= n) v = make_uint4(0, 0, 0, 0);
+              x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const uint32_t pick = j & 1 ? 0x7632u : 0x5410u;
@@ -354,33 +365,29 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
           // what a row does not see does not reach it (0 times NaN would)
           const int lo = __reduce_min_sync(0xffffffffu, live[0] ? pos[0] : 0x7fffffff);
           const int hi = __reduce_max_sync(0xffffffffu, max(live[0] ? pos[0] : 0, live[1] ? pos[1] : 0));
-          for (int at = lo; at <= hi && lo != 0x7fffffff; ++at) {
-            bool mask[4];
+#pragma unroll 1
+          for (int at = lo; at <= hi; ++at) {
+            unsigned mask = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int key = key_of(i), sl = st * kKeys + key;
-              int j = 0;
-              if (fresh) j = w.past + key;
-              else if (sl < p.sinks) j = sl;
-              else if (key < n) j = sl + (w.past - 1 - sl) / p.window * p.window;
-              mask[i] = key < n && sees(p, at, j);
-            }
+            for (int i = 0; i < 4; ++i)
+              if (key_of(i) < n && sees(p, at, position(i))) mask |= 1u << i;
             const uint32_t at4[4] = {pos[0] == at ? a[0] : 0u, pos[1] == at ? a[1] : 0u,
                                      pos[0] == at ? a[2] : 0u, pos[1] == at ? a[3] : 0u};
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h)
+            for (int h = 0; h < kHalves; ++h) {
+              uint32_t x[4][4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint4 v = value(i, h);
+                if (!(mask >> i & 1)) v = make_uint4(0, 0, 0, 0);
+                x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
+              }
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
                 const uint32_t pick = j & 1 ? 0x7632u : 0x5410u;
-                uint32_t x[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint32_t word = (j >> 1) == 0 ? v[i][h].x : (j >> 1) == 1 ? v[i][h].y
-                                        : (j >> 1) == 2 ? v[i][h].z : v[i][h].w;
-                  x[i] = mask[i] ? word : 0u;
-                }
                 float c[4] = {0.f, 0.f, 0.f, 0.f};
-                mma16816(c, at4, __byte_perm(x[0], x[1], pick), __byte_perm(x[2], x[3], pick));
+                mma16816(c, at4, __byte_perm(x[0][j >> 1], x[1][j >> 1], pick),
+                         __byte_perm(x[2][j >> 1], x[3][j >> 1], pick));
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
                   if (pos[r] == at) {
@@ -388,12 +395,14 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
                     o[h][j][2 * r + 1] += c[2 * r + 1];
                   }
               }
+            }
           }
         }
       }
       if (st + 1 < w.end) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty[slot]);
+        if (warp == 0) bring(take + kStages);
       }
     }
 #pragma unroll
@@ -407,7 +416,7 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
     const int slot = (take + kStages - 1) % kStages;
     float* meet = reinterpret_cast<float*>(&sm.kv[slot][0][0][0]);  // [warp][16][D]
     static_assert(sizeof(sm.kv[0]) >= sizeof(float) * kWarps * 16 * D, "room for the parts");
-    consumer_sync();
+    __syncthreads();
     if (some) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -427,11 +436,11 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
         }
       }
     }
-    consumer_sync();
+    __syncthreads();
     const int unit = u / parts;  // whose parts meet
     float* mine_left = left + (size_t)u * part_floats<D>();
     // four columns of a row at a time
-    for (int i = tid; i < rows * (D / 4); i += 32 * kWarps) {
+    for (int i = tid; i < rows * (D / 4); i += kThreads) {
       const int row = i / (D / 4), c = i % (D / 4) * 4, tile = row >> 4, r = row & 15;
       float m = -INFINITY, l = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -466,24 +475,25 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
     bool last = true;
     if (parts > 1) {
       __threadfence();
-      consumer_sync();
+      __syncthreads();
       if (tid == 0) {
         sm.last = atomicAdd(&arrived[unit], 1) == parts - 1;
         if (sm.last) arrived[unit] = 0;  // for the next call
         __threadfence();
       }
-      consumer_sync();
+      __syncthreads();
       last = sm.last;
     }
     // (the stage's memory is read: the copies to come are ordered behind the writes above)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    if (parts == 1) consumer_sync();
+    if (parts == 1) __syncthreads();
     __syncwarp();
     if (some && lane == 0) mbar_arrive(&sm.empty[slot]);
+    if (warp == 0) bring(take + kStages);
     if (!last) continue;
     if (parts > 1) {
       const float* all = left + (size_t)unit * parts * part_floats<D>();
-      for (int i = tid; i < rows * (D / 4); i += 32 * kWarps) {
+      for (int i = tid; i < rows * (D / 4); i += kThreads) {
         const int row = i / (D / 4), c = i % (D / 4) * 4;
         float m = -INFINITY, l = 0.f;
         for (int k = 0; k < parts; ++k)
@@ -508,7 +518,7 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
       }
     }
     // the new keys and values into the block: all of this kv head's window has been read
-    for (int i = tid; i < 2 * w.len * (D / 8); i += 32 * kWarps) {
+    for (int i = tid; i < 2 * w.len * (D / 8); i += kThreads) {
       const int part = i / (w.len * (D / 8)), x = i % (w.len * (D / 8)), tok = x / (D / 8), c = x % (D / 8) * 8;
       const int j = w.past + tok;
       if (j >= p.sinks && tok < w.len - p.window) continue;  // out of every later window
@@ -517,7 +527,10 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
       *reinterpret_cast<uint4*>(ring_of<__nv_bfloat16>(p, w.blk, part, w.hk) + (size_t)slot_of(p, j) * D + c) =
           *reinterpret_cast<const uint4*>(src);
     }
-  }
+  }  // (where a wait gave up, what is on its way lands before the CTA ends)
+  if (warp == 0 && dead)
+    for (uint32_t i = fill > kStages ? fill - kStages : 0; i < fill; ++i)
+      mbar_wait_bounded(&sm.full[i % kStages], i / kStages & 1);
 }
 
 template <int D>
