@@ -3,23 +3,23 @@
 // heads that share a kv head).
 //
 // Bound by HBM: a kv head's window streams in once for all of those rows.  A
-// block keeps it as one contiguous run of slots, cut into groups of 16,
-// whatever the positions in them: the softmax does not depend on the keys'
-// order, and slots that a row does not see are masked by their position.  The
-// new tokens come as last groups.  Each of a CTA's four warps works on groups of
-// its own, with a ring of stages of its own that it fills itself with bulk
-// copies: no warp waits for another before the end of a unit (a ring that the
-// warps share takes 221 us for 256 single tokens x 8 kv heads x 1,028 slots, and
-// 361 with a warp for the copies alone, whose share of the registers makes the
-// others spill; this form TIME_256).  With more than 16 rows the warps take
-// different rows, and a group is read by several of them, out of L2.
-// S = Q K^T and O += P V are m16n8k16 products of fragments read from shared
-// memory as they lie: the products' inner index may be in any order that is the
-// same for both sides, so a lane takes 16 bytes of a key's channels at once, and
-// the output's columns in any order as well, so it takes 8 channels of a value at
-// once and pairs keys in registers.  At m = 16 the legacy tensor instruction is at
-// a tenth of its rate here, and tcgen05's least tile, 64 rows, would be mostly
-// padding.
+// block keeps it as one contiguous run of slots, whatever the positions in them:
+// the softmax does not depend on the keys' order, and slots that a row does not
+// see are masked by their position.  A producer warp brings it into a ring of
+// stages of 64 slots, keys and values, with bulk copies of 16 KB (d = 128), the
+// new tokens as last stages, a copy per row; four consumer warps work on 16 keys
+// each, or, with more than 8 rows, on a part of the rows and more keys.  What
+// counts is the bytes on their way: 256 single tokens x 8 kv heads x 1,028 slots
+// take 193 us, with a consumer that issues the copies 221, with stages of 32
+// slots 258, with a ring of 8 KB stages for each warp 203 (three of them) and 248
+// (two).
+// S^T = K Q^T and O^T += V^T P^T are m16n8k16 products (8 rows are their
+// narrow side) of fragments read from shared memory as they lie: the products'
+// inner index may be in any order that is the same for both sides, so a lane
+// takes 16 bytes of a key's channels at once, and the output's channels in any
+// order as well, so it takes 8 channels of a value at once and pairs keys in
+// registers.  With 8 rows the legacy tensor instruction is at a tenth of its rate
+// here, and tcgen05's least tile, 64 rows, would be mostly padding.
 //
 // P is rounded to bf16 as the product's operand (its sum is not): an output's
 // error is 2^-9 / sqrt(3) relative to the root of the sum of its squared terms, on top
@@ -37,18 +37,18 @@ namespace gdn {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kKeys = 16;     // per group
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxRows = 16 * kWarps;
+constexpr int kKeys = 64;     // per stage
+constexpr int kWarps = 4;     // consumers
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kMaxRows = 8 * kWarps;
 
 template <int D>
 struct ShortSmem {
-  static constexpr int kStages = D == 64 ? 6 : 3;  // 24 KB per warp; two CTAs per SM
-  __nv_bfloat16 kv[kWarps][kStages][2][kKeys][D];
-  float meet[kWarps][16][32];  // the warps' parts of an output, 32 columns at a time
-  uint64_t full[kWarps][kStages];
-  float top[kWarps][16], sum[kWarps][16];
+  static constexpr int kStages = 3 * (128 / D);  // 96 KB; two CTAs per SM
+  __nv_bfloat16 kv[kStages][2][kKeys][D];
+  float meet[kWarps][8][32];  // the warps' parts of an output, 32 columns at a time
+  uint64_t full[kStages], empty[kStages];
+  float top[kWarps][8], sum[kWarps][8];
   int last;
   PlanSmem plan;
 };
@@ -65,18 +65,31 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// The 8 x 8 matrix of 16-bit elements whose row lane / 4 this lane has two of, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack(float a, float b) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
-// A unit: one kv head of one sequence, and a part of its groups of keys.
+// The consumer warps' barrier.
+__device__ __forceinline__ void consumer_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// A unit: one kv head of one sequence, and a part of its stages.
 struct Unit {
   int s, hk, part;
   int row0, len, past, blk;
   int slots;        // of the block that hold a position
-  int ring_groups;  // behind them those of the new tokens
-  int first, end;   // groups of this part
-  int tiles;        // of 16 rows
+  int ring_stages;  // behind them those of the new tokens
+  int first, end;   // stages of this part
 };
 
 __device__ __forceinline__ Unit unit_of(const WinParams& p, const SeqList& list, const PlanSmem* plan,
@@ -91,12 +104,14 @@ __device__ __forceinline__ Unit unit_of(const WinParams& p, const SeqList& list,
   w.blk = plan ? plan->blk[w.s] : b.blk[w.s];
   w.past = b.past_len[w.s];
   w.slots = min(w.past, p.sinks + p.window);
-  w.ring_groups = (w.slots + kKeys - 1) / kKeys;
-  const int all = w.ring_groups + (w.len + kKeys - 1) / kKeys;
-  w.first = (int)((long long)all * w.part / parts);
-  w.end = (int)((long long)all * (w.part + 1) / parts);
-  const int rows = w.len * p.group;
-  w.tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  w.ring_stages = (w.slots + kKeys - 1) / kKeys;
+  const int all = w.ring_stages + (w.len + kKeys - 1) / kKeys;
+  w.first = 0;
+  w.end = all;
+  if (parts > 1) {
+    w.first = (int)((long long)all * w.part / parts);
+    w.end = (int)((long long)all * (w.part + 1) / parts);
+  }
   return w;
 }
 
@@ -116,8 +131,11 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
   extern __shared__ __align__(128) unsigned char short_smem[];
   ShortSmem<D>& sm = *reinterpret_cast<ShortSmem<D>*>(short_smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid < kWarps * kStages) {
-    mbar_init(&sm.full[0][0] + tid, 1);
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], kWarps);
+    }
     fence_mbar_init();
   }
   pdl_wait_then_release();
@@ -139,82 +157,84 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
     dead = true;
     if (lane == 0) atomicOr((unsigned*)&b.work.header()[kErr], GDN_FLAG_TIMEOUT);
   };
-  auto& ring = sm.kv[warp];
-
-  // This warp's groups are on their way kStages ahead, across the units' borders.
-  uint32_t fill = 0, take = 0, fill_slot = 0, slot = 0, phase = 0;
-  int fill_u = blockIdx.x, fill_g = 0;
-  Unit fw;
-  fw.end = 0;
-  auto fill_unit = [&]() {
-    if (fill_u >= units) return;
-    fw = unit_of(p, list, plan, fill_u, parts);
-    fill_g = fw.first + warp / fw.tiles;
-  };
-  fill_unit();
-  auto bring = [&]() {
-    while (fill < take + kStages && fill_u < units) {
-      if (fill_g >= fw.end) {
-        fill_u += gridDim.x;
-        fill_unit();
-        continue;
-      }
-      if (!dead) {
-        uint64_t* full = &sm.full[warp][fill_slot];
-        if (fill_g < fw.ring_groups) {
-          if (lane == 0) {
-            const uint32_t bytes = (uint32_t)min(kKeys, fw.slots - fill_g * kKeys) * D * 2;
-            mbar_arrive_expect_tx(full, 2 * bytes);
-            bulk_g2s(&ring[fill_slot][0][0][0],
-                     ring_of<__nv_bfloat16>(p, fw.blk, 0, fw.hk) + (size_t)fill_g * kKeys * D, bytes, full);
-            bulk_g2s(&ring[fill_slot][1][0][0],
-                     ring_of<__nv_bfloat16>(p, fw.blk, 1, fw.hk) + (size_t)fill_g * kKeys * D, bytes, full);
-          }
-        } else {
-          // a copy per row
-          const int i0 = (fill_g - fw.ring_groups) * kKeys, n = min(kKeys, fw.len - i0);
-          if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)n * D * 4);
-          __syncwarp();
-          const int part = lane >> 4, i = lane & 15;
-          const size_t row = fw.row0 + i0 + i;
-          if (i < n)
-            bulk_g2s(&ring[fill_slot][part][i][0],
-                     part ? static_cast<const __nv_bfloat16*>(p.v) + row * p.ldv + (size_t)fw.hk * D
-                          : static_cast<const __nv_bfloat16*>(p.k) + row * p.ldk + (size_t)fw.hk * D,
-                     D * 2, full);
-        }
-      }
-      ++fill;
-      if (++fill_slot == kStages) fill_slot = 0;
-      fill_g += kWarps / fw.tiles;
+  int slot = 0;  // the stage's place in the ring, and its round
+  uint32_t phase = 0;
+  auto next_stage = [&]() {
+    if (++slot == kStages) {
+      slot = 0;
+      phase ^= 1;
     }
   };
-  bring();
 
+  if (warp == kWarps) {
+    // the producer
+    uint32_t fills = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+      const Unit w = unit_of(p, list, plan, u, parts);
+      const __nv_bfloat16* rk = ring_of<__nv_bfloat16>(p, w.blk, 0, w.hk);
+      const __nv_bfloat16* rv = ring_of<__nv_bfloat16>(p, w.blk, 1, w.hk);
+      for (int st = w.first; st < w.end; ++st) {
+        wait(&sm.empty[slot], phase ^ 1);
+        if (dead) break;
+        uint64_t* full = &sm.full[slot];
+        if (st < w.ring_stages) {
+          if (lane == 0) {
+            const uint32_t bytes = (uint32_t)min(kKeys, w.slots - st * kKeys) * D * 2;
+            mbar_arrive_expect_tx(full, 2 * bytes);
+            bulk_g2s(&sm.kv[slot][0][0][0], rk + (size_t)st * kKeys * D, bytes, full);
+            bulk_g2s(&sm.kv[slot][1][0][0], rv + (size_t)st * kKeys * D, bytes, full);
+          }
+        } else {
+          const int i0 = (st - w.ring_stages) * kKeys, n = min(kKeys, w.len - i0);
+          if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)n * D * 4);
+          __syncwarp();
+          for (int i = lane; i < 2 * n; i += 32) {
+            const int part = i & 1, r = i >> 1;
+            const size_t row = w.row0 + i0 + r;
+            bulk_g2s(&sm.kv[slot][part][r][0],
+                     part ? static_cast<const __nv_bfloat16*>(p.v) + row * p.ldv + (size_t)w.hk * D
+                          : static_cast<const __nv_bfloat16*>(p.k) + row * p.ldk + (size_t)w.hk * D,
+                     D * 2, full);
+          }
+        }
+        ++fills;
+        next_stage();
+      }
+      if (dead) break;
+    }
+    // (where a wait gave up, what is on its way lands before the CTA ends)
+    if (dead)
+      for (uint32_t i = fills > kStages ? fills - kStages : 0; i < fills; ++i)
+        mbar_wait_bounded(&sm.full[i % kStages], i / kStages & 1);
+    return;
+  }
+
+  // a consumer
   const int g = lane >> 2, t = lane & 3;
   const float to2 = p.scale * kLog2e;
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     const Unit w = unit_of(p, list, plan, u, parts);
-    const int rows = w.len * p.group, tiles = w.tiles;
-    const int mine = warp % tiles;  // this warp's tile of 16 rows
-    const int sharing = kWarps / tiles;  // warps that work on its keys
-    // rows g and g + 8 of the tile: their tokens and q
-    uint32_t q[kChunks][2][4];
-    int pos[2];
-    bool live[2];
+    const int rows = w.len * p.group, tiles = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+    const int mine = warp % tiles * 8;                      // this warp's first row
+    const int sharing = kWarps / tiles, my = warp / tiles;  // the warps that share its keys
+    // q of row g; the positions of rows 2t and 2t + 1, whose scores and outputs
+    // this lane has, and of row g, whose weights it hands to the product
+    auto token_of = [&](int row) { return row < rows ? row / p.group : 0; };
+    uint32_t q[kChunks][4];
+    int pos[2], pos_g;
+    {
+      const int row = mine + g, token = token_of(row);
+      const int head = w.hk * p.group + (row < rows ? row - token * p.group : 0);
+      pos_g = w.past + token;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = mine * 16 + g + 8 * r;
-      live[r] = row < rows;
-      const int token = live[r] ? row / p.group : 0, head = w.hk * p.group + (live[r] ? row % p.group : 0);
-      pos[r] = w.past + token;
+      for (int r = 0; r < 2; ++r) pos[r] = w.past + token_of(mine + 2 * t + r);
       const __nv_bfloat16* src =
           static_cast<const __nv_bfloat16*>(p.q) + (size_t)(w.row0 + token) * p.ldq + (size_t)head * D;
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         uint4 x = make_uint4(0, 0, 0, 0);
-        if (live[r]) x = *reinterpret_cast<const uint4*>(src + 32 * i + 8 * t);
-        q[i][r][0] = x.x; q[i][r][1] = x.y; q[i][r][2] = x.z; q[i][r][3] = x.w;
+        if (row < rows) x = *reinterpret_cast<const uint4*>(src + 32 * i + 8 * t);
+        q[i][0] = x.x; q[i][1] = x.y; q[i][2] = x.z; q[i][3] = x.w;
       }
     }
     // slots that not every row sees: two runs
@@ -231,57 +251,58 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
       n0 = p.sinks;
       n1 = p_last - p.window + 1;
     }
-    float o[kHalves][8][4];
+    // o[4 h + j]: channels 64 h + 8 g + 2 j (and + 1: elements 2 and 3) of rows 2t, 2t + 1
+    float o[4 * kHalves][4];
     float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int h = 0; h < kHalves; ++h)
+    for (int j = 0; j < 4 * kHalves; ++j)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[h][j][c] = 0.f;
+      for (int c = 0; c < 4; ++c) o[j][c] = 0.f;
 
-    int gr = w.first + warp / tiles;
-    // A group's keys.  partly: some row may not see some of them.
-    auto group = [&](auto partly_c, bool fresh, int base0, int n) {
+    // 16 keys, from row k0 of the stage on; base0: the first one's index among the
+    // block's slots or (fresh) the new tokens; n of them are there.  Partly: some row
+    // may not see some of them.
+    auto group = [&](auto partly_c, bool fresh, int k0, int base0, int n) {
       constexpr bool kPartly = decltype(partly_c)::value;
-      // scores of 16 keys
-      float sc[2][4];
+      // scores of keys g and g + 8 and rows 2t, 2t + 1, in two chains of products
+      float sc[4] = {0.f, 0.f, 0.f, 0.f}, more[4] = {0.f, 0.f, 0.f, 0.f};
+      const __nv_bfloat16* kr = &sm.kv[slot][0][k0 + g][8 * t];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) sc[h][c] = 0.f;
-        const __nv_bfloat16* kr = &ring[slot][0][8 * h + g][8 * t];
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-          const uint4 x = *reinterpret_cast<const uint4*>(kr + 32 * i);
-          const uint32_t lo[4] = {q[i][0][0], q[i][1][0], q[i][0][1], q[i][1][1]};
-          const uint32_t hi[4] = {q[i][0][2], q[i][1][2], q[i][0][3], q[i][1][3]};
-          mma16816(sc[h], lo, x.x, x.y);
-          mma16816(sc[h], hi, x.z, x.w);
-        }
+      for (int i = 0; i < kChunks; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(kr + 32 * i);
+        const uint4 y = *reinterpret_cast<const uint4*>(kr + 8 * D + 32 * i);
+        const uint32_t lo[4] = {x.x, y.x, x.y, y.y}, hi[4] = {x.z, y.z, x.w, y.w};
+        mma16816(sc, lo, q[i][0], q[i][1]);
+        mma16816(more, hi, q[i][2], q[i][3]);
       }
-      // this lane's keys' values: 2t, 2t+1, 2t+8, 2t+9, channels 8g .. of each half
+#pragma unroll
+      for (int c = 0; c < 4; ++c) sc[c] += more[c];
+      // values of keys 2t, 2t + 1, 2t + 8, 2t + 9, channels 8 g .. of each half
       auto key_of = [&](int i) { return 2 * t + (i & 1) + 8 * (i >> 1); };
       auto value = [&](int i, int h) {
-        return *reinterpret_cast<const uint4*>(&ring[slot][1][key_of(i)][64 * h + 8 * g]);
+        return *reinterpret_cast<const uint4*>(&sm.kv[slot][1][k0 + key_of(i)][64 * h + 8 * g]);
       };
-      // position of key i (only of one that is there)
-      auto position = [&](int i) {
-        const int sl = base0 + key_of(i);
+      // the position of a key that is there
+      auto position = [&](int key) {
+        const int sl = base0 + key;
         return fresh ? w.past + sl : sl < p.sinks ? sl : sl + (w.past - 1 - sl) / p.window * p.window;
       };
-      unsigned seen = 0xffu;  // bit 2 i + r: row r sees key i
-      bool split = false;     // a value that is not finite, which not every row sees
+      unsigned seen = 0xfu;  // bit c: score c counts
+      bool split = false;    // a value that is not finite, which not every row may see
       if constexpr (kPartly) {
         seen = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (g + 8 * k >= n) continue;
+          const int j = position(g + 8 * k);
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (sees(p, pos[r], j)) seen |= 1u << (2 * k + r);
+        }
         bool odd = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (key_of(i) >= n) continue;
-          const int j = position(i);
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-            if (sees(p, pos[r], j)) seen |= 1u << (2 * i + r);
 #pragma unroll
           for (int h = 0; h < kHalves; ++h) {
             const uint4 x4 = value(i, h);
@@ -295,19 +316,17 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
         split = __any_sync(0xffffffffu, odd);
       }
       // the softmax's next maximum
-      float high[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float& x = sc[i >> 1][2 * r + (i & 1)];
-          x = !kPartly || (seen >> (2 * i + r) & 1) ? x * to2 : -INFINITY;
-          high[r] = fmaxf(high[r], x);
-        }
+      float high[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        high[r] = fmaxf(high[r], __shfl_xor_sync(0xffffffffu, high[r], 1));
-        high[r] = fmaxf(high[r], __shfl_xor_sync(0xffffffffu, high[r], 2));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float& x = sc[2 * k + r];
+          x = !kPartly || (seen >> (2 * k + r) & 1) ? x * to2 : -INFINITY;
+        }
+        high[r] = fmaxf(sc[r], sc[2 + r]);
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) high[r] = fmaxf(high[r], __shfl_xor_sync(0xffffffffu, high[r], d));
       }
       if (__any_sync(0xffffffffu, high[0] > top[0] || high[1] > top[1])) {
 #pragma unroll
@@ -317,134 +336,119 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
           top[r] = now;
           sum[r] *= f;
 #pragma unroll
-          for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              o[h][j][2 * r] *= f;
-              o[h][j][2 * r + 1] *= f;
-            }
+          for (int j = 0; j < 4 * kHalves; ++j) {
+            o[j][r] *= f;
+            o[j][2 + r] *= f;
+          }
         }
       }
-      float wt[4][2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
+        // (nothing but -inf so far: any number in the maximum's place)
         const float base = top[r] == -INFINITY ? 0.f : top[r];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float e = ex2(sc[i >> 1][2 * r + (i & 1)] - base);
-          wt[i][r] = !kPartly || (seen >> (2 * i + r) & 1) ? e : 0.f;
-          sum[r] += wt[i][r];
+        for (int k = 0; k < 2; ++k) {
+          float& x = sc[2 * k + r];
+          x = ex2(x - base);
+          if (kPartly && !(seen >> (2 * k + r) & 1)) x = 0.f;
+          sum[r] += x;
         }
       }
-      const uint32_t a[4] = {pack(wt[0][0], wt[1][0]), pack(wt[0][1], wt[1][1]),
-                             pack(wt[2][0], wt[3][0]), pack(wt[2][1], wt[3][1])};
-      if (!kPartly || !split) {
+      // the weights as the product takes them: keys 2t .., row g
+      const uint32_t b0 = transpose8x8(pack(sc[0], sc[1])), b1 = transpose8x8(pack(sc[2], sc[3]));
+      // one half's products; mask: the keys that count
+      auto products = [&](int h, unsigned mask, auto&& each) {
+        uint32_t x[4][4];
 #pragma unroll
-        for (int h = 0; h < kHalves; ++h) {
-          uint32_t x[4][4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 v = value(i, h);
-            // (what lies behind the last key may be anything)
-            if (kPartly && key_of(i) >= n) v = make_uint4(0, 0, 0, 0);
-            x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t pick = j & 1 ? 0x7632u : 0x5410u;
-            mma16816(o[h][j], a, __byte_perm(x[0][j >> 1], x[1][j >> 1], pick),
-                     __byte_perm(x[2][j >> 1], x[3][j >> 1], pick));
-          }
+        for (int i = 0; i < 4; ++i) {
+          uint4 v = value(i, h);
+          if (kPartly && !(mask >> i & 1)) v = make_uint4(0, 0, 0, 0);
+          x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
         }
-      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a[4] = {__byte_perm(x[0][j], x[1][j], 0x5410), __byte_perm(x[0][j], x[1][j], 0x7632),
+                                 __byte_perm(x[2][j], x[3][j], 0x5410), __byte_perm(x[2][j], x[3][j], 0x7632)};
+          each(4 * h + j, a);
+        }
+      };
+      if (!kPartly || !split) {
+        unsigned there = 0;  // (what lies behind the last key may be anything)
+        if constexpr (kPartly) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) there |= (key_of(i) < n ? 1u : 0u) << i;
+        }
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+          products(h, there, [&](int j, const uint32_t* a) { mma16816(o[j], a, b0, b1); });
+      } else if constexpr (kPartly) {
         // token by token: its rows' weights alone, on the values that it sees, so that
         // what a row does not see does not reach it (0 times NaN would)
-        const int lo = __reduce_min_sync(0xffffffffu, live[0] ? pos[0] : 0x7fffffff);
-        const int hi = __reduce_max_sync(0xffffffffu, max(live[0] ? pos[0] : 0, live[1] ? pos[1] : 0));
+        const int lo = __reduce_min_sync(0xffffffffu, pos_g), hi = __reduce_max_sync(0xffffffffu, pos_g);
 #pragma unroll 1
         for (int at = lo; at <= hi; ++at) {
           unsigned mask = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (key_of(i) < n && sees(p, at, position(i))) mask |= 1u << i;
-          const uint32_t at4[4] = {pos[0] == at ? a[0] : 0u, pos[1] == at ? a[1] : 0u,
-                                   pos[0] == at ? a[2] : 0u, pos[1] == at ? a[3] : 0u};
+            if (key_of(i) < n && sees(p, at, position(key_of(i)))) mask |= 1u << i;
 #pragma unroll
-          for (int h = 0; h < kHalves; ++h) {
-            uint32_t x[4][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint4 v = value(i, h);
-              if (!(mask >> i & 1)) v = make_uint4(0, 0, 0, 0);
-              x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint32_t pick = j & 1 ? 0x7632u : 0x5410u;
+          for (int h = 0; h < kHalves; ++h)
+            products(h, mask, [&](int j, const uint32_t* a) {
               float c[4] = {0.f, 0.f, 0.f, 0.f};
-              mma16816(c, at4, __byte_perm(x[0][j >> 1], x[1][j >> 1], pick),
-                       __byte_perm(x[2][j >> 1], x[3][j >> 1], pick));
+              mma16816(c, a, pos_g == at ? b0 : 0u, pos_g == at ? b1 : 0u);
 #pragma unroll
               for (int r = 0; r < 2; ++r)
                 if (pos[r] == at) {
-                  o[h][j][2 * r] += c[2 * r];
-                  o[h][j][2 * r + 1] += c[2 * r + 1];
+                  o[j][r] += c[r];
+                  o[j][2 + r] += c[2 + r];
                 }
-            }
-          }
+            });
         }
       }
     };
-    for (; gr < w.end; gr += sharing) {
-      const bool fresh = gr >= w.ring_groups;
-      // the group's first key, among the block's slots or the new tokens
-      const int base0 = (fresh ? gr - w.ring_groups : gr) * kKeys;
-      const int n = min(kKeys, (fresh ? w.len : w.slots) - base0);
-      wait(&sm.full[warp][slot], phase);
-      if (fresh || n < kKeys || (base0 < m1 && base0 + 16 > m0) || (base0 < n1 && base0 + 16 > n0))
-        group(std::true_type(), fresh, base0, n);
-      else
-        group(std::false_type(), false, base0, n);
-      __syncwarp();  // the stage is read: bring() may fill it
-      ++take;
-      if (++slot == kStages) {
-        slot = 0;
-        phase ^= 1;
+    for (int st = w.first; st < w.end; ++st) {
+      const bool fresh = st >= w.ring_stages;
+      const int first = (fresh ? st - w.ring_stages : st) * kKeys;
+      const int n = min(kKeys, (fresh ? w.len : w.slots) - first);
+      wait(&sm.full[slot], phase);
+      for (int k0 = my * 16; k0 < n; k0 += 16 * sharing) {
+        const int base0 = first + k0;
+        if (fresh || n - k0 < 16 || (base0 < m1 && base0 + 16 > m0) || (base0 < n1 && base0 + 16 > n0))
+          group(std::true_type(), fresh, k0, base0, n - k0);
+        else
+          group(std::false_type(), false, k0, base0, 16);
       }
-      bring();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[slot]);
+      next_stage();
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-    }
-    if (t == 0) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        sm.top[warp][g + 8 * r] = top[r];
-        sm.sum[warp][g + 8 * r] = sum[r];
+      for (int d = 4; d < 32; d <<= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], d);
+      if (g == 0) {
+        sm.top[warp][2 * t + r] = top[r];
+        sm.sum[warp][2 * t + r] = sum[r];
       }
     }
     const int unit = u / parts;  // whose parts meet
     float* mine_left = left + (size_t)u * part_floats<D>();
-    // (this lane's columns of a half are 16 t .. + 15: lanes 0 and 1, then 2 and 3, put theirs down)
+    // (a half's 64 channels in two rounds: those of lanes g < 4, then the others')
 #pragma unroll
     for (int h = 0; h < D / 32; ++h) {
-      if (t >> 1 == (h & 1)) {
+      if (g >> 2 == (h & 1)) {
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int j = 0; j < 8; j += 4)
-              *reinterpret_cast<float4*>(&sm.meet[warp][g + 8 * r][16 * (t & 1) + 8 * c + j]) =
-                  make_float4(o[h / 2][j][2 * r + c], o[h / 2][j + 1][2 * r + c],
-                              o[h / 2][j + 2][2 * r + c], o[h / 2][j + 3][2 * r + c]);
+          for (int j = 0; j < 4; j += 2)
+            *reinterpret_cast<float4*>(&sm.meet[warp][2 * t + r][8 * (g & 3) + 2 * j]) =
+                make_float4(o[h / 2 * 4 + j][r], o[h / 2 * 4 + j][2 + r], o[h / 2 * 4 + j + 1][r],
+                            o[h / 2 * 4 + j + 1][2 + r]);
       }
-      __syncthreads();
+      consumer_sync();
       // four columns of a row at a time
-      for (int i = tid; i < rows * 8; i += kThreads) {
-        const int row = i / 8, c = i % 8 * 4, tile = row >> 4, r = row & 15;
+      for (int i = tid; i < rows * 8; i += 32 * kWarps) {
+        const int row = i / 8, c = i % 8 * 4, tile = row / 8, r = row % 8;
         float m = -INFINITY, l = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < sharing; ++k) m = fmaxf(m, sm.top[tile + k * tiles][r]);
@@ -473,24 +477,24 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
           }
         }
       }
-      __syncthreads();  // the room is free again, and (the last time) all groups are read
+      consumer_sync();  // the room is free again, and (the last time) all stages are read
     }
     bool last = true;
     if (parts > 1) {
       __threadfence();
-      __syncthreads();
+      consumer_sync();
       if (tid == 0) {
         sm.last = atomicAdd(&arrived[unit], 1) == parts - 1;
         if (sm.last) arrived[unit] = 0;  // for the next call
         __threadfence();
       }
-      __syncthreads();
+      consumer_sync();
       last = sm.last;
     }
     if (!last) continue;
     if (parts > 1) {
       const float* all = left + (size_t)unit * parts * part_floats<D>();
-      for (int i = tid; i < rows * (D / 4); i += kThreads) {
+      for (int i = tid; i < rows * (D / 4); i += 32 * kWarps) {
         const int row = i / (D / 4), c = i % (D / 4) * 4;
         float m = -INFINITY, l = 0.f;
         for (int k = 0; k < parts; ++k)
@@ -515,7 +519,7 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
       }
     }
     // the new keys and values into the block: all of this kv head's window has been read
-    for (int i = tid; i < 2 * w.len * (D / 8); i += kThreads) {
+    for (int i = tid; i < 2 * w.len * (D / 8); i += 32 * kWarps) {
       const int part = i / (w.len * (D / 8)), x = i % (w.len * (D / 8)), tok = x / (D / 8), c = x % (D / 8) * 8;
       const int j = w.past + tok;
       if (j >= p.sinks && tok < w.len - p.window) continue;  // out of every later window
@@ -524,10 +528,7 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
       *reinterpret_cast<uint4*>(ring_of<__nv_bfloat16>(p, w.blk, part, w.hk) + (size_t)slot_of(p, j) * D + c) =
           *reinterpret_cast<const uint4*>(src);
     }
-  }  // (where a wait gave up, what is on its way lands before the CTA ends)
-  if (dead)
-    for (uint32_t i = fill > kStages ? fill - kStages : 0; i < fill; ++i)
-      mbar_wait_bounded(&sm.full[warp][i % kStages], i / kStages & 1);
+  }
 }
 
 template <int D>
@@ -556,13 +557,14 @@ size_t win_short_room(int sms, int d) {
 cudaError_t launch_win_short(const WinParams& p, const Pieces& of, int max_items, int sms, void* room,
                              cudaStream_t s) {
   // Where the kv heads of all sequences leave CTAs idle, their windows are cut into
-  // parts of two groups per warp at least.
+  // parts of two stages at least.
   const long long heads = (long long)max_items * p.Hkv;
-  const int groups = (p.sinks + p.window + kKeys - 1) / kKeys + 1;
-  int parts = heads > 0 && heads < 2 * sms && heads * sizeof(int32_t) <= kWinCounterBytes ? (int)(2 * sms / heads) : 1;
-  if (parts > (groups + 7) / 8) parts = (groups + 7) / 8;
+  const int stages = (p.sinks + p.window + kKeys - 1) / kKeys + 1, side = 2 * sms;
+  int parts = 1;
+  if (heads > 0 && heads < side && heads * sizeof(int32_t) <= kWinCounterBytes) parts = (int)(side / heads);
+  if (parts > (stages + 1) / 2) parts = (stages + 1) / 2;
   const long long units = heads * parts;
-  const int ctas = (int)(units < 2 * sms ? (units > 0 ? units : 1) : 2 * sms);
+  const int ctas = (int)(units < side ? (units > 0 ? units : 1) : side);
   return p.d == 64 ? launch_short<64>(p, of, parts, ctas, room, s)
                    : launch_short<128>(p, of, parts, ctas, room, s);
 }
