@@ -38,24 +38,14 @@ struct RowSmem {
   PlanSmem plan;
 };
 
+// Tokens t0 .. t0 + tokens - 1 of sequence s (or, with more than kRows heads to a
+// kv head, part `sub` of one token's heads).
 template <typename T, int D>
-__global__ void __launch_bounds__(kRowThreads) win_rows_kernel(WinParams p, Pieces pieces) {
-  extern __shared__ __align__(16) unsigned char row_smem[];
-  RowSmem<D>& sm = *reinterpret_cast<RowSmem<D>*>(row_smem);
-  pdl_wait_then_release();
+__device__ void rows_of(const WinParams& p, RowSmem<D>& sm, int s, int t0, int tokens, int hk, int sub) {
   const Batch& b = p.batch;
-  const SeqList list = b.listed ? listed_long(b)
-                                : plan_self(b, pieces, sm.plan, p.report && blockIdx.x == 0);
-  const int subs = (p.group + kRows - 1) / kRows;  // parts of a token's heads
-  const int sub = blockIdx.x % subs, hk = blockIdx.x / subs % p.Hkv;
-  const int piece = blockIdx.x / (subs * p.Hkv);
-  if (piece >= list.total) return;
-  const int e = entry_of(list, piece), s = list.items[e];
-  const int t0 = (piece - list.first[e]) * pieces.tokens;
-  const int row0 = b.cu[s], len = b.cu[s + 1] - row0, past = b.past_len[s], blk = b.blk[s];
-  const int tokens = min(pieces.tokens, len - t0);
+  const int row0 = b.cu[s], past = b.past_len[s], blk = b.blk[s];
   const int per = min(kRows, p.group - sub * kRows);  // heads of a token here
-  const int rows = subs > 1 ? per : tokens * p.group;
+  const int rows = p.group > kRows ? per : tokens * p.group;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const T* ring_k = ring_of<T>(p, blk, 0, hk);
   const T* ring_v = ring_of<T>(p, blk, 1, hk);
@@ -175,6 +165,45 @@ __global__ void __launch_bounds__(kRowThreads) win_rows_kernel(WinParams p, Piec
   }
 }
 
+// left: over the units in the list, pieces of the tensor-core form (p.group is at
+// most its tile's 128 rows).
+template <typename T, int D, bool kLeft>
+__global__ void __launch_bounds__(kRowThreads) win_rows_kernel(WinParams p, Pieces pieces, const int32_t* left) {
+  extern __shared__ __align__(16) unsigned char row_smem[];
+  RowSmem<D>& sm = *reinterpret_cast<RowSmem<D>*>(row_smem);
+  pdl_wait_then_release();
+  const Batch& b = p.batch;
+  int n_left = 0;
+  if (kLeft) {
+    n_left = b.work.header()[kWorkHead];
+    if (n_left == 0) return;
+  }
+  const SeqList list = b.listed ? listed_long(b)
+                                : plan_self(b, pieces, sm.plan, p.report && blockIdx.x == 0);
+  const int subs = (p.group + kRows - 1) / kRows;  // parts of a token's heads
+  const int step = subs > 1 ? 1 : kRows / p.group;  // tokens at a time
+  auto unit = [&](int piece, int hk, int sub) {
+    const int e = entry_of(list, piece), s = list.items[e];
+    const int t0 = (piece - list.first[e]) * pieces.tokens;
+    const int end = min(t0 + pieces.tokens, b.cu[s + 1] - b.cu[s]);
+    for (int t = t0; t < end; t += step) {
+      rows_of<T, D>(p, sm, s, t, min(step, end - t), hk, sub);
+      __syncthreads();
+    }
+  };
+  if (kLeft) {
+    // (more than the list holds: all)
+    const int n = n_left > kWinLeft ? list.total * p.Hkv : n_left;
+    for (int i = blockIdx.x; i < n * subs; i += gridDim.x) {
+      const int u = n_left > kWinLeft ? i / subs : left[i / subs];
+      unit(u / p.Hkv, u % p.Hkv, i % subs);
+    }
+  } else {
+    const int sub = blockIdx.x % subs, hk = blockIdx.x / subs % p.Hkv, piece = blockIdx.x / (subs * p.Hkv);
+    if (piece < list.total) unit(piece, hk, sub);
+  }
+}
+
 // --- the new keys and values into the blocks ----------------------------------
 // Behind the attention, which reads what they replace.
 constexpr int kAppendThreads = 256;
@@ -185,6 +214,7 @@ __global__ void __launch_bounds__(kAppendThreads) win_append_kernel(WinParams p,
   __shared__ PlanSmem plan;
   pdl_wait_then_release();
   const Batch& b = p.batch;
+  if (blockIdx.x == 0 && threadIdx.x == 0) b.work.header()[kWorkHead] = 0;  // nothing is left
   const SeqList list = b.listed ? listed_long(b) : plan_self(b, pieces, plan, p.report && blockIdx.x == 0);
   const int row16 = p.Hkv * p.d * (int)sizeof(T) / 16, head16 = p.d * (int)sizeof(T) / 16;
   for (int piece = blockIdx.x; piece < list.total; piece += gridDim.x) {
@@ -207,18 +237,24 @@ __global__ void __launch_bounds__(kAppendThreads) win_append_kernel(WinParams p,
   }
 }
 
-template <typename T, int D>
-cudaError_t launch_rows(const WinParams& p, const Pieces& of, unsigned ctas, cudaStream_t s) {
-  auto kern = win_rows_kernel<T, D>;
+template <typename T, int D, bool kLeft>
+cudaError_t launch_rows(const WinParams& p, const Pieces& of, unsigned ctas, const int32_t* left,
+                        cudaStream_t s) {
+  auto kern = win_rows_kernel<T, D, kLeft>;
   const size_t smem = sizeof(RowSmem<D>);
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(ctas), dim3(kRowThreads), smem, s, p, of);
+  return launch_pdl(kern, dim3(ctas), dim3(kRowThreads), smem, s, p, of, left);
 }
 
 size_t roundup(size_t v, size_t m) { return (v + m - 1) / m * m; }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+size_t win_stride(int Hkv, int d, int window, int sinks, int act, size_t align) {
+  const size_t row = (size_t)d * (act == GDN_F32 ? 4 : 2);
+  return roundup(2 * (size_t)Hkv * ((size_t)window + sinks) * row, align > 128 ? align : 128);
+}
 
 int check_win_dims(int num_blocks, int num_layers, int Hkv, int d, int window, int sinks, int act,
                    size_t align) {
@@ -228,29 +264,32 @@ int check_win_dims(int num_blocks, int num_layers, int Hkv, int d, int window, i
   if (act != GDN_F32 && act != GDN_BF16) return GDN_ERR_DIMS;
   if (align != 0 && (align < 128 || (align & (align - 1)) != 0)) return GDN_ERR_DIMS;
   if ((long long)num_blocks * num_layers >= (1ll << 30)) return GDN_ERR_RANGE;
+  // (a layer's rows of keys and values are counted in 32 bits)
+  if ((double)num_blocks * win_stride(Hkv, d, window, sinks, act, align) / (d * (act == GDN_F32 ? 4 : 2)) > 2147483000.0)
+    return GDN_ERR_RANGE;
   return GDN_OK;
-}
-
-size_t win_stride(int Hkv, int d, int window, int sinks, int act, size_t align) {
-  const size_t row = (size_t)d * (act == GDN_F32 ? 4 : 2);
-  return roundup(2 * (size_t)Hkv * ((size_t)window + sinks) * row, align > 128 ? align : 128);
 }
 
 }  // namespace
 
-cudaError_t launch_win_rows(const WinParams& p, int act, const Pieces& of, int max_pieces,
-                            cudaStream_t s) {
+cudaError_t launch_win_rows(const WinParams& p, int act, const Pieces& of, int max_pieces, int sms,
+                            const void* room, bool left, cudaStream_t s) {
   const int subs = (p.group + kRows - 1) / kRows;
+  if (left) {  // (bf16, d = 64 or 128)
+    const int32_t* list =
+        reinterpret_cast<const int32_t*>(static_cast<const unsigned char*>(room) + kWinCounterBytes);
+    return p.d == 64 ? launch_rows<__nv_bfloat16, 64, true>(p, of, 2 * sms, list, s)
+                     : launch_rows<__nv_bfloat16, 128, true>(p, of, 2 * sms, list, s);
+  }
   const unsigned ctas = (unsigned)max_pieces * subs * p.Hkv;
   if (act == GDN_F32)
-    return p.d == 32   ? launch_rows<float, 32>(p, of, ctas, s)
-           : p.d == 64 ? launch_rows<float, 64>(p, of, ctas, s)
-                       : launch_rows<float, 128>(p, of, ctas, s);
-  return p.d == 32   ? launch_rows<__nv_bfloat16, 32>(p, of, ctas, s)
-         : p.d == 64 ? launch_rows<__nv_bfloat16, 64>(p, of, ctas, s)
-                     : launch_rows<__nv_bfloat16, 128>(p, of, ctas, s);
+    return p.d == 32   ? launch_rows<float, 32, false>(p, of, ctas, nullptr, s)
+           : p.d == 64 ? launch_rows<float, 64, false>(p, of, ctas, nullptr, s)
+                       : launch_rows<float, 128, false>(p, of, ctas, nullptr, s);
+  return p.d == 32   ? launch_rows<__nv_bfloat16, 32, false>(p, of, ctas, nullptr, s)
+         : p.d == 64 ? launch_rows<__nv_bfloat16, 64, false>(p, of, ctas, nullptr, s)
+                     : launch_rows<__nv_bfloat16, 128, false>(p, of, ctas, nullptr, s);
 }
-
 
 cudaError_t launch_win_append(const WinParams& p, int act, const Pieces& of, int max_pieces, int sms,
                               cudaStream_t s) {
@@ -396,17 +435,24 @@ int gdn_win_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
   const int few = gdn::win_short_supported(d, p->act) ? gdn::win_short_tokens(wp.group) : 0;
   const bool may_long = few == 0 || (T > few && (max_seqlen_hint == 0 || max_seqlen_hint > few));
   const bool may_short = few > 0 && !(N == 1 && T > few);
-  gdn::Pieces of = {few + 1, 0x7fffffff, wp.group < gdn::kRows ? gdn::kRows / wp.group : 1};
+  const bool tc = T > 0 && gdn::win_tc_supported(d, p->act, wp.group);
+  gdn::Pieces of = {few + 1, 0x7fffffff,
+                    tc ? gdn::win_tc_tokens(wp.group) : wp.group < gdn::kRows ? gdn::kRows / wp.group : 1};
   const int max_long = max_items < T / (few + 1) ? max_items : T / (few + 1);
   auto most_pieces = [&](int tokens) {
     const int n = T / tokens + max_long;
     return n > 0 ? n : 1;  // (a kernel that looks at the batch)
   };
-  p->last_path = may_long && T > 1 && max_seqlen_hint != 1 ? GDN_PREFILL_SERIAL : GDN_PREFILL_NONE;
+  p->last_path = !may_long || T < 2 || max_seqlen_hint == 1 ? GDN_PREFILL_NONE
+                 : tc                                        ? GDN_PREFILL_FUSED
+                                                             : GDN_PREFILL_SERIAL;
   if (b.listed && gdn::launch_plan(b, of, s) != cudaSuccess) return GDN_ERR_CUDA;
   if (p->ev_before && cudaEventRecord(p->ev_before, s) != cudaSuccess) return GDN_ERR_CUDA;
   if (may_long) {
-    if (gdn::launch_win_rows(wp, p->act, of, most_pieces(of.tokens), s) != cudaSuccess)
+    if (tc && gdn::launch_win_tc(wp, of, most_pieces(of.tokens), p->sms, p->win_parts, s) != cudaSuccess)
+      return GDN_ERR_CUDA;
+    if (tc) wp.report = 0;
+    if (gdn::launch_win_rows(wp, p->act, of, most_pieces(of.tokens), p->sms, p->win_parts, tc, s) != cudaSuccess)
       return GDN_ERR_CUDA;
     wp.report = 0;
     if (!b.listed) of.tokens = gdn::kAppendTokens;

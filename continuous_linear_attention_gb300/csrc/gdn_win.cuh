@@ -35,19 +35,33 @@ __device__ __forceinline__ bool sees(const WinParams& p, int pos, int j) {
   return j <= pos && (j > pos - p.window || j < p.sinks);
 }
 
-// The form for any type and shape, over the sequences of the given pieces.
-cudaError_t launch_win_rows(const WinParams& p, int act, const Pieces& of, int max_pieces, cudaStream_t s);
+// Work memory of a pool for the forms below: arrival counters of split windows,
+// the units that the tensor-core form leaves (the header's kWorkHead counts
+// them), partial results of split windows.
+constexpr size_t kWinCounterBytes = 4096;
+constexpr int kWinLeft = 16384;
+constexpr size_t kWinListBytes = kWinLeft * sizeof(int32_t);
+
+// The form for any type and shape, over the sequences of the given pieces; with
+// left, over the units that the tensor-core form has left, in its pieces.
+cudaError_t launch_win_rows(const WinParams& p, int act, const Pieces& of, int max_pieces, int sms,
+                            const void* room, bool left, cudaStream_t s);
 // The new keys and values of those sequences into their blocks, behind it.
 cudaError_t launch_win_append(const WinParams& p, int act, const Pieces& of, int max_pieces, int sms,
                               cudaStream_t s);
 // The form for few tokens (gdn_win_short.cu), which appends by itself: up to
 // win_short_tokens(group) tokens per sequence (0: none); room: work memory of
 // the pool, win_short_room bytes, zeroed once.
-constexpr size_t kWinCounterBytes = 4096;
 bool win_short_supported(int d, int act);
 int win_short_tokens(int group);
 size_t win_short_room(int sms, int d);
 cudaError_t launch_win_short(const WinParams& p, const Pieces& of, int max_items, int sms, void* room,
                              cudaStream_t s);
+
+// The form for prompts (gdn_win_tc.cu): pieces of win_tc_tokens(group) tokens.
+bool win_tc_supported(int d, int act, int group);
+int win_tc_tokens(int group);
+cudaError_t launch_win_tc(const WinParams& p, const Pieces& of, int max_pieces, int sms, void* room,
+                          cudaStream_t s);
 
 }  // namespace gdn

@@ -540,7 +540,7 @@ cudaError_t launch_short(const WinParams& p, const Pieces& of, int parts, int ct
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   int32_t* arrived = static_cast<int32_t*>(room);
-  float* left = reinterpret_cast<float*>(static_cast<unsigned char*>(room) + kWinCounterBytes);
+  float* left = reinterpret_cast<float*>(static_cast<unsigned char*>(room) + kWinCounterBytes + kWinListBytes);
   return launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, s, p, of, parts, arrived, left);
 }
 
@@ -551,7 +551,7 @@ bool win_short_supported(int d, int act) { return act == GDN_BF16 && (d == 64 ||
 int win_short_tokens(int group) { return group <= kMaxRows ? kMaxRows / group : 0; }
 
 size_t win_short_room(int sms, int d) {
-  return kWinCounterBytes + (size_t)2 * sms * (d == 64 ? part_floats<64>() : part_floats<128>()) * sizeof(float);
+  return kWinCounterBytes + kWinListBytes + (size_t)2 * sms * (d == 64 ? part_floats<64>() : part_floats<128>()) * sizeof(float);
 }
 
 cudaError_t launch_win_short(const WinParams& p, const Pieces& of, int max_items, int sms, void* room,

@@ -1,0 +1,665 @@
+// Windowed attention for prompts: bf16, d = 64 or 128, on the tensor cores.
+//
+// A unit is one kv head of 2 * (128 / group) consecutive tokens of a sequence:
+// two tiles, A and B, of up to 128 rows (queries of consecutive tokens, the heads
+// that share the kv head next to each other), which read the same keys: the
+// first tokens and the window of the first query up to the last query.  The keys
+// lie in up to five runs (in the block: the sinks, and the ring in two parts; in
+// the call's rows: the sinks, and the window), which are cut into segments of 16
+// rows, eight to a tile of 128 keys, so that a tile is full wherever the runs
+// begin and end.  With X in {A, B}, per tile of keys:
+//   S_X = Q_X K^T                   (128 x 128, tensor memory)
+//   P_X = 2^(scale log2 e S - m_X)  (bf16, over S), l_X += its row sums (fp32)
+//   O_X += P_X V                    (128 x d, tensor memory)
+// m_X is a row's maximum so far, or up to 2^8 below it: only a larger step scales
+// O_X and l_X (in exact arithmetic m_X does not matter; in fp32 a weight up to
+// 2^8 costs no precision either).
+//
+// Floors: the products, 4 d per pair of query and key, and the exponentials, one
+// per pair, take the same time at the hardware's rates (a 128 x 128 tile of
+// both products of two tiles 2,048 cycles, its exponentials as much), so the two
+// tiles alternate: the softmax of one beside the products of the other.
+// 15,843 tokens x 32 heads (8 kv heads), window 1,024: TIME_PROMPT.
+//
+// One CTA per SM, units by a fixed stride.  Roles:
+//   softmax A, B  four warps each, a thread per row: S from tensor memory, P back
+//                 to it, in the end the output
+//   MMA           one warp: S and P V of both tiles
+//   producer      one warp: TMA loads, and what the others need to know of a tile
+//   check         two warps: whether a value is not finite in a tile of which some
+//                 row does not see all.  0 times it would reach that row; such a
+//                 unit is left to the form for any shape, which runs behind this
+//                 kernel over the list of them.
+// P is rounded to bf16 as the product's operand (its sum is not): an output's
+// error is 2^-9 / sqrt(3) relative to the root of the sum of its squared terms, on
+// top of its own rounding by about as much.
+#include <cuda.h>
+
+#include "gdn_ptx.cuh"
+#include "gdn_tc.cuh"
+#include "gdn_win.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 384;  // softmax A and B (4 warps each), MMA, producer, check (2)
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kCheckWarp = 10;
+constexpr int kTile = 128, kSeg = 16, kSegs = kTile / kSeg;
+constexpr int kRing = 16;      // descriptions of tiles
+constexpr float kSlack = 8.f;  // how far m may be below the maximum (powers of two)
+constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;  // of tile A; B's 128 columns behind
+
+// One tile of keys, as the producer describes it.
+struct Tile {
+  int flags, segs;
+  int pos[kSegs], n[kSegs];  // first position of a segment and how many keys it has
+  // the unit
+  int row, pos0, tokens, hk, number;  // first packed row, its position, tokens
+  int odd;                       // (check warps) a value is not finite
+};
+enum : int {
+  kFirst = 1,   // first tile of its unit
+  kLast = 2,
+  kEnd = 4,     // no more tiles
+  kHasB = 8,    // the unit has rows in tile B
+  kPartly = 16, // some row does not see some key
+};
+
+template <int D>
+struct TcSmem {
+  static constexpr uint32_t kOperand = 128u * D * 2;  // a tile of Q, K or V: blocks of 64 columns
+  static constexpr int kStages = D == 128 ? 2 : 4;    // of K and of V
+  unsigned char q[2][kOperand];
+  unsigned char k[kStages][kOperand], v[kStages][kOperand];
+  Tile tile[kRing];
+  uint64_t described[kRing], checked[kRing], read[kRing];
+  uint64_t q_full[2], q_free[2], k_full[kStages], k_free[kStages], v_full[kStages], v_free[kStages];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint32_t tmem;
+  PlanSmem plan;
+};
+
+struct TcMaps {
+  CUtensorMap q;                   // [T][H][d], boxes of a tile's rows x 64 columns
+  CUtensorMap ring128, ring16;     // the layer's blocks as rows of d
+  CUtensorMap k128, k16, v128, v16;  // [T][Hkv d]
+};
+
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+}
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) arrive(bar);
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int c0, int c1, int c2,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// Ring position of a role: its stage and the parity of its pass.
+template <int kN>
+struct Pos {
+  int at = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == kN) {
+      at = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+// A run of keys: consecutive rows of the ring or of the call's tokens.
+struct Run {
+  int pos, n, row, ring;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__ TcMaps maps) {
+  using Smem = TcSmem<D>;
+  constexpr int kStages = Smem::kStages, kBlocks = D / 64;
+  constexpr uint32_t kBox = 128 * 128;  // bytes of a block of 64 columns x 128 rows
+  extern __shared__ __align__(1024) unsigned char tc_smem[];
+  Smem& sm = *reinterpret_cast<Smem*>(tc_smem);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sm.described[i], 1);
+      mbar_init(&sm.checked[i], 2);
+      mbar_init(&sm.read[i], 8);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sm.k_full[i], 1);
+      mbar_init(&sm.k_free[i], 1);
+      mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.v_free[i], 3);  // MMA, check warps
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&sm.q_full[x], 1);
+      mbar_init(&sm.q_free[x], 1);
+      mbar_init(&sm.s_full[x], 1);
+      mbar_init(&sm.p_full[x], 4);
+      mbar_init(&sm.o_full[x], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 0) tc::tmem_alloc(&sm.tmem, TM_COLS);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = sm.tmem;
+  pdl_wait_then_release();
+  const Batch& b = p.batch;
+  const SeqList list = b.listed ? listed_long(b) : plan_self(b, pieces, sm.plan, p.report && blockIdx.x == 0);
+  const int units = list.total * p.Hkv;
+  const int tile_tokens = pieces.tokens / 2;
+  const bool aligned = (smem_u32(tc_smem) & 1023u) == 0;  // the operand tiles' swizzle counts on it
+  bool dead = !aligned;
+
+  // registers a thread, of 168 at launch: softmax 216, the others 72
+  if (warp < 8) {
+    // ============================== softmax ===============================
+    regs_inc<216>();
+    const int x = warp >> 2, row = (warp & 3) * 32 + lane;  // tile, and row of it
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;      // this warp's tensor memory lanes
+    const uint32_t ts = tmem + TM_S + 128u * x + lanes, to = tmem + TM_O + 128u * x + lanes;
+    float to2 = p.scale * kLog2e;
+    const bool negative = to2 < 0.f;
+    to2 = fmaxf(fabsf(to2), 1e-37f);  // (0: all weights equal, and -inf stays -inf)
+    const int token = row / p.group, head_in = row % p.group;
+    Pos<kRing> at;
+    uint32_t turn = 0, unit = 0;  // parities of s_full, and of o_full
+    float top = -INFINITY, sum = 0.f;
+    bool odd = false;
+    while (!dead) {
+      if (!wait_for(&sm.described[at.at], at.ph)) { dead = true; break; }
+      const Tile& tile = sm.tile[at.at];
+      const int flags = tile.flags;
+      if (flags & kEnd) break;
+      if (x == 1 && !(flags & kHasB)) {
+        warp_arrive(&sm.read[at.at]);
+        at.next();
+        continue;
+      }
+      if (flags & kFirst) {
+        top = -INFINITY;
+        sum = 0.f;
+        odd = false;
+      }
+      const int pos = tile.pos0 + x * tile_tokens + token;
+      // what this row sees of each segment, as bits: only where some row does not see all
+      uint32_t mask[kSegs / 2];
+      if (flags & kPartly) {
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i) {
+          const int p0 = tile.pos[i], n = i < tile.segs ? tile.n[i] : 0;
+          const int upto = min(n, max(0, pos - p0 + 1));                       // not behind the row
+          const int from = min(16, max(0, pos - p.window - p0 + 1));           // in the window
+          const int sink = min(16, max(0, p.sinks - p0));                      // or one of the first
+          const uint32_t m = ((1u << upto) - 1u) & (~((1u << from) - 1u) | ((1u << sink) - 1u));
+          if (i & 1) mask[i / 2] |= (m & 0xffffu) << 16;
+          else mask[i / 2] = m & 0xffffu;
+        }
+      }
+      if (!wait_for(&sm.s_full[x], turn)) { dead = true; break; }
+      turn ^= 1;
+      tc::fence_after_sync();
+      float v[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tc::tmem_ld32(ts + 32 * c, v + 32 * c);
+      tc::tmem_wait_ld();
+      if (negative) {
+#pragma unroll
+        for (int i = 0; i < 128; ++i) v[i] = -v[i];
+      }
+      if (flags & kPartly) {
+#pragma unroll
+        for (int i = 0; i < 128; ++i)
+          v[i] = mask[i / 32] >> (i & 31) & 1 ? v[i] : -INFINITY;
+      }
+      float m4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+      for (int i = 4; i < 124; i += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m4[k] = max3(m4[k], v[i + k], v[i + 4 + k]);
+      const float high = fmaxf(max3(m4[0], m4[1], v[124]), max3(m4[2], m4[3], fmaxf(v[125], fmaxf(v[126], v[127])))) * to2;
+      const bool more = high > top + kSlack;  // (the first one that is not -inf as well)
+      if (__any_sync(0xffffffffu, more)) {
+        const float now = fmaxf(top, high);
+        const float f = now == -INFINITY ? 1.f : ex2(top - now);
+        top = now;
+        sum *= f;
+        if (!(flags & kFirst)) {
+          // (S_X full: all products before it are done, P V of the last tile among them)
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tc::tmem_ld32(to + c, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= f;
+            tc::tmem_st32(to + c, o);
+          }
+        }
+      }
+      const float base = top == -INFINITY ? 0.f : top;
+      float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float e0 = ex2(fmaf(v[32 * c + i], to2, -base)), e1 = ex2(fmaf(v[32 * c + i + 1], to2, -base));
+          s4[i & 2] += e0;
+          s4[(i & 2) + 1] += e1;
+          w[i / 2] = tc::pack2(e0, e1, (__nv_bfloat16*)nullptr);
+        }
+        tc::tmem_st16u(ts + 16 * c, w);  // (over scores that are read)
+      }
+      sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      warp_arrive(&sm.p_full[x]);
+      if (flags & kPartly) {
+        if (!wait_for(&sm.checked[at.at], at.ph)) { dead = true; break; }
+        odd |= tile.odd != 0;
+      }
+      if (flags & kLast) {
+        const int tokens = min(tile_tokens, tile.tokens - x * tile_tokens);
+        const bool live = token < tokens && row < tile_tokens * p.group;
+        const int out_row = tile.row + x * tile_tokens + token, hk = tile.hk, number = tile.number;
+        if (!wait_for(&sm.o_full[x], unit)) { dead = true; break; }
+        unit ^= 1;
+        tc::fence_after_sync();
+        const float inv = 1.f / sum;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (size_t)(live ? out_row : 0) * p.ldo +
+                             (size_t)(hk * p.group + head_in) * D;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tc::tmem_ld32(to + c, o);
+          tc::tmem_wait_ld();
+          if (live && !odd) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint4 y;
+              y.x = tc::pack2(o[i] * inv, o[i + 1] * inv, (__nv_bfloat16*)nullptr);
+              y.y = tc::pack2(o[i + 2] * inv, o[i + 3] * inv, (__nv_bfloat16*)nullptr);
+              y.z = tc::pack2(o[i + 4] * inv, o[i + 5] * inv, (__nv_bfloat16*)nullptr);
+              y.w = tc::pack2(o[i + 6] * inv, o[i + 7] * inv, (__nv_bfloat16*)nullptr);
+              *reinterpret_cast<uint4*>(out + c + i) = y;
+            }
+          }
+        }
+        if (odd && tid == 0) {
+          const int i = atomicAdd(&b.work.header()[kWorkHead], 1);
+          if (i < kWinLeft) left[i] = number;
+        }
+      }
+      warp_arrive(&sm.read[at.at]);
+      at.next();
+    }
+  } else {
+    regs_dec<72>();
+    if (warp == kMmaWarp) {
+      // ================================ MMA =================================
+      const uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // high word: 8-row groups, 128-byte swizzle
+      auto desc = [&](uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; };
+      auto lo_k = [](uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); };
+      auto lo_mn = [](uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | ((kBox >> 4) << 16); };
+      Pos<kRing> at;
+      Pos<kStages> ks, vs;
+      uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0};
+      // S of tile X with the keys in stage `st`
+      auto scores = [&](int x, int st, int segs) {
+        const uint32_t id = tc::idesc_bf16_f32(128, 16 * segs);
+        if (elect_one()) {
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t off = (uint32_t)(s >> 2) * (kBox >> 4) + (uint32_t)(s & 3) * 2u;
+            tc::mma_bf16(tmem + TM_S + 128u * x, desc(lo_k(smem_u32(sm.q[x])) + off),
+                         desc(lo_k(smem_u32(sm.k[st])) + off), id, s > 0);
+          }
+          tc::commit(&sm.s_full[x]);
+        }
+        __syncwarp();
+      };
+      auto values = [&](int x, int st, int segs, bool first) {
+        const uint32_t id = tc::idesc_bf16_f32(128, D, false, true);
+        if (elect_one()) {
+          for (int s = 0; s < segs; ++s)
+            tc::mma_ts(tmem + TM_O + 128u * x, tmem + TM_S + 128u * x + 8u * s,
+                       desc(lo_mn(smem_u32(sm.v[st])) + (uint32_t)s * (2048u >> 4)), id, !first || s > 0);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) tc::commit(bar);
+        __syncwarp();
+      };
+      // S of the tile at `at` for X; (for the last X) its keys' stage is free
+      // behind it; (for a unit's last tile) so is Q
+      auto begin = [&](int x, int flags, int segs) {
+        if (flags & kFirst) {
+          if (!wait_for(&sm.q_full[x], q_ph[x])) { dead = true; return; }
+          q_ph[x] ^= 1;
+        }
+        if (x == 0 && !wait_for(&sm.k_full[ks.at], ks.ph)) { dead = true; return; }
+        tc::fence_after_sync();
+        scores(x, ks.at, segs);
+        if (flags & kLast) commit(&sm.q_free[x]);
+        if (x == 1 || !(flags & kHasB)) {
+          commit(&sm.k_free[ks.at]);
+          ks.next();
+        }
+      };
+      auto described = [&]() {
+        if (!wait_for(&sm.described[at.at], at.ph)) dead = true;
+        return dead ? (int)kEnd : sm.tile[at.at].flags;
+      };
+      int flags = described();
+      int segs = flags & kEnd ? 0 : sm.tile[at.at].segs;
+      if (!(flags & kEnd)) {
+        begin(0, flags, segs);
+        if (!dead && (flags & kHasB)) begin(1, flags, segs);
+      }
+      while (!dead && !(flags & kEnd)) {
+        at.next();
+        const int next = described();
+        if (dead) break;
+        const int next_segs = next & kEnd ? 0 : sm.tile[at.at].segs;
+        if (!wait_for(&sm.v_full[vs.at], vs.ph)) { dead = true; break; }
+        for (int x = 0; x < 2 && !dead; ++x) {
+          // (B's products of a unit that has it; the next tile's scores beside the other's softmax)
+          if (x == 0 || (flags & kHasB)) {
+            if (!wait_for(&sm.p_full[x], p_ph[x])) { dead = true; break; }
+            p_ph[x] ^= 1;
+            tc::fence_after_sync();
+            values(x, vs.at, segs, flags & kFirst);
+            if (flags & kLast) commit(&sm.o_full[x]);
+          }
+          if (x == 1 || !(flags & kHasB)) {
+            if (x == 0 || (flags & kHasB)) commit(&sm.v_free[vs.at]);
+          }
+          if (!(next & kEnd) && (x == 0 || (next & kHasB))) begin(x, next, next_segs);
+        }
+        vs.next();
+        flags = next;
+        segs = next_segs;
+      }
+    } else if (warp == kLoadWarp) {
+      // ============================== producer ==============================
+      Pos<kRing> at;
+      Pos<kStages> st;
+      uint32_t q_ph = 0;
+      int loads = 0;
+      const int total = p.sinks + p.window;
+      const int rows_of = (int)(p.stride / (D * 2));  // rows of a block
+      for (int u = blockIdx.x; u < units && !dead; u += gridDim.x) {
+        const int piece = u / p.Hkv, hk = u % p.Hkv;
+        const int e = entry_of(list, piece), s = list.items[e];
+        const int t0 = (piece - list.first[e]) * pieces.tokens;
+        const int row0 = b.cu[s], len = b.cu[s + 1] - row0, past = b.past_len[s], blk = b.blk[s];
+        const int tokens = min(pieces.tokens, len - t0);
+        const int p0 = past + t0, p1 = p0 + tokens;
+        const bool has_b = tokens > tile_tokens;
+        // the runs of keys, in order of their positions
+        const int lo = max(0, p0 - p.window + 1), before = min(p.sinks, lo);
+        const int block_row = blk * rows_of + hk * total;
+        Run run[5];
+        run[0] = {0, min(before, past), block_row, 1};
+        run[1] = {run[0].n, before - run[0].n, row0 + (run[0].n - past), 0};
+        const int old = max(0, min(past, p1) - lo), slot = slot_of(p, lo);
+        run[2] = {lo, min(old, total - slot), block_row + slot, 1};
+        run[3] = {lo + run[2].n, old - run[2].n, block_row + p.sinks, 1};
+        const int fresh = max(lo, past);
+        run[4] = {fresh, p1 - fresh, row0 + (fresh - past), 0};
+        int segs_upto[5], n_segs = 0;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+          n_segs += (run[i].n + kSeg - 1) / kSeg;
+          segs_upto[i] = n_segs;
+        }
+        const int n_tiles = (n_segs + kSegs - 1) / kSegs;
+        for (int j = 0; j < n_tiles && !dead; ++j) {
+          const int segs = min(kSegs, n_segs - j * kSegs);
+          // segment lane % 8 of the tile
+          const int seg = j * kSegs + (lane & 7);
+          int r = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) r += seg >= segs_upto[i];
+          Run mine = run[4];
+          int upto = n_segs;
+#pragma unroll
+          for (int i = 3; i >= 0; --i)
+            if (r == i) {
+              mine = run[i];
+              upto = segs_upto[i];
+            }
+          const int in = (seg - (upto - (mine.n + kSeg - 1) / kSeg)) * kSeg;
+          const bool there = (lane & 7) < segs;
+          const int pos = mine.pos + in, n = there ? min(kSeg, mine.n - in) : 0, row = mine.row + in;
+          // every row sees a key that is not behind the first one and in the last one's window
+          const bool all = there && n == kSeg && pos + kSeg - 1 <= p0 &&
+                           (pos > p1 - 1 - p.window || pos + kSeg <= p.sinks);
+          const bool full = __all_sync(0xffffffffu, all) && segs == kSegs;
+          // one box where all rows of the tile lie behind one another
+          const int row_first = __shfl_sync(0xffffffffu, row, 0), ring_first = __shfl_sync(0xffffffffu, mine.ring, 0);
+          const bool one = segs == kSegs &&
+                           __all_sync(0xffffffffu, row == row_first + kSeg * (lane & 7) && mine.ring == ring_first);
+          // (described kRing tiles ago, and read by all softmax warps)
+          if (!wait_for(&sm.read[at.at], at.ph ^ 1)) { dead = true; break; }
+          Tile& tile = sm.tile[at.at];
+          if (lane < kSegs) {
+            tile.pos[lane] = pos;
+            tile.n[lane] = n;
+          }
+          if (lane == 0) {
+            tile.flags = (j == 0 ? kFirst : 0) | (j == n_tiles - 1 ? kLast : 0) | (has_b ? kHasB : 0) |
+                         (full ? 0 : kPartly);
+            tile.segs = segs;
+            tile.row = row0 + t0;
+            tile.pos0 = p0;
+            tile.tokens = tokens;
+            tile.hk = hk;
+            tile.number = u;
+            tile.odd = 0;
+          }
+          warp_arrive(&sm.described[at.at]);
+          at.next();
+          if (j == 0) {
+            for (int x = 0; x < (has_b ? 2 : 1); ++x) {
+              // (B's turns differ from A's: each counts its own)
+              const uint32_t ph = q_ph >> x & 1;
+              if (!wait_for(&sm.q_free[x], ph ^ 1)) { dead = true; break; }
+              q_ph ^= 1u << x;
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&sm.q_full[x], (uint32_t)tile_tokens * p.group * D * 2);
+#pragma unroll
+                for (int h = 0; h < kBlocks; ++h)
+                  tma_load_3d(sm.q[x] + h * kBox, &maps.q, 64 * h, hk * p.group, row0 + t0 + x * tile_tokens,
+                              &sm.q_full[x]);
+              }
+              __syncwarp();
+            }
+            if (dead) break;
+          }
+          // keys, then values: a lane per segment and block, or two boxes
+          for (int part = 0; part < 2; ++part) {
+            uint64_t* full_bar = part ? &sm.v_full[st.at] : &sm.k_full[st.at];
+            unsigned char* dst = part ? sm.v[st.at] : sm.k[st.at];
+            if (!wait_for(part ? &sm.v_free[st.at] : &sm.k_free[st.at], st.ph ^ 1)) { dead = true; break; }
+            if (lane == 0) mbar_arrive_expect_tx(full_bar, (uint32_t)segs * kSeg * D * 2);
+            __syncwarp();
+            const int shift = mine.ring && part ? p.Hkv * total : 0;  // the values' rows in a block
+            const int h = one ? lane : lane >> 3;
+            if (h < kBlocks && (one || there)) {
+              const void* map = one ? (mine.ring ? &maps.ring128 : part ? &maps.v128 : &maps.k128)
+                                    : (mine.ring ? &maps.ring16 : part ? &maps.v16 : &maps.k16);
+              const int col = (mine.ring ? 0 : hk * D) + 64 * h;
+              const uint32_t to = (uint32_t)h * kBox + (one ? 0u : (uint32_t)(lane & 7) * (kSeg * 128u));
+              tma_load_2d(dst + to, map, col, (one ? row_first : row) + shift, full_bar);
+            }
+            __syncwarp();
+          }
+          ++loads;
+          st.next();
+        }
+      }
+      if (!dead) {
+        if (wait_for(&sm.read[at.at], at.ph ^ 1)) {
+          if (lane == 0) sm.tile[at.at].flags = kEnd;
+          warp_arrive(&sm.described[at.at]);
+        } else {
+          dead = true;
+        }
+      } else {
+        // what is on its way lands before the CTA ends
+        for (int i = max(0, loads - kStages); i < loads; ++i) {
+          mbar_wait_bounded(&sm.k_full[i % kStages], (uint32_t)(i / kStages) & 1u);
+          mbar_wait_bounded(&sm.v_full[i % kStages], (uint32_t)(i / kStages) & 1u);
+        }
+      }
+    } else {
+      // =============================== check ================================
+      Pos<kRing> at;
+      Pos<kStages> vs;
+      const int half = warp - kCheckWarp;
+      while (!dead) {
+        if (!wait_for(&sm.described[at.at], at.ph)) { dead = true; break; }
+        Tile& tile = sm.tile[at.at];
+        const int flags = tile.flags;
+        if (flags & kEnd) break;
+        if (!wait_for(&sm.v_full[vs.at], vs.ph)) { dead = true; break; }
+        if (flags & kPartly) {
+          // this warp's half of the rows: 16 bytes of 4 rows at a time
+          const int rows = tile.segs * kSeg;
+          bool odd = false;
+#pragma unroll 4
+          for (int r = half * 4 + (lane >> 3); r < rows; r += 8)
+#pragma unroll
+            for (int h = 0; h < kBlocks; ++h) {
+              const uint4 x4 = *reinterpret_cast<const uint4*>(sm.v[vs.at] + h * kBox + r * 128 + (lane & 7) * 16);
+              const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                odd |= (x[c] & 0x7f80u) == 0x7f80u || (x[c] & 0x7f800000u) == 0x7f800000u;
+            }
+          if (__any_sync(0xffffffffu, odd) && lane == 0) tile.odd = 1;
+        }
+        warp_arrive(&sm.checked[at.at]);
+        warp_arrive(&sm.v_free[vs.at]);
+        vs.next();
+        at.next();
+      }
+    }
+  }
+  if (dead && lane == 0) atomicOr((unsigned*)&b.work.header()[kErr], GDN_FLAG_TIMEOUT);
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) tc::tmem_dealloc(tmem, TM_COLS);
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                             CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                             CUtensorMapFloatOOBfill);
+
+// Tensor map of bf16, 128-byte swizzled, zero fill past the end.
+cudaError_t encode_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box) {
+  static const EncodeFn encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                           cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeFn>(fn) : nullptr;
+  }();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r =
+      encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+cudaError_t rows_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld,
+                     int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  return encode_map(m, base, 2, dims, strides, box);
+}
+
+template <int D>
+cudaError_t launch_tc(const WinParams& p, const Pieces& of, int ctas, int32_t* left, cudaStream_t s) {
+  TcMaps maps;
+  const long long kc = (long long)p.Hkv * D, ring_rows = (long long)(p.stride / (D * 2)) * p.batch.num_blocks;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.H, (cuuint64_t)p.batch.T};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)p.ldq * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)p.group, (cuuint32_t)(of.tokens / 2)};
+  cudaError_t e = encode_map(&maps.q, p.q, 3, dims, strides, box);
+  if (e == cudaSuccess) e = rows_map(&maps.ring128, p.layer_base, ring_rows, D, D, kTile);
+  if (e == cudaSuccess) e = rows_map(&maps.ring16, p.layer_base, ring_rows, D, D, kSeg);
+  if (e == cudaSuccess) e = rows_map(&maps.k128, p.k, p.batch.T, kc, p.ldk, kTile);
+  if (e == cudaSuccess) e = rows_map(&maps.k16, p.k, p.batch.T, kc, p.ldk, kSeg);
+  if (e == cudaSuccess) e = rows_map(&maps.v128, p.v, p.batch.T, kc, p.ldv, kTile);
+  if (e == cudaSuccess) e = rows_map(&maps.v16, p.v, p.batch.T, kc, p.ldv, kSeg);
+  if (e != cudaSuccess) return e;
+  auto kern = win_tc_kernel<D>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(TcSmem<D>));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(ctas), dim3(kThreads), sizeof(TcSmem<D>), s, p, of, left, maps);
+}
+
+}  // namespace
+
+bool win_tc_supported(int d, int act, int group) {
+  return act == GDN_BF16 && (d == 64 || d == 128) && group <= kTile;
+}
+
+int win_tc_tokens(int group) { return 2 * (kTile / group); }
+
+cudaError_t launch_win_tc(const WinParams& p, const Pieces& of, int max_pieces, int sms, void* room,
+                          cudaStream_t s) {
+  int32_t* left = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(room) + kWinCounterBytes);
+  const long long units = (long long)max_pieces * p.Hkv;
+  const int ctas = (int)(units < sms ? units : sms);
+  return p.d == 64 ? launch_tc<64>(p, of, ctas, left, s) : launch_tc<128>(p, of, ctas, left, s);
+}
+
+}  // namespace gdn
