@@ -35,6 +35,10 @@
 // top of its own rounding by about as much.
 #include <cuda.h>
 
+#include <cstddef>
+#include <type_traits>
+
+#include "gdn_lin.cuh"
 #include "gdn_ptx.cuh"
 #include "gdn_tc.cuh"
 #include "gdn_win.cuh"
@@ -75,7 +79,7 @@ struct TcSmem {
   Tile tile[kRing];
   uint64_t described[kRing], checked[kRing], read[kRing];
   uint64_t q_full[2], q_free[2], k_full[kStages], k_free[kStages], v_full[kStages], v_free[kStages];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_half[2], p_full[2], o_full[2];
   uint32_t tmem;
   PlanSmem plan;
 };
@@ -120,6 +124,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 template <int kRegs>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -127,6 +136,11 @@ __device__ __forceinline__ void regs_dec() {
 template <int kRegs>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// K-major operands advance by 32 bytes per 16 elements, blocks of 64 by 16 KB.
+__host__ __device__ constexpr uint32_t step_k(int s) {
+  return (uint32_t)(s >> 2) * (16384u >> 4) + (uint32_t)(s & 3) * 2u;
 }
 
 // Ring position of a role: its stage and the parity of its pass.
@@ -173,6 +187,7 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
       mbar_init(&sm.q_full[x], 1);
       mbar_init(&sm.q_free[x], 1);
       mbar_init(&sm.s_full[x], 1);
+      mbar_init(&sm.p_half[x], 4);
       mbar_init(&sm.p_full[x], 4);
       mbar_init(&sm.o_full[x], 1);
     }
@@ -188,7 +203,8 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
   const SeqList list = b.listed ? listed_long(b) : plan_self(b, pieces, sm.plan, p.report && blockIdx.x == 0);
   const int units = list.total * p.Hkv;
   const int tile_tokens = pieces.tokens / 2;
-  const bool aligned = (smem_u32(tc_smem) & 1023u) == 0;  // the operand tiles' swizzle counts on it
+  const uint32_t sbase = smem_u32(tc_smem);
+  const bool aligned = (sbase & 1023u) == 0;  // the operand tiles' swizzle counts on it
   bool dead = !aligned;
 
   // registers a thread, of 168 at launch: softmax 216, the others 72
@@ -278,20 +294,31 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
         }
       }
       const float base = top == -INFINITY ? 0.f : top;
-      float s4[4] = {0.f, 0.f, 0.f, 0.f};
+      const F2 scale2 = f2(to2, to2), base2 = f2(-base, -base);
+      F2 sum2[2] = {0ull, 0ull};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-          const float e0 = ex2(fmaf(v[32 * c + i], to2, -base)), e1 = ex2(fmaf(v[32 * c + i + 1], to2, -base));
-          s4[i & 2] += e0;
-          s4[(i & 2) + 1] += e1;
+          float e0, e1;
+          unf2(fma2(f2(v[32 * c + i], v[32 * c + i + 1]), scale2, base2), e0, e1);
+          e0 = ex2(e0);
+          e1 = ex2(e1);
+          sum2[i >> 1 & 1] = add2(sum2[i >> 1 & 1], f2(e0, e1));
           w[i / 2] = tc::pack2(e0, e1, (__nv_bfloat16*)nullptr);
         }
         tc::tmem_st16u(ts + 16 * c, w);  // (over scores that are read)
+        if (c == 1) {  // the first 64 keys' weights: their product may begin
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          warp_arrive(&sm.p_half[x]);
+        }
       }
-      sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+      float s0, s1, s2, s3;
+      unf2(sum2[0], s0, s1);
+      unf2(sum2[1], s2, s3);
+      sum += (s0 + s1) + (s2 + s3);
       tc::tmem_wait_st();
       tc::fence_before_sync();
       warp_arrive(&sm.p_full[x]);
@@ -345,79 +372,106 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
       Pos<kRing> at;
       Pos<kStages> ks, vs;
       uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0};
+      // (descriptors and addresses stay in uniform registers where a whole warp runs
+      // this code with values that the compiler knows to be uniform and one elected
+      // lane issues: else every operand is moved there, some 100 cycles a product)
+      const bool one = elect_one();
+      const uint32_t q_lo = lo_k(sbase + (uint32_t)offsetof(Smem, q)), k_lo = lo_k(sbase + (uint32_t)offsetof(Smem, k)),
+                     v_lo = lo_mn(sbase + (uint32_t)offsetof(Smem, v));
       // S of tile X with the keys in stage `st`
-      auto scores = [&](int x, int st, int segs) {
-        const uint32_t id = tc::idesc_bf16_f32(128, 16 * segs);
-        if (elect_one()) {
+      auto scores = [&](auto xc, int st, int segs) {
+        constexpr int x = decltype(xc)::value;
+        const uint32_t qx = q_lo + x * (Smem::kOperand >> 4), ks = k_lo + (uint32_t)st * (Smem::kOperand >> 4);
+        if (one) {
+          if (segs == kSegs) {
 #pragma unroll
-          for (int s = 0; s < D / 16; ++s) {
-            const uint32_t off = (uint32_t)(s >> 2) * (kBox >> 4) + (uint32_t)(s & 3) * 2u;
-            tc::mma_bf16(tmem + TM_S + 128u * x, desc(lo_k(smem_u32(sm.q[x])) + off),
-                         desc(lo_k(smem_u32(sm.k[st])) + off), id, s > 0);
+            for (int s = 0; s < D / 16; ++s)
+              tc::mma_bf16(tmem + TM_S + 128u * x, desc(qx + step_k(s)), desc(ks + step_k(s)),
+                           tc::idesc_bf16_f32(128, 128), s > 0);
+          } else {
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+              tc::mma_bf16(tmem + TM_S + 128u * x, desc(qx + step_k(s)), desc(ks + step_k(s)),
+                           tc::idesc_bf16_f32(128, 16 * segs), s > 0);
           }
           tc::commit(&sm.s_full[x]);
         }
         __syncwarp();
       };
-      auto values = [&](int x, int st, int segs, bool first) {
-        const uint32_t id = tc::idesc_bf16_f32(128, D, false, true);
-        if (elect_one()) {
-          for (int s = 0; s < segs; ++s)
-            tc::mma_ts(tmem + TM_O + 128u * x, tmem + TM_S + 128u * x + 8u * s,
-                       desc(lo_mn(smem_u32(sm.v[st])) + (uint32_t)s * (2048u >> 4)), id, !first || s > 0);
+      // O += P V over half of a tile's keys
+      auto values = [&](auto xc, auto half, int st, int segs, bool first) {
+        constexpr int x = decltype(xc)::value, h = decltype(half)::value * (kSegs / 2);
+        constexpr uint32_t id = tc::idesc_bf16_f32(128, D, false, true);
+        const uint32_t vs = v_lo + (uint32_t)st * (Smem::kOperand >> 4);
+        if (one) {
+#pragma unroll
+          for (int s = h; s < h + kSegs / 2; ++s)
+            if (s < segs)
+              tc::mma_ts(tmem + TM_O + 128u * x, tmem + TM_S + 128u * x + 8u * s, desc(vs + (uint32_t)s * (2048u >> 4)),
+                         id, !first || s > 0);
         }
         __syncwarp();
       };
       auto commit = [&](uint64_t* bar) {
-        if (elect_one()) tc::commit(bar);
+        if (one) tc::commit(bar);
         __syncwarp();
       };
       // S of the tile at `at` for X; (for the last X) its keys' stage is free
       // behind it; (for a unit's last tile) so is Q
-      auto begin = [&](int x, int flags, int segs) {
+      auto begin = [&](auto xc, int flags, int segs) {
+        constexpr int x = decltype(xc)::value;
         if (flags & kFirst) {
           if (!wait_for(&sm.q_full[x], q_ph[x])) { dead = true; return; }
           q_ph[x] ^= 1;
         }
         if (x == 0 && !wait_for(&sm.k_full[ks.at], ks.ph)) { dead = true; return; }
         tc::fence_after_sync();
-        scores(x, ks.at, segs);
+        scores(xc, ks.at, segs);
         if (flags & kLast) commit(&sm.q_free[x]);
         if (x == 1 || !(flags & kHasB)) {
           commit(&sm.k_free[ks.at]);
           ks.next();
         }
       };
-      auto described = [&]() {
-        if (!wait_for(&sm.described[at.at], at.ph)) dead = true;
-        return dead ? (int)kEnd : sm.tile[at.at].flags;
+      using A = std::integral_constant<int, 0>;
+      using B = std::integral_constant<int, 1>;
+      int flags, segs;
+      auto described = [&](int& flags, int& segs) {
+        if (!wait_for(&sm.described[at.at], at.ph)) {
+          dead = true;
+          return;
+        }
+        flags = __shfl_sync(0xffffffffu, sm.tile[at.at].flags, 0);
+        segs = __shfl_sync(0xffffffffu, sm.tile[at.at].segs, 0);
       };
-      int flags = described();
-      int segs = flags & kEnd ? 0 : sm.tile[at.at].segs;
-      if (!(flags & kEnd)) {
-        begin(0, flags, segs);
-        if (!dead && (flags & kHasB)) begin(1, flags, segs);
+      described(flags, segs);
+      if (!dead && !(flags & kEnd)) {
+        begin(A(), flags, segs);
+        if (!dead && (flags & kHasB)) begin(B(), flags, segs);
       }
+      // the products of X's tile, and the next tile's scores beside the other's softmax
+      auto advance = [&](auto xc, int next, int next_segs) {
+        constexpr int x = decltype(xc)::value;
+        if (x == 0 || (flags & kHasB)) {
+          if (!wait_for(&sm.p_half[x], p_ph[x])) { dead = true; return; }
+          tc::fence_after_sync();
+          values(xc, A(), vs.at, segs, flags & kFirst);
+          if (!wait_for(&sm.p_full[x], p_ph[x])) { dead = true; return; }
+          p_ph[x] ^= 1;
+          tc::fence_after_sync();
+          values(xc, B(), vs.at, segs, false);
+          if (flags & kLast) commit(&sm.o_full[x]);
+          if (x == 1 || !(flags & kHasB)) commit(&sm.v_free[vs.at]);
+        }
+        if (!(next & kEnd) && (x == 0 || (next & kHasB))) begin(xc, next, next_segs);
+      };
       while (!dead && !(flags & kEnd)) {
         at.next();
-        const int next = described();
-        if (dead) break;
-        const int next_segs = next & kEnd ? 0 : sm.tile[at.at].segs;
-        if (!wait_for(&sm.v_full[vs.at], vs.ph)) { dead = true; break; }
-        for (int x = 0; x < 2 && !dead; ++x) {
-          // (B's products of a unit that has it; the next tile's scores beside the other's softmax)
-          if (x == 0 || (flags & kHasB)) {
-            if (!wait_for(&sm.p_full[x], p_ph[x])) { dead = true; break; }
-            p_ph[x] ^= 1;
-            tc::fence_after_sync();
-            values(x, vs.at, segs, flags & kFirst);
-            if (flags & kLast) commit(&sm.o_full[x]);
-          }
-          if (x == 1 || !(flags & kHasB)) {
-            if (x == 0 || (flags & kHasB)) commit(&sm.v_free[vs.at]);
-          }
-          if (!(next & kEnd) && (x == 0 || (next & kHasB))) begin(x, next, next_segs);
-        }
+        int next = kEnd, next_segs = 0;
+        described(next, next_segs);
+        if (dead || !wait_for(&sm.v_full[vs.at], vs.ph)) { dead = true; break; }
+        advance(A(), next, next_segs);
+        if (!dead) advance(B(), next, next_segs);
         vs.next();
         flags = next;
         segs = next_segs;
