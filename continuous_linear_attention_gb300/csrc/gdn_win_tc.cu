@@ -24,9 +24,13 @@
 // One CTA per SM, units by a fixed stride.  Roles:
 //   softmax A, B  four warps each, a thread per row: S from tensor memory, P back
 //                 to it, in the end the output
-//   MMA           one warp: S and P V of both tiles
+//   MMA A, B      a warp each: P V of a tile and S of the next one, in turns, so
+//                 that the tiles do not fall into step: the softmax of one runs
+//                 beside the products of the other (one warp for both leaves some
+//                 500 cycles between them; without turns they start together, and
+//                 the products wait for both softmaxes)
 //   producer      one warp: TMA loads, and what the others need to know of a tile
-//   check         two warps: whether a value is not finite in a tile of which some
+//   check         one warp: whether a value is not finite in a tile of which some
 //                 row does not see all.  0 times it would reach that row; such a
 //                 unit is left to the form for any shape, which runs behind this
 //                 kernel over the list of them.
@@ -47,8 +51,8 @@ namespace gdn {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kThreads = 384;  // softmax A and B (4 warps each), MMA, producer, check (2)
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kCheckWarp = 10;
+constexpr int kThreads = 384;  // softmax A and B (4 warps each), MMA A and B, producer, check
+constexpr int kMmaWarp = 8, kLoadWarp = 10;
 constexpr int kTile = 128, kSeg = 16, kSegs = kTile / kSeg;
 constexpr int kRing = 16;      // descriptions of tiles
 constexpr float kSlack = 8.f;  // how far m may be below the maximum (powers of two)
@@ -70,16 +74,24 @@ enum : int {
   kPartly = 16, // some row does not see some key
 };
 
+// A run of keys: consecutive rows of the ring or of the call's tokens.
+struct Run {
+  int pos, n, row, ring;
+};
+
 template <int D>
 struct TcSmem {
   static constexpr uint32_t kOperand = 128u * D * 2;  // a tile of Q, K or V: blocks of 64 columns
   static constexpr int kStages = D == 128 ? 2 : 4;    // of K and of V
   unsigned char q[2][kOperand];
   unsigned char k[kStages][kOperand], v[kStages][kOperand];
+  unsigned char out[8][32 * 64];  // a softmax warp's 32 columns of output
   Tile tile[kRing];
+  Run run[5];   // (producer) the unit's
+  int seg0[5];  // and the first segment of each
   uint64_t described[kRing], checked[kRing], read[kRing];
   uint64_t q_full[2], q_free[2], k_full[kStages], k_free[kStages], v_full[kStages], v_free[kStages];
-  uint64_t s_full[2], p_half[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_full[2], o_full[2], turn[2];
   uint32_t tmem;
   PlanSmem plan;
 };
@@ -90,7 +102,18 @@ struct TcMaps {
   CUtensorMap k128, k16, v128, v16;  // [T][Hkv d]
 };
 
+// A bounded wait of a warp.  The first test has no suspend time, which would add
+// to a wait whose phase is complete.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  if (__all_sync(0xffffffffu, ok != 0)) return true;
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
 }
 __device__ __forceinline__ void arrive(uint64_t* bar) {
@@ -124,6 +147,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// 16 consecutive tensor memory columns of this thread's lane, as they are.
+__device__ __forceinline__ void tmem_ld16u(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   F2 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -156,11 +188,6 @@ struct Pos {
   }
 };
 
-// A run of keys: consecutive rows of the ring or of the call's tokens.
-struct Run {
-  int pos, n, row, ring;
-};
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__ TcMaps maps) {
@@ -174,22 +201,22 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sm.described[i], 1);
-      mbar_init(&sm.checked[i], 2);
+      mbar_init(&sm.checked[i], 1);
       mbar_init(&sm.read[i], 8);
     }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sm.k_full[i], 1);
-      mbar_init(&sm.k_free[i], 1);
+      mbar_init(&sm.k_free[i], 2);  // MMA A and B
       mbar_init(&sm.v_full[i], 1);
-      mbar_init(&sm.v_free[i], 3);  // MMA, check warps
+      mbar_init(&sm.v_free[i], 3);  // and check
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sm.q_full[x], 1);
       mbar_init(&sm.q_free[x], 1);
       mbar_init(&sm.s_full[x], 1);
-      mbar_init(&sm.p_half[x], 4);
       mbar_init(&sm.p_full[x], 4);
       mbar_init(&sm.o_full[x], 1);
+      mbar_init(&sm.turn[x], 1);
     }
     fence_mbar_init();
   }
@@ -197,7 +224,7 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = sm.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
   pdl_wait_then_release();
   const Batch& b = p.batch;
   const SeqList list = b.listed ? listed_long(b) : plan_self(b, pieces, sm.plan, p.report && blockIdx.x == 0);
@@ -207,17 +234,18 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
   const bool aligned = (sbase & 1023u) == 0;  // the operand tiles' swizzle counts on it
   bool dead = !aligned;
 
-  // registers a thread, of 168 at launch: softmax 216, the others 72
+  // registers a thread, of 168 at launch: softmax 208, the others 88
   if (warp < 8) {
     // ============================== softmax ===============================
-    regs_inc<216>();
+    regs_inc<208>();
     const int x = warp >> 2, row = (warp & 3) * 32 + lane;  // tile, and row of it
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;      // this warp's tensor memory lanes
     const uint32_t ts = tmem + TM_S + 128u * x + lanes, to = tmem + TM_O + 128u * x + lanes;
-    float to2 = p.scale * kLog2e;
-    const bool negative = to2 < 0.f;
-    to2 = fmaxf(fabsf(to2), 1e-37f);  // (0: all weights equal, and -inf stays -inf)
-    const int token = row / p.group, head_in = row % p.group;
+    // (a negative scale: the product takes -Q; 0: all weights equal, and -inf stays -inf)
+    const float to2 = fmaxf(fabsf(p.scale * kLog2e), 1e-37f);
+    // (a quotient by p.group of less than 128 rows: exact)
+    const uint32_t over_group = (65536u + p.group - 1) / p.group;
+    const int token = (int)((uint32_t)row * over_group >> 16);
     Pos<kRing> at;
     uint32_t turn = 0, unit = 0;  // parities of s_full, and of o_full
     float top = -INFINITY, sum = 0.f;
@@ -238,36 +266,34 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
         odd = false;
       }
       const int pos = tile.pos0 + x * tile_tokens + token;
-      // what this row sees of each segment, as bits: only where some row does not see all
-      uint32_t mask[kSegs / 2];
-      if (flags & kPartly) {
-#pragma unroll
-        for (int i = 0; i < kSegs; ++i) {
-          const int p0 = tile.pos[i], n = i < tile.segs ? tile.n[i] : 0;
-          const int upto = min(n, max(0, pos - p0 + 1));                       // not behind the row
-          const int from = min(16, max(0, pos - p.window - p0 + 1));           // in the window
-          const int sink = min(16, max(0, p.sinks - p0));                      // or one of the first
-          const uint32_t m = ((1u << upto) - 1u) & (~((1u << from) - 1u) | ((1u << sink) - 1u));
-          if (i & 1) mask[i / 2] |= (m & 0xffffu) << 16;
-          else mask[i / 2] = m & 0xffffu;
-        }
-      }
       if (!wait_for(&sm.s_full[x], turn)) { dead = true; break; }
       turn ^= 1;
       tc::fence_after_sync();
+      if (flags & kPartly) {
+        // what this row does not see: -inf in the scores' place.  (Rolled loops here, in
+        // the scaling and in the output: code that runs once or twice a unit is fetched
+        // anew each time, at some 6 cycles an instruction.)
+#pragma unroll 1
+        for (int i = 0; i < kSegs; ++i) {
+          const int p0 = tile.pos[i], n = i < tile.segs ? tile.n[i] : 0;
+          const int upto = min(n, max(0, pos - p0 + 1));              // not behind the row
+          const int from = min(16, max(0, pos - p.window - p0 + 1));  // in the window
+          const int sink = min(16, max(0, p.sinks - p0));             // or one of the first
+          const uint32_t seen = ((1u << upto) - 1u) & (~((1u << from) - 1u) | ((1u << sink) - 1u));
+          if (__all_sync(0xffffffffu, seen == 0xffffu)) continue;
+          uint32_t w[kSeg];
+          tmem_ld16u(ts + kSeg * i, w);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < kSeg; ++k) w[k] = seen >> k & 1 ? w[k] : 0xff800000u;
+          tc::tmem_st16u(ts + kSeg * i, w);
+        }
+        tc::tmem_wait_st();
+      }
       float v[128];
 #pragma unroll
       for (int c = 0; c < 4; ++c) tc::tmem_ld32(ts + 32 * c, v + 32 * c);
       tc::tmem_wait_ld();
-      if (negative) {
-#pragma unroll
-        for (int i = 0; i < 128; ++i) v[i] = -v[i];
-      }
-      if (flags & kPartly) {
-#pragma unroll
-        for (int i = 0; i < 128; ++i)
-          v[i] = mask[i / 32] >> (i & 31) & 1 ? v[i] : -INFINITY;
-      }
       float m4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
       for (int i = 4; i < 124; i += 8)
@@ -282,7 +308,7 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
         sum *= f;
         if (!(flags & kFirst)) {
           // (S_X full: all products before it are done, P V of the last tile among them)
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float o[32];
             tc::tmem_ld32(to + c, o);
@@ -309,11 +335,6 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
           w[i / 2] = tc::pack2(e0, e1, (__nv_bfloat16*)nullptr);
         }
         tc::tmem_st16u(ts + 16 * c, w);  // (over scores that are read)
-        if (c == 1) {  // the first 64 keys' weights: their product may begin
-          tc::tmem_wait_st();
-          tc::fence_before_sync();
-          warp_arrive(&sm.p_half[x]);
-        }
       }
       float s0, s1, s2, s3;
       unf2(sum2[0], s0, s1);
@@ -328,29 +349,45 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
       }
       if (flags & kLast) {
         const int tokens = min(tile_tokens, tile.tokens - x * tile_tokens);
-        const bool live = token < tokens && row < tile_tokens * p.group;
-        const int out_row = tile.row + x * tile_tokens + token, hk = tile.hk, number = tile.number;
+        const int rows = tile_tokens * p.group;
+        const int out_row = tile.row + x * tile_tokens, hk = tile.hk, number = tile.number;
         if (!wait_for(&sm.o_full[x], unit)) { dead = true; break; }
         unit ^= 1;
         tc::fence_after_sync();
         const float inv = 1.f / sum;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (size_t)(live ? out_row : 0) * p.ldo +
-                             (size_t)(hk * p.group + head_in) * D;
+        // 32 columns at a time through shared memory, so that four lanes write 64 bytes
+        // of a row (a lane per row writes 32 rows' 16 bytes at once: 5,000 cycles)
+        unsigned char* room = sm.out[warp];
+        __nv_bfloat16* dst[4];  // of rows 8 i + lane / 4 of the warp; nullptr: nothing to write
 #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int of = (warp & 3) * 32 + 8 * i + (lane >> 2), t = (int)((uint32_t)of * over_group >> 16);
+          dst[i] = t < tokens && of < rows && !odd
+                       ? static_cast<__nv_bfloat16*>(p.out) + (size_t)(out_row + t) * p.ldo +
+                             (size_t)(hk * p.group + of - t * p.group) * D + 8 * (lane & 3)
+                       : nullptr;
+        }
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
           tc::tmem_ld32(to + c, o);
           tc::tmem_wait_ld();
-          if (live && !odd) {
+          __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint4 y;
-              y.x = tc::pack2(o[i] * inv, o[i + 1] * inv, (__nv_bfloat16*)nullptr);
-              y.y = tc::pack2(o[i + 2] * inv, o[i + 3] * inv, (__nv_bfloat16*)nullptr);
-              y.z = tc::pack2(o[i + 4] * inv, o[i + 5] * inv, (__nv_bfloat16*)nullptr);
-              y.w = tc::pack2(o[i + 6] * inv, o[i + 7] * inv, (__nv_bfloat16*)nullptr);
-              *reinterpret_cast<uint4*>(out + c + i) = y;
-            }
+          for (int i = 0; i < 4; ++i) {
+            uint4 y;
+            y.x = tc::pack2(o[8 * i] * inv, o[8 * i + 1] * inv, (__nv_bfloat16*)nullptr);
+            y.y = tc::pack2(o[8 * i + 2] * inv, o[8 * i + 3] * inv, (__nv_bfloat16*)nullptr);
+            y.z = tc::pack2(o[8 * i + 4] * inv, o[8 * i + 5] * inv, (__nv_bfloat16*)nullptr);
+            y.w = tc::pack2(o[8 * i + 6] * inv, o[8 * i + 7] * inv, (__nv_bfloat16*)nullptr);
+            *reinterpret_cast<uint4*>(room + lane * 64 + ((i ^ (lane >> 1)) & 3) * 16) = y;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2);
+            const uint4 y = *reinterpret_cast<const uint4*>(room + r * 64 + (((lane & 3) ^ (r >> 1)) & 3) * 16);
+            if (dst[i]) *reinterpret_cast<uint4*>(dst[i] + c) = y;
           }
         }
         if (odd && tid == 0) {
@@ -362,120 +399,149 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
       at.next();
     }
   } else {
-    regs_dec<72>();
-    if (warp == kMmaWarp) {
+    regs_dec<88>();
+    if (warp < kLoadWarp) {
       // ================================ MMA =================================
-      const uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // high word: 8-row groups, 128-byte swizzle
-      auto desc = [&](uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; };
-      auto lo_k = [](uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); };
-      auto lo_mn = [](uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | ((kBox >> 4) << 16); };
-      Pos<kRing> at;
-      Pos<kStages> ks, vs;
-      uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0};
-      // (descriptors and addresses stay in uniform registers where a whole warp runs
-      // this code with values that the compiler knows to be uniform and one elected
-      // lane issues: else every operand is moved there, some 100 cycles a product)
+      // One elected lane of a warp that runs all of it issues.  (The empty asm keeps
+      // the descriptors from being made ahead, all of them, and spilled.)
+      constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups, 128-byte swizzle
+      auto desc = [](uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; };
+      const uint32_t q_lo = (sbase + (uint32_t)offsetof(Smem, q)) >> 4 | 1u << 16;
+      const uint32_t k_lo = (sbase + (uint32_t)offsetof(Smem, k)) >> 4 | 1u << 16;
+      const uint32_t v_lo = (sbase + (uint32_t)offsetof(Smem, v)) >> 4 | (kBox >> 4) << 16;
       const bool one = elect_one();
-      const uint32_t q_lo = lo_k(sbase + (uint32_t)offsetof(Smem, q)), k_lo = lo_k(sbase + (uint32_t)offsetof(Smem, k)),
-                     v_lo = lo_mn(sbase + (uint32_t)offsetof(Smem, v));
-      // S of tile X with the keys in stage `st`
-      auto scores = [&](auto xc, int st, int segs) {
-        constexpr int x = decltype(xc)::value;
-        const uint32_t qx = q_lo + x * (Smem::kOperand >> 4), ks = k_lo + (uint32_t)st * (Smem::kOperand >> 4);
-        if (one) {
-          if (segs == kSegs) {
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-              tc::mma_bf16(tmem + TM_S + 128u * x, desc(qx + step_k(s)), desc(ks + step_k(s)),
-                           tc::idesc_bf16_f32(128, 128), s > 0);
-          } else {
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-              tc::mma_bf16(tmem + TM_S + 128u * x, desc(qx + step_k(s)), desc(ks + step_k(s)),
-                           tc::idesc_bf16_f32(128, 16 * segs), s > 0);
-          }
-          tc::commit(&sm.s_full[x]);
-        }
-        __syncwarp();
-      };
-      // O += P V over half of a tile's keys
-      auto values = [&](auto xc, auto half, int st, int segs, bool first) {
-        constexpr int x = decltype(xc)::value, h = decltype(half)::value * (kSegs / 2);
-        constexpr uint32_t id = tc::idesc_bf16_f32(128, D, false, true);
-        const uint32_t vs = v_lo + (uint32_t)st * (Smem::kOperand >> 4);
-        if (one) {
-#pragma unroll
-          for (int s = h; s < h + kSegs / 2; ++s)
-            if (s < segs)
-              tc::mma_ts(tmem + TM_O + 128u * x, tmem + TM_S + 128u * x + 8u * s, desc(vs + (uint32_t)s * (2048u >> 4)),
-                         id, !first || s > 0);
-        }
-        __syncwarp();
-      };
       auto commit = [&](uint64_t* bar) {
         if (one) tc::commit(bar);
         __syncwarp();
       };
-      // S of the tile at `at` for X; (for the last X) its keys' stage is free
-      // behind it; (for a unit's last tile) so is Q
-      auto begin = [&](auto xc, int flags, int segs) {
+      auto role = [&](auto xc) {
         constexpr int x = decltype(xc)::value;
-        if (flags & kFirst) {
-          if (!wait_for(&sm.q_full[x], q_ph[x])) { dead = true; return; }
-          q_ph[x] ^= 1;
-        }
-        if (x == 0 && !wait_for(&sm.k_full[ks.at], ks.ph)) { dead = true; return; }
-        tc::fence_after_sync();
-        scores(xc, ks.at, segs);
-        if (flags & kLast) commit(&sm.q_free[x]);
-        if (x == 1 || !(flags & kHasB)) {
-          commit(&sm.k_free[ks.at]);
+        Pos<kRing> at;
+        Pos<kStages> ks, vs;
+        uint32_t q_ph = 0, p_ph = 0, turn = 0;
+        // (A begins)
+        auto my_turn = [&]() {
+          if (!wait_for(&sm.turn[x], x == 0 ? turn ^ 1 : turn)) dead = true;
+          turn ^= 1;
+        };
+        auto your_turn = [&]() {
+          if (lane == 0) arrive(&sm.turn[x ^ 1]);
+          __syncwarp();
+        };
+        int flags = kEnd, segs = 0;
+        auto described = [&](int& flags, int& segs) {
+          if (!wait_for(&sm.described[at.at], at.ph)) {
+            dead = true;
+            return;
+          }
+          flags = __shfl_sync(0xffffffffu, sm.tile[at.at].flags, 0);
+          segs = __shfl_sync(0xffffffffu, sm.tile[at.at].segs, 0);
+        };
+        // does this warp have rows in the unit
+        auto mine = [&](int flags) { return x == 0 || (flags & kHasB) != 0; };
+        // S = Q K^T of a tile (always of 128 keys: scores behind the last one are masked)
+        const uint32_t id_s = tc::idesc_bf16_f32(128, 128) | (p.scale < 0.f ? 1u << 13 : 0u);  // (bit 13: -A)
+        auto scores = [&](int flags) {
+          if (one) {
+            uint32_t q0 = q_lo + x * (Smem::kOperand >> 4), k0 = k_lo + (uint32_t)ks.at * (Smem::kOperand >> 4);
+            asm volatile("" : "+r"(q0), "+r"(k0));
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+              tc::mma_bf16(tmem + TM_S + 128u * x, desc(q0 + step_k(s)), desc(k0 + step_k(s)), id_s, s > 0);
+            tc::commit(&sm.s_full[x]);
+          }
+          __syncwarp();
+        };
+        // and behind them
+        auto begun = [&](int flags) {
+          if (one) {
+            tc::commit(&sm.k_free[ks.at]);
+            if (flags & kLast) tc::commit(&sm.q_free[x]);
+          }
+          __syncwarp();
           ks.next();
-        }
-      };
-      using A = std::integral_constant<int, 0>;
-      using B = std::integral_constant<int, 1>;
-      int flags, segs;
-      auto described = [&](int& flags, int& segs) {
-        if (!wait_for(&sm.described[at.at], at.ph)) {
-          dead = true;
-          return;
-        }
-        flags = __shfl_sync(0xffffffffu, sm.tile[at.at].flags, 0);
-        segs = __shfl_sync(0xffffffffu, sm.tile[at.at].segs, 0);
-      };
-      described(flags, segs);
-      if (!dead && !(flags & kEnd)) {
-        begin(A(), flags, segs);
-        if (!dead && (flags & kHasB)) begin(B(), flags, segs);
-      }
-      // the products of X's tile, and the next tile's scores beside the other's softmax
-      auto advance = [&](auto xc, int next, int next_segs) {
-        constexpr int x = decltype(xc)::value;
-        if (x == 0 || (flags & kHasB)) {
-          if (!wait_for(&sm.p_half[x], p_ph[x])) { dead = true; return; }
+        };
+        auto keys = [&](int flags) {
+          if (flags & kFirst) {
+            if (!wait_for(&sm.q_full[x], q_ph)) dead = true;
+            q_ph ^= 1;
+          }
+          if (dead || !wait_for(&sm.k_full[ks.at], ks.ph)) dead = true;
+        };
+        // a tile without rows of this warp (not before its stages are full: one arrival
+        // for each of their fills)
+        auto pass = [&](uint64_t* full, uint64_t* free, uint32_t ph) {
+          if (!wait_for(full, ph)) {
+            dead = true;
+            return;
+          }
+          if (lane == 0) arrive(free);
+          __syncwarp();
+        };
+        // O += P V
+        auto values = [&](int segs, bool first) {
+          constexpr uint32_t id = tc::idesc_bf16_f32(128, D, false, true);
+          if (one) {
+            uint32_t v0 = v_lo + (uint32_t)vs.at * (Smem::kOperand >> 4);
+            asm volatile("" : "+r"(v0));
+#pragma unroll
+            for (int s = 0; s < kSegs; ++s)
+              if (s < segs)
+                tc::mma_ts(tmem + TM_O + 128u * x, tmem + TM_S + 128u * x + 8u * s,
+                           desc(v0 + (uint32_t)s * (2048u >> 4)), id, !first || s > 0);
+          }
+          __syncwarp();
+        };
+        // a unit's first scores: no turn, as the products of the unit before are behind
+        auto begin = [&](int flags) {
+          if (!mine(flags)) {
+            pass(&sm.k_full[ks.at], &sm.k_free[ks.at], ks.ph);
+            ks.next();
+            return;
+          }
+          keys(flags);
+          if (dead) return;
           tc::fence_after_sync();
-          values(xc, A(), vs.at, segs, flags & kFirst);
-          if (!wait_for(&sm.p_full[x], p_ph[x])) { dead = true; return; }
-          p_ph[x] ^= 1;
-          tc::fence_after_sync();
-          values(xc, B(), vs.at, segs, false);
-          if (flags & kLast) commit(&sm.o_full[x]);
-          if (x == 1 || !(flags & kHasB)) commit(&sm.v_free[vs.at]);
+          scores(flags);
+          begun(flags);
+        };
+        described(flags, segs);
+        if (!dead && !(flags & kEnd)) begin(flags);
+        while (!dead && !(flags & kEnd)) {
+          at.next();
+          int next = kEnd, next_segs = 0;
+          described(next, next_segs);
+          if (dead) break;
+          // all that the turn needs first: within it the products follow one another
+          const bool more = !(next & (kEnd | kFirst));  // (then of this unit, and of this warp's rows as well)
+          if (mine(flags)) {
+            if (more) keys(next);
+            if (dead || !wait_for(&sm.v_full[vs.at], vs.ph) || !wait_for(&sm.p_full[x], p_ph)) { dead = true; break; }
+            p_ph ^= 1;
+            my_turn();
+            if (dead) break;
+            tc::fence_after_sync();
+            values(segs, (flags & kFirst) != 0);
+            if (flags & kLast) commit(&sm.o_full[x]);
+            if (more) scores(next);
+            your_turn();
+            commit(&sm.v_free[vs.at]);
+            if (more) begun(next);
+          } else {
+            my_turn();
+            if (!dead) your_turn();
+            if (!dead) pass(&sm.v_full[vs.at], &sm.v_free[vs.at], vs.ph);
+            if (!dead && more) begin(next);
+            if (dead) break;
+          }
+          vs.next();
+          if (!more && !(next & kEnd)) begin(next);
+          flags = next;
+          segs = next_segs;
         }
-        if (!(next & kEnd) && (x == 0 || (next & kHasB))) begin(xc, next, next_segs);
       };
-      while (!dead && !(flags & kEnd)) {
-        at.next();
-        int next = kEnd, next_segs = 0;
-        described(next, next_segs);
-        if (dead || !wait_for(&sm.v_full[vs.at], vs.ph)) { dead = true; break; }
-        advance(A(), next, next_segs);
-        if (!dead) advance(B(), next, next_segs);
-        vs.next();
-        flags = next;
-        segs = next_segs;
-      }
+      if (warp == kMmaWarp) role(std::integral_constant<int, 0>());
+      else role(std::integral_constant<int, 1>());
     } else if (warp == kLoadWarp) {
       // ============================== producer ==============================
       Pos<kRing> at;
@@ -484,48 +550,59 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
       int loads = 0;
       const int total = p.sinks + p.window;
       const int rows_of = (int)(p.stride / (D * 2));  // rows of a block
-      for (int u = blockIdx.x; u < units && !dead; u += gridDim.x) {
-        const int piece = u / p.Hkv, hk = u % p.Hkv;
-        const int e = entry_of(list, piece), s = list.items[e];
-        const int t0 = (piece - list.first[e]) * pieces.tokens;
-        const int row0 = b.cu[s], len = b.cu[s + 1] - row0, past = b.past_len[s], blk = b.blk[s];
+      // a unit's sequence is looked up while the one before it is loaded
+      int t0 = 0, row0 = 0, len = 0, past = 0, blk = 0;
+      auto look_up = [&](int u) {
+        const int piece = u / p.Hkv, e = entry_of(list, piece), s = list.items[e];
+        t0 = (piece - list.first[e]) * pieces.tokens;
+        row0 = b.cu[s];
+        len = b.cu[s + 1];
+        past = b.past_len[s];
+        blk = b.blk[s];
+      };
+      int next_u = blockIdx.x;
+      if (next_u < units) look_up(next_u);
+      while (next_u < units && !dead) {
+        const int u = next_u, hk = u % p.Hkv;
+        len -= row0;
         const int tokens = min(pieces.tokens, len - t0);
         const int p0 = past + t0, p1 = p0 + tokens;
         const bool has_b = tokens > tile_tokens;
+        const int row_first_q = row0 + t0;
         // the runs of keys, in order of their positions
         const int lo = max(0, p0 - p.window + 1), before = min(p.sinks, lo);
         const int block_row = blk * rows_of + hk * total;
-        Run run[5];
-        run[0] = {0, min(before, past), block_row, 1};
-        run[1] = {run[0].n, before - run[0].n, row0 + (run[0].n - past), 0};
-        const int old = max(0, min(past, p1) - lo), slot = slot_of(p, lo);
-        run[2] = {lo, min(old, total - slot), block_row + slot, 1};
-        run[3] = {lo + run[2].n, old - run[2].n, block_row + p.sinks, 1};
-        const int fresh = max(lo, past);
-        run[4] = {fresh, p1 - fresh, row0 + (fresh - past), 0};
-        int segs_upto[5], n_segs = 0;
-#pragma unroll
-        for (int i = 0; i < 5; ++i) {
-          n_segs += (run[i].n + kSeg - 1) / kSeg;
-          segs_upto[i] = n_segs;
+        __syncwarp();
+        int n_segs = 0;
+        {
+          auto put = [&](int i, int pos, int n, int row, int ring) {
+            if (lane == 0) {
+              sm.run[i] = {pos, n, row, ring};
+              sm.seg0[i] = n_segs;
+            }
+            n_segs += (n + kSeg - 1) / kSeg;
+          };
+          const int sinks = min(before, past), old = max(0, min(past, p1) - lo), slot = slot_of(p, lo);
+          const int straight = min(old, total - slot), fresh = max(lo, past);
+          put(0, 0, sinks, block_row, 1);
+          put(1, sinks, before - sinks, row0 + (sinks - past), 0);
+          put(2, lo, straight, block_row + slot, 1);
+          put(3, lo + straight, old - straight, block_row + p.sinks, 1);
+          put(4, fresh, p1 - fresh, row0 + (fresh - past), 0);
         }
+        __syncwarp();
         const int n_tiles = (n_segs + kSegs - 1) / kSegs;
+        next_u += gridDim.x;
+        if (next_u < units) look_up(next_u);
         for (int j = 0; j < n_tiles && !dead; ++j) {
           const int segs = min(kSegs, n_segs - j * kSegs);
           // segment lane % 8 of the tile
           const int seg = j * kSegs + (lane & 7);
           int r = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) r += seg >= segs_upto[i];
-          Run mine = run[4];
-          int upto = n_segs;
-#pragma unroll
-          for (int i = 3; i >= 0; --i)
-            if (r == i) {
-              mine = run[i];
-              upto = segs_upto[i];
-            }
-          const int in = (seg - (upto - (mine.n + kSeg - 1) / kSeg)) * kSeg;
+          for (int i = 1; i < 5; ++i) r += seg >= sm.seg0[i];
+          const Run mine = sm.run[r];
+          const int in = (seg - sm.seg0[r]) * kSeg;
           const bool there = (lane & 7) < segs;
           const int pos = mine.pos + in, n = there ? min(kSeg, mine.n - in) : 0, row = mine.row + in;
           // every row sees a key that is not behind the first one and in the last one's window
@@ -547,7 +624,7 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
             tile.flags = (j == 0 ? kFirst : 0) | (j == n_tiles - 1 ? kLast : 0) | (has_b ? kHasB : 0) |
                          (full ? 0 : kPartly);
             tile.segs = segs;
-            tile.row = row0 + t0;
+            tile.row = row_first_q;
             tile.pos0 = p0;
             tile.tokens = tokens;
             tile.hk = hk;
@@ -566,7 +643,7 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
                 mbar_arrive_expect_tx(&sm.q_full[x], (uint32_t)tile_tokens * p.group * D * 2);
 #pragma unroll
                 for (int h = 0; h < kBlocks; ++h)
-                  tma_load_3d(sm.q[x] + h * kBox, &maps.q, 64 * h, hk * p.group, row0 + t0 + x * tile_tokens,
+                  tma_load_3d(sm.q[x] + h * kBox, &maps.q, 64 * h, hk * p.group, row_first_q + x * tile_tokens,
                               &sm.q_full[x]);
               }
               __syncwarp();
@@ -613,7 +690,6 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
       // =============================== check ================================
       Pos<kRing> at;
       Pos<kStages> vs;
-      const int half = warp - kCheckWarp;
       while (!dead) {
         if (!wait_for(&sm.described[at.at], at.ph)) { dead = true; break; }
         Tile& tile = sm.tile[at.at];
@@ -621,11 +697,11 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
         if (flags & kEnd) break;
         if (!wait_for(&sm.v_full[vs.at], vs.ph)) { dead = true; break; }
         if (flags & kPartly) {
-          // this warp's half of the rows: 16 bytes of 4 rows at a time
+          // 16 bytes of 4 rows at a time
           const int rows = tile.segs * kSeg;
           bool odd = false;
 #pragma unroll 4
-          for (int r = half * 4 + (lane >> 3); r < rows; r += 8)
+          for (int r = lane >> 3; r < rows; r += 4)
 #pragma unroll
             for (int h = 0; h < kBlocks; ++h) {
               const uint4 x4 = *reinterpret_cast<const uint4*>(sm.v[vs.at] + h * kBox + r * 128 + (lane & 7) * 16);
