@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kRowThreads) win_rows_kernel(WinParams p, Piec
 // --- the new keys and values into the blocks ----------------------------------
 // Behind the attention, which reads what they replace.
 constexpr int kAppendThreads = 256;
-constexpr int kAppendTokens = 16;  // per piece
+constexpr int kAppendTokens = 8;  // per piece
 
 template <typename T>
 __global__ void __launch_bounds__(kAppendThreads) win_append_kernel(WinParams p, Pieces pieces) {
@@ -223,16 +223,28 @@ __global__ void __launch_bounds__(kAppendThreads) win_append_kernel(WinParams p,
     const int row0 = b.cu[s], len = b.cu[s + 1] - row0, past = b.past_len[s], blk = b.blk[s];
     const int n = min(pieces.tokens, len - t0);
     if (past + t0 >= p.sinks && t0 + n <= len - p.window) continue;  // out of every later window
-    for (int i = threadIdx.x; i < n * row16; i += kAppendThreads) {
-      const int t = t0 + i / row16, x = i % row16, hk = x / head16, c = x % head16;
-      const int j = past + t;
-      if (j >= p.sinks && t < len - p.window) continue;
-      const size_t at = (size_t)slot_of(p, j) * head16 + c;
-      const size_t row = row0 + t;
-      reinterpret_cast<uint4*>(ring_of<T>(p, blk, 0, hk))[at] =
-          reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + row * p.ldk + (size_t)hk * p.d)[c];
-      reinterpret_cast<uint4*>(ring_of<T>(p, blk, 1, hk))[at] =
-          reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + row * p.ldv + (size_t)hk * p.d)[c];
+    // a thread has 16 bytes of a row (keys, then values) and walks the tokens, the
+    // reads of kAhead of them on their way together
+    constexpr int kAhead = 8;
+    for (int x = threadIdx.x; x < 2 * row16; x += kAppendThreads) {
+      const int part = x >= row16, y = part ? x - row16 : x, hk = y / head16, c = y - hk * head16;
+      const long long ld = part ? p.ldv : p.ldk;
+      const T* src = static_cast<const T*>(part ? p.v : p.k) + (size_t)(row0 + t0) * ld + (size_t)hk * p.d;
+      uint4* dst = reinterpret_cast<uint4*>(ring_of<T>(p, blk, part, hk)) + c;
+      for (int i0 = 0; i0 < n; i0 += kAhead) {
+        uint4 v[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+          if (i0 + i < n) v[i] = reinterpret_cast<const uint4*>(src + (size_t)(i0 + i) * ld)[c];
+        int slot = slot_of(p, past + t0 + i0);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int t = t0 + i0 + i;
+          // (what is out of every later window stays out)
+          if (i0 + i < n && (past + t < p.sinks || t >= len - p.window)) dst[(size_t)slot * head16] = v[i];
+          if (++slot == p.sinks + p.window) slot = p.sinks;
+        }
+      }
     }
   }
 }
@@ -293,7 +305,7 @@ cudaError_t launch_win_rows(const WinParams& p, int act, const Pieces& of, int m
 
 cudaError_t launch_win_append(const WinParams& p, int act, const Pieces& of, int max_pieces, int sms,
                               cudaStream_t s) {
-  const int ctas = max_pieces < 4 * sms ? max_pieces : 4 * sms;
+  const int ctas = max_pieces < 8 * sms ? max_pieces : 8 * sms;
   auto kern = act == GDN_F32 ? win_append_kernel<float> : win_append_kernel<__nv_bfloat16>;
   return launch_pdl(kern, dim3(ctas), dim3(kAppendThreads), 0, s, p, of);
 }
@@ -448,20 +460,22 @@ int gdn_win_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
                                                              : GDN_PREFILL_SERIAL;
   if (b.listed && gdn::launch_plan(b, of, s) != cudaSuccess) return GDN_ERR_CUDA;
   if (p->ev_before && cudaEventRecord(p->ev_before, s) != cudaSuccess) return GDN_ERR_CUDA;
-  if (may_long) {
-    if (tc && gdn::launch_win_tc(wp, of, most_pieces(of.tokens), p->sms, p->win_parts, s) != cudaSuccess)
+  const gdn::Pieces of_few = {1, few, 0x7fffffff};
+  if (may_long && tc) {
+    if (gdn::launch_win_tc(wp, of, most_pieces(of.tokens), p->sms, p->win_parts, s) != cudaSuccess)
       return GDN_ERR_CUDA;
-    if (tc) wp.report = 0;
+    wp.report = 0;
+  }
+  // (behind the prompts' kernel, not behind what follows it)
+  if (may_short && gdn::launch_win_short(wp, of_few, max_items, p->sms, may_long && tc, p->win_parts, s) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  if (may_short) wp.report = 0;
+  if (may_long) {
     if (gdn::launch_win_rows(wp, p->act, of, most_pieces(of.tokens), p->sms, p->win_parts, tc, s) != cudaSuccess)
       return GDN_ERR_CUDA;
     wp.report = 0;
     if (!b.listed) of.tokens = gdn::kAppendTokens;
     if (gdn::launch_win_append(wp, p->act, of, most_pieces(of.tokens), p->sms, s) != cudaSuccess)
-      return GDN_ERR_CUDA;
-  }
-  if (may_short) {
-    of = {1, few, 0x7fffffff};
-    if (gdn::launch_win_short(wp, of, max_items, p->sms, p->win_parts, s) != cudaSuccess)
       return GDN_ERR_CUDA;
   }
   if (p->ev_after && cudaEventRecord(p->ev_after, s) != cudaSuccess) return GDN_ERR_CUDA;

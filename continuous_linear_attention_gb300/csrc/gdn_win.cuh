@@ -55,8 +55,9 @@ cudaError_t launch_win_append(const WinParams& p, int act, const Pieces& of, int
 bool win_short_supported(int d, int act);
 int win_short_tokens(int group);
 size_t win_short_room(int sms, int d);
-cudaError_t launch_win_short(const WinParams& p, const Pieces& of, int max_items, int sms, void* room,
-                             cudaStream_t s);
+// late: right behind launch_win_tc, beside its last units.
+cudaError_t launch_win_short(const WinParams& p, const Pieces& of, int max_items, int sms, bool late,
+                             void* room, cudaStream_t s);
 
 // The form for prompts (gdn_win_tc.cu): pieces of win_tc_tokens(group) tokens.
 bool win_tc_supported(int d, int act, int group);

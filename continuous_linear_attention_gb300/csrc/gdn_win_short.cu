@@ -124,7 +124,7 @@ __host__ __device__ constexpr size_t part_floats() {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
-win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float* left) {
+win_short_kernel(WinParams p, Pieces pieces, int parts, int late, int32_t* arrived, float* left) {
   constexpr int kChunks = D / 32;  // 16-byte chunks per lane of a row of q or k
   constexpr int kHalves = D / 64;  // column halves of the output
   constexpr int kStages = ShortSmem<D>::kStages;
@@ -138,7 +138,13 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
     }
     fence_mbar_init();
   }
-  pdl_wait_then_release();
+  // late: launched behind the prompts' kernel, whose SMs it takes as they come free
+  // without waiting for it (other sequences, other blocks; the inputs and the list are
+  // there, as that kernel releases after its own wait); it waits before it ends.
+  if (late)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  else
+    pdl_wait_then_release();
   const Batch& b = p.batch;
   SeqList list;
   const PlanSmem* plan = nullptr;
@@ -206,6 +212,7 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
     if (dead)
       for (uint32_t i = fills > kStages ? fills - kStages : 0; i < fills; ++i)
         mbar_wait_bounded(&sm.full[i % kStages], i / kStages & 1);
+    if (late) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
 
@@ -529,10 +536,11 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int32_t* arrived, float*
           *reinterpret_cast<const uint4*>(src);
     }
   }
+  if (late) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int D>
-cudaError_t launch_short(const WinParams& p, const Pieces& of, int parts, int ctas, void* room,
+cudaError_t launch_short(const WinParams& p, const Pieces& of, int parts, int ctas, bool late, void* room,
                          cudaStream_t s) {
   auto kern = win_short_kernel<D>;
   const size_t smem = sizeof(ShortSmem<D>);
@@ -541,7 +549,7 @@ cudaError_t launch_short(const WinParams& p, const Pieces& of, int parts, int ct
   if (e != cudaSuccess) return e;
   int32_t* arrived = static_cast<int32_t*>(room);
   float* left = reinterpret_cast<float*>(static_cast<unsigned char*>(room) + kWinCounterBytes + kWinListBytes);
-  return launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, s, p, of, parts, arrived, left);
+  return launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, s, p, of, parts, (int)late, arrived, left);
 }
 
 }  // namespace
@@ -554,8 +562,8 @@ size_t win_short_room(int sms, int d) {
   return kWinCounterBytes + kWinListBytes + (size_t)2 * sms * (d == 64 ? part_floats<64>() : part_floats<128>()) * sizeof(float);
 }
 
-cudaError_t launch_win_short(const WinParams& p, const Pieces& of, int max_items, int sms, void* room,
-                             cudaStream_t s) {
+cudaError_t launch_win_short(const WinParams& p, const Pieces& of, int max_items, int sms, bool late,
+                             void* room, cudaStream_t s) {
   // Where the kv heads of all sequences leave CTAs idle, their windows are cut into
   // parts of two stages at least.
   const long long heads = (long long)max_items * p.Hkv;
@@ -565,8 +573,8 @@ cudaError_t launch_win_short(const WinParams& p, const Pieces& of, int max_items
   if (parts > (stages + 1) / 2) parts = (stages + 1) / 2;
   const long long units = heads * parts;
   const int ctas = (int)(units < side ? (units > 0 ? units : 1) : side);
-  return p.d == 64 ? launch_short<64>(p, of, parts, ctas, room, s)
-                   : launch_short<128>(p, of, parts, ctas, room, s);
+  return p.d == 64 ? launch_short<64>(p, of, parts, ctas, late, room, s)
+                   : launch_short<128>(p, of, parts, ctas, late, room, s);
 }
 
 }  // namespace gdn
