@@ -391,6 +391,7 @@ int gdn_state_pool_destroy(gdn_pool_t* p) {
   cudaFree(p->work);
   cudaFree(p->lin_states);
   cudaFree(p->win_parts);
+  cudaFree(p->sel_room);
   scratch_release(p);
   if (prev >= 0) cudaSetDevice(prev);
   delete p;

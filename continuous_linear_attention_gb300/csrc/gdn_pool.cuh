@@ -37,6 +37,8 @@ struct gdn_pool {
   int lin_slots;
   // windowed attention pools: partial results of split windows (gdn_win.cu)
   void* win_parts;
+  // selective scan pools: states between the segments of a split prompt (gdn_sel.cu)
+  void* sel_room;
 };
 
 namespace gdn {

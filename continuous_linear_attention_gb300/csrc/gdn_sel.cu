@@ -15,6 +15,7 @@
 #include <new>
 
 #include "gdn_cta.cuh"
+#include "gdn_lin.cuh"
 #include "gdn_pool.cuh"
 #include "gdn_seqs.cuh"
 
@@ -63,11 +64,22 @@ __device__ __forceinline__ float ex2(float x) {
 // 2^x for a decay (x <= 0).  Near 0, where a state keeps its value over many
 // steps and a bias of the exponential adds up over as many (the hardware's is
 // about 2^-27 there: 2e-5 of the state after 3,000 steps of 2^-13), from its
-// series, whose next term is 1.3e-9 at -1/16, rounded to nearest.
+// series, rounded to nearest: its next term is 6e-10 at -1/64, where a state
+// forgets fast enough for the bias (6e-7 of it).
+constexpr float kNear = -0.015625f;
+constexpr float kExp1 = 6.9314718e-1f, kExp2 = 2.4022651e-1f, kExp3 = 5.5504109e-2f;
 __device__ __forceinline__ float decay2(float x) {
-  const float p = fmaf(x, fmaf(x, fmaf(x, fmaf(x, 9.6181291e-3f, 5.5504109e-2f), 2.4022651e-1f), 6.9314718e-1f), 1.f);
+  const float p = fmaf(x, fmaf(x, fmaf(x, kExp3, kExp2), kExp1), 1.f);
   const float a = ex2(x);
-  return x > -0.0625f ? p : a;
+  return x > kNear ? p : a;
+}
+__device__ __forceinline__ F2 decay2(F2 x) {
+  const F2 p = fma2(x, fma2(x, fma2(x, f2(kExp3, kExp3), f2(kExp2, kExp2)), f2(kExp1, kExp1)), f2(1.f, 1.f));
+  float x0, x1, p0, p1;
+  unf2(x, x0, x1);
+  unf2(p, p0, p1);
+  const float a0 = ex2(x0), a1 = ex2(x1);
+  return f2(x0 > kNear ? p0 : a0, x1 > kNear ? p1 : a1);
 }
 
 // --- convolution -------------------------------------------------------------
@@ -200,6 +212,10 @@ struct ScanParams {
   size_t stride, ssm_off;
   int channels;
   int report;  // this kernel raises the batch's flags
+  // segments of long sequences: how many there is room for (0: none), the states at
+  // their starts (first their own), their steps' sums
+  int slots, sms;
+  float *seg_states, *seg_sums;
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -210,7 +226,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kStepThreads = 256;
 
 template <typename T, int N>
-__global__ void __launch_bounds__(kStepThreads) sel_step_kernel(ScanParams p) {
+__global__ void __launch_bounds__(kStepThreads, 3) sel_step_kernel(ScanParams p) {
   constexpr int kLanes = N / 4;  // threads per channel
   constexpr int kSeqs = 4;
   __shared__ PlanSmem plan;
@@ -230,33 +246,47 @@ __global__ void __launch_bounds__(kStepThreads) sel_step_kernel(ScanParams p) {
   const float A[4] = {-expf(al.x) * kLog2e, -expf(al.y) * kLog2e, -expf(al.z) * kLog2e,
                       -expf(al.w) * kLog2e};
   const float bias = p.dt_bias && live ? p.dt_bias[c] : 0.f, skip = p.D && live ? p.D[c] : 0.f;
+  const int* lo = b.listed ? b.cu : plan.lo;
+  const int* blocks = b.listed ? b.blk : plan.blk;
+  auto four = [](const T* q, float* f) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(q);
+      f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(q);
+      f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
+      f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
+    }
+  };
   for (int i0 = blockIdx.y * kSeqs; i0 < list.n; i0 += gridDim.y * kSeqs) {
     const int m = min(kSeqs, list.n - i0);
     float4 h[kSeqs];
     float* st[kSeqs];
     float B[kSeqs][4], C[kSeqs][4], u[kSeqs], dt[kSeqs], z[kSeqs];
-    size_t row[kSeqs];
+    int row[kSeqs];
+    bool past[kSeqs];
 #pragma unroll
     for (int i = 0; i < kSeqs; ++i) {
       if (i >= m || !live) continue;
       const int s = list.items[i0 + i];
-      row[i] = b.cu[s];
-      st[i] = reinterpret_cast<float*>(p.layer_base + (size_t)b.blk[s] * p.stride + p.ssm_off) + at;
-      h[i] = b.has_past[s] ? *reinterpret_cast<const float4*>(st[i]) : make_float4(0.f, 0.f, 0.f, 0.f);
-      u[i] = to_f32(static_cast<const T*>(p.u)[row[i] * p.ldu + c]);
-      dt[i] = to_f32(static_cast<const T*>(p.dt)[row[i] * p.lddt + c]);
-      z[i] = p.z ? to_f32(static_cast<const T*>(p.z)[row[i] * p.ldz + c]) : 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        B[i][k] = to_f32(static_cast<const T*>(p.B)[row[i] * p.ldb + g * 4 + k]);
-        C[i][k] = to_f32(static_cast<const T*>(p.C)[row[i] * p.ldc + g * 4 + k]);
-      }
+      row[i] = lo[s];
+      // (read whether it counts or not: no wait for has_past)
+      st[i] = reinterpret_cast<float*>(p.layer_base + (size_t)blocks[s] * p.stride + p.ssm_off) + at;
+      h[i] = *reinterpret_cast<const float4*>(st[i]);
+      past[i] = b.has_past[s];
+      const size_t r = row[i];
+      u[i] = to_f32(static_cast<const T*>(p.u)[r * p.ldu + c]);
+      dt[i] = to_f32(static_cast<const T*>(p.dt)[r * p.lddt + c]);
+      z[i] = p.z ? to_f32(static_cast<const T*>(p.z)[r * p.ldz + c]) : 0.f;
+      four(static_cast<const T*>(p.B) + r * p.ldb + g * 4, B[i]);
+      four(static_cast<const T*>(p.C) + r * p.ldc + g * 4, C[i]);
     }
 #pragma unroll
     for (int i = 0; i < kSeqs; ++i) {
       if (i >= m) continue;  // (the same for the whole CTA)
       float y = 0.f;
       if (live) {
+        if (!past[i]) h[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         const float d = softplus_f32(dt[i] + bias), du = d * u[i];
         h[i].x = fmaf(h[i].x, decay2(d * A[0]), du * B[i][0]);
         h[i].y = fmaf(h[i].y, decay2(d * A[1]), du * B[i][1]);
@@ -270,7 +300,7 @@ __global__ void __launch_bounds__(kStepThreads) sel_step_kernel(ScanParams p) {
       if (live && g == 0) {
         y = fmaf(skip, u[i], y);
         if (p.z) y *= silu_f32(z[i]);
-        static_cast<T*>(p.y)[row[i] * p.ldy + c] = from_f32<T>(y);
+        static_cast<T*>(p.y)[(size_t)row[i] * p.ldy + c] = from_f32<T>(y);
       }
     }
   }
@@ -288,41 +318,82 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// Longer sequences: a CTA walks the tokens of one sequence for kCB channels,
-// kG threads per channel with N / kG states each in registers, a tile of kTT
-// tokens at a time, the next one on its way.
+// Longer sequences: a CTA walks the tokens of one sequence, or of a segment of
+// it, for kCB channels, kG threads per channel with N / kG states each in
+// registers, a tile of kTT tokens at a time, the next one on its way.  Bound by
+// issue slots: per state and token two multiplications, the exponential with its
+// series and its choice, two multiply-adds, in packed pairs 14 instructions for
+// two states, and some 50 per token and channel for softplus, SiLU and the
+// tile's way through shared memory.  15,843 tokens x 4,096 channels: TIME_SCAN.
+//
+// Long sequences of few channels are cut into segments: a first pass (kState)
+// computes each segment's own state (from zeros) and its steps' sum, a small
+// kernel the states at the segments' starts, h_start <- e^{A sum} h_start + own, and the
+// output pass runs all segments side by side.  The work is 1.7 times as much, so
+// that is done where otherwise too few CTAs run or one sequence is longer than an
+// SM's share of all (segment_tokens; every kernel finds the same from the lengths).
 constexpr int kScanThreads = 128;
+constexpr int kSegmentBytes = 32 << 20;  // room for states between segments
+constexpr int kSegmentsMax = 8192;       // (and for their steps' sums)
 
-template <typename T, int N, int kG>
+// Tokens per segment for a call whose longest sequence has `longest` and all
+// together `tokens`, in ch_blocks CTAs each; slots: segments there is room for.
+// In units of a token of one CTA where an SM is full: alone on an SM a CTA takes
+// about two for a token; a segment's first loads, and the launches, cost as much
+// as some 300.
+__host__ __device__ inline int segment_tokens(int longest, long long tokens, int ch_blocks, int slots,
+                                              int n, int sms) {
+  const long long share = tokens * ch_blocks / sms;
+  const long long whole = 2ll * longest > share ? 2ll * longest : share;
+  long long seg = (share / 4 + 31) / 32 * 32;  // four of them to an SM
+  if (seg < 64) seg = 64;
+  const long long split = share * 7 / 4 + 2 * seg + 300;
+  if (split >= whole || tokens / seg + n > slots) return 0x7fffffff;
+  return (int)seg;
+}
+
+template <typename T, int N, int kG, bool kState>
 struct ScanSmem {
   static constexpr int kCB = kScanThreads / kG;
-  static constexpr int kTT = kG == 1 ? 16 : 32;
+  static constexpr int kTT = 32;
   static constexpr int kPad = kG > 1 ? 32 / kG : 0;  // the lanes of a channel write rows of y: apart by banks
-  T u[2][kTT][kCB], dt[2][kTT][kCB], z[2][kTT][kCB];
-  T B[2][kTT][N], C[2][kTT][N];
-  float2 step[kTT][kCB];  // dt and dt u
-  float Bf[kTT][N], Cf[kTT][N];
-  float y[kTT][kCB + kPad];
+  static constexpr int kOut = kState ? 1 : kTT;
+  T u[2][kTT][kCB], dt[2][kTT][kCB], z[2][kOut][kCB];
+  T B[2][kTT][N], C[2][kOut][N];
+  alignas(16) float2 step[kTT][kCB];  // dt and dt u
+  alignas(16) float Bf[kTT][N], Cf[kOut][N];
+  float y[kOut][kCB + kPad];
   PlanSmem plan;
 };
 
-template <typename T, int N, int kG>
+template <typename T, int N, int kG, bool kState>
 __global__ void __launch_bounds__(kScanThreads) sel_scan_kernel(ScanParams p) {
-  using Smem = ScanSmem<T, N, kG>;
+  using Smem = ScanSmem<T, N, kG, kState>;
   constexpr int kCB = Smem::kCB, kTT = Smem::kTT, kNS = N / kG, kPer = 16 / (int)sizeof(T);
   extern __shared__ __align__(16) unsigned char scan_smem[];
   Smem& sm = *reinterpret_cast<Smem*>(scan_smem);
   pdl_wait_then_release();
   const Batch& b = p.batch;
+  const int ch_blocks = (p.channels + kCB - 1) / kCB;
+  int seg_tokens = 0x7fffffff;
   const SeqList list =
       b.listed ? listed_long(b)
-               : plan_self(b, Pieces{2, 0x7fffffff, 0x7fffffff}, sm.plan, p.report && blockIdx.x == 0);
-  const int ch_blocks = (p.channels + kCB - 1) / kCB;
+               : plan_self(b, Pieces{2, 0x7fffffff, 0x7fffffff}, sm.plan, p.report && blockIdx.x == 0,
+                           [&](int longest, int tokens) {
+                             if (p.slots > 0)
+                               seg_tokens = segment_tokens(longest, tokens, ch_blocks, p.slots, b.N, p.sms);
+                             return seg_tokens;
+                           });
+  if (kState && seg_tokens == 0x7fffffff) return;
   const int piece = blockIdx.x / ch_blocks;
   if (piece >= list.total) return;
-  const int s = list.items[entry_of(list, piece)];
+  const int e = entry_of(list, piece), s = list.items[e];
+  const int seg = piece - list.first[e], segs = list.first[e + 1] - list.first[e];
+  if (kState && seg == segs - 1) return;  // (its own state is not needed by any other)
   const int cb = (int)(blockIdx.x % ch_blocks) * kCB;  // first channel
-  const int row0 = b.cu[s], len = b.cu[s + 1] - row0;
+  const int t_first = segs > 1 ? seg * seg_tokens : 0;
+  const int row0 = b.cu[s] + t_first;
+  const int len = segs > 1 ? min(seg_tokens, b.cu[s + 1] - row0) : b.cu[s + 1] - row0;
   const int tid = threadIdx.x, c = tid / kG, g = tid % kG;
   const bool live = cb + c < p.channels;
   const int wide = min(kCB, p.channels - cb);
@@ -336,27 +407,50 @@ __global__ void __launch_bounds__(kScanThreads) sel_scan_kernel(ScanParams p) {
       const size_t row = row0 + t0 + t;
       cp_async16(&sm.u[buf][t][x], static_cast<const T*>(p.u) + row * p.ldu + cb + x);
       cp_async16(&sm.dt[buf][t][x], static_cast<const T*>(p.dt) + row * p.lddt + cb + x);
-      if (p.z) cp_async16(&sm.z[buf][t][x], static_cast<const T*>(p.z) + row * p.ldz + cb + x);
+      if (!kState && p.z) cp_async16(&sm.z[buf][t][x], static_cast<const T*>(p.z) + row * p.ldz + cb + x);
     }
     for (int i = tid; i < n * kStates; i += kScanThreads) {
       const int t = i / kStates, x = i % kStates * kPer;
       const size_t row = row0 + t0 + t;
       cp_async16(&sm.B[buf][t][x], static_cast<const T*>(p.B) + row * p.ldb + x);
-      cp_async16(&sm.C[buf][t][x], static_cast<const T*>(p.C) + row * p.ldc + x);
+      if (!kState) cp_async16(&sm.C[buf][t][x], static_cast<const T*>(p.C) + row * p.ldc + x);
     }
     cp_async_commit();
   };
   stage(0, 0);
 
-  float* st = reinterpret_cast<float*>(p.layer_base + (size_t)b.blk[s] * p.stride + p.ssm_off) +
-              (size_t)(cb + c) * N + g * kNS;
-  float h[kNS], A[kNS];
-  const bool past = b.has_past[s];
+  const size_t at = (size_t)(live ? cb + c : 0) * N + g * kNS;
+  float* st = reinterpret_cast<float*>(p.layer_base + (size_t)b.blk[s] * p.stride + p.ssm_off) + at;
+  float* slot = p.seg_states + (size_t)piece * p.channels * N + at;
+  const float* from = kState ? nullptr : segs > 1 ? slot : b.has_past[s] ? st : nullptr;
+  F2 h[kNS / 2], A[kNS / 2];
 #pragma unroll
-  for (int i = 0; i < kNS; ++i) {
-    h[i] = live && past ? st[i] : 0.f;
-    A[i] = live ? -expf(p.A_log[(size_t)(cb + c) * N + g * kNS + i]) * kLog2e : 0.f;
+  for (int i = 0; i < kNS / 2; ++i) {
+    h[i] = from ? f2(from[2 * i], from[2 * i + 1]) : 0ull;
+    A[i] = f2(-expf(p.A_log[at + 2 * i]) * kLog2e, -expf(p.A_log[at + 2 * i + 1]) * kLog2e);
   }
+  // a thread's channels of a tile's other work: two of them, the same ones always
+  // (a half of a 32-bit word of bf16 each)
+  constexpr int kPairs = kCB / 2;
+  const int xc = tid % kPairs * 2;
+  const bool x_live = xc < wide;
+  float bias[2] = {0.f, 0.f}, skip[2] = {0.f, 0.f}, sum[2] = {0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (p.dt_bias && x_live) bias[k] = p.dt_bias[cb + xc + k];
+    if (p.D && x_live) skip[k] = p.D[cb + xc + k];
+  }
+  auto two = [](const T* q, float& a, float& b2) {
+    if constexpr (sizeof(T) == 4) {
+      const float2 v = *reinterpret_cast<const float2*>(q);
+      a = v.x;
+      b2 = v.y;
+    } else {
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(q);
+      a = __uint_as_float(v << 16);
+      b2 = __uint_as_float(v & 0xffff0000u);
+    }
+  };
   for (int t0 = 0, buf = 0; t0 < len; t0 += kTT, buf ^= 1) {
     const int n = min(kTT, len - t0);
     if (t0 + kTT < len) {
@@ -367,31 +461,44 @@ __global__ void __launch_bounds__(kScanThreads) sel_scan_kernel(ScanParams p) {
     }
     __syncthreads();  // the tile has landed, and the last one's y is read
     // the time steps, and B and C in fp32
-    for (int i = tid; i < n * kCB; i += kScanThreads) {
-      const int t = i / kCB, x = i % kCB;
-      if (x >= wide) continue;
-      const float d = softplus_f32(to_f32(sm.dt[buf][t][x]) + (p.dt_bias ? p.dt_bias[cb + x] : 0.f));
-      sm.step[t][x] = make_float2(d, d * to_f32(sm.u[buf][t][x]));
+    for (int t = tid / kPairs; t < n; t += kScanThreads / kPairs) {
+      if (!x_live) break;
+      float d[2], u[2];
+      two(&sm.dt[buf][t][xc], d[0], d[1]);
+      two(&sm.u[buf][t][xc], u[0], u[1]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        d[k] = softplus_f32(d[k] + bias[k]);
+        if (kState) sum[k] += d[k];
+      }
+      *reinterpret_cast<float4*>(&sm.step[t][xc]) = make_float4(d[0], d[0] * u[0], d[1], d[1] * u[1]);
     }
-    for (int i = tid; i < n * N; i += kScanThreads) {
-      (&sm.Bf[0][0])[i] = to_f32((&sm.B[buf][0][0])[i]);
-      (&sm.Cf[0][0])[i] = to_f32((&sm.C[buf][0][0])[i]);
+    for (int i = 2 * tid; i < n * N; i += 2 * kScanThreads) {
+      two(&sm.B[buf][0][0] + i, (&sm.Bf[0][0])[i], (&sm.Bf[0][0])[i + 1]);
+      if (!kState) two(&sm.C[buf][0][0] + i, (&sm.Cf[0][0])[i], (&sm.Cf[0][0])[i + 1]);
     }
     __syncthreads();
-    for (int t = 0; t < n; t += kG) {
-      float part[kG];
+    auto token = [&](int t) {
+      const float2 d = sm.step[t][c];
+      const F2 dd = f2(d.x, d.x), du = f2(d.y, d.y);
+      [[maybe_unused]] F2 part = 0ull;
 #pragma unroll
-      for (int k = 0; k < kG; ++k) {
-        part[k] = 0.f;
-        if (t + k >= n) continue;
-        const float2 d = sm.step[t + k][c];
-#pragma unroll
-        for (int i = 0; i < kNS; ++i) {
-          h[i] = fmaf(h[i], decay2(d.x * A[i]), d.y * sm.Bf[t + k][g * kNS + i]);
-          part[k] = fmaf(h[i], sm.Cf[t + k][g * kNS + i], part[k]);
+      for (int i = 0; i < kNS / 2; i += 2) {
+        const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(&sm.Bf[t][g * kNS + 2 * i]);
+        h[i] = fma2(h[i], decay2(mul2(dd, A[i])), mul2(du, b2.x));
+        h[i + 1] = fma2(h[i + 1], decay2(mul2(dd, A[i + 1])), mul2(du, b2.y));
+        if constexpr (!kState) {
+          const ulonglong2 c2 = *reinterpret_cast<const ulonglong2*>(&sm.Cf[t][g * kNS + 2 * i]);
+          part = i == 0 ? mul2(h[i], c2.x) : fma2(h[i], c2.x, part);
+          part = fma2(h[i + 1], c2.y, part);
         }
       }
-      // the sums over a channel's lanes: lane k ends up with token k's
+      float y0 = 0.f, y1 = 0.f;
+      if constexpr (!kState) unf2(part, y0, y1);
+      return y0 + y1;
+    };
+    // the sums over a channel's lanes: lane k ends up with token k's
+    auto across = [&](float* part) {
 #pragma unroll
       for (int w = kG / 2; w >= 1; w >>= 1) {
 #pragma unroll
@@ -401,40 +508,150 @@ __global__ void __launch_bounds__(kScanThreads) sel_scan_kernel(ScanParams p) {
           part[i] = keep + __shfl_xor_sync(0xffffffffu, send, w);
         }
       }
-      if (t + g < n) sm.y[t + g][c] = part[0];
+      return part[0];
+    };
+    int t = 0;
+    for (; t + kG <= n; t += kG) {
+      float part[kG];
+#pragma unroll
+      for (int k = 0; k < kG; ++k) part[k] = token(t + k);
+      if constexpr (!kState) sm.y[t + g][c] = across(part);
+    }
+    if (t < n) {
+      float part[kG];
+#pragma unroll
+      for (int k = 0; k < kG; ++k) part[k] = t + k < n ? token(t + k) : 0.f;
+      if constexpr (!kState) {
+        const float y = across(part);
+        if (t + g < n) sm.y[t + g][c] = y;
+      }
     }
     __syncthreads();
-    for (int i = tid; i < n * kCB; i += kScanThreads) {
-      const int t = i / kCB, x = i % kCB;
-      if (x >= wide) continue;
-      float y = sm.y[t][x];
-      if (p.D) y = fmaf(p.D[cb + x], to_f32(sm.u[buf][t][x]), y);
-      if (p.z) y *= silu_f32(to_f32(sm.z[buf][t][x]));
-      static_cast<T*>(p.y)[(size_t)(row0 + t0 + t) * p.ldy + cb + x] = from_f32<T>(y);
-    }
-    __syncthreads();  // the buffer may be staged over
-  }
-  if (live) {
+    if constexpr (!kState) {
+      for (int q = tid / kPairs; q < n; q += kScanThreads / kPairs) {
+        if (!x_live) break;
+        float u[2], y[2];
+        two(&sm.u[buf][q][xc], u[0], u[1]);
 #pragma unroll
-    for (int i = 0; i < kNS; ++i) st[i] = h[i];
+        for (int k = 0; k < 2; ++k) y[k] = fmaf(skip[k], u[k], sm.y[q][xc + k]);
+        if (p.z) {
+          float z[2];
+          two(&sm.z[buf][q][xc], z[0], z[1]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) y[k] *= silu_f32(z[k]);
+        }
+        T* out = static_cast<T*>(p.y) + (size_t)(row0 + t0 + q) * p.ldy + cb + xc;
+        if constexpr (sizeof(T) == 4) {
+          *reinterpret_cast<float2*>(out) = make_float2(y[0], y[1]);
+        } else {
+          *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(y[0], y[1]);
+        }
+      }
+      __syncthreads();  // the buffer may be staged over
+    }
+  }
+  if (live && (kState || seg == segs - 1)) {
+    float* to = kState ? slot : st;
+#pragma unroll
+    for (int i = 0; i < kNS / 2; ++i) unf2(h[i], to[2 * i], to[2 * i + 1]);
+  }
+  if constexpr (kState) {
+    // the steps' sums, over the threads that share a pair of channels
+    __syncthreads();
+    float2* room = &sm.step[0][0];
+    room[tid] = make_float2(sum[0], sum[1]);
+    __syncthreads();
+    if (tid < kPairs && x_live) {
+      float2 all = make_float2(0.f, 0.f);
+      for (int i = tid; i < kScanThreads; i += kPairs) {
+        all.x += room[i].x;
+        all.y += room[i].y;
+      }
+      *reinterpret_cast<float2*>(p.seg_sums + (size_t)piece * p.channels + cb + xc) = all;
+    }
   }
 }
 
-template <typename T, int N, int kG>
-cudaError_t launch_scan(const ScanParams& p, int max_items, cudaStream_t s) {
+// The states at the segments' starts, in the place of their own ones: a thread
+// per state entry, a chain of as many steps as there are segments.
+template <int kCB>
+__global__ void __launch_bounds__(256) sel_segments_kernel(ScanParams p, int n_states) {
+  __shared__ PlanSmem plan;
+  pdl_wait_then_release();
+  const Batch& b = p.batch;
+  int seg_tokens = 0x7fffffff;
+  const SeqList list = plan_self(b, Pieces{2, 0x7fffffff, 0x7fffffff}, plan, false, [&](int longest, int tokens) {
+    return seg_tokens = segment_tokens(longest, tokens, (p.channels + kCB - 1) / kCB, p.slots, b.N, p.sms);
+  });
+  if (seg_tokens == 0x7fffffff) return;
+  const int words = p.channels * n_states, parts = (words + 255) / 256;
+  for (int u = blockIdx.x; u < list.n * parts; u += gridDim.x) {
+    const int e = u / parts, at = u % parts * 256 + threadIdx.x;
+    const int first = list.first[e], segs = list.first[e + 1] - first;
+    if (segs < 2 || at >= words) continue;
+    const int s = list.items[e], c = at / n_states;
+    const float A = -expf(p.A_log[at]) * kLog2e;
+    float h = b.has_past[s]
+                  ? reinterpret_cast<const float*>(p.layer_base + (size_t)b.blk[s] * p.stride + p.ssm_off)[at]
+                  : 0.f;
+    constexpr int kAhead = 8;
+    for (int i0 = 0; i0 < segs; i0 += kAhead) {
+      float own[kAhead], sum[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (i0 + i < segs - 1) {  // (the last one's own state is not there)
+          own[i] = p.seg_states[(size_t)(first + i0 + i) * words + at];
+          sum[i] = p.seg_sums[(size_t)(first + i0 + i) * p.channels + c];
+        }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (i0 + i >= segs) break;
+        p.seg_states[(size_t)(first + i0 + i) * words + at] = h;
+        h = fmaf(h, decay2(sum[i] * A), own[i]);
+      }
+    }
+  }
+}
+
+template <typename T, int N, int kG, bool kState>
+cudaError_t launch_scan_pass(const ScanParams& p, long long pieces, cudaStream_t s) {
   constexpr int kCB = kScanThreads / kG;
-  auto kern = sel_scan_kernel<T, N, kG>;
-  const size_t smem = sizeof(ScanSmem<T, N, kG>);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  auto kern = sel_scan_kernel<T, N, kG, kState>;
+  const size_t smem = sizeof(ScanSmem<T, N, kG, kState>);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const long long ctas = (long long)max_items * ((p.channels + kCB - 1) / kCB);
-  return launch_pdl(kern, dim3((unsigned)ctas), dim3(kScanThreads), smem, s, p);
+  return launch_pdl(kern, dim3((unsigned)(pieces * ((p.channels + kCB - 1) / kCB))), dim3(kScanThreads), smem,
+                    s, p);
+}
+
+template <typename T, int N, int kG>
+cudaError_t launch_scan(ScanParams p, int max_items, cudaStream_t s) {
+  constexpr int kCB = kScanThreads / kG;
+  const int ch_blocks = (p.channels + kCB - 1) / kCB;
+  // What the segments' rule can say for any lengths that the call may have: none if
+  // the longest possible one is not worth it.
+  long long pieces = max_items;
+  const Batch& b = p.batch;
+  const int longest = b.hint > 0 && b.hint < b.T ? b.hint : b.T;
+  if (b.listed || p.slots < 2 ||
+      segment_tokens(longest, b.T, ch_blocks, 0x7fffffff, b.N, p.sms) == 0x7fffffff) {
+    p.slots = 0;
+  } else {
+    pieces += 4ll * p.sms / ch_blocks + 1;  // (segments are a quarter of an SM's share at least)
+    cudaError_t e = launch_scan_pass<T, N, kG, true>(p, pieces, s);
+    if (e == cudaSuccess) {
+      p.report = 0;
+      e = launch_pdl(sel_segments_kernel<kCB>, dim3(4 * p.sms), dim3(256), 0, s, p, N);
+    }
+    if (e != cudaSuccess) return e;
+  }
+  return launch_scan_pass<T, N, kG, false>(p, pieces, s);
 }
 
 template <typename T, int N>
 cudaError_t launch_step(const ScanParams& p, int max_items, int sms, cudaStream_t s) {
   const int per = kStepThreads / (N / 4), x = (p.channels + per - 1) / per;
-  int y = (4 * sms + x - 1) / x;  // about four CTAs per SM
+  int y = (3 * sms + x - 1) / x;  // about three CTAs per SM
   const int most = (max_items + 3) / 4;
   if (y > most) y = most;
   return launch_pdl(sel_step_kernel<T, N>, dim3(x, y), dim3(kStepThreads), 0, s, p);
@@ -572,6 +789,13 @@ int gdn_sel_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int ch
     delete p;
     return st;
   }
+  // states between segments, and their steps' sums (less than that again)
+  if (cudaMalloc(&p->sel_room, gdn::kSegmentBytes + gdn::kSegmentBytes / 16) != cudaSuccess) {
+    cudaGetLastError();
+    p->sel_room = nullptr;
+    gdn_state_pool_destroy(p);
+    return GDN_ERR_NOMEM;
+  }
   *out = p;
   return GDN_OK;
 }
@@ -679,6 +903,12 @@ int gdn_sel_scan_varlen_forward(gdn_pool_t* p, int layer, const void* u, int64_t
   sp.stride = p->stride;
   sp.ssm_off = p->rec_off;
   sp.channels = p->sel_C;
+  sp.sms = p->sms;
+  const size_t state_bytes = (size_t)p->sel_C * p->sel_N * sizeof(float);
+  sp.slots = (int)(gdn::kSegmentBytes / state_bytes);
+  if (sp.slots > gdn::kSegmentsMax) sp.slots = gdn::kSegmentsMax;
+  sp.seg_states = static_cast<float*>(p->sel_room);
+  sp.seg_sums = sp.seg_states + gdn::kSegmentBytes / sizeof(float);
   // what the call can hold: single tokens, and longer sequences
   int max_one = N < p->num_blocks - 1 ? N : p->num_blocks - 1;
   if (max_one > T) max_one = T;

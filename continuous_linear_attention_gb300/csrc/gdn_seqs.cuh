@@ -44,7 +44,7 @@ struct PlanSmem {
   int32_t lo[kSelfPlan + 1], blk[kSelfPlan], len[kSelfPlan], items[kSelfPlan], first[kSelfPlan + 1];
   int32_t named[kPlanSlots];  // a block index, kPlanTwice with it where two sequences name it
   unsigned flags;
-  int n, total;
+  int n, total, longest, tokens;  // (longest, tokens: of the sequences with pieces)
 };
 constexpr int kPlanTwice = 0x40000000;  // (block indices are below 2^30)
 
@@ -66,12 +66,15 @@ __device__ __forceinline__ unsigned sequence_flags(const Batch& b, int s, int le
 // sequences.  raise: this CTA reports what is wrong.  A block named by two
 // sequences with tokens leaves both out.  Up to kPlanSort sequences are listed
 // longest first (of equals the lower index first), more in order of their
-// indices.  Some 250 instructions a warp, and the latency of two dependent reads.
-__device__ inline SeqList plan_self(const Batch& b, const Pieces& pieces, PlanSmem& sm, bool raise) {
+// indices.  size: called with the longest one and the sum of their lengths, says
+// how many tokens a piece has.  Some 250 instructions a warp, and the latency of
+// two dependent reads.
+template <typename Size>
+__device__ inline SeqList plan_self(const Batch& b, Pieces pieces, PlanSmem& sm, bool raise, Size size) {
   const int tid = threadIdx.x, threads = blockDim.x, N = b.N;
   if (tid == 0) {
     sm.flags = 0u;
-    sm.n = sm.total = 0;
+    sm.n = sm.total = sm.longest = sm.tokens = 0;
   }
   for (int i = tid; i < kPlanSlots; i += threads) sm.named[i] = -1;
   for (int i = tid; i <= N; i += threads) sm.lo[i] = b.cu[i];
@@ -110,8 +113,13 @@ __device__ inline SeqList plan_self(const Batch& b, const Pieces& pieces, PlanSm
     if (flags && raise) atomicOr(&sm.flags, flags);
     if (flags || blk < 0 || len == 0 || !pieces.of(len)) len = 0;  // nothing to do here
     sm.len[i] = len;
+    if (len > 0) {
+      atomicMax(&sm.longest, len);
+      atomicAdd(&sm.tokens, len);
+    }
   }
   __syncthreads();
+  pieces.tokens = size(sm.longest, sm.tokens);
   if (raise && tid == 0 && sm.flags) atomicOr((unsigned*)&b.work.header()[kErr], sm.flags);
   if (tid < 32) {
     // the list's entries and pieces before each run of kRun sequences
@@ -167,6 +175,10 @@ __device__ inline SeqList plan_self(const Batch& b, const Pieces& pieces, PlanSm
   list.n = sm.n;
   list.total = sm.total;
   return list;
+}
+
+__device__ inline SeqList plan_self(const Batch& b, const Pieces& pieces, PlanSmem& sm, bool raise) {
+  return plan_self(b, pieces, sm, raise, [&](int, int) { return pieces.tokens; });
 }
 
 // plan_kernel's list of the sequences with pieces (the others are in dec(),
