@@ -23,6 +23,7 @@ namespace gdn {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeAhead = 4, kRopeCtas = 2;
 
 struct RopeParams {
   const void *q, *k;
@@ -80,9 +81,9 @@ struct Run8 {
 // kAny: a rotated half that is no multiple of 8 channels (and not interleaved),
 // whose pairs lie in different threads' runs: they meet in shared memory.
 template <typename T, int D, bool kAny>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(RopeParams p) {
   constexpr int kLanes = D / 16;  // threads per head
-  constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;  // heads whose reads are on their way together
+  constexpr int kAhead = sizeof(T) == 2 ? kRopeAhead : 2;  // heads whose reads are on their way together
   // inv_freq / 2 pi as 64-bit fractions of a turn: an angle is the product with
   // the position modulo 2^64, exact for any position (an fp32 angle at position
   // 10^6 would be off by 0.06)
@@ -218,7 +219,7 @@ cudaError_t launch_rope(RopeParams& p, int sms, cudaStream_t s) {
   const int lanes = p.d / 16, heads = p.H + p.Hkv;
   // As many heads for a group as leave every SM 512 threads, and all of them
   // where that is so anyway.
-  const long long want = (long long)sms * 512 / lanes;
+  const long long want = (long long)sms * (kRopeThreads * kRopeCtas) / lanes;
   long long slices = (want + p.T - 1) / p.T;
   if (slices > heads) slices = heads;
   p.per = (int)((heads + slices - 1) / slices);

@@ -55,6 +55,8 @@ __device__ __forceinline__ void store16(T* p, const float* f) {
   *reinterpret_cast<uint4*>(p) = w;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -82,12 +84,29 @@ __device__ __forceinline__ F2 decay2(F2 x) {
   return f2(x0 > kNear ? p0 : a0, x1 > kNear ? p1 : a1);
 }
 
+// softplus(x) = max(x, 0) + log(1 + t), t = e^-|x|, of two values: log(1 + t) / t on
+// [0, 1] is the interpolating polynomial of degree 8 at the Chebyshev points, off by
+// 2e-7 relative (a small softplus, a slow step, keeps its relative precision).
+__device__ __constant__ const float kLogOnePlus[9] = {
+    0.9999999403953552f,  -0.4999944567680359f,  0.3331812024116516f,
+    -0.2483539879322052f, 0.19076880812644958f,  -0.13602247834205627f,
+    0.0775160863995552f,  -0.029074065387248993f, 0.005126102361828089f};
+__device__ __forceinline__ void softplus2(float& a, float& b) {
+  const float ta = ex2(-fabsf(a) * kLog2e), tb = ex2(-fabsf(b) * kLog2e);
+  const F2 t = f2(ta, tb);
+  F2 q = f2(kLogOnePlus[8], kLogOnePlus[8]);
+#pragma unroll
+  for (int i = 7; i >= 0; --i) q = fma2(q, t, f2(kLogOnePlus[i], kLogOnePlus[i]));
+  unf2(fma2(q, t, f2(fmaxf(a, 0.f), fmaxf(b, 0.f))), a, b);
+}
+
 // --- convolution -------------------------------------------------------------
 // Bound by HBM: each input is read once (the K-1 rows before a piece twice, out
 // of L2) and each output written once.  A thread owns 16 bytes of channels and
 // walks the tokens of a piece with the K-1 inputs before in registers.
 constexpr int kConvThreads = 128;
 constexpr int kConvTokens = 32;  // per piece
+constexpr int kConvAhead = 8;    // tokens whose reads are on their way together (1: single tokens only)
 
 struct ConvParams {
   Batch batch;
@@ -102,10 +121,9 @@ struct ConvParams {
   int tx;  // threads across the channels (a power of two); the others take pieces
 };
 
-template <typename T, int K>
+template <typename T, int K, int kAhead>
 __global__ void __launch_bounds__(kConvThreads) sel_conv_kernel(ConvParams p) {
   constexpr int kV = Vec16<T>::kN;
-  constexpr int kAhead = 8;  // tokens whose reads are on their way together
   __shared__ PlanSmem plan;
   pdl_wait_then_release();
   const Batch& b = p.batch;
@@ -117,7 +135,7 @@ __global__ void __launch_bounds__(kConvThreads) sel_conv_kernel(ConvParams p) {
   // (the grid is a multiple of ch_blocks, or all units: a CTA's channels stay the same)
   const int c0 = ((int)(blockIdx.x % ch_blocks) * p.tx + tx) * kV;
   if (c0 >= p.C) return;
-  float w[K][kV], bias[kV];
+  F2 w[K][kV / 2], bias[kV / 2];  // channels in pairs
   {
     const T* wp = static_cast<const T*>(p.w) + (size_t)c0 * K;
     float flat[K * kV];
@@ -128,14 +146,14 @@ __global__ void __launch_bounds__(kConvThreads) sel_conv_kernel(ConvParams p) {
       for (int j = 0; j < kV; ++j) flat[i * kV + j] = v.at(j);
     }
 #pragma unroll
-    for (int j = 0; j < kV; ++j)
+    for (int j = 0; j < kV; j += 2)
 #pragma unroll
-      for (int k = 0; k < K; ++k) w[k][j] = flat[j * K + k];
+      for (int k = 0; k < K; ++k) w[k][j / 2] = f2(flat[j * K + k], flat[(j + 1) * K + k]);
     Vec16<T> v;
     v.w = make_uint4(0, 0, 0, 0);
     if (p.bias) v = load16(static_cast<const T*>(p.bias) + c0);
 #pragma unroll
-    for (int j = 0; j < kV; ++j) bias[j] = v.at(j);
+    for (int j = 0; j < kV; j += 2) bias[j / 2] = f2(v.at(j), v.at(j + 1));
   }
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
     const int piece = (int)(u / ch_blocks) * rows + ty;
@@ -175,23 +193,32 @@ __global__ void __launch_bounds__(kConvThreads) sel_conv_kernel(ConvParams p) {
 #pragma unroll
       for (int j = 0; j < K - 1; ++j) win[j] = load16(x + (size_t)(at - (K - 1) + j) * p.ldx);
     }
+    // kAhead tokens at a time, the next ones on their way
+    Vec16<T> next[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i < n) next[i] = load16(x + (size_t)(at + i) * p.ldx);
     for (int t = 0; t < n; t += kAhead) {
       Vec16<T> in[K - 1 + kAhead];
 #pragma unroll
       for (int j = 0; j < K - 1; ++j) in[j] = win[j];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        if (t + i < n) in[K - 1 + i] = load16(x + (size_t)(at + t + i) * p.ldx);
+      for (int i = 0; i < kAhead; ++i) {
+        in[K - 1 + i] = next[i];
+        if (t + kAhead + i < n) next[i] = load16(x + (size_t)(at + t + kAhead + i) * p.ldx);
+      }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         if (t + i >= n) break;
         float y[kV];
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
-          float acc = bias[j];
+        for (int j = 0; j < kV; j += 2) {
+          F2 acc = bias[j / 2];
 #pragma unroll
-          for (int k = 0; k < K; ++k) acc = fmaf(w[k][j], in[i + k].at(j), acc);
-          y[j] = silu_f32(acc);
+          for (int k = 0; k < K; ++k) acc = fma2(w[k][j / 2], f2(in[i + k].at(j), in[i + k].at(j + 1)), acc);
+          unf2(acc, y[j], y[j + 1]);
+          y[j] = silu_f32(y[j]);
+          y[j + 1] = silu_f32(y[j + 1]);
         }
         store16(out + (size_t)(at + t + i) * p.ldo, y);
       }
@@ -218,17 +245,16 @@ struct ScanParams {
   float *seg_states, *seg_sums;
 };
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-// Single tokens: each state is read once and written once, bound by HBM.  A
-// thread has four entries of a channel's state; a CTA keeps its channels and
-// walks the sequences, kSeqs of them at a time on their way.
+// Single tokens: each state is read once and written once.  A thread has eight
+// entries of a channel's state (with four, what is done once per channel, softplus
+// above all, took most of the instructions: 52 us for 256 sequences x 4,096
+// channels, now 30); a CTA keeps its channels and walks the sequences.
 constexpr int kStepThreads = 256;
+constexpr int kStepCtas = 4;  // per SM: reads in flight
 
 template <typename T, int N>
-__global__ void __launch_bounds__(kStepThreads, 3) sel_step_kernel(ScanParams p) {
-  constexpr int kLanes = N / 4;  // threads per channel
-  constexpr int kSeqs = 4;
+__global__ void __launch_bounds__(kStepThreads, kStepCtas) sel_step_kernel(ScanParams p) {
+  constexpr int kLanes = N / 8;  // threads per channel
   __shared__ PlanSmem plan;
   pdl_wait_then_release();
   const Batch& b = p.batch;
@@ -241,67 +267,62 @@ __global__ void __launch_bounds__(kStepThreads, 3) sel_step_kernel(ScanParams p)
   }
   const int c = (blockIdx.x * kStepThreads + threadIdx.x) / kLanes, g = threadIdx.x % kLanes;
   const bool live = c < p.channels;
-  const size_t at = (size_t)(live ? c : 0) * N + g * 4;
-  const float4 al = *reinterpret_cast<const float4*>(p.A_log + at);
-  const float A[4] = {-expf(al.x) * kLog2e, -expf(al.y) * kLog2e, -expf(al.z) * kLog2e,
-                      -expf(al.w) * kLog2e};
+  const size_t at = (size_t)(live ? c : 0) * N + g * 8;
+  F2 A[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 al = *reinterpret_cast<const float2*>(p.A_log + at + 2 * i);
+    A[i] = f2(-expf(al.x) * kLog2e, -expf(al.y) * kLog2e);
+  }
   const float bias = p.dt_bias && live ? p.dt_bias[c] : 0.f, skip = p.D && live ? p.D[c] : 0.f;
   const int* lo = b.listed ? b.cu : plan.lo;
   const int* blocks = b.listed ? b.blk : plan.blk;
-  auto four = [](const T* q, float* f) {
+  // eight elements, in pairs
+  auto eight = [](const T* q, F2* f) {
     if constexpr (sizeof(T) == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(q);
-      f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+      const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(q), w = *reinterpret_cast<const ulonglong2*>(q + 4);
+      f[0] = v.x; f[1] = v.y; f[2] = w.x; f[3] = w.y;
     } else {
-      const uint2 v = *reinterpret_cast<const uint2*>(q);
-      f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
-      f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
+      const Vec16<T> v = load16(q);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = f2(v.at(2 * i), v.at(2 * i + 1));
     }
   };
-  for (int i0 = blockIdx.y * kSeqs; i0 < list.n; i0 += gridDim.y * kSeqs) {
-    const int m = min(kSeqs, list.n - i0);
-    float4 h[kSeqs];
-    float* st[kSeqs];
-    float B[kSeqs][4], C[kSeqs][4], u[kSeqs], dt[kSeqs], z[kSeqs];
-    int row[kSeqs];
-    bool past[kSeqs];
+  for (int i0 = blockIdx.y; i0 < list.n; i0 += gridDim.y) {
+    const int s = list.items[i0];
+    const size_t row = lo[s];
+    // (read whether it counts or not: no wait for has_past)
+    float* st = reinterpret_cast<float*>(p.layer_base + (size_t)blocks[s] * p.stride + p.ssm_off) + at;
+    const ulonglong2 h01 = *reinterpret_cast<const ulonglong2*>(st), h23 = *reinterpret_cast<const ulonglong2*>(st + 4);
+    F2 h[4] = {h01.x, h01.y, h23.x, h23.y}, B[4], C[4];
+    const bool past = b.has_past[s];
+    const int cc = live ? c : 0;
+    const float u = to_f32(static_cast<const T*>(p.u)[row * p.ldu + cc]);
+    float d = to_f32(static_cast<const T*>(p.dt)[row * p.lddt + cc]) + bias;
+    const float z = p.z ? to_f32(static_cast<const T*>(p.z)[row * p.ldz + cc]) : 0.f;
+    eight(static_cast<const T*>(p.B) + row * p.ldb + g * 8, B);
+    eight(static_cast<const T*>(p.C) + row * p.ldc + g * 8, C);
+    d = softplus_f32(d);
+    const F2 dd = f2(d, d), du = f2(d * u, d * u);
+    F2 part = 0ull;
 #pragma unroll
-    for (int i = 0; i < kSeqs; ++i) {
-      if (i >= m || !live) continue;
-      const int s = list.items[i0 + i];
-      row[i] = lo[s];
-      // (read whether it counts or not: no wait for has_past)
-      st[i] = reinterpret_cast<float*>(p.layer_base + (size_t)blocks[s] * p.stride + p.ssm_off) + at;
-      h[i] = *reinterpret_cast<const float4*>(st[i]);
-      past[i] = b.has_past[s];
-      const size_t r = row[i];
-      u[i] = to_f32(static_cast<const T*>(p.u)[r * p.ldu + c]);
-      dt[i] = to_f32(static_cast<const T*>(p.dt)[r * p.lddt + c]);
-      z[i] = p.z ? to_f32(static_cast<const T*>(p.z)[r * p.ldz + c]) : 0.f;
-      four(static_cast<const T*>(p.B) + r * p.ldb + g * 4, B[i]);
-      four(static_cast<const T*>(p.C) + r * p.ldc + g * 4, C[i]);
+    for (int i = 0; i < 4; ++i) {
+      h[i] = fma2(past ? h[i] : 0ull, decay2(mul2(dd, A[i])), mul2(du, B[i]));
+      part = fma2(h[i], C[i], part);
     }
+    if (live) {
+      *reinterpret_cast<ulonglong2*>(st) = make_ulonglong2(h[0], h[1]);
+      *reinterpret_cast<ulonglong2*>(st + 4) = make_ulonglong2(h[2], h[3]);
+    }
+    float y, odd;
+    unf2(part, y, odd);
+    y += odd;
 #pragma unroll
-    for (int i = 0; i < kSeqs; ++i) {
-      if (i >= m) continue;  // (the same for the whole CTA)
-      float y = 0.f;
-      if (live) {
-        if (!past[i]) h[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float d = softplus_f32(dt[i] + bias), du = d * u[i];
-        h[i].x = fmaf(h[i].x, decay2(d * A[0]), du * B[i][0]);
-        h[i].y = fmaf(h[i].y, decay2(d * A[1]), du * B[i][1]);
-        h[i].z = fmaf(h[i].z, decay2(d * A[2]), du * B[i][2]);
-        h[i].w = fmaf(h[i].w, decay2(d * A[3]), du * B[i][3]);
-        *reinterpret_cast<float4*>(st[i]) = h[i];
-        y = fmaf(h[i].x, C[i][0], fmaf(h[i].y, C[i][1], fmaf(h[i].z, C[i][2], h[i].w * C[i][3])));
-      }
-#pragma unroll
-      for (int w = 1; w < kLanes; w <<= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
-      if (live && g == 0) {
-        y = fmaf(skip, u[i], y);
-        if (p.z) y *= silu_f32(z[i]);
-        static_cast<T*>(p.y)[(size_t)row[i] * p.ldy + c] = from_f32<T>(y);
-      }
+    for (int w = 1; w < kLanes; w <<= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
+    if (live && g == 0) {
+      y = fmaf(skip, u, y);
+      if (p.z) y *= silu_f32(z);
+      static_cast<T*>(p.y)[row * p.ldy + c] = from_f32<T>(y);
     }
   }
 }
@@ -324,7 +345,7 @@ __device__ __forceinline__ void cp_async_wait() {
 // issue slots: per state and token two multiplications, the exponential with its
 // series and its choice, two multiply-adds, in packed pairs 14 instructions for
 // two states, and some 50 per token and channel for softplus, SiLU and the
-// tile's way through shared memory.  15,843 tokens x 4,096 channels: TIME_SCAN.
+// tile's way through shared memory.  15,843 tokens x 4,096 channels: 593 us.
 //
 // Long sequences of few channels are cut into segments: a first pass (kState)
 // computes each segment's own state (from zeros) and its steps' sum, a small
@@ -332,7 +353,8 @@ __device__ __forceinline__ void cp_async_wait() {
 // output pass runs all segments side by side.  The work is 1.7 times as much, so
 // that is done where otherwise too few CTAs run or one sequence is longer than an
 // SM's share of all (segment_tokens; every kernel finds the same from the lengths).
-constexpr int kScanThreads = 128;
+constexpr int kScanThreads = 256;
+constexpr int kTileTokens = 32;
 constexpr int kSegmentBytes = 32 << 20;  // room for states between segments
 constexpr int kSegmentsMax = 8192;       // (and for their steps' sums)
 
@@ -345,7 +367,7 @@ __host__ __device__ inline int segment_tokens(int longest, long long tokens, int
                                               int n, int sms) {
   const long long share = tokens * ch_blocks / sms;
   const long long whole = 2ll * longest > share ? 2ll * longest : share;
-  long long seg = (share / 4 + 31) / 32 * 32;  // four of them to an SM
+  long long seg = (share / 8 + 31) / 32 * 32;  // eight of them to an SM
   if (seg < 64) seg = 64;
   const long long split = share * 7 / 4 + 2 * seg + 300;
   if (split >= whole || tokens / seg + n > slots) return 0x7fffffff;
@@ -355,15 +377,19 @@ __host__ __device__ inline int segment_tokens(int longest, long long tokens, int
 template <typename T, int N, int kG, bool kState>
 struct ScanSmem {
   static constexpr int kCB = kScanThreads / kG;
-  static constexpr int kTT = 32;
+  static constexpr int kTT = kTileTokens;
   static constexpr int kPad = kG > 1 ? 32 / kG : 0;  // the lanes of a channel write rows of y: apart by banks
   static constexpr int kOut = kState ? 1 : kTT;
   T u[2][kTT][kCB], dt[2][kTT][kCB], z[2][kOut][kCB];
   T B[2][kTT][N], C[2][kOut][N];
-  alignas(16) float2 step[kTT][kCB];  // dt and dt u
   alignas(16) float Bf[kTT][N], Cf[kOut][N];
-  float y[kOut][kCB + kPad];
-  PlanSmem plan;
+  union {
+    struct {
+      alignas(16) float2 step[kTT][kCB];  // dt and dt u
+      float y[kOut][kCB + kPad];
+    };
+    PlanSmem plan;  // (before the first tile's)
+  };
 };
 
 template <typename T, int N, int kG, bool kState>
@@ -397,6 +423,7 @@ __global__ void __launch_bounds__(kScanThreads) sel_scan_kernel(ScanParams p) {
   const int tid = threadIdx.x, c = tid / kG, g = tid % kG;
   const bool live = cb + c < p.channels;
   const int wide = min(kCB, p.channels - cb);
+  __syncthreads();  // the plan is read
 
   auto stage = [&](int t0, int buf) {
     const int n = min(kTT, len - t0);
@@ -466,10 +493,12 @@ __global__ void __launch_bounds__(kScanThreads) sel_scan_kernel(ScanParams p) {
       float d[2], u[2];
       two(&sm.dt[buf][t][xc], d[0], d[1]);
       two(&sm.u[buf][t][xc], u[0], u[1]);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        d[k] = softplus_f32(d[k] + bias[k]);
-        if (kState) sum[k] += d[k];
+      d[0] += bias[0];
+      d[1] += bias[1];
+      softplus2(d[0], d[1]);
+      if (kState) {
+        sum[0] += d[0];
+        sum[1] += d[1];
       }
       *reinterpret_cast<float4*>(&sm.step[t][xc]) = make_float4(d[0], d[0] * u[0], d[1], d[1] * u[1]);
     }
@@ -482,8 +511,12 @@ __global__ void __launch_bounds__(kScanThreads) sel_scan_kernel(ScanParams p) {
       const float2 d = sm.step[t][c];
       const F2 dd = f2(d.x, d.x), du = f2(d.y, d.y);
       [[maybe_unused]] F2 part = 0ull;
+      if constexpr (kNS == 2) {
+        h[0] = fma2(h[0], decay2(mul2(dd, A[0])), mul2(du, *reinterpret_cast<const F2*>(&sm.Bf[t][g * 2])));
+        if constexpr (!kState) part = mul2(h[0], *reinterpret_cast<const F2*>(&sm.Cf[t][g * 2]));
+      }
 #pragma unroll
-      for (int i = 0; i < kNS / 2; i += 2) {
+      for (int i = 0; i + 2 <= kNS / 2; i += 2) {
         const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(&sm.Bf[t][g * kNS + 2 * i]);
         h[i] = fma2(h[i], decay2(mul2(dd, A[i])), mul2(du, b2.x));
         h[i + 1] = fma2(h[i + 1], decay2(mul2(dd, A[i + 1])), mul2(du, b2.y));
@@ -493,9 +526,9 @@ __global__ void __launch_bounds__(kScanThreads) sel_scan_kernel(ScanParams p) {
           part = fma2(h[i + 1], c2.y, part);
         }
       }
-      float y0 = 0.f, y1 = 0.f;
-      if constexpr (!kState) unf2(part, y0, y1);
-      return y0 + y1;
+      float even = 0.f, odd = 0.f;
+      if constexpr (!kState) unf2(part, even, odd);
+      return even + odd;
     };
     // the sums over a channel's lanes: lane k ends up with token k's
     auto across = [&](float* part) {
@@ -637,7 +670,7 @@ cudaError_t launch_scan(ScanParams p, int max_items, cudaStream_t s) {
       segment_tokens(longest, b.T, ch_blocks, 0x7fffffff, b.N, p.sms) == 0x7fffffff) {
     p.slots = 0;
   } else {
-    pieces += 4ll * p.sms / ch_blocks + 1;  // (segments are a quarter of an SM's share at least)
+    pieces += 8ll * p.sms / ch_blocks + 1;  // (segments are an eighth of an SM's share at least)
     cudaError_t e = launch_scan_pass<T, N, kG, true>(p, pieces, s);
     if (e == cudaSuccess) {
       p.report = 0;
@@ -650,10 +683,9 @@ cudaError_t launch_scan(ScanParams p, int max_items, cudaStream_t s) {
 
 template <typename T, int N>
 cudaError_t launch_step(const ScanParams& p, int max_items, int sms, cudaStream_t s) {
-  const int per = kStepThreads / (N / 4), x = (p.channels + per - 1) / per;
-  int y = (3 * sms + x - 1) / x;  // about three CTAs per SM
-  const int most = (max_items + 3) / 4;
-  if (y > most) y = most;
+  const int per = kStepThreads / (N / 8), x = (p.channels + per - 1) / per;
+  int y = (kStepCtas * sms + x - 1) / x;
+  if (y > max_items) y = max_items;
   return launch_pdl(sel_step_kernel<T, N>, dim3(x, y), dim3(kStepThreads), 0, s, p);
 }
 
@@ -664,7 +696,12 @@ cudaError_t launch_scan_of(const ScanParams& p, int n, int max_long, int max_one
   cudaError_t e = cudaSuccess;
   q.report = 1;
   if (max_long > 0) {
-    e = n == 16   ? launch_scan<T, 16, 4>(q, max_long, s)
+    // (whole sequences with two states to a thread, segments with four: 593 and 645 us
+    // for 15,843 tokens x 4,096 channels, 922 and 806 for 32,768 x 2,048)
+    const Batch& b = q.batch;
+    const int longest = b.hint > 0 && b.hint < b.T ? b.hint : b.T;
+    const bool whole = b.listed || segment_tokens(longest, b.T, (q.channels + 63) / 64, q.slots, b.N, sms) == 0x7fffffff;
+    e = n == 16   ? whole ? launch_scan<T, 16, 8>(q, max_long, s) : launch_scan<T, 16, 4>(q, max_long, s)
         : n == 32 ? launch_scan<T, 32, 4>(q, max_long, s)
                   : launch_scan<T, 64, 8>(q, max_long, s);
     q.report = 0;
@@ -678,7 +715,11 @@ cudaError_t launch_scan_of(const ScanParams& p, int n, int max_long, int max_one
 
 template <typename T>
 cudaError_t launch_conv(const ConvParams& p, int K, unsigned ctas, cudaStream_t s) {
-  auto kern = K == 2 ? sel_conv_kernel<T, 2> : K == 3 ? sel_conv_kernel<T, 3> : sel_conv_kernel<T, 4>;
+  auto kern = p.batch.hint == 1
+                  ? K == 2 ? sel_conv_kernel<T, 2, 1> : K == 3 ? sel_conv_kernel<T, 3, 1> : sel_conv_kernel<T, 4, 1>
+              : K == 2 ? sel_conv_kernel<T, 2, kConvAhead>
+              : K == 3 ? sel_conv_kernel<T, 3, kConvAhead>
+                       : sel_conv_kernel<T, 4, kConvAhead>;
   return launch_pdl(kern, dim3(ctas), dim3(kConvThreads), 0, s, p);
 }
 
