@@ -185,6 +185,10 @@ def _index(t, device: Optional[int] = None) -> Optional[int]:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+# (torch.cuda.current_device() checks that CUDA is initialised first)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _stream(stream, device: Optional[int] = None) -> Optional[int]:
     """A stream's handle; None: the current one, of the current device or the
     one given."""
@@ -583,7 +587,7 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, q_out=
         raise ValueError("q and k are [T][heads][d]")
     T, H, d = q.shape
     dtype, dev = q.dtype, q.get_device()
-    if not q.is_cuda or dev != torch.cuda.current_device():
+    if dev < 0 or dev != _current_device():
         raise ValueError(f"q is on {q.device}, not on the current CUDA device")
     q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
     if k is None and k_out is not None:

@@ -43,8 +43,9 @@ constexpr int kPlanSort = 32;              // lists of up to this many are put i
 struct PlanSmem {
   int32_t lo[kSelfPlan + 1], blk[kSelfPlan], len[kSelfPlan], items[kSelfPlan], first[kSelfPlan + 1];
   int32_t named[kPlanSlots];  // a block index, kPlanTwice with it where two sequences name it
+  int32_t runs[kSelfPlan / 32], run_pieces[kSelfPlan / 32];
   unsigned flags;
-  int n, total, longest, tokens;  // (longest, tokens: of the sequences with pieces)
+  int longest, tokens;  // (longest, tokens: of the sequences with pieces)
 };
 constexpr int kPlanTwice = 0x40000000;  // (block indices are below 2^30)
 
@@ -74,7 +75,7 @@ __device__ inline SeqList plan_self(const Batch& b, Pieces pieces, PlanSmem& sm,
   const int tid = threadIdx.x, threads = blockDim.x, N = b.N;
   if (tid == 0) {
     sm.flags = 0u;
-    sm.n = sm.total = sm.longest = sm.tokens = 0;
+    sm.longest = sm.tokens = 0;
   }
   for (int i = tid; i < kPlanSlots; i += threads) sm.named[i] = -1;
   for (int i = tid; i <= N; i += threads) sm.lo[i] = b.cu[i];
@@ -121,40 +122,42 @@ __device__ inline SeqList plan_self(const Batch& b, Pieces pieces, PlanSmem& sm,
   __syncthreads();
   pieces.tokens = size(sm.longest, sm.tokens);
   if (raise && tid == 0 && sm.flags) atomicOr((unsigned*)&b.work.header()[kErr], sm.flags);
-  if (tid < 32) {
-    // the list's entries and pieces before each run of kRun sequences
-    constexpr int kRun = kSelfPlan / 32;
-    int n = 0, sum = 0;
-    for (int i = tid * kRun; i < min(N, (tid + 1) * kRun); ++i) {
-      const int len = sm.len[i];
-      n += len > 0;
-      sum += len > 0 ? pieces.of(len) : 0;
+  // the entries and pieces before each run of 32 sequences, then before each sequence
+  const int lane = tid & 31, warps = threads >> 5;
+  for (int run = tid >> 5; run * 32 < N; run += warps) {
+    const int i = run * 32 + lane, len = i < N ? sm.len[i] : 0, count = len > 0 ? pieces.of(len) : 0;
+    const int n = __popc(__ballot_sync(0xffffffffu, len > 0));
+    const int sum = __reduce_add_sync(0xffffffffu, count);
+    if (lane == 0) {
+      sm.runs[run] = n;
+      sm.run_pieces[run] = sum;
     }
-    int n_upto = n, sum_upto = sum;
+  }
+  __syncthreads();
+  int all = 0, all_pieces = 0;
+  for (int run = 0; run * 32 < N; ++run) {
+    if (run % warps == tid >> 5) {
+      const int i = run * 32 + lane, len = i < N ? sm.len[i] : 0, count = len > 0 ? pieces.of(len) : 0;
+      const unsigned mask = __ballot_sync(0xffffffffu, len > 0);
+      int upto = count;
 #pragma unroll
-    for (int w = 1; w < 32; w <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, n_upto, w), y = __shfl_up_sync(0xffffffffu, sum_upto, w);
-      if (tid >= w) {
-        n_upto += x;
-        sum_upto += y;
+      for (int w = 1; w < 32; w <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, w);
+        if (lane >= w) upto += x;
+      }
+      if (len > 0) {
+        const int at = all + __popc(mask & ((1u << lane) - 1u));
+        sm.items[at] = i;
+        sm.first[at] = all_pieces + upto - count;
       }
     }
-    const int all = __shfl_sync(0xffffffffu, n_upto, 31);
-    int at = n_upto - n, before = sum_upto - sum;
-    for (int i = tid * kRun; i < min(N, (tid + 1) * kRun); ++i) {
-      const int len = sm.len[i];
-      if (len == 0) continue;
-      sm.items[at] = i;
-      sm.first[at++] = before;
-      before += pieces.of(len);
-    }
-    if (tid == 31) {
-      sm.first[all] = sum_upto;
-      sm.n = all;
-      sm.total = sum_upto;
-    }
-    __syncwarp();
-    if (all <= kPlanSort && all > 1) {
+    all += sm.runs[run];
+    all_pieces += sm.run_pieces[run];
+  }
+  if (tid == 0) sm.first[all] = all_pieces;
+  __syncthreads();
+  if (all <= kPlanSort && all > 1) {
+    if (tid < 32) {
       const int mine = tid < all ? sm.items[tid] : -1, len = tid < all ? sm.len[mine] : 0;
       const int count = tid < all ? pieces.of(len) : 0;
       int rank = 0, ahead = 0;
@@ -170,10 +173,10 @@ __device__ inline SeqList plan_self(const Batch& b, Pieces pieces, PlanSmem& sm,
         sm.first[rank] = ahead;
       }
     }
+    __syncthreads();
   }
-  __syncthreads();
-  list.n = sm.n;
-  list.total = sm.total;
+  list.n = all;
+  list.total = all_pieces;
   return list;
 }
 

@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include <new>
+#include <type_traits>
 
 #include "gdn_cta.cuh"
 #include "gdn_pool.cuh"
@@ -33,7 +34,8 @@ constexpr int kRows = 32, kKeys = 32;
 template <int D>
 struct RowSmem {
   float q[kRows][D + 4], k[kKeys][D + 4], v[kKeys][D + 4];
-  float p[kRows][kKeys + 1];  // the weights; -1: masked
+  float p[kKeys][kRows + 4];  // the weights; -1: masked
+  const void *from_k[kKeys], *from_v[kKeys];  // where a tile's rows lie
   float top[kRows], sum[kRows], shrink[kRows];
   PlanSmem plan;
 };
@@ -50,13 +52,23 @@ __device__ void rows_of(const WinParams& p, RowSmem<D>& sm, int s, int t0, int t
   const T* ring_k = ring_of<T>(p, blk, 0, hk);
   const T* ring_v = ring_of<T>(p, blk, 1, hk);
   auto head = [&](int r) { return hk * p.group + sub * kRows + r % per; };
-  for (int i = tid; i < kRows * D; i += kRowThreads) {
-    const int r = i / D, c = i % D;
-    float x = 0.f;
+  // four channels of a row
+  auto four = [](const T* p4) {
+    if constexpr (sizeof(T) == 4) {
+      return *reinterpret_cast<const float4*>(p4);
+    } else {
+      const uint2 w = *reinterpret_cast<const uint2*>(p4);
+      return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                         __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+    }
+  };
+  constexpr int kVecs = D / 4;
+  for (int i = tid; i < kRows * kVecs; i += kRowThreads) {
+    const int r = i / kVecs, c = i % kVecs * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < rows)
-      x = to_f32(static_cast<const T*>(p.q)[(size_t)(row0 + t0 + r / per) * p.ldq +
-                                            (size_t)head(r) * D + c]);
-    sm.q[r][c] = x;
+      x = four(static_cast<const T*>(p.q) + (size_t)(row0 + t0 + r / per) * p.ldq + (size_t)head(r) * D + c);
+    *reinterpret_cast<float4*>(&sm.q[r][c]) = x;
   }
   if (tid < kRows) {
     sm.top[tid] = -INFINITY;
@@ -66,8 +78,9 @@ __device__ void rows_of(const WinParams& p, RowSmem<D>& sm, int s, int t0, int t
   const int p0 = past + t0, p1 = p0 + tokens;
   const int lo = max(0, p0 - p.window + 1), before = min(p.sinks, lo), n_keys = before + p1 - lo;
   auto position = [&](int i) { return i < before ? i : lo + i - before; };
-  constexpr int kCols = D / 16;  // each thread's part of the output: 4 rows, D/16 columns
-  const int or0 = tid / 16 * 4, oc = tid % 16;
+  // each thread's part of the output: 4 rows, D/16 columns side by side
+  constexpr int kCols = D / 16;
+  const int or0 = tid / 16 * 4, oc = tid % 16 * kCols;
   float acc[4][kCols];
 #pragma unroll
   for (int r = 0; r < 4; ++r)
@@ -77,21 +90,30 @@ __device__ void rows_of(const WinParams& p, RowSmem<D>& sm, int s, int t0, int t
   for (int k0 = 0; k0 < n_keys; k0 += kKeys) {
     const int n = min(kKeys, n_keys - k0);
     __syncthreads();  // the last tile is read
-    for (int i = tid; i < n * D; i += kRowThreads) {
-      const int r = i / D, c = i % D, j = position(k0 + r);
-      const T *pk, *pv;
+    if (tid < n) {
+      const int j = position(k0 + tid);
       if (j < past) {
-        const size_t at = (size_t)slot_of(p, j) * D + c;
-        pk = ring_k + at;
-        pv = ring_v + at;
+        const size_t at = (size_t)slot_of(p, j) * D;
+        sm.from_k[tid] = ring_k + at;
+        sm.from_v[tid] = ring_v + at;
       } else {
         const size_t row = row0 + (j - past);
-        pk = static_cast<const T*>(p.k) + row * p.ldk + (size_t)hk * D + c;
-        pv = static_cast<const T*>(p.v) + row * p.ldv + (size_t)hk * D + c;
+        sm.from_k[tid] = static_cast<const T*>(p.k) + row * p.ldk + (size_t)hk * D;
+        sm.from_v[tid] = static_cast<const T*>(p.v) + row * p.ldv + (size_t)hk * D;
       }
-      sm.k[r][c] = to_f32(*pk);
-      sm.v[r][c] = to_f32(*pv);
     }
+    __syncthreads();
+#pragma unroll 4
+    for (int i = tid; i < n * kVecs; i += kRowThreads) {
+      const int r = i / kVecs, c = i % kVecs * 4;
+      const float4 x = four(static_cast<const T*>(sm.from_k[r]) + c), y = four(static_cast<const T*>(sm.from_v[r]) + c);
+      *reinterpret_cast<float4*>(&sm.k[r][c]) = x;
+      *reinterpret_cast<float4*>(&sm.v[r][c]) = y;
+    }
+    // whether every row sees every key of the tile
+    const int first = position(k0), last = position(k0 + n - 1);
+    const bool all = rows == kRows && n == kKeys && last <= p0 &&
+                     (first > p1 - 1 - p.window || last < p.sinks);
     __syncthreads();
     // scores: a warp has 8 rows, a lane one key
     const int j = lane < n ? position(k0 + lane) : 0;
@@ -112,7 +134,7 @@ __device__ void rows_of(const WinParams& p, RowSmem<D>& sm, int s, int t0, int t
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const int row = warp * 8 + r;
-      const bool seen = row < rows && lane < n && sees(p, p0 + row / per, j);
+      const bool seen = all || (row < rows && lane < n && sees(p, p0 + row / per, j));
       const float x = seen ? sc[r] * to2 : -INFINITY;
       float m = x;
 #pragma unroll
@@ -124,7 +146,7 @@ __device__ void rows_of(const WinParams& p, RowSmem<D>& sm, int s, int t0, int t
       float sum = w;
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      sm.p[row][lane] = seen ? w : -1.f;
+      sm.p[lane][row] = seen ? w : -1.f;
       __syncwarp();
       if (lane == 0) {
         const float shrink = exp2f(was - base);
@@ -140,19 +162,28 @@ __device__ void rows_of(const WinParams& p, RowSmem<D>& sm, int s, int t0, int t
 #pragma unroll
       for (int c = 0; c < kCols; ++c) acc[r][c] *= f;
     }
-    for (int i = 0; i < n; ++i) {
-      float w[4];
+    auto values = [&](auto all_c) {
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float4 w4 = *reinterpret_cast<const float4*>(&sm.p[i][or0]);
+        const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+        float vv[kCols];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) w[r] = sm.p[or0 + r][i];
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        const float vv = sm.v[i][oc + 16 * c];
+        for (int c = 0; c < kCols; c += 2) {
+          const float2 v2 = *reinterpret_cast<const float2*>(&sm.v[i][oc + c]);
+          vv[c] = v2.x;
+          vv[c + 1] = v2.y;
+        }
         // (a masked value is not touched: it may be infinite or NaN)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (!(w[r] < 0.f)) acc[r][c] = fmaf(w[r], vv, acc[r][c]);
+#pragma unroll
+          for (int c = 0; c < kCols; ++c)
+            if (decltype(all_c)::value || !(w[r] < 0.f)) acc[r][c] = fmaf(w[r], vv[c], acc[r][c]);
       }
-    }
+    };
+    if (all) values(std::true_type());
+    else values(std::false_type());
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
@@ -161,7 +192,7 @@ __device__ void rows_of(const WinParams& p, RowSmem<D>& sm, int s, int t0, int t
     const float inv = 1.f / sm.sum[row];
     T* o = static_cast<T*>(p.out) + (size_t)(row0 + t0 + row / per) * p.ldo + (size_t)head(row) * D;
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) o[oc + 16 * c] = from_f32<T>(acc[r][c] * inv);
+    for (int c = 0; c < kCols; ++c) o[oc + c] = from_f32<T>(acc[r][c] * inv);
   }
 }
 

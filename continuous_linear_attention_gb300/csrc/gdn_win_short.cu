@@ -504,10 +504,12 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int late, int32_t* arriv
       for (int i = tid; i < rows * (D / 4); i += 32 * kWarps) {
         const int row = i / (D / 4), c = i % (D / 4) * 4;
         float m = -INFINITY, l = 0.f;
+#pragma unroll 8
         for (int k = 0; k < parts; ++k)
           m = fmaxf(m, __ldcg(all + k * part_floats<D>() + (size_t)kMaxRows * D + 2 * row));
         const float base = m == -INFINITY ? 0.f : m;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
         for (int k = 0; k < parts; ++k) {
           const float* from = all + k * part_floats<D>();
           const float f = ex2(__ldcg(from + (size_t)kMaxRows * D + 2 * row) - base);
