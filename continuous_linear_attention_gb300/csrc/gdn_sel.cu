@@ -155,19 +155,21 @@ __global__ void __launch_bounds__(kConvThreads) sel_conv_kernel(ConvParams p) {
 #pragma unroll
     for (int j = 0; j < kV; j += 2) bias[j / 2] = f2(v.at(j), v.at(j + 1));
   }
+  const int* lo = b.listed ? b.cu : plan.lo;
+  const int* blocks = b.listed ? b.blk : plan.blk;
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
     const int piece = (int)(u / ch_blocks) * rows + ty;
     if (piece >= list.total) continue;
     const int e = entry_of(list, piece), s = list.items[e];
     const int at = (piece - list.first[e]) * kConvTokens;
-    const int row0 = b.cu[s], len = b.cu[s + 1] - row0, n = min(kConvTokens, len - at);
+    const int row0 = lo[s], len = lo[s + 1] - row0, n = min(kConvTokens, len - at);
     const T* x = static_cast<const T*>(p.x) + (size_t)row0 * p.ldx + c0;
     T* out = static_cast<T*>(p.out) + (size_t)row0 * p.ldo + c0;
     Vec16<T> win[K - 1];
     if (at == 0) {
       // the state, and (only this thread reads it) its new rows: the last K-1
       // inputs, former ones among them where the sequence is short
-      T* st = reinterpret_cast<T*>(p.layer_base + (size_t)b.blk[s] * p.stride) + c0;
+      T* st = reinterpret_cast<T*>(p.layer_base + (size_t)blocks[s] * p.stride) + c0;
       const bool past = b.has_past[s];
 #pragma unroll
       for (int j = 0; j < K - 1; ++j) {
@@ -404,7 +406,7 @@ __global__ void __launch_bounds__(kScanThreads) sel_scan_kernel(ScanParams p) {
   int seg_tokens = 0x7fffffff;
   const SeqList list =
       b.listed ? listed_long(b)
-               : plan_self(b, Pieces{2, 0x7fffffff, 0x7fffffff}, sm.plan, p.report && blockIdx.x == 0,
+               : plan_self<true>(b, Pieces{2, 0x7fffffff, 0x7fffffff}, sm.plan, p.report && blockIdx.x == 0,
                            [&](int longest, int tokens) {
                              if (p.slots > 0)
                                seg_tokens = segment_tokens(longest, tokens, ch_blocks, p.slots, b.N, p.sms);
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(256) sel_segments_kernel(ScanParams p, int n_s
   pdl_wait_then_release();
   const Batch& b = p.batch;
   int seg_tokens = 0x7fffffff;
-  const SeqList list = plan_self(b, Pieces{2, 0x7fffffff, 0x7fffffff}, plan, false, [&](int longest, int tokens) {
+  const SeqList list = plan_self<true>(b, Pieces{2, 0x7fffffff, 0x7fffffff}, plan, false, [&](int longest, int tokens) {
     return seg_tokens = segment_tokens(longest, tokens, (p.channels + kCB - 1) / kCB, p.slots, b.N, p.sms);
   });
   if (seg_tokens == 0x7fffffff) return;

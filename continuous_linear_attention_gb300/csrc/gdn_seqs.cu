@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Batch b, Pieces piec
     if (i < N) {
       len = b.cu[i + 1] - b.cu[i];
       const int blk = b.blk[i];
-      unsigned flags = sequence_flags(b, i, len, blk);
+      unsigned flags = sequence_flags(b, b.past_len ? b.past_len[i] : 0, len, blk);
       if (len > 0 && blk > 0 && blk < nb && atomicAdd(&uses[blk], 0) > 1) flags = GDN_FLAG_DUPLICATE;
       if (flags) atomicOr(&s_flags, flags);
       if (flags || blk < 0) len = 0;

@@ -16,6 +16,7 @@
 #include <type_traits>
 
 #include "gdn_cta.cuh"
+#include "gdn_lin.cuh"
 #include "gdn_pool.cuh"
 #include "gdn_win.cuh"
 
@@ -81,11 +82,11 @@ __device__ void rows_of(const WinParams& p, RowSmem<D>& sm, int s, int t0, int t
   // each thread's part of the output: 4 rows, D/16 columns side by side
   constexpr int kCols = D / 16;
   const int or0 = tid / 16 * 4, oc = tid % 16 * kCols;
-  float acc[4][kCols];
+  F2 acc[4][kCols / 2];
 #pragma unroll
   for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) acc[r][c] = 0.f;
+    for (int c = 0; c < kCols / 2; ++c) acc[r][c] = 0ull;
   const float to2 = p.scale * kLog2e;
   for (int k0 = 0; k0 < n_keys; k0 += kKeys) {
     const int n = min(kKeys, n_keys - k0);
@@ -118,17 +119,24 @@ __device__ void rows_of(const WinParams& p, RowSmem<D>& sm, int s, int t0, int t
     // scores: a warp has 8 rows, a lane one key
     const int j = lane < n ? position(k0 + lane) : 0;
     float sc[8];
+    {
+      F2 even[8];  // (sums over even and odd channels)
 #pragma unroll
-    for (int r = 0; r < 8; ++r) sc[r] = 0.f;
-    if (lane < n) {
+      for (int r = 0; r < 8; ++r) even[r] = 0ull;
 #pragma unroll 4
-      for (int c = 0; c < D; c += 4) {
-        const float4 kk = *reinterpret_cast<const float4*>(&sm.k[lane][c]);
+      for (int c = 0; c < D; c += 4) {  // (lanes behind the last key: anything)
+        const ulonglong2 kk = *reinterpret_cast<const ulonglong2*>(&sm.k[lane][c]);
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-          const float4 qq = *reinterpret_cast<const float4*>(&sm.q[warp * 8 + r][c]);
-          sc[r] = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, fmaf(qq.z, kk.z, fmaf(qq.w, kk.w, sc[r]))));
+          const ulonglong2 qq = *reinterpret_cast<const ulonglong2*>(&sm.q[warp * 8 + r][c]);
+          even[r] = fma2(qq.x, kk.x, fma2(qq.y, kk.y, even[r]));
         }
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        float x, y;
+        unf2(even[r], x, y);
+        sc[r] = x + y;
       }
     }
 #pragma unroll
@@ -160,26 +168,22 @@ __device__ void rows_of(const WinParams& p, RowSmem<D>& sm, int s, int t0, int t
     for (int r = 0; r < 4; ++r) {
       const float f = sm.shrink[or0 + r];
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) acc[r][c] *= f;
+      for (int c = 0; c < kCols / 2; ++c) acc[r][c] = mul2(acc[r][c], f2(f, f));
     }
     auto values = [&](auto all_c) {
 #pragma unroll 4
       for (int i = 0; i < n; ++i) {
         const float4 w4 = *reinterpret_cast<const float4*>(&sm.p[i][or0]);
         const float w[4] = {w4.x, w4.y, w4.z, w4.w};
-        float vv[kCols];
+        F2 vv[kCols / 2];
 #pragma unroll
-        for (int c = 0; c < kCols; c += 2) {
-          const float2 v2 = *reinterpret_cast<const float2*>(&sm.v[i][oc + c]);
-          vv[c] = v2.x;
-          vv[c + 1] = v2.y;
-        }
+        for (int c = 0; c < kCols / 2; ++c) vv[c] = *reinterpret_cast<const F2*>(&sm.v[i][oc + 2 * c]);
         // (a masked value is not touched: it may be infinite or NaN)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            if (decltype(all_c)::value || !(w[r] < 0.f)) acc[r][c] = fmaf(w[r], vv[c], acc[r][c]);
+          for (int c = 0; c < kCols / 2; ++c)
+            if (decltype(all_c)::value || !(w[r] < 0.f)) acc[r][c] = fma2(f2(w[r], w[r]), vv[c], acc[r][c]);
       }
     };
     if (all) values(std::true_type());
@@ -192,14 +196,19 @@ __device__ void rows_of(const WinParams& p, RowSmem<D>& sm, int s, int t0, int t
     const float inv = 1.f / sm.sum[row];
     T* o = static_cast<T*>(p.out) + (size_t)(row0 + t0 + row / per) * p.ldo + (size_t)head(row) * D;
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) o[oc + c] = from_f32<T>(acc[r][c] * inv);
+    for (int c = 0; c < kCols / 2; ++c) {
+      float x, y;
+      unf2(acc[r][c], x, y);
+      o[oc + 2 * c] = from_f32<T>(x * inv);
+      o[oc + 2 * c + 1] = from_f32<T>(y * inv);
+    }
   }
 }
 
 // left: over the units in the list, pieces of the tensor-core form (p.group is at
 // most its tile's 128 rows).
 template <typename T, int D, bool kLeft>
-__global__ void __launch_bounds__(kRowThreads) win_rows_kernel(WinParams p, Pieces pieces, const int32_t* left) {
+__global__ void __launch_bounds__(kRowThreads, 5) win_rows_kernel(WinParams p, Pieces pieces, const int32_t* left) {
   extern __shared__ __align__(16) unsigned char row_smem[];
   RowSmem<D>& sm = *reinterpret_cast<RowSmem<D>*>(row_smem);
   pdl_wait_then_release();

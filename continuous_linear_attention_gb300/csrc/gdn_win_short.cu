@@ -102,7 +102,7 @@ __device__ __forceinline__ Unit unit_of(const WinParams& p, const SeqList& list,
   w.row0 = plan ? plan->lo[w.s] : b.cu[w.s];
   w.len = (plan ? plan->lo[w.s + 1] : b.cu[w.s + 1]) - w.row0;
   w.blk = plan ? plan->blk[w.s] : b.blk[w.s];
-  w.past = b.past_len[w.s];
+  w.past = plan ? plan->past[w.s] : b.past_len[w.s];
   w.slots = min(w.past, p.sinks + p.window);
   w.ring_stages = (w.slots + kKeys - 1) / kKeys;
   const int all = w.ring_stages + (w.len + kKeys - 1) / kKeys;
