@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) win_rows_kernel(WinParams p, P
     const int n = n_left > kWinLeft ? list.total * p.Hkv : n_left;
     for (int i = blockIdx.x; i < n * subs; i += gridDim.x) {
       const int u = n_left > kWinLeft ? i / subs : left[i / subs];
-      unit(u / p.Hkv, u % p.Hkv, i % subs);
+      if (u < list.total * p.Hkv) unit(u / p.Hkv, u % p.Hkv, i % subs);
     }
   } else {
     const int sub = blockIdx.x % subs, hk = blockIdx.x / subs % p.Hkv, piece = blockIdx.x / (subs * p.Hkv);
@@ -428,6 +428,7 @@ int gdn_win_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
   if (layer < 0 || layer >= p->num_layers || T < 0 || N < 0 || max_seqlen_hint < 0)
     return GDN_ERR_RANGE;
   if (num_heads < 1 || num_heads > 4096 || num_heads % p->Hk != 0) return GDN_ERR_DIMS;
+  if (!(scale <= 3.402823466e38f && scale >= -3.402823466e38f)) return GDN_ERR_RANGE;
   if (N == 0) return T == 0 ? GDN_OK : GDN_ERR_RANGE;
   if (!cu_seqlens || !state_block_idx || !past_lens) return GDN_ERR_NULL;
   if (T > 0 && (!q || !k || !v || !out)) return GDN_ERR_NULL;

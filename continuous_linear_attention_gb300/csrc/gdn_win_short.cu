@@ -21,9 +21,9 @@
 // registers.  With 8 rows the legacy tensor instruction is at a tenth of its rate
 // here, and tcgen05's least tile, 64 rows, would be mostly padding.
 //
-// P is rounded to bf16 as the product's operand (its sum is not): an output's
-// error is 2^-9 / sqrt(3) relative to the root of the sum of its squared terms, on top
-// of its own rounding by about as much.
+// P enters its product as two bf16 terms, exact to 2^-16, so that an output is off
+// by its own rounding alone (with one term by 1.3 times that; the products have
+// room for it beside the copies).
 //
 // Few sequences: a window is cut into parts for several CTAs; each leaves its
 // maximum, sum and output, and the last one to finish joins them, in order.
@@ -361,8 +361,16 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int late, int32_t* arriv
           sum[r] += x;
         }
       }
-      // the weights as the product takes them: keys 2t .., row g
-      const uint32_t b0 = transpose8x8(pack(sc[0], sc[1])), b1 = transpose8x8(pack(sc[2], sc[3]));
+      // The weights as the product takes them: keys 2t .., row g; two bf16 terms each,
+      // the first one cut off, so that the second is not negative, and not zero where
+      // the weight is not: an infinite value stays infinite.
+      auto rest = [](float x) {
+        return x > 0.f ? fmaxf(x - __uint_as_float(__float_as_uint(x) & 0xffff0000u), 1.2e-38f) : x;
+      };
+      const uint32_t b0 = transpose8x8(__byte_perm(__float_as_uint(sc[0]), __float_as_uint(sc[1]), 0x7632));
+      const uint32_t b1 = transpose8x8(__byte_perm(__float_as_uint(sc[2]), __float_as_uint(sc[3]), 0x7632));
+      const uint32_t c0 = transpose8x8(pack(rest(sc[0]), rest(sc[1])));
+      const uint32_t c1 = transpose8x8(pack(rest(sc[2]), rest(sc[3])));
       // one half's products; mask: the keys that count
       auto products = [&](int h, unsigned mask, auto&& each) {
         uint32_t x[4][4];
@@ -387,7 +395,10 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int late, int32_t* arriv
         }
 #pragma unroll
         for (int h = 0; h < kHalves; ++h)
-          products(h, there, [&](int j, const uint32_t* a) { mma16816(o[j], a, b0, b1); });
+          products(h, there, [&](int j, const uint32_t* a) {
+            mma16816(o[j], a, c0, c1);
+            mma16816(o[j], a, b0, b1);
+          });
       } else if constexpr (kPartly) {
         // token by token: its rows' weights alone, on the values that it sees, so that
         // what a row does not see does not reach it (0 times NaN would)
@@ -402,6 +413,7 @@ win_short_kernel(WinParams p, Pieces pieces, int parts, int late, int32_t* arriv
           for (int h = 0; h < kHalves; ++h)
             products(h, mask, [&](int j, const uint32_t* a) {
               float c[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816(c, a, pos_g == at ? c0 : 0u, pos_g == at ? c1 : 0u);
               mma16816(c, a, pos_g == at ? b0 : 0u, pos_g == at ? b1 : 0u);
 #pragma unroll
               for (int r = 0; r < 2; ++r)
