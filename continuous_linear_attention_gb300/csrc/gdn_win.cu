@@ -254,7 +254,10 @@ __global__ void __launch_bounds__(kAppendThreads) win_append_kernel(WinParams p,
   __shared__ PlanSmem plan;
   pdl_wait_then_release();
   const Batch& b = p.batch;
-  if (blockIdx.x == 0 && threadIdx.x == 0) b.work.header()[kWorkHead] = 0;  // nothing is left
+  if (blockIdx.x == 0 && threadIdx.x == 0) {  // nothing is left, and no unit claimed
+    b.work.header()[kWorkHead] = 0;
+    b.work.header()[kItemHeadC] = 0;
+  }
   const SeqList list = b.listed ? listed_long(b) : plan_self(b, pieces, plan, p.report && blockIdx.x == 0);
   const int row16 = p.Hkv * p.d * (int)sizeof(T) / 16, head16 = p.d * (int)sizeof(T) / 16;
   for (int piece = blockIdx.x; piece < list.total; piece += gridDim.x) {

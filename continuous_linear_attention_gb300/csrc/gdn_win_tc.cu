@@ -21,7 +21,7 @@
 // tiles alternate: the softmax of one beside the products of the other.
 // 15,843 tokens x 32 heads (8 kv heads), window 1,024: TIME_PROMPT.
 //
-// One CTA per SM, units by a fixed stride.  Roles:
+// One CTA per SM.  Roles:
 //   softmax A, B  four warps each, a thread per row: S from tensor memory, P back
 //                 to it, in the end the output
 //   MMA A, B      a warp each: P V of a tile and S of the next one, in turns, so
@@ -553,17 +553,25 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
       // a unit's sequence is looked up while the one before it is loaded
       int t0 = 0, row0 = 0, len = 0, past = 0, blk = 0;
       auto look_up = [&](int u) {
-        const int piece = u / p.Hkv, e = entry_of(list, piece), s = list.items[e];
+        const int piece = (units - 1 - u) / p.Hkv, e = entry_of(list, piece), s = list.items[e];
         t0 = (piece - list.first[e]) * pieces.tokens;
         row0 = b.cu[s];
         len = b.cu[s + 1];
         past = b.past_len[s];
         blk = b.blk[s];
       };
+      // units from the last to the first (the first ones of a prompt see fewer keys than
+      // the others) and, behind a CTA's first one, claimed from a counter that
+      // win_append_kernel sets back: prompts of 16 Ki tokens 225 us by a fixed stride, 206 so
+      auto claim = [&]() {
+        int u = 0;
+        if (lane == 0) u = atomicAdd(&b.work.header()[kItemHeadC], 1);
+        return (int)gridDim.x + __shfl_sync(0xffffffffu, u, 0);
+      };
       int next_u = blockIdx.x;
       if (next_u < units) look_up(next_u);
       while (next_u < units && !dead) {
-        const int u = next_u, hk = u % p.Hkv;
+        const int u = units - 1 - next_u, hk = u % p.Hkv;
         len -= row0;
         const int tokens = min(pieces.tokens, len - t0);
         const int p0 = past + t0, p1 = p0 + tokens;
@@ -592,8 +600,6 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
         }
         __syncwarp();
         const int n_tiles = (n_segs + kSegs - 1) / kSegs;
-        next_u += gridDim.x;
-        if (next_u < units) look_up(next_u);
         for (int j = 0; j < n_tiles && !dead; ++j) {
           const int segs = min(kSegs, n_segs - j * kSegs);
           // segment lane % 8 of the tile
@@ -670,6 +676,10 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
           }
           ++loads;
           st.next();
+          if (j == min(1, n_tiles - 1)) {  // (with the copies of two tiles on their way)
+            next_u = claim();
+            if (next_u < units) look_up(next_u);
+          }
         }
       }
       if (!dead) {
