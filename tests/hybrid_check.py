@@ -72,9 +72,10 @@ class SelRun(Packed):
 
     def __init__(self, lens, past, channels, N=16, K=4, act="bf16", seed=0, blocks=None, num_blocks=None,
                  bias=True, gate=True, skip_weight=True, hint=0, rows_after=0, values=None, num_layers=1,
-                 layer=0, A_log=None, dt_bias=None, dense=False):
+                 layer=0, A_log=None, dt_bias=None, dense=False, segment=0):
         g = torch.Generator().manual_seed(seed)
         self.batch(lens, num_blocks, blocks, g, rows_after=rows_after)
+        self.segment = segment
         C, dt = channels, dtype_of(act)
         self.C, self.n, self.K, self.act, self.hint = C, N, K, act, hint
         self.num_layers, self.layer = num_layers, layer
@@ -166,6 +167,14 @@ class SelRun(Packed):
                     h["u"], h["dt"], h["B"], h["C"], h["z"] if self.z is not None else None, self.cu, past,
                     f64(self.A_log), None if self.D is None else f64(self.D),
                     None if self.dt_bias is None else f64(self.dt_bias))
+                # a start of a segment decays by e^x, x the sum of its tokens' in fp32: off by
+                # segment EPS |x| e^x, which is segment EPS / e at most, and as much again
+                # from the starts before it
+                far = 2 * self.segment * EPS / np.e * max(np.abs(past).max(), np.abs(hs).max())
+                if far:
+                    gate = 1 if self.z is None else np.abs(ref.silu(h["z"]))
+                    ey = ey + far * np.abs(h["C"]).sum(1, keepdims=True) * gate
+                    eh = eh + far
                 for s in live:
                     rows = slice(self.cu[s], self.cu[s + 1])
                     close(got[rows], y[rows], ey[rows] + ULP[self.act] * np.abs(y[rows]) + 2.0 ** -126, ("y", s))

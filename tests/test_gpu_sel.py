@@ -264,3 +264,72 @@ def test_block_operations_move_both_states():
     torch.cuda.synchronize()
     page = run.mem.view(8, -1)
     assert torch.equal(page[free[0]], page[run.blk[0]])
+
+
+# Long sequences of few channels: their segments run side by side, from states that
+# a pass before them finds.
+SEGMENTED = [([900], [0]), ([900], [1]), ([700, 1, 0, 450, 2, 64, 65], [1, 1, 1, 0, 1, 0, 1]),
+             ([1, 1, 230, 1, 640], [0, 1, 0, 1, 1])]
+
+
+@pytest.mark.parametrize("lens,past", SEGMENTED)
+@pytest.mark.parametrize("act,N", [("f32", 16), ("bf16", 16), ("f32", 32), ("bf16", 64)])
+@pytest.mark.parametrize("channels", [8, 136])
+def test_segments_of_long_sequences(lens, past, act, N, channels):
+    run = sel_check("scan", lens, past, channels, N=N, act=act, gate=N != 32, skip_weight=N != 64, seed=N,
+                    rows_after=2, segment=64)
+    assert run.pool.error_flags() == 0
+
+
+def test_segments_with_other_layers_and_a_long_sequence():
+    sel_check("scan", [5000, 300], [1, 0], 264, act="bf16", num_layers=2, layer=1, segment=192)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_values_reach_no_segment_before_them_and_no_other_sequence(value):
+    lens = [700, 300, 1]
+
+    def put(host, run):
+        for t in host.values():
+            t[500] = value
+        host["u"][700 + 299] = value
+
+    a, b = SelRun(lens, [1, 0, 1], 48), SelRun(lens, [1, 0, 1], 48, values=put)
+    for r in (a, b):
+        r.run_scan()
+    torch.cuda.synchronize()
+    for rows in (slice(0, 500), slice(700, 999), slice(1000, 1001)):
+        assert torch.isfinite(b.out[rows]).all() and torch.equal(bits(a.out[rows]), bits(b.out[rows]))
+    assert torch.equal(bits(a.ssm[a.blk[2]]), bits(b.ssm[b.blk[2]]))
+    assert not torch.isfinite(b.out[500:564]).any()
+
+
+def test_segments_in_two_graphs_on_one_pool():
+    """Both use the pool's room for states, one behind the other."""
+    runs = [SelRun([800, 1, 300], [1, 1, 0], 72, seed=3, blocks=[3, 1, 2]), SelRun([260, 640], [0, 1], 72, seed=4)]
+    first, second = runs
+    second.pool, second.blk_d = first.pool, torch.tensor([4, 5], dtype=torch.int32, device="cuda")
+    graphs = []
+    for r in runs:
+        r.run_scan()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            r.run_scan()
+        graphs.append(g)
+    start = first.before.clone()
+    start.view(6, -1)[4:] = start.view(6, -1)[1:3].flip(0)
+    want = []
+    for r in runs:
+        first.mem.copy_(start)
+        r.run_scan()
+        torch.cuda.synchronize()
+        want.append(r.out.clone())
+    first.mem.copy_(start)
+    for r in runs:
+        r.out.fill_(SENTINEL)
+    for g in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    for r, w in zip(runs, want):
+        assert torch.equal(bits(r.out), bits(w))

@@ -312,3 +312,77 @@ def test_host_refusals():
             f()
     torch.cuda.synchronize()
     assert (run.out == SENTINEL).all() and torch.equal(run.mem, run.before)
+
+
+@LEAK
+@pytest.mark.parametrize("value", BAD)
+def test_queries_that_are_not_finite_reach_their_own_row_only(act, d, H, Hkv, value):
+    def put(x, run):
+        for s in range(run.N):
+            x[run.cu[s + 1] - 1, 0] = value
+
+    lens = [150, 5, 1]
+    a = WinRun(lens, [7, 30, 60], H, Hkv, d, 64, 4, act)
+    b = WinRun(lens, [7, 30, 60], H, Hkv, d, 64, 4, act, values=put)
+    for r in (a, b):
+        r.run()
+    torch.cuda.synchronize()
+    for s in range(3):
+        last = b.cu[s + 1] - 1
+        assert torch.isnan(b.out[last, 0]).all()
+        assert torch.equal(bits(a.out[b.cu[s]:last]), bits(b.out[b.cu[s]:last]))
+        assert torch.equal(bits(a.out[last, 1:]), bits(b.out[last, 1:]))
+
+
+def test_prompts_in_two_graphs_on_one_pool():
+    """Both use the pool's lists and counters, one behind the other, replayed in both orders."""
+    a = WinRun([300, 1, 40], [10, 90, 0], 8, 2, 128, 48, 4, seed=3, blocks=[1, 2, 3], num_blocks=8)
+    b = WinRun([700, 1], [100, 50], 8, 2, 128, 48, 4, seed=4, blocks=[4, 5], num_blocks=8)
+    b.kv[a.blk] = a.kv[a.blk]
+    start = b.mem.clone()
+    a.pool = b.pool
+    graphs, want = [], []
+    for r in (a, b):
+        b.mem.copy_(start)
+        r.run()
+        torch.cuda.synchronize()
+        want.append(r.out.clone())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            r.run()
+        graphs.append(g)
+    for order in ((0, 1), (1, 0), (1, 0)):
+        b.mem.copy_(start)
+        for r in (a, b):
+            r.out.fill_(SENTINEL)
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for r, w in zip((a, b), want):
+            assert torch.equal(bits(r.out), bits(w)), order
+    assert b.pool.error_flags() == 0
+
+
+def test_more_sequences_than_a_cta_lists_with_long_prompts():
+    lens = [0, 1] * 150 + [260, 40, 300]
+    win_check(lens, [3] * 303, 4, 2, 128, 50, 2)
+    win_check(lens, [3] * 303, 4, 2, 64, 50, 2)
+
+
+def test_values_that_are_not_finite_in_every_prompt_and_head():
+    """More units than the list of those done again holds: all of them are."""
+    def put(x, run):
+        for s in range(run.N):
+            x[run.cu[s] + 30, 130:, 1] = float("inf")
+
+    win_check([33] * 256, [0] * 256, 65, 65, 64, 20, 0, values=put)
+
+
+def test_scales_that_are_not_finite_are_refused():
+    run = WinRun([3, 1], [5, 0], 4, 2, 64, 20, 2)
+    for scale in (float("nan"), float("inf"), -float("inf")):
+        run.scale = scale
+        with pytest.raises(binding.GdnError):
+            run.run()
+    torch.cuda.synchronize()
+    assert (run.out == SENTINEL).all() and torch.equal(run.mem, run.before)
