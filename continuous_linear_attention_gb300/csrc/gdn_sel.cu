@@ -367,9 +367,10 @@ constexpr int kSegmentsMax = 8192;       // (and for their steps' sums)
 // as some 300.
 __host__ __device__ inline int segment_tokens(int longest, long long tokens, int ch_blocks, int slots,
                                               int n, int sms) {
-  const long long share = tokens * ch_blocks / sms;
+  const long long share = (tokens * ch_blocks + sms - 1) / sms;
   const long long whole = 2ll * longest > share ? 2ll * longest : share;
-  long long seg = (share / 8 + 31) / 32 * 32;  // eight of them to an SM
+  // eight of them to an SM, and never more: the grid has room for so many
+  long long seg = ((share + 7) / 8 + 31) / 32 * 32;
   if (seg < 64) seg = 64;
   const long long split = share * 7 / 4 + 2 * seg + 300;
   if (split >= whole || tokens / seg + n > slots) return 0x7fffffff;

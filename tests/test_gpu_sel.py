@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from continuous_linear_attention_gb300 import binding
-from hybrid_check import SENTINEL, SelRun, bits, sel_check
+from hybrid_check import I32, SENTINEL, SelRun, bits, sel_check
 
 pytestmark = pytest.mark.gpu
 
@@ -333,3 +333,24 @@ def test_segments_in_two_graphs_on_one_pool():
     torch.cuda.synchronize()
     for r, w in zip(runs, want):
         assert torch.equal(bits(r.out), bits(w))
+
+
+@pytest.mark.parametrize("n", [79_030, 77_824, 77_825])
+def test_lengths_whose_segments_just_fit(n):
+    """A share of the tokens that is no whole number of segments: every token is in one."""
+    run = SelRun([n], [1], 8, act="f32", seed=1, gate=False)
+    run.run_scan()
+    other, out = 2 if run.blk[0] != 2 else 1, run.out.clone()
+    run.ssm[other] = run.past_ssm[0].cuda()
+    for lo, hi in ((0, n // 2), (n // 2, n)):
+        part = SelRun([hi - lo], [1], 8, act="f32", seed=1, gate=False)
+        part.pool, part.blk_d, part.dev, part.T = run.pool, torch.tensor([other], **I32), run.dev, hi - lo
+        for name in ("u", "dt", "B", "Cm"):
+            setattr(part, name, getattr(run, name)[lo:hi])
+        part.out = out[lo:hi]
+        part.run_scan()
+    torch.cuda.synchronize()
+    # (the same sums in another order)
+    assert (run.out - out).abs().max() <= 2.0 ** -16 * run.out.abs().max()
+    a, b = run.ssm[run.blk[0]], run.ssm[other]
+    assert (a - b).abs().max() <= 2.0 ** -16 * a.abs().max()
