@@ -9,11 +9,15 @@
 // Bound by HBM: each element is read once and written once.  A head's row is
 // worked on by d/16 threads, each with the two runs of 8 channels whose halves
 // belong together, so that the rotation needs no other thread; the sum of
-// squares is the only thing that crosses lanes.  A group of d/16 threads takes
-// all heads of a token where there are tokens enough (the angle's sine and
-// cosine are computed once per token), fewer where not.
-// 15,843 tokens x 40 heads x 128: 64.5 us, 5.0 TB/s.
+// squares is the only thing that crosses lanes.  A warp takes as many tokens side
+// by side as it has groups of d/16 threads and walks its share of their heads,
+// over the next tokens' where the share is longer: every warp has the same work,
+// and a token's sines and cosines are made once (CTAs of 32 whole tokens each came
+// in 1.6 waves: 62 us).  The copies of the next rows are on their way meanwhile.
+// 15,843 tokens x 40 heads x 128: 56.1 us, 5.8 TB/s.
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "gdn_cta.cuh"
 #include "gdn_internal.cuh"
@@ -23,6 +27,9 @@ namespace gdn {
 namespace {
 
 constexpr int kRopeThreads = 256;
+// Places of a thread for rows on their way, and CTAs of an SM: 56.1 us with 4 and 2, 56.4
+// with 3 and 2, 58.4 with 6 and 2, 62.1 with 4 and 3 (more warps are at more places of the
+// memory at a time), 74 with 8 and 1.
 constexpr int kRopeAhead = 4, kRopeCtas = 2;
 
 struct RopeParams {
@@ -34,17 +41,25 @@ struct RopeParams {
   const float* inv_freq;             // [rot / 2]
   float eps, offset;
   int T, H, Hkv, d, rot, interleaved;
-  int per;     // heads a group takes
-  int slices;  // groups a token takes
+  long long rows;  // of a warp: one head of its tokens each
+  int per;         // rows a warp takes
 };
 
 // A run of 8 channels, as it lies.
 template <typename T>
 struct Run8 {
   uint4 w[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T* p) {
+  // the copy to this thread's places in shared memory, a row of them for 16 bytes
+  static __device__ __forceinline__ void fetch(uint4 (*to)[kRopeThreads], const T* p) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&to[i][threadIdx.x])),
+                   "l"(reinterpret_cast<const uint4*>(p) + i)
+                   : "memory");
+  }
+  __device__ __forceinline__ void take(const uint4 (*from)[kRopeThreads]) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = from[i][threadIdx.x];
   }
   __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
@@ -78,161 +93,209 @@ struct Run8 {
   }
 };
 
+template <typename T, int D, bool kAny>
+struct RopeSmem {
+  static constexpr int kWords = sizeof(T) / 2;  // 16 bytes each, of a run
+  uint4 ring[kRopeAhead][2 * kWords][kRopeThreads];
+  // inv_freq / 2 pi as 64-bit fractions of a turn: an angle is the product with
+  // the position modulo 2^64, exact for any position (an fp32 angle at position
+  // 10^6 would be off by 0.06)
+  unsigned long long turns[D / 2];
+  float rows[kAny ? kRopeThreads * 16 : 1];
+};
+
 // kAny: a rotated half that is no multiple of 8 channels (and not interleaved),
 // whose pairs lie in different threads' runs: they meet in shared memory.
 template <typename T, int D, bool kAny>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(RopeParams p) {
   constexpr int kLanes = D / 16;  // threads per head
-  constexpr int kAhead = sizeof(T) == 2 ? kRopeAhead : 2;  // heads whose reads are on their way together
-  // inv_freq / 2 pi as 64-bit fractions of a turn: an angle is the product with
-  // the position modulo 2^64, exact for any position (an fp32 angle at position
-  // 10^6 would be off by 0.06)
-  __shared__ unsigned long long turns[D / 2];
-  __shared__ float rows[kAny ? kRopeThreads * 16 : 1];
+  constexpr int kAhead = kRopeAhead;
+  extern __shared__ __align__(16) unsigned char rope_smem[];
+  using Smem = RopeSmem<T, D, kAny>;
+  constexpr int kWords = Smem::kWords;
+  Smem& sm = *reinterpret_cast<Smem*>(rope_smem);
   pdl_wait_then_release();
-  const int half = p.rot / 2;
-  if ((int)threadIdx.x < half) {
-    double t = (double)p.inv_freq[threadIdx.x] * 0.15915494309189533577;
-    t -= floor(t);
-    turns[threadIdx.x] = t < 1.0 ? (unsigned long long)(t * 18446744073709551616.0) : 0ull;
-  }
-  __syncthreads();
   const int lane = threadIdx.x % kLanes;
-  const long long group =
-      ((long long)blockIdx.x * kRopeThreads + threadIdx.x) / kLanes;
-  const long long token = group / p.slices;
-  const int pos = token < p.T ? p.positions[token] : -1;
-  const bool live = pos >= 0;  // (a group that is not lends its lanes to the sums)
+  const int half = p.rot / 2;
   // this thread's two runs
   const bool apart = !kAny && !p.interleaved && lane < half / 8;  // those of a half and of the other
   const int ca = apart ? 8 * lane : 16 * lane, cb = apart ? ca + half : ca + 8;
-  // the turns of their pairs, or (kAny) of their channels
+  // the warp's rows: of kTokens tokens side by side, head by head
+  constexpr int kTokens = 32 / kLanes;
+  const int heads = p.H + p.Hkv, side = threadIdx.x % 32 / kLanes;
+  const long long r0 = ((long long)blockIdx.x * (kRopeThreads / 32) + threadIdx.x / 32) * p.per;
+  const int n = (int)min((long long)p.per, max(0ll, p.rows - r0));
+  long long token = r0 / heads * kTokens + side;
+  int h = (int)(r0 % heads);
+  // kAhead - 1 rows on their way (queries, then keys), each to where the one before the
+  // last lay: the first ones while the angles are made
+  long long token_in = token;
+  int h_in = h, in = 0;
+  auto ahead = [&]() {
+    if (in < n) {
+      if (token_in < p.T) {
+        const T* src = h_in < p.H ? static_cast<const T*>(p.q) + token_in * p.ldq + (size_t)h_in * D
+                                  : static_cast<const T*>(p.k) + token_in * p.ldk + (size_t)(h_in - p.H) * D;
+        Run8<T>::fetch(sm.ring[in % kAhead], src + ca);
+        Run8<T>::fetch(sm.ring[in % kAhead] + kWords, src + cb);
+      }
+      if (++h_in == heads) {
+        h_in = 0;
+        token_in += kTokens;
+      }
+    }
+    ++in;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead - 1; ++i) ahead();
+  int pos = token < p.T ? p.positions[token] : -1, pos_next = -1;
+  if ((int)threadIdx.x < half) {
+    double t = (double)p.inv_freq[threadIdx.x] * 0.15915494309189533577;
+    t -= floor(t);
+    sm.turns[threadIdx.x] = t < 1.0 ? (unsigned long long)(t * 18446744073709551616.0) : 0ull;
+  }
+  __syncthreads();
+  // the turns of a token's pairs, or (kAny) of their channels
   constexpr int kTurns = kAny ? 16 : 8;
   float co[kTurns], si[kTurns];
+  auto turn = [&]() {
 #pragma unroll
-  for (int i = 0; i < kTurns; ++i) {
-    co[i] = 1.f;
-    si[i] = 0.f;
-    int of = 8 * lane + i;  // the pair, in either order
-    if (kAny) {
-      of = ca + i;
-      of = of < half ? of : of < 2 * half ? of - half : half;
+    for (int i = 0; i < kTurns; ++i) {
+      co[i] = 1.f;
+      si[i] = 0.f;
+      int of = 8 * lane + i;  // the pair, in either order
+      if (kAny) {
+        of = ca + i;
+        of = of < half ? of : of < 2 * half ? of - half : half;
+      }
+      if (pos >= 0 && of < half) {
+        const unsigned long long a = sm.turns[of] * (unsigned long long)(unsigned)pos;
+        sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &si[i], &co[i]);
+      }
     }
-    if (live && of < half) {
-      const unsigned long long a = turns[of] * (unsigned long long)(unsigned)pos;
-      sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &si[i], &co[i]);
-    }
-  }
+  };
   // the lanes of one head: they come to its sum together or not at all
   const unsigned mask = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
-  const int heads = p.H + p.Hkv;
-  const int h0 = (int)(group % p.slices) * p.per, h1 = min(heads, h0 + p.per);
-  // queries, then keys: their weights stay in registers
+  const float* weight = nullptr;
+  T* dst = nullptr;
+  float wa[8], wb[8];
 #pragma unroll 1
-  for (int part = 0; part < 2; ++part) {
-    const int lo = part ? max(h0, p.H) - p.H : h0, hi = part ? h1 - p.H : min(h1, p.H);
-    if (lo >= hi) continue;  // (the same for all groups of a slice: a warp's may differ)
-    const float* weight = part ? p.k_weight : p.q_weight;
-    const T* src = static_cast<const T*>(part ? p.k : p.q) + token * (part ? p.ldk : p.ldq);
-    T* dst = static_cast<T*>(part ? p.k_out : p.q_out) + token * (part ? p.ldko : p.ldqo);
-    float wa[8], wb[8];
-    if (weight) {
+  for (int i = 0; i < n; ++i) {
+    if (i == 0 || h == 0) {
+      if (i > 0) pos = pos_next;
+      turn();
+      // (a position ahead of its token)
+      pos_next = token + kTokens < p.T ? p.positions[token + kTokens] : -1;
+    }
+    if (i == 0 || h == 0 || h == p.H) {
+      weight = h < p.H ? p.q_weight : p.k_weight;
+      dst = h < p.H ? static_cast<T*>(p.q_out) + token * p.ldqo + (size_t)h * D
+                    : static_cast<T*>(p.k_out) + token * p.ldko + (size_t)(h - p.H) * D;
+      if (weight) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        wa[i] = weight[ca + i] + p.offset;
-        wb[i] = weight[cb + i] + p.offset;
+        for (int i = 0; i < 8; ++i) {
+          wa[i] = weight[ca + i] + p.offset;
+          wb[i] = weight[cb + i] + p.offset;
+        }
       }
     }
-    for (int h = lo; h < hi; h += kAhead) {
-      Run8<T> ra[kAhead], rb[kAhead];
+    ahead();
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    // (the rows of no token, or of one without a position: not read and not written)
+    if (pos >= 0) {
+      Run8<T> ra, rb;
+      ra.take(sm.ring[i % kAhead]);
+      rb.take(sm.ring[i % kAhead] + kWords);
+      float a[8], b[8];
+      ra.get(a);
+      rb.get(b);
+      if (weight) {
+        float sum = 0.f;
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (live && h + u < hi) {
-          ra[u].load(src + (size_t)(h + u) * D + ca);
-          rb[u].load(src + (size_t)(h + u) * D + cb);
+        for (int i = 0; i < 8; ++i) sum = fmaf(a[i], a[i], fmaf(b[i], b[i], sum));
+#pragma unroll
+        for (int w = 1; w < kLanes; w <<= 1) sum += __shfl_xor_sync(mask, sum, w);
+        const float r = rsqrtf(sum * (1.f / D) + p.eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          a[i] *= r * wa[i];
+          b[i] *= r * wb[i];
         }
       }
+      if constexpr (kAny) {
+        float* row = sm.rows + threadIdx.x / kLanes * D;
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (!live || h + u >= hi) continue;
-        float a[8], b[8];
-        ra[u].get(a);
-        rb[u].get(b);
-        if (weight) {
-          float sum = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sum = fmaf(a[i], a[i], fmaf(b[i], b[i], sum));
-#pragma unroll
-          for (int w = 1; w < kLanes; w <<= 1) sum += __shfl_xor_sync(mask, sum, w);
-          const float r = rsqrtf(sum * (1.f / D) + p.eps);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            a[i] *= r * wa[i];
-            b[i] *= r * wb[i];
-          }
+        for (int i = 0; i < 8; ++i) {
+          row[ca + i] = a[i];
+          row[cb + i] = b[i];
         }
-        if constexpr (kAny) {
-          float* row = rows + threadIdx.x / kLanes * D;
+        __syncwarp(mask);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            row[ca + i] = a[i];
-            row[cb + i] = b[i];
-          }
-          __syncwarp(mask);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int c = ca + i;
-            float& x = i < 8 ? a[i] : b[i - 8];
-            if (c < half) x = x * co[i] - row[c + half] * si[i];
-            else if (c < 2 * half) x = x * co[i] + row[c - half] * si[i];
-          }
-          __syncwarp(mask);
-        } else if (p.interleaved) {
-#pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            const float x = a[i], y = b[i];
-            a[i] = x * co[i / 2] - a[i + 1] * si[i / 2];
-            a[i + 1] = a[i + 1] * co[i / 2] + x * si[i / 2];
-            b[i] = y * co[4 + i / 2] - b[i + 1] * si[4 + i / 2];
-            b[i + 1] = b[i + 1] * co[4 + i / 2] + y * si[4 + i / 2];
-          }
-        } else if (apart) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float x = a[i];
-            a[i] = x * co[i] - b[i] * si[i];
-            b[i] = b[i] * co[i] + x * si[i];
-          }
+        for (int i = 0; i < 16; ++i) {
+          const int c = ca + i;
+          float& x = i < 8 ? a[i] : b[i - 8];
+          if (c < half) x = x * co[i] - row[c + half] * si[i];
+          else if (c < 2 * half) x = x * co[i] + row[c - half] * si[i];
         }
-        Run8<T> oa, ob;
-        oa.set(a);
-        ob.set(b);
-        oa.store(dst + (size_t)(h + u) * D + ca);
-        ob.store(dst + (size_t)(h + u) * D + cb);
+        __syncwarp(mask);
+      } else if (p.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const float x = a[i], y = b[i];
+          a[i] = x * co[i / 2] - a[i + 1] * si[i / 2];
+          a[i + 1] = a[i + 1] * co[i / 2] + x * si[i / 2];
+          b[i] = y * co[4 + i / 2] - b[i + 1] * si[4 + i / 2];
+          b[i + 1] = b[i + 1] * co[4 + i / 2] + y * si[4 + i / 2];
+        }
+      } else if (apart) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float x = a[i];
+          a[i] = x * co[i] - b[i] * si[i];
+          b[i] = b[i] * co[i] + x * si[i];
+        }
       }
+      Run8<T> oa, ob;
+      oa.set(a);
+      ob.set(b);
+      oa.store(dst + ca);
+      ob.store(dst + cb);
+    }
+    dst += D;
+    if (++h == heads) {
+      h = 0;
+      token += kTokens;
     }
   }
 }
 
 template <typename T>
 cudaError_t launch_rope(RopeParams& p, int sms, cudaStream_t s) {
-  const int lanes = p.d / 16, heads = p.H + p.Hkv;
-  // As many heads for a group as leave every SM 512 threads, and all of them
-  // where that is so anyway.
-  const long long want = (long long)sms * (kRopeThreads * kRopeCtas) / lanes;
-  long long slices = (want + p.T - 1) / p.T;
-  if (slices > heads) slices = heads;
-  p.per = (int)((heads + slices - 1) / slices);
-  p.slices = (heads + p.per - 1) / p.per;
-  const long long groups = (long long)p.T * p.slices;
-  const long long ctas = (groups * lanes + kRopeThreads - 1) / kRopeThreads;
+  const int tokens = 32 / (p.d / 16);
+  constexpr int kWarps = kRopeThreads / 32;
+  p.rows = ((long long)p.T + tokens - 1) / tokens * (p.H + p.Hkv);
+  // as many for a warp as leave every SM its CTAs
+  const long long warps = (long long)sms * kRopeCtas * kWarps;
+  p.per = (int)((p.rows + warps - 1) / warps);
+  const long long ctas = (p.rows + (long long)p.per * kWarps - 1) / ((long long)p.per * kWarps);
   const bool any = !p.interleaved && p.rot % 16 != 0;
-  auto kern = p.d == 32    ? any ? rope_kernel<T, 32, true> : rope_kernel<T, 32, false>
-              : p.d == 64  ? any ? rope_kernel<T, 64, true> : rope_kernel<T, 64, false>
-              : p.d == 128 ? any ? rope_kernel<T, 128, true> : rope_kernel<T, 128, false>
-              : any        ? rope_kernel<T, 256, true>
-                           : rope_kernel<T, 256, false>;
-  return launch_pdl(kern, dim3((unsigned)ctas), dim3(kRopeThreads), 0, s, p);
+  auto go = [&](auto kern, size_t smem) {
+    if (smem > 48 << 10) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(kern, dim3((unsigned)ctas), dim3(kRopeThreads), smem, s, p);
+  };
+  auto of = [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
+    return any ? go(rope_kernel<T, D, true>, sizeof(RopeSmem<T, D, true>))
+               : go(rope_kernel<T, D, false>, sizeof(RopeSmem<T, D, false>));
+  };
+  return p.d == 32    ? of(std::integral_constant<int, 32>())
+         : p.d == 64  ? of(std::integral_constant<int, 64>())
+         : p.d == 128 ? of(std::integral_constant<int, 128>())
+                      : of(std::integral_constant<int, 256>());
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -265,7 +328,7 @@ extern "C" int gdn_qk_norm_rope(const void* q, const void* k, int64_t ldq, int64
       return GDN_ERR_ALIGN;
     if (ldk < kcols || ldko < kcols || ldk > most || ldko > most) return GDN_ERR_RANGE;
   }
-  // (groups of d/16 threads for up to 8,192 heads a token: the grid's size)
+  // (a warp's rows are counted in 32 bits)
   if ((long long)T * (H + Hkv) * (d / 16) / gdn::kRopeThreads >= 0x7fffffffll) return GDN_ERR_RANGE;
   gdn::RopeParams p = {};
   p.q = q;

@@ -160,3 +160,12 @@ def test_binding_refusals():
             bad()
     with pytest.raises(binding.GdnError):
         binding.qk_norm_rope(q, k, pos, torch.zeros(33, device="cuda"))
+
+
+@pytest.mark.parametrize("act,d,rot", [("bf16", 128, 128), ("f32", 32, 6), ("f32", 256, 20), ("bf16", 64, 32)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_a_warps_share_goes_over_many_tokens(act, d, rot, in_place):
+    """Few heads of many tokens, some without a position between the others."""
+    for H, Hkv, T in ((1, 0, 50_011), (2, 1, 20_003)):
+        pos = [-1 if i % 7 == 3 or 900 < i < 950 else 3 * i for i in range(T)]
+        rope_check(T, H, Hkv, d, rot, act, positions=pos, in_place=in_place, seed=H)
