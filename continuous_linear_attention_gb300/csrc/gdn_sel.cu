@@ -100,13 +100,40 @@ __device__ __forceinline__ void softplus2(float& a, float& b) {
   unf2(fma2(q, t, f2(fmaxf(a, 0.f), fmaxf(b, 0.f))), a, b);
 }
 
+// y / (1 + e^-y) of two values.
+__device__ __forceinline__ F2 silu2(F2 y) {
+  float a, b;
+  unf2(mul2(y, f2(-kLog2e, -kLog2e)), a, b);
+  a = 1.f + ex2(a);
+  b = 1.f + ex2(b);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+  return mul2(y, f2(a, b));
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
 // --- convolution -------------------------------------------------------------
 // Bound by HBM: each input is read once (the K-1 rows before a piece twice, out
 // of L2) and each output written once.  A thread owns 16 bytes of channels and
 // walks the tokens of a piece with the K-1 inputs before in registers.
 constexpr int kConvThreads = 128;
 constexpr int kConvTokens = 32;  // per piece
-constexpr int kConvAhead = 8;    // tokens whose reads are on their way together (1: single tokens only)
+// Places of a thread for tokens on their way to it (1: single tokens only), in shared
+// memory: as registers they leave an SM three CTAs (15,843 tokens x 4,096 channels 55.2 us,
+// 49.0 us so; with 16 places 54.8).
+constexpr int kConvAhead = 8;
+constexpr int kConvCtas = 4;
 
 struct ConvParams {
   Batch batch;
@@ -122,9 +149,10 @@ struct ConvParams {
 };
 
 template <typename T, int K, int kAhead>
-__global__ void __launch_bounds__(kConvThreads) sel_conv_kernel(ConvParams p) {
+__global__ void __launch_bounds__(kConvThreads, kConvCtas) sel_conv_kernel(ConvParams p) {
   constexpr int kV = Vec16<T>::kN;
   __shared__ PlanSmem plan;
+  __shared__ uint4 ring[kAhead > 1 ? kAhead : 1][kConvThreads];
   pdl_wait_then_release();
   const Batch& b = p.batch;
   const SeqList list = b.listed ? listed_long(b)
@@ -195,37 +223,38 @@ __global__ void __launch_bounds__(kConvThreads) sel_conv_kernel(ConvParams p) {
 #pragma unroll
       for (int j = 0; j < K - 1; ++j) win[j] = load16(x + (size_t)(at - (K - 1) + j) * p.ldx);
     }
-    // kAhead tokens at a time, the next ones on their way
-    Vec16<T> next[kAhead];
+    // the copies of kAhead - 1 tokens on their way to this thread's places in shared
+    // memory, each to where the token before the last one lay
+    auto ahead = [&](int t) {
+      if (kAhead > 1 && t < n) cp_async16(&ring[t % kAhead][threadIdx.x], x + (size_t)(at + t) * p.ldx);
+      cp_async_commit();
+    };
+    if (kAhead > 1)
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (i < n) next[i] = load16(x + (size_t)(at + i) * p.ldx);
-    for (int t = 0; t < n; t += kAhead) {
-      Vec16<T> in[K - 1 + kAhead];
+      for (int i = 0; i < kAhead - 1; ++i) ahead(i);
+#pragma unroll 4
+    for (int t = 0; t < n; ++t) {
+      Vec16<T> in[K];
 #pragma unroll
       for (int j = 0; j < K - 1; ++j) in[j] = win[j];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        in[K - 1 + i] = next[i];
-        if (t + kAhead + i < n) next[i] = load16(x + (size_t)(at + t + kAhead + i) * p.ldx);
+      if (kAhead > 1) {
+        ahead(t + kAhead - 1);
+        cp_async_wait<kAhead - 1>();
+        in[K - 1].w = ring[t % kAhead][threadIdx.x];
+      } else {
+        in[K - 1] = load16(x + (size_t)(at + t) * p.ldx);
       }
+      float y[kV];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (t + i >= n) break;
-        float y[kV];
+      for (int j = 0; j < kV; j += 2) {
+        F2 acc = bias[j / 2];
 #pragma unroll
-        for (int j = 0; j < kV; j += 2) {
-          F2 acc = bias[j / 2];
-#pragma unroll
-          for (int k = 0; k < K; ++k) acc = fma2(w[k][j / 2], f2(in[i + k].at(j), in[i + k].at(j + 1)), acc);
-          unf2(acc, y[j], y[j + 1]);
-          y[j] = silu_f32(y[j]);
-          y[j + 1] = silu_f32(y[j + 1]);
-        }
-        store16(out + (size_t)(at + t + i) * p.ldo, y);
+        for (int k = 0; k < K; ++k) acc = fma2(w[k][j / 2], f2(in[k].at(j), in[k].at(j + 1)), acc);
+        unf2(silu2(acc), y[j], y[j + 1]);
       }
+      store16(out + (size_t)(at + t) * p.ldo, y);
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j) win[j] = in[kAhead + j];
+      for (int j = 0; j < K - 1; ++j) win[j] = in[j + 1];
     }
   }
 }
@@ -327,18 +356,6 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) sel_step_kernel(ScanP
       static_cast<T*>(p.y)[row * p.ldy + c] = from_f32<T>(y);
     }
   }
-}
-
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int kLeft>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
 // Longer sequences: a CTA walks the tokens of one sequence, or of a segment of
@@ -573,8 +590,7 @@ __global__ void __launch_bounds__(kScanThreads) sel_scan_kernel(ScanParams p) {
         if (p.z) {
           float z[2];
           two(&sm.z[buf][q][xc], z[0], z[1]);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) y[k] *= silu_f32(z[k]);
+          unf2(mul2(f2(y[0], y[1]), silu2(f2(z[0], z[1]))), y[0], y[1]);
         }
         T* out = static_cast<T*>(p.y) + (size_t)(row0 + t0 + q) * p.ldy + cb + xc;
         if constexpr (sizeof(T) == 4) {
@@ -883,8 +899,9 @@ int gdn_sel_conv_varlen_forward(gdn_pool_t* p, int layer, const void* x, int64_t
   if (pieces < 1) pieces = 1;
   const long long units = (pieces + rows - 1) / rows * ch_blocks;
   // (CTAs per SM: for single tokens fewer, as each lists the batch first: 256 of them x
-  // 4,096 channels 8.8 us with 4, 11.2 with 12; 15,843 tokens 69 and 60)
-  const int per_ch = (max_seqlen_hint == 1 ? 4 : 12) * p->sms / ch_blocks;
+  // 4,096 channels 8.6 us with 4, 11.2 with 12; 15,843 tokens 51.4 with 4, 49.0 with 8,
+  // 51.0 with 16)
+  const int per_ch = (max_seqlen_hint == 1 ? 4 : 8) * p->sms / ch_blocks;
   long long ctas = (long long)(per_ch > 0 ? per_ch : 1) * ch_blocks;
   if (ctas > units) ctas = units;
   cudaStream_t s = (cudaStream_t)stream;
