@@ -77,7 +77,8 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
 //    predecessor releases after its own wait, as here.
 // Reading early are schedule_kernel (the call's lists; it also releases at
 // once, so the kernel behind it may not) and the late kernels behind a prompt
-// batch's last one (the scheduler's lists, the inputs and states of other
+// batch's last one, windowed attention's for few tokens behind its prompts' among
+// them (the scheduler's lists, the inputs and states of other
 // sequences; they release at once too, so that a scheduler may start beside
 // them and the kernel before them, which write no lists).  The one writer of
 // lists is plan_compact_kernel: move_blocks_kernel, always behind it, must not

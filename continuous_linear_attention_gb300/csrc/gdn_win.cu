@@ -29,15 +29,21 @@ constexpr float kLog2e = 1.4426950408889634f;
 // A CTA takes kRows rows of one kv head (queries of consecutive tokens, the
 // heads that share the kv head next to each other) and walks the keys in tiles
 // of kKeys, with the running maximum and sum of the softmax: fp32 throughout.
+// Bound by latency (a tile's loads, products and softmax follow one another) and,
+// with many CTAs, by its 131,072 multiply-adds a tile (d = 64) at 128 a clock: six
+// sequences of 1,554 tokens x 12 heads of d = 64 in fp32, window 200, 68.6 us (82
+// with a row's maximum and sum by shuffles, row after row, and each masked weight
+// looked at in the products).  Tensor cores would round the operands to less than
+// fp32.
 constexpr int kRowThreads = 128;
 constexpr int kRows = 32, kKeys = 32;
 
 template <int D>
 struct RowSmem {
   float q[kRows][D + 4], k[kKeys][D + 4], v[kKeys][D + 4];
-  float p[kKeys][kRows + 4];  // the weights; -1: masked
+  float p[kKeys][kRows + 4];  // the weights (below 0: a masked value must not be touched)
   const void *from_k[kKeys], *from_v[kKeys];  // where a tile's rows lie
-  float top[kRows], sum[kRows], shrink[kRows];
+  float sum[kRows], shrink[kRows];
   PlanSmem plan;
 };
 
@@ -71,9 +77,12 @@ __device__ void rows_of(const WinParams& p, RowSmem<D>& sm, int s, int t0, int t
       x = four(static_cast<const T*>(p.q) + (size_t)(row0 + t0 + r / per) * p.ldq + (size_t)head(r) * D + c);
     *reinterpret_cast<float4*>(&sm.q[r][c]) = x;
   }
-  if (tid < kRows) {
-    sm.top[tid] = -INFINITY;
-    sm.sum[tid] = 0.f;
+  // of the warp's 8 rows: the maximum so far, and each lane's part of the sum
+  float top[8], sum[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    top[r] = -INFINITY;
+    sum[r] = 0.f;
   }
   // the positions that any row sees: sinks before the window's first, then those
   const int p0 = past + t0, p1 = p0 + tokens;
@@ -104,18 +113,21 @@ __device__ void rows_of(const WinParams& p, RowSmem<D>& sm, int s, int t0, int t
       }
     }
     __syncthreads();
+    bool odd = false;
 #pragma unroll 4
     for (int i = tid; i < n * kVecs; i += kRowThreads) {
       const int r = i / kVecs, c = i % kVecs * 4;
       const float4 x = four(static_cast<const T*>(sm.from_k[r]) + c), y = four(static_cast<const T*>(sm.from_v[r]) + c);
       *reinterpret_cast<float4*>(&sm.k[r][c]) = x;
       *reinterpret_cast<float4*>(&sm.v[r][c]) = y;
+      odd |= !(fabsf(y.x) + fabsf(y.y) + fabsf(y.z) + fabsf(y.w) < INFINITY);
     }
     // whether every row sees every key of the tile
     const int first = position(k0), last = position(k0 + n - 1);
     const bool all = rows == kRows && n == kKeys && last <= p0 &&
                      (first > p1 - 1 - p.window || last < p.sinks);
-    __syncthreads();
+    // (finite values, or all seen: 0 is a masked one's weight)
+    const bool plain = !__syncthreads_or(odd) || all;
     // scores: a warp has 8 rows, a lane one key
     const int j = lane < n ? position(k0 + lane) : 0;
     float sc[8];
@@ -139,29 +151,30 @@ __device__ void rows_of(const WinParams& p, RowSmem<D>& sm, int s, int t0, int t
         sc[r] = x + y;
       }
     }
+    float most[8];
+    unsigned unseen = 0;
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const int row = warp * 8 + r;
       const bool seen = all || (row < rows && lane < n && sees(p, p0 + row / per, j));
-      const float x = seen ? sc[r] * to2 : -INFINITY;
-      float m = x;
+      if (!seen) unseen |= 1u << r;
+      most[r] = sc[r] = seen ? sc[r] * to2 : -INFINITY;
+    }
 #pragma unroll
-      for (int w = 16; w >= 1; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-      const float was = sm.top[row], top = fmaxf(was, m);
+    for (int r = 0; r < 8; ++r)
+      asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(most[r]));
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const float to = fmaxf(top[r], most[r]);
       // (nothing but -inf so far: any number in the maximum's place)
-      const float base = top == -INFINITY ? 0.f : top;
-      const float w = seen ? exp2f(x - base) : 0.f;
-      float sum = w;
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      sm.p[lane][row] = seen ? w : -1.f;
-      __syncwarp();
-      if (lane == 0) {
-        const float shrink = exp2f(was - base);
-        sm.top[row] = top;
-        sm.sum[row] = fmaf(sm.sum[row], shrink, sum);
-        sm.shrink[row] = shrink;
-      }
+      const float base = to == -INFINITY ? 0.f : to;
+      const float shrink = exp2f(top[r] - base);
+      const bool seen = !(unseen >> r & 1);
+      const float w = seen ? exp2f(sc[r] - base) : 0.f;
+      sum[r] = fmaf(sum[r], shrink, w);
+      top[r] = to;
+      sm.p[lane][warp * 8 + r] = seen || plain ? w : -1.f;
+      if (lane == 0) sm.shrink[warp * 8 + r] = shrink;
     }
     __syncthreads();
 #pragma unroll
@@ -186,9 +199,16 @@ __device__ void rows_of(const WinParams& p, RowSmem<D>& sm, int s, int t0, int t
             if (decltype(all_c)::value || !(w[r] < 0.f)) acc[r][c] = fma2(f2(w[r], w[r]), vv[c], acc[r][c]);
       }
     };
-    if (all) values(std::true_type());
+    if (plain) values(std::true_type());
     else values(std::false_type());
   }
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], w);
+    if (lane == 0) sm.sum[warp * 8 + r] = sum[r];
+  }
+  __syncthreads();
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int row = or0 + r;

@@ -37,7 +37,7 @@ __device__ __forceinline__ bool sees(const WinParams& p, int pos, int j) {
 
 // Work memory of a pool for the forms below: arrival counters of split windows,
 // the units that the tensor-core form leaves (the header's kWorkHead counts
-// them), partial results of split windows.
+// them, its kItemHeadC the units claimed), partial results of split windows.
 constexpr size_t kWinCounterBytes = 4096;
 constexpr int kWinLeft = 16384;
 constexpr size_t kWinListBytes = kWinLeft * sizeof(int32_t);

@@ -456,7 +456,9 @@ int gdn_sel_scan_varlen_forward(gdn_pool_t* pool, int layer, const void* u, int6
  * which the caller keeps, a block is all there is of it.
  * Supported: d in {32, 64, 128}, 1 <= Hkv <= 1024, 1 <= window <= 2^20,
  * 0 <= sinks <= 4096, GDN_F32 or GDN_BF16.  gdn_state_pool_reserve has nothing
- * to do for it. */
+ * to do for it; gdn_pool_last_prefill_path: GDN_PREFILL_FUSED where the prompts'
+ * tensor-core form may have run, GDN_PREFILL_SERIAL where they had the form for
+ * any shape, GDN_PREFILL_NONE where the call had single tokens only. */
 int gdn_win_pool_layout_for(int num_blocks, int num_layers, int num_kv_heads, int d, int window,
                             int sinks, int act_dtype, size_t block_align, size_t* block_stride,
                             size_t* v_off, size_t* total_bytes);
@@ -483,9 +485,10 @@ int gdn_win_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int nu
  * state_block_idx, T, N, max_seqlen_hint, the skip rules, error flags and
  * stream contract: as gdn_varlen_forward; a past length below 0, or whose sum
  * with the sequence's length passes 2^31 - 1, raises GDN_FLAG_RANGE and the
- * sequence is skipped.  Scores, maxima, sums and outputs are fp32 (bf16: the
- * weights are rounded to bf16 for their product with the values) and rounded
- * once to the activation dtype.  What a query does not see does not
+ * sequence is skipped.  Scores, maxima, sums and outputs are fp32 and rounded
+ * once to the activation dtype; in the prompts' tensor-core form (bf16, d 64 or
+ * 128) the weights are rounded to bf16 for their
+ * product with the values.  What a query does not see does not
  * change its output, NaN and infinities among it; slots that hold no position
  * yet are not read.  Never synchronises; graph-capturable. */
 int gdn_win_varlen_forward(gdn_pool_t* pool, int layer, const void* q, const void* k,
