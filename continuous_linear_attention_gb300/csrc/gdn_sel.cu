@@ -365,7 +365,8 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) sel_step_kernel(ScanP
 // issue slots: per state and token two multiplications, the exponential with its
 // series and its choice, two multiply-adds, in packed pairs 14 instructions for
 // two states, and some 50 per token and channel for softplus, SiLU and the
-// tile's way through shared memory.  15,843 tokens x 4,096 channels: 593 us.
+// tile's way through shared memory.  15,843 tokens x 4,096 channels: 575 to 608 us,
+// issue slots at 74%.
 //
 // Long sequences of few channels are cut into segments: a first pass (kState)
 // computes each segment's own state (from zeros) and its steps' sum, a small
@@ -387,7 +388,8 @@ __host__ __device__ inline int segment_tokens(int longest, long long tokens, int
                                               int n, int sms) {
   const long long share = (tokens * ch_blocks + sms - 1) / sms;
   const long long whole = 2ll * longest > share ? 2ll * longest : share;
-  // eight of them to an SM, and never more: the grid has room for so many
+  // eight of them to an SM (with four, 32,768 tokens x 2,048 channels took 1.5 times as
+  // long), and never more: the grid has room for so many
   long long seg = ((share + 7) / 8 + 31) / 32 * 32;
   if (seg < 64) seg = 64;
   const long long split = share * 7 / 4 + 2 * seg + 300;
@@ -717,7 +719,7 @@ cudaError_t launch_scan_of(const ScanParams& p, int n, int max_long, int max_one
   q.report = 1;
   if (max_long > 0) {
     // (whole sequences with two states to a thread, segments with four: 593 and 645 us
-    // for 15,843 tokens x 4,096 channels, 922 and 806 for 32,768 x 2,048)
+    // for 15,843 tokens x 4,096 channels, 922 and 806 (now 799) for 32,768 x 2,048)
     const Batch& b = q.batch;
     const int longest = b.hint > 0 && b.hint < b.T ? b.hint : b.T;
     const bool whole = b.listed || segment_tokens(longest, b.T, (q.channels + 63) / 64, q.slots, b.N, sms) == 0x7fffffff;

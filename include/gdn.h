@@ -458,7 +458,7 @@ int gdn_sel_scan_varlen_forward(gdn_pool_t* pool, int layer, const void* u, int6
  * 0 <= sinks <= 4096, GDN_F32 or GDN_BF16.  gdn_state_pool_reserve has nothing
  * to do for it; gdn_pool_last_prefill_path: GDN_PREFILL_FUSED where the prompts'
  * tensor-core form may have run, GDN_PREFILL_SERIAL where they had the form for
- * any shape, GDN_PREFILL_NONE where the call had single tokens only. */
+ * any shape, GDN_PREFILL_NONE where the call could hold few tokens only. */
 int gdn_win_pool_layout_for(int num_blocks, int num_layers, int num_kv_heads, int d, int window,
                             int sinks, int act_dtype, size_t block_align, size_t* block_stride,
                             size_t* v_off, size_t* total_bytes);
