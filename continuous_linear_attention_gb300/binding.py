@@ -201,12 +201,14 @@ def _stream(stream, device: Optional[int] = None) -> Optional[int]:
     return stream.cuda_stream
 
 
+_ACT_CODES = {torch.float32: GDN_F32, "f32": GDN_F32, torch.bfloat16: GDN_BF16, "bf16": GDN_BF16}
+
+
 def act_code(dtype) -> int:
-    if dtype in (torch.float32, "f32"):
-        return GDN_F32
-    if dtype in (torch.bfloat16, "bf16"):
-        return GDN_BF16
-    raise ValueError(f"unsupported activation dtype {dtype}")
+    code = _ACT_CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported activation dtype {dtype}")
+    return code
 
 
 def layout_for(num_blocks, num_layers, Hk, Hv, dk, dv, K, act, block_align=0):
@@ -395,15 +397,15 @@ def _heads(t, name, heads, d, dtype, T, device):
         raise ValueError(f"{name} is [>= {T}][{heads}][{d}] of {dtype}: got {tuple(shape)} of "
                          f"{t.dtype}")
     rows = shape[0]
-    if rows and (stride[2] != 1 or (heads > 1 and stride[1] != d) or not t.is_cuda or
-                 t.get_device() != device):
+    # (get_device() is -1 for a tensor of the host)
+    if rows and (stride[2] != 1 or (heads > 1 and stride[1] != d) or t.get_device() != device):
         raise ValueError(f"the rows of {name} have to be dense, on cuda:{device}")
     return t.data_ptr(), stride[0] if rows > 1 else heads * d
 
 
 def _list(t, name, dtype, n, device):
     """The address of a dense device list of at least n elements."""
-    if (t.dtype != dtype or t.numel() < n or not t.is_cuda or t.get_device() != device or
+    if (t.dtype != dtype or t.numel() < n or t.get_device() != device or
             not t.is_contiguous()):
         raise ValueError(f"{name} is a contiguous tensor of >= {n} {dtype} on cuda:{device}: got "
                          f"{t.numel()} of {t.dtype} on {t.device}")
@@ -503,11 +505,13 @@ class WinPool(_TypedPool):
 
 def _rows(t, name, cols, dtype, T, device):
     """(address, row pitch) of at least T dense rows [T][cols], any row pitch."""
-    if t.dim() != 2 or t.shape[1] != cols or t.dtype != dtype or t.shape[0] < T:
-        raise ValueError(f"{name} is [>= {T}][{cols}] of {dtype}: got {tuple(t.shape)} of {t.dtype}")
-    if t.shape[0] and (t.stride(1) != 1 or not t.is_cuda or t.get_device() != device):
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or t.dtype != dtype or shape[0] < T:
+        raise ValueError(f"{name} is [>= {T}][{cols}] of {dtype}: got {tuple(shape)} of {t.dtype}")
+    rows, stride = shape[0], t.stride()
+    if rows and (stride[1] != 1 or t.get_device() != device):
         raise ValueError(f"the rows of {name} have to be dense, on cuda:{device}")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else cols
+    return t.data_ptr(), stride[0] if rows > 1 else cols
 
 
 def _maybe(t, name, dtype, n, device):
@@ -522,7 +526,7 @@ def sel_conv_varlen_forward(pool: SelPool, layer: int, x, cu_seqlens, state_bloc
     C, K, dtype, dev = pool.dims[2], pool.dims[4], pool.dtype, pool.device
     px, ldx = _rows(x, "x", C, dtype, T, dev)
     po, ldo = _rows(out, "out", C, dtype, T, dev)
-    _check(load().gdn_sel_conv_varlen_forward(
+    _check((_lib or load()).gdn_sel_conv_varlen_forward(
         pool.handle, layer, px, ldx,
         _list(cu_seqlens, "cu_seqlens", torch.int32, N + 1, dev),
         _list(state_block_idx, "state_block_idx", torch.int32, N, dev),
@@ -545,7 +549,7 @@ def sel_scan_varlen_forward(pool: SelPool, layer: int, u, dt, B, C, z, cu_seqlen
     w = SelWeights(_list(A_log, "A_log", torch.float32, chan * n, dev),
                    _maybe(D, "D", torch.float32, chan, dev),
                    _maybe(dt_bias, "dt_bias", torch.float32, chan, dev))
-    _check(load().gdn_sel_scan_varlen_forward(
+    _check((_lib or load()).gdn_sel_scan_varlen_forward(
         pool.handle, layer, *rows,
         _list(cu_seqlens, "cu_seqlens", torch.int32, N + 1, dev),
         _list(state_block_idx, "state_block_idx", torch.int32, N, dev),
@@ -567,7 +571,7 @@ def win_varlen_forward(pool: WinPool, layer: int, q, k, v, cu_seqlens, state_blo
     pk, ldk = _heads(k, "k", Hkv, d, dtype, T, dev)
     pv, ldv = _heads(v, "v", Hkv, d, dtype, T, dev)
     po, ldo = _heads(out, "out", H, d, dtype, T, dev)
-    _check(load().gdn_win_varlen_forward(
+    _check((_lib or load()).gdn_win_varlen_forward(
         pool.handle, layer, pq, pk, pv, ldq, ldk, ldv, H,
         _list(cu_seqlens, "cu_seqlens", torch.int32, N + 1, dev),
         _list(state_block_idx, "state_block_idx", torch.int32, N, dev),
@@ -583,29 +587,39 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, q_out=
     be None), each with any row pitch; positions [T] int32; inv_freq [rot/2]
     fp32 (None: no rotation).  Without q_out and k_out in place.  Returns
     (q_out, k_out)."""
-    if q.dim() != 3 or (k is not None and k.dim() != 3):
+    shape = q.shape
+    if len(shape) != 3 or (k is not None and k.dim() != 3):
         raise ValueError("q and k are [T][heads][d]")
-    T, H, d = q.shape
+    T, H, d = shape
     dtype, dev = q.dtype, q.get_device()
     if dev < 0 or dev != _current_device():
         raise ValueError(f"q is on {q.device}, not on the current CUDA device")
-    q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
-    if k is None and k_out is not None:
-        raise ValueError("k_out without k")
-    if k is not None and k.shape[0] != T:
-        raise ValueError(f"{T} rows of q and {k.shape[0]} of k")
-    Hkv = 0 if k is None else k.shape[1]
     pq, ldq = _heads(q, "q", H, d, dtype, T, dev)
-    pqo, ldqo = _heads(q_out, "q_out", H, d, dtype, T, dev)
-    pk, ldk = (None, 0) if k is None else _heads(k, "k", Hkv, d, dtype, T, dev)
-    pko, ldko = (None, 0) if k is None else _heads(k_out, "k_out", Hkv, d, dtype, T, dev)
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    _check(load().gdn_qk_norm_rope(
+    if q_out is None or q_out is q:
+        q_out, pqo, ldqo = q, pq, ldq
+    else:
+        pqo, ldqo = _heads(q_out, "q_out", H, d, dtype, T, dev)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+        Hkv, pk, ldk, pko, ldko = 0, None, 0, None, 0
+    else:
+        rows, Hkv, _ = k.shape
+        if rows != T:
+            raise ValueError(f"{T} rows of q and {rows} of k")
+        pk, ldk = _heads(k, "k", Hkv, d, dtype, T, dev)
+        if k_out is None or k_out is k:
+            k_out, pko, ldko = k, pk, ldk
+        else:
+            pko, ldko = _heads(k_out, "k_out", Hkv, d, dtype, T, dev)
+    half = 0 if inv_freq is None else inv_freq.numel()
+    f32 = torch.float32
+    _check((_lib or load()).gdn_qk_norm_rope(
         pq, pk, ldq, ldk, _list(positions, "positions", torch.int32, T, dev),
-        _maybe(inv_freq, "inv_freq", torch.float32, rot // 2, dev), rot, 1 if interleaved else 0,
-        _maybe(q_weight, "q_weight", torch.float32, d, dev),
-        _maybe(k_weight, "k_weight", torch.float32, d, dev), weight_offset, eps, T, H, Hkv, d,
-        act_code(dtype), pqo, pko, ldqo, ldko, _stream(stream, dev)), "gdn_qk_norm_rope")
+        _maybe(inv_freq, "inv_freq", f32, half, dev), 2 * half, 1 if interleaved else 0,
+        _maybe(q_weight, "q_weight", f32, d, dev), _maybe(k_weight, "k_weight", f32, d, dev),
+        weight_offset, eps, T, H, Hkv, d, act_code(dtype), pqo, pko, ldqo, ldko,
+        _stream(stream, dev)), "gdn_qk_norm_rope")
     return q_out, k_out
 
 
