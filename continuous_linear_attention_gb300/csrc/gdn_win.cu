@@ -368,6 +368,7 @@ cudaError_t launch_win_rows(const WinParams& p, int act, const Pieces& of, int m
 
 cudaError_t launch_win_append(const WinParams& p, int act, const Pieces& of, int max_pieces, int sms,
                               cudaStream_t s) {
+  // (eight to an SM list the batch twice as often: 1.5 us more)
   const int ctas = max_pieces < 4 * sms ? max_pieces : 4 * sms;
   auto kern = act == GDN_F32 ? win_append_kernel<float> : win_append_kernel<__nv_bfloat16>;
   return launch_pdl(kern, dim3(ctas), dim3(kAppendThreads), 0, s, p, of);
