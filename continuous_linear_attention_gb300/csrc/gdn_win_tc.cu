@@ -20,7 +20,7 @@
 // both products of two tiles 2,048 cycles, its exponentials as much), so the two
 // tiles alternate: the softmax of one beside the products of the other.
 // 15,843 tokens x 32 heads (8 kv heads) x 128, window 1,024, the append with it:
-// 203 us, 985 TFLOP/s; tensor pipe 49%, the exponentials' 27%.  What is left is in
+// 203 to 206 us, 970 to 985 TFLOP/s; tensor pipe 49%, the exponentials' 27%.  What is left is in
 // the hand-overs between the two (a softmax of 128 keys takes some 1,500 clocks of
 // latency, more than its half of the exponentials) and some 5,000 clocks where a
 // unit ends and the next one begins.
