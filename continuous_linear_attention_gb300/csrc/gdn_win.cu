@@ -511,7 +511,8 @@ int gdn_win_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
   // few tokens in a form of their own, where there is one
   const int few = gdn::win_short_supported(d, p->act) ? gdn::win_short_tokens(wp.group) : 0;
   const bool may_long = few == 0 || (T > few && (max_seqlen_hint == 0 || max_seqlen_hint > few));
-  const bool may_short = few > 0 && !(N == 1 && T > few);
+  // (a single sequence that no form may take: a kernel that looks at the batch)
+  const bool may_short = few > 0 && !(N == 1 && T > few && may_long);
   const bool tc = T > 0 && gdn::win_tc_supported(d, p->act, wp.group);
   gdn::Pieces of = {few + 1, 0x7fffffff,
                     tc ? gdn::win_tc_tokens(wp.group) : wp.group < gdn::kRows ? gdn::kRows / wp.group : 1};
