@@ -34,10 +34,12 @@
 //                 500 cycles between them; without turns they start together, and
 //                 the products wait for both softmaxes)
 //   producer      one warp: TMA loads, and what the others need to know of a tile
-//   check         one warp: whether a value is not finite in a tile of which some
-//                 row does not see all.  0 times it would reach that row; such a
-//                 unit is left to the form for any shape, which runs behind this
-//                 kernel over the list of them.
+//   check         one warp: zeros over the values behind a run's end (its last box of
+//                 16 rows holds what follows in memory: other slots, another block,
+//                 another sequence's tokens), and whether a value is not finite in a
+//                 tile of which some row does not see all.  0 times it would reach
+//                 that row; such a unit is left to the form for any shape, which runs
+//                 behind this kernel over the list of them.
 // P is rounded to bf16, 2^-8 relative at most, as the product's operand (its sum is
 // not): outputs are off by 2.1e-3 to 2.3e-3 (2-norm), by 1.7e-3 where only they
 // themselves are rounded.  A second term of P would be a third product as large as
@@ -77,6 +79,7 @@ enum : int {
   kEnd = 4,     // no more tiles
   kHasB = 8,    // the unit has rows in tile B
   kPartly = 16, // some row does not see some key
+  kTails = 32,  // a segment has less than 16 keys
 };
 
 // A run of keys: consecutive rows of the ring or of the call's tokens.
@@ -96,6 +99,7 @@ struct TcSmem {
   int seg0[5];  // and the first segment of each
   uint64_t described[kRing], checked[kRing], read[kRing];
   uint64_t q_full[2], q_free[2], k_full[kStages], k_free[kStages], v_full[kStages], v_free[kStages];
+  uint64_t v_clean[kStages];  // (check warp) nothing but values of the segments' keys, and zeros
   uint64_t s_full[2], p_full[2], o_full[2], turn[2];
   uint32_t tmem;
   PlanSmem plan;
@@ -213,6 +217,7 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
       mbar_init(&sm.k_full[i], 1);
       mbar_init(&sm.k_free[i], 2);  // MMA A and B
       mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.v_clean[i], 1);
       mbar_init(&sm.v_free[i], 3);  // and check
     }
     for (int x = 0; x < 2; ++x) {
@@ -521,7 +526,8 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
           const bool more = !(next & (kEnd | kFirst));  // (then of this unit, and of this warp's rows as well)
           if (mine(flags)) {
             if (more) keys(next);
-            if (dead || !wait_for(&sm.v_full[vs.at], vs.ph) || !wait_for(&sm.p_full[x], p_ph)) { dead = true; break; }
+            uint64_t* v_there = flags & kTails ? &sm.v_clean[vs.at] : &sm.v_full[vs.at];
+            if (dead || !wait_for(v_there, vs.ph) || !wait_for(&sm.p_full[x], p_ph)) { dead = true; break; }
             p_ph ^= 1;
             my_turn();
             if (dead) break;
@@ -620,6 +626,7 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
           const bool all = there && n == kSeg && pos + kSeg - 1 <= p0 &&
                            (pos > p1 - 1 - p.window || pos + kSeg <= p.sinks);
           const bool full = __all_sync(0xffffffffu, all) && segs == kSegs;
+          const bool tails = __any_sync(0xffffffffu, there && n < kSeg);
           // one box where all rows of the tile lie behind one another
           const int row_first = __shfl_sync(0xffffffffu, row, 0), ring_first = __shfl_sync(0xffffffffu, mine.ring, 0);
           const bool one = segs == kSegs &&
@@ -633,7 +640,7 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
           }
           if (lane == 0) {
             tile.flags = (j == 0 ? kFirst : 0) | (j == n_tiles - 1 ? kLast : 0) | (has_b ? kHasB : 0) |
-                         (full ? 0 : kPartly);
+                         (full ? 0 : kPartly) | (tails ? kTails : 0);
             tile.segs = segs;
             tile.row = row_first_q;
             tile.pos0 = p0;
@@ -710,21 +717,38 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
         Tile& tile = sm.tile[at.at];
         const int flags = tile.flags;
         if (flags & kEnd) break;
+        const int n = lane < tile.segs ? tile.n[lane & 7] : kSeg;
         if (!wait_for(&sm.v_full[vs.at], vs.ph)) { dead = true; break; }
+        unsigned char* values = sm.v[vs.at] + (lane & 7) * 16;  // (8 lanes a row)
+        for (unsigned tails = __ballot_sync(0xffffffffu, n < kSeg); tails; tails &= tails - 1) {
+          const int i = __ffs(tails) - 1;
+#pragma unroll 1
+          for (int r = kSeg * i + __shfl_sync(0xffffffffu, n, i) + (lane >> 3); r < kSeg * (i + 1); r += 4)
+#pragma unroll
+            for (int h = 0; h < kBlocks; ++h)
+              *reinterpret_cast<uint4*>(values + h * kBox + r * 128) = make_uint4(0, 0, 0, 0);
+        }
+        if (flags & kTails) tc::fence_proxy_async_smem();
+        warp_arrive(&sm.v_clean[vs.at]);
         if (flags & kPartly) {
-          // 16 bytes of 4 rows at a time
+          // 16 bytes of 4 rows at a time; 0 times a value that is not finite is NaN.  (The stage
+          // is not free before this is done: with the exponents compared, five instructions
+          // for two values, the prompts took 5% longer.)
           const int rows = tile.segs * kSeg;
-          bool odd = false;
+          const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+          __nv_bfloat162 sum[4] = {zero, zero, zero, zero};
 #pragma unroll 4
           for (int r = lane >> 3; r < rows; r += 4)
 #pragma unroll
             for (int h = 0; h < kBlocks; ++h) {
-              const uint4 x4 = *reinterpret_cast<const uint4*>(sm.v[vs.at] + h * kBox + r * 128 + (lane & 7) * 16);
+              const uint4 x4 = *reinterpret_cast<const uint4*>(values + h * kBox + r * 128);
               const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
               for (int c = 0; c < 4; ++c)
-                odd |= (x[c] & 0x7f80u) == 0x7f80u || (x[c] & 0x7f800000u) == 0x7f800000u;
+                sum[c] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x[c]), zero, sum[c]);
             }
+          const __nv_bfloat162 all = __hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3]));
+          const bool odd = !(__low2float(all) == 0.f && __high2float(all) == 0.f);
           if (__any_sync(0xffffffffu, odd) && lane == 0) tile.odd = 1;
         }
         warp_arrive(&sm.checked[at.at]);

@@ -488,9 +488,12 @@ int gdn_win_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int nu
  * sequence is skipped.  Scores, maxima, sums and outputs are fp32 and rounded
  * once to the activation dtype; in the prompts' tensor-core form (bf16, d 64 or
  * 128) the weights are rounded to bf16 for their
- * product with the values.  What a query does not see does not
- * change its output, NaN and infinities among it; slots that hold no position
- * yet are not read.  Never synchronises; graph-capturable. */
+ * product with the values.  What a query does not see has no part in its output,
+ * NaN and infinities among it; other requests, other heads and slots that hold no
+ * position yet do not change a bit of it.  (In the prompts' form a value of the
+ * request itself that is not finite, and that a query does not see, sends the
+ * queries near it to the form for any shape, which rounds the weights to fp32.)
+ * Never synchronises; graph-capturable. */
 int gdn_win_varlen_forward(gdn_pool_t* pool, int layer, const void* q, const void* k,
                            const void* v, int64_t ldq, int64_t ldk, int64_t ldv, int num_heads,
                            const int32_t* cu_seqlens, const int32_t* state_block_idx,
