@@ -312,9 +312,9 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
       const float high = fmaxf(max3(m4[0], m4[1], v[124]), max3(m4[2], m4[3], fmaxf(v[125], fmaxf(v[126], v[127])))) * to2;
       const bool more = high > top + kSlack;  // (the first one that is not -inf as well)
       if (__any_sync(0xffffffffu, more)) {
-        const float now = fmaxf(top, high);
-        const float f = now == -INFINITY ? 1.f : ex2(top - now);
-        top = now;
+        // (a row without a larger step stays as it is: its rounding is its own)
+        const float f = more ? ex2(top - high) : 1.f;
+        top = more ? high : top;
         sum *= f;
         if (!(flags & kFirst)) {
           // (S_X full: all products before it are done, P V of the last tile among them)

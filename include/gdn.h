@@ -489,7 +489,7 @@ int gdn_win_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int nu
  * once to the activation dtype; in the prompts' tensor-core form (bf16, d 64 or
  * 128) the weights are rounded to bf16 for their
  * product with the values.  What a query does not see has no part in its output,
- * NaN and infinities among it; other requests, other heads and slots that hold no
+ * NaN and infinities among it; what other requests and heads hold, and slots that hold no
  * position yet do not change a bit of it.  (In the prompts' form a value of the
  * request itself that is not finite, and that a query does not see, sends the
  * queries near it to the form for any shape, which rounds the weights to fp32.)
