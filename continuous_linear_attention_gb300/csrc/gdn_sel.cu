@@ -662,7 +662,10 @@ __global__ void __launch_bounds__(256) sel_segments_kernel(ScanParams p, int n_s
       for (int i = 0; i < kAhead; ++i) {
         if (i0 + i >= segs) break;
         p.seg_states[(size_t)(first + i0 + i) * words + at] = h;
-        h = fmaf(h, decay2(sum[i] * A), own[i]);
+        // (an infinite state stays infinite, as it does step by step, where the segment's decay
+        // is too small for fp32: the least normal number in its place)
+        const float x = sum[i] * A, decay = decay2(x);
+        h = fmaf(h, isinf(h) && x > -INFINITY ? fmaxf(decay, 1.17549435e-38f) : decay, own[i]);
       }
     }
   }
