@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kAppendThreads) win_append_kernel(WinParams p,
     b.work.header()[kWorkHead] = 0;
     b.work.header()[kItemHeadC] = 0;
   }
-  const SeqList list = b.listed ? listed_long(b) : plan_self(b, pieces, plan, p.report && blockIdx.x == 0);
+  const SeqList list = b.listed ? listed_long(b) : plan_self(b, pieces, plan, false);  // (reported before)
   const int row16 = p.Hkv * p.d * (int)sizeof(T) / 16, head16 = p.d * (int)sizeof(T) / 16;
   for (int piece = blockIdx.x; piece < list.total; piece += gridDim.x) {
     const int e = entry_of(list, piece), s = list.items[e];
@@ -532,17 +532,24 @@ int gdn_win_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
       return GDN_ERR_CUDA;
     wp.report = 0;
   }
-  // (behind the prompts' kernel, not behind what follows it)
-  if (may_short && gdn::launch_win_short(wp, of_few, max_items, p->sms, may_long && tc, p->win_parts, s) != cudaSuccess)
-    return GDN_ERR_CUDA;
-  if (may_short) wp.report = 0;
-  if (may_long) {
-    if (gdn::launch_win_rows(wp, p->act, of, most_pieces(of.tokens), p->sms, p->win_parts, tc, s) != cudaSuccess)
-      return GDN_ERR_CUDA;
-    wp.report = 0;
+  auto behind = [&]() {
+    // (behind the prompts' kernel, not behind what follows it)
+    if (may_short) {
+      const cudaError_t e = gdn::launch_win_short(wp, of_few, max_items, p->sms, may_long && tc, p->win_parts, s);
+      if (e != cudaSuccess) return e;
+      wp.report = 0;
+    }
+    if (!may_long) return cudaSuccess;
+    const cudaError_t e = gdn::launch_win_rows(wp, p->act, of, most_pieces(of.tokens), p->sms, p->win_parts, tc, s);
+    if (e != cudaSuccess) return e;
     if (!b.listed) of.tokens = gdn::kAppendTokens;
-    if (gdn::launch_win_append(wp, p->act, of, most_pieces(of.tokens), p->sms, s) != cudaSuccess)
-      return GDN_ERR_CUDA;
+    return gdn::launch_win_append(wp, p->act, of, most_pieces(of.tokens), p->sms, s);
+  };
+  if (behind() != cudaSuccess) {
+    // (what the append, which was not launched, would have set back for the next call)
+    static_assert(gdn::kItemHeadC == gdn::kWorkHead + 2, "the claimed and the left units' counters");
+    if (may_long && tc) cudaMemsetAsync(b.work.header() + gdn::kWorkHead, 0, 3 * sizeof(int32_t), s);
+    return GDN_ERR_CUDA;
   }
   if (p->ev_after && cudaEventRecord(p->ev_after, s) != cudaSuccess) return GDN_ERR_CUDA;
   return GDN_OK;

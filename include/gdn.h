@@ -35,7 +35,9 @@
  *    the stream has reached the call (the engine's warmup race, where a
  *    forward read cu_seqlens that were being rewritten, is exactly this).
  *  - Return value: GDN_OK (0) or a negative GDN_ERR_* code; on error nothing
- *    was launched and nothing was written.
+ *    was launched and nothing was written (but after GDN_ERR_CUDA kernels
+ *    before a failed launch may have run: what the call writes is undefined
+ *    then, and the pool as usable as before).
  *  - No entry point except gdn_get_error synchronises with the device, so
  *    gdn_varlen_forward can be captured in a CUDA graph.
  */
