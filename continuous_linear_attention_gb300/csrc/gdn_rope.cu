@@ -14,7 +14,7 @@
 // over the next tokens' where the share is longer: every warp has the same work,
 // and a token's sines and cosines are made once (CTAs of 32 whole tokens each came
 // in 1.6 waves: 62 us).  The copies of the next rows are on their way meanwhile.
-// 15,843 tokens x 40 heads x 128: 56.1 us, 5.8 TB/s.
+// 15,843 tokens x 40 heads x 128: 56.4 us, 5.75 TB/s.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -93,14 +93,27 @@ struct Run8 {
   }
 };
 
+// A frequency / 2 pi as a 64-bit fraction of a turn.  An angle is its product with the
+// position modulo 2^64, off by 2^-32 of a turn at position 2^31 (an fp32 angle would be
+// off by 0.06 at position 10^6).  1 / 2 pi enters in two doubles, so that the fraction is
+// right to 2^-63 for frequencies up to 2^40 (in one, what is off by 2^-54 of the frequency
+// grows with the position: 3e-4 at position 2^31 for a frequency of 1,000).
+__device__ __forceinline__ unsigned long long turns_of(float frequency) {
+  constexpr double kHigh = 0.15915494309189535, kLow = -9.839338337591243e-18, kOne = 18446744073709551616.0;
+  const double f = fabs((double)frequency), high = f * kHigh;
+  double low = fma(f, kLow, fma(f, kHigh, -high));  // f / 2 pi = high + low
+  const double part = high - floor(high);
+  low -= rint(low);
+  if (!(part < 1.0)) return 0ull;  // (a frequency that is not finite)
+  const unsigned long long turns = (unsigned long long)(part * kOne) + (unsigned long long)__double2ll_rn(low * kOne);
+  return frequency < 0.f ? 0ull - turns : turns;
+}
+
 template <typename T, int D, bool kAny>
 struct RopeSmem {
   static constexpr int kWords = sizeof(T) / 2;  // 16 bytes each, of a run
   uint4 ring[kRopeAhead][2 * kWords][kRopeThreads];
-  // inv_freq / 2 pi as 64-bit fractions of a turn: an angle is the product with
-  // the position modulo 2^64, exact for any position (an fp32 angle at position
-  // 10^6 would be off by 0.06)
-  unsigned long long turns[D / 2];
+  unsigned long long turns[D / 2];  // turns_of each frequency
   float rows[kAny ? kRopeThreads * 16 : 1];
 };
 
@@ -150,11 +163,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(RopeParam
 #pragma unroll
   for (int i = 0; i < kAhead - 1; ++i) ahead();
   int pos = token < p.T ? p.positions[token] : -1, pos_next = -1;
-  if ((int)threadIdx.x < half) {
-    double t = (double)p.inv_freq[threadIdx.x] * 0.15915494309189533577;
-    t -= floor(t);
-    sm.turns[threadIdx.x] = t < 1.0 ? (unsigned long long)(t * 18446744073709551616.0) : 0ull;
-  }
+  if ((int)threadIdx.x < half) sm.turns[threadIdx.x] = turns_of(p.inv_freq[threadIdx.x]);
   __syncthreads();
   // the turns of a token's pairs, or (kAny) of their channels
   constexpr int kTurns = kAny ? 16 : 8;

@@ -508,8 +508,9 @@ int gdn_win_varlen_forward(gdn_pool_t* pool, int layer, const void* q, const voi
  *   y = x / sqrt(mean_c(x_c^2) + eps) * (weight_c + weight_offset)
  * (weight NULL: y = x), then for the pairs i < rot/2 of channels (a, b) =
  * (i, i + rot/2), or (2i, 2i + 1) if interleaved, with the angle
- * positions[t] * inv_freq[i] (exact for any position: it is reduced modulo a
- * turn before it is rounded),
+ * positions[t] * inv_freq[i] (reduced modulo a turn before it is rounded to
+ * fp32: right to 2^-31 of a turn before that rounding, for any position and
+ * frequencies up to 2^40),
  *   (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin)
  * and channels from rot on as they are; fp32, rounded once.
  *   q, k         : T rows of H and Hkv heads x d, row pitches in elements; H or
