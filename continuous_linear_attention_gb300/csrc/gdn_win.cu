@@ -12,6 +12,7 @@
 // values, and the C entry points.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <new>
 #include <type_traits>
 
@@ -452,7 +453,8 @@ int gdn_win_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
   if (layer < 0 || layer >= p->num_layers || T < 0 || N < 0 || max_seqlen_hint < 0)
     return GDN_ERR_RANGE;
   if (num_heads < 1 || num_heads > 4096 || num_heads % p->Hk != 0) return GDN_ERR_DIMS;
-  if (!(scale <= 3.402823466e38f && scale >= -3.402823466e38f)) return GDN_ERR_RANGE;
+  // (its product with log2 e, which the kernels scale by, is finite)
+  if (!(fabsf(scale) <= 0x1p127f)) return GDN_ERR_RANGE;
   if (N == 0) return T == 0 ? GDN_OK : GDN_ERR_RANGE;
   if (!cu_seqlens || !state_block_idx || !past_lens) return GDN_ERR_NULL;
   if (T > 0 && (!q || !k || !v || !out)) return GDN_ERR_NULL;
@@ -513,7 +515,9 @@ int gdn_win_varlen_forward(gdn_pool_t* p, int layer, const void* q, const void* 
   const bool may_long = few == 0 || (T > few && (max_seqlen_hint == 0 || max_seqlen_hint > few));
   // (a single sequence that no form may take: a kernel that looks at the batch)
   const bool may_short = few > 0 && !(N == 1 && T > few && may_long);
-  const bool tc = T > 0 && gdn::win_tc_supported(d, p->act, wp.group);
+  // (in the prompts' form a masked score is -inf before it is scaled, and 0 times it NaN: a scale
+  // near 0 goes to the form for any shape)
+  const bool tc = T > 0 && gdn::win_tc_supported(d, p->act, wp.group) && fabsf(scale) >= 0x1p-100f;
   gdn::Pieces of = {few + 1, 0x7fffffff,
                     tc ? gdn::win_tc_tokens(wp.group) : wp.group < gdn::kRows ? gdn::kRows / wp.group : 1};
   const int max_long = max_items < T / (few + 1) ? max_items : T / (few + 1);

@@ -251,8 +251,8 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
     const int x = warp >> 2, row = (warp & 3) * 32 + lane;  // tile, and row of it
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;      // this warp's tensor memory lanes
     const uint32_t ts = tmem + TM_S + 128u * x + lanes, to = tmem + TM_O + 128u * x + lanes;
-    // (a negative scale: the product takes -Q; 0: all weights equal, and -inf stays -inf)
-    const float to2 = fmaxf(fabsf(p.scale * kLog2e), 1e-37f);
+    // (a negative scale: the product takes -Q; it is not 0, so that -inf stays -inf)
+    const float to2 = fabsf(p.scale * kLog2e);
     // (a quotient by p.group of less than 128 rows: exact)
     const uint32_t over_group = (65536u + p.group - 1) / p.group;
     const int token = (int)((uint32_t)row * over_group >> 16);
@@ -451,7 +451,7 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
         auto mine = [&](int flags) { return x == 0 || (flags & kHasB) != 0; };
         // S = Q K^T of a tile (always of 128 keys: scores behind the last one are masked)
         const uint32_t id_s = tc::idesc_bf16_f32(128, 128) | (p.scale < 0.f ? 1u << 13 : 0u);  // (bit 13: -A)
-        auto scores = [&](int flags) {
+        auto scores = [&]() {
           if (one) {
             uint32_t q0 = q_lo + x * (Smem::kOperand >> 4), k0 = k_lo + (uint32_t)ks.at * (Smem::kOperand >> 4);
             asm volatile("" : "+r"(q0), "+r"(k0));
@@ -512,7 +512,7 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
           keys(flags);
           if (dead) return;
           tc::fence_after_sync();
-          scores(flags);
+          scores();
           begun(flags);
         };
         described(flags, segs);
@@ -534,7 +534,7 @@ win_tc_kernel(WinParams p, Pieces pieces, int32_t* left, const __grid_constant__
             tc::fence_after_sync();
             values(segs, (flags & kFirst) != 0);
             if (flags & kLast) commit(&sm.o_full[x]);
-            if (more) scores(next);
+            if (more) scores();
             your_turn();
             commit(&sm.v_free[vs.at]);
             if (more) begun(next);

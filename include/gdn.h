@@ -479,7 +479,7 @@ int gdn_win_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int nu
  *   q, out : T rows of num_heads heads x d, row pitches ldq, ldo elements;
  *            num_heads is a multiple of Hkv (head h reads kv head h / (num_heads / Hkv))
  *   k, v   : T rows of Hkv heads x d, row pitches ldk, ldv
- *   scale  : finite (GDN_ERR_RANGE)
+ *   scale  : up to 2^127 in size (GDN_ERR_RANGE)
  *   past_lens : [N] int32 device, the request's tokens before this call (0: a
  *            new request, its block is not read)
  * q, k, v and out are 16-byte aligned and their pitches multiples of 16 bytes

@@ -126,3 +126,24 @@ def test_windowed_attention(lib, N, T, act, d):
         if act == 1 and d >= 64 and k > (N > 256):  # behind the prompts' kernel
             assert (header[5], header[7]) == (0, 0), k
     lib.gdn_state_pool_destroy(pool)
+
+
+def test_refused_scales_launch_nothing(lib):
+    pool = ctypes.c_void_p()
+    lib.fake_fail(-1)
+    lib.fake_reset()
+    assert lib.gdn_win_pool_create(ctypes.byref(pool), 8, 1, 2, 64, 64, 4, 1, 0, None, 0) == 0
+    buf = (ctypes.c_char * (1 << 16))()
+    at = (ctypes.addressof(buf) + 255) // 256 * 256
+
+    def call(scale):
+        lib.fake_fail(-1)
+        status = lib.gdn_win_varlen_forward(pool, 0, at, at, at, 256, 128, 128, 4, at, at, at, scale, at, 256, 500, 4, 0,
+                                            None)
+        return status, lib.fake_launches() > 0
+
+    for scale in (float("nan"), float("inf"), -float("inf"), 1.8e38, -3.4e38):
+        assert call(scale) == (-3, False), scale
+    for scale in (0.0, 1.0, -1.0, 2.0 ** 127, -2.0 ** 127, 1e-38):
+        assert call(scale) == (0, True), scale
+    lib.gdn_state_pool_destroy(pool)
