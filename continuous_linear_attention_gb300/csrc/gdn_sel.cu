@@ -362,11 +362,12 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) sel_step_kernel(ScanP
 // Longer sequences: a CTA walks the tokens of one sequence, or of a segment of
 // it, for kCB channels, kG threads per channel with N / kG states each in
 // registers, a tile of kTT tokens at a time, the next one on its way.  Bound by
-// issue slots: per state and token two multiplications, the exponential with its
-// series and its choice, two multiply-adds, in packed pairs 14 instructions for
-// two states, and some 50 per token and channel for softplus, SiLU and the
-// tile's way through shared memory.  15,843 tokens x 4,096 channels: 575 to 608 us,
-// issue slots at 74%.
+// issue slots, some 250 instructions per token and channel (N = 16) by the counter:
+// per state two multiplications, the exponential with its series and its choice, two
+// multiply-adds, in packed pairs 14 for two states, 112 in all; some 50 for softplus,
+// SiLU and the tile's way through shared memory; and some 90 that each of a channel's
+// lanes repeats (loads of the step, B and C, the step's pairs, the sums across
+// lanes).  15,843 tokens x 4,096 channels: 575 to 608 us, issue slots at 74%.
 //
 // Long sequences of few channels are cut into segments: a first pass (kState)
 // computes each segment's own state (from zeros) and its steps' sum, a small
@@ -374,6 +375,10 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) sel_step_kernel(ScanP
 // output pass runs all segments side by side.  The work is 1.7 times as much, so
 // that is done where otherwise too few CTAs run or one sequence is longer than an
 // SM's share of all (segment_tokens; every kernel finds the same from the lengths).
+// Only a batch that every CTA lists for itself is cut (up to kSelfPlan entries), and
+// only where the room holds a segment for each entry besides: 32,768 tokens x 2,048
+// channels, 800 us by themselves, are one piece beside 255 single tokens (3.1 ms) or
+// 256 (2.3 ms).
 constexpr int kScanThreads = 256;
 constexpr int kTileTokens = 32;
 constexpr int kSegmentBytes = 32 << 20;  // room for states between segments

